@@ -39,6 +39,11 @@ EXPORTED = (
     "awq_permute_rows",
     "awq_linear_forward_sorted",
     "awq_reserve",
+    "awq_paged_plan",
+    "awq_kv_append",
+    "awq_tree_attention",
+    "awq_reserve_tree_attention",
+    "awq_process_logits",
 )
 
 RESERVE_SORTED = 1
@@ -73,7 +78,40 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
+_I32 = ctypes.c_int32
 _INT = ctypes.c_int
+
+
+class DType(enum.IntEnum):
+    F16 = 0
+    BF16 = 1
+    F32 = 2
+
+
+class Cache(ctypes.Structure):
+    """awq_cache_t"""
+    _fields_ = [("data", _P), ("block_stride", _I64), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class TreeAttention(ctypes.Structure):
+    """awq_tree_attention_t"""
+    _fields_ = [("q", _P), ("q_token_stride", _I64), ("q_head_stride", _I64), ("out", _P), ("lse", _P),
+                ("k_cache", Cache), ("v_cache", Cache), ("block_table", _P), ("table_width", _I64),
+                ("table_stride", _I64), ("context_lens", _P), ("cu_new", _P), ("tree_mask", _P),
+                ("mask_words", _I64), ("B", _I64), ("tokens", _I64), ("q_heads", _I64), ("kv_heads", _I64),
+                ("head_dim", _I64), ("num_blocks", _I64), ("block_size", _I64), ("max_new", _I64),
+                ("max_context", _I64), ("scale", ctypes.c_float), ("dtype", _I32)]
+
+
+class Logits(ctypes.Structure):
+    """awq_logits_t"""
+    _fields_ = [("logits", _P), ("out", _P), ("logits_row_stride", _I64), ("out_row_stride", _I64),
+                ("rows", _I64), ("vocab", _I64), ("B", _I64), ("row_request", _P), ("history", _P),
+                ("history_offsets", _P), ("prompt_lens", _P), ("history_size", _I64), ("repetition", _P),
+                ("frequency", _P), ("presence", _P), ("draft_tokens", _P), ("cu_new", _P), ("tree_mask", _P),
+                ("mask_words", _I64), ("bias_tokens", _P), ("bias_offsets", _P), ("bias_values", _P),
+                ("bias_size", _I64), ("grammar_mask", _P), ("grammar_rows", _P), ("grammar_count", _I64),
+                ("dtype", _I32)]
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
@@ -131,6 +169,18 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.awq_quantize_rtn.restype = _INT
         lib.awq_reserve.argtypes = [_I64, _I64, _I64, ctypes.c_uint, _P]
         lib.awq_reserve.restype = _INT
+        lib.awq_paged_plan.argtypes = [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                       _I64, _P, _P]
+        lib.awq_paged_plan.restype = _INT
+        lib.awq_kv_append.argtypes = [_P, _I64, _I64, _P, _I64, _I64, ctypes.POINTER(Cache), ctypes.POINTER(Cache), _P,
+                                      _I64, _I64, _I64, _I64, _I64, _P]
+        lib.awq_kv_append.restype = _INT
+        lib.awq_tree_attention.argtypes = [ctypes.POINTER(TreeAttention), _P]
+        lib.awq_tree_attention.restype = _INT
+        lib.awq_reserve_tree_attention.argtypes = [_I64, _I64, _I64, _I64, _I64, _P]
+        lib.awq_reserve_tree_attention.restype = _INT
+        lib.awq_process_logits.argtypes = [ctypes.POINTER(Logits), _P]
+        lib.awq_process_logits.restype = _INT
         lib.awq_shutdown.argtypes = []
         lib.awq_shutdown.restype = None
         _lib = lib
@@ -224,6 +274,32 @@ def awq_last_device_status(stream) -> int:
 
 def awq_reserve(max_M, max_K, max_N, flags, stream) -> int:
     return load_library().awq_reserve(max_M, max_K, max_N, flags, stream)
+
+
+def awq_paged_plan(context_lens, new_lens, B, block_table, table_width, table_stride, free_blocks, num_free,
+                   block_size, parents, max_tokens, cu_new, slot_map, positions, token_request, tree_mask, mask_words,
+                   counts, stream) -> int:
+    return load_library().awq_paged_plan(context_lens, new_lens, B, block_table, table_width, table_stride,
+                                         free_blocks, num_free, block_size, parents, max_tokens, cu_new, slot_map,
+                                         positions, token_request, tree_mask, mask_words, counts, stream)
+
+
+def awq_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, k_cache: Cache, v_cache: Cache,
+                  slot_map, tokens, num_blocks, block_size, kv_heads, head_dim, stream) -> int:
+    return load_library().awq_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, k_cache,
+                                        v_cache, slot_map, tokens, num_blocks, block_size, kv_heads, head_dim, stream)
+
+
+def awq_tree_attention(args: TreeAttention, stream) -> int:
+    return load_library().awq_tree_attention(args, stream)
+
+
+def awq_reserve_tree_attention(max_tokens, max_requests, q_heads, kv_heads, head_dim, stream) -> int:
+    return load_library().awq_reserve_tree_attention(max_tokens, max_requests, q_heads, kv_heads, head_dim, stream)
+
+
+def awq_process_logits(args: Logits, stream) -> int:
+    return load_library().awq_process_logits(args, stream)
 
 
 def awq_shutdown() -> None:

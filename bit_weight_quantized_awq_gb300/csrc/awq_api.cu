@@ -598,6 +598,38 @@ awq_status_t awq_reserve(int64_t max_M, int64_t max_K, int64_t max_N, unsigned f
     return AWQ_OK;
 }
 
+awq_status_t awq_reserve_tree_attention(int64_t max_tokens, int64_t max_requests, int64_t q_heads,
+                                        int64_t kv_heads, int64_t head_dim, awq_stream_t stream)
+{
+    if (max_tokens < 0 || max_requests < 0 || max_requests > 16384 || q_heads <= 0 || kv_heads <= 0 ||
+        q_heads % kv_heads != 0 || head_dim <= 0 || head_dim % 8 != 0 || head_dim > 256 ||
+        q_heads >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) || max_tokens * q_heads >= (int64_t(1) << 31))
+        return AWQ_ERR_INVALID_ARG;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
+        return AWQ_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    size_t floats = 0, counters = 0;
+    awq::tree_attention_scratch(max_tokens, max_requests, q_heads, kv_heads, head_dim, sms, &floats, &counters);
+    try {
+        const auto key = std::make_pair(dev, s);
+        bool reserved;
+        {
+            std::lock_guard<std::mutex> lock(awq::g_mutex);
+            reserved = awq::g_scratch[key].reserved;
+            awq::g_scratch[key].reserved = false;
+        }
+        awq::Scratch sc{};
+        const bool ok = awq::get_scratch(s, floats, counters, &sc) && cudaStreamSynchronize(s) == cudaSuccess;
+        std::lock_guard<std::mutex> lock(awq::g_mutex);
+        awq::g_scratch[key].reserved = reserved;
+        return ok ? AWQ_OK : AWQ_ERR_CUDA;
+    } catch (...) {
+        return AWQ_ERR_CUDA;
+    }
+}
+
 awq_status_t awq_last_device_status(awq_stream_t stream)
 {
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -621,6 +653,7 @@ awq_status_t awq_last_device_status(awq_stream_t stream)
         return AWQ_ERR_TIMEOUT;
     }
     if (word & awq::kStatusBadIndex) return AWQ_ERR_INVALID_ARG;
+    if (word & awq::kStatusTooLarge) return AWQ_ERR_TOO_LARGE;
     return AWQ_ERR_CUDA;
 }
 

@@ -1,0 +1,580 @@
+// awq_attention.cu -- attention of a step's new tokens over a paged cache, for
+// few rows a key-value head (plain decode, small trees) and for every head_dim up
+// to 256; awq_attention_tc.cu takes the calls with many rows.
+//
+//   out[r, :] = sum_j exp(s_rj - m_r) v_j / sum_j exp(s_rj - m_r),  s_rj = scale q_r . k_j
+//
+// in one pass over keys and values with a running maximum and sum (awq_attention.cuh
+// has the split of the work and the join of its pieces).
+//
+// Bound: the cache is read once, 4 head_dim bytes a key and head, against
+// 4 head_dim flops a row, so 16 rows have 16 flops a byte: HBM. A CTA therefore is
+// one producer warp, which asks for key and value tiles (64 keys) with TMA, a box
+// a page, as far ahead as shared memory allows, and four consumer warps that
+// each take 16 of the tile's keys: S = Q K^T and O += P V with mma.sync
+// m16n8k16 (16 rows of q, held in registers), the warp's own maximum and sum. The
+// warps never meet before the segment ends. mma.sync, not tcgen05: at 16
+// rows a 128-row tcgen05 tile would be seven eighths padding and its operands and
+// accumulators would take the detour over shared and tensor memory.
+#include <algorithm>
+#include <cstring>
+#include <map>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "awq_attention.h"
+#include "awq_attention.cuh"
+
+namespace awq {
+namespace attn {
+namespace {
+
+constexpr int kRows = 16;        // rows of q a CTA works on (one mma.sync M)
+constexpr int kKeys = 64;        // keys a tile
+constexpr int kConsumers = 128;  // threads of the four consumer warps
+constexpr int kThreads = kConsumers + 32;
+
+// DP: head_dim rounded up to 64, 128 or 256 (TMA fills the rest with zeros).
+template <int DP>
+struct Cfg {
+    static constexpr int kHalves = DP / 64;              // 128-byte columns of a tile
+    static constexpr int kTile = kKeys * DP * 2;         // keys or values of one stage
+    static constexpr int kStages = DP == 64 ? 6 : 3;     // 96 KB in flight (192 KB at DP = 256)
+    static constexpr int kMergeOff = kStages * 2 * kTile;
+    static constexpr int kMerge = kRows * DP * 4;        // one warp's O
+    static constexpr int kRedOff = kMergeOff + kMerge;   // m and l of the four warps; the join's sums
+    static constexpr int kRed = (kConsumers + 2 * kRows + 8 * kRows) * 4;
+    static constexpr int kBarOff = kRedOff + kRed;
+    static constexpr int kSmem = kBarOff + 128 + 1024;
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    ptx::mma_16816(d, a, b0, b1);
+}
+template <>
+__device__ __forceinline__ void mma<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&d)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(addr) : "memory");
+}
+
+// 16-byte piece `c` of row `r` of a tile in the 128-byte swizzle TMA writes
+template <int DP>
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int c)
+{
+    return tile + (uint32_t)(c >> 3) * (kKeys * 128) + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads)
+attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ Params p)
+{
+    using C = Cfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);
+    uint64_t *empty = full + C::kStages;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + C::kStages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(empty + i), kConsumers / 32);
+        }
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    Work<kRows, kKeys> work;
+    if (!work.template find<kThreads>(p)) return;   // its barriers also publish the mbarriers
+    Segment s;
+
+    if (warp == kConsumers / 32) {
+        // ---------------------------------------------------------------- producer
+        const int box = min(1 << p.shift, kKeys);            // keys of one TMA box
+        const int pages = kKeys / box;                       // boxes a tile: 1, 2 or 4
+        int it = 0;
+        bool ok = true;
+#ifdef AWQ_FAULT_TEST
+        if (p.fault && blockIdx.x == 0) ok = false;
+#endif
+        while (ok && work.next(p, s)) {
+            const int keys = s.ctx + s.n;
+            const int32_t *table = p.table + (int64_t)s.b * p.table_stride;
+            auto page_of = [&](int tile) {   // this lane's page of a tile; -1: none
+                const int key = tile * kKeys + lane * box;
+                if (lane >= pages || tile >= s.tile1 || key >= keys) return -1;
+                const int id = table[key >> p.shift];
+                if (id >= 0 && id < p.num_blocks) return id;
+                raise_status(p.status, kStatusBadIndex);
+                return p.num_blocks;         // past the tensor: TMA fills zeros
+            };
+            int id = page_of(s.tile0);
+            for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
+                const int next_id = page_of(tile + 1);
+                const int st = it % C::kStages;
+                ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + st), ((it / C::kStages) & 1) ^ 1, abort_flag, p.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const uint32_t fb = ptx::smem_addr(full + st);
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, id >= 0));
+                if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * 2 * C::kHalves * box * 128);
+                __syncwarp();
+                if (id >= 0) {
+                    const uint32_t dst = ptx::smem_addr(smem + st * 2 * C::kTile) + (uint32_t)lane * box * 128;
+                    const int in_page = (tile * kKeys) & ((1 << p.shift) - 1) & ~(box - 1);
+#pragma unroll
+                    for (int half = 0; half < C::kHalves; ++half)
+                        ptx::tma_load_4d(dst + half * (kKeys * 128), &tm_k, fb, half * 64, s.h, in_page, id);
+#pragma unroll
+                    for (int half = 0; half < C::kHalves; ++half)
+                        ptx::tma_load_4d(dst + C::kTile + half * (kKeys * 128), &tm_v, fb, half * 64, s.h, in_page, id);
+                }
+                id = next_id;
+            }
+        }
+        if (!ok) {
+            // the copies in flight land before the CTA's shared memory goes
+            for (int i = std::max(0, it - C::kStages); i < it; ++i)
+                ptx::mbar_wait_bounded(ptx::smem_addr(full + i % C::kStages), (i / C::kStages) & 1, nullptr, nullptr);
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------- consumers
+    const int g = lane >> 2, t4 = lane & 3;
+    float *merge = reinterpret_cast<float *>(smem + C::kMergeOff);
+    float *red = reinterpret_cast<float *>(smem + C::kRedOff);
+    float *warp_m = red + kConsumers + 2 * kRows, *warp_l = warp_m + 4 * kRows;
+    int it = 0;
+    bool ok = true;
+    while (work.next(p, s)) {
+        const int all_rows = s.n * p.group, row0 = s.rb * kRows;
+        const int rows = min(kRows, all_rows - row0);
+        // this lane's rows g and g + 8 (the last row again where they do not exist)
+        const int ra = min(row0 + g, all_rows - 1), rb = min(row0 + g + 8, all_rows - 1);
+        const int ta = ra / p.group, tb = rb / p.group;
+        uint32_t qf[DP / 16][4];
+        {
+            const T *qa = static_cast<const T *>(p.q) + (int64_t)(s.token0 + ta) * p.q_token_stride +
+                          (int64_t)(s.h * p.group + ra % p.group) * p.q_head_stride;
+            const T *qb = static_cast<const T *>(p.q) + (int64_t)(s.token0 + tb) * p.q_token_stride +
+                          (int64_t)(s.h * p.group + rb % p.group) * p.q_head_stride;
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+                const int c = kk * 16 + t4 * 2;
+                qf[kk][0] = c < p.head_dim ? *reinterpret_cast<const uint32_t *>(qa + c) : 0u;
+                qf[kk][1] = c < p.head_dim ? *reinterpret_cast<const uint32_t *>(qb + c) : 0u;
+                qf[kk][2] = c + 8 < p.head_dim ? *reinterpret_cast<const uint32_t *>(qa + c + 8) : 0u;
+                qf[kk][3] = c + 8 < p.head_dim ? *reinterpret_cast<const uint32_t *>(qb + c + 8) : 0u;
+            }
+        }
+        float o[DP / 8][4];
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+        float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
+
+        for (int tile = s.tile0; tile < s.tile1 && ok; ++tile, ++it) {
+            const int st = it % C::kStages;
+            ok = ptx::mbar_wait_bounded(ptx::smem_addr(full + st), (it / C::kStages) & 1, abort_flag, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const uint32_t kt = ptx::smem_addr(smem + st * 2 * C::kTile);
+            const uint32_t vt = kt + C::kTile;
+            // scores of this warp's 16 keys: columns 2 t4, 2 t4 + 1 of keys 0-7 and 8-15
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const int krow = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+                uint32_t b[4];
+                ptx::ldmatrix_x4(piece<DP>(kt, krow, kk * 2 + ((lane >> 3) & 1)), b);
+                mma<T>(sc[0], qf[kk], b[0], b[1]);
+                mma<T>(sc[1], qf[kk], b[2], b[3]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[i][e] *= p.scale_log2;
+            const int key0 = tile * kKeys + warp * 16;       // this warp's first key
+            const bool drafted = key0 + 16 > s.ctx;          // drafted (or no) keys among them
+            uint32_t seen_a = 0xFFFFFFFFu, seen_b = 0xFFFFFFFFu;   // bit k: key0 + k is visible
+            if (drafted) {
+                const int before = s.ctx - key0;             // keys of the context among the 16
+                if (before > 0) {
+                    const uint32_t ctx_bits = (1u << before) - 1;
+                    seen_a = ctx_bits | (seen_bits(p, s, ta, 0) << before);
+                    seen_b = ctx_bits | (seen_bits(p, s, tb, 0) << before);
+                } else {
+                    seen_a = seen_bits(p, s, ta, -before);
+                    seen_b = seen_bits(p, s, tb, -before);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int k = i * 8 + t4 * 2 + e;
+                        if (!((seen_a >> k) & 1u)) sc[i][e] = -INFINITY;
+                        if (!((seen_b >> k) & 1u)) sc[i][2 + e] = -INFINITY;
+                    }
+            }
+            float na = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+            float nb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                na = fmaxf(na, __shfl_xor_sync(0xFFFFFFFFu, na, d));
+                nb = fmaxf(nb, __shfl_xor_sync(0xFFFFFFFFu, nb, d));
+            }
+            // the maximum less the weights' scaling; a row without a visible key keeps -inf
+            na = fmaxf(ma, na - Elem<T>::kBias);
+            nb = fmaxf(mb, nb - Elem<T>::kBias);
+            const float ea = na == -INFINITY ? 0.f : na, eb = nb == -INFINITY ? 0.f : nb;
+            if (__any_sync(0xFFFFFFFFu, na != ma || nb != mb)) {
+                const float fa = exp2_fast(ma - ea), fb = exp2_fast(mb - eb);
+                la *= fa;
+                lb *= fb;
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) {
+                    o[i][0] *= fa;
+                    o[i][1] *= fa;
+                    o[i][2] *= fb;
+                    o[i][3] *= fb;
+                }
+                ma = na;
+                mb = nb;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sc[i][0] = exp2_fast(sc[i][0] - ea);
+                sc[i][1] = exp2_fast(sc[i][1] - ea);
+                sc[i][2] = exp2_fast(sc[i][2] - eb);
+                sc[i][3] = exp2_fast(sc[i][3] - eb);
+                la += sc[i][0] + sc[i][1];
+                lb += sc[i][2] + sc[i][3];
+            }
+            const uint32_t pf[4] = {Elem<T>::pack(sc[0][0], sc[0][1]), Elem<T>::pack(sc[0][2], sc[0][3]),
+                                    Elem<T>::pack(sc[1][0], sc[1][1]), Elem<T>::pack(sc[1][2], sc[1][3])};
+            if (drafted) {
+                // Values of keys past the last one may be anything: made zero, so
+                // that a weight of zero takes nothing from them. A drafted key's
+                // infinities and NaN reach the rows that see it only.
+                bool odd = false;
+                for (int e = lane; e < 16 * (DP / 8); e += 32) {
+                    const int r = e / (DP / 8), key = key0 + r;
+                    const uint32_t at = piece<DP>(vt, warp * 16 + r, e % (DP / 8));
+                    if (key >= s.ctx + s.n) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                    } else if (key >= s.ctx) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) odd = odd || has_nonfinite<T>(w[i]);
+                    }
+                }
+                __syncwarp();
+                if (__any_sync(0xFFFFFFFFu, odd)) {
+                    for (int k = max(0, s.ctx - key0); k < 16 && key0 + k < s.ctx + s.n; ++k) {
+                        const bool sa = (seen_a >> k) & 1u, sb = (seen_b >> k) & 1u;
+#pragma unroll
+                        for (int i = 0; i < DP / 8; ++i) {
+                            uint32_t w;
+                            const uint32_t at = piece<DP>(vt, warp * 16 + k, i) + t4 * 4;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint16_t half = (uint16_t)(w >> (16 * e));
+                                if ((half & Elem<T>::kExpMask) != Elem<T>::kExpMask) continue;
+                                const float v = Elem<T>::to_float(half);
+                                if (sa) o[i][e] += v;
+                                if (sb) o[i][2 + e] += v;
+                            }
+                        }
+                        __syncwarp();
+                        // the lanes of row 0 of the fragment clear what all have read
+                        for (int c = lane; c < DP / 2; c += 32) {
+                            const uint32_t at = piece<DP>(vt, warp * 16 + k, c >> 2) + (c & 3) * 4;
+                            uint32_t w;
+                            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                            if ((w & Elem<T>::kExpMask) == Elem<T>::kExpMask) w &= 0xFFFF0000u;
+                            if (((w >> 16) & Elem<T>::kExpMask) == Elem<T>::kExpMask) w &= 0x0000FFFFu;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+                        }
+                        __syncwarp();
+                    }
+                }
+                // these stores come before the TMA's next write of the stage
+                ptx::fence_proxy_async_smem();
+            }
+            const int vrow = warp * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < DP / 16; ++i) {
+                uint32_t b[4];
+                ldmatrix_x4_trans(piece<DP>(vt, vrow, i * 2 + (lane >> 4)), b);
+                mma<T>(o[2 * i], pf, b[0], b[1]);
+                mma<T>(o[2 * i + 1], pf, b[2], b[3]);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(empty + st));
+        }
+
+        // ---- the four warps' sums become one, in warp 0
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            la += __shfl_xor_sync(0xFFFFFFFFu, la, d);
+            lb += __shfl_xor_sync(0xFFFFFFFFu, lb, d);
+        }
+        if (t4 == 0) {
+            warp_m[warp * kRows + g] = ma;
+            warp_m[warp * kRows + g + 8] = mb;
+            warp_l[warp * kRows + g] = la;
+            warp_l[warp * kRows + g + 8] = lb;
+        }
+        // all four leave together if one gave up
+        if (!ptx::named_barrier_and(1, kConsumers, ok)) return;
+        float m2a = -INFINITY, m2b = -INFINITY, l2a = 0.f, l2b = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            m2a = fmaxf(m2a, warp_m[w * kRows + g]);
+            m2b = fmaxf(m2b, warp_m[w * kRows + g + 8]);
+        }
+        const float ea = m2a == -INFINITY ? 0.f : m2a, eb = m2b == -INFINITY ? 0.f : m2b;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            l2a += warp_l[w * kRows + g] * exp2_fast(warp_m[w * kRows + g] - ea);
+            l2b += warp_l[w * kRows + g + 8] * exp2_fast(warp_m[w * kRows + g + 8] - eb);
+        }
+        const float fa = exp2_fast(ma - ea), fb = exp2_fast(mb - eb);
+#pragma unroll
+        for (int i = 0; i < DP / 8; ++i) {
+            o[i][0] *= fa;
+            o[i][1] *= fa;
+            o[i][2] *= fb;
+            o[i][3] *= fb;
+        }
+        float4 *mine = reinterpret_cast<float4 *>(merge) + lane;
+#pragma unroll 1
+        for (int w = 1; w < 4; ++w) {
+            if (warp == w)
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) mine[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+            ptx::named_barrier(1, kConsumers);
+            if (warp == 0)
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) {
+                    const float4 v = mine[i * 32];
+                    o[i][0] += v.x;
+                    o[i][1] += v.y;
+                    o[i][2] += v.z;
+                    o[i][3] += v.w;
+                }
+            ptx::named_barrier(1, kConsumers);
+        }
+        if (s.whole()) {
+            if (warp == 0) {
+                const float ia = l2a == 0.f ? 0.f : 1.f / l2a, ib = l2b == 0.f ? 0.f : 1.f / l2b;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int r = g + 8 * half;
+                    if (r >= rows) continue;
+                    const int64_t t = s.token0 + (row0 + r) / p.group;
+                    const int64_t head = (int64_t)s.h * p.group + (row0 + r) % p.group;
+                    T *out = static_cast<T *>(p.out) + (t * p.q_heads + head) * p.head_dim;
+                    const float inv = half ? ib : ia;
+#pragma unroll
+                    for (int i = 0; i < DP / 8; ++i)
+                        if (i * 8 < p.head_dim)
+                            *reinterpret_cast<uint32_t *>(out + i * 8 + t4 * 2) =
+                                Elem<T>::pack(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
+                    if (t4 == 0) store_lse(p, s, row0 + r, half ? eb : ea, half ? l2b : l2a);
+                }
+            }
+        } else {
+            if (warp == 0) {
+                float *slot = p.partials + (int64_t)work.slot_of(blockIdx.x, s.u0) * slot_floats(kRows, DP);
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) {
+                    __stcg(reinterpret_cast<float2 *>(slot + g * DP + i * 8 + t4 * 2), make_float2(o[i][0], o[i][1]));
+                    __stcg(reinterpret_cast<float2 *>(slot + (g + 8) * DP + i * 8 + t4 * 2), make_float2(o[i][2], o[i][3]));
+                }
+                if (t4 == 0) {
+                    __stcg(slot + kRows * DP + g, m2a);
+                    __stcg(slot + kRows * DP + g + 8, m2b);
+                    __stcg(slot + kRows * DP + kRows + g, l2a);
+                    __stcg(slot + kRows * DP + kRows + g + 8, l2b);
+                }
+            }
+            join<T, kRows, DP, kConsumers>(p, work, s, threadIdx.x, rows, red, 1);
+        }
+    }
+}
+
+struct LaunchInfo {
+    int ctas = 0;            // CTAs that fit the GPU at once
+    cudaError_t err = cudaSuccess;
+    unsigned gen = 0;
+};
+
+template <typename T, int DP>
+LaunchInfo launch_info()
+{
+    static std::mutex mu;
+    static std::map<int, LaunchInfo> cache;
+    int dev = 0;
+    LaunchInfo li;
+    li.err = cudaGetDevice(&dev);
+    if (li.err != cudaSuccess) return li;
+    const unsigned gen = cache_generation();
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = cache.find(dev);
+    if (it != cache.end() && it->second.gen == gen) return it->second;
+    li.gen = gen;
+    int sms = 0, per_sm = 0;
+    li.err = cudaFuncSetAttribute(attention_rows_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  Cfg<DP>::kSmem);
+    if (li.err == cudaSuccess) li.err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (li.err == cudaSuccess)
+        li.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_rows_kernel<T, DP>, kThreads,
+                                                               Cfg<DP>::kSmem);
+    li.ctas = sms * std::max(1, per_sm);
+    if (li.err == cudaSuccess) cache[dev] = li;
+    return li;
+}
+
+template <typename T, int DP>
+cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
+{
+    const LaunchInfo li = launch_info<T, DP>();
+    if (li.err != cudaSuccess) return li.err;
+    Params p = make_params(a);
+    CUtensorMap tk, tv;
+    if (!make_cache_map(&tk, a, a.k_cache, kKeys) || !make_cache_map(&tv, a, a.v_cache, kKeys))
+        return cudaErrorInvalidValue;
+    // a launch no larger than the work the bounds allow
+    const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
+    const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
+    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * tiles;
+    p.min_units = 4;
+    const int ctas = (int)std::min<int64_t>(li.ctas, std::max<int64_t>(1, units / p.min_units));
+    Scratch sc{};
+    if (!get_scratch(stream, (size_t)2 * ctas * slot_floats(kRows, DP),
+                     (size_t)a.kv_heads * ((size_t)(a.tokens * p.group) / kRows + (size_t)a.B), &sc))
+        return cudaErrorMemoryAllocation;
+    p.partials = sc.partials;
+    p.counters = sc.counters;
+#ifdef AWQ_FAULT_TEST
+    p.fault = fault_injection();
+#endif
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<DP>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_rows_kernel<T, DP>, tk, tv, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+} // namespace
+
+Params make_params(const awq_tree_attention_t &a)
+{
+    Params p{};
+    p.q = a.q;
+    p.q_token_stride = a.q_token_stride;
+    p.q_head_stride = a.q_head_stride;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.table = a.block_table;
+    p.table_stride = a.table_stride;
+    p.ctx = a.context_lens;
+    p.cu = a.cu_new;
+    p.mask = a.tree_mask;
+    p.status = device_status_word();
+    p.table_width = (int)a.table_width;
+    p.mask_words = (int)a.mask_words;
+    p.B = (int)a.B;
+    p.tokens = (int)a.tokens;
+    p.q_heads = (int)a.q_heads;
+    p.kv_heads = (int)a.kv_heads;
+    p.group = (int)(a.q_heads / a.kv_heads);
+    p.head_dim = (int)a.head_dim;
+    p.num_blocks = (int)a.num_blocks;
+    while ((int64_t(1) << p.shift) < a.block_size) ++p.shift;
+    p.min_units = 1;
+    p.scale_log2 = a.scale * 1.44269504088896341f;
+    return p;
+}
+
+bool make_cache_map(CUtensorMap *m, const awq_tree_attention_t &a, const awq_cache_t &c, int tile_keys)
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.kv_heads, (cuuint64_t)a.block_size,
+                          (cuuint64_t)a.num_blocks};
+    cuuint64_t strides[3] = {(cuuint64_t)c.head_stride * 2, (cuuint64_t)c.token_stride * 2,
+                             (cuuint64_t)c.block_stride * 2};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)std::min<int64_t>(a.block_size, tile_keys), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, a.dtype == AWQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c.data,
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_rows_any(const awq_tree_attention_t &a, cudaStream_t stream)
+{
+    const bool f16 = a.dtype == AWQ_F16;
+    if (a.head_dim <= 64)
+        return f16 ? launch_rows<__half, 64>(a, stream) : launch_rows<__nv_bfloat16, 64>(a, stream);
+    if (a.head_dim <= 128)
+        return f16 ? launch_rows<__half, 128>(a, stream) : launch_rows<__nv_bfloat16, 128>(a, stream);
+    return f16 ? launch_rows<__half, 256>(a, stream) : launch_rows<__nv_bfloat16, 256>(a, stream);
+}
+
+} // namespace attn
+
+cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream)
+{
+    return attn::launch_rows_any(a, stream);
+}
+
+void tree_attention_scratch(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int sms,
+                            size_t *partial_floats, size_t *n_counters)
+{
+    const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
+    *partial_floats = (size_t)2 * sms * 4 * attn::slot_floats(attn::kRows, dp);
+    *n_counters = (size_t)kv_heads * ((size_t)(tokens * (q_heads / kv_heads)) / attn::kRows + (size_t)B);
+}
+
+} // namespace awq

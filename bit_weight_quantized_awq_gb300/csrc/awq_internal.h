@@ -6,6 +6,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "../../include/awq_gb300.h"
+
 namespace awq {
 
 // One validated forward/dequant problem. g is the resolved group size (the
@@ -51,6 +53,7 @@ int fault_injection();
 unsigned int *device_status_word();
 constexpr unsigned int kStatusTimeout = 1u;
 constexpr unsigned int kStatusBadIndex = 2u;   // a group or row index out of range
+constexpr unsigned int kStatusTooLarge = 4u;   // a capacity exceeded (free blocks, table width, tokens)
 
 // Scratch for `stream` on the current device, grown to at least the given
 // sizes. Returns false if an allocation failed, or if the stream's scratch
@@ -122,6 +125,37 @@ cudaError_t launch_gather_rows(const int32_t *src, const int32_t *perm, int32_t 
 cudaError_t launch_gather_cols(const void *x, int64_t ldx, const int32_t *perm, void *xs, int64_t M,
                                int64_t K, cudaStream_t stream);
 bool get_xs_scratch(cudaStream_t stream, size_t bytes, void **out);
+// ---- the decoding step around the layers (arguments already checked) ----
+
+struct PlanProblem {
+    const int32_t *context_lens, *new_lens;
+    int32_t *block_table;
+    const int32_t *free_blocks, *parents;
+    int32_t *cu_new;
+    int64_t *slot_map;
+    int32_t *positions, *token_request, *tree_mask, *counts;
+    int64_t table_stride;
+    int B, table_width, num_free, block_size, max_tokens, mask_words;
+};
+cudaError_t launch_paged_plan(const PlanProblem &p, cudaStream_t stream);
+
+struct AppendProblem {
+    const void *k, *v;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    awq_cache_t k_cache, v_cache;
+    const int64_t *slot_map;
+    int64_t tokens, num_blocks;
+    int block_size, kv_heads, head_dim;
+};
+cudaError_t launch_kv_append(const AppendProblem &p, cudaStream_t stream);
+
+cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream);
+// largest scratch any tree-attention launch of these bounds asks for
+void tree_attention_scratch(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                            int sms, size_t *partial_floats, size_t *n_counters);
+
+cudaError_t launch_process_logits(const awq_logits_t &a, cudaStream_t stream);
+
 // fp16 weight columns per window of the dequantise-then-GEMM path
 int64_t dequant_gemm_window(int64_t K, int64_t N);
 

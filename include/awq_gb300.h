@@ -380,6 +380,214 @@ awq_status_t awq_linear_forward_decode_noalloc(const void *x, const int32_t *qwe
 awq_status_t awq_reserve(int64_t max_M, int64_t max_K, int64_t max_N, unsigned flags,
                          awq_stream_t stream);
 
+/*
+ * ---- The decoding step around the quantised layers -------------------------
+ *
+ * Between the qkv and the output projection of a serving process lies a paged
+ * cache of keys and values; after the head lie the logits. The four calls below
+ * plan, fill and read that cache for one step -- single tokens, drafted token
+ * trees or causal chunks of new tokens, ragged over the requests -- and apply
+ * the sampling controls to the logits. Requests are numbered 0 .. B - 1; the
+ * new tokens of all requests lie one after another (request b's are rows
+ * cu_new[b] .. cu_new[b + 1] - 1). A cache is [num_blocks, block_size,
+ * kv_heads, head_dim] of fp16 or bf16; slot s is token s % block_size of block
+ * s / block_size; position i of request b lives in block
+ * block_table[b, i / block_size].
+ *
+ * Lengths, tables and masks are read on the device, so a captured call serves
+ * every later step of the same bounds. What cannot be checked before the kernel
+ * runs (a length, an index, a table entry out of range) never makes it read or
+ * write out of bounds: it is recorded for awq_last_device_status, as
+ * AWQ_ERR_INVALID_ARG, or AWQ_ERR_TOO_LARGE where a capacity was exceeded.
+ * Integer arrays need their natural alignment only.
+ */
+typedef enum { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 } awq_dtype_t;
+
+/*
+ * awq_paged_plan -- block tables, slot map, positions and ancestor masks of one
+ * step, from request lengths, in one launch:
+ *   cu_new[b]   = sum of new_lens[0 .. b - 1]                      int32 [B + 1]
+ *   have[b]     = ceil(context_lens[b] / block_size)
+ *   need[b]     = ceil((context_lens[b] + new_lens[b]) / block_size) - have[b]
+ *   block_table[b, have[b] + j] = free_blocks[need[0] + .. + need[b - 1] + j],
+ *                 j < need[b]; other entries are left as they are
+ *   slot_map[t], positions[t], token_request[t] of new token i of request b
+ *               (t = cu_new[b] + i): its slot in the cache (int64), the context
+ *               length plus its depth in the tree (int32), and b (int32);
+ *               entries from cu_new[B] to max_tokens - 1 get -1, 0 and -1
+ *   tree_mask[t, :] = bit i, and tree_mask of its parent               int32
+ *   counts      = {cu_new[B], need[0] + .. + need[B - 1]}            int32 [2]
+ *
+ *   context_lens int32 [B]  tokens of each request already in the cache (read)
+ *   new_lens     int32 [B]  tokens this step adds                       (read)
+ *   block_table  int32 [B, table_width], rows table_stride apart (read, written)
+ *   free_blocks  int32 [num_free], taken from the start on (read; the caller
+ *                drops counts[1] of them)
+ *   parents      int32 [max_tokens] or NULL: the index within its request of each
+ *                new token's parent, smaller than its own, or -1 for a child of
+ *                the context's last token. NULL: each token follows the one before
+ *                it (parent i - 1; depth i).
+ *   tree_mask    int32 [max_tokens, mask_words] or NULL with mask_words == 0;
+ *                mask_words * 32 >= the longest new length
+ * A token whose page is not in the table's width, or for which no free block is
+ * left, gets slot -1, and the device status becomes AWQ_ERR_TOO_LARGE (so does
+ * it when cu_new[B] > max_tokens: the tokens past it are dropped, or when a
+ * request has more new tokens than its mask has bits).
+ * A negative length counts as 0, a bad parent as -1, a negative table entry of
+ * the context gives slot -1; each is reported as AWQ_ERR_INVALID_ARG.
+ *
+ * Requires 0 <= B <= 16384, block_size a power of two from 16 to 1024,
+ * 0 <= max_tokens <= 2^30, table_stride >= table_width > 0, num_free >= 0,
+ * 0 <= mask_words <= 1024 (AWQ_ERR_INVALID_ARG otherwise).
+ */
+awq_status_t awq_paged_plan(const int32_t *context_lens, const int32_t *new_lens, int64_t B,
+                            int32_t *block_table, int64_t table_width, int64_t table_stride,
+                            const int32_t *free_blocks, int64_t num_free, int64_t block_size,
+                            const int32_t *parents, int64_t max_tokens, int32_t *cu_new,
+                            int64_t *slot_map, int32_t *positions, int32_t *token_request,
+                            int32_t *tree_mask, int64_t mask_words, int32_t *counts,
+                            awq_stream_t stream);
+
+/*
+ * A paged cache of keys or values. Strides are in elements; the head_dim
+ * elements of one head are contiguous. data and every stride * 2 are multiples
+ * of 16 bytes. Any order of the block, token and head axes will do.
+ */
+typedef struct {
+    void *data;
+    int64_t block_stride, token_stride, head_stride;
+} awq_cache_t;
+
+/*
+ * awq_kv_append -- cache[slot_map[t]] = k[t] (and v[t]) for t < tokens: the new
+ * tokens' keys and values into the slots awq_paged_plan gave them. A slot of -1
+ * is skipped; any other slot outside [0, num_blocks * block_size) is skipped and
+ * reported. Two tokens with the same slot leave either one's values.
+ *   k, v   [tokens, kv_heads, head_dim], 16-byte aligned, strides in elements
+ *          (multiples of 8): the parts of a fused qkv projection's rows serve as
+ *          they are
+ * Elements are 16-bit (fp16 or bf16) and copied as they are. head_dim % 8 == 0.
+ */
+awq_status_t awq_kv_append(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                           const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                           const awq_cache_t *k_cache, const awq_cache_t *v_cache,
+                           const int64_t *slot_map, int64_t tokens, int64_t num_blocks,
+                           int64_t block_size, int64_t kv_heads, int64_t head_dim,
+                           awq_stream_t stream);
+
+/*
+ * awq_tree_attention -- attention of the new tokens over their requests' caches,
+ * into which their own keys and values have been appended:
+ *   s[t, h, j] = scale * (q[t, h, :] . k[j, h / group, :])   over the visible j
+ *   out[t, h, :] = sum_j softmax_j(s[t, h, :]) v[j, h / group, :]
+ *   lse[t, h]    = ln sum_j exp(s[t, h, j])
+ * with group = q_heads / kv_heads. New token i of a request sees all of its
+ * context (positions below context_lens[b]) and the new token j (at position
+ * context_lens[b] + j) if bit j of tree_mask[t, :] is set, or, with
+ * tree_mask == NULL, if j <= i. Bits at or past the request's new length count
+ * for nothing. A row that sees no key gives zeros and lse = -inf. Keys and values that
+ * a row does not see do not reach it, whatever they hold (infinities and NaN too).
+ * Scores, maxima, sums and the output are held in fp32; the softmax weights are
+ * rounded to q's type for the product with v; the output is rounded once.
+ *
+ *   q             [tokens, q_heads, head_dim] fp16 or bf16, 16-byte aligned,
+ *                 strides in elements, multiples of 8
+ *   out           [tokens, q_heads, head_dim], contiguous, q's type
+ *   lse           fp32 [tokens, q_heads] or NULL
+ *   block_table   int32 [B, table_width], rows table_stride apart
+ *   context_lens  int32 [B], cu_new int32 [B + 1], both of this step
+ *   max_new, max_context  bounds of the new and the context lengths: they size
+ *                 the launch and choose the kernel, and every length within the
+ *                 table's width is still computed right if they are too small
+ * Rows of q past cu_new[B] are left unwritten in out.
+ *
+ * Requires head_dim % 8 == 0 and <= 256, q_heads % kv_heads == 0, block_size a
+ * power of two from 16 to 1024, num_blocks < 2^31, table_width * block_size < 2^31 - 1024,
+ * tokens * q_heads < 2^31, B <= 16384 (AWQ_ERR_INVALID_ARG otherwise). If cu_new decreases or leaves [0, tokens], or
+ * a length is negative or exceeds the table's width, nothing is written and the
+ * device status becomes AWQ_ERR_INVALID_ARG; so it does for a table entry outside
+ * [0, num_blocks) below a request's length, whose page then reads as zeros.
+ */
+typedef struct {
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *out;
+    float *lse;
+    awq_cache_t k_cache, v_cache;
+    const int32_t *block_table;
+    int64_t table_width, table_stride;
+    const int32_t *context_lens, *cu_new, *tree_mask;
+    int64_t mask_words;
+    int64_t B, tokens, q_heads, kv_heads, head_dim, num_blocks, block_size, max_new, max_context;
+    float scale;
+    int32_t dtype;   /* AWQ_F16 or AWQ_BF16 */
+} awq_tree_attention_t;
+awq_status_t awq_tree_attention(const awq_tree_attention_t *args, awq_stream_t stream);
+
+/*
+ * awq_reserve_tree_attention -- awq_reserve for awq_tree_attention: sizes the
+ * scratch of `stream` for calls of up to max_tokens new tokens in max_requests
+ * requests, and leaves it as it was reserved or not. A reserved stream refuses
+ * calls beyond its reservations with AWQ_ERR_TOO_LARGE.
+ */
+awq_status_t awq_reserve_tree_attention(int64_t max_tokens, int64_t max_requests, int64_t q_heads,
+                                        int64_t kv_heads, int64_t head_dim, awq_stream_t stream);
+
+/*
+ * awq_process_logits -- penalties for repeated tokens, biases and a grammar mask
+ * on logits[rows, vocab], in fp32, rounded once. For row r of request
+ * b = row_request[r] (r itself if NULL), with count = how often the token occurs
+ * in the generated part of b's history and on the row's draft path, and known =
+ * whether it occurs there or in the prompt part:
+ *   x = logits[r, v]
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]      if known
+ *   x = x - frequency[b] * count - (count > 0 ? presence[b] : 0)
+ *   x = x + sum of bias_values of token v in b's list
+ *   out[r, v] = x, or -inf if bit v of grammar_mask[grammar_rows[r], :] is 0
+ *
+ *   history        int32 tokens of all requests, request b's at history_offsets[b]
+ *                  .. history_offsets[b + 1] - 1 (int32 [B + 1]), the first
+ *                  prompt_lens[b] of them its prompt (NULL: all generated).
+ *                  Negative tokens are skipped (padding). history (history_size
+ *                  tokens in all) may be NULL.
+ *   repetition, frequency, presence  fp32 [B], or NULL for 1, 0 and 0
+ *   draft_tokens   int32 [rows] or NULL: the tokens of the drafted trees; row r's
+ *                  path is draft_tokens[cu_new[b] + j] for the bits j of
+ *                  tree_mask[r, :] (mask_words words; NULL: for
+ *                  j <= r - cu_new[b]), as awq_paged_plan lays them out
+ *   bias_tokens    int32, bias_values fp32: request b's pairs at bias_offsets[b] ..
+ *                  bias_offsets[b + 1] - 1 (int32 [B + 1]), sorted by token; several
+ *                  of one token are added up in their order. All three (bias_size
+ *                  pairs in all), or NULL
+ *   grammar_mask   int32 [grammar_count, ceil(vocab / 32)] or NULL, contiguous;
+ *                  bit v % 32 of word v / 32
+ *   grammar_rows   int32 [rows] or NULL (row r has mask r): -1 means no mask
+ *   logits, out    fp16, bf16 or fp32 (dtype), the elements of a row contiguous,
+ *                  rows `*_row_stride` elements apart; out == logits is allowed
+ *                  (with the same stride)
+ * A token, offset, request or mask index out of range is skipped and reported; a
+ * bias list that is not sorted is reported. Requires rows >= 0, 0 < vocab <= 2^27,
+ * 0 <= B < 2^31, history_size and bias_size < 2^31, logits and out aligned to their elements.
+ */
+typedef struct {
+    const void *logits;
+    void *out;
+    int64_t logits_row_stride, out_row_stride, rows, vocab, B;
+    const int32_t *row_request;
+    const int32_t *history, *history_offsets, *prompt_lens;
+    int64_t history_size;
+    const float *repetition, *frequency, *presence;
+    const int32_t *draft_tokens, *cu_new, *tree_mask;
+    int64_t mask_words;
+    const int32_t *bias_tokens, *bias_offsets;
+    const float *bias_values;
+    int64_t bias_size;
+    const int32_t *grammar_mask, *grammar_rows;
+    int64_t grammar_count;
+    int32_t dtype;
+} awq_logits_t;
+awq_status_t awq_process_logits(const awq_logits_t *args, awq_stream_t stream);
+
 /* Static description of a status code. Never NULL. */
 const char *awq_status_string(awq_status_t status);
 
@@ -387,8 +595,9 @@ const char *awq_status_string(awq_status_t status);
  * awq_last_device_status -- synchronises `stream`, then reads and clears the
  * current device's status word. Returns AWQ_OK, AWQ_ERR_TIMEOUT if a kernel's
  * bounded wait ran out since the last read, AWQ_ERR_INVALID_ARG if a g_idx
- * entry was outside [0, G), or AWQ_ERR_CUDA if a synchronisation or reset
- * failed.
+ * entry was outside [0, G) or a length, index or table entry of the decoding
+ * step was out of range, AWQ_ERR_TOO_LARGE if one exceeded a capacity, or
+ * AWQ_ERR_CUDA if a synchronisation or reset failed.
  *
  * After a timeout: the kernel that gave up wrote no result, and it may have
  * left split-K arrival counters of its stream non-zero. Results of later
