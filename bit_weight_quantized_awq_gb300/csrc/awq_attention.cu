@@ -423,7 +423,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     __stcg(slot + kRows * DP + kRows + g + 8, l2b);
                 }
             }
-            join<T, kRows, DP, kConsumers>(p, work, s, threadIdx.x, rows, red, 1);
+            join<T, kRows, DP, kConsumers, false>(p, work, s, threadIdx.x, rows, red, 1);
         }
     }
 }
@@ -510,6 +510,10 @@ Params make_params(const awq_tree_attention_t &a)
     p.lse = a.lse;
     p.table = a.block_table;
     p.table_stride = a.table_stride;
+    p.v_data = a.v_cache.data;
+    p.v_block_stride = a.v_cache.block_stride;
+    p.v_token_stride = a.v_cache.token_stride;
+    p.v_head_stride = a.v_cache.head_stride;
     p.ctx = a.context_lens;
     p.cu = a.cu_new;
     p.mask = a.tree_mask;
@@ -566,6 +570,8 @@ cudaError_t launch_rows_any(const awq_tree_attention_t &a, cudaStream_t stream)
 
 cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream)
 {
+    const int64_t rows = a.max_new * (a.q_heads / a.kv_heads);
+    if (rows > attn::kRows && a.head_dim <= 128) return attn::launch_tc_any(a, stream);
     return attn::launch_rows_any(a, stream);
 }
 
@@ -573,7 +579,8 @@ void tree_attention_scratch(int64_t tokens, int64_t B, int64_t q_heads, int64_t 
                             size_t *partial_floats, size_t *n_counters)
 {
     const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    *partial_floats = (size_t)2 * sms * 4 * attn::slot_floats(attn::kRows, dp);
+    *partial_floats = std::max((size_t)2 * sms * 4 * attn::slot_floats(attn::kRows, dp),
+                               attn::tc_partial_floats(sms, head_dim));
     *n_counters = (size_t)kv_heads * ((size_t)(tokens * (q_heads / kv_heads)) / attn::kRows + (size_t)B);
 }
 

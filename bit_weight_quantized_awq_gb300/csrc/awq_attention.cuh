@@ -38,6 +38,8 @@ struct Params {
     float *lse;
     const int32_t *table;
     int64_t table_stride;
+    const void *v_data;     // the values, for the few elements read outside the tiles
+    int64_t v_block_stride, v_token_stride, v_head_stride;
     const int32_t *ctx, *cu, *mask;
     float *partials;
     unsigned int *counters, *status;
@@ -329,7 +331,8 @@ __device__ __forceinline__ void store_lse(const Params &p, const Segment &s, int
 // Called by the THREADS consecutive threads whose index is tid, after they have
 // written this CTA's piece to its slot; `rows` of the block's RB rows exist.
 // red: shared, THREADS + 2 RB floats. bar: a named barrier of these threads.
-template <typename T, int RB, int DP, int THREADS, typename W>
+// kByColumn: a slot's O is stored [column / 4][row][4] instead of [row][column].
+template <typename T, int RB, int DP, int THREADS, bool kByColumn, typename W>
 __device__ void join(const Params &p, const W &work, const Segment &s, int tid, int rows, float *red, int bar)
 {
     __shared__ unsigned arrived;
@@ -376,13 +379,14 @@ __device__ void join(const Params &p, const W &work, const Segment &s, int tid, 
         ptx::named_barrier(bar, THREADS);
     }
     for (int e = tid; e < rows * (DP / 4); e += THREADS) {
-        const int r = e / (DP / 4), c4 = (e % (DP / 4)) * 4;
+        const int r = kByColumn ? e % rows : e / (DP / 4), c4 = (kByColumn ? e / rows : e % (DP / 4)) * 4;
+        const int at = kByColumn ? c4 * RB + r * 4 : r * DP + c4;
         const float mx = row_m[r], l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int c = c0; c <= c1; ++c) {
             const float *slot = p.partials + (int64_t)work.slot_of(c, s.u0) * SF;
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot + r * DP + c4));
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot + at));
             const float w = exp2_fast(__ldcg(slot + RB * DP + r) - mx);
             acc.x += v.x * w;
             acc.y += v.y * w;

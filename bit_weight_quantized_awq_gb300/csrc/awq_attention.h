@@ -18,5 +18,9 @@ Params make_params(const awq_tree_attention_t &a);
 // one head for min(block_size, tile_keys) tokens of one block, 128-byte swizzle.
 bool make_cache_map(CUtensorMap *m, const awq_tree_attention_t &a, const awq_cache_t &c, int tile_keys);
 
+// The tensor-core kernel (head_dim <= 128), and the partial sums its largest launch keeps.
+cudaError_t launch_tc_any(const awq_tree_attention_t &a, cudaStream_t stream);
+size_t tc_partial_floats(int sms, int64_t head_dim);
+
 } // namespace attn
 } // namespace awq

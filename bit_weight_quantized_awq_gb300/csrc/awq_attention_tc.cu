@@ -1,0 +1,629 @@
+// awq_attention_tc.cu -- attention of a step's new tokens over a paged cache, for
+// many rows a key-value head (drafted trees, chunks of a prompt), on the 5th-generation
+// tensor cores; head_dim up to 128. awq_attention.cuh has the split of the work.
+//
+// A row block is 256 rows, a tile 128 keys. Two streams of work alternate on the
+// tensor cores, so that one multiplies while the other's softmax runs:
+//   more than 128 rows in the block: stream i has rows 128 i .. 128 i + 127 and
+//     both take every tile (a tile is read once for 256 rows);
+//   128 rows or fewer: both have the same rows, stream i takes tiles i, i + 2, ..,
+//     and their two sums are joined at the segment's end.
+// For a stream and tile: S = Q K^T (tcgen05, 128 x 128, into tensor memory), the
+// stream's four warps read S (a thread has one row: no shuffles), write
+// P = exp2(S - m) over it as 16-bit values, and O += P V takes P from tensor
+// memory. Tensor memory is full: S 2 x 128, O 2 x DP columns. The MMAs of the one
+// issuing thread run in order, so S of the stream's next tile may be written over
+// P as soon as it is issued behind O += P V.
+//
+// The maximum is lazy: O is rescaled only when a row's maximum has grown by more
+// than 2^kSlack since the last time (P then is up to 2^kSlack instead of 1, which
+// its floating-point format holds as exactly); after a few tiles that is rare, and
+// the accumulator stays where it is.
+//
+// Bounds: 4 DP flops a row and key against 4 DP bytes a key: HBM below about 280 rows a
+// head, then the tensor cores and, close to them, the exponentials (128 x 128 of
+// them a stream and tile).
+//
+//   warp 0      producer: K and V tiles, a TMA box a page, in one ring, in the order
+//               the MMAs take them
+//   warp 1      the MMAs (one thread) and tensor memory
+//   warps 2-5   softmax and epilogue of stream 0, warps 6-9 of stream 1
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include <cuda.h>
+
+#include "awq_attention.h"
+#include "awq_attention.cuh"
+#include "awq_tcgen05.cuh"
+
+namespace awq {
+namespace attn {
+namespace {
+
+constexpr int kRows = 256;       // rows of a block
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kThreads = 320;
+constexpr int kSoftmax = 256;    // threads of the softmax warps
+constexpr float kSlack = 8.f;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kO = 256;     // first column of O 0; S i is at 128 i
+
+template <int DP>
+struct Cfg {
+    static constexpr int kHalves = DP / 64;
+    static constexpr int kHalf = kKeys * 128;          // 64 columns of a tile, 128-byte rows
+    static constexpr int kTile = kHalves * kHalf;
+    static constexpr int kQ = 2 * kTile;               // 256 rows of q
+    static constexpr int kSlots = DP == 128 ? 5 : 10;  // 160 KB of tiles
+    static constexpr int kBarOff = kQ + kSlots * kTile;
+    static constexpr int kSmem = kBarOff + 512 + 1024;
+    static_assert(kSmem <= 226 * 1024, "shared memory budget");
+    // the epilogue's exchange and the join use q's space
+    static_assert((kSoftmax + 2 * kRows) * 4 + 4 * 128 * 4 <= kQ, "q's space");
+};
+
+// fp16 weights are 2^(7 + kSlack) at most, and keep all their bits down to 2^-21 of the maximum
+template <typename T>
+constexpr float kWeightBias = 0.f;
+template <>
+constexpr float kWeightBias<__half> = 7.f;
+
+// Bits of the keys key0 .. key0 + 31 that token t sees.
+__device__ __forceinline__ uint32_t seen32(const Params &p, const Segment &s, int t, int key0)
+{
+    const int before = s.ctx - key0;   // keys of the context among them
+    if (before >= 32) return 0xFFFFFFFFu;
+    if (before > 0) return ((1u << before) - 1) | (seen_bits(p, s, t, 0) << before);
+    return seen_bits(p, s, t, -before);
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ Params p)
+{
+    using C = Cfg<DP>;
+    constexpr bool kBf16 = !std::is_same<T, __half>::value;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);   // [kSlots] tile landed
+    uint64_t *freed = full + C::kSlots;      // [kSlots] MMAs that read the tile are done
+    uint64_t *s_full = freed + C::kSlots;    // [2] S of the stream is complete
+    uint64_t *p_full = s_full + 2;           // [2] P of the stream is written
+    uint64_t *o_full = p_full + 2;           // [2] O of the stream and segment is complete
+    uint64_t *q_full = o_full + 2;
+    uint64_t *drain = q_full + 1;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *odd_flag = abort_flag + 1;   // a drafted value of the segment is infinite or NaN
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    Work<kRows, kKeys> work;
+    if (!work.template find<kThreads>(p)) return;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(freed + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(s_full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(p_full + i), 4);
+            ptx::mbar_init(ptx::smem_addr(o_full + i), 1);
+        }
+        ptx::mbar_init(ptx::smem_addr(q_full), kSoftmax);
+        ptx::mbar_init(ptx::smem_addr(drain), 1);
+        *abort_flag = 0;
+        *odd_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(ptx::smem_addr(const_cast<uint32_t *>(tmem_slot)), kTmemCols);
+        tc::tmem_relinquish();
+        tc::fence_before_sync();
+    }
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    Segment s;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- producer
+        const int box = min(1 << p.shift, kKeys);
+        const int pages = kKeys / box;               // boxes of a tile, one a lane
+        int at = 0;                                  // position in the ring
+        bool ok = true;
+#ifdef AWQ_FAULT_TEST
+        if (p.fault && blockIdx.x == 0) ok = false;
+#endif
+        while (ok && work.next(p, s)) {
+            const int keys = s.ctx + s.n, nt = s.tile1 - s.tile0;
+            const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
+            const int ahead = two ? 1 : 2;           // K tiles before the first V tile
+            const int32_t *table = p.table + (int64_t)s.b * p.table_stride;
+            auto page_of = [&](int j) {
+                const int key = (s.tile0 + j) * kKeys + lane * box;
+                if (lane >= pages || j >= nt || key >= keys) return -1;
+                const int id = table[key >> p.shift];
+                if (id >= 0 && id < p.num_blocks) return id;
+                raise_status(p.status, kStatusBadIndex);
+                return p.num_blocks;                 // past the tensor: TMA fills zeros
+            };
+            auto load = [&](int j, int id, const CUtensorMap *map) {
+                const int slot = at % C::kSlots;
+                ok = ptx::mbar_wait_bounded(ptx::smem_addr(freed + slot), ((at / C::kSlots) & 1) ^ 1, abort_flag, p.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) return;
+                const uint32_t fb = ptx::smem_addr(full + slot);
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, id >= 0));
+                if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * C::kHalves * box * 128);
+                __syncwarp();
+                if (id >= 0) {
+                    const uint32_t dst = ptx::smem_addr(smem + C::kQ + slot * C::kTile) + (uint32_t)lane * box * 128;
+                    const int in_page = ((s.tile0 + j) * kKeys) & ((1 << p.shift) - 1) & ~(box - 1);
+#pragma unroll
+                    for (int half = 0; half < C::kHalves; ++half)
+                        ptx::tma_load_4d(dst + half * C::kHalf, map, fb, half * 64, s.h, in_page, id);
+                }
+                ++at;
+            };
+            // K 0 (K 1), then V j, K j + ahead: the order of the MMAs. Page
+            // numbers are fetched a tile before they are needed.
+            int id0 = page_of(0), id1 = page_of(1), id2 = page_of(2);
+            load(0, id0, &tm_k);
+            if (!two && nt > 1 && ok) load(1, id1, &tm_k);
+            for (int j = 0; j < nt && ok; ++j) {
+                const int id3 = page_of(j + 3);
+                load(j, id0, &tm_v);
+                if (ok && j + ahead < nt) load(j + ahead, two ? id1 : id2, &tm_k);
+                id0 = id1;
+                id1 = id2;
+                id2 = id3;
+            }
+        }
+        if (!ok) {
+            for (int i = std::max(0, at - C::kSlots); i < at; ++i)
+                ptx::mbar_wait_bounded(ptx::smem_addr(full + i % C::kSlots), (i / C::kSlots) & 1, nullptr, nullptr);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMAs
+        if (lane == 0) {
+            constexpr uint32_t id_qk = tc::idesc_16bit_f32(128, kKeys, false, kBf16);
+            constexpr uint32_t id_pv = tc::idesc_16bit_f32(128, DP, true, kBf16);
+            const int k_steps = (p.head_dim + 15) / 16;
+            int at = 0, seg = 0;
+            uint32_t taken[2] = {0, 0};              // P tiles used, for the parity of p_full
+            bool ok = true;
+            auto wait_tile = [&](int i) {
+                ok = ok && ptx::mbar_wait_bounded(ptx::smem_addr(full + i % C::kSlots), (i / C::kSlots) & 1, abort_flag,
+                                                  p.status);
+                tc::fence_after_sync();
+            };
+            auto tile_at = [&](int i) { return ptx::smem_addr(smem + C::kQ + (i % C::kSlots) * C::kTile); };
+            auto qk = [&](int i, int stream, int qrows) {
+                const uint32_t kt = tile_at(i), qt = ptx::smem_addr(smem) + qrows * C::kTile;
+                for (int k = 0; k < k_steps; ++k) {
+                    const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
+                    tc::mma_f16(tmem + stream * 128, tc::smem_desc_sw128(qt + off, 16, 1024),
+                                tc::smem_desc_sw128(kt + off, 16, 1024), id_qk, k != 0);
+                }
+                tc::commit(ptx::smem_addr(s_full + stream));
+            };
+            auto pv = [&](int i, int stream, bool first, bool last) {
+                const uint32_t vt = tile_at(i);
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    tc::mma_f16_ts(tmem + kO + stream * 128, tmem + stream * 128 + k * 8,
+                                   tc::smem_desc_sw128(vt + k * 2048, C::kHalf, 1024), id_pv, !first || k != 0);
+                if (last) tc::commit(ptx::smem_addr(o_full + stream));
+            };
+            auto wait_p = [&](int stream) {
+                ok = ok && ptx::mbar_wait_bounded(ptx::smem_addr(p_full + stream), taken[stream] & 1, abort_flag, p.status);
+                ++taken[stream];
+                tc::fence_after_sync();
+            };
+            auto release = [&](int i) { tc::commit(ptx::smem_addr(freed + i % C::kSlots)); };
+            while (ok && work.next(p, s)) {
+                const int nt = s.tile1 - s.tile0;
+                const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
+                ok = ptx::mbar_wait_bounded(ptx::smem_addr(q_full), seg & 1, abort_flag, p.status);
+                tc::fence_after_sync();
+                ++seg;
+                if (!two) {
+                    for (int j = 0; j < min(2, nt) && ok; ++j) {
+                        wait_tile(at);
+                        if (!ok) break;
+                        qk(at, j, 0);
+                        release(at++);
+                    }
+                    for (int j = 0; j < nt && ok; ++j) {
+                        const int st = j & 1;
+                        wait_tile(at);
+                        wait_p(st);
+                        if (!ok) break;
+                        pv(at, st, j < 2, j + 2 >= nt);
+                        release(at++);
+                        if (j + 2 < nt) {
+                            wait_tile(at);
+                            if (!ok) break;
+                            qk(at, st, 0);
+                            release(at++);
+                        }
+                    }
+                } else {
+                    wait_tile(at);
+                    if (!ok) break;
+                    qk(at, 0, 0);
+                    qk(at, 1, 1);
+                    release(at++);
+                    for (int j = 0; j < nt && ok; ++j) {
+                        const bool more = j + 1 < nt;
+                        for (int st = 0; st < 2 && ok; ++st) {
+                            if (st == 0) wait_tile(at);
+                            wait_p(st);
+                            if (!ok) break;
+                            pv(at, st, j == 0, !more);
+                            if (st == 1) release(at);
+                            if (more) {
+                                if (st == 0) wait_tile(at + 1);
+                                if (!ok) break;
+                                qk(at + 1, st, st);
+                                if (st == 1) release(at + 1);
+                            }
+                        }
+                        at += more ? 2 : 1;
+                    }
+                }
+            }
+            // every MMA issued has completed once `drain` flips
+            tc::commit(ptx::smem_addr(drain));
+            ptx::mbar_wait_bounded(ptx::smem_addr(drain), 0, nullptr, p.status);
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax, epilogue
+        const int tid = threadIdx.x - 64;
+        const int stream = tid >> 7;
+        const int quarter = warp & 3;                // tensor-memory lanes this warp may touch
+        const int row = quarter * 32 + lane;         // row of the stream's 128
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t t_s = t_lane + stream * 128, t_o = t_lane + kO + stream * 128;
+        float *red = reinterpret_cast<float *>(smem);
+        float *pair_m = red + kSoftmax + 2 * kRows, *pair_l = pair_m + 256;   // [2 streams][128 rows]
+        const bool negative = p.scale_log2 < 0.f;
+        const float scale = fabsf(p.scale_log2);
+        int base = 0;                                // ring position of the segment's first tile
+        uint32_t tiles_done = 0, segs_done[2] = {0, 0};
+        bool ok = true;
+        while (true) {
+            // everybody is done with the segment before: q's space and O are free
+            if (!ptx::named_barrier_and(1, kSoftmax, ok)) break;
+            if (!work.next(p, s)) break;
+            const int nt = s.tile1 - s.tile0;
+            const int row0 = s.rb * kRows, rows = min(kRows, s.n * p.group - row0);
+            const bool two = rows > 128;
+            if (tid == 0) *odd_flag = 0;
+            for (int e = tid; e < (two ? 256 : 128) * (DP / 8); e += kSoftmax) {
+                const int r = e / (DP / 8), c = e % (DP / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows && c * 8 < p.head_dim) {
+                    const int qr = row0 + r;
+                    v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                         (int64_t)(s.token0 + qr / p.group) * p.q_token_stride +
+                                                         (int64_t)(s.h * p.group + qr % p.group) * p.q_head_stride + c * 8);
+                    if (negative) {                  // scores are scaled by |scale|
+                        v.x ^= 0x80008000u;
+                        v.y ^= 0x80008000u;
+                        v.z ^= 0x80008000u;
+                        v.w ^= 0x80008000u;
+                    }
+                }
+                const uint32_t dst = ptx::smem_addr(smem) + (uint32_t)(r >> 7) * C::kTile + (uint32_t)(c >> 3) * C::kHalf +
+                                     (uint32_t)(r & 127) * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(ptx::smem_addr(q_full));
+
+            const int my_row = (two ? stream * 128 : 0) + row;            // of the block
+            const bool warp_works = (two ? stream * 128 : 0) + quarter * 32 < rows;
+            const int t = min(row0 + my_row, s.n * p.group - 1) / p.group;    // its token
+            float m = -INFINITY, l = 0.f;
+            for (int j = two ? 0 : stream; j < nt && ok; j += two ? 1 : 2) {
+                ok = ptx::mbar_wait_bounded(ptx::smem_addr(s_full + stream), tiles_done & 1, abort_flag, p.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                ++tiles_done;
+                tc::fence_after_sync();
+                const int key0 = (s.tile0 + j) * kKeys;
+                const bool drafted = key0 + kKeys > s.ctx;
+                if (warp_works) {
+                    float x[128];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tc::ld_32x32b_x32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
+                    tc::ld_wait();
+                    if (drafted) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t seen = seen32(p, s, t, key0 + c * 32);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((seen >> e) & 1u)) x[c * 32 + e] = -INFINITY;
+                        }
+                    }
+                    float top[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                    for (int e = 4; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], x[e]);
+                    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale - kWeightBias<T>;
+                    const bool grown = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
+                    if (__any_sync(0xFFFFFFFFu, grown)) {
+                        const float nm = grown ? mx : m;
+                        const float f = nm == m ? 1.f : exp2_fast(m - nm);
+                        m = nm;
+                        l *= f;
+                        // O so far (the MMAs that added to it are done: this
+                        // tile's S came after them)
+                        if (j >= (two ? 1 : 2)) {
+#pragma unroll 1
+                            for (int c = 0; c < DP / 32; ++c) {
+                                uint32_t o[32];
+                                tc::ld_32x32b_x32(t_o + c * 32, o);
+                                tc::ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::st_32x32b_x32(t_o + c * 32, o);
+                            }
+                        }
+                    }
+                    const float mm = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float a = exp2_fast(fmaf(x[c * 64 + 2 * e], scale, -mm));
+                            const float b = exp2_fast(fmaf(x[c * 64 + 2 * e + 1], scale, -mm));
+                            sum[(2 * e) & 3] += a;
+                            sum[(2 * e + 1) & 3] += b;
+                            w[e] = Elem<T>::pack(a, b);
+                        }
+                        tc::st_32x32b_x32(t_s + c * 32, w);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc::st_wait();
+                }
+                if (drafted && (!two || stream == 0)) {
+                    // The tile's values before P V reads them (with two row
+                    // halves stream 0's product comes first): rows past the last key
+                    // become zero, and so do infinities and NaN of drafted keys,
+                    // which the epilogue gives to the rows that see them.
+                    const int v_at = base + (two ? 1 + j + min(j, nt - 1) : min(2, nt) + j + min(j, max(0, nt - 2)));
+                    const int slot = v_at % C::kSlots;
+                    ok = ptx::mbar_wait_bounded(ptx::smem_addr(full + slot), (v_at / C::kSlots) & 1, abort_flag, p.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    const uint32_t vt = ptx::smem_addr(smem + C::kQ + slot * C::kTile);
+                    const int first = max(0, s.ctx - key0);
+                    for (int e = first * (DP / 8) + (tid & 127); e < kKeys * (DP / 8); e += 128) {
+                        const int r = e / (DP / 8), c = e % (DP / 8);
+                        const uint32_t a = vt + (uint32_t)(c >> 3) * C::kHalf + (uint32_t)r * 128 +
+                                           (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+                        if (key0 + r >= s.ctx + s.n) {
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                            continue;
+                        }
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+                        bool odd = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (has_nonfinite<T>(w[i])) {
+                                odd = true;
+                                if ((w[i] & Elem<T>::kExpMask) == Elem<T>::kExpMask) w[i] &= 0xFFFF0000u;
+                                if (((w[i] >> 16) & Elem<T>::kExpMask) == Elem<T>::kExpMask) w[i] &= 0x0000FFFFu;
+                            }
+                        if (odd) {
+                            *odd_flag = 1;
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                         ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(p_full + stream));
+            }
+            base += 2 * nt;
+
+            // ---- the segment's end: all MMAs of both streams are done
+            const int streams = two || nt > 1 ? 2 : 1;
+            for (int st = 0; st < streams; ++st) {
+                ok = ok && ptx::mbar_wait_bounded(ptx::smem_addr(o_full + st), segs_done[st] & 1, abort_flag, p.status);
+                ++segs_done[st];
+            }
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            tc::fence_after_sync();
+            if (!ptx::named_barrier_and(1, kSoftmax, ok)) {
+                ok = false;
+                break;
+            }
+            pair_m[stream * 128 + row] = m;
+            pair_l[stream * 128 + row] = l;
+            ptx::named_barrier(1, kSoftmax);
+            // factors of the two streams' O (of this one's alone with two row halves)
+            float f0 = 1.f, f1 = 0.f;
+            if (!two) {
+                const float m0 = pair_m[row], m1 = pair_m[128 + row], l0 = pair_l[row], l1 = pair_l[128 + row];
+                m = fmaxf(m0, m1);
+                const float mm = m == -INFINITY ? 0.f : m;
+                f0 = exp2_fast(m0 - mm);
+                f1 = exp2_fast(m1 - mm);
+                l = l0 * f0 + l1 * f1;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            const bool whole = s.whole(), odd = *odd_flag != 0;
+            float *slot = p.partials + (int64_t)work.slot_of(blockIdx.x, s.u0) * slot_floats(kRows, DP);
+            if (warp_works) {
+                const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+                f0 *= inv;
+                f1 *= inv;
+                // with shared rows each stream's warps write half of the columns
+                const int c_lo = two ? 0 : stream * (DP / 2), c_hi = two ? DP : c_lo + DP / 2;
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; c += 32) {
+                    uint32_t raw[32];
+                    float o[32];
+                    tc::ld_32x32b_x32((two ? t_o : t_lane + kO) + c, raw);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(raw[e]) * f0;
+                    if (!two && nt > 1) {
+                        tc::ld_32x32b_x32(t_lane + kO + 128 + c, raw);
+                        tc::ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] += __uint_as_float(raw[e]) * f1;
+                    }
+                    if (odd) {
+                        for (int key = max(s.ctx, s.tile0 * kKeys); key < min(s.ctx + s.n, s.tile1 * kKeys); ++key) {
+                            if (!(seen_bits(p, s, t, key - s.ctx) & 1u)) continue;
+                            const int id = p.table[(int64_t)s.b * p.table_stride + (key >> p.shift)];
+                            if (id < 0 || id >= p.num_blocks) continue;
+                            const T *v = static_cast<const T *>(p.v_data) + id * p.v_block_stride +
+                                         (int64_t)(key & ((1 << p.shift) - 1)) * p.v_token_stride + s.h * p.v_head_stride;
+#pragma unroll 1
+                            for (int e = 0; e < 32; ++e) {
+                                if (c + e >= p.head_dim) break;
+                                const uint16_t bits = reinterpret_cast<const uint16_t *>(v)[c + e];
+                                if ((bits & Elem<T>::kExpMask) != Elem<T>::kExpMask) continue;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i == e) o[i] += Elem<T>::to_float(bits);
+                            }
+                        }
+                    }
+                    if (whole) {
+                        if (my_row < rows) {
+                            const int64_t head = (int64_t)s.h * p.group + (row0 + my_row) % p.group;
+                            T *out = static_cast<T *>(p.out) + ((int64_t)(s.token0 + t) * p.q_heads + head) * p.head_dim + c;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                if (c + e < p.head_dim)
+                                    *reinterpret_cast<uint4 *>(out + e) =
+                                        make_uint4(Elem<T>::pack(o[e], o[e + 1]), Elem<T>::pack(o[e + 2], o[e + 3]),
+                                                   Elem<T>::pack(o[e + 4], o[e + 5]), Elem<T>::pack(o[e + 6], o[e + 7]));
+                        }
+                    } else if (my_row < rows) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            __stcg(reinterpret_cast<float4 *>(slot + (c + e) * kRows + my_row * 4),
+                                   make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                    }
+                }
+                if (my_row < rows && (two || stream == 0)) {
+                    if (whole) {
+                        store_lse(p, s, row0 + my_row, mm, l);
+                    } else {
+                        __stcg(slot + kRows * DP + my_row, m);
+                        __stcg(slot + kRows * DP + kRows + my_row, l);
+                    }
+                }
+            }
+            tc::fence_before_sync();
+            if (!whole) join<T, kRows, DP, kSoftmax, true>(p, work, s, tid, rows, red, 1);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+struct LaunchInfo {
+    int sms = 0;
+    cudaError_t err = cudaSuccess;
+    unsigned gen = 0;
+};
+
+template <typename T, int DP>
+LaunchInfo launch_info()
+{
+    static std::mutex mu;
+    static std::map<int, LaunchInfo> cache;
+    int dev = 0;
+    LaunchInfo li;
+    li.err = cudaGetDevice(&dev);
+    if (li.err != cudaSuccess) return li;
+    const unsigned gen = cache_generation();
+    std::lock_guard<std::mutex> lock(mu);
+    auto it = cache.find(dev);
+    if (it != cache.end() && it->second.gen == gen) return it->second;
+    li.gen = gen;
+    li.err = cudaFuncSetAttribute(attention_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+    if (li.err == cudaSuccess) li.err = cudaDeviceGetAttribute(&li.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (li.err == cudaSuccess) cache[dev] = li;
+    return li;
+}
+
+template <typename T, int DP>
+cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
+{
+    const LaunchInfo li = launch_info<T, DP>();
+    if (li.err != cudaSuccess) return li.err;
+    Params p = make_params(a);
+    // no zero: a masked score, -inf times the scale, has to stay -inf
+    if (p.scale_log2 == 0.f) p.scale_log2 = 1e-30f;
+    CUtensorMap tk, tv;
+    if (!make_cache_map(&tk, a, a.k_cache, kKeys) || !make_cache_map(&tv, a, a.v_cache, kKeys))
+        return cudaErrorInvalidValue;
+    const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
+    const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
+    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * tiles;
+    p.min_units = 2;
+    const int ctas = (int)std::min<int64_t>(li.sms, std::max<int64_t>(1, units / p.min_units));
+    Scratch sc{};
+    if (!get_scratch(stream, (size_t)2 * ctas * slot_floats(kRows, DP),
+                     (size_t)a.kv_heads * ((size_t)(a.tokens * p.group) / kRows + (size_t)a.B), &sc))
+        return cudaErrorMemoryAllocation;
+    p.partials = sc.partials;
+    p.counters = sc.counters;
+#ifdef AWQ_FAULT_TEST
+    p.fault = fault_injection();
+#endif
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<DP>::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, DP>, tk, tv, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+} // namespace
+
+cudaError_t launch_tc_any(const awq_tree_attention_t &a, cudaStream_t stream)
+{
+    const bool f16 = a.dtype == AWQ_F16;
+    if (a.head_dim <= 64) return f16 ? launch_tc<__half, 64>(a, stream) : launch_tc<__nv_bfloat16, 64>(a, stream);
+    return f16 ? launch_tc<__half, 128>(a, stream) : launch_tc<__nv_bfloat16, 128>(a, stream);
+}
+
+size_t tc_partial_floats(int sms, int64_t head_dim)
+{
+    return head_dim > 128 ? 0 : (size_t)2 * sms * slot_floats(kRows, head_dim <= 64 ? 64 : 128);
+}
+
+} // namespace attn
+} // namespace awq
