@@ -45,7 +45,7 @@ struct Cfg {
     static constexpr int kMergeOff = kStages * 2 * kTile;
     static constexpr int kMerge = kRows * DP * 4;        // one warp's O
     static constexpr int kRedOff = kMergeOff + kMerge;   // m and l of the four warps; the join's sums
-    static constexpr int kRed = (kConsumers + 2 * kRows + 8 * kRows) * 4;
+    static constexpr int kRed = (join_floats(kRows, kConsumers) + 8 * kRows) * 4;
     static constexpr int kBarOff = kRedOff + kRed;
     static constexpr int kSmem = kBarOff + 128 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -163,7 +163,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     const int g = lane >> 2, t4 = lane & 3;
     float *merge = reinterpret_cast<float *>(smem + C::kMergeOff);
     float *red = reinterpret_cast<float *>(smem + C::kRedOff);
-    float *warp_m = red + kConsumers + 2 * kRows, *warp_l = warp_m + 4 * kRows;
+    float *warp_m = red + join_floats(kRows, kConsumers), *warp_l = warp_m + 4 * kRows;
     int it = 0;
     bool ok = true;
     while (work.next(p, s)) {

@@ -302,6 +302,34 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// ---- waiting ----
+
+// ptx::mbar_wait_bounded without a suspend hint: for waits in a chain of short
+// steps, where a suspended thread's way back would count.
+__device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, volatile int *abort, unsigned int *status)
+{
+    long long t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63) != 63) continue;
+        if (t0 == 0) t0 = clock64();
+        if (*abort) return false;
+        if (clock64() - t0 > ptx::kWaitLimitCycles) {
+            *abort = 1;
+            if (status) atomicOr(status, 1u);
+            return false;
+        }
+    }
+}
+
 // ---- joining ----
 
 constexpr int slot_floats(int rb, int dp) { return rb * dp + 2 * rb; }
@@ -330,10 +358,17 @@ __device__ __forceinline__ void store_lse(const Params &p, const Segment &s, int
 // The CTA that finishes the last piece of a row block joins all of them.
 // Called by the THREADS consecutive threads whose index is tid, after they have
 // written this CTA's piece to its slot; `rows` of the block's RB rows exist.
-// red: shared, THREADS + 2 RB floats. bar: a named barrier of these threads.
-// kByColumn: a slot's O is stored [column / 4][row][4] instead of [row][column].
+// red: shared, join_floats(RB, THREADS) floats. bar: a named barrier of these threads.
+// kByColumn: a slot's O is stored [column / 4][row][4] instead of [row][column], and
+// a thread joins neighbouring columns of one row.
+// The pieces lie in L2, half a microsecond away: a thread asks for 16
+// four-float values (of E places and 16 / E pieces) before it uses the first.
+// Not inlined, its arguments by value: the callers' loops keep their registers.
+constexpr int kJoinPieces = 16;   // pieces whose weights are held at a time
+constexpr int join_floats(int rb, int threads) { return threads + 2 * rb + kJoinPieces * rb; }
+
 template <typename T, int RB, int DP, int THREADS, bool kByColumn, typename W>
-__device__ void join(const Params &p, const W &work, const Segment &s, int tid, int rows, float *red, int bar)
+__device__ __noinline__ void join(const Params &p, const W work, const Segment s, int tid, int rows, float *red, int bar)
 {
     __shared__ unsigned arrived;
     const int c0 = work.cta_of(s.u0), c1 = work.cta_of(s.u0 + s.tiles - 1);
@@ -348,52 +383,106 @@ __device__ void join(const Params &p, const W &work, const Segment &s, int tid, 
     if (arrived != (unsigned)(c1 - c0)) return;
     __threadfence();
     constexpr int SF = slot_floats(RB, DP);
-    float *row_m = red + THREADS, *row_l = row_m + RB;
+    float *row_m = red + THREADS, *row_l = row_m + RB, *weight = row_l + RB;
+    auto slot_at = [&](int c) { return p.partials + (int64_t)work.slot_of(c, s.u0) * SF; };
     // maxima and sums of every row: `subs` threads share a row's pieces
-    constexpr int subs = THREADS >= RB ? THREADS / RB : 1;
-    for (int r0 = 0; r0 < RB; r0 += THREADS / subs) {
-        const int r = r0 + tid % (THREADS / subs), sub = tid / (THREADS / subs);
-        float m = -INFINITY;
-        for (int c = c0 + sub; c <= c1; c += subs)
-            m = fmaxf(m, __ldcg(p.partials + (int64_t)work.slot_of(c, s.u0) * SF + RB * DP + r));
-        red[tid] = m;
-        ptx::named_barrier(bar, THREADS);
-        m = -INFINITY;
-        for (int i = 0; i < subs; ++i) m = fmaxf(m, red[i * (THREADS / subs) + tid % (THREADS / subs)]);
-        const float mx = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
+    constexpr int subs = THREADS / RB;
+    static_assert(subs >= 1, "a thread a row at least");
+    {
+        const int r = tid % RB, sub = tid / RB;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 8
         for (int c = c0 + sub; c <= c1; c += subs) {
-            const float *q = p.partials + (int64_t)work.slot_of(c, s.u0) * SF + RB * DP + r;
-            l += __ldcg(q + RB) * exp2_fast(__ldcg(q) - mx);
+            const float *ml = slot_at(c) + RB * DP + r;
+            const float mc = __ldcg(ml), lc = __ldcg(ml + RB);
+            const float nm = fmaxf(m, mc), mx = nm == -INFINITY ? 0.f : nm;
+            l = l * exp2_fast(m - mx) + lc * exp2_fast(mc - mx);
+            m = nm;
         }
-        ptx::named_barrier(bar, THREADS);
-        red[tid] = l;
-        ptx::named_barrier(bar, THREADS);
-        if (sub == 0) {
+        if (subs > 1) {
+            red[tid] = m;
+            ptx::named_barrier(bar, THREADS);
+            float all = -INFINITY;
+            for (int i = 0; i < subs; ++i) all = fmaxf(all, red[i * RB + r]);
+            l *= exp2_fast(m - (all == -INFINITY ? 0.f : all));
+            m = all;
+            ptx::named_barrier(bar, THREADS);
+            red[tid] = l;
+            ptx::named_barrier(bar, THREADS);
             l = 0.f;
-            for (int i = 0; i < subs; ++i) l += red[i * (THREADS / subs) + tid];
-            row_m[r] = mx;
+            for (int i = 0; i < subs; ++i) l += red[i * RB + r];
+        }
+        if (sub == 0) {
+            row_m[r] = m == -INFINITY ? 0.f : m;
             row_l[r] = l;
-            if (r < rows) store_lse(p, s, s.rb * RB + r, m, l);
+            if (r < rows) store_lse(p, s, s.rb * RB + r, row_m[r], l);
         }
-        ptx::named_barrier(bar, THREADS);
     }
-    for (int e = tid; e < rows * (DP / 4); e += THREADS) {
-        const int r = kByColumn ? e % rows : e / (DP / 4), c4 = (kByColumn ? e / rows : e % (DP / 4)) * 4;
-        const int at = kByColumn ? c4 * RB + r * 4 : r * DP + c4;
-        const float mx = row_m[r], l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int c = c0; c <= c1; ++c) {
-            const float *slot = p.partials + (int64_t)work.slot_of(c, s.u0) * SF;
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot + at));
-            const float w = exp2_fast(__ldcg(slot + RB * DP + r) - mx);
-            acc.x += v.x * w;
-            acc.y += v.y * w;
-            acc.z += v.z * w;
-            acc.w += v.w * w;
+    ptx::named_barrier(bar, THREADS);
+    constexpr int kPlaces = RB * DP / 4 / THREADS;
+    constexpr int E = kByColumn ? 4 : kPlaces < 8 ? kPlaces : 8, PU = 16 / E;
+    // by column: the threads' rows, and how many of them share a row's columns
+    const int share = kByColumn && rows * 2 <= THREADS ? 2 : 1;
+    const int places = kByColumn ? DP / 4 / share : rows * (DP / 4), step = kByColumn ? E : E * THREADS;
+    for (int first = 0; first < places; first += step) {
+        float4 acc[E];
+        int at[E], row[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            int r, c4;
+            if (kByColumn) {
+                r = share == 2 ? tid & (THREADS / 2 - 1) : tid;
+                c4 = ((share == 2 && tid >= THREADS / 2 ? places : 0) + first + i) * 4;
+                r = min(r, rows - 1);
+            } else {
+                const int e = min(first + tid + i * THREADS, places - 1);
+                r = e / (DP / 4);
+                c4 = (e % (DP / 4)) * 4;
+            }
+            row[i] = r | (c4 << 16);
+            at[i] = kByColumn ? c4 * RB + r * 4 : r * DP + c4;
+            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        store4<T>(p, s, s.rb * RB + r, c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        for (int cc = c0; cc <= c1; cc += kJoinPieces) {
+            const int n = min(kJoinPieces, c1 - cc + 1);
+            if (c1 - c0 >= kJoinPieces || first == 0) {      // the weights held are others, or none
+                ptx::named_barrier(bar, THREADS);
+#pragma unroll 4
+                for (int i = tid; i < n * RB; i += THREADS)
+                    weight[i] = exp2_fast(__ldcg(slot_at(cc + i / RB) + RB * DP + i % RB) - row_m[i % RB]);
+                ptx::named_barrier(bar, THREADS);
+            }
+            for (int j = 0; j < n; j += PU) {
+                float4 v[PU][E];
+#pragma unroll
+                for (int u = 0; u < PU; ++u) {
+                    const float *slot = slot_at(cc + min(j + u, n - 1));
+#pragma unroll
+                    for (int i = 0; i < E; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4 *>(slot + at[i]));
+                }
+#pragma unroll
+                for (int u = 0; u < PU; ++u) {
+                    if (j + u >= n) break;
+#pragma unroll
+                    for (int i = 0; i < E; ++i) {
+                        const float w = weight[(j + u) * RB + (row[i] & 0xFFFF)];
+                        acc[i].x += v[u][i].x * w;
+                        acc[i].y += v[u][i].y * w;
+                        acc[i].z += v[u][i].z * w;
+                        acc[i].w += v[u][i].w * w;
+                    }
+                }
+            }
+        }
+        if (kByColumn && (share == 2 ? tid & (THREADS / 2 - 1) : tid) >= rows) continue;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (!kByColumn && first + tid + i * THREADS >= places) break;
+            const int r = row[i] & 0xFFFF;
+            const float l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
+            store4<T>(p, s, s.rb * RB + r, row[i] >> 16,
+                      make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
+        }
     }
     ptx::named_barrier(bar, THREADS);
 }

@@ -61,7 +61,7 @@ struct Cfg {
     static constexpr int kSmem = kBarOff + 512 + 1024;
     static_assert(kSmem <= 226 * 1024, "shared memory budget");
     // the epilogue's exchange and the join use q's space
-    static_assert((kSoftmax + 2 * kRows) * 4 + 4 * 128 * 4 <= kQ, "q's space");
+    static_assert(join_floats(kRows, kSoftmax) * 4 + 4 * 128 * 4 <= kQ, "q's space");
 };
 
 // fp16 weights are 2^(7 + kSlack) at most, and keep all their bits down to 2^-21 of the maximum
@@ -190,98 +190,113 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMAs
-        if (lane == 0) {
-            constexpr uint32_t id_qk = tc::idesc_16bit_f32(128, kKeys, false, kBf16);
-            constexpr uint32_t id_pv = tc::idesc_16bit_f32(128, DP, true, kBf16);
-            const int k_steps = (p.head_dim + 15) / 16;
-            int at = 0, seg = 0;
-            uint32_t taken[2] = {0, 0};              // P tiles used, for the parity of p_full
-            bool ok = true;
-            auto wait_tile = [&](int i) {
-                ok = ok && ptx::mbar_wait_bounded(ptx::smem_addr(full + i % C::kSlots), (i / C::kSlots) & 1, abort_flag,
-                                                  p.status);
-                tc::fence_after_sync();
-            };
-            auto tile_at = [&](int i) { return ptx::smem_addr(smem + C::kQ + (i % C::kSlots) * C::kTile); };
-            auto qk = [&](int i, int stream, int qrows) {
-                const uint32_t kt = tile_at(i), qt = ptx::smem_addr(smem) + qrows * C::kTile;
-                for (int k = 0; k < k_steps; ++k) {
-                    const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
-                    tc::mma_f16(tmem + stream * 128, tc::smem_desc_sw128(qt + off, 16, 1024),
-                                tc::smem_desc_sw128(kt + off, 16, 1024), id_qk, k != 0);
+        // The whole warp walks the list and waits; one elected lane issues, so
+        // that addresses and descriptors stay in uniform registers: the issue of
+        // a product has to take less than the product (512 cycles).
+        constexpr uint32_t id_qk = tc::idesc_16bit_f32(128, kKeys, false, kBf16);
+        constexpr uint32_t id_pv = tc::idesc_16bit_f32(128, DP, true, kBf16);
+        constexpr uint32_t hi = tc::desc_hi(1024);
+        const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+        const uint32_t smem0 = ptx::smem_addr(smem);
+        const uint32_t q_lo = tc::desc_lo(smem0, 16);
+        const uint32_t k_lo = tc::desc_lo(smem0 + C::kQ, 16), v_lo = tc::desc_lo(smem0 + C::kQ, C::kHalf);
+        const uint32_t full0 = ptx::smem_addr(full), freed0 = ptx::smem_addr(freed);
+        const int k_steps = (p.head_dim + 15) / 16;
+        int slot = 0, seg = 0;                       // ring slot and the parity of its tiles
+        uint32_t ring = 0, taken0 = 0, taken1 = 0;   // P tiles used, for the parities of p_full
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xFFFFFFFFu, wait_soon(bar, parity, abort_flag, p.status));
+            tc::fence_after_sync();
+            return ok;
+        };
+        auto next_slot = [&](int &i, uint32_t &parity) {
+            if (++i == C::kSlots) {
+                i = 0;
+                parity ^= 1;
+            }
+        };
+        auto qk = [&](int i, int stream, int half, bool release) {
+            if (tc::elect_one()) {
+                const uint32_t a = q_lo + half * (C::kTile >> 4), b = k_lo + i * (C::kTile >> 4);
+                const uint32_t d = tm + stream * 128;
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+                    if (k < k_steps) tc::mma_f16_ss(d, a + off, b + off, hi, id_qk, k != 0);
                 }
                 tc::commit(ptx::smem_addr(s_full + stream));
-            };
-            auto pv = [&](int i, int stream, bool first, bool last) {
-                const uint32_t vt = tile_at(i);
+                if (release) tc::commit(freed0 + i * 8);
+            }
+            __syncwarp();
+        };
+        auto pv = [&](int i, int stream, bool first, bool last, bool release) {
+            if (tc::elect_one()) {
+                const uint32_t b = v_lo + i * (C::kTile >> 4);
+                const uint32_t d = tm + kO + stream * 128, a = tm + stream * 128;
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_f16_ts(tmem + kO + stream * 128, tmem + stream * 128 + k * 8,
-                                   tc::smem_desc_sw128(vt + k * 2048, C::kHalf, 1024), id_pv, !first || k != 0);
+                    tc::mma_f16_ts(d, a + k * 8, b + k * (2048 >> 4), hi, id_pv, !first || k != 0);
                 if (last) tc::commit(ptx::smem_addr(o_full + stream));
-            };
-            auto wait_p = [&](int stream) {
-                ok = ok && ptx::mbar_wait_bounded(ptx::smem_addr(p_full + stream), taken[stream] & 1, abort_flag, p.status);
-                ++taken[stream];
-                tc::fence_after_sync();
-            };
-            auto release = [&](int i) { tc::commit(ptx::smem_addr(freed + i % C::kSlots)); };
-            while (ok && work.next(p, s)) {
-                const int nt = s.tile1 - s.tile0;
-                const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
-                ok = ptx::mbar_wait_bounded(ptx::smem_addr(q_full), seg & 1, abort_flag, p.status);
-                tc::fence_after_sync();
-                ++seg;
-                if (!two) {
-                    for (int j = 0; j < min(2, nt) && ok; ++j) {
-                        wait_tile(at);
-                        if (!ok) break;
-                        qk(at, j, 0);
-                        release(at++);
-                    }
-                    for (int j = 0; j < nt && ok; ++j) {
-                        const int st = j & 1;
-                        wait_tile(at);
-                        wait_p(st);
-                        if (!ok) break;
-                        pv(at, st, j < 2, j + 2 >= nt);
-                        release(at++);
-                        if (j + 2 < nt) {
-                            wait_tile(at);
-                            if (!ok) break;
-                            qk(at, st, 0);
-                            release(at++);
-                        }
-                    }
-                } else {
-                    wait_tile(at);
-                    if (!ok) break;
-                    qk(at, 0, 0);
-                    qk(at, 1, 1);
-                    release(at++);
-                    for (int j = 0; j < nt && ok; ++j) {
-                        const bool more = j + 1 < nt;
-                        for (int st = 0; st < 2 && ok; ++st) {
-                            if (st == 0) wait_tile(at);
-                            wait_p(st);
-                            if (!ok) break;
-                            pv(at, st, j == 0, !more);
-                            if (st == 1) release(at);
-                            if (more) {
-                                if (st == 0) wait_tile(at + 1);
-                                if (!ok) break;
-                                qk(at + 1, st, st);
-                                if (st == 1) release(at + 1);
-                            }
-                        }
-                        at += more ? 2 : 1;
+                if (release) tc::commit(freed0 + i * 8);
+            }
+            __syncwarp();
+        };
+        auto wait_tile = [&](int i, uint32_t parity) { return wait(full0 + i * 8, parity); };
+        auto wait_p = [&](int stream) {
+            return stream == 0 ? wait(ptx::smem_addr(p_full), taken0++ & 1) : wait(ptx::smem_addr(p_full + 1), taken1++ & 1);
+        };
+        while (ok && work.next(p, s)) {
+            const int nt = s.tile1 - s.tile0;
+            const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
+            if (!wait(ptx::smem_addr(q_full), seg & 1)) break;
+            ++seg;
+            if (!two) {
+                for (int j = 0; j < min(2, nt) && wait_tile(slot, ring); ++j) {
+                    qk(slot, j, 0, true);
+                    next_slot(slot, ring);
+                }
+                for (int j = 0; j < nt && ok; ++j) {
+                    const int st = j & 1;
+                    if (!wait_tile(slot, ring) || !wait_p(st)) break;
+                    pv(slot, st, j < 2, j + 2 >= nt, true);
+                    next_slot(slot, ring);
+                    if (j + 2 < nt) {
+                        if (!wait_tile(slot, ring)) break;
+                        qk(slot, st, 0, true);
+                        next_slot(slot, ring);
                     }
                 }
+            } else {
+                if (!wait_tile(slot, ring)) break;
+                qk(slot, 0, 0, false);
+                qk(slot, 1, 1, true);
+                next_slot(slot, ring);
+                for (int j = 0; j < nt && ok; ++j) {
+                    const bool more = j + 1 < nt;
+                    int after = slot;
+                    uint32_t after_ring = ring;
+                    next_slot(after, after_ring);
+                    if (!wait_tile(slot, ring) || !wait_p(0)) break;
+                    pv(slot, 0, j == 0, !more, false);
+                    if (more) {
+                        if (!wait_tile(after, after_ring)) break;
+                        qk(after, 0, 0, false);
+                    }
+                    if (!wait_p(1)) break;
+                    pv(slot, 1, j == 0, !more, true);
+                    if (more) qk(after, 1, 1, true);
+                    next_slot(slot, ring);
+                    if (more) next_slot(slot, ring);
+                }
             }
-            // every MMA issued has completed once `drain` flips
+        }
+        // every MMA issued has completed once `drain` flips
+        if (tc::elect_one()) {   // the lane that issued them
             tc::commit(ptx::smem_addr(drain));
             ptx::mbar_wait_bounded(ptx::smem_addr(drain), 0, nullptr, p.status);
         }
+        __syncwarp();
     } else {
         // ---------------------------------------------------------------- softmax, epilogue
         const int tid = threadIdx.x - 64;
@@ -291,7 +306,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t t_s = t_lane + stream * 128, t_o = t_lane + kO + stream * 128;
         float *red = reinterpret_cast<float *>(smem);
-        float *pair_m = red + kSoftmax + 2 * kRows, *pair_l = pair_m + 256;   // [2 streams][128 rows]
+        float *pair_m = red + join_floats(kRows, kSoftmax), *pair_l = pair_m + 256;   // [2 streams][128 rows]
         const bool negative = p.scale_log2 < 0.f;
         const float scale = fabsf(p.scale_log2);
         int base = 0;                                // ring position of the segment's first tile
@@ -305,25 +320,36 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int row0 = s.rb * kRows, rows = min(kRows, s.n * p.group - row0);
             const bool two = rows > 128;
             if (tid == 0) *odd_flag = 0;
-            for (int e = tid; e < (two ? 256 : 128) * (DP / 8); e += kSoftmax) {
-                const int r = e / (DP / 8), c = e % (DP / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows && c * 8 < p.head_dim) {
-                    const int qr = row0 + r;
-                    v = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
-                                                         (int64_t)(s.token0 + qr / p.group) * p.q_token_stride +
-                                                         (int64_t)(s.h * p.group + qr % p.group) * p.q_head_stride + c * 8);
-                    if (negative) {                  // scores are scaled by |scale|
-                        v.x ^= 0x80008000u;
-                        v.y ^= 0x80008000u;
-                        v.z ^= 0x80008000u;
-                        v.w ^= 0x80008000u;
+            {
+                // a thread has one 16-byte column and every kStep-th row; eight
+                // loads are under way before the first is stored
+                constexpr int kStep = kSoftmax / (DP / 8);
+                const int c = tid % (DP / 8), limit = two ? 256 : 128;
+                const T *q = static_cast<const T *>(p.q) + (int64_t)s.token0 * p.q_token_stride +
+                             (int64_t)s.h * p.group * p.q_head_stride + c * 8;
+                for (int r0 = tid / (DP / 8); r0 < limit; r0 += 8 * kStep) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * kStep, qr = row0 + r, token = qr / p.group;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (r < rows && c * 8 < p.head_dim)
+                            v[i] = *reinterpret_cast<const uint4 *>(q + token * p.q_token_stride +
+                                                                    (qr - token * p.group) * p.q_head_stride);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * kStep;
+                        if (r >= limit) break;
+                        const uint32_t flip = negative ? 0x80008000u : 0u;   // scores are scaled by |scale|
+                        const uint32_t dst = ptx::smem_addr(smem) + (uint32_t)(r >> 7) * C::kTile +
+                                             (uint32_t)(c >> 3) * C::kHalf + (uint32_t)(r & 127) * 128 +
+                                             (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(dst), "r"(v[i].x ^ flip), "r"(v[i].y ^ flip), "r"(v[i].z ^ flip),
+                                       "r"(v[i].w ^ flip) : "memory");
                     }
                 }
-                const uint32_t dst = ptx::smem_addr(smem) + (uint32_t)(r >> 7) * C::kTile + (uint32_t)(c >> 3) * C::kHalf +
-                                     (uint32_t)(r & 127) * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                             : "memory");
             }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(ptx::smem_addr(q_full));
@@ -333,7 +359,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int t = min(row0 + my_row, s.n * p.group - 1) / p.group;    // its token
             float m = -INFINITY, l = 0.f;
             for (int j = two ? 0 : stream; j < nt && ok; j += two ? 1 : 2) {
-                ok = ptx::mbar_wait_bounded(ptx::smem_addr(s_full + stream), tiles_done & 1, abort_flag, p.status);
+                ok = wait_soon(ptx::smem_addr(s_full + stream), tiles_done & 1, abort_flag, p.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 ++tiles_done;
@@ -404,7 +430,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     // which the epilogue gives to the rows that see them.
                     const int v_at = base + (two ? 1 + j + min(j, nt - 1) : min(2, nt) + j + min(j, max(0, nt - 2)));
                     const int slot = v_at % C::kSlots;
-                    ok = ptx::mbar_wait_bounded(ptx::smem_addr(full + slot), (v_at / C::kSlots) & 1, abort_flag, p.status);
+                    ok = wait_soon(ptx::smem_addr(full + slot), (v_at / C::kSlots) & 1, abort_flag, p.status);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     const uint32_t vt = ptx::smem_addr(smem + C::kQ + slot * C::kTile);
@@ -445,7 +471,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             // ---- the segment's end: all MMAs of both streams are done
             const int streams = two || nt > 1 ? 2 : 1;
             for (int st = 0; st < streams; ++st) {
-                ok = ok && ptx::mbar_wait_bounded(ptx::smem_addr(o_full + st), segs_done[st] & 1, abort_flag, p.status);
+                ok = ok && wait_soon(ptx::smem_addr(o_full + st), segs_done[st] & 1, abort_flag, p.status);
                 ++segs_done[st];
             }
             ok = __all_sync(0xFFFFFFFFu, ok);
