@@ -610,8 +610,7 @@ awq_status_t awq_reserve_tree_attention(int64_t max_tokens, int64_t max_requests
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
         return AWQ_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    size_t floats = 0, counters = 0;
-    awq::tree_attention_scratch(max_tokens, max_requests, q_heads, kv_heads, head_dim, sms, &floats, &counters);
+    const size_t floats = awq::tree_attention_partial_floats(head_dim, sms);
     try {
         const auto key = std::make_pair(dev, s);
         bool reserved;
@@ -621,7 +620,7 @@ awq_status_t awq_reserve_tree_attention(int64_t max_tokens, int64_t max_requests
             awq::g_scratch[key].reserved = false;
         }
         awq::Scratch sc{};
-        const bool ok = awq::get_scratch(s, floats, counters, &sc) && cudaStreamSynchronize(s) == cudaSuccess;
+        const bool ok = awq::get_scratch(s, floats, 0, &sc) && cudaStreamSynchronize(s) == cudaSuccess;
         std::lock_guard<std::mutex> lock(awq::g_mutex);
         awq::g_scratch[key].reserved = reserved;
         return ok ? AWQ_OK : AWQ_ERR_CUDA;

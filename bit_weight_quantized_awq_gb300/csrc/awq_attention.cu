@@ -44,8 +44,8 @@ struct Cfg {
     static constexpr int kStages = DP == 64 ? 6 : 3;     // 96 KB in flight (192 KB at DP = 256)
     static constexpr int kMergeOff = kStages * 2 * kTile;
     static constexpr int kMerge = kRows * DP * 4;        // one warp's O
-    static constexpr int kRedOff = kMergeOff + kMerge;   // m and l of the four warps; the join's sums
-    static constexpr int kRed = (join_floats(kRows, kConsumers) + 8 * kRows) * 4;
+    static constexpr int kRedOff = kMergeOff + kMerge;   // m and l of the four warps
+    static constexpr int kRed = 8 * kRows * 4;
     static constexpr int kBarOff = kRedOff + kRed;
     static constexpr int kSmem = kBarOff + 128 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -162,8 +162,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     // -------------------------------------------------------------------- consumers
     const int g = lane >> 2, t4 = lane & 3;
     float *merge = reinterpret_cast<float *>(smem + C::kMergeOff);
-    float *red = reinterpret_cast<float *>(smem + C::kRedOff);
-    float *warp_m = red + join_floats(kRows, kConsumers), *warp_l = warp_m + 4 * kRows;
+    float *warp_m = reinterpret_cast<float *>(smem + C::kRedOff), *warp_l = warp_m + 4 * kRows;
     int it = 0;
     bool ok = true;
     while (work.next(p, s)) {
@@ -405,7 +404,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         if (i * 8 < p.head_dim)
                             *reinterpret_cast<uint32_t *>(out + i * 8 + t4 * 2) =
                                 Elem<T>::pack(o[i][2 * half] * inv, o[i][2 * half + 1] * inv);
-                    if (t4 == 0) store_lse(p, s, row0 + r, half ? eb : ea, half ? l2b : l2a);
+                    if (t4 == 0) store_lse(p, s.token0, s.h, row0 + r, half ? eb : ea, half ? l2b : l2a);
                 }
             }
         } else {
@@ -413,8 +412,9 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 float *slot = p.partials + (int64_t)work.slot_of(blockIdx.x, s.u0) * slot_floats(kRows, DP);
 #pragma unroll
                 for (int i = 0; i < DP / 8; ++i) {
-                    __stcg(reinterpret_cast<float2 *>(slot + g * DP + i * 8 + t4 * 2), make_float2(o[i][0], o[i][1]));
-                    __stcg(reinterpret_cast<float2 *>(slot + (g + 8) * DP + i * 8 + t4 * 2), make_float2(o[i][2], o[i][3]));
+                    const int c = i * 8 + t4 * 2;
+                    __stcg(reinterpret_cast<float2 *>(slot + slot_at(kRows, g, c)), make_float2(o[i][0], o[i][1]));
+                    __stcg(reinterpret_cast<float2 *>(slot + slot_at(kRows, g + 8, c)), make_float2(o[i][2], o[i][3]));
                 }
                 if (t4 == 0) {
                     __stcg(slot + kRows * DP + g, m2a);
@@ -423,7 +423,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     __stcg(slot + kRows * DP + kRows + g + 8, l2b);
                 }
             }
-            join<T, kRows, DP, kConsumers, false>(p, work, s, threadIdx.x, rows, red, 1);
+            if (threadIdx.x == 0 && s.tile1 == s.tiles) work.note_join(p, s, rows);
         }
     }
 }
@@ -475,27 +475,10 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * tiles;
     p.min_units = 4;
     const int ctas = (int)std::min<int64_t>(li.ctas, std::max<int64_t>(1, units / p.min_units));
-    Scratch sc{};
-    if (!get_scratch(stream, (size_t)2 * ctas * slot_floats(kRows, DP),
-                     (size_t)a.kv_heads * ((size_t)(a.tokens * p.group) / kRows + (size_t)a.B), &sc))
-        return cudaErrorMemoryAllocation;
-    p.partials = sc.partials;
-    p.counters = sc.counters;
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
 #endif
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<DP>::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_rows_kernel<T, DP>, tk, tv, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_pair<T, kRows, DP>(attention_rows_kernel<T, DP>, ctas, kThreads, Cfg<DP>::kSmem, stream, tk, tv, p);
 }
 
 } // namespace
@@ -575,13 +558,11 @@ cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t st
     return attn::launch_rows_any(a, stream);
 }
 
-void tree_attention_scratch(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int sms,
-                            size_t *partial_floats, size_t *n_counters)
+size_t tree_attention_partial_floats(int64_t head_dim, int sms)
 {
+    // at most four CTAs of the few-row kernel fit an SM's shared memory
     const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    *partial_floats = std::max((size_t)2 * sms * 4 * attn::slot_floats(attn::kRows, dp),
-                               attn::tc_partial_floats(sms, head_dim));
-    *n_counters = (size_t)kv_heads * ((size_t)(tokens * (q_heads / kv_heads)) / attn::kRows + (size_t)B);
+    return std::max(attn::scratch_floats(4 * sms, attn::kRows, dp), attn::tc_partial_floats(sms, head_dim));
 }
 
 } // namespace awq

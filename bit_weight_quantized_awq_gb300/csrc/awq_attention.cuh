@@ -15,13 +15,16 @@
 // (m, l, O): O = sum_j exp2(s_j - m) v_j and l = sum_j exp2(s_j - m), joined by
 //   M = max m,  L = sum l exp2(m - M),  out = (sum O exp2(m - M)) / L.
 // Each piece is written to a slot of its CTA (its first segment in slot 0, its
-// last in slot 1); the CTA that finishes a row block's last piece -- told by a
-// counter -- joins all of them in the order of the CTAs, so the sum's order is
-// the same in every call, and no CTA ever waits for another.
+// last in slot 1), and the CTA that has a row block's last piece writes down what
+// there is to join. A second kernel, launched as a programmatic dependent, joins
+// the pieces in the order of the CTAs, so the sum's order is the same in every
+// call, and no CTA ever waits for another. (Joined by whichever CTA came last the
+// pieces took 10 to 20 us at 256 rows: one CTA's loads, behind a fence.)
 #pragma once
 
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,6 +33,14 @@
 
 namespace awq {
 namespace attn {
+
+// What is to be joined because a CTA has the last piece of a split row block.
+struct Join {
+    int valid;
+    int cta0, slot0;        // CTA of the first piece, and its slot; the others are slot 0 of
+    int cta1;               // the CTAs after it up to cta1
+    int h, rb, token0, rows;
+};
 
 struct Params {
     const void *q;
@@ -41,8 +52,9 @@ struct Params {
     const void *v_data;     // the values, for the few elements read outside the tiles
     int64_t v_block_stride, v_token_stride, v_head_stride;
     const int32_t *ctx, *cu, *mask;
-    float *partials;
-    unsigned int *counters, *status;
+    float *partials;        // slots, two a CTA
+    struct Join *joins;     // one a CTA
+    unsigned int *status;
     int table_width, mask_words;
     int B, tokens, q_heads, kv_heads, group, head_dim, num_blocks;
     int shift;              // log2 of the block size
@@ -61,7 +73,6 @@ struct Segment {
     int ctx, n, token0;     // the request: context length, new tokens, first row of q
     int tile0, tile1, tiles;
     int64_t u0;             // unit of the row block's first tile
-    int block;              // counter of the row block
     __device__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
@@ -70,7 +81,7 @@ struct Work {
     int64_t units, pos, end;
     int ctas;               // CTAs that take part
     int b, h, rb, tile, tiles;
-    int ctx, n, token0, row_blocks, block0;
+    int ctx, n, token0, row_blocks;
 
     // Tiles of one row block: all keys, or without a mask (causal) those up to
     // the block's last token.
@@ -98,14 +109,14 @@ struct Work {
     __device__ bool find(const Params &p)
     {
         __shared__ int64_t warp_units[THREADS / 32];
-        __shared__ int warp_blocks[THREADS / 32];
         __shared__ int64_t found_units;
-        __shared__ int found_b, found_block;
+        __shared__ int found_b;
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+        if (tid == 0) p.joins[blockIdx.x].valid = 0;
         const int per = (p.B + THREADS - 1) / THREADS;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
         int64_t mine = 0;
-        int blocks = 0, bad = 0;
+        int bad = 0;
         for (int i = b_lo; i < b_hi; ++i) {
             const int c = p.ctx[i], t0 = p.cu[i], t1 = p.cu[i + 1];
             if (t0 < 0 || t1 < t0 || t1 > p.tokens || c < 0 ||
@@ -114,39 +125,25 @@ struct Work {
                 break;
             }
             mine += head_units(p, c, t1 - t0) * p.kv_heads;
-            blocks += row_blocks_of(p, t1 - t0) * p.kv_heads;
         }
         int64_t su = mine;
-        int sb = blocks;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t ou = __shfl_up_sync(0xFFFFFFFFu, su, d);
-            const int ob = __shfl_up_sync(0xFFFFFFFFu, sb, d);
-            if (lane >= d) {
-                su += ou;
-                sb += ob;
-            }
+            if (lane >= d) su += ou;
         }
-        if (lane == 31) {
-            warp_units[warp] = su;
-            warp_blocks[warp] = sb;
-        }
+        if (lane == 31) warp_units[warp] = su;
         if (__syncthreads_or(bad)) {
             if (tid == 0 && blockIdx.x == 0) raise_status(p.status, kStatusBadIndex);
             return false;
         }
         units = 0;
         int64_t before = 0;
-        int before_blocks = 0;
         for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) {
-                before += warp_units[w];
-                before_blocks += warp_blocks[w];
-            }
+            if (w < warp) before += warp_units[w];
             units += warp_units[w];
         }
         before += su - mine;
-        before_blocks += sb - blocks;
         if (units == 0) return false;
         ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, units / p.min_units));
         if ((int)blockIdx.x >= ctas) return false;
@@ -159,15 +156,12 @@ struct Work {
                 const int64_t u = head_units(p, c, len) * p.kv_heads;
                 if (pos < before + u) break;
                 before += u;
-                before_blocks += row_blocks_of(p, len) * p.kv_heads;
             }
             found_b = i;
             found_units = before;
-            found_block = before_blocks;
         }
         __syncthreads();
         b = found_b;
-        block0 = found_block;
         load(p);
         int64_t rem = pos - found_units;
         const int64_t per_head = head_units(p, ctx, n);
@@ -212,7 +206,6 @@ struct Work {
         s.tile1 = tile + count;
         s.tiles = tiles;
         s.u0 = pos - tile;
-        s.block = block0 + h * row_blocks + rb;
         pos += count;
         if (pos < end) {
             tile = 0;
@@ -220,7 +213,6 @@ struct Work {
                 rb = 0;
                 if (++h == p.kv_heads) {
                     h = 0;
-                    block0 += p.kv_heads * row_blocks;
                     do {
                         ++b;
                         load(p);
@@ -234,6 +226,12 @@ struct Work {
 
     // The slot of CTA c's piece of the row block whose first unit is u0.
     __device__ int slot_of(int c, int64_t u0) const { return 2 * c + (begin_of(c) >= u0 ? 0 : 1); }
+    // One thread of a CTA whose segment is a row block's last piece, of several.
+    __device__ void note_join(const Params &p, const Segment &s, int rows) const
+    {
+        const int c0 = cta_of(s.u0);
+        p.joins[blockIdx.x] = Join{1, c0, slot_of(c0, s.u0), (int)blockIdx.x, s.h, s.rb, s.token0, rows};
+    }
 };
 
 // ---- masks ----
@@ -332,159 +330,147 @@ __device__ __forceinline__ bool wait_soon(uint32_t bar, uint32_t parity, volatil
 
 // ---- joining ----
 
+// A slot: O as [column / 4][row][4], then m and l of every row.
 constexpr int slot_floats(int rb, int dp) { return rb * dp + 2 * rb; }
-
-// Writes rows of a finished row block: `v` the four values of columns c .. c + 3.
-template <typename T>
-__device__ __forceinline__ void store4(const Params &p, const Segment &s, int r, int c, float4 v)
+__host__ __device__ constexpr int slot_at(int rb, int r, int c) { return (c >> 2) * rb * 4 + r * 4 + (c & 3); }
+// Floats of the partial sums of `ctas` CTAs: their slots and what is to be joined.
+constexpr size_t scratch_floats(int ctas, int rb, int dp)
 {
-    if (c >= p.head_dim) return;
-    const int64_t t = s.token0 + r / p.group;
-    const int64_t head = (int64_t)s.h * p.group + r % p.group;
-    uint2 o;
-    o.x = Elem<T>::pack(v.x, v.y);
-    o.y = Elem<T>::pack(v.z, v.w);
-    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (t * p.q_heads + head) * p.head_dim + c) = o;
+    return (size_t)ctas * (2 * slot_floats(rb, dp) + sizeof(Join) / sizeof(float));
 }
 
-__device__ __forceinline__ void store_lse(const Params &p, const Segment &s, int r, float m, float l)
+__device__ __forceinline__ void store_lse(const Params &p, int token0, int h, int r, float m, float l)
 {
     if (p.lse == nullptr) return;
-    const int64_t t = s.token0 + r / p.group;
-    const int64_t head = (int64_t)s.h * p.group + r % p.group;
+    const int64_t t = token0 + r / p.group;
+    const int64_t head = (int64_t)h * p.group + r % p.group;
     p.lse[t * p.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// The CTA that finishes the last piece of a row block joins all of them.
-// Called by the THREADS consecutive threads whose index is tid, after they have
-// written this CTA's piece to its slot; `rows` of the block's RB rows exist.
-// red: shared, join_floats(RB, THREADS) floats. bar: a named barrier of these threads.
-// kByColumn: a slot's O is stored [column / 4][row][4] instead of [row][column], and
-// a thread joins neighbouring columns of one row.
-// The pieces lie in L2, half a microsecond away: a thread asks for 16
-// four-float values (of E places and 16 / E pieces) before it uses the first.
-// Not inlined, its arguments by value: the callers' loops keep their registers.
-constexpr int kJoinPieces = 16;   // pieces whose weights are held at a time
-constexpr int join_floats(int rb, int threads) { return threads + 2 * rb + kJoinPieces * rb; }
+// Joins the pieces of the row block whose last one CTA blockIdx.x had, columns
+// 32 blockIdx.y .. + 31. A thread has one row; where the rows are fewer than the
+// threads, `subs` of them share a row's pieces and add up their parts in shared
+// memory. Eight 16-byte loads a piece, of two pieces, are under way at a time: the
+// pieces come from L2.
+constexpr int kJoinThreads = 256;
 
-template <typename T, int RB, int DP, int THREADS, bool kByColumn, typename W>
-__device__ __noinline__ void join(const Params &p, const W work, const Segment s, int tid, int rows, float *red, int bar)
+template <typename T, int RB, int DP>
+__global__ void __launch_bounds__(kJoinThreads)
+attention_join_kernel(const __grid_constant__ Params p)
 {
-    __shared__ unsigned arrived;
-    const int c0 = work.cta_of(s.u0), c1 = work.cta_of(s.u0 + s.tiles - 1);
-    __threadfence();
-    ptx::named_barrier(bar, THREADS);
-    if (tid == 0) {
-        const unsigned old = atomicAdd(p.counters + s.block, 1u);
-        arrived = old;
-        if (old == (unsigned)(c1 - c0)) p.counters[s.block] = 0;   // as the next call expects it
-    }
-    ptx::named_barrier(bar, THREADS);
-    if (arrived != (unsigned)(c1 - c0)) return;
-    __threadfence();
+    __shared__ float part[kJoinThreads][33];
+    __shared__ float part_m[kJoinThreads], part_l[kJoinThreads];
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    const Join j = p.joins[blockIdx.x];
+    const int c0 = blockIdx.y * 32;
+    if (!j.valid || c0 >= p.head_dim) return;
+    const int lanes = j.rows <= 16 ? 16 : (j.rows + 31) & ~31;      // rows, rounded up
+    const int subs = kJoinThreads / lanes;
+    const int r = threadIdx.x % lanes, sub = threadIdx.x / lanes;
     constexpr int SF = slot_floats(RB, DP);
-    float *row_m = red + THREADS, *row_l = row_m + RB, *weight = row_l + RB;
-    auto slot_at = [&](int c) { return p.partials + (int64_t)work.slot_of(c, s.u0) * SF; };
-    // maxima and sums of every row: `subs` threads share a row's pieces
-    constexpr int subs = THREADS / RB;
-    static_assert(subs >= 1, "a thread a row at least");
-    {
-        const int r = tid % RB, sub = tid / RB;
-        float m = -INFINITY, l = 0.f;
+    auto slot = [&](int c) { return p.partials + (int64_t)(c == j.cta0 ? j.slot0 : 2 * c) * SF; };
+    float m = -INFINITY, l = 0.f;
+    float acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+    if (sub < subs && r < j.rows) {
 #pragma unroll 8
-        for (int c = c0 + sub; c <= c1; c += subs) {
-            const float *ml = slot_at(c) + RB * DP + r;
-            const float mc = __ldcg(ml), lc = __ldcg(ml + RB);
-            const float nm = fmaxf(m, mc), mx = nm == -INFINITY ? 0.f : nm;
-            l = l * exp2_fast(m - mx) + lc * exp2_fast(mc - mx);
-            m = nm;
-        }
-        if (subs > 1) {
-            red[tid] = m;
-            ptx::named_barrier(bar, THREADS);
-            float all = -INFINITY;
-            for (int i = 0; i < subs; ++i) all = fmaxf(all, red[i * RB + r]);
-            l *= exp2_fast(m - (all == -INFINITY ? 0.f : all));
-            m = all;
-            ptx::named_barrier(bar, THREADS);
-            red[tid] = l;
-            ptx::named_barrier(bar, THREADS);
-            l = 0.f;
-            for (int i = 0; i < subs; ++i) l += red[i * RB + r];
-        }
-        if (sub == 0) {
-            row_m[r] = m == -INFINITY ? 0.f : m;
-            row_l[r] = l;
-            if (r < rows) store_lse(p, s, s.rb * RB + r, row_m[r], l);
-        }
-    }
-    ptx::named_barrier(bar, THREADS);
-    constexpr int kPlaces = RB * DP / 4 / THREADS;
-    constexpr int E = kByColumn ? 4 : kPlaces < 8 ? kPlaces : 8, PU = 16 / E;
-    // by column: the threads' rows, and how many of them share a row's columns
-    const int share = kByColumn && rows * 2 <= THREADS ? 2 : 1;
-    const int places = kByColumn ? DP / 4 / share : rows * (DP / 4), step = kByColumn ? E : E * THREADS;
-    for (int first = 0; first < places; first += step) {
-        float4 acc[E];
-        int at[E], row[E];
+        for (int c = j.cta0 + sub; c <= j.cta1; c += subs) m = fmaxf(m, __ldcg(slot(c) + RB * DP + r));
+        const float mx = m == -INFINITY ? 0.f : m;
+        for (int c = j.cta0 + sub; c <= j.cta1; c += 2 * subs) {
+            float4 v[2][8];
+            float mc[2], lc[2];
+            const bool both = c + subs <= j.cta1;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            int r, c4;
-            if (kByColumn) {
-                r = share == 2 ? tid & (THREADS / 2 - 1) : tid;
-                c4 = ((share == 2 && tid >= THREADS / 2 ? places : 0) + first + i) * 4;
-                r = min(r, rows - 1);
-            } else {
-                const int e = min(first + tid + i * THREADS, places - 1);
-                r = e / (DP / 4);
-                c4 = (e % (DP / 4)) * 4;
+            for (int u = 0; u < 2; ++u) {
+                if (u && !both) break;
+                const float *from = slot(c + u * subs);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[u][i] = __ldcg(reinterpret_cast<const float4 *>(from + slot_at(RB, r, c0 + 4 * i)));
+                mc[u] = __ldcg(from + RB * DP + r);
+                lc[u] = __ldcg(from + RB * DP + RB + r);
             }
-            row[i] = r | (c4 << 16);
-            at[i] = kByColumn ? c4 * RB + r * 4 : r * DP + c4;
-            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        for (int cc = c0; cc <= c1; cc += kJoinPieces) {
-            const int n = min(kJoinPieces, c1 - cc + 1);
-            if (c1 - c0 >= kJoinPieces || first == 0) {      // the weights held are others, or none
-                ptx::named_barrier(bar, THREADS);
-#pragma unroll 4
-                for (int i = tid; i < n * RB; i += THREADS)
-                    weight[i] = exp2_fast(__ldcg(slot_at(cc + i / RB) + RB * DP + i % RB) - row_m[i % RB]);
-                ptx::named_barrier(bar, THREADS);
-            }
-            for (int j = 0; j < n; j += PU) {
-                float4 v[PU][E];
 #pragma unroll
-                for (int u = 0; u < PU; ++u) {
-                    const float *slot = slot_at(cc + min(j + u, n - 1));
+            for (int u = 0; u < 2; ++u) {
+                if (u && !both) break;
+                const float w = exp2_fast(mc[u] - mx);
+                l += lc[u] * w;
 #pragma unroll
-                    for (int i = 0; i < E; ++i) v[u][i] = __ldcg(reinterpret_cast<const float4 *>(slot + at[i]));
-                }
-#pragma unroll
-                for (int u = 0; u < PU; ++u) {
-                    if (j + u >= n) break;
-#pragma unroll
-                    for (int i = 0; i < E; ++i) {
-                        const float w = weight[(j + u) * RB + (row[i] & 0xFFFF)];
-                        acc[i].x += v[u][i].x * w;
-                        acc[i].y += v[u][i].y * w;
-                        acc[i].z += v[u][i].z * w;
-                        acc[i].w += v[u][i].w * w;
-                    }
+                for (int i = 0; i < 8; ++i) {
+                    acc[4 * i] += v[u][i].x * w;
+                    acc[4 * i + 1] += v[u][i].y * w;
+                    acc[4 * i + 2] += v[u][i].z * w;
+                    acc[4 * i + 3] += v[u][i].w * w;
                 }
             }
         }
-        if (kByColumn && (share == 2 ? tid & (THREADS / 2 - 1) : tid) >= rows) continue;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (!kByColumn && first + tid + i * THREADS >= places) break;
-            const int r = row[i] & 0xFFFF;
-            const float l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
-            store4<T>(p, s, s.rb * RB + r, row[i] >> 16,
-                      make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv));
-        }
     }
-    ptx::named_barrier(bar, THREADS);
+    if (subs > 1) {
+        part_m[threadIdx.x] = m;
+        part_l[threadIdx.x] = l;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) part[threadIdx.x][e] = acc[e];
+        __syncthreads();
+        if (sub != 0 || r >= j.rows) return;
+        float top = m;
+        for (int i = 1; i < subs; ++i) top = fmaxf(top, part_m[i * lanes + r]);
+        const float mx = top == -INFINITY ? 0.f : top, w0 = exp2_fast(m - mx);
+        l *= w0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] *= w0;
+        for (int i = 1; i < subs; ++i) {
+            const float w = exp2_fast(part_m[i * lanes + r] - mx);
+            l += part_l[i * lanes + r] * w;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] += part[i * lanes + r][e] * w;
+        }
+        m = top;
+    }
+    if (sub != 0 || r >= j.rows) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = j.rb * RB + r;
+    const int64_t token = j.token0 + row / p.group;
+    T *out = static_cast<T *>(p.out) + (token * p.q_heads + (int64_t)j.h * p.group + row % p.group) * p.head_dim + c0;
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+        if (c0 + e < p.head_dim)
+            *reinterpret_cast<uint4 *>(out + e) =
+                make_uint4(Elem<T>::pack(acc[e] * inv, acc[e + 1] * inv), Elem<T>::pack(acc[e + 2] * inv, acc[e + 3] * inv),
+                           Elem<T>::pack(acc[e + 4] * inv, acc[e + 5] * inv), Elem<T>::pack(acc[e + 6] * inv, acc[e + 7] * inv));
+    if (blockIdx.y == 0) store_lse(p, j.token0, j.h, row, m == -INFINITY ? 0.f : m, l);
+}
+
+// Launches a main kernel of `ctas` CTAs and, unless there is one only, its join.
+template <typename T, int RB, int DP, typename K>
+cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t stream, const CUtensorMap &tk,
+                        const CUtensorMap &tv, Params &p)
+{
+    Scratch sc{};
+    if (!get_scratch(stream, scratch_floats(ctas, RB, DP), 0, &sc)) return cudaErrorMemoryAllocation;
+    p.partials = sc.partials;
+    p.joins = reinterpret_cast<Join *>(sc.partials + (size_t)ctas * 2 * slot_floats(RB, DP));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    if (ctas > 1) {
+        cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.head_dim + 31) / 32);
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, attention_join_kernel<T, RB, DP>, p);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaGetLastError();
 }
 
 } // namespace attn

@@ -11,8 +11,8 @@
 // For a stream and tile: S = Q K^T (tcgen05, 128 x 128, into tensor memory), the
 // stream's four warps read S (a thread has one row: no shuffles), write
 // P = exp2(S - m) over it as 16-bit values, and O += P V takes P from tensor
-// memory. Tensor memory is full: S 2 x 128, O 2 x DP columns. The MMAs of the one
-// issuing thread run in order, so S of the stream's next tile may be written over
+// memory. Tensor memory is full: S 2 x 128, O 2 x DP columns. A stream's MMAs
+// are issued by one thread and run in order, so S of the stream's next tile may be written over
 // P as soon as it is issued behind O += P V.
 //
 // The maximum is lazy: O is rescaled only when a row's maximum has grown by more
@@ -26,8 +26,9 @@
 //
 //   warp 0      producer: K and V tiles, a TMA box a page, in one ring, in the order
 //               the MMAs take them
-//   warp 1      the MMAs (one thread) and tensor memory
-//   warps 2-5   softmax and epilogue of stream 0, warps 6-9 of stream 1
+//   warps 1, 2  the MMAs of streams 0 and 1: while one waits for its softmax the
+//               other keeps the tensor cores busy; warp 1 also has tensor memory
+//   warps 4-7   softmax and epilogue of stream 0, warps 8-11 of stream 1
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -44,7 +45,7 @@ namespace {
 
 constexpr int kRows = 256;       // rows of a block
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;    // threads of the softmax warps
 constexpr float kSlack = 8.f;
 constexpr uint32_t kTmemCols = 512;
@@ -60,8 +61,6 @@ struct Cfg {
     static constexpr int kBarOff = kQ + kSlots * kTile;
     static constexpr int kSmem = kBarOff + 512 + 1024;
     static_assert(kSmem <= 226 * 1024, "shared memory budget");
-    // the epilogue's exchange and the join use q's space
-    static_assert(join_floats(kRows, kSoftmax) * 4 + 4 * 128 * 4 <= kQ, "q's space");
 };
 
 // fp16 weights are 2^(7 + kSlack) at most, and keep all their bits down to 2^-21 of the maximum
@@ -69,6 +68,31 @@ template <typename T>
 constexpr float kWeightBias = 0.f;
 template <>
 constexpr float kWeightBias<__half> = 7.f;
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// two at a time
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 // Bits of the keys key0 .. key0 + 31 that token t sees.
 __device__ __forceinline__ uint32_t seen32(const Params &p, const Segment &s, int t, int key0)
@@ -89,7 +113,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);   // [kSlots] tile landed
-    uint64_t *freed = full + C::kSlots;      // [kSlots] MMAs that read the tile are done
+    uint64_t *freed = full + C::kSlots;      // [kSlots] MMAs that read the tile are done (two arrivals)
     uint64_t *s_full = freed + C::kSlots;    // [2] S of the stream is complete
     uint64_t *p_full = s_full + 2;           // [2] P of the stream is written
     uint64_t *o_full = p_full + 2;           // [2] O of the stream and segment is complete
@@ -107,7 +131,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             ptx::mbar_init(ptx::smem_addr(full + i), 1);
-            ptx::mbar_init(ptx::smem_addr(freed + i), 1);
+            ptx::mbar_init(ptx::smem_addr(freed + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(s_full + i), 1);
@@ -115,7 +139,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             ptx::mbar_init(ptx::smem_addr(o_full + i), 1);
         }
         ptx::mbar_init(ptx::smem_addr(q_full), kSoftmax);
-        ptx::mbar_init(ptx::smem_addr(drain), 1);
+        ptx::mbar_init(ptx::smem_addr(drain), 2);
         *abort_flag = 0;
         *odd_flag = 0;
         ptx::fence_mbar_init();
@@ -188,7 +212,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             for (int i = std::max(0, at - C::kSlots); i < at; ++i)
                 ptx::mbar_wait_bounded(ptx::smem_addr(full + i % C::kSlots), (i / C::kSlots) & 1, nullptr, nullptr);
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 2) {
         // ---------------------------------------------------------------- MMAs
         // The whole warp walks the list and waits; one elected lane issues, so
         // that addresses and descriptors stay in uniform registers: the issue of
@@ -202,115 +226,117 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const uint32_t k_lo = tc::desc_lo(smem0 + C::kQ, 16), v_lo = tc::desc_lo(smem0 + C::kQ, C::kHalf);
         const uint32_t full0 = ptx::smem_addr(full), freed0 = ptx::smem_addr(freed);
         const int k_steps = (p.head_dim + 15) / 16;
-        int slot = 0, seg = 0;                       // ring slot and the parity of its tiles
-        uint32_t ring = 0, taken0 = 0, taken1 = 0;   // P tiles used, for the parities of p_full
+        const int stream = __shfl_sync(0xFFFFFFFFu, warp - 1, 0);
+        const uint32_t t_s = tm + stream * 128, t_o = tm + kO + stream * 128;
+        const uint32_t s_bar = ptx::smem_addr(s_full + stream), p_bar = ptx::smem_addr(p_full + stream);
+        const uint32_t o_bar = ptx::smem_addr(o_full + stream);
+        int slot = 0, seg = 0;
+        uint32_t ring = 0, taken = 0;                // parities: of the slot's tile, of P
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = __all_sync(0xFFFFFFFFu, wait_soon(bar, parity, abort_flag, p.status));
             tc::fence_after_sync();
             return ok;
         };
-        auto next_slot = [&](int &i, uint32_t &parity) {
-            if (++i == C::kSlots) {
-                i = 0;
-                parity ^= 1;
+        auto wait_tile = [&] { return wait(full0 + slot * 8, ring); };
+        auto advance = [&](int n) {
+            slot += n;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                ring ^= 1;
             }
         };
-        auto qk = [&](int i, int stream, int half, bool release) {
+        // Every tile of the ring is waited for by both warps, in order, and
+        // released by both -- by the end of its product or, where only the other
+        // stream takes it, at once: so neither can be a round ahead of or behind
+        // the slot's parity.
+        auto pass = [&] {
+            if (!wait_tile()) return;
+            if (lane == 0) ptx::mbar_arrive(freed0 + slot * 8);
+            advance(1);
+        };
+        auto qk = [&](int half) {
             if (tc::elect_one()) {
-                const uint32_t a = q_lo + half * (C::kTile >> 4), b = k_lo + i * (C::kTile >> 4);
-                const uint32_t d = tm + stream * 128;
+                const uint32_t a = q_lo + half * (C::kTile >> 4), b = k_lo + slot * (C::kTile >> 4);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
-                    if (k < k_steps) tc::mma_f16_ss(d, a + off, b + off, hi, id_qk, k != 0);
+                    if (k < k_steps) tc::mma_f16_ss(t_s, a + off, b + off, hi, id_qk, k != 0);
                 }
-                tc::commit(ptx::smem_addr(s_full + stream));
-                if (release) tc::commit(freed0 + i * 8);
+                tc::commit(s_bar);
+                tc::commit(freed0 + slot * 8);
             }
             __syncwarp();
         };
-        auto pv = [&](int i, int stream, bool first, bool last, bool release) {
+        auto pv = [&](bool first, bool last) {
             if (tc::elect_one()) {
-                const uint32_t b = v_lo + i * (C::kTile >> 4);
-                const uint32_t d = tm + kO + stream * 128, a = tm + stream * 128;
+                const uint32_t b = v_lo + slot * (C::kTile >> 4);
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_f16_ts(d, a + k * 8, b + k * (2048 >> 4), hi, id_pv, !first || k != 0);
-                if (last) tc::commit(ptx::smem_addr(o_full + stream));
-                if (release) tc::commit(freed0 + i * 8);
+                    tc::mma_f16_ts(t_o, t_s + k * 8, b + k * (2048 >> 4), hi, id_pv, !first || k != 0);
+                if (last) tc::commit(o_bar);
+                tc::commit(freed0 + slot * 8);
             }
             __syncwarp();
-        };
-        auto wait_tile = [&](int i, uint32_t parity) { return wait(full0 + i * 8, parity); };
-        auto wait_p = [&](int stream) {
-            return stream == 0 ? wait(ptx::smem_addr(p_full), taken0++ & 1) : wait(ptx::smem_addr(p_full + 1), taken1++ & 1);
         };
         while (ok && work.next(p, s)) {
             const int nt = s.tile1 - s.tile0;
             const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
             if (!wait(ptx::smem_addr(q_full), seg & 1)) break;
             ++seg;
-            if (!two) {
-                for (int j = 0; j < min(2, nt) && wait_tile(slot, ring); ++j) {
-                    qk(slot, j, 0, true);
-                    next_slot(slot, ring);
+            // the ring: K 0 (K 1), then V j, K j + ahead; with shared rows this
+            // stream takes its own tiles of it and passes over the others
+            const int ahead = two ? 1 : 2;
+            auto mine = [&](int j) { return two || (j & 1) == stream; };
+            for (int j = 0; j < min(ahead, nt) && ok; ++j) {
+                if (!mine(j)) {
+                    pass();
+                    continue;
                 }
-                for (int j = 0; j < nt && ok; ++j) {
-                    const int st = j & 1;
-                    if (!wait_tile(slot, ring) || !wait_p(st)) break;
-                    pv(slot, st, j < 2, j + 2 >= nt, true);
-                    next_slot(slot, ring);
-                    if (j + 2 < nt) {
-                        if (!wait_tile(slot, ring)) break;
-                        qk(slot, st, 0, true);
-                        next_slot(slot, ring);
-                    }
+                if (!wait_tile()) break;
+                qk(two ? stream : 0);
+                advance(1);
+            }
+            for (int j = 0; j < nt && ok; ++j) {
+                const bool more = j + ahead < nt;
+                if (!mine(j)) {
+                    pass();
+                    if (more && ok) pass();
+                    continue;
                 }
-            } else {
-                if (!wait_tile(slot, ring)) break;
-                qk(slot, 0, 0, false);
-                qk(slot, 1, 1, true);
-                next_slot(slot, ring);
-                for (int j = 0; j < nt && ok; ++j) {
-                    const bool more = j + 1 < nt;
-                    int after = slot;
-                    uint32_t after_ring = ring;
-                    next_slot(after, after_ring);
-                    if (!wait_tile(slot, ring) || !wait_p(0)) break;
-                    pv(slot, 0, j == 0, !more, false);
-                    if (more) {
-                        if (!wait_tile(after, after_ring)) break;
-                        qk(after, 0, 0, false);
-                    }
-                    if (!wait_p(1)) break;
-                    pv(slot, 1, j == 0, !more, true);
-                    if (more) qk(after, 1, 1, true);
-                    next_slot(slot, ring);
-                    if (more) next_slot(slot, ring);
+                if (!wait_tile() || !wait(p_bar, taken++ & 1)) break;
+                pv(j < ahead, !more);
+                advance(1);
+                if (more) {
+                    if (!wait_tile()) break;
+                    qk(two ? stream : 0);
+                    advance(1);
                 }
             }
+            // a stream without a tile has its O at once
+            if (!two && stream >= nt && ok && lane == 0) ptx::mbar_arrive(o_bar);
+            __syncwarp();
         }
-        // every MMA issued has completed once `drain` flips
+        // every MMA issued, of both streams, has completed once `drain` flips
         if (tc::elect_one()) {   // the lane that issued them
             tc::commit(ptx::smem_addr(drain));
             ptx::mbar_wait_bounded(ptx::smem_addr(drain), 0, nullptr, p.status);
         }
         __syncwarp();
-    } else {
+    } else if (warp >= 4) {
         // ---------------------------------------------------------------- softmax, epilogue
-        const int tid = threadIdx.x - 64;
+        const int tid = threadIdx.x - 128;
         const int stream = tid >> 7;
         const int quarter = warp & 3;                // tensor-memory lanes this warp may touch
         const int row = quarter * 32 + lane;         // row of the stream's 128
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t t_s = t_lane + stream * 128, t_o = t_lane + kO + stream * 128;
-        float *red = reinterpret_cast<float *>(smem);
-        float *pair_m = red + join_floats(kRows, kSoftmax), *pair_l = pair_m + 256;   // [2 streams][128 rows]
+        // the two streams' m and l at a segment's end, [2][128], in q's space
+        float *pair_m = reinterpret_cast<float *>(smem), *pair_l = pair_m + 256;
         const bool negative = p.scale_log2 < 0.f;
         const float scale = fabsf(p.scale_log2);
         int base = 0;                                // ring position of the segment's first tile
-        uint32_t tiles_done = 0, segs_done[2] = {0, 0};
+        uint32_t tiles_done = 0, segs_done = 0;
         bool ok = true;
         while (true) {
             // everybody is done with the segment before: q's space and O are free
@@ -367,23 +393,33 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const int key0 = (s.tile0 + j) * kKeys;
                 const bool drafted = key0 + kKeys > s.ctx;
                 if (warp_works) {
-                    float x[128];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tc::ld_32x32b_x32(t_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&x[c * 32]));
-                    tc::ld_wait();
+                    // The row twice, 32 scores at a time, the next 32 on their way
+                    // meanwhile: for its maximum, then for the weights. (All 128 in
+                    // registers spilled.)
+                    uint32_t seen[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
                     if (drafted) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const uint32_t seen = seen32(p, s, t, key0 + c * 32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((seen >> e) & 1u)) x[c * 32 + e] = -INFINITY;
-                        }
+                        for (int c = 0; c < 4; ++c) seen[c] = seen32(p, s, t, key0 + c * 32);
                     }
-                    float top[4] = {x[0], x[1], x[2], x[3]};
+                    uint32_t x[2][32];
+                    auto masked = [&](uint32_t(&v)[32], uint32_t bits) {
 #pragma unroll
-                    for (int e = 4; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], x[e]);
+                        for (int e = 0; e < 32; ++e)
+                            if (!((bits >> e) & 1u)) v[e] = 0xFF800000u;   // -inf
+                    };
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    tc::ld_32x32b_x32(t_s, x[0]);
+                    tc::ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tc::ld_32x32b_x32(t_s + ((c + 1) & 3) * 32, x[(c + 1) & 1]);   // the last: 0 again
+                        uint32_t(&v)[32] = x[c & 1];
+                        if (drafted) masked(v, seen[c]);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                        tc::ld_wait();
+                    }
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale - kWeightBias<T>;
                     const bool grown = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
                     if (__any_sync(0xFFFFFFFFu, grown)) {
@@ -406,28 +442,38 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         }
                     }
                     const float mm = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 scale2 = make_float2(scale, scale), mm2 = make_float2(-mm, -mm);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < 4; c += 2) {
                         uint32_t w[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float a = exp2_fast(fmaf(x[c * 64 + 2 * e], scale, -mm));
-                            const float b = exp2_fast(fmaf(x[c * 64 + 2 * e + 1], scale, -mm));
-                            sum[(2 * e) & 3] += a;
-                            sum[(2 * e + 1) & 3] += b;
-                            w[e] = Elem<T>::pack(a, b);
+                        for (int h = 0; h < 2; ++h) {
+                            if (c + h < 3) tc::ld_32x32b_x32(t_s + (c + h + 1) * 32, x[(h + 1) & 1]);
+                            uint32_t(&v)[32] = x[h];
+                            if (drafted) masked(v, seen[c + h]);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                float2 a = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, mm2);
+                                a.x = exp2_fast(a.x);
+                                a.y = exp2_fast(a.y);
+                                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], a);
+                                w[h * 16 + (e >> 1)] = Elem<T>::pack(a.x, a.y);
+                            }
+                            if (c + h < 3) tc::ld_wait();
                         }
-                        tc::st_32x32b_x32(t_s + c * 32, w);
+                        // over scores that have been read: 32 columns hold 64 weights
+                        tc::st_32x32b_x32(t_s + c * 16, w);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc::st_wait();
                 }
-                if (drafted && (!two || stream == 0)) {
-                    // The tile's values before P V reads them (with two row
-                    // halves stream 0's product comes first): rows past the last key
-                    // become zero, and so do infinities and NaN of drafted keys,
-                    // which the epilogue gives to the rows that see them.
+                if (drafted) {
+                    // The tile's values before this stream's P V reads them: rows
+                    // past the last key become zero, and so do infinities and NaN of
+                    // drafted keys, which the epilogue gives to the rows that see
+                    // them. With two row halves both streams do so, each for its
+                    // own product: a second write is the same zero.
                     const int v_at = base + (two ? 1 + j + min(j, nt - 1) : min(2, nt) + j + min(j, max(0, nt - 2)));
                     const int slot = v_at % C::kSlots;
                     ok = wait_soon(ptx::smem_addr(full + slot), (v_at / C::kSlots) & 1, abort_flag, p.status);
@@ -469,11 +515,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             base += 2 * nt;
 
             // ---- the segment's end: all MMAs of both streams are done
-            const int streams = two || nt > 1 ? 2 : 1;
-            for (int st = 0; st < streams; ++st) {
-                ok = ok && wait_soon(ptx::smem_addr(o_full + st), segs_done[st] & 1, abort_flag, p.status);
-                ++segs_done[st];
-            }
+            for (int st = 0; st < 2; ++st)
+                ok = ok && wait_soon(ptx::smem_addr(o_full + st), segs_done & 1, abort_flag, p.status);
+            ++segs_done;
             ok = __all_sync(0xFFFFFFFFu, ok);
             tc::fence_after_sync();
             if (!ptx::named_barrier_and(1, kSoftmax, ok)) {
@@ -548,13 +592,13 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     } else if (my_row < rows) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            __stcg(reinterpret_cast<float4 *>(slot + (c + e) * kRows + my_row * 4),
+                            __stcg(reinterpret_cast<float4 *>(slot + slot_at(kRows, my_row, c + e)),
                                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
                 }
                 if (my_row < rows && (two || stream == 0)) {
                     if (whole) {
-                        store_lse(p, s, row0 + my_row, mm, l);
+                        store_lse(p, s.token0, s.h, row0 + my_row, mm, l);
                     } else {
                         __stcg(slot + kRows * DP + my_row, m);
                         __stcg(slot + kRows * DP + kRows + my_row, l);
@@ -562,7 +606,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
             }
             tc::fence_before_sync();
-            if (!whole) join<T, kRows, DP, kSoftmax, true>(p, work, s, tid, rows, red, 1);
+            if (!whole && tid == 0 && s.tile1 == s.tiles) work.note_join(p, s, rows);
         }
     }
     __syncthreads();
@@ -614,27 +658,10 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
     const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * tiles;
     p.min_units = 2;
     const int ctas = (int)std::min<int64_t>(li.sms, std::max<int64_t>(1, units / p.min_units));
-    Scratch sc{};
-    if (!get_scratch(stream, (size_t)2 * ctas * slot_floats(kRows, DP),
-                     (size_t)a.kv_heads * ((size_t)(a.tokens * p.group) / kRows + (size_t)a.B), &sc))
-        return cudaErrorMemoryAllocation;
-    p.partials = sc.partials;
-    p.counters = sc.counters;
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
 #endif
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<DP>::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attention_tc_kernel<T, DP>, tk, tv, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_pair<T, kRows, DP>(attention_tc_kernel<T, DP>, ctas, kThreads, Cfg<DP>::kSmem, stream, tk, tv, p);
 }
 
 } // namespace
@@ -648,7 +675,7 @@ cudaError_t launch_tc_any(const awq_tree_attention_t &a, cudaStream_t stream)
 
 size_t tc_partial_floats(int sms, int64_t head_dim)
 {
-    return head_dim > 128 ? 0 : (size_t)2 * sms * slot_floats(kRows, head_dim <= 64 ? 64 : 128);
+    return head_dim > 128 ? 0 : scratch_floats(sms, kRows, head_dim <= 64 ? 64 : 128);
 }
 
 } // namespace attn

@@ -150,9 +150,8 @@ struct AppendProblem {
 cudaError_t launch_kv_append(const AppendProblem &p, cudaStream_t stream);
 
 cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream);
-// largest scratch any tree-attention launch of these bounds asks for
-void tree_attention_scratch(int64_t tokens, int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                            int sms, size_t *partial_floats, size_t *n_counters);
+// floats of partial sums that the largest tree-attention launch asks for, whatever the lengths
+size_t tree_attention_partial_floats(int64_t head_dim, int sms);
 
 cudaError_t launch_process_logits(const awq_logits_t &a, cudaStream_t stream);
 
