@@ -8,12 +8,15 @@
 //     both take every tile (a tile is read once for 256 rows);
 //   128 rows or fewer: both have the same rows, stream i takes tiles i, i + 2, ..,
 //     and their two sums are joined at the segment's end.
-// For a stream and tile: S = Q K^T (tcgen05, 128 x 128, into tensor memory), the
-// stream's four warps read S (a thread has one row: no shuffles), write
-// P = exp2(S - m) over it as 16-bit values, and O += P V takes P from tensor
-// memory. Tensor memory is full: S 2 x 128, O 2 x DP columns. A stream's MMAs
-// are issued by one thread and run in order, so S of the stream's next tile may be written over
-// P as soon as it is issued behind O += P V.
+// For a stream and half a tile (64 keys): S = Q K^T (tcgen05, 128 x 64, into tensor
+// memory), the stream's four warps read S (a thread has one row: no shuffles),
+// write P = exp2(S - m) over it as 16-bit values, and O += P V takes P from tensor
+// memory. Tensor memory is full: S 2 streams x 2 halves x 64, O 2 x DP columns.
+// A stream's MMAs are issued by one thread and run in order, so S of the next
+// tile's half may be written over P as soon as it is issued behind O += P V; and
+// while that runs, the softmax has the other half. (S of 128 keys at once left the
+// softmax waiting for both products of every tile: 4,700 cycles a tile of two
+// streams, twice what either side needs.)
 //
 // The maximum is lazy: O is rescaled only when a row's maximum has grown by more
 // than 2^kSlack since the last time (P then is up to 2^kSlack instead of 1, which
@@ -49,7 +52,7 @@ constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;    // threads of the softmax warps
 constexpr float kSlack = 8.f;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kO = 256;     // first column of O 0; S i is at 128 i
+constexpr uint32_t kO = 256;     // first column of O 0; S of stream i and half h is at 128 i + 64 h
 
 template <int DP>
 struct Cfg {
@@ -114,9 +117,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBarOff);   // [kSlots] tile landed
     uint64_t *freed = full + C::kSlots;      // [kSlots] MMAs that read the tile are done (two arrivals)
-    uint64_t *s_full = freed + C::kSlots;    // [2] S of the stream is complete
-    uint64_t *p_full = s_full + 2;           // [2] P of the stream is written
-    uint64_t *o_full = p_full + 2;           // [2] O of the stream and segment is complete
+    uint64_t *s_full = freed + C::kSlots;    // [2 streams][2 halves] S is complete
+    uint64_t *p_full = s_full + 4;           // [2][2] P is written
+    uint64_t *pv_done = p_full + 4;          // [2] the stream's last O += P V is complete
+    uint64_t *o_full = pv_done + 2;          // [2] O of the stream and segment is complete
     uint64_t *q_full = o_full + 2;
     uint64_t *drain = q_full + 1;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(drain + 1);
@@ -134,8 +138,11 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             ptx::mbar_init(ptx::smem_addr(freed + i), 2);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(ptx::smem_addr(s_full + i), 1);
-            ptx::mbar_init(ptx::smem_addr(p_full + i), 4);
+            for (int h = 0; h < 2; ++h) {
+                ptx::mbar_init(ptx::smem_addr(s_full + 2 * i + h), 1);
+                ptx::mbar_init(ptx::smem_addr(p_full + 2 * i + h), 4);
+            }
+            ptx::mbar_init(ptx::smem_addr(pv_done + i), 1);
             ptx::mbar_init(ptx::smem_addr(o_full + i), 1);
         }
         ptx::mbar_init(ptx::smem_addr(q_full), kSoftmax);
@@ -217,7 +224,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         // The whole warp walks the list and waits; one elected lane issues, so
         // that addresses and descriptors stay in uniform registers: the issue of
         // a product has to take less than the product (512 cycles).
-        constexpr uint32_t id_qk = tc::idesc_16bit_f32(128, kKeys, false, kBf16);
+        constexpr uint32_t id_qk = tc::idesc_16bit_f32(128, 64, false, kBf16);
         constexpr uint32_t id_pv = tc::idesc_16bit_f32(128, DP, true, kBf16);
         constexpr uint32_t hi = tc::desc_hi(1024);
         const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
@@ -228,8 +235,8 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const int k_steps = (p.head_dim + 15) / 16;
         const int stream = __shfl_sync(0xFFFFFFFFu, warp - 1, 0);
         const uint32_t t_s = tm + stream * 128, t_o = tm + kO + stream * 128;
-        const uint32_t s_bar = ptx::smem_addr(s_full + stream), p_bar = ptx::smem_addr(p_full + stream);
-        const uint32_t o_bar = ptx::smem_addr(o_full + stream);
+        const uint32_t s_bar = ptx::smem_addr(s_full + 2 * stream), p_bar = ptx::smem_addr(p_full + 2 * stream);
+        const uint32_t done_bar = ptx::smem_addr(pv_done + stream), o_bar = ptx::smem_addr(o_full + stream);
         int slot = 0, seg = 0;
         uint32_t ring = 0, taken = 0;                // parities: of the slot's tile, of P
         bool ok = true;
@@ -239,11 +246,10 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             return ok;
         };
         auto wait_tile = [&] { return wait(full0 + slot * 8, ring); };
-        auto advance = [&](int n) {
-            slot += n;
-            if (slot >= C::kSlots) {
-                slot -= C::kSlots;
-                ring ^= 1;
+        auto advance = [&](int &i, uint32_t &parity) {
+            if (++i == C::kSlots) {
+                i = 0;
+                parity ^= 1;
             }
         };
         // Every tile of the ring is waited for by both warps, in order, and
@@ -253,29 +259,33 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         auto pass = [&] {
             if (!wait_tile()) return;
             if (lane == 0) ptx::mbar_arrive(freed0 + slot * 8);
-            advance(1);
+            advance(slot, ring);
         };
-        auto qk = [&](int half) {
+        // half h of the tile in slot i: 64 rows of 128 bytes are 8 KB
+        constexpr uint32_t kHalfKeys = 64 * 128;
+        auto qk = [&](int i, int h, int q_half) {
             if (tc::elect_one()) {
-                const uint32_t a = q_lo + half * (C::kTile >> 4), b = k_lo + slot * (C::kTile >> 4);
+                const uint32_t a = q_lo + q_half * (C::kTile >> 4);
+                const uint32_t b = k_lo + i * (C::kTile >> 4) + h * (kHalfKeys >> 4);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
                     const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
-                    if (k < k_steps) tc::mma_f16_ss(t_s, a + off, b + off, hi, id_qk, k != 0);
+                    if (k < k_steps) tc::mma_f16_ss(t_s + h * 64, a + off, b + off, hi, id_qk, k != 0);
                 }
-                tc::commit(s_bar);
-                tc::commit(freed0 + slot * 8);
+                tc::commit(s_bar + h * 8);
+                if (h == 1) tc::commit(freed0 + i * 8);
             }
             __syncwarp();
         };
-        auto pv = [&](bool first, bool last) {
+        auto pv = [&](int i, int h, bool first, bool last) {
             if (tc::elect_one()) {
-                const uint32_t b = v_lo + slot * (C::kTile >> 4);
+                const uint32_t b = v_lo + i * (C::kTile >> 4) + h * (kHalfKeys >> 4);
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_f16_ts(t_o, t_s + k * 8, b + k * (2048 >> 4), hi, id_pv, !first || k != 0);
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_f16_ts(t_o, t_s + h * 64 + k * 8, b + k * (2048 >> 4), hi, id_pv, !first || k != 0);
+                tc::commit(done_bar);
+                if (h == 1) tc::commit(freed0 + i * 8);
                 if (last) tc::commit(o_bar);
-                tc::commit(freed0 + slot * 8);
             }
             __syncwarp();
         };
@@ -294,8 +304,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     continue;
                 }
                 if (!wait_tile()) break;
-                qk(two ? stream : 0);
-                advance(1);
+                qk(slot, 0, two ? stream : 0);
+                qk(slot, 1, two ? stream : 0);
+                advance(slot, ring);
             }
             for (int j = 0; j < nt && ok; ++j) {
                 const bool more = j + ahead < nt;
@@ -304,14 +315,21 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     if (more && ok) pass();
                     continue;
                 }
-                if (!wait_tile() || !wait(p_bar, taken++ & 1)) break;
-                pv(j < ahead, !more);
-                advance(1);
+                int next = slot;                     // of the K tile behind this V tile
+                uint32_t next_ring = ring;
+                advance(next, next_ring);
+                if (!wait_tile() || !wait(p_bar, taken & 1)) break;
+                pv(slot, 0, j < ahead, false);
                 if (more) {
-                    if (!wait_tile()) break;
-                    qk(two ? stream : 0);
-                    advance(1);
+                    if (!wait(full0 + next * 8, next_ring)) break;
+                    qk(next, 0, two ? stream : 0);
                 }
+                if (!wait(p_bar + 8, taken & 1)) break;
+                pv(slot, 1, false, !more);
+                if (more) qk(next, 1, two ? stream : 0);
+                ++taken;
+                advance(slot, ring);
+                if (more) advance(slot, ring);
             }
             // a stream without a tile has its O at once
             if (!two && stream >= nt && ok && lane == 0) ptx::mbar_arrive(o_bar);
@@ -384,42 +402,34 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const bool warp_works = (two ? stream * 128 : 0) + quarter * 32 < rows;
             const int t = min(row0 + my_row, s.n * p.group - 1) / p.group;    // its token
             float m = -INFINITY, l = 0.f;
-            for (int j = two ? 0 : stream; j < nt && ok; j += two ? 1 : 2) {
-                ok = wait_soon(ptx::smem_addr(s_full + stream), tiles_done & 1, abort_flag, p.status);
+            bool begun = false;                          // O has a product in it
+            for (int j = two ? 0 : stream; j < nt && ok; j += two ? 1 : 2, ++tiles_done) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                ok = wait_soon(ptx::smem_addr(s_full + 2 * stream + h), tiles_done & 1, abort_flag, p.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                ++tiles_done;
                 tc::fence_after_sync();
-                const int key0 = (s.tile0 + j) * kKeys;
-                const bool drafted = key0 + kKeys > s.ctx;
+                const int key0 = (s.tile0 + j) * kKeys + h * 64;
+                const bool drafted = key0 + 64 > s.ctx, tile_drafted = h == 0 && key0 + kKeys > s.ctx;
                 if (warp_works) {
-                    // The row twice, 32 scores at a time, the next 32 on their way
-                    // meanwhile: for its maximum, then for the weights. (All 128 in
-                    // registers spilled.)
-                    uint32_t seen[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                    uint32_t x[64];
+                    tc::ld_32x32b_x32(t_s + h * 64, *reinterpret_cast<uint32_t(*)[32]>(&x[0]));
+                    tc::ld_32x32b_x32(t_s + h * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&x[32]));
+                    tc::ld_wait();
                     if (drafted) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) seen[c] = seen32(p, s, t, key0 + c * 32);
-                    }
-                    uint32_t x[2][32];
-                    auto masked = [&](uint32_t(&v)[32], uint32_t bits) {
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t seen = seen32(p, s, t, key0 + c * 32);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((bits >> e) & 1u)) v[e] = 0xFF800000u;   // -inf
-                    };
+                            for (int e = 0; e < 32; ++e)
+                                if (!((seen >> e) & 1u)) x[c * 32 + e] = 0xFF800000u;   // -inf
+                        }
+                    }
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    tc::ld_32x32b_x32(t_s, x[0]);
-                    tc::ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tc::ld_32x32b_x32(t_s + ((c + 1) & 3) * 32, x[(c + 1) & 1]);   // the last: 0 again
-                        uint32_t(&v)[32] = x[c & 1];
-                        if (drafted) masked(v, seen[c]);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                        tc::ld_wait();
-                    }
+                    for (int e = 0; e < 64; e += 2)
+                        top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale - kWeightBias<T>;
                     const bool grown = mx > m + kSlack || (m == -INFINITY && mx > -INFINITY);
                     if (__any_sync(0xFFFFFFFFu, grown)) {
@@ -427,9 +437,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                         const float f = nm == m ? 1.f : exp2_fast(m - nm);
                         m = nm;
                         l *= f;
-                        // O so far (the MMAs that added to it are done: this
-                        // tile's S came after them)
-                        if (j >= (two ? 1 : 2)) {
+                        if (begun) {
+                            // The half before may still be added to O. (Those before
+                            // it are: this S was issued behind them.)
+                            const uint32_t half = 2 * tiles_done + h;
+                            ok = wait_soon(ptx::smem_addr(pv_done + stream), (half - 1) & 1, abort_flag, p.status);
+                            ok = __all_sync(0xFFFFFFFFu, ok);
+                            if (!ok) break;
+                            tc::fence_after_sync();
 #pragma unroll 1
                             for (int c = 0; c < DP / 32; ++c) {
                                 uint32_t o[32];
@@ -444,31 +459,21 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                     const float mm = m == -INFINITY ? 0.f : m;
                     const float2 scale2 = make_float2(scale, scale), mm2 = make_float2(-mm, -mm);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    uint32_t w[32];
 #pragma unroll
-                    for (int c = 0; c < 4; c += 2) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (c + h < 3) tc::ld_32x32b_x32(t_s + (c + h + 1) * 32, x[(h + 1) & 1]);
-                            uint32_t(&v)[32] = x[h];
-                            if (drafted) masked(v, seen[c + h]);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float2 a = fma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), scale2, mm2);
-                                a.x = exp2_fast(a.x);
-                                a.y = exp2_fast(a.y);
-                                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], a);
-                                w[h * 16 + (e >> 1)] = Elem<T>::pack(a.x, a.y);
-                            }
-                            if (c + h < 3) tc::ld_wait();
-                        }
-                        // over scores that have been read: 32 columns hold 64 weights
-                        tc::st_32x32b_x32(t_s + c * 16, w);
+                    for (int e = 0; e < 64; e += 2) {
+                        float2 a = fma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), scale2, mm2);
+                        a.x = exp2_fast(a.x);
+                        a.y = exp2_fast(a.y);
+                        sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], a);
+                        w[e >> 1] = Elem<T>::pack(a.x, a.y);
                     }
+                    tc::st_32x32b_x32(t_s + h * 64, w);
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc::st_wait();
                 }
-                if (drafted) {
+                begun = true;
+                if (tile_drafted) {
                     // The tile's values before this stream's P V reads them: rows
                     // past the last key become zero, and so do infinities and NaN of
                     // drafted keys, which the epilogue gives to the rows that see
@@ -510,7 +515,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(p_full + stream));
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(p_full + 2 * stream + h));
+                }
+                if (!ok) break;
             }
             base += 2 * nt;
 
