@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kRows = 16;        // rows of q a CTA works on (one mma.sync M)
 constexpr int kKeys = 64;        // keys a tile
+constexpr int kBlockCost = 1;    // a row block's beginning and end, in tiles
 constexpr int kConsumers = 128;  // threads of the four consumer warps
 constexpr int kThreads = kConsumers + 32;
 
@@ -103,7 +104,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     }
     ptx::launch_dependents();
     ptx::wait_prerequisites();
-    Work<kRows, kKeys> work;
+    Work<kRows, kKeys, kBlockCost> work;
     if (!work.template find<kThreads>(p)) return;   // its barriers also publish the mbarriers
     Segment s;
 
@@ -409,7 +410,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             }
         } else {
             if (warp == 0) {
-                float *slot = p.partials + (int64_t)work.slot_of(blockIdx.x, s.u0) * slot_floats(kRows, DP);
+                float *slot = p.partials + (int64_t)work.slot_of(s) * slot_floats(kRows, DP);
 #pragma unroll
                 for (int i = 0; i < DP / 8; ++i) {
                     const int c = i * 8 + t4 * 2;
@@ -472,8 +473,8 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     // a launch no larger than the work the bounds allow
     const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
-    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * tiles;
-    p.min_units = 4;
+    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * (kBlockCost + tiles);
+    p.min_units = kBlockCost + 4;
     const int ctas = (int)std::min<int64_t>(li.ctas, std::max<int64_t>(1, units / p.min_units));
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();

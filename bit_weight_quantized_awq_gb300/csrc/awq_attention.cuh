@@ -5,18 +5,19 @@
 // Rows. The queries that share one head of the cache are, for a request with n
 // new tokens and `group` query heads a key-value head, n * group rows; row r is
 // token r / group, head r % group of the group. They are cut into blocks of RB
-// rows, the keys into tiles of KT. A unit of work is one (request, key-value
-// head, row block, key tile); all units, in that order, form one line, and CTA c
-// of G takes the range [c U / G, (c + 1) U / G). So every CTA has the same work
+// rows, the keys into tiles of KT. The work is the row blocks of all (request,
+// key-value head) pairs, one after another on a line: a block takes kBlockCost
+// units for its beginning and end and its weight for each tile. CTA c of G takes
+// the tiles that begin in [c U / G, (c + 1) U / G). So every CTA has the same work
 // whatever the lengths are, a long cache is split along its length, and nothing
 // but the lengths on the device is needed to find a CTA's range.
 //
 // Pieces. A row block whose tiles fall to several CTAs is a sum of pieces
 // (m, l, O): O = sum_j exp2(s_j - m) v_j and l = sum_j exp2(s_j - m), joined by
 //   M = max m,  L = sum l exp2(m - M),  out = (sum O exp2(m - M)) / L.
-// Each piece is written to a slot of its CTA (its first segment in slot 0, its
-// last in slot 1), and the CTA that has a row block's last piece writes down what
-// there is to join. A second kernel, launched as a programmatic dependent, joins
+// Each piece is written to a slot of its CTA (one that begins its row block in
+// slot 1, any other in slot 0), and the CTA that has a row block's last piece
+// writes down what there is to join. A second kernel, launched as a programmatic dependent, joins
 // the pieces in the order of the CTAs, so the sum's order is the same in every
 // call, and no CTA ever waits for another. (Joined by whichever CTA came last the
 // pieces took 10 to 20 us at 256 rows: one CTA's loads, behind a fence.)
@@ -37,8 +38,7 @@ namespace attn {
 // What is to be joined because a CTA has the last piece of a split row block.
 struct Join {
     int valid;
-    int cta0, slot0;        // CTA of the first piece, and its slot; the others are slot 0 of
-    int cta1;               // the CTAs after it up to cta1
+    int cta0, cta1;         // the pieces: slot 1 of cta0, slot 0 of those after it up to cta1
     int h, rb, token0, rows;
 };
 
@@ -58,7 +58,7 @@ struct Params {
     int table_width, mask_words;
     int B, tokens, q_heads, kv_heads, group, head_dim, num_blocks;
     int shift;              // log2 of the block size
-    int min_units;          // a CTA takes at least this many units (fewer pieces to join)
+    int min_units;          // a CTA takes at least this many units: one tile at least
     float scale_log2;       // scale * log2(e): scores are kept in powers of two
 #ifdef AWQ_FAULT_TEST
     int fault;              // CTA 0's producer issues nothing (fault-test build only)
@@ -72,13 +72,13 @@ struct Segment {
     int b, h, rb;
     int ctx, n, token0;     // the request: context length, new tokens, first row of q
     int tile0, tile1, tiles;
-    int64_t u0;             // unit of the row block's first tile
+    int64_t u0;             // the row block's first unit
     __device__ bool whole() const { return tile0 == 0 && tile1 == tiles; }
 };
 
-template <int RB, int KT>
+template <int RB, int KT, int kBlockCost>
 struct Work {
-    int64_t units, pos, end;
+    int64_t units, pos, end;   // pos: where this CTA's next row block begins on the line
     int ctas;               // CTAs that take part
     int b, h, rb, tile, tiles;
     int ctx, n, token0, row_blocks;
@@ -92,16 +92,37 @@ struct Work {
         return (ctx + seen + KT - 1) / KT;
     }
     static __device__ int row_blocks_of(const Params &p, int n) { return (n * p.group + RB - 1) / RB; }
+    // Units a tile: 1, or 2 where it takes the tensor-core kernel twice as long -- a
+    // block of more than 128 rows, and any first block, whose tiles come from HBM
+    // (those of the later ones are in L2 by then).
+    static __device__ int weight_of(const Params &p, int n, int rb)
+    {
+        return RB > 128 && (rb == 0 || n * p.group - rb * RB > 128) ? 2 : 1;
+    }
+    static __device__ int64_t block_units(const Params &p, int ctx, int n, int rb)
+    {
+        return kBlockCost + (int64_t)tiles_of(p, ctx, n, rb) * weight_of(p, n, rb);
+    }
     static __device__ int64_t head_units(const Params &p, int ctx, int n)
     {
         const int blocks = row_blocks_of(p, n);
-        if (p.mask != nullptr) return (int64_t)blocks * tiles_of(p, ctx, n, 0);
+        if (blocks == 0) return 0;
+        if (p.mask != nullptr)
+            return (blocks - 1) * block_units(p, ctx, n, 0) + block_units(p, ctx, n, blocks - 1);
         int64_t sum = 0;
-        for (int rb = 0; rb < blocks; ++rb) sum += tiles_of(p, ctx, n, rb);
+        for (int rb = 0; rb < blocks; ++rb) sum += block_units(p, ctx, n, rb);
         return sum;
     }
     __device__ int64_t begin_of(int c) const { return units * c / ctas; }
     __device__ int cta_of(int64_t u) const { return (int)(((u + 1) * ctas - 1) / units); }
+    // A block's first tile begins at its first unit u0, tile i at u0 + kBlockCost + i
+    // weight: the first one that begins at `at` or later.
+    static __device__ int first_tile(int64_t at, int64_t u0, int weight, int tiles)
+    {
+        if (at <= u0) return 0;
+        const int64_t i = (at - u0 - kBlockCost + weight - 1) / weight;
+        return (int)min((int64_t)tiles, max((int64_t)1, i));
+    }
 
     // All threads of the CTA (THREADS of them, a multiple of 32) call this. False if there is
     // nothing to do for this CTA; if the lengths are not valid, for any CTA.
@@ -169,17 +190,18 @@ struct Work {
         rem -= h * per_head;
         rb = 0;
         if (p.mask != nullptr) {
-            tiles = tiles_of(p, ctx, n, 0);
-            rb = (int)(rem / tiles);
-            rem -= (int64_t)rb * tiles;
+            const int64_t full = block_units(p, ctx, n, 0);
+            rb = (int)min((int64_t)(row_blocks - 1), rem / full);
+            rem -= rb * full;
         } else {
-            tiles = tiles_of(p, ctx, n, 0);
-            while (rem >= tiles) {
-                rem -= tiles;
-                tiles = tiles_of(p, ctx, n, ++rb);
+            for (int64_t u = block_units(p, ctx, n, 0); rem >= u; u = block_units(p, ctx, n, rb)) {
+                rem -= u;
+                ++rb;
             }
         }
-        tile = (int)rem;
+        tiles = tiles_of(p, ctx, n, rb);
+        tile = first_tile(pos, pos - rem, weight_of(p, n, rb), tiles);
+        pos -= rem;
         return true;
     }
 
@@ -191,11 +213,29 @@ struct Work {
         row_blocks = row_blocks_of(p, n);
     }
 
+    __device__ void next_block(const Params &p)
+    {
+        pos += block_units(p, ctx, n, rb);
+        tile = 0;
+        if (pos >= end) return;
+        if (++rb == row_blocks) {
+            rb = 0;
+            if (++h == p.kv_heads) {
+                h = 0;
+                do {
+                    ++b;
+                    load(p);
+                } while (n == 0);
+            }
+        }
+        tiles = tiles_of(p, ctx, n, rb);
+    }
+
     // The next segment of this CTA's range; every thread walks the same list.
     __device__ bool next(const Params &p, Segment &s)
     {
+        if (pos < end && tile == tiles) next_block(p);   // the range began behind a block's last tile
         if (pos >= end) return false;
-        const int count = (int)min((int64_t)(tiles - tile), end - pos);
         s.b = b;
         s.h = h;
         s.rb = rb;
@@ -203,34 +243,20 @@ struct Work {
         s.n = n;
         s.token0 = token0;
         s.tile0 = tile;
-        s.tile1 = tile + count;
+        s.tile1 = first_tile(end, pos, weight_of(p, n, rb), tiles);
         s.tiles = tiles;
-        s.u0 = pos - tile;
-        pos += count;
-        if (pos < end) {
-            tile = 0;
-            if (++rb == row_blocks) {
-                rb = 0;
-                if (++h == p.kv_heads) {
-                    h = 0;
-                    do {
-                        ++b;
-                        load(p);
-                    } while (n == 0);
-                }
-            }
-            tiles = tiles_of(p, ctx, n, rb);
-        }
+        s.u0 = pos;
+        if (s.tile1 <= s.tile0) return false;            // no tile begins in what is left
+        next_block(p);
         return true;
     }
 
-    // The slot of CTA c's piece of the row block whose first unit is u0.
-    __device__ int slot_of(int c, int64_t u0) const { return 2 * c + (begin_of(c) >= u0 ? 0 : 1); }
+    // The slot of this CTA's piece.
+    static __device__ int slot_of(const Segment &s) { return 2 * blockIdx.x + (s.tile0 == 0 ? 1 : 0); }
     // One thread of a CTA whose segment is a row block's last piece, of several.
     __device__ void note_join(const Params &p, const Segment &s, int rows) const
     {
-        const int c0 = cta_of(s.u0);
-        p.joins[blockIdx.x] = Join{1, c0, slot_of(c0, s.u0), (int)blockIdx.x, s.h, s.rb, s.token0, rows};
+        p.joins[blockIdx.x] = Join{1, cta_of(s.u0), (int)blockIdx.x, s.h, s.rb, s.token0, rows};
     }
 };
 
@@ -347,63 +373,69 @@ __device__ __forceinline__ void store_lse(const Params &p, int token0, int h, in
     p.lse[t * p.q_heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
-// Joins the pieces of the row block whose last one CTA blockIdx.x had, columns
-// 32 blockIdx.y .. + 31. A thread has one row; where the rows are fewer than the
-// threads, `subs` of them share a row's pieces and add up their parts in shared
-// memory. Eight 16-byte loads a piece, of two pieces, are under way at a time: the
-// pieces come from L2.
+// Joins the pieces of the row block whose last one CTA blockIdx.x had. A thread has
+// eight columns of one row, or of a part of its pieces: `subs` threads share a
+// row's pieces and add up their parts in shared memory. All loads of eight pieces
+// are under way at a time -- the pieces come from L2, half a microsecond away, and
+// there are seldom more -- so that a join is about one such wait.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinColumns = 8;
+// eight-column groups of a CTA
+constexpr int join_groups(int rb) { return rb <= 16 ? 4 : 1; }
 
 template <typename T, int RB, int DP>
 __global__ void __launch_bounds__(kJoinThreads)
 attention_join_kernel(const __grid_constant__ Params p)
 {
-    __shared__ float part[kJoinThreads][33];
+    constexpr int kGroups = join_groups(RB), kBatch = 8;
+    __shared__ float part[kJoinThreads][kJoinColumns + 1];
     __shared__ float part_m[kJoinThreads], part_l[kJoinThreads];
     ptx::launch_dependents();
     ptx::wait_prerequisites();
     const Join j = p.joins[blockIdx.x];
-    const int c0 = blockIdx.y * 32;
-    if (!j.valid || c0 >= p.head_dim) return;
-    const int lanes = j.rows <= 16 ? 16 : (j.rows + 31) & ~31;      // rows, rounded up
-    const int subs = kJoinThreads / lanes;
-    const int r = threadIdx.x % lanes, sub = threadIdx.x / lanes;
+    if (!j.valid) return;
+    const int lanes = RB <= 16 ? 16 : (j.rows + 31) & ~31;          // rows, rounded up
+    const int per_sub = lanes * kGroups, subs = kJoinThreads / per_sub;
+    const int sub = threadIdx.x / per_sub, in_sub = threadIdx.x % per_sub;
+    const int r = in_sub % lanes;
+    const int col = (blockIdx.y * kGroups + in_sub / lanes) * kJoinColumns;
+    const bool works = sub < subs && r < j.rows && col < p.head_dim;
     constexpr int SF = slot_floats(RB, DP);
-    auto slot = [&](int c) { return p.partials + (int64_t)(c == j.cta0 ? j.slot0 : 2 * c) * SF; };
     float m = -INFINITY, l = 0.f;
-    float acc[32];
+    float acc[kJoinColumns];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-    if (sub < subs && r < j.rows) {
-#pragma unroll 8
-        for (int c = j.cta0 + sub; c <= j.cta1; c += subs) m = fmaxf(m, __ldcg(slot(c) + RB * DP + r));
-        const float mx = m == -INFINITY ? 0.f : m;
-        for (int c = j.cta0 + sub; c <= j.cta1; c += 2 * subs) {
-            float4 v[2][8];
-            float mc[2], lc[2];
-            const bool both = c + subs <= j.cta1;
+    for (int e = 0; e < kJoinColumns; ++e) acc[e] = 0.f;
+    if (works) {
+        for (int c = j.cta0 + sub; c <= j.cta1; c += kBatch * subs) {
+            float4 v[kBatch][2];
+            float mc[kBatch], lc[kBatch];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u && !both) break;
-                const float *from = slot(c + u * subs);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[u][i] = __ldcg(reinterpret_cast<const float4 *>(from + slot_at(RB, r, c0 + 4 * i)));
+            for (int u = 0; u < kBatch; ++u) {
+                const int cu = c + u * subs;
+                mc[u] = -INFINITY;
+                if (cu > j.cta1) continue;
+                const float *from = p.partials + (int64_t)(2 * cu + (cu == j.cta0 ? 1 : 0)) * SF;
                 mc[u] = __ldcg(from + RB * DP + r);
                 lc[u] = __ldcg(from + RB * DP + RB + r);
+                v[u][0] = __ldcg(reinterpret_cast<const float4 *>(from + slot_at(RB, r, col)));
+                v[u][1] = __ldcg(reinterpret_cast<const float4 *>(from + slot_at(RB, r, col + 4)));
             }
+            float top = m;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u && !both) break;
+            for (int u = 0; u < kBatch; ++u) top = fmaxf(top, mc[u]);
+            const float mx = top == -INFINITY ? 0.f : top, w0 = exp2_fast(m - mx);
+            l *= w0;
+#pragma unroll
+            for (int e = 0; e < kJoinColumns; ++e) acc[e] *= w0;
+            m = top;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                if (c + u * subs > j.cta1) break;
                 const float w = exp2_fast(mc[u] - mx);
                 l += lc[u] * w;
+                const float *f = reinterpret_cast<const float *>(v[u]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[4 * i] += v[u][i].x * w;
-                    acc[4 * i + 1] += v[u][i].y * w;
-                    acc[4 * i + 2] += v[u][i].z * w;
-                    acc[4 * i + 3] += v[u][i].w * w;
-                }
+                for (int e = 0; e < kJoinColumns; ++e) acc[e] += f[e] * w;
             }
         }
     }
@@ -411,35 +443,32 @@ attention_join_kernel(const __grid_constant__ Params p)
         part_m[threadIdx.x] = m;
         part_l[threadIdx.x] = l;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) part[threadIdx.x][e] = acc[e];
+        for (int e = 0; e < kJoinColumns; ++e) part[threadIdx.x][e] = acc[e];
         __syncthreads();
-        if (sub != 0 || r >= j.rows) return;
+        if (sub != 0 || !works) return;
         float top = m;
-        for (int i = 1; i < subs; ++i) top = fmaxf(top, part_m[i * lanes + r]);
+        for (int i = 1; i < subs; ++i) top = fmaxf(top, part_m[i * per_sub + in_sub]);
         const float mx = top == -INFINITY ? 0.f : top, w0 = exp2_fast(m - mx);
         l *= w0;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[e] *= w0;
+        for (int e = 0; e < kJoinColumns; ++e) acc[e] *= w0;
         for (int i = 1; i < subs; ++i) {
-            const float w = exp2_fast(part_m[i * lanes + r] - mx);
-            l += part_l[i * lanes + r] * w;
+            const float w = exp2_fast(part_m[i * per_sub + in_sub] - mx);
+            l += part_l[i * per_sub + in_sub] * w;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] += part[i * lanes + r][e] * w;
+            for (int e = 0; e < kJoinColumns; ++e) acc[e] += part[i * per_sub + in_sub][e] * w;
         }
         m = top;
     }
-    if (sub != 0 || r >= j.rows) return;
+    if (sub != 0 || !works) return;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int row = j.rb * RB + r;
     const int64_t token = j.token0 + row / p.group;
-    T *out = static_cast<T *>(p.out) + (token * p.q_heads + (int64_t)j.h * p.group + row % p.group) * p.head_dim + c0;
-#pragma unroll
-    for (int e = 0; e < 32; e += 8)
-        if (c0 + e < p.head_dim)
-            *reinterpret_cast<uint4 *>(out + e) =
-                make_uint4(Elem<T>::pack(acc[e] * inv, acc[e + 1] * inv), Elem<T>::pack(acc[e + 2] * inv, acc[e + 3] * inv),
-                           Elem<T>::pack(acc[e + 4] * inv, acc[e + 5] * inv), Elem<T>::pack(acc[e + 6] * inv, acc[e + 7] * inv));
-    if (blockIdx.y == 0) store_lse(p, j.token0, j.h, row, m == -INFINITY ? 0.f : m, l);
+    T *out = static_cast<T *>(p.out) + (token * p.q_heads + (int64_t)j.h * p.group + row % p.group) * p.head_dim + col;
+    *reinterpret_cast<uint4 *>(out) =
+        make_uint4(Elem<T>::pack(acc[0] * inv, acc[1] * inv), Elem<T>::pack(acc[2] * inv, acc[3] * inv),
+                   Elem<T>::pack(acc[4] * inv, acc[5] * inv), Elem<T>::pack(acc[6] * inv, acc[7] * inv));
+    if (col == 0) store_lse(p, j.token0, j.h, row, m == -INFINITY ? 0.f : m, l);
 }
 
 // Launches a main kernel of `ctas` CTAs and, unless there is one only, its join.
@@ -464,7 +493,8 @@ cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t 
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (ctas > 1) {
-        cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.head_dim + 31) / 32);
+        constexpr int kColumns = kJoinColumns * join_groups(RB);
+        cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.head_dim + kColumns - 1) / kColumns);
         cfg.blockDim = dim3(kJoinThreads);
         cfg.dynamicSmemBytes = 0;
         e = cudaLaunchKernelEx(&cfg, attention_join_kernel<T, RB, DP>, p);

@@ -48,6 +48,7 @@ namespace {
 
 constexpr int kRows = 256;       // rows of a block
 constexpr int kKeys = 128;       // keys of a tile
+constexpr int kBlockCost = 2;    // a row block's beginning and end: as a tile of the heavier kind
 constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;    // threads of the softmax warps
 constexpr float kSlack = 8.f;
@@ -130,7 +131,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 
     ptx::launch_dependents();
     ptx::wait_prerequisites();
-    Work<kRows, kKeys> work;
+    Work<kRows, kKeys, kBlockCost> work;
     if (!work.template find<kThreads>(p)) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
@@ -546,7 +547,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             const float mm = m == -INFINITY ? 0.f : m;
             const bool whole = s.whole(), odd = *odd_flag != 0;
-            float *slot = p.partials + (int64_t)work.slot_of(blockIdx.x, s.u0) * slot_floats(kRows, DP);
+            float *slot = p.partials + (int64_t)work.slot_of(s) * slot_floats(kRows, DP);
             if (warp_works) {
                 const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
                 f0 *= inv;
@@ -662,8 +663,8 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
         return cudaErrorInvalidValue;
     const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
-    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * tiles;
-    p.min_units = 2;
+    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * (kBlockCost + 2 * tiles);
+    p.min_units = kBlockCost + 4;
     const int ctas = (int)std::min<int64_t>(li.sms, std::max<int64_t>(1, units / p.min_units));
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
