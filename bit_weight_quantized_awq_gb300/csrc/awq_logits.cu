@@ -1,14 +1,14 @@
 // awq_logits.cu -- penalties for repeated tokens, biases and grammar masks on
 // logits, in one pass over them:
-//   x = x > 0 ? x / rep : x * rep   (token known),  x -= freq * count,
+//   x = x > 0 ? x / rep : x * rep   (token known; by 1 / rep),  x -= freq * count,
 //   x -= pres (count > 0),  x += bias,  -inf where the grammar's bit is 0.
 //
 // Bound: every logit is read and written once (HBM); a row's history has a few
 // thousand tokens against a hundred thousand logits. A CTA owns a range of kRange
 // vocabulary entries (rounded up to fill the GPU) and a run of rows. It counts the tokens of the row's
 // history that fall into its range in shared memory (a counter and a touched bit
-// an entry), then streams the logits: 16 bytes at a time, and only pieces with a
-// touched or biased entry look further. Consecutive rows of one request -- the
+// an entry), then takes the logits, fetched a row ahead, 16 bytes at a time; only
+// pieces with a touched or biased entry look further. Consecutive rows of one request -- the
 // nodes of a drafted tree -- share the counts: only the tokens of the row's own
 // path are added before and taken back after it. Counts are whole numbers, so the
 // atomics' order does not matter.
@@ -26,7 +26,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRange = 8192;              // vocabulary entries of a CTA
-constexpr int kWords = kRange / 32;
+constexpr int kBitmap = kRange / 32 + 4;  // words of a bitmap of the range: one to spare, and 16-byte pieces
+constexpr int kSmemWords = 2 * kRange + 2 * kBitmap;
 constexpr unsigned kPrompt = 1u << 31;    // counter: in the prompt; below it the generated count
 
 struct LogitsParams {
@@ -60,15 +61,24 @@ __device__ __forceinline__ unsigned bits_at(const unsigned *map, int at, int cou
     return __funnelshift_r(map[w], map[w + 1], at & 31) & ((1u << count) - 1);
 }
 
+// CTAs an SM has room for: a row of 16 or 32 KB is on its way to each
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+constexpr int kPerSm = sizeof(T) == 4 ? 2 : 3;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kPerSm<T>)
 process_logits_kernel(const __grid_constant__ LogitsParams p)
 {
     constexpr int kVec = 16 / sizeof(T);
+    constexpr int kHeld = kRange / (kThreads * kVec);   // 16-byte pieces of a row that a thread holds
+    constexpr unsigned kAll = (1u << kVec) - 1;
+    constexpr int kStep = kThreads * kVec;              // entries between a thread's pieces: whole words of bits
+    static_assert(kHeld * kVec == 32 && kStep % 32 == 0, "the grammar's bits of a thread's pieces fill a word");
     extern __shared__ unsigned smem[];
     unsigned *counts = smem;                       // [kRange]
-    unsigned *touched = counts + kRange;           // [kWords + 1]
-    unsigned *biased = touched + kWords + 1;       // [kWords + 1]
+    unsigned *touched = counts + kRange;           // [kBitmap]
+    unsigned *biased = touched + kBitmap;          // [kBitmap]
+    float *bias = reinterpret_cast<float *>(biased + kBitmap);   // [kRange], set where the bit is
     const awq_logits_t &a = p.a;
     const int tid = threadIdx.x;
     const int64_t v0 = (int64_t)blockIdx.x * kRange;
@@ -79,161 +89,220 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
     ptx::launch_dependents();
     ptx::wait_prerequisites();
 
-    auto count_token = [&](int64_t token, unsigned add) {
-        const int64_t at = token - v0;
+    auto count_token = [&](int token, unsigned add) {
+        const int at = token - (int)v0;
         if (at < 0 || at >= range) {
-            if (token >= a.vocab) bad |= kStatusBadIndex;
+            if (token >= (int)a.vocab) bad |= kStatusBadIndex;
             return;
         }
         if (add == kPrompt) atomicOr(counts + at, kPrompt);
         else atomicAdd(counts + at, add);
         atomicOr(touched + (at >> 5), 1u << (at & 31));
     };
-
-    auto clamp_offset = [&](int64_t at, int64_t size) {
+    auto clamp_offset = [&](int at, int64_t size) {
         if (at < 0 || at > size) bad |= kStatusBadIndex;
-        return min(max(at, (int64_t)0), size);
+        return (int)min(max((int64_t)at, (int64_t)0), size);
     };
 
-    int64_t have = -2;                             // request whose counts are held (-1: a row without one)
-    for (int64_t r = r_lo; r < r_hi; ++r) {
+    // A row as it is fetched, a row ahead of its turn: the thread's pieces of its
+    // logits, the grammar's bits of all of them in one word, its word of the path,
+    // and what is known of its request.
+    struct Row {
+        const T *in;
+        const int32_t *mask;       // the grammar's words from the range's first entry on
+        int head, pieces;          // elements before the first 16-byte boundary, whole pieces behind it
+        int request, history_lo, history_hi, prompt, bias_lo, bias_hi, first;
+        float rep, freq, pres;
+        unsigned path, allowed;
+        uint4 raw[kHeld];
+    };
+    auto fetch = [&](int64_t r, Row &row) {
         int64_t b = a.row_request ? a.row_request[r] : r;
         if (b < 0 || b >= a.B) {
             if (a.B > 0 || a.row_request) bad |= kStatusBadIndex;
             b = -1;
         }
-        const float rep = b >= 0 && a.repetition ? a.repetition[b] : 1.f;
-        const float freq = b >= 0 && a.frequency ? a.frequency[b] : 0.f;
-        const float pres = b >= 0 && a.presence ? a.presence[b] : 0.f;
-        const bool penal = rep != 1.f || freq != 0.f || pres != 0.f;   // else counts change nothing
-        int bias_lo = 0, bias_hi = 0;
-        if (b >= 0 && a.bias_tokens) {
-            bias_lo = (int)clamp_offset(a.bias_offsets[b], a.bias_size);
-            bias_hi = (int)clamp_offset(a.bias_offsets[b + 1], a.bias_size);
+        row.path = a.tree_mask && tid < a.mask_words * 32 ? (unsigned)a.tree_mask[r * a.mask_words + (tid >> 5)] : 0u;
+        row.mask = nullptr;
+        if (a.grammar_mask) {
+            const int64_t m = a.grammar_rows ? a.grammar_rows[r] : r;
+            if (m >= 0 && m < a.grammar_count) row.mask = a.grammar_mask + m * p.grammar_words + (v0 >> 5);
+            else if (m != -1 || !a.grammar_rows) bad |= kStatusBadIndex;
         }
+        row.in = static_cast<const T *>(a.logits) + r * a.logits_row_stride + v0;
+        const T *out = static_cast<const T *>(a.out) + r * a.out_row_stride + v0;
+        // all one by one where input and output do not share their alignment
+        const unsigned mis_in = (unsigned)(reinterpret_cast<uintptr_t>(row.in) / sizeof(T)) % kVec;
+        const unsigned mis_out = (unsigned)(reinterpret_cast<uintptr_t>(out) / sizeof(T)) % kVec;
+        row.head = mis_in == mis_out ? min(range, (int)((kVec - mis_in) % kVec)) : range;
+        row.pieces = (range - row.head) / kVec;
+        row.allowed = ~0u;
+        const int at = row.head + tid * kVec;      // the thread's first piece; the others kStep further on each
+        const uint4 *piece = reinterpret_cast<const uint4 *>(row.in + at);
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+            if (tid + u * kThreads < row.pieces) row.raw[u] = __ldcs(piece + u * kThreads);
+        if (row.mask) {
+            row.allowed = 0;
+            const int32_t *w = row.mask + (at >> 5);
+            const bool crosses = (at & 31) + kVec > 32;
+#pragma unroll
+            for (int u = 0; u < kHeld; ++u)
+                if (tid + u * kThreads < row.pieces) {
+                    const unsigned lo = (unsigned)w[u * (kStep / 32)], hi = crosses ? (unsigned)w[u * (kStep / 32) + 1] : 0u;
+                    row.allowed |= (__funnelshift_r(lo, hi, at & 31) & kAll) << (u * kVec);
+                }
+        }
+        row.request = (int)b;
+        row.rep = b >= 0 && a.repetition ? a.repetition[b] : 1.f;
+        row.freq = b >= 0 && a.frequency ? a.frequency[b] : 0.f;
+        row.pres = b >= 0 && a.presence ? a.presence[b] : 0.f;
+        row.history_lo = row.history_hi = row.prompt = row.bias_lo = row.bias_hi = row.first = 0;
+        if (b >= 0 && a.history) {
+            row.history_lo = a.history_offsets[b];
+            row.history_hi = a.history_offsets[b + 1];
+            if (a.prompt_lens) row.prompt = a.prompt_lens[b];
+        }
+        if (b >= 0 && a.bias_tokens) {
+            row.bias_lo = a.bias_offsets[b];
+            row.bias_hi = a.bias_offsets[b + 1];
+        }
+        if (b >= 0 && a.draft_tokens) row.first = a.cu_new[b];
+    };
+
+    Row row;
+    fetch(r_lo, row);
+    int have = -2;                                 // request whose counts are held (-1: a row without one)
+    float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
+    bool penal = false, any_bias = false;          // else counts change nothing; no bias in the range
+    int64_t first = 0;                             // the request's first drafted token
+    int my_token = -1;                             // its token number tid
+    for (int64_t r = r_lo; r < r_hi; ++r) {
+        const int b = row.request;
         if (b != have) {
             have = b;
-            __syncthreads();
-            for (int i = tid; i < kRange + 2 * kWords + 2; i += kThreads) smem[i] = 0;
-            __syncthreads();
-            if (penal && a.history) {
-                const int64_t h_lo = clamp_offset(a.history_offsets[b], a.history_size);
-                const int64_t h_hi = clamp_offset(a.history_offsets[b + 1], a.history_size);
-                const int64_t prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
-                for (int64_t i = h_lo + tid; i < h_hi; i += kThreads)
-                    count_token(a.history[i], i - h_lo < prompt ? kPrompt : 1u);
+            rep = row.rep;
+            freq = row.freq;
+            pres = row.pres;
+            penal = rep != 1.f || freq != 0.f || pres != 0.f;
+            inv = 1.f / rep;
+            first = row.first;
+            my_token = -1;
+            if (penal && a.draft_tokens && first + tid >= 0 && first + tid < a.rows) my_token = a.draft_tokens[first + tid];
+            int h_lo = 0, h_hi = 0;
+            if (penal) {
+                h_lo = clamp_offset(row.history_lo, a.history_size);
+                h_hi = clamp_offset(row.history_hi, a.history_size);
             }
-            // the request's biases: entries of the range are marked
+            const int bias_lo = clamp_offset(row.bias_lo, a.bias_size), bias_hi = clamp_offset(row.bias_hi, a.bias_size);
+            // the first tokens are on their way while the counts are cleared
+            constexpr int kBatch = 8;
+            int token[kBatch];
+            auto load = [&](int i0) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) token[u] = i0 + u * kThreads < h_hi ? a.history[i0 + u * kThreads] : -1;
+            };
+            load(h_lo + tid);
+            __syncthreads();
+            for (int i = tid; i < (kSmemWords - kRange) / 4; i += kThreads)
+                reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+            for (int i0 = h_lo + tid; i0 - tid < h_hi; i0 += kThreads * kBatch) {
+                int now[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) now[u] = token[u];
+                load(i0 + kThreads * kBatch);
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    count_token(now[u], i0 + u * kThreads - h_lo < row.prompt ? kPrompt : 1u);
+            }
+            // the request's biases: the first of a token's entries adds all of them up
+            bool mine = false;
             for (int i = bias_lo + tid; i < bias_hi; i += kThreads) {
-                const int64_t token = a.bias_tokens[i];
-                if (i > bias_lo && a.bias_tokens[i - 1] > token) bad |= kStatusBadIndex;
-                if (token < 0 || token >= a.vocab) bad |= kStatusBadIndex;
-                const int64_t at = token - v0;
-                if (at >= 0 && at < range) atomicOr(biased + (at >> 5), 1u << (at & 31));
+                const int t = a.bias_tokens[i];
+                float sum = a.bias_values[i];
+                if (i > bias_lo) {
+                    const int before = a.bias_tokens[i - 1];
+                    if (before > t) bad |= kStatusBadIndex;
+                    if (before == t) continue;
+                }
+                if (t < 0 || t >= a.vocab) bad |= kStatusBadIndex;
+                const int at = t - (int)v0;
+                if (at < 0 || at >= range) continue;
+                for (int k = i + 1; k < bias_hi && a.bias_tokens[k] == t; ++k) sum += a.bias_values[k];
+                bias[at] = sum;
+                atomicOr(biased + (at >> 5), 1u << (at & 31));
+                mine = true;
             }
+            any_bias = __syncthreads_or(mine);
         }
-        // the row's own path, `sign` 1 to add and -1 (mod 2^32) to take back
-        const int64_t first = b >= 0 && a.draft_tokens ? a.cu_new[b] : 0;
+        // the row's own path, `sign` 1 to add and -1 (mod 2^32) to take back: token
+        // tid from its register, those a longer path has from memory
+        const unsigned word = row.path;
         auto path = [&](unsigned sign) {
             if (!penal || !a.draft_tokens || b < 0) return;
             const int64_t last = a.tree_mask ? a.mask_words * 32 : r - first + 1;
             for (int64_t j = tid; j < last; j += kThreads) {
-                if (a.tree_mask && !((a.tree_mask[r * a.mask_words + (j >> 5)] >> (j & 31)) & 1)) continue;
+                const unsigned bits = !a.tree_mask ? ~0u : j == tid ? word : (unsigned)a.tree_mask[r * a.mask_words + (j >> 5)];
+                if (!((bits >> (j & 31)) & 1u)) continue;
                 if (first + j < 0 || first + j >= a.rows) {
                     bad |= kStatusBadIndex;
                     continue;
                 }
-                const int64_t token = a.draft_tokens[first + j];
+                const int token = j == tid ? my_token : a.draft_tokens[first + j];
                 if (token >= 0) count_token(token, sign);
             }
         };
         path(1u);
         __syncthreads();
 
-        const int32_t *mask = nullptr;
-        if (a.grammar_mask) {
-            const int64_t m = a.grammar_rows ? a.grammar_rows[r] : r;
-            if (m >= 0 && m < a.grammar_count) mask = a.grammar_mask + m * p.grammar_words;
-            else if (m != -1 || !a.grammar_rows) bad |= kStatusBadIndex;
-        }
-        const T *in = static_cast<const T *>(a.logits) + r * a.logits_row_stride + v0;
         T *out = static_cast<T *>(a.out) + r * a.out_row_stride + v0;
-
-        // the value of entry `at` of the range from its logit; `seen`: it has
-        // counts, `bias`: it is in the bias list
-        auto value = [&](T raw, int at, bool seen, bool bias, bool allowed) -> T {
+        // entry `at` of the range: its counts and its bias applied to its logit
+        auto value = [&](T raw, int at, bool seen, bool has_bias) -> T {
             float x = to_f<T>(raw);
             if (seen) {
-                const unsigned c = counts[at];
-                if (c) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-                if (c & ~kPrompt) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, (float)(c & ~kPrompt))), pres);
+                const unsigned c = counts[at], n = c & ~kPrompt;
+                if (c) x *= x > 0.f ? inv : rep;
+                if (n) x = fmaf(-freq, (float)n, x) - pres;
             }
-            if (bias) {
-                const int token = (int)(v0 + at);
-                int lo = bias_lo, hi = bias_hi;
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.bias_tokens[mid] < token) lo = mid + 1;
-                    else hi = mid;
-                }
-                float sum = 0.f;
-                for (; lo < bias_hi && a.bias_tokens[lo] == token; ++lo) sum += a.bias_values[lo];
-                x += sum;
-            }
-            return allowed ? from_f<T>(x) : from_f<T>(-INFINITY);
+            if (has_bias) x += bias[at];
+            return from_f<T>(x);
         };
         auto one = [&](int at) {
-            const int64_t v = v0 + at;
-            const bool allowed = !mask || ((mask[v >> 5] >> (v & 31)) & 1);
-            out[at] = value(in[at], at, bits_at(touched, at, 1), bits_at(biased, at, 1), allowed);
+            const bool allowed = !row.mask || ((row.mask[at >> 5] >> (at & 31)) & 1);
+            out[at] = allowed ? value(row.in[at], at, bits_at(touched, at, 1), bits_at(biased, at, 1)) : from_f<T>(-INFINITY);
         };
-        // elements before the first 16-byte boundary, whole pieces, the rest; all
-        // one by one where input and output do not share their alignment
-        const int mis_in = (int)((reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kVec);
-        const int mis_out = (int)((reinterpret_cast<uintptr_t>(out) / sizeof(T)) % kVec);
-        const int head = mis_in == mis_out ? min(range, (kVec - mis_in) % kVec) : range;
-        const int pieces = (range - head) / kVec;
-        for (int at = tid; at < head; at += kThreads) one(at);
-        for (int at = head + pieces * kVec + tid; at < range; at += kThreads) one(at);
-        constexpr int kAhead = 4;
-        for (int i0 = tid; i0 < pieces; i0 += kThreads * kAhead) {
-            uint4 raw[kAhead];
-            unsigned allowed[kAhead];
+        for (int at = tid; at < row.head; at += kThreads) one(at);
+        for (int at = row.head + row.pieces * kVec + tid; at < range; at += kThreads) one(at);
+        const int at0 = row.head + tid * kVec;
+        const unsigned *seen0 = touched + (at0 >> 5), *bias0 = biased + (at0 >> 5);
+        uint4 *to = reinterpret_cast<uint4 *>(out + at0);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + u * kThreads;
-                allowed[u] = (1u << kVec) - 1;
-                if (i >= pieces) continue;
-                raw[u] = *reinterpret_cast<const uint4 *>(in + head + i * kVec);
-                if (mask) {
-                    const int64_t v = v0 + head + i * kVec;
-                    const unsigned lo = (unsigned)mask[v >> 5];
-                    const unsigned hi = (v & 31) + kVec > 32 ? (unsigned)mask[(v >> 5) + 1] : 0u;
-                    allowed[u] &= __funnelshift_r(lo, hi, v & 31);
-                }
+        for (int u = 0; u < kHeld; ++u) {
+            if (tid + u * kThreads >= row.pieces) break;
+            const int at = at0 + u * kStep, w = u * (kStep / 32);
+            const unsigned t = __funnelshift_r(seen0[w], seen0[w + 1], at0 & 31) & kAll;
+            const unsigned bi = any_bias ? __funnelshift_r(bias0[w], bias0[w + 1], at0 & 31) & kAll : 0u;
+            const unsigned ok = (row.allowed >> (u * kVec)) & kAll;
+            T v[kVec];
+            *reinterpret_cast<uint4 *>(v) = row.raw[u];
+            if ((t | bi) & ok) {
+#pragma unroll
+                for (int e = 0; e < kVec; ++e)
+                    if (((t | bi) >> e) & 1u) v[e] = value(v[e], at + e, (t >> e) & 1u, (bi >> e) & 1u);
             }
+            if (ok != kAll) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int i = i0 + u * kThreads;
-                if (i >= pieces) continue;
-                const int at = head + i * kVec;
-                const unsigned t = bits_at(touched, at, kVec), bi = bits_at(biased, at, kVec);
-                T v[kVec];
-                *reinterpret_cast<uint4 *>(v) = raw[u];
-                if (t | bi) {
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        v[e] = value(v[e], at + e, (t >> e) & 1, (bi >> e) & 1, (allowed[u] >> e) & 1);
-                } else if (allowed[u] != (1u << kVec) - 1) {
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e)
-                        if (!((allowed[u] >> e) & 1)) v[e] = from_f<T>(-INFINITY);
-                }
-                *reinterpret_cast<uint4 *>(out + at) = *reinterpret_cast<uint4 *>(v);
+                for (int e = 0; e < kVec; ++e)
+                    if (!((ok >> e) & 1)) v[e] = from_f<T>(-INFINITY);
             }
+            __stcs(to + u * kThreads, *reinterpret_cast<uint4 *>(v));
         }
-        __syncthreads();
-        if (r + 1 < r_hi) path(0xFFFFFFFFu);
+        if (r + 1 < r_hi) {
+            fetch(r + 1, row);      // under way while the threads meet and the path is taken back
+            __syncthreads();
+            if (row.request == have) path(0xFFFFFFFFu);
+        }
     }
     if (bad) raise_status(p.status, bad);
 }
@@ -246,10 +315,12 @@ cudaError_t launch(const awq_logits_t &a, cudaStream_t stream)
     p.status = device_status_word();
     p.grammar_words = (a.vocab + 31) / 32;
     const int64_t ranges = (a.vocab + kRange - 1) / kRange;
-    // runs of rows: enough CTAs to fill the GPU several times over
-    const int64_t want = std::max<int64_t>(1, 152 * 16 / ranges);
-    p.rows_per_cta = (int)std::max<int64_t>(std::max<int64_t>(1, a.rows / want), (a.rows + 65534) / 65535);
-    const size_t smem = (kRange + 2 * kWords + 2) * sizeof(unsigned);
+    // runs of rows, so long that one wave of CTAs does all of them
+    const int64_t want = std::max<int64_t>(1, 152 * kPerSm<T> / ranges);
+    p.rows_per_cta = (int)std::max<int64_t>((a.rows + want - 1) / want, (a.rows + 65534) / 65535);
+    const size_t smem = kSmemWords * sizeof(unsigned);
+    cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ranges, (unsigned)((a.rows + p.rows_per_cta - 1) / p.rows_per_cta));
     cfg.blockDim = dim3(kThreads);
@@ -260,7 +331,7 @@ cudaError_t launch(const awq_logits_t &a, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, process_logits_kernel<T>, p);
+    e = cudaLaunchKernelEx(&cfg, process_logits_kernel<T>, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
