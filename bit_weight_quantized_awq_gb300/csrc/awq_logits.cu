@@ -4,15 +4,23 @@
 //   x -= pres (count > 0),  x += bias,  -inf where the grammar's bit is 0.
 //
 // Bound: every logit is read and written once (HBM); a row's history has a few
-// thousand tokens against a hundred thousand logits. A CTA owns a range of kRange
-// vocabulary entries (rounded up to fill the GPU) and a run of rows. It counts the tokens of the row's
-// history that fall into its range in shared memory (a counter and a touched bit
-// an entry), then takes the logits, fetched a row ahead, 16 bytes at a time; only
-// pieces with a touched or biased entry look further. Consecutive rows of one request -- the
-// nodes of a drafted tree -- share the counts: only the tokens of the row's own
-// path are added before and taken back after it. Counts are whole numbers, so the
-// atomics' order does not matter.
+// thousand tokens against a hundred thousand logits, but most of them are the
+// frequent tokens, which lie close together. A CTA owns a range of vocabulary
+// entries and a run of rows. Eight warps count the tokens of a request's history
+// that fall into the range in shared memory and list the entries met; then, row by
+// row, the listed entries are changed, an entry a thread, so that their number
+// alone counts and not how they crowd, and 16 bytes at a time are masked and
+// stored. A ninth warp brings the rows in, two ahead: logits by bulk copies, and
+// beside them whatever the others would have to wait for -- grammar words, path
+// words, the request's settings. (With the change made as the logits stream by,
+// nearly every warp walked through the few entries of its pieces: 92 us for 580
+// rows of 100,000 fp16 logits. With every warp fetching for itself a row ahead, a
+// third of the time went into waiting for one conditional load after the other:
+// 67 us.) Consecutive rows of one request -- the nodes of a drafted tree -- share
+// the counts: only the tokens in which the rows' paths differ are added or taken
+// back. Counts are whole numbers, so the atomics' order does not matter.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,10 +32,10 @@
 namespace awq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRange = 8192;              // vocabulary entries of a CTA
-constexpr int kBitmap = kRange / 32 + 4;  // words of a bitmap of the range: one to spare, and 16-byte pieces
-constexpr int kSmemWords = 2 * kRange + 2 * kBitmap;
+constexpr int kThreads = 256;             // of the eight working warps
+// vocabulary entries of a CTA: 16 KB of a row
+template <typename T>
+constexpr int kRange = 16384 / sizeof(T);
 constexpr unsigned kPrompt = 1u << 31;    // counter: in the prompt; below it the generated count
 
 struct LogitsParams {
@@ -54,255 +62,379 @@ __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// `count` (at most 8) bits from bit position `at` of a shared bitmap with a spare word at its end
-__device__ __forceinline__ unsigned bits_at(const unsigned *map, int at, int count)
+// -inf where a bit of `ok` is 0: two 16-bit values or one fp32 a word
+template <typename T>
+__device__ __forceinline__ uint4 masked(uint4 v, unsigned ok)
 {
-    const int w = at >> 5;
-    return __funnelshift_r(map[w], map[w + 1], at & 31) & ((1u << count) - 1);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (sizeof(T) == 4) {
+            if (!((ok >> i) & 1u)) w[i] = 0xFF800000u;
+        } else {
+            constexpr uint32_t inf = std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+            // bits 2 i and 2 i + 1 at bits 0 and 16, each spread over its half
+            const uint32_t keep = (((ok | ok << 15) >> (2 * i)) & 0x00010001u) * 0xFFFFu;
+            w[i] = (w[i] & keep) | (inf & ~keep);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// CTAs an SM has room for: a row of 16 or 32 KB is on its way to each
+constexpr int kStages = 3;
+constexpr int kPathWords = 8;             // words of a path that come with the row: a token a thread
+
+// What comes with a row beside its logits.
 template <typename T>
-constexpr int kPerSm = sizeof(T) == 4 ? 2 : 3;
+struct RowInfo {
+    int request;                          // -1: none
+    float rep, freq, pres;
+    int history_lo, history_hi, prompt, bias_lo, bias_hi, first;
+    int masked;                           // has a grammar mask
+    unsigned path[kPathWords];
+    unsigned bits[kRange<T> / 32 + 1];    // the grammar's bits of the range
+};
+
+// shared memory: the rows' logits, each behind one spare piece and with one after
+// it; the counts; bitmaps of the entries met and of those with a bias; the list of
+// the entries met; what comes with the rows
+template <typename T>
+constexpr size_t kSmem = kStages * (kRange<T> * sizeof(T) + 32) +
+                         (kRange<T> + 2 * (kRange<T> / 32)) * sizeof(unsigned) + kRange<T> * sizeof(uint16_t) +
+                         kStages * sizeof(RowInfo<T>);
+
+// CTAs an SM has room for: two rows of 16 KB are on their way to each
+template <typename T>
+constexpr int kPerSm = sizeof(T) == 4 ? 3 : 2;
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kPerSm<T>)
+__global__ void __launch_bounds__(kThreads + 32, kPerSm<T>)
 process_logits_kernel(const __grid_constant__ LogitsParams p)
 {
     constexpr int kVec = 16 / sizeof(T);
-    constexpr int kHeld = kRange / (kThreads * kVec);   // 16-byte pieces of a row that a thread holds
+    constexpr int kRange = awq::kRange<T>, kBitmap = kRange / 32, kStage = kRange + 2 * kVec;
+    constexpr int kHeld = kRange / (kThreads * kVec);   // 16-byte pieces of a row a thread
     constexpr unsigned kAll = (1u << kVec) - 1;
     constexpr int kStep = kThreads * kVec;              // entries between a thread's pieces: whole words of bits
-    static_assert(kHeld * kVec == 32 && kStep % 32 == 0, "the grammar's bits of a thread's pieces fill a word");
-    extern __shared__ unsigned smem[];
-    unsigned *counts = smem;                       // [kRange]
+    static_assert(kStep % 32 == 0 && kBitmap <= kThreads, "words of bits");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ int listed;
+    T *stage = reinterpret_cast<T *>(smem);        // [kStages][kStage]
+    unsigned *counts = reinterpret_cast<unsigned *>(stage + kStages * kStage);   // [kRange]
     unsigned *touched = counts + kRange;           // [kBitmap]
     unsigned *biased = touched + kBitmap;          // [kBitmap]
-    float *bias = reinterpret_cast<float *>(biased + kBitmap);   // [kRange], set where the bit is
+    uint16_t *list = reinterpret_cast<uint16_t *>(biased + kBitmap);   // [kRange]
+    RowInfo<T> *infos = reinterpret_cast<RowInfo<T> *>(list + kRange);  // [kStages]
     const awq_logits_t &a = p.a;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int64_t v0 = (int64_t)blockIdx.x * kRange;
     const int range = (int)min((int64_t)kRange, a.vocab - v0);
     const int64_t r_lo = (int64_t)blockIdx.y * p.rows_per_cta;
     const int64_t r_hi = min(r_lo + p.rows_per_cta, a.rows);
     unsigned bad = 0;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 2);                // the copy's issue, and the rest
+            ptx::mbar_init(ptx::smem_addr(empty + i), kThreads / 32);
+        }
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
     ptx::launch_dependents();
     ptx::wait_prerequisites();
 
+    // Where a row's logits of the range lie: elements before the first 16-byte
+    // boundary, then whole pieces. All one by one (no pieces) where input and output
+    // do not share their alignment.
+    auto split = [&](int64_t r, const T *&in, T *&out, int &head, int &pieces) {
+        in = static_cast<const T *>(a.logits) + r * a.logits_row_stride + v0;
+        out = static_cast<T *>(a.out) + r * a.out_row_stride + v0;
+        const unsigned mis_in = (unsigned)(reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kVec;
+        const unsigned mis_out = (unsigned)(reinterpret_cast<uintptr_t>(out) / sizeof(T)) % kVec;
+        head = mis_in == mis_out ? min(range, (int)((kVec - mis_in) % kVec)) : range;
+        pieces = (range - head) / kVec;
+    };
+    // Entry 0 of a row in its stage: the first piece is on a boundary, one piece in.
+    auto entry0 = [&](int s, int head, int pieces) { return stage + s * kStage + kVec - (pieces > 0 ? head : 0); };
+    // element number i of those outside the pieces
+    auto outside = [&](int i, int head, int pieces) { return i < head ? i : i + pieces * kVec; };
+
+    if (tid >= kThreads) {
+        // ------------------------------------------------------------ the rows' way in
+        // What a row needs of its request is one word a lane, so that it takes one
+        // wait; and the two indices it starts from are asked for a row earlier.
+        const int32_t *words = nullptr;
+        switch (lane) {
+        case 0: words = reinterpret_cast<const int32_t *>(a.repetition); break;
+        case 1: words = reinterpret_cast<const int32_t *>(a.frequency); break;
+        case 2: words = reinterpret_cast<const int32_t *>(a.presence); break;
+        case 3: words = a.history ? a.history_offsets : nullptr; break;
+        case 4: words = a.history ? a.history_offsets + 1 : nullptr; break;
+        case 5: words = a.history ? a.prompt_lens : nullptr; break;
+        case 6: words = a.bias_tokens ? a.bias_offsets : nullptr; break;
+        case 7: words = a.bias_tokens ? a.bias_offsets + 1 : nullptr; break;
+        case 8: words = a.draft_tokens ? a.cu_new : nullptr; break;
+        }
+        const int none = lane == 0 ? __float_as_int(1.f) : 0;
+        int64_t request = a.row_request ? a.row_request[r_lo] : r_lo;
+        int64_t mask_row = a.grammar_rows ? a.grammar_rows[r_lo] : r_lo;
+        bool ok = true;
+        int64_t r = r_lo;
+        for (; r < r_hi; ++r) {
+            const int n = (int)(r - r_lo), s = n % kStages;
+            ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + s), ((n / kStages) & 1) ^ 1, nullptr, p.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const T *in;
+            T *out;
+            int head, pieces;
+            split(r, in, out, head, pieces);
+            T *at0 = entry0(s, head, pieces);
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), (uint32_t)pieces * 16);
+                if (pieces > 0)
+                    ptx::bulk_load(ptx::smem_addr(at0 + head), in + head, (uint32_t)pieces * 16, ptx::smem_addr(full + s));
+            }
+            __syncwarp();
+            int64_t b = request, m = a.grammar_mask ? mask_row : -1;
+            if (r + 1 < r_hi) {
+                request = a.row_request ? a.row_request[r + 1] : r + 1;
+                mask_row = a.grammar_rows ? a.grammar_rows[r + 1] : r + 1;
+            }
+            if (b < 0 || b >= a.B) {
+                if (a.B > 0 || a.row_request) bad |= kStatusBadIndex;
+                b = -1;
+            }
+            if (m < 0 || m >= a.grammar_count) {
+                if (a.grammar_mask && (m != -1 || !a.grammar_rows)) bad |= kStatusBadIndex;
+                m = -1;
+            }
+            RowInfo<T> &info = infos[s];
+            int word = none;
+            unsigned path = 0, bits[kBitmap / 32 + 1];
+            T edge{};
+            const int edges = range - pieces * kVec;
+            if (words && b >= 0) word = words[b];
+            if (a.tree_mask && lane < min((int64_t)kPathWords, a.mask_words)) path = (unsigned)a.tree_mask[r * a.mask_words + lane];
+            if (lane < edges) edge = in[outside(lane, head, pieces)];
+            const int32_t *grammar = a.grammar_mask + m * p.grammar_words + (v0 >> 5);
+            const int have_words = m < 0 ? 0 : (range + 31) / 32;
+#pragma unroll
+            for (int i = 0; i < kBitmap / 32 + 1; ++i)
+                if (lane + 32 * i < have_words) bits[i] = (unsigned)grammar[lane + 32 * i];
+            // ---- all of it asked for; now put away
+            if (lane < 9) (&info.request)[1 + lane] = word;
+            if (lane == 9) info.request = (int)b;
+            if (lane == 10) info.masked = m >= 0;
+            if (lane < kPathWords) info.path[lane] = path;
+#pragma unroll
+            for (int i = 0; i < kBitmap / 32 + 1; ++i)
+                if (lane + 32 * i < have_words) info.bits[lane + 32 * i] = bits[i];
+            if (lane < edges) at0[outside(lane, head, pieces)] = edge;
+            for (int i = lane + 32; i < edges; i += 32) at0[outside(i, head, pieces)] = in[outside(i, head, pieces)];
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(full + s));
+        }
+        if (!ok) {
+            // the copies on their way land before the shared memory goes
+            for (int64_t i = max(r_lo, r - kStages); i < r; ++i)
+                ptx::mbar_wait_bounded(ptx::smem_addr(full + (i - r_lo) % kStages), ((i - r_lo) / kStages) & 1, nullptr, nullptr);
+        }
+        if (bad) raise_status(p.status, bad);
+        return;
+    }
+
+    // ---------------------------------------------------------------- counts, changes, output
+    // counts a token of the range; whether it is the first to meet its entry
     auto count_token = [&](int token, unsigned add) {
         const int at = token - (int)v0;
         if (at < 0 || at >= range) {
             if (token >= (int)a.vocab) bad |= kStatusBadIndex;
-            return;
+            return false;
         }
         if (add == kPrompt) atomicOr(counts + at, kPrompt);
         else atomicAdd(counts + at, add);
-        atomicOr(touched + (at >> 5), 1u << (at & 31));
+        const unsigned bit = 1u << (at & 31);
+        return !(atomicOr(touched + (at >> 5), bit) & bit);
     };
     auto clamp_offset = [&](int at, int64_t size) {
         if (at < 0 || at > size) bad |= kStatusBadIndex;
         return (int)min(max((int64_t)at, (int64_t)0), size);
     };
-
-    // A row as it is fetched, a row ahead of its turn: the thread's pieces of its
-    // logits, the grammar's bits of all of them in one word, its word of the path,
-    // and what is known of its request.
-    struct Row {
-        const T *in;
-        const int32_t *mask;       // the grammar's words from the range's first entry on
-        int head, pieces;          // elements before the first 16-byte boundary, whole pieces behind it
-        int request, history_lo, history_hi, prompt, bias_lo, bias_hi, first;
-        float rep, freq, pres;
-        unsigned path, allowed;
-        uint4 raw[kHeld];
-    };
-    auto fetch = [&](int64_t r, Row &row) {
-        int64_t b = a.row_request ? a.row_request[r] : r;
-        if (b < 0 || b >= a.B) {
-            if (a.B > 0 || a.row_request) bad |= kStatusBadIndex;
-            b = -1;
-        }
-        row.path = a.tree_mask && tid < a.mask_words * 32 ? (unsigned)a.tree_mask[r * a.mask_words + (tid >> 5)] : 0u;
-        row.mask = nullptr;
-        if (a.grammar_mask) {
-            const int64_t m = a.grammar_rows ? a.grammar_rows[r] : r;
-            if (m >= 0 && m < a.grammar_count) row.mask = a.grammar_mask + m * p.grammar_words + (v0 >> 5);
-            else if (m != -1 || !a.grammar_rows) bad |= kStatusBadIndex;
-        }
-        row.in = static_cast<const T *>(a.logits) + r * a.logits_row_stride + v0;
-        const T *out = static_cast<const T *>(a.out) + r * a.out_row_stride + v0;
-        // all one by one where input and output do not share their alignment
-        const unsigned mis_in = (unsigned)(reinterpret_cast<uintptr_t>(row.in) / sizeof(T)) % kVec;
-        const unsigned mis_out = (unsigned)(reinterpret_cast<uintptr_t>(out) / sizeof(T)) % kVec;
-        row.head = mis_in == mis_out ? min(range, (int)((kVec - mis_in) % kVec)) : range;
-        row.pieces = (range - row.head) / kVec;
-        row.allowed = ~0u;
-        const int at = row.head + tid * kVec;      // the thread's first piece; the others kStep further on each
-        const uint4 *piece = reinterpret_cast<const uint4 *>(row.in + at);
-#pragma unroll
-        for (int u = 0; u < kHeld; ++u)
-            if (tid + u * kThreads < row.pieces) row.raw[u] = __ldcs(piece + u * kThreads);
-        if (row.mask) {
-            row.allowed = 0;
-            const int32_t *w = row.mask + (at >> 5);
-            const bool crosses = (at & 31) + kVec > 32;
-#pragma unroll
-            for (int u = 0; u < kHeld; ++u)
-                if (tid + u * kThreads < row.pieces) {
-                    const unsigned lo = (unsigned)w[u * (kStep / 32)], hi = crosses ? (unsigned)w[u * (kStep / 32) + 1] : 0u;
-                    row.allowed |= (__funnelshift_r(lo, hi, at & 31) & kAll) << (u * kVec);
-                }
-        }
-        row.request = (int)b;
-        row.rep = b >= 0 && a.repetition ? a.repetition[b] : 1.f;
-        row.freq = b >= 0 && a.frequency ? a.frequency[b] : 0.f;
-        row.pres = b >= 0 && a.presence ? a.presence[b] : 0.f;
-        row.history_lo = row.history_hi = row.prompt = row.bias_lo = row.bias_hi = row.first = 0;
-        if (b >= 0 && a.history) {
-            row.history_lo = a.history_offsets[b];
-            row.history_hi = a.history_offsets[b + 1];
-            if (a.prompt_lens) row.prompt = a.prompt_lens[b];
-        }
-        if (b >= 0 && a.bias_tokens) {
-            row.bias_lo = a.bias_offsets[b];
-            row.bias_hi = a.bias_offsets[b + 1];
-        }
-        if (b >= 0 && a.draft_tokens) row.first = a.cu_new[b];
+    // The entry in the range that pair i of the request's list begins, given its token
+    // and the one before it, and the sum of all its pairs; -1 if it begins none.
+    auto bias_entry = [&](int i, int token, int before, int end, float &sum) {
+        const int at = token - (int)v0;
+        if (at < 0 || at >= range || before == token) return -1;
+        for (int k = i + 1; k < end && a.bias_tokens[k] == token; ++k) sum += a.bias_values[k];
+        return at;
     };
 
-    Row row;
-    fetch(r_lo, row);
-    int have = -2;                                 // request whose counts are held (-1: a row without one)
+    int have = -2;                                 // request whose counts are held
     float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
-    bool penal = false, any_bias = false;          // else counts change nothing; no bias in the range
+    bool penal = false;                            // else counts change nothing
+    int my_bias = -1, more_lo = 0, more_hi = 0;    // the entry of this thread's bias; pairs past the threads'
+    float my_sum = 0.f;
     int64_t first = 0;                             // the request's first drafted token
     int my_token = -1;                             // its token number tid
+    int64_t held = -1;                             // the row whose path is counted, if any
+    unsigned held_word = 0;                        // and this thread's word of it
     for (int64_t r = r_lo; r < r_hi; ++r) {
-        const int b = row.request;
+        const int n = (int)(r - r_lo), s = n % kStages;
+        const RowInfo<T> &info = infos[s];
+        const bool landed = ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (n / kStages) & 1, nullptr, p.status);
+        if (!ptx::named_barrier_and(1, kThreads, landed)) break;
+        const int b = info.request;
         if (b != have) {
             have = b;
-            rep = row.rep;
-            freq = row.freq;
-            pres = row.pres;
+            rep = info.rep;
+            freq = info.freq;
+            pres = info.pres;
             penal = rep != 1.f || freq != 0.f || pres != 0.f;
             inv = 1.f / rep;
-            first = row.first;
-            my_token = -1;
-            if (penal && a.draft_tokens && first + tid >= 0 && first + tid < a.rows) my_token = a.draft_tokens[first + tid];
-            int h_lo = 0, h_hi = 0;
-            if (penal) {
-                h_lo = clamp_offset(row.history_lo, a.history_size);
-                h_hi = clamp_offset(row.history_hi, a.history_size);
-            }
-            const int bias_lo = clamp_offset(row.bias_lo, a.bias_size), bias_hi = clamp_offset(row.bias_hi, a.bias_size);
-            // the first tokens are on their way while the counts are cleared
-            constexpr int kBatch = 8;
+            first = info.first;
+            const int h_lo = penal ? clamp_offset(info.history_lo, a.history_size) : 0;
+            const int h_hi = penal ? clamp_offset(info.history_hi, a.history_size) : 0;
+            const int bias_lo = clamp_offset(info.bias_lo, a.bias_size);
+            const int bias_hi = clamp_offset(info.bias_hi, a.bias_size);
+            // the first tokens, the thread's pair of the biases and its drafted token
+            // are on their way while the counts are cleared
+            constexpr int kBatch = 16;
             int token[kBatch];
             auto load = [&](int i0) {
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u) token[u] = i0 + u * kThreads < h_hi ? a.history[i0 + u * kThreads] : -1;
             };
             load(h_lo + tid);
-            __syncthreads();
-            for (int i = tid; i < (kSmemWords - kRange) / 4; i += kThreads)
-                reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
-            __syncthreads();
-            for (int i0 = h_lo + tid; i0 - tid < h_hi; i0 += kThreads * kBatch) {
-                int now[kBatch];
-#pragma unroll
-                for (int u = 0; u < kBatch; ++u) now[u] = token[u];
-                load(i0 + kThreads * kBatch);
+            int bias_token = -1, bias_before = -1;
+            if (bias_lo + tid < bias_hi) {
+                bias_token = a.bias_tokens[bias_lo + tid];
+                my_sum = a.bias_values[bias_lo + tid];
+                if (tid > 0) bias_before = a.bias_tokens[bias_lo + tid - 1];
+            }
+            my_token = -1;
+            if (penal && a.draft_tokens && first + tid >= 0 && first + tid < a.rows) my_token = a.draft_tokens[first + tid];
+            held = -1;
+            held_word = 0;
+            for (int i = tid; i < (kRange + 2 * kBitmap) / 4; i += kThreads)
+                reinterpret_cast<uint4 *>(counts)[i] = make_uint4(0, 0, 0, 0);
+            if (tid == 0) listed = 0;
+            ptx::named_barrier(1, kThreads);
+            for (int i0 = h_lo; i0 < h_hi; i0 += kThreads * kBatch) {
+                if (i0 > h_lo) load(i0 + tid);
 #pragma unroll
                 for (int u = 0; u < kBatch; ++u)
-                    count_token(now[u], i0 + u * kThreads - h_lo < row.prompt ? kPrompt : 1u);
+                    count_token(token[u], i0 + tid + u * kThreads - h_lo < info.prompt ? kPrompt : 1u);
             }
-            // the request's biases: the first of a token's entries adds all of them up
-            bool mine = false;
-            for (int i = bias_lo + tid; i < bias_hi; i += kThreads) {
-                const int t = a.bias_tokens[i];
-                float sum = a.bias_values[i];
-                if (i > bias_lo) {
-                    const int before = a.bias_tokens[i - 1];
-                    if (before > t) bad |= kStatusBadIndex;
-                    if (before == t) continue;
-                }
-                if (t < 0 || t >= a.vocab) bad |= kStatusBadIndex;
-                const int at = t - (int)v0;
-                if (at < 0 || at >= range) continue;
-                for (int k = i + 1; k < bias_hi && a.bias_tokens[k] == t; ++k) sum += a.bias_values[k];
-                bias[at] = sum;
-                atomicOr(biased + (at >> 5), 1u << (at & 31));
-                mine = true;
+            // the request's biases: the thread's own pair, and those past the threads'
+            auto check = [&](int t, int before) {
+                if (t < 0 || before > t || t >= a.vocab) bad |= kStatusBadIndex;
+            };
+            my_bias = -1;
+            if (bias_lo + tid < bias_hi) {
+                check(bias_token, bias_before);
+                my_bias = bias_entry(bias_lo + tid, bias_token, bias_before, bias_hi, my_sum);
             }
-            any_bias = __syncthreads_or(mine);
+            more_lo = bias_lo + kThreads;
+            more_hi = bias_hi;
+            if (my_bias >= 0) atomicOr(biased + (my_bias >> 5), 1u << (my_bias & 31));
+            for (int i = more_lo + tid; i < more_hi; i += kThreads) {
+                const int t = a.bias_tokens[i], at = t - (int)v0;
+                check(t, a.bias_tokens[i - 1]);
+                if (at >= 0 && at < range) atomicOr(biased + (at >> 5), 1u << (at & 31));
+            }
+            ptx::named_barrier(1, kThreads);
+            // the entries met, listed: a word of the bitmap a thread
+            unsigned left = tid < kBitmap ? touched[tid] : 0u;
+            int place = __popc(left);
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, place, d);
+                if (lane >= d) place += o;
+            }
+            int base = 0;
+            if (lane == 31 && place > 0) base = atomicAdd(&listed, place);
+            place += __shfl_sync(0xFFFFFFFFu, base, 31) - __popc(left);
+            for (; left; left &= left - 1) list[place++] = (uint16_t)(tid * 32 + __ffs(left) - 1);
+            ptx::named_barrier(1, kThreads);
         }
-        // the row's own path, `sign` 1 to add and -1 (mod 2^32) to take back: token
-        // tid from its register, those a longer path has from memory
-        const unsigned word = row.path;
-        auto path = [&](unsigned sign) {
-            if (!penal || !a.draft_tokens || b < 0) return;
+        // The row's path in place of the one that is counted: where the two differ.
+        // Token tid and its bits are at hand, those a longer path has in memory.
+        const unsigned my_word = info.path[tid >> 5];
+        if (penal && a.draft_tokens && b >= 0) {
             const int64_t last = a.tree_mask ? a.mask_words * 32 : r - first + 1;
             for (int64_t j = tid; j < last; j += kThreads) {
-                const unsigned bits = !a.tree_mask ? ~0u : j == tid ? word : (unsigned)a.tree_mask[r * a.mask_words + (j >> 5)];
-                if (!((bits >> (j & 31)) & 1u)) continue;
+                bool now, was;
+                if (a.tree_mask) {
+                    const unsigned w = j == tid ? my_word : (unsigned)a.tree_mask[r * a.mask_words + (j >> 5)];
+                    const unsigned h = held < 0 ? 0u : j == tid ? held_word : (unsigned)a.tree_mask[held * a.mask_words + (j >> 5)];
+                    now = (w >> (j & 31)) & 1u;
+                    was = (h >> (j & 31)) & 1u;
+                } else {
+                    now = true;
+                    was = held >= 0 && j <= held - first;
+                }
+                if (now == was) continue;
                 if (first + j < 0 || first + j >= a.rows) {
                     bad |= kStatusBadIndex;
                     continue;
                 }
                 const int token = j == tid ? my_token : a.draft_tokens[first + j];
-                if (token >= 0) count_token(token, sign);
+                if (token >= 0 && count_token(token, now ? 1u : 0xFFFFFFFFu))
+                    list[atomicAdd(&listed, 1)] = (uint16_t)(token - (int)v0);
             }
-        };
-        path(1u);
-        __syncthreads();
+            held = r;
+            held_word = my_word;
+        }
+        const T *in;
+        T *out;
+        int head, pieces;
+        split(r, in, out, head, pieces);
+        T *at0 = entry0(s, head, pieces);
+        ptx::named_barrier(1, kThreads);
 
-        T *out = static_cast<T *>(a.out) + r * a.out_row_stride + v0;
-        // entry `at` of the range: its counts and its bias applied to its logit
-        auto value = [&](T raw, int at, bool seen, bool has_bias) -> T {
-            float x = to_f<T>(raw);
-            if (seen) {
-                const unsigned c = counts[at], n = c & ~kPrompt;
-                if (c) x *= x > 0.f ? inv : rep;
-                if (n) x = fmaf(-freq, (float)n, x) - pres;
-            }
-            if (has_bias) x += bias[at];
-            return from_f<T>(x);
+        // ---- the entries that change
+        auto change = [&](int at, float sum) {
+            float x = to_f<T>(at0[at]);
+            const unsigned c = counts[at], times = c & ~kPrompt;
+            if (c) x *= x > 0.f ? inv : rep;
+            if (times) x = fmaf(-freq, (float)times, x) - pres;
+            at0[at] = from_f<T>(x + sum);
         };
-        auto one = [&](int at) {
-            const bool allowed = !row.mask || ((row.mask[at >> 5] >> (at & 31)) & 1);
-            out[at] = allowed ? value(row.in[at], at, bits_at(touched, at, 1), bits_at(biased, at, 1)) : from_f<T>(-INFINITY);
-        };
-        for (int at = tid; at < row.head; at += kThreads) one(at);
-        for (int at = row.head + row.pieces * kVec + tid; at < range; at += kThreads) one(at);
-        const int at0 = row.head + tid * kVec;
-        const unsigned *seen0 = touched + (at0 >> 5), *bias0 = biased + (at0 >> 5);
-        uint4 *to = reinterpret_cast<uint4 *>(out + at0);
-#pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
-            if (tid + u * kThreads >= row.pieces) break;
-            const int at = at0 + u * kStep, w = u * (kStep / 32);
-            const unsigned t = __funnelshift_r(seen0[w], seen0[w + 1], at0 & 31) & kAll;
-            const unsigned bi = any_bias ? __funnelshift_r(bias0[w], bias0[w + 1], at0 & 31) & kAll : 0u;
-            const unsigned ok = (row.allowed >> (u * kVec)) & kAll;
-            T v[kVec];
-            *reinterpret_cast<uint4 *>(v) = row.raw[u];
-            if ((t | bi) & ok) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e)
-                    if (((t | bi) >> e) & 1u) v[e] = value(v[e], at + e, (t >> e) & 1u, (bi >> e) & 1u);
-            }
-            if (ok != kAll) {
-#pragma unroll
-                for (int e = 0; e < kVec; ++e)
-                    if (!((ok >> e) & 1)) v[e] = from_f<T>(-INFINITY);
-            }
-            __stcs(to + u * kThreads, *reinterpret_cast<uint4 *>(v));
+        const int entries = listed;
+        for (int i = tid; i < entries; i += kThreads) {
+            const int at = list[i];
+            if (!((biased[at >> 5] >> (at & 31)) & 1u)) change(at, 0.f);
         }
-        if (r + 1 < r_hi) {
-            fetch(r + 1, row);      // under way while the threads meet and the path is taken back
-            __syncthreads();
-            if (row.request == have) path(0xFFFFFFFFu);
+        if (my_bias >= 0) change(my_bias, my_sum);
+        for (int i = more_lo + tid; i < more_hi; i += kThreads) {
+            float sum = a.bias_values[i];
+            const int at = bias_entry(i, a.bias_tokens[i], a.bias_tokens[i - 1], more_hi, sum);
+            if (at >= 0) change(at, sum);
         }
+        ptx::named_barrier(1, kThreads);
+
+        // ---- masked and stored
+        const bool masks = info.masked != 0;
+        const int at1 = head + tid * kVec, shift = at1 & 31;      // the thread's first piece
+        const unsigned *bits = info.bits + (at1 >> 5);
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+            if (tid + u * kThreads < pieces) {
+                uint4 v = reinterpret_cast<const uint4 *>(at0 + head)[tid + u * kThreads];
+                if (masks)
+                    v = masked<T>(v, __funnelshift_r(bits[u * (kStep / 32)], bits[u * (kStep / 32) + 1], shift) & kAll);
+                __stcs(reinterpret_cast<uint4 *>(out + head) + tid + u * kThreads, v);
+            }
+        for (int i = tid; i < range - pieces * kVec; i += kThreads) {
+            const int at = outside(i, head, pieces);
+            out[at] = !masks || ((info.bits[at >> 5] >> (at & 31)) & 1) ? at0[at] : from_f<T>(-INFINITY);
+        }
+        // the stage's next copy comes after these accesses
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(empty + s));
     }
     if (bad) raise_status(p.status, bad);
 }
@@ -314,16 +446,16 @@ cudaError_t launch(const awq_logits_t &a, cudaStream_t stream)
     p.a = a;
     p.status = device_status_word();
     p.grammar_words = (a.vocab + 31) / 32;
-    const int64_t ranges = (a.vocab + kRange - 1) / kRange;
+    const int64_t ranges = (a.vocab + kRange<T> - 1) / kRange<T>;
     // runs of rows, so long that one wave of CTAs does all of them
     const int64_t want = std::max<int64_t>(1, 152 * kPerSm<T> / ranges);
     p.rows_per_cta = (int)std::max<int64_t>((a.rows + want - 1) / want, (a.rows + 65534) / 65535);
-    const size_t smem = kSmemWords * sizeof(unsigned);
+    constexpr size_t smem = kSmem<T>;
     cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ranges, (unsigned)((a.rows + p.rows_per_cta - 1) / p.rows_per_cta));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads + 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
