@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -114,9 +115,35 @@ class Logits(ctypes.Structure):
                 ("dtype", _I32)]
 
 
+def _packer(structure):
+    """Packs a structure's fields, in order (a nested structure's one after another),
+    into bytes that are passed for a pointer to it: a third of the time that
+    filling the structure takes."""
+    codes = {_P: "P", _I64: "q", _I32: "i", ctypes.c_float: "f"}
+
+    def code(s):
+        return "".join(codes[t] if t in codes else code(t) for _, t in s._fields_)
+
+    layout = struct.Struct("@" + code(structure) + "0P")     # padded to a pointer's alignment, as C does
+    assert layout.size == ctypes.sizeof(structure)
+    return layout.pack
+
+
+pack_cache = _packer(Cache)
+pack_tree_attention = _packer(TreeAttention)
+pack_logits = _packer(Logits)
+
+
+def _arg(value):
+    """A structure or its packed bytes, as a pointer argument."""
+    return value if value is None or isinstance(value, bytes) else ctypes.byref(value)
+
+
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Loads the CUDA library once. Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -172,14 +199,13 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.awq_paged_plan.argtypes = [_P, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P,
                                        _I64, _P, _P]
         lib.awq_paged_plan.restype = _INT
-        lib.awq_kv_append.argtypes = [_P, _I64, _I64, _P, _I64, _I64, ctypes.POINTER(Cache), ctypes.POINTER(Cache), _P,
-                                      _I64, _I64, _I64, _I64, _I64, _P]
+        lib.awq_kv_append.argtypes = [_P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _P]
         lib.awq_kv_append.restype = _INT
-        lib.awq_tree_attention.argtypes = [ctypes.POINTER(TreeAttention), _P]
+        lib.awq_tree_attention.argtypes = [_P, _P]
         lib.awq_tree_attention.restype = _INT
         lib.awq_reserve_tree_attention.argtypes = [_I64, _I64, _I64, _I64, _I64, _P]
         lib.awq_reserve_tree_attention.restype = _INT
-        lib.awq_process_logits.argtypes = [ctypes.POINTER(Logits), _P]
+        lib.awq_process_logits.argtypes = [_P, _P]
         lib.awq_process_logits.restype = _INT
         lib.awq_shutdown.argtypes = []
         lib.awq_shutdown.restype = None
@@ -286,12 +312,13 @@ def awq_paged_plan(context_lens, new_lens, B, block_table, table_width, table_st
 
 def awq_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, k_cache: Cache, v_cache: Cache,
                   slot_map, tokens, num_blocks, block_size, kv_heads, head_dim, stream) -> int:
-    return load_library().awq_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride, k_cache,
-                                        v_cache, slot_map, tokens, num_blocks, block_size, kv_heads, head_dim, stream)
+    return load_library().awq_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride, v_head_stride,
+                                        _arg(k_cache), _arg(v_cache), slot_map, tokens, num_blocks, block_size,
+                                        kv_heads, head_dim, stream)
 
 
 def awq_tree_attention(args: TreeAttention, stream) -> int:
-    return load_library().awq_tree_attention(args, stream)
+    return load_library().awq_tree_attention(_arg(args), stream)
 
 
 def awq_reserve_tree_attention(max_tokens, max_requests, q_heads, kv_heads, head_dim, stream) -> int:
@@ -299,7 +326,7 @@ def awq_reserve_tree_attention(max_tokens, max_requests, q_heads, kv_heads, head
 
 
 def awq_process_logits(args: Logits, stream) -> int:
-    return load_library().awq_process_logits(args, stream)
+    return load_library().awq_process_logits(_arg(args), stream)
 
 
 def awq_shutdown() -> None:

@@ -34,6 +34,9 @@ namespace {
 constexpr int kRows = 16;        // rows of q a CTA works on (one mma.sync M)
 constexpr int kKeys = 64;        // keys a tile
 constexpr int kBlockCost = 1;    // a row block's beginning and end, in tiles
+// Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
+// in the time that a second kernel would take to join the pieces.
+constexpr int kWholeTiles = 16;
 constexpr int kConsumers = 128;  // threads of the four consumer warps
 constexpr int kThreads = kConsumers + 32;
 
@@ -473,8 +476,10 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     // a launch no larger than the work the bounds allow
     const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
-    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * (kBlockCost + tiles);
-    p.min_units = kBlockCost + 4;
+    const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
+    p.whole = tiles <= kWholeTiles;
+    p.min_units = p.whole ? 1 : kBlockCost + 4;
+    const int64_t units = p.whole ? blocks : blocks * (kBlockCost + tiles);
     const int ctas = (int)std::min<int64_t>(li.ctas, std::max<int64_t>(1, units / p.min_units));
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();

@@ -59,6 +59,7 @@ struct Params {
     int B, tokens, q_heads, kv_heads, group, head_dim, num_blocks;
     int shift;              // log2 of the block size
     int min_units;          // a CTA takes at least this many units: one tile at least
+    int whole;              // row blocks are not split: one unit each, and nothing to join
     float scale_log2;       // scale * log2(e): scores are kept in powers of two
 #ifdef AWQ_FAULT_TEST
     int fault;              // CTA 0's producer issues nothing (fault-test build only)
@@ -101,7 +102,7 @@ struct Work {
     }
     static __device__ int64_t block_units(const Params &p, int ctx, int n, int rb)
     {
-        return kBlockCost + (int64_t)tiles_of(p, ctx, n, rb) * weight_of(p, n, rb);
+        return p.whole ? 1 : kBlockCost + (int64_t)tiles_of(p, ctx, n, rb) * weight_of(p, n, rb);
     }
     static __device__ int64_t head_units(const Params &p, int ctx, int n)
     {
@@ -117,9 +118,10 @@ struct Work {
     __device__ int cta_of(int64_t u) const { return (int)(((u + 1) * ctas - 1) / units); }
     // A block's first tile begins at its first unit u0, tile i at u0 + kBlockCost + i
     // weight: the first one that begins at `at` or later.
-    static __device__ int first_tile(int64_t at, int64_t u0, int weight, int tiles)
+    static __device__ int first_tile(const Params &p, int64_t at, int64_t u0, int weight, int tiles)
     {
         if (at <= u0) return 0;
+        if (p.whole) return tiles;
         const int64_t i = (at - u0 - kBlockCost + weight - 1) / weight;
         return (int)min((int64_t)tiles, max((int64_t)1, i));
     }
@@ -200,7 +202,7 @@ struct Work {
             }
         }
         tiles = tiles_of(p, ctx, n, rb);
-        tile = first_tile(pos, pos - rem, weight_of(p, n, rb), tiles);
+        tile = first_tile(p, pos, pos - rem, weight_of(p, n, rb), tiles);
         pos -= rem;
         return true;
     }
@@ -243,7 +245,7 @@ struct Work {
         s.n = n;
         s.token0 = token0;
         s.tile0 = tile;
-        s.tile1 = first_tile(end, pos, weight_of(p, n, rb), tiles);
+        s.tile1 = first_tile(p, end, pos, weight_of(p, n, rb), tiles);
         s.tiles = tiles;
         s.u0 = pos;
         if (s.tile1 <= s.tile0) return false;            // no tile begins in what is left
@@ -471,7 +473,8 @@ attention_join_kernel(const __grid_constant__ Params p)
     if (col == 0) store_lse(p, j.token0, j.h, row, m == -INFINITY ? 0.f : m, l);
 }
 
-// Launches a main kernel of `ctas` CTAs and, unless there is one only, its join.
+// Launches a main kernel of `ctas` CTAs and, unless there is one only or each has
+// whole row blocks, its join.
 template <typename T, int RB, int DP, typename K>
 cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t stream, const CUtensorMap &tk,
                         const CUtensorMap &tv, Params &p)
@@ -492,7 +495,7 @@ cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t 
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
     if (e != cudaSuccess) return e;
-    if (ctas > 1) {
+    if (ctas > 1 && !p.whole) {
         constexpr int kColumns = kJoinColumns * join_groups(RB);
         cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.head_dim + kColumns - 1) / kColumns);
         cfg.blockDim = dim3(kJoinThreads);

@@ -49,6 +49,9 @@ namespace {
 constexpr int kRows = 256;       // rows of a block
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kBlockCost = 2;    // a row block's beginning and end: as a tile of the heavier kind
+// Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
+// in the time that a second kernel would take to join the pieces.
+constexpr int kWholeTiles = 8;
 constexpr int kThreads = 384;
 constexpr int kSoftmax = 256;    // threads of the softmax warps
 constexpr float kSlack = 8.f;
@@ -663,8 +666,10 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
         return cudaErrorInvalidValue;
     const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
-    const int64_t units = a.B * a.kv_heads * ((rows + kRows - 1) / kRows) * (kBlockCost + 2 * tiles);
-    p.min_units = kBlockCost + 4;
+    const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
+    p.whole = tiles <= kWholeTiles;
+    p.min_units = p.whole ? 1 : kBlockCost + 4;
+    const int64_t units = p.whole ? blocks : blocks * (kBlockCost + 2 * tiles);
     const int ctas = (int)std::min<int64_t>(li.sms, std::max<int64_t>(1, units / p.min_units));
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();

@@ -345,18 +345,22 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
                 if (at >= 0 && at < range) atomicOr(biased + (at >> 5), 1u << (at & 31));
             }
             ptx::named_barrier(1, kThreads);
-            // the entries met, listed: a word of the bitmap a thread
-            unsigned left = tid < kBitmap ? touched[tid] : 0u;
-            int place = __popc(left);
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xFFFFFFFFu, place, d);
-                if (lane >= d) place += o;
+            // the entries met, listed: a warp takes its words of the bitmap one by one,
+            // a bit a lane
+            constexpr int kWarpWords = kBitmap / (kThreads / 32);
+            const unsigned *words = touched + (tid >> 5) * kWarpWords;
+            const unsigned mine = lane < kWarpWords ? words[lane] : 0u;
+            int place = 0;
+            const int met = __reduce_add_sync(0xFFFFFFFFu, __popc(mine));
+            if (lane == 0 && met > 0) place = atomicAdd(&listed, met);
+            place = __shfl_sync(0xFFFFFFFFu, place, 0);
+#pragma unroll 4
+            for (int i = 0; i < kWarpWords; ++i) {
+                const unsigned w = __shfl_sync(0xFFFFFFFFu, mine, i);
+                if ((w >> lane) & 1u)
+                    list[place + __popc(w & ((1u << lane) - 1))] = (uint16_t)(((tid >> 5) * kWarpWords + i) * 32 + lane);
+                place += __popc(w);
             }
-            int base = 0;
-            if (lane == 31 && place > 0) base = atomicAdd(&listed, place);
-            place += __shfl_sync(0xFFFFFFFFu, base, 31) - __popc(left);
-            for (; left; left &= left - 1) list[place++] = (uint16_t)(tid * 32 + __ffs(left) - 1);
             ptx::named_barrier(1, kThreads);
         }
         // The row's path in place of the one that is counted: where the two differ.

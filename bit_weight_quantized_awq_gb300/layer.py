@@ -24,7 +24,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it, where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -7,6 +7,9 @@ table entries, tokens) is checked there: ``awq_last_device_status`` reports it.
 A step is ``paged_plan`` -> per layer ``kv_append``, ``tree_attention`` ->
 ``process_logits``: the plan's ``cu_new``, ``slot_map`` and ``tree_mask`` are the
 others' arguments.
+
+A step's kernels take a few microseconds each, so the wrappers look at every
+argument once, in one test; what is wrong is only looked for if that fails.
 """
 from __future__ import annotations
 
@@ -14,12 +17,13 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import (AWQError, Cache, DType, Logits, Status, TreeAttention, awq_kv_append, awq_paged_plan,
-                       awq_process_logits, awq_tree_attention)
-from .layer import _check, _ptr, _stream
+from ._binding import AWQError, Status, awq_kv_append, awq_paged_plan, awq_process_logits, awq_tree_attention
+from ._binding import pack_cache, pack_logits, pack_tree_attention
+from .layer import _check, _stream
 
-_I32 = torch.int32
-_DTYPES = {torch.float16: DType.F16, torch.bfloat16: DType.BF16, torch.float32: DType.F32}
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}     # awq_dtype_t
+_CACHE_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
 
 class PagedPlan(NamedTuple):
@@ -33,17 +37,14 @@ class PagedPlan(NamedTuple):
 
 
 def _cuda(t: torch.Tensor) -> torch.device:
-    dev = t.device
-    if dev.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("the AWQ library runs on CUDA tensors only")
-    return dev
+    return t.device
 
 
-def _ints(dev: torch.device, **tensors):
-    """Every given tensor is a contiguous int32 tensor on `dev`."""
-    for name, t in tensors.items():
-        if t is not None and not (t.dtype == _I32 and t.device == dev and t.is_contiguous()):
-            _check(t, name, _I32, dev)
+def _plain(t: torch.Tensor | None, dtype: torch.dtype, index: int) -> bool:
+    """No tensor, or a contiguous one of `dtype` on device `index`."""
+    return t is None or (t.dtype == dtype and t.get_device() == index and t.is_contiguous())
 
 
 def _length(t: torch.Tensor | None, name: str, n: int):
@@ -51,11 +52,15 @@ def _length(t: torch.Tensor | None, name: str, n: int):
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
 
 
-def _table(block_table: torch.Tensor, requests: int, dev: torch.device):
-    if block_table.dtype != _I32 or block_table.device != dev:
-        raise ValueError(f"block_table must be torch.int32 on {dev}")
-    if block_table.dim() != 2 or block_table.shape[0] != requests or block_table.stride(1) != 1:
+def _table(t: torch.Tensor, requests: int, index: int) -> int:
+    """The table's row stride."""
+    if t.dtype != _I32 or t.get_device() != index or t.dim() != 2:
+        raise ValueError("block_table must be a torch.int32 [requests, blocks] tensor on the others' device")
+    rows, width = t.shape
+    stride, step = t.stride()
+    if rows != requests or (step != 1 and width > 1):
         raise ValueError("block_table must be [requests, blocks] with adjacent entries in a row")
+    return stride if rows > 1 else width
 
 
 def paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -66,49 +71,58 @@ def paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: 
     cache slot, position and request, and with ``mask_words`` > 0 its ancestors in
     the drafted tree that ``parents`` describes (a chain if None)."""
     dev = _cuda(context_lens)
+    at = dev.index
     B = context_lens.numel()
-    _ints(dev, context_lens=context_lens, new_lens=new_lens, free_blocks=free_blocks, parents=parents)
-    _length(new_lens, "new_lens", B)
-    _length(parents, "parents", max_tokens)
-    _table(block_table, B, dev)
+    if not (_plain(context_lens, _I32, at) and _plain(new_lens, _I32, at) and _plain(free_blocks, _I32, at)
+            and _plain(parents, _I32, at) and new_lens.numel() == B):
+        for t, name in ((context_lens, "context_lens"), (new_lens, "new_lens"), (free_blocks, "free_blocks"),
+                        (parents, "parents")):
+            if t is not None:
+                _check(t, name, _I32, dev)
+        _length(new_lens, "new_lens", B)
+    if parents is not None:
+        _length(parents, "parents", max_tokens)
+    stride = _table(block_table, B, at)
     if max_tokens < 0 or mask_words < 0:
         raise ValueError("max_tokens and mask_words must not be negative")
-    cu_new = torch.empty(B + 1, dtype=_I32, device=dev)
-    counts = torch.empty(2, dtype=_I32, device=dev)
-    slot_map = torch.empty(max_tokens, dtype=torch.int64, device=dev)
-    positions = torch.empty(max_tokens, dtype=_I32, device=dev)
-    token_request = torch.empty(max_tokens, dtype=_I32, device=dev)
-    tree_mask = torch.empty((max_tokens, mask_words), dtype=_I32, device=dev) if mask_words else None
+    # one allocation for all that is laid out
+    T = max_tokens
+    sizes = [2 * T, T, T, T * mask_words, B + 1, 2]
+    slots, positions, request, mask, cu_new, counts = context_lens.new_empty(sum(sizes)).split_with_sizes(sizes)
+    slot_map = slots.view(_I64)
+    tree_mask = mask.view(T, mask_words) if mask_words else None
+    base = slots.data_ptr() if T else counts.data_ptr() - 4 * (B + 1)
     st = awq_paged_plan(context_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_table.shape[1],
-                        block_table.stride(0) if B > 1 else block_table.shape[1], free_blocks.data_ptr(),
-                        free_blocks.numel(), block_size, _ptr(parents), max_tokens, cu_new.data_ptr(),
-                        slot_map.data_ptr(), positions.data_ptr(), token_request.data_ptr(), _ptr(tree_mask),
-                        mask_words, counts.data_ptr(), _stream(dev))
+                        stride, free_blocks.data_ptr(), free_blocks.numel(), block_size,
+                        None if parents is None else parents.data_ptr(), T, base + 4 * (4 + mask_words) * T,
+                        base, base + 8 * T, base + 12 * T, base + 16 * T if mask_words else None, mask_words,
+                        base + 4 * ((4 + mask_words) * T + B + 1), _stream(dev))
     if st != Status.OK:
         raise AWQError(st, "awq_paged_plan")
-    return PagedPlan(cu_new, slot_map, positions, token_request, tree_mask, counts)
+    return PagedPlan(cu_new, slot_map, positions, request, tree_mask, counts)
 
 
-def _cache(t: torch.Tensor, name: str, dtype: torch.dtype, dev: torch.device) -> Cache:
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
-    if t.dim() != 4 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be [blocks, block_size, kv_heads, head_dim] with adjacent head_dim elements")
-    n, page, heads, dim = t.shape
-    s = t.stride()
+def _cache(t: torch.Tensor, name: str, dtype: torch.dtype, index: int, shape) -> tuple[int, int, int, int]:
+    """(data, block, token and head stride) of a paged cache of this shape."""
+    stride = t.stride()
+    if t.dtype != dtype or t.get_device() != index or len(stride) != 4 or t.shape != shape or \
+            (stride[3] != 1 and shape[3] > 1):
+        raise ValueError(f"{name} must be a {dtype} [blocks, block_size, kv_heads, head_dim] tensor with adjacent "
+                         f"head_dim elements on the others' device, of shape {tuple(shape)}")
+    n, page, heads, dim = shape
     # the stride of an axis with one entry is never used: a valid one stands in
-    return Cache(t.data_ptr(), s[0] if n > 1 else page * heads * dim, s[1], s[2] if heads > 1 else dim)
+    return (t.data_ptr(), stride[0] if n > 1 else page * heads * dim, stride[1], stride[2] if heads > 1 else dim)
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: torch.device):
-    """(token stride, head stride) of [tokens, heads, head_dim]."""
-    if t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, index: int):
+    """(tokens, heads, head_dim, token stride, head stride)."""
+    if t.dtype != dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on the others' device, got {t.dtype} on {t.device}")
+    stride, shape = t.stride(), t.shape
+    if len(stride) != 3 or (stride[2] != 1 and shape[2] > 1):
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with adjacent head_dim elements")
-    n, heads, dim = t.shape
-    s = t.stride()
-    return s[0] if n > 1 else heads * dim, s[1] if heads > 1 else dim
+    n, heads, dim = shape
+    return n, heads, dim, stride[0] if n > 1 else heads * dim, stride[1] if heads > 1 else dim
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -117,18 +131,21 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     a fused projection's output serve as they are) into the slots of a paged
     cache [blocks, block_size, kv_heads, head_dim]; slot -1 is skipped."""
     dev = _cuda(k_cache)
-    dtype = k_cache.dtype
-    if dtype not in (torch.float16, torch.bfloat16):
+    at = dev.index
+    dtype, shape = k_cache.dtype, k_cache.shape
+    if dtype not in _CACHE_DTYPES:
         raise ValueError(f"the cache must be float16 or bfloat16, got {dtype}")
-    kc, vc = _cache(k_cache, "k_cache", dtype, dev), _cache(v_cache, "v_cache", dtype, dev)
-    (kt, kh), (vt, vh) = _rows(k, "k", dtype, dev), _rows(v, "v", dtype, dev)
-    n, page, heads, dim = k_cache.shape
-    if v_cache.shape != k_cache.shape or k.shape != v.shape or k.shape[1:] != (heads, dim):
+    kc, vc = _cache(k_cache, "k_cache", dtype, at, shape), _cache(v_cache, "v_cache", dtype, at, shape)
+    T, heads, dim, kt, kh = _rows(k, "k", dtype, at)
+    vT, v_heads, v_dim, vt, vh = _rows(v, "v", dtype, at)
+    n, page, c_heads, c_dim = shape
+    if not (T == vT and heads == v_heads == c_heads and dim == v_dim == c_dim):
         raise ValueError("k, v and the two caches must agree in heads and head_dim")
-    _check(slot_map, "slot_map", torch.int64, dev)
-    _length(slot_map, "slot_map", k.shape[0])
-    st = awq_kv_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, kc, vc, slot_map.data_ptr(), k.shape[0], n, page,
-                       heads, dim, _stream(dev))
+    if not _plain(slot_map, _I64, at) or slot_map.numel() != T:
+        _check(slot_map, "slot_map", _I64, dev)
+        _length(slot_map, "slot_map", T)
+    st = awq_kv_append(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, pack_cache(*kc), pack_cache(*vc),
+                       slot_map.data_ptr(), T, n, page, heads, dim, _stream(dev))
     if st != Status.OK:
         raise AWQError(st, "awq_kv_append")
 
@@ -143,40 +160,42 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     the ones before it if None). ``max_new`` and ``max_context`` bound the
     lengths; ``lse`` (fp32 [tokens, q_heads]) receives the log-sum-exp."""
     dev = _cuda(q)
-    dtype = q.dtype
-    if dtype not in (torch.float16, torch.bfloat16):
+    at = dev.index
+    dtype, shape = q.dtype, k_cache.shape
+    if dtype not in _CACHE_DTYPES:
         raise ValueError(f"q must be float16 or bfloat16, got {dtype}")
-    qt, qh = _rows(q, "q", dtype, dev)
-    kc, vc = _cache(k_cache, "k_cache", dtype, dev), _cache(v_cache, "v_cache", dtype, dev)
-    tokens, heads, dim = q.shape
-    n, page, kv_heads, kv_dim = k_cache.shape
-    if v_cache.shape != k_cache.shape or kv_dim != dim:
-        raise ValueError("q and the two caches must agree in head_dim, the caches in every size")
+    T, heads, dim, qt, qh = _rows(q, "q", dtype, at)
+    kc, vc = _cache(k_cache, "k_cache", dtype, at, shape), _cache(v_cache, "v_cache", dtype, at, shape)
+    n, page, kv_heads, kv_dim = shape
+    if kv_dim != dim:
+        raise ValueError("q and the caches must agree in head_dim")
     B = context_lens.numel()
-    _ints(dev, context_lens=context_lens, cu_new=cu_new, tree_mask=tree_mask)
-    _length(cu_new, "cu_new", B + 1)
-    _table(block_table, B, dev)
-    words = 0
+    if not (_plain(context_lens, _I32, at) and _plain(cu_new, _I32, at) and cu_new.numel() == B + 1):
+        _check(context_lens, "context_lens", _I32, dev)
+        _check(cu_new, "cu_new", _I32, dev)
+        _length(cu_new, "cu_new", B + 1)
+    stride = _table(block_table, B, at)
+    words = mask = 0
     if tree_mask is not None:
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != tokens:
+        if not _plain(tree_mask, _I32, at):
+            _check(tree_mask, "tree_mask", _I32, dev)
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] == 0:
             raise ValueError("tree_mask must be [tokens, mask_words]")
-        words = tree_mask.shape[1]
-        if words == 0:
-            raise ValueError("tree_mask has no words")
+        words, mask = tree_mask.shape[1], tree_mask.data_ptr()
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _check(out, "out", dtype, dev)
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
     if lse is not None:
-        _check(lse, "lse", torch.float32, dev)
-        if lse.shape != (tokens, heads):
+        _check(lse, "lse", _F32, dev)
+        if lse.shape != (T, heads):
             raise ValueError("lse must be [tokens, q_heads]")
-    args = TreeAttention(q.data_ptr(), qt, qh, out.data_ptr(), _ptr(lse), kc, vc, block_table.data_ptr(),
-                         block_table.shape[1], block_table.stride(0) if B > 1 else block_table.shape[1],
-                         context_lens.data_ptr(), cu_new.data_ptr(), _ptr(tree_mask), words, B, tokens, heads,
-                         kv_heads, dim, n, page, max_new, max_context, scale, _DTYPES[dtype])
+    args = pack_tree_attention(q.data_ptr(), qt, qh, out.data_ptr(), 0 if lse is None else lse.data_ptr(), *kc, *vc,
+                               block_table.data_ptr(), block_table.shape[1], stride, context_lens.data_ptr(),
+                               cu_new.data_ptr(), mask, words, B, T, heads, kv_heads, dim, n, page, max_new,
+                               max_context, scale, _CACHE_DTYPES[dtype])
     st = awq_tree_attention(args, _stream(dev))
     if st != Status.OK:
         raise AWQError(st, "awq_tree_attention")
@@ -197,6 +216,7 @@ def process_logits(logits: torch.Tensor, row_request: torch.Tensor | None = None
     tensors are indexed by ``row_request`` (the row itself if None); a drafted
     token's row counts the tokens of its path in ``tree_mask`` as generated."""
     dev = _cuda(logits)
+    at = dev.index
     dtype = logits.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"logits must be float16, bfloat16 or float32, got {dtype}")
@@ -205,52 +225,69 @@ def process_logits(logits: torch.Tensor, row_request: torch.Tensor | None = None
     rows, vocab = logits.shape
     # the requests: the rows, or as many as the per-request tensors have
     B = rows if row_request is None else None
-    for t, name, more in ((repetition, "repetition", 0), (frequency, "frequency", 0), (presence, "presence", 0),
-                          (prompt_lens, "prompt_lens", 0), (history_offsets, "history_offsets", 1),
-                          (bias_offsets, "bias_offsets", 1), (cu_new, "cu_new", 1)):
+    pointers = {}
+
+    def take(name, t, dtype, length=None, per_request=None):
+        nonlocal B
         if t is None:
-            continue
-        if B is None:
-            B = t.numel() - more
-        _length(t, name, B + more)
+            pointers[name] = 0
+            return
+        if t.dtype != dtype or t.get_device() != at or not t.is_contiguous():
+            _check(t, name, dtype, dev)
+        if per_request is not None:
+            if B is None:
+                B = t.numel() - per_request
+            length = B + per_request
+        if length is not None and t.numel() != length:
+            _length(t, name, length)
+        pointers[name] = t.data_ptr()
+
+    take("repetition", repetition, _F32, per_request=0)
+    take("frequency", frequency, _F32, per_request=0)
+    take("presence", presence, _F32, per_request=0)
+    take("prompt_lens", prompt_lens, _I32, per_request=0)
+    take("history_offsets", history_offsets, _I32, per_request=1)
+    take("bias_offsets", bias_offsets, _I32, per_request=1)
+    take("cu_new", cu_new, _I32, per_request=1)
+    take("row_request", row_request, _I32, rows)
+    take("history", history, _I32)
+    take("draft_tokens", draft_tokens, _I32, rows)
+    take("tree_mask", tree_mask, _I32)
+    take("bias_tokens", bias_tokens, _I32)
+    take("grammar_mask", grammar_mask, _I32)
+    take("grammar_rows", grammar_rows, _I32, rows)
     if B is None:
         B = 2 ** 31 - 1      # nothing is indexed by a request
-    for t, name in ((repetition, "repetition"), (frequency, "frequency"), (presence, "presence"),
-                    (bias_values, "bias_values")):
-        if t is not None and not (t.dtype == torch.float32 and t.device == dev and t.is_contiguous()):
-            _check(t, name, torch.float32, dev)
-    _ints(dev, row_request=row_request, history=history, history_offsets=history_offsets, prompt_lens=prompt_lens,
-          draft_tokens=draft_tokens, cu_new=cu_new, tree_mask=tree_mask, bias_tokens=bias_tokens,
-          bias_offsets=bias_offsets, grammar_mask=grammar_mask, grammar_rows=grammar_rows)
-    _length(row_request, "row_request", rows)
-    _length(draft_tokens, "draft_tokens", rows)
-    _length(grammar_rows, "grammar_rows", rows)
-    if bias_tokens is not None:
-        if bias_values is None or bias_offsets is None:
-            raise ValueError("bias_tokens, bias_values and bias_offsets go together")
-        _length(bias_values, "bias_values", bias_tokens.numel())
+    if bias_tokens is not None and (bias_values is None or bias_offsets is None):
+        raise ValueError("bias_tokens, bias_values and bias_offsets go together")
+    take("bias_values", bias_values, _F32, None if bias_tokens is None else bias_tokens.numel())
     if history is not None and history_offsets is None:
         raise ValueError("history needs history_offsets")
     if draft_tokens is not None and cu_new is None:
         raise ValueError("draft_tokens needs cu_new")
-    if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != rows):
-        raise ValueError("tree_mask must be [rows, mask_words]")
-    if grammar_mask is not None and (grammar_mask.dim() != 2 or grammar_mask.shape[1] != (vocab + 31) // 32):
-        raise ValueError("grammar_mask must be [masks, ceil(vocab / 32)]")
+    words = masks = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != rows:
+            raise ValueError("tree_mask must be [rows, mask_words]")
+        words = tree_mask.shape[1]
+    if grammar_mask is not None:
+        if grammar_mask.dim() != 2 or grammar_mask.shape[1] != (vocab + 31) // 32:
+            raise ValueError("grammar_mask must be [masks, ceil(vocab / 32)]")
+        masks = grammar_mask.shape[0]
     if out is None:
-        out = torch.empty((rows, vocab), dtype=dtype, device=dev)
+        out = torch.empty_like(logits, memory_format=torch.contiguous_format)
     elif out is not logits:
         if out.dtype != dtype or out.device != dev or out.shape != logits.shape or \
                 (out.stride(1) != 1 and vocab > 1):
             raise ValueError("out must be like logits, with adjacent elements in a row")
-    args = Logits(logits.data_ptr(), out.data_ptr(), logits.stride(0) if rows > 1 else vocab,
-                  out.stride(0) if rows > 1 else vocab, rows, vocab, B, _ptr(row_request), _ptr(history),
-                  _ptr(history_offsets), _ptr(prompt_lens), 0 if history is None else history.numel(),
-                  _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(draft_tokens), _ptr(cu_new),
-                  _ptr(tree_mask), 0 if tree_mask is None else tree_mask.shape[1], _ptr(bias_tokens),
-                  _ptr(bias_offsets), _ptr(bias_values), 0 if bias_tokens is None else bias_tokens.numel(),
-                  _ptr(grammar_mask), _ptr(grammar_rows), 0 if grammar_mask is None else grammar_mask.shape[0],
-                  _DTYPES[dtype])
+    p = pointers
+    args = pack_logits(logits.data_ptr(), out.data_ptr(), logits.stride(0) if rows > 1 else vocab,
+                       out.stride(0) if rows > 1 else vocab, rows, vocab, B, p["row_request"], p["history"],
+                       p["history_offsets"], p["prompt_lens"], 0 if history is None else history.numel(),
+                       p["repetition"], p["frequency"], p["presence"], p["draft_tokens"], p["cu_new"],
+                       p["tree_mask"], words, p["bias_tokens"], p["bias_offsets"], p["bias_values"],
+                       0 if bias_tokens is None else bias_tokens.numel(), p["grammar_mask"], p["grammar_rows"], masks,
+                       _DTYPES[dtype])
     st = awq_process_logits(args, _stream(dev))
     if st != Status.OK:
         raise AWQError(st, "awq_process_logits")
