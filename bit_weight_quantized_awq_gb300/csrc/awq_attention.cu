@@ -480,7 +480,7 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     p.whole = tiles <= kWholeTiles;
     p.min_units = p.whole ? 1 : kBlockCost + 4;
     const int64_t units = p.whole ? blocks : blocks * (kBlockCost + tiles);
-    const int ctas = (int)std::min<int64_t>(li.ctas, std::max<int64_t>(1, units / p.min_units));
+    const int ctas = lay_out(p, li.ctas, units);
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
 #endif

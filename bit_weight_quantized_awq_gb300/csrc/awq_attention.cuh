@@ -10,7 +10,10 @@
 // units for its beginning and end and its weight for each tile. CTA c of G takes
 // the tiles that begin in [c U / G, (c + 1) U / G). So every CTA has the same work
 // whatever the lengths are, a long cache is split along its length, and nothing
-// but the lengths on the device is needed to find a CTA's range.
+// but the lengths on the device is needed to find a CTA's range. Where the CTAs
+// divide well by the key-value heads, each head has a line of its own and its share
+// of the CTAs, neighbouring ones for the heads: they then go through the same
+// tokens at the same time, whose keys of all heads lie side by side in HBM.
 //
 // Pieces. A row block whose tiles fall to several CTAs is a sum of pieces
 // (m, l, O): O = sum_j exp2(s_j - m) v_j and l = sum_j exp2(s_j - m), joined by
@@ -23,6 +26,7 @@
 // pieces took 10 to 20 us at 256 rows: one CTA's loads, behind a fence.)
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda.h>
@@ -38,7 +42,7 @@ namespace attn {
 // What is to be joined because a CTA has the last piece of a split row block.
 struct Join {
     int valid;
-    int cta0, cta1;         // the pieces: slot 1 of cta0, slot 0 of those after it up to cta1
+    int cta0, cta1;         // the pieces: slot 1 of cta0, slot 0 of the line's CTAs after it up to cta1
     int h, rb, token0, rows;
 };
 
@@ -60,6 +64,7 @@ struct Params {
     int shift;              // log2 of the block size
     int min_units;          // a CTA takes at least this many units: one tile at least
     int whole;              // row blocks are not split: one unit each, and nothing to join
+    int lines;              // 1, or kv_heads: lines of work, one a key-value head (see Work)
     float scale_log2;       // scale * log2(e): scores are kept in powers of two
 #ifdef AWQ_FAULT_TEST
     int fault;              // CTA 0's producer issues nothing (fault-test build only)
@@ -80,7 +85,8 @@ struct Segment {
 template <int RB, int KT, int kBlockCost>
 struct Work {
     int64_t units, pos, end;   // pos: where this CTA's next row block begins on the line
-    int ctas;               // CTAs that take part
+    int ctas;               // CTAs of the line that take part
+    int heads, head0, cta;  // heads of the line, the first of them, and this CTA's number in it
     int b, h, rb, tile, tiles;
     int ctx, n, token0, row_blocks;
 
@@ -136,6 +142,9 @@ struct Work {
         __shared__ int found_b;
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         if (tid == 0) p.joins[blockIdx.x].valid = 0;
+        heads = p.lines == 1 ? p.kv_heads : 1;
+        head0 = p.lines == 1 ? 0 : blockIdx.x % p.lines;
+        cta = blockIdx.x / p.lines;
         const int per = (p.B + THREADS - 1) / THREADS;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
         int64_t mine = 0;
@@ -147,7 +156,7 @@ struct Work {
                 bad = 1;
                 break;
             }
-            mine += head_units(p, c, t1 - t0) * p.kv_heads;
+            mine += head_units(p, c, t1 - t0) * heads;
         }
         int64_t su = mine;
 #pragma unroll
@@ -168,15 +177,15 @@ struct Work {
         }
         before += su - mine;
         if (units == 0) return false;
-        ctas = (int)min((int64_t)gridDim.x, max((int64_t)1, units / p.min_units));
-        if ((int)blockIdx.x >= ctas) return false;
-        pos = begin_of(blockIdx.x);
-        end = begin_of(blockIdx.x + 1);
+        ctas = (int)min((int64_t)(gridDim.x / p.lines), max((int64_t)1, units / p.min_units));
+        if (cta >= ctas) return false;
+        pos = begin_of(cta);
+        end = begin_of(cta + 1);
         if (pos >= before && pos < before + mine) {
             int i = b_lo;
             for (;; ++i) {
                 const int c = p.ctx[i], len = p.cu[i + 1] - p.cu[i];
-                const int64_t u = head_units(p, c, len) * p.kv_heads;
+                const int64_t u = head_units(p, c, len) * heads;
                 if (pos < before + u) break;
                 before += u;
             }
@@ -222,7 +231,7 @@ struct Work {
         if (pos >= end) return;
         if (++rb == row_blocks) {
             rb = 0;
-            if (++h == p.kv_heads) {
+            if (++h == heads) {
                 h = 0;
                 do {
                     ++b;
@@ -239,7 +248,7 @@ struct Work {
         if (pos < end && tile == tiles) next_block(p);   // the range began behind a block's last tile
         if (pos >= end) return false;
         s.b = b;
-        s.h = h;
+        s.h = head0 + h;
         s.rb = rb;
         s.ctx = ctx;
         s.n = n;
@@ -258,7 +267,7 @@ struct Work {
     // One thread of a CTA whose segment is a row block's last piece, of several.
     __device__ void note_join(const Params &p, const Segment &s, int rows) const
     {
-        p.joins[blockIdx.x] = Join{1, cta_of(s.u0), (int)blockIdx.x, s.h, s.rb, s.token0, rows};
+        p.joins[blockIdx.x] = Join{1, cta_of(s.u0) * p.lines + (int)blockIdx.x % p.lines, (int)blockIdx.x, s.h, s.rb, s.token0, rows};
     }
 };
 
@@ -408,12 +417,13 @@ attention_join_kernel(const __grid_constant__ Params p)
 #pragma unroll
     for (int e = 0; e < kJoinColumns; ++e) acc[e] = 0.f;
     if (works) {
-        for (int c = j.cta0 + sub; c <= j.cta1; c += kBatch * subs) {
+        const int step = subs * p.lines;
+        for (int c = j.cta0 + sub * p.lines; c <= j.cta1; c += kBatch * step) {
             float4 v[kBatch][2];
             float mc[kBatch], lc[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                const int cu = c + u * subs;
+                const int cu = c + u * step;
                 mc[u] = -INFINITY;
                 if (cu > j.cta1) continue;
                 const float *from = p.partials + (int64_t)(2 * cu + (cu == j.cta0 ? 1 : 0)) * SF;
@@ -432,7 +442,7 @@ attention_join_kernel(const __grid_constant__ Params p)
             m = top;
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                if (c + u * subs > j.cta1) break;
+                if (c + u * step > j.cta1) break;
                 const float w = exp2_fast(mc[u] - mx);
                 l += lc[u] * w;
                 const float *f = reinterpret_cast<const float *>(v[u]);
@@ -471,6 +481,16 @@ attention_join_kernel(const __grid_constant__ Params p)
         make_uint4(Elem<T>::pack(acc[0] * inv, acc[1] * inv), Elem<T>::pack(acc[2] * inv, acc[3] * inv),
                    Elem<T>::pack(acc[4] * inv, acc[5] * inv), Elem<T>::pack(acc[6] * inv, acc[7] * inv));
     if (col == 0) store_lse(p, j.token0, j.h, row, m == -INFINITY ? 0.f : m, l);
+}
+
+// CTAs of a launch, at most `most` of them, and how its work is laid out: `units` as
+// the bounds allow, `min_units` a CTA.
+inline int lay_out(Params &p, int most, int64_t units)
+{
+    const int a_head = most / p.kv_heads;
+    p.lines = a_head * p.kv_heads * 10 >= most * 9 ? p.kv_heads : 1;
+    const int64_t line = units / p.lines;
+    return (int)std::min<int64_t>(most / p.lines, std::max<int64_t>(1, line / p.min_units)) * p.lines;
 }
 
 // Launches a main kernel of `ctas` CTAs and, unless there is one only or each has

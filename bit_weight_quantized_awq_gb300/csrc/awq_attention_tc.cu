@@ -670,7 +670,7 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
     p.whole = tiles <= kWholeTiles;
     p.min_units = p.whole ? 1 : kBlockCost + 4;
     const int64_t units = p.whole ? blocks : blocks * (kBlockCost + 2 * tiles);
-    const int ctas = (int)std::min<int64_t>(li.sms, std::max<int64_t>(1, units / p.min_units));
+    const int ctas = lay_out(p, li.sms, units);
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
 #endif

@@ -85,18 +85,18 @@ def paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: 
     stride = _table(block_table, B, at)
     if max_tokens < 0 or mask_words < 0:
         raise ValueError("max_tokens and mask_words must not be negative")
-    # one allocation for all that is laid out
     T = max_tokens
-    sizes = [2 * T, T, T, T * mask_words, B + 1, 2]
-    slots, positions, request, mask, cu_new, counts = context_lens.new_empty(sum(sizes)).split_with_sizes(sizes)
-    slot_map = slots.view(_I64)
-    tree_mask = mask.view(T, mask_words) if mask_words else None
-    base = slots.data_ptr() if T else counts.data_ptr() - 4 * (B + 1)
+    cu_new = torch.empty(B + 1, dtype=_I32, device=dev)
+    counts = torch.empty(2, dtype=_I32, device=dev)
+    slot_map = torch.empty(T, dtype=_I64, device=dev)
+    positions = torch.empty(T, dtype=_I32, device=dev)
+    request = torch.empty(T, dtype=_I32, device=dev)
+    tree_mask = torch.empty((T, mask_words), dtype=_I32, device=dev) if mask_words else None
     st = awq_paged_plan(context_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(), block_table.shape[1],
                         stride, free_blocks.data_ptr(), free_blocks.numel(), block_size,
-                        None if parents is None else parents.data_ptr(), T, base + 4 * (4 + mask_words) * T,
-                        base, base + 8 * T, base + 12 * T, base + 16 * T if mask_words else None, mask_words,
-                        base + 4 * ((4 + mask_words) * T + B + 1), _stream(dev))
+                        None if parents is None else parents.data_ptr(), T, cu_new.data_ptr(), slot_map.data_ptr(),
+                        positions.data_ptr(), request.data_ptr(), tree_mask.data_ptr() if mask_words else None,
+                        mask_words, counts.data_ptr(), _stream(dev))
     if st != Status.OK:
         raise AWQError(st, "awq_paged_plan")
     return PagedPlan(cu_new, slot_map, positions, request, tree_mask, counts)
