@@ -9,11 +9,13 @@
 //
 // Bound: the cache is read once, 4 head_dim bytes a key and head, against
 // 4 head_dim flops a row, so 16 rows have 16 flops a byte: HBM. A CTA therefore is
-// one producer warp, which asks for key and value tiles (64 keys) with TMA, a box
-// a page, as far ahead as shared memory allows, and four consumer warps that
-// each take 16 of the tile's keys: S = Q K^T and O += P V with mma.sync
-// m16n8k16 (16 rows of q, held in registers), the warp's own maximum and sum. The
-// warps never meet before the segment ends. mma.sync, not tcgen05: at 16
+// one producer warp, which asks for key and value tiles (32 keys) with TMA, a box
+// a page, as far ahead as shared memory allows, and three consumer warps that take
+// whole tiles in turn: S = Q K^T and O += P V with mma.sync m16n8k16 (16 rows of q,
+// held in registers), the warp's own maximum and sum. A stage of the ring always
+// goes to the same warp, and the warps never meet before the segment ends. (Four
+// warps with 16 keys each of a common tile went through maximum, sum and rescaling
+// four times as often: 6 us for 500 keys instead of 4.) mma.sync, not tcgen05: at 16
 // rows a 128-row tcgen05 tile would be seven eighths padding and its operands and
 // accumulators would take the detour over shared and tensor memory.
 #include <algorithm>
@@ -32,12 +34,13 @@ namespace attn {
 namespace {
 
 constexpr int kRows = 16;        // rows of q a CTA works on (one mma.sync M)
-constexpr int kKeys = 64;        // keys a tile
-constexpr int kBlockCost = 1;    // a row block's beginning and end, in tiles
+constexpr int kKeys = 32;        // keys a tile
+constexpr int kBlockCost = 2;    // a row block's beginning and end, in tiles
 // Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
 // in the time that a second kernel would take to join the pieces.
-constexpr int kWholeTiles = 16;
-constexpr int kConsumers = 128;  // threads of the four consumer warps
+constexpr int kWholeTiles = 32;
+constexpr int kWarps = 3;        // consumer warps
+constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
 
 // DP: head_dim rounded up to 64, 128 or 256 (TMA fills the rest with zeros).
@@ -45,13 +48,14 @@ template <int DP>
 struct Cfg {
     static constexpr int kHalves = DP / 64;              // 128-byte columns of a tile
     static constexpr int kTile = kKeys * DP * 2;         // keys or values of one stage
-    static constexpr int kStages = DP == 64 ? 6 : 3;     // 96 KB in flight (192 KB at DP = 256)
+    static constexpr int kStages = DP == 64 ? 12 : 6;    // 96 KB in flight (192 KB at DP = 256)
+    static_assert(kStages % kWarps == 0, "a stage always goes to the same warp");
     static constexpr int kMergeOff = kStages * 2 * kTile;
     static constexpr int kMerge = kRows * DP * 4;        // one warp's O
-    static constexpr int kRedOff = kMergeOff + kMerge;   // m and l of the four warps
-    static constexpr int kRed = 8 * kRows * 4;
+    static constexpr int kRedOff = kMergeOff + kMerge;   // m and l of the warps
+    static constexpr int kRed = 2 * kWarps * kRows * 4;
     static constexpr int kBarOff = kRedOff + kRed;
-    static constexpr int kSmem = kBarOff + 128 + 1024;
+    static constexpr int kSmem = kBarOff + 256 + 1024;
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
 
@@ -85,7 +89,7 @@ __device__ __forceinline__ uint32_t piece(uint32_t tile, int r, int c)
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Params p)
 {
@@ -100,7 +104,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             ptx::mbar_init(ptx::smem_addr(full + i), 1);
-            ptx::mbar_init(ptx::smem_addr(empty + i), kConsumers / 32);
+            ptx::mbar_init(ptx::smem_addr(empty + i), 1);
         }
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -111,10 +115,15 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     if (!work.template find<kThreads>(p)) return;   // its barriers also publish the mbarriers
     Segment s;
 
-    if (warp == kConsumers / 32) {
+    if (warp == kWarps) {
         // ---------------------------------------------------------------- producer
         const int box = min(1 << p.shift, kKeys);            // keys of one TMA box
-        const int pages = kKeys / box;                       // boxes a tile: 1, 2 or 4
+        const int pages = kKeys / box;                       // pages of a tile: 1 or 2
+        // a box a lane: page, then keys or values, then the half of head_dim
+        constexpr int kBoxes = 2 * C::kHalves;
+        const int page = lane / kBoxes, part = lane % kBoxes, half = part % C::kHalves;
+        const CUtensorMap *map = part < C::kHalves ? &tm_k : &tm_v;
+        const uint32_t to = (part < C::kHalves ? 0 : C::kTile) + half * (kKeys * 128) + page * box * 128;
         int it = 0;
         bool ok = true;
 #ifdef AWQ_FAULT_TEST
@@ -124,8 +133,8 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             const int keys = s.ctx + s.n;
             const int32_t *table = p.table + (int64_t)s.b * p.table_stride;
             auto page_of = [&](int tile) {   // this lane's page of a tile; -1: none
-                const int key = tile * kKeys + lane * box;
-                if (lane >= pages || tile >= s.tile1 || key >= keys) return -1;
+                const int key = tile * kKeys + page * box;
+                if (page >= pages || tile >= s.tile1 || key >= keys) return -1;
                 const int id = table[key >> p.shift];
                 if (id >= 0 && id < p.num_blocks) return id;
                 raise_status(p.status, kStatusBadIndex);
@@ -140,18 +149,11 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 if (!ok) break;
                 const uint32_t fb = ptx::smem_addr(full + st);
                 const int count = __popc(__ballot_sync(0xFFFFFFFFu, id >= 0));
-                if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * 2 * C::kHalves * box * 128);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * box * 128);
                 __syncwarp();
-                if (id >= 0) {
-                    const uint32_t dst = ptx::smem_addr(smem + st * 2 * C::kTile) + (uint32_t)lane * box * 128;
-                    const int in_page = (tile * kKeys) & ((1 << p.shift) - 1) & ~(box - 1);
-#pragma unroll
-                    for (int half = 0; half < C::kHalves; ++half)
-                        ptx::tma_load_4d(dst + half * (kKeys * 128), &tm_k, fb, half * 64, s.h, in_page, id);
-#pragma unroll
-                    for (int half = 0; half < C::kHalves; ++half)
-                        ptx::tma_load_4d(dst + C::kTile + half * (kKeys * 128), &tm_v, fb, half * 64, s.h, in_page, id);
-                }
+                if (id >= 0)
+                    ptx::tma_load_4d(ptx::smem_addr(smem + st * 2 * C::kTile) + to, map, fb, half * 64, s.h,
+                                     (tile * kKeys) & ((1 << p.shift) - 1), id);
                 id = next_id;
             }
         }
@@ -166,8 +168,8 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     // -------------------------------------------------------------------- consumers
     const int g = lane >> 2, t4 = lane & 3;
     float *merge = reinterpret_cast<float *>(smem + C::kMergeOff);
-    float *warp_m = reinterpret_cast<float *>(smem + C::kRedOff), *warp_l = warp_m + 4 * kRows;
-    int it = 0;
+    float *warp_m = reinterpret_cast<float *>(smem + C::kRedOff), *warp_l = warp_m + kWarps * kRows;
+    int base = 0;                    // tiles of the segments before
     bool ok = true;
     while (work.next(p, s)) {
         const int all_rows = s.n * p.group, row0 = s.rb * kRows;
@@ -197,42 +199,44 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
         float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
 
-        for (int tile = s.tile0; tile < s.tile1 && ok; ++tile, ++it) {
-            const int st = it % C::kStages;
+        // this warp's tiles: those whose place in the ring goes to it
+        const int skip = (warp - base % kWarps + kWarps) % kWarps;
+        for (int tile = s.tile0 + skip; tile < s.tile1 && ok; tile += kWarps) {
+            const int it = base + tile - s.tile0, st = it % C::kStages;
             ok = ptx::mbar_wait_bounded(ptx::smem_addr(full + st), (it / C::kStages) & 1, abort_flag, p.status);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             const uint32_t kt = ptx::smem_addr(smem + st * 2 * C::kTile);
             const uint32_t vt = kt + C::kTile;
-            // scores of this warp's 16 keys: columns 2 t4, 2 t4 + 1 of keys 0-7 and 8-15
-            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int krow = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+            // scores: columns 2 t4, 2 t4 + 1 of each eight keys
+            float sc[kKeys / 8][4];
+#pragma unroll
+            for (int i = 0; i < kKeys / 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[i][e] = 0.f;
+            const int krow = ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
-                uint32_t b[4];
-                ptx::ldmatrix_x4(piece<DP>(kt, krow, kk * 2 + ((lane >> 3) & 1)), b);
-                mma<T>(sc[0], qf[kk], b[0], b[1]);
-                mma<T>(sc[1], qf[kk], b[2], b[3]);
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i) {
+                    uint32_t b[4];
+                    ptx::ldmatrix_x4(piece<DP>(kt, i * 16 + krow, kk * 2 + ((lane >> 3) & 1)), b);
+                    mma<T>(sc[2 * i], qf[kk], b[0], b[1]);
+                    mma<T>(sc[2 * i + 1], qf[kk], b[2], b[3]);
+                }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kKeys / 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[i][e] *= p.scale_log2;
-            const int key0 = tile * kKeys + warp * 16;       // this warp's first key
-            const bool drafted = key0 + 16 > s.ctx;          // drafted (or no) keys among them
+            const int key0 = tile * kKeys;
+            const bool drafted = key0 + kKeys > s.ctx;       // drafted (or no) keys among them
             uint32_t seen_a = 0xFFFFFFFFu, seen_b = 0xFFFFFFFFu;   // bit k: key0 + k is visible
             if (drafted) {
-                const int before = s.ctx - key0;             // keys of the context among the 16
-                if (before > 0) {
-                    const uint32_t ctx_bits = (1u << before) - 1;
-                    seen_a = ctx_bits | (seen_bits(p, s, ta, 0) << before);
-                    seen_b = ctx_bits | (seen_bits(p, s, tb, 0) << before);
-                } else {
-                    seen_a = seen_bits(p, s, ta, -before);
-                    seen_b = seen_bits(p, s, tb, -before);
-                }
+                seen_a = seen32(p, s, ta, key0);
+                seen_b = seen32(p, s, tb, key0);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < kKeys / 8; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int k = i * 8 + t4 * 2 + e;
@@ -240,8 +244,12 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         if (!((seen_b >> k) & 1u)) sc[i][2 + e] = -INFINITY;
                     }
             }
-            float na = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-            float nb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+            float na = -INFINITY, nb = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kKeys / 8; ++i) {
+                na = fmaxf(na, fmaxf(sc[i][0], sc[i][1]));
+                nb = fmaxf(nb, fmaxf(sc[i][2], sc[i][3]));
+            }
 #pragma unroll
             for (int d = 1; d < 4; d <<= 1) {
                 na = fmaxf(na, __shfl_xor_sync(0xFFFFFFFFu, na, d));
@@ -265,25 +273,26 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 ma = na;
                 mb = nb;
             }
+            uint32_t pf[kKeys / 16][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < kKeys / 8; ++i) {
                 sc[i][0] = exp2_fast(sc[i][0] - ea);
                 sc[i][1] = exp2_fast(sc[i][1] - ea);
                 sc[i][2] = exp2_fast(sc[i][2] - eb);
                 sc[i][3] = exp2_fast(sc[i][3] - eb);
                 la += sc[i][0] + sc[i][1];
                 lb += sc[i][2] + sc[i][3];
+                pf[i >> 1][2 * (i & 1)] = Elem<T>::pack(sc[i][0], sc[i][1]);
+                pf[i >> 1][2 * (i & 1) + 1] = Elem<T>::pack(sc[i][2], sc[i][3]);
             }
-            const uint32_t pf[4] = {Elem<T>::pack(sc[0][0], sc[0][1]), Elem<T>::pack(sc[0][2], sc[0][3]),
-                                    Elem<T>::pack(sc[1][0], sc[1][1]), Elem<T>::pack(sc[1][2], sc[1][3])};
             if (drafted) {
                 // Values of keys past the last one may be anything: made zero, so
                 // that a weight of zero takes nothing from them. A drafted key's
                 // infinities and NaN reach the rows that see it only.
                 bool odd = false;
-                for (int e = lane; e < 16 * (DP / 8); e += 32) {
+                for (int e = lane; e < kKeys * (DP / 8); e += 32) {
                     const int r = e / (DP / 8), key = key0 + r;
-                    const uint32_t at = piece<DP>(vt, warp * 16 + r, e % (DP / 8));
+                    const uint32_t at = piece<DP>(vt, r, e % (DP / 8));
                     if (key >= s.ctx + s.n) {
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
                     } else if (key >= s.ctx) {
@@ -296,12 +305,12 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 }
                 __syncwarp();
                 if (__any_sync(0xFFFFFFFFu, odd)) {
-                    for (int k = max(0, s.ctx - key0); k < 16 && key0 + k < s.ctx + s.n; ++k) {
+                    for (int k = max(0, s.ctx - key0); k < kKeys && key0 + k < s.ctx + s.n; ++k) {
                         const bool sa = (seen_a >> k) & 1u, sb = (seen_b >> k) & 1u;
 #pragma unroll
                         for (int i = 0; i < DP / 8; ++i) {
                             uint32_t w;
-                            const uint32_t at = piece<DP>(vt, warp * 16 + k, i) + t4 * 4;
+                            const uint32_t at = piece<DP>(vt, k, i) + t4 * 4;
                             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
@@ -313,9 +322,9 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                             }
                         }
                         __syncwarp();
-                        // the lanes of row 0 of the fragment clear what all have read
+                        // cleared once all lanes have read it
                         for (int c = lane; c < DP / 2; c += 32) {
-                            const uint32_t at = piece<DP>(vt, warp * 16 + k, c >> 2) + (c & 3) * 4;
+                            const uint32_t at = piece<DP>(vt, k, c >> 2) + (c & 3) * 4;
                             uint32_t w;
                             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
                             if ((w & Elem<T>::kExpMask) == Elem<T>::kExpMask) w &= 0xFFFF0000u;
@@ -328,19 +337,23 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 // these stores come before the TMA's next write of the stage
                 ptx::fence_proxy_async_smem();
             }
-            const int vrow = warp * 16 + (lane & 15);
 #pragma unroll
-            for (int i = 0; i < DP / 16; ++i) {
-                uint32_t b[4];
-                ldmatrix_x4_trans(piece<DP>(vt, vrow, i * 2 + (lane >> 4)), b);
-                mma<T>(o[2 * i], pf, b[0], b[1]);
-                mma<T>(o[2 * i + 1], pf, b[2], b[3]);
+            for (int j = 0; j < kKeys / 16; ++j) {
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                    uint32_t b[4];
+                    ldmatrix_x4_trans(piece<DP>(vt, j * 16 + (lane & 15), i * 2 + (lane >> 4)), b);
+                    mma<T>(o[2 * i], pf[j], b[0], b[1]);
+                    mma<T>(o[2 * i + 1], pf[j], b[2], b[3]);
+                }
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(empty + st));
         }
 
-        // ---- the four warps' sums become one, in warp 0
+        base += s.tile1 - s.tile0;
+
+        // ---- the warps' sums become one, in warp 0
 #pragma unroll
         for (int d = 1; d < 4; d <<= 1) {
             la += __shfl_xor_sync(0xFFFFFFFFu, la, d);
@@ -352,17 +365,17 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             warp_l[warp * kRows + g] = la;
             warp_l[warp * kRows + g + 8] = lb;
         }
-        // all four leave together if one gave up
+        // all leave together if one gave up
         if (!ptx::named_barrier_and(1, kConsumers, ok)) return;
         float m2a = -INFINITY, m2b = -INFINITY, l2a = 0.f, l2b = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             m2a = fmaxf(m2a, warp_m[w * kRows + g]);
             m2b = fmaxf(m2b, warp_m[w * kRows + g + 8]);
         }
         const float ea = m2a == -INFINITY ? 0.f : m2a, eb = m2b == -INFINITY ? 0.f : m2b;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             l2a += warp_l[w * kRows + g] * exp2_fast(warp_m[w * kRows + g] - ea);
             l2b += warp_l[w * kRows + g + 8] * exp2_fast(warp_m[w * kRows + g + 8] - eb);
         }
@@ -376,7 +389,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         }
         float4 *mine = reinterpret_cast<float4 *>(merge) + lane;
 #pragma unroll 1
-        for (int w = 1; w < 4; ++w) {
+        for (int w = 1; w < kWarps; ++w) {
             if (warp == w)
 #pragma unroll
                 for (int i = 0; i < DP / 8; ++i) mine[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
@@ -478,7 +491,7 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
     const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
     p.whole = tiles <= kWholeTiles;
-    p.min_units = p.whole ? 1 : kBlockCost + 4;
+    p.min_units = p.whole ? 1 : kBlockCost + 8;
     const int64_t units = p.whole ? blocks : blocks * (kBlockCost + tiles);
     const int ctas = lay_out(p, li.ctas, units);
 #ifdef AWQ_FAULT_TEST

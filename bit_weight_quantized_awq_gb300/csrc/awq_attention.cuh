@@ -120,15 +120,20 @@ struct Work {
         for (int rb = 0; rb < blocks; ++rb) sum += block_units(p, ctx, n, rb);
         return sum;
     }
-    __device__ int64_t begin_of(int c) const { return units * c / ctas; }
-    __device__ int cta_of(int64_t u) const { return (int)(((u + 1) * ctas - 1) / units); }
+    // a / b of non-negative numbers; most fit 32 bits, whose division takes a tenth of the time
+    static __device__ int64_t quotient(int64_t a, int64_t b)
+    {
+        return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+    }
+    __device__ int64_t begin_of(int c) const { return quotient(units * c, ctas); }
+    __device__ int cta_of(int64_t u) const { return (int)quotient((u + 1) * ctas - 1, units); }
     // A block's first tile begins at its first unit u0, tile i at u0 + kBlockCost + i
     // weight: the first one that begins at `at` or later.
     static __device__ int first_tile(const Params &p, int64_t at, int64_t u0, int weight, int tiles)
     {
         if (at <= u0) return 0;
         if (p.whole) return tiles;
-        const int64_t i = (at - u0 - kBlockCost + weight - 1) / weight;
+        const int64_t i = weight == 1 ? at - u0 - kBlockCost : (at - u0 - kBlockCost + 1) >> 1;   // weight is 1 or 2
         return (int)min((int64_t)tiles, max((int64_t)1, i));
     }
 
@@ -138,8 +143,10 @@ struct Work {
     __device__ bool find(const Params &p)
     {
         __shared__ int64_t warp_units[THREADS / 32];
-        __shared__ int64_t found_units;
-        __shared__ int found_b;
+        __shared__ struct {
+            int64_t before, per_head;
+            int b, ctx, token0, n;
+        } found;
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         if (tid == 0) p.joins[blockIdx.x].valid = 0;
         heads = p.lines == 1 ? p.kv_heads : 1;
@@ -147,8 +154,8 @@ struct Work {
         cta = blockIdx.x / p.lines;
         const int per = (p.B + THREADS - 1) / THREADS;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
-        int64_t mine = 0;
-        int bad = 0;
+        int64_t mine = 0, units0 = 0;          // of the thread's requests, and of the first of them
+        int bad = 0, ctx0 = 0, at0 = 0, len0 = 0;
         for (int i = b_lo; i < b_hi; ++i) {
             const int c = p.ctx[i], t0 = p.cu[i], t1 = p.cu[i + 1];
             if (t0 < 0 || t1 < t0 || t1 > p.tokens || c < 0 ||
@@ -156,7 +163,14 @@ struct Work {
                 bad = 1;
                 break;
             }
-            mine += head_units(p, c, t1 - t0) * heads;
+            const int64_t u = head_units(p, c, t1 - t0);
+            mine += u * heads;
+            if (i == b_lo) {
+                units0 = u;
+                ctx0 = c;
+                at0 = t0;
+                len0 = t1 - t0;
+            }
         }
         int64_t su = mine;
 #pragma unroll
@@ -177,32 +191,43 @@ struct Work {
         }
         before += su - mine;
         if (units == 0) return false;
-        ctas = (int)min((int64_t)(gridDim.x / p.lines), max((int64_t)1, units / p.min_units));
+        ctas = (int)min((int64_t)(gridDim.x / p.lines), max((int64_t)1, quotient(units, p.min_units)));
         if (cta >= ctas) return false;
         pos = begin_of(cta);
         end = begin_of(cta + 1);
         if (pos >= before && pos < before + mine) {
+            // the request, and what has just been read of it
             int i = b_lo;
-            for (;; ++i) {
-                const int c = p.ctx[i], len = p.cu[i + 1] - p.cu[i];
-                const int64_t u = head_units(p, c, len) * heads;
-                if (pos < before + u) break;
-                before += u;
+            int64_t per_head = units0;
+            while (pos >= before + per_head * heads) {
+                before += per_head * heads;
+                ++i;
+                ctx0 = p.ctx[i];
+                at0 = p.cu[i];
+                len0 = p.cu[i + 1] - at0;
+                per_head = head_units(p, ctx0, len0);
             }
-            found_b = i;
-            found_units = before;
+            found.b = i;
+            found.ctx = ctx0;
+            found.token0 = at0;
+            found.n = len0;
+            found.before = before;
+            found.per_head = per_head;
         }
         __syncthreads();
-        b = found_b;
-        load(p);
-        int64_t rem = pos - found_units;
-        const int64_t per_head = head_units(p, ctx, n);
-        h = (int)(rem / per_head);
+        b = found.b;
+        ctx = found.ctx;
+        token0 = found.token0;
+        n = found.n;
+        row_blocks = row_blocks_of(p, n);
+        int64_t rem = pos - found.before;
+        const int64_t per_head = found.per_head;
+        h = (int)quotient(rem, per_head);
         rem -= h * per_head;
         rb = 0;
         if (p.mask != nullptr) {
             const int64_t full = block_units(p, ctx, n, 0);
-            rb = (int)min((int64_t)(row_blocks - 1), rem / full);
+            rb = (int)min((int64_t)(row_blocks - 1), quotient(rem, full));
             rem -= rb * full;
         } else {
             for (int64_t u = block_units(p, ctx, n, 0); rem >= u; u = block_units(p, ctx, n, rb)) {
@@ -291,6 +316,15 @@ __device__ __forceinline__ uint32_t seen_bits(const Params &p, const Segment &s,
     }
     const int left = s.n - j0;
     return left >= 32 ? bits : bits & ((1u << left) - 1);
+}
+
+// Bits of the keys key0 .. key0 + 31 that token t sees.
+__device__ __forceinline__ uint32_t seen32(const Params &p, const Segment &s, int t, int key0)
+{
+    const int before = s.ctx - key0;   // keys of the context among them
+    if (before >= 32) return 0xFFFFFFFFu;
+    if (before > 0) return ((1u << before) - 1) | (seen_bits(p, s, t, 0) << before);
+    return seen_bits(p, s, t, -before);
 }
 
 // ---- element types ----

@@ -101,15 +101,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-// Bits of the keys key0 .. key0 + 31 that token t sees.
-__device__ __forceinline__ uint32_t seen32(const Params &p, const Segment &s, int t, int key0)
-{
-    const int before = s.ctx - key0;   // keys of the context among them
-    if (before >= 32) return 0xFFFFFFFFu;
-    if (before > 0) return ((1u << before) - 1) | (seen_bits(p, s, t, 0) << before);
-    return seen_bits(p, s, t, -before);
-}
-
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
