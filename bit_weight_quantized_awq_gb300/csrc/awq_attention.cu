@@ -131,30 +131,23 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 #endif
         while (ok && work.next(p, s)) {
             const int keys = s.ctx + s.n;
-            const int32_t *table = p.table + (int64_t)s.b * p.table_stride;
-            auto page_of = [&](int tile) {   // this lane's page of a tile; -1: none
-                const int key = tile * kKeys + page * box;
-                if (page >= pages || tile >= s.tile1 || key >= keys) return -1;
-                const int id = table[key >> p.shift];
-                if (id >= 0 && id < p.num_blocks) return id;
-                raise_status(p.status, kStatusBadIndex);
-                return p.num_blocks;         // past the tensor: TMA fills zeros
-            };
-            int id = page_of(s.tile0);
+            Pages ids;
+            ids.open(p, s, (s.tile0 * kKeys) >> p.shift, lane);
             for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
-                const int next_id = page_of(tile + 1);
+                const int key = tile * kKeys + (page < pages ? page * box : 0);
+                const int id = ids.block(p, key >> p.shift, lane);
+                const bool mine = page < pages && key < keys;
                 const int st = it % C::kStages;
                 ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + st), ((it / C::kStages) & 1) ^ 1, abort_flag, p.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 const uint32_t fb = ptx::smem_addr(full + st);
-                const int count = __popc(__ballot_sync(0xFFFFFFFFu, id >= 0));
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, mine));
                 if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * box * 128);
                 __syncwarp();
-                if (id >= 0)
+                if (mine)
                     ptx::tma_load_4d(ptx::smem_addr(smem + st * 2 * C::kTile) + to, map, fb, half * 64, s.h,
                                      (tile * kKeys) & ((1 << p.shift) - 1), id);
-                id = next_id;
             }
         }
         if (!ok) {

@@ -327,6 +327,42 @@ __device__ __forceinline__ uint32_t seen32(const Params &p, const Segment &s, in
     return seen_bits(p, s, t, -before);
 }
 
+// ---- page numbers ----
+
+// A producer warp's view of a request's block table: a window of 32 entries, one a
+// lane, and the next window already asked for, so that no tile waits for its
+// pages' numbers (with each tile's looked up just ahead of it, a warp spent a
+// microsecond a tile waiting).
+struct Pages {
+    const int32_t *table;
+    int last;               // the last page of the request
+    int base, now, next;    // the window's first page; this lane's entries of both windows
+    __device__ int entry(int page) const { return page <= last ? table[page] : 0; }
+    __device__ void open(const Params &p, const Segment &s, int first, int lane)
+    {
+        table = p.table + (int64_t)s.b * p.table_stride;
+        last = (s.ctx + s.n - 1) >> p.shift;
+        base = first;
+        now = entry(base + lane);
+        next = entry(base + 32 + lane);
+    }
+    // This lane's page's block, called by all lanes; pages only grow, and those of one
+    // call lie in one window. A number outside the cache is reported, and becomes one
+    // past the tensor, where TMA reads zeros.
+    __device__ int block(const Params &p, int page, int lane)
+    {
+        if (__any_sync(0xFFFFFFFFu, page >= base + 32)) {
+            base += 32;
+            now = next;
+            next = entry(base + 32 + lane);
+        }
+        const int id = __shfl_sync(0xFFFFFFFFu, now, (page - base) & 31);
+        if (id >= 0 && id < p.num_blocks) return id;
+        if (page <= last) raise_status(p.status, kStatusBadIndex);
+        return p.num_blocks;
+    }
+};
+
 // ---- element types ----
 
 template <typename T>

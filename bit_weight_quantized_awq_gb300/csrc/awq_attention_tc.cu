@@ -169,25 +169,19 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             const int keys = s.ctx + s.n, nt = s.tile1 - s.tile0;
             const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
             const int ahead = two ? 1 : 2;           // K tiles before the first V tile
-            const int32_t *table = p.table + (int64_t)s.b * p.table_stride;
-            auto page_of = [&](int j) {
-                const int key = (s.tile0 + j) * kKeys + lane * box;
-                if (lane >= pages || j >= nt || key >= keys) return -1;
-                const int id = table[key >> p.shift];
-                if (id >= 0 && id < p.num_blocks) return id;
-                raise_status(p.status, kStatusBadIndex);
-                return p.num_blocks;                 // past the tensor: TMA fills zeros
-            };
-            auto load = [&](int j, int id, const CUtensorMap *map) {
+            auto load = [&](int j, Pages &ids, const CUtensorMap *map) {
+                const int key = (s.tile0 + j) * kKeys + (lane < pages ? lane * box : 0);
+                const int id = ids.block(p, key >> p.shift, lane);
+                const bool mine = lane < pages && key < keys;
                 const int slot = at % C::kSlots;
                 ok = ptx::mbar_wait_bounded(ptx::smem_addr(freed + slot), ((at / C::kSlots) & 1) ^ 1, abort_flag, p.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) return;
                 const uint32_t fb = ptx::smem_addr(full + slot);
-                const int count = __popc(__ballot_sync(0xFFFFFFFFu, id >= 0));
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, mine));
                 if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * C::kHalves * box * 128);
                 __syncwarp();
-                if (id >= 0) {
+                if (mine) {
                     const uint32_t dst = ptx::smem_addr(smem + C::kQ + slot * C::kTile) + (uint32_t)lane * box * 128;
                     const int in_page = ((s.tile0 + j) * kKeys) & ((1 << p.shift) - 1) & ~(box - 1);
 #pragma unroll
@@ -196,18 +190,14 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 }
                 ++at;
             };
-            // K 0 (K 1), then V j, K j + ahead: the order of the MMAs. Page
-            // numbers are fetched a tile before they are needed.
-            int id0 = page_of(0), id1 = page_of(1), id2 = page_of(2);
-            load(0, id0, &tm_k);
-            if (!two && nt > 1 && ok) load(1, id1, &tm_k);
+            // K 0 (K 1), then V j, K j + ahead: the order of the MMAs
+            Pages k_ids, v_ids;
+            k_ids.open(p, s, (s.tile0 * kKeys) >> p.shift, lane);
+            v_ids = k_ids;
+            for (int j = 0; j < min(ahead, nt) && ok; ++j) load(j, k_ids, &tm_k);
             for (int j = 0; j < nt && ok; ++j) {
-                const int id3 = page_of(j + 3);
-                load(j, id0, &tm_v);
-                if (ok && j + ahead < nt) load(j + ahead, two ? id1 : id2, &tm_k);
-                id0 = id1;
-                id1 = id2;
-                id2 = id3;
+                load(j, v_ids, &tm_v);
+                if (ok && j + ahead < nt) load(j + ahead, k_ids, &tm_k);
             }
         }
         if (!ok) {
