@@ -2,7 +2,7 @@
 // many rows a key-value head (drafted trees, chunks of a prompt), on the 5th-generation
 // tensor cores; head_dim up to 128. awq_attention.cuh has the split of the work.
 //
-// A row block is 256 rows, a tile 128 keys. Two streams of work alternate on the
+// A row block is 256 rows (128 where no request has more), a tile 128 keys. Two streams of work alternate on the
 // tensor cores, so that one multiplies while the other's softmax runs:
 //   more than 128 rows in the block: stream i has rows 128 i .. 128 i + 127 and
 //     both take every tile (a tile is read once for 256 rows);
@@ -46,7 +46,6 @@ namespace awq {
 namespace attn {
 namespace {
 
-constexpr int kRows = 256;       // rows of a block
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kBlockCost = 2;    // a row block's beginning and end: as a tile of the heavier kind
 // Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
@@ -58,13 +57,17 @@ constexpr float kSlack = 8.f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kO = 256;     // first column of O 0; S of stream i and half h is at 128 i + 64 h
 
-template <int DP>
+// kRows: rows of a block, 256, or 128 for calls whose requests have no more -- their
+// keys and values come from HBM at the pace of the loads under way, and up to four
+// tiles have landed and wait for their turn, so the space of q's other half goes
+// to the ring.
+template <int DP, int kRows>
 struct Cfg {
     static constexpr int kHalves = DP / 64;
     static constexpr int kHalf = kKeys * 128;          // 64 columns of a tile, 128-byte rows
     static constexpr int kTile = kHalves * kHalf;
-    static constexpr int kQ = 2 * kTile;               // 256 rows of q
-    static constexpr int kSlots = DP == 128 ? 5 : 10;  // 160 KB of tiles
+    static constexpr int kQ = kRows / 128 * kTile;
+    static constexpr int kSlots = (224 * 1024 - kQ) / kTile;   // 5 or 6 tiles of 32 KB, 12 or 13 of 16 KB
     static constexpr int kBarOff = kQ + kSlots * kTile;
     static constexpr int kSmem = kBarOff + 512 + 1024;
     static_assert(kSmem <= 226 * 1024, "shared memory budget");
@@ -101,12 +104,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ Params p)
 {
-    using C = Cfg<DP>;
+    using C = Cfg<DP, kRows>;
     constexpr bool kBf16 = !std::is_same<T, __half>::value;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -167,7 +170,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
 #endif
         while (ok && work.next(p, s)) {
             const int keys = s.ctx + s.n, nt = s.tile1 - s.tile0;
-            const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
+            const bool two = kRows > 128 && min(kRows, s.n * p.group - s.rb * kRows) > 128;
             const int ahead = two ? 1 : 2;           // K tiles before the first V tile
             auto load = [&](int j, Pages &ids, const CUtensorMap *map) {
                 const int key = (s.tile0 + j) * kKeys + (lane < pages ? lane * box : 0);
@@ -276,7 +279,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         };
         while (ok && work.next(p, s)) {
             const int nt = s.tile1 - s.tile0;
-            const bool two = min(kRows, s.n * p.group - s.rb * kRows) > 128;
+            const bool two = kRows > 128 && min(kRows, s.n * p.group - s.rb * kRows) > 128;
             if (!wait(ptx::smem_addr(q_full), seg & 1)) break;
             ++seg;
             // the ring: K 0 (K 1), then V j, K j + ahead; with shared rows this
@@ -347,7 +350,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             if (!work.next(p, s)) break;
             const int nt = s.tile1 - s.tile0;
             const int row0 = s.rb * kRows, rows = min(kRows, s.n * p.group - row0);
-            const bool two = rows > 128;
+            const bool two = kRows > 128 && rows > 128;
             if (tid == 0) *odd_flag = 0;
             {
                 // a thread has one 16-byte column and every kStep-th row; eight
@@ -614,7 +617,7 @@ struct LaunchInfo {
     unsigned gen = 0;
 };
 
-template <typename T, int DP>
+template <typename T, int DP, int kRows>
 LaunchInfo launch_info()
 {
     static std::mutex mu;
@@ -628,16 +631,16 @@ LaunchInfo launch_info()
     auto it = cache.find(dev);
     if (it != cache.end() && it->second.gen == gen) return it->second;
     li.gen = gen;
-    li.err = cudaFuncSetAttribute(attention_tc_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP>::kSmem);
+    li.err = cudaFuncSetAttribute(attention_tc_kernel<T, DP, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DP, kRows>::kSmem);
     if (li.err == cudaSuccess) li.err = cudaDeviceGetAttribute(&li.sms, cudaDevAttrMultiProcessorCount, dev);
     if (li.err == cudaSuccess) cache[dev] = li;
     return li;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int kRows>
 cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
 {
-    const LaunchInfo li = launch_info<T, DP>();
+    const LaunchInfo li = launch_info<T, DP, kRows>();
     if (li.err != cudaSuccess) return li.err;
     Params p = make_params(a);
     // no zero: a masked score, -inf times the scale, has to stay -inf
@@ -655,21 +658,27 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
 #endif
-    return launch_pair<T, kRows, DP>(attention_tc_kernel<T, DP>, ctas, kThreads, Cfg<DP>::kSmem, stream, tk, tv, p);
+    return launch_pair<T, kRows, DP>(attention_tc_kernel<T, DP, kRows>, ctas, kThreads, Cfg<DP, kRows>::kSmem, stream, tk, tv, p);
 }
 
 } // namespace
 
+template <typename T, int DP>
+cudaError_t launch_tc_rows(const awq_tree_attention_t &a, cudaStream_t stream)
+{
+    return a.max_new * (a.q_heads / a.kv_heads) <= 128 ? launch_tc<T, DP, 128>(a, stream) : launch_tc<T, DP, 256>(a, stream);
+}
+
 cudaError_t launch_tc_any(const awq_tree_attention_t &a, cudaStream_t stream)
 {
     const bool f16 = a.dtype == AWQ_F16;
-    if (a.head_dim <= 64) return f16 ? launch_tc<__half, 64>(a, stream) : launch_tc<__nv_bfloat16, 64>(a, stream);
-    return f16 ? launch_tc<__half, 128>(a, stream) : launch_tc<__nv_bfloat16, 128>(a, stream);
+    if (a.head_dim <= 64) return f16 ? launch_tc_rows<__half, 64>(a, stream) : launch_tc_rows<__nv_bfloat16, 64>(a, stream);
+    return f16 ? launch_tc_rows<__half, 128>(a, stream) : launch_tc_rows<__nv_bfloat16, 128>(a, stream);
 }
 
 size_t tc_partial_floats(int sms, int64_t head_dim)
 {
-    return head_dim > 128 ? 0 : scratch_floats(sms, kRows, head_dim <= 64 ? 64 : 128);
+    return head_dim > 128 ? 0 : scratch_floats(sms, 256, head_dim <= 64 ? 64 : 128);
 }
 
 } // namespace attn
