@@ -27,8 +27,8 @@
 // head, then the tensor cores and, close to them, the exponentials (128 x 128 of
 // them a stream and tile).
 //
-//   warp 0      producer: K and V tiles, a TMA box a page, in one ring, in the order
-//               the MMAs take them
+//   warps 0, 3  producers of K and of V tiles, a TMA box a page, in one ring, in the
+//               order the MMAs take them
 //   warps 1, 2  the MMAs of streams 0 and 1: while one waits for its softmax the
 //               other keeps the tensor cores busy; warp 1 also has tensor memory
 //   warps 4-7   softmax and epilogue of stream 0, warps 8-11 of stream 1
@@ -159,53 +159,61 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     const uint32_t tmem = *tmem_slot;
     Segment s;
 
-    if (warp == 0) {
-        // ---------------------------------------------------------------- producer
+    if (warp == 0 || warp == 3) {
+        // ---------------------------------------------------------------- producers
+        // Warp 0 has the keys, warp 3 the values; a tile takes one of them 700
+        // cycles and more to ask for (a box a page, a wait, a barrier), so two.
+        const bool values = warp == 3;
+        const CUtensorMap *map = values ? &tm_v : &tm_k;
         const int box = min(1 << p.shift, kKeys);
         const int pages = kKeys / box;               // boxes of a tile, one a lane
-        int at = 0;                                  // position in the ring
+        const int my_page = lane < pages ? lane * box : 0;
+        int base = 0;                                // ring position of the segment's first tile
         bool ok = true;
 #ifdef AWQ_FAULT_TEST
         if (p.fault && blockIdx.x == 0) ok = false;
 #endif
+        uint32_t asked = 0, rounds = 0;              // slots this warp has filled, the parity of the last time
         while (ok && work.next(p, s)) {
             const int keys = s.ctx + s.n, nt = s.tile1 - s.tile0;
             const bool two = kRows > 128 && min(kRows, s.n * p.group - s.rb * kRows) > 128;
-            const int ahead = two ? 1 : 2;           // K tiles before the first V tile
-            auto load = [&](int j, Pages &ids, const CUtensorMap *map) {
-                const int key = (s.tile0 + j) * kKeys + (lane < pages ? lane * box : 0);
-                const int id = ids.block(p, key >> p.shift, lane);
-                const bool mine = lane < pages && key < keys;
+            const int ahead = min(nt, two ? 1 : 2);  // K tiles before the first V tile
+            Pages ids;
+            ids.open(p, s, (s.tile0 * kKeys) >> p.shift, lane);
+            for (int j = 0; j < nt; ++j) {
+                // the order of the MMAs: K 0 (K 1), then V j, K j + ahead
+                const int v_at = ahead + (values ? j : j - ahead) + min(values ? j : j - ahead, nt - ahead);
+                const int at = base + (values ? v_at : j < ahead ? j : v_at + 1);
                 const int slot = at % C::kSlots;
-                ok = ptx::mbar_wait_bounded(ptx::smem_addr(freed + slot), ((at / C::kSlots) & 1) ^ 1, abort_flag, p.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) return;
+                const int key = (s.tile0 + j) * kKeys + my_page;
+                const int id = ids.block(p, key >> p.shift, lane);
+                const bool there = lane < pages && key < keys;
+                const int count = __popc(__ballot_sync(0xFFFFFFFFu, there));
+                const uint32_t round = (uint32_t)(at / C::kSlots) & 1u;
+                ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait_bounded(ptx::smem_addr(freed + slot), round ^ 1u, abort_flag,
+                                                                    p.status));
+                if (!ok) break;
+                asked |= 1u << slot;
+                rounds = (rounds & ~(1u << slot)) | round << slot;
                 const uint32_t fb = ptx::smem_addr(full + slot);
-                const int count = __popc(__ballot_sync(0xFFFFFFFFu, mine));
                 if (lane == 0) ptx::mbar_arrive_expect_tx(fb, (uint32_t)count * C::kHalves * box * 128);
                 __syncwarp();
-                if (mine) {
-                    const uint32_t dst = ptx::smem_addr(smem + C::kQ + slot * C::kTile) + (uint32_t)lane * box * 128;
+                if (there) {
+                    const uint32_t dst = ptx::smem_addr(smem + C::kQ + slot * C::kTile) + (uint32_t)my_page * 128;
                     const int in_page = ((s.tile0 + j) * kKeys) & ((1 << p.shift) - 1) & ~(box - 1);
 #pragma unroll
                     for (int half = 0; half < C::kHalves; ++half)
                         ptx::tma_load_4d(dst + half * C::kHalf, map, fb, half * 64, s.h, in_page, id);
                 }
-                ++at;
-            };
-            // K 0 (K 1), then V j, K j + ahead: the order of the MMAs
-            Pages k_ids, v_ids;
-            k_ids.open(p, s, (s.tile0 * kKeys) >> p.shift, lane);
-            v_ids = k_ids;
-            for (int j = 0; j < min(ahead, nt) && ok; ++j) load(j, k_ids, &tm_k);
-            for (int j = 0; j < nt && ok; ++j) {
-                load(j, v_ids, &tm_v);
-                if (ok && j + ahead < nt) load(j + ahead, k_ids, &tm_k);
+                __syncwarp();
             }
+            base += 2 * nt;
         }
         if (!ok) {
-            for (int i = std::max(0, at - C::kSlots); i < at; ++i)
-                ptx::mbar_wait_bounded(ptx::smem_addr(full + i % C::kSlots), (i / C::kSlots) & 1, nullptr, nullptr);
+            // the warp's copies land before the shared memory goes
+            for (int i = 0; i < C::kSlots; ++i)
+                if ((asked >> i) & 1u)
+                    ptx::mbar_wait_bounded(ptx::smem_addr(full + i), (rounds >> i) & 1u, nullptr, nullptr);
         }
     } else if (warp == 1 || warp == 2) {
         // ---------------------------------------------------------------- MMAs
