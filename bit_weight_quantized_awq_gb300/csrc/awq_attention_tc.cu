@@ -47,7 +47,10 @@ namespace attn {
 namespace {
 
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kBlockCost = 2;    // a row block's beginning and end: as a tile of the heavier kind
+// A row block's beginning and end, in units: 6,000 to 9,000 cycles at 128 rows, where a
+// tile takes 1,900 and is one unit, and 20,000 at 256, where it takes 3,200 and is two.
+template <int kRows>
+constexpr int kBlockCost = kRows > 128 ? 16 : 3;
 // Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
 // in the time that a second kernel would take to join the pieces.
 constexpr int kWholeTiles = 8;
@@ -126,10 +129,6 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
     volatile int *odd_flag = abort_flag + 1;   // a drafted value of the segment is infinite or NaN
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    ptx::launch_dependents();
-    ptx::wait_prerequisites();
-    Work<kRows, kKeys, kBlockCost> work;
-    if (!work.template find<kThreads>(p)) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             ptx::mbar_init(ptx::smem_addr(full + i), 1);
@@ -154,9 +153,18 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         tc::tmem_relinquish();
         tc::fence_before_sync();
     }
+    // all that does not depend on the kernel before comes before this wait
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    Work<kRows, kKeys, kBlockCost<kRows>> work;
+    const bool works = work.template find<kThreads>(p);
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (!works) {
+        if (warp == 1) tc::tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
     Segment s;
 
     if (warp == 0 || warp == 3) {
@@ -393,7 +401,6 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(ptx::smem_addr(q_full));
-
             const int my_row = (two ? stream * 128 : 0) + row;            // of the block
             const bool warp_works = (two ? stream * 128 : 0) + quarter * 32 < rows;
             const int t = min(row0 + my_row, s.n * p.group - 1) / p.group;    // its token
@@ -660,8 +667,8 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
     const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
     p.whole = tiles <= kWholeTiles;
-    p.min_units = p.whole ? 1 : kBlockCost + 4;
-    const int64_t units = p.whole ? blocks : blocks * (kBlockCost + 2 * tiles);
+    p.min_units = p.whole ? 1 : kBlockCost<kRows> + 4;
+    const int64_t units = p.whole ? blocks : blocks * (kBlockCost<kRows> + (kRows > 128 ? 2 : 1) * tiles);
     const int ctas = lay_out(p, li.sms, units);
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
