@@ -203,7 +203,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.awq_kv_append.restype = _INT
         lib.awq_tree_attention.argtypes = [_P, _P]
         lib.awq_tree_attention.restype = _INT
-        lib.awq_reserve_tree_attention.argtypes = [_I64, _I64, _I64, _I64, _I64, _P]
+        lib.awq_reserve_tree_attention.argtypes = [_I64, _P]
         lib.awq_reserve_tree_attention.restype = _INT
         lib.awq_process_logits.argtypes = [_P, _P]
         lib.awq_process_logits.restype = _INT
@@ -321,8 +321,8 @@ def awq_tree_attention(args: TreeAttention, stream) -> int:
     return load_library().awq_tree_attention(_arg(args), stream)
 
 
-def awq_reserve_tree_attention(max_tokens, max_requests, q_heads, kv_heads, head_dim, stream) -> int:
-    return load_library().awq_reserve_tree_attention(max_tokens, max_requests, q_heads, kv_heads, head_dim, stream)
+def awq_reserve_tree_attention(head_dim, stream) -> int:
+    return load_library().awq_reserve_tree_attention(head_dim, stream)
 
 
 def awq_process_logits(args: Logits, stream) -> int:

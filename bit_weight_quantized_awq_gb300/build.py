@@ -6,7 +6,7 @@ only what is older than its sources (any header change rebuilds all units).
 
 It also builds ``_build/libawq_gb300_fault_test.so``, the fault-test build
 used only by the tests: the units with bounded device waits (the C ABI, the
-decode and prefill kernels) compiled again with ``-DAWQ_FAULT_TEST`` (a wait
+decode, prefill and attention kernels) compiled again with ``-DAWQ_FAULT_TEST`` (a wait
 limit of about 2 ms and the switch declared in
 ``include/awq_gb300_fault_test.h``), linked with the other units' objects.
 
@@ -30,7 +30,7 @@ LIB = os.path.join(BUILD, "libawq_gb300.so")
 FAULT_LIB = os.path.join(BUILD, "libawq_gb300_fault_test.so")
 FAULT_BUILD = os.path.join(BUILD, "fault_test")
 # units whose kernels wait on barriers or flags (and the ABI that sets the switch)
-FAULT_UNITS = ("awq_api.cu", "awq_decode.cu", "awq_prefill.cu")
+FAULT_UNITS = ("awq_api.cu", "awq_decode.cu", "awq_prefill.cu", "awq_attention.cu", "awq_attention_tc.cu")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

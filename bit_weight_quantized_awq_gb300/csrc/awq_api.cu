@@ -598,13 +598,9 @@ awq_status_t awq_reserve(int64_t max_M, int64_t max_K, int64_t max_N, unsigned f
     return AWQ_OK;
 }
 
-awq_status_t awq_reserve_tree_attention(int64_t max_tokens, int64_t max_requests, int64_t q_heads,
-                                        int64_t kv_heads, int64_t head_dim, awq_stream_t stream)
+awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream)
 {
-    if (max_tokens < 0 || max_requests < 0 || max_requests > 16384 || q_heads <= 0 || kv_heads <= 0 ||
-        q_heads % kv_heads != 0 || head_dim <= 0 || head_dim % 8 != 0 || head_dim > 256 ||
-        q_heads >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) || max_tokens * q_heads >= (int64_t(1) << 31))
-        return AWQ_ERR_INVALID_ARG;
+    if (head_dim <= 0 || head_dim % 8 != 0 || head_dim > 256) return AWQ_ERR_INVALID_ARG;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)

@@ -20,6 +20,8 @@
 // the counts: only the tokens in which the rows' paths differ are added or taken
 // back. Counts are whole numbers, so the atomics' order does not matter.
 #include <algorithm>
+#include <map>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -443,6 +445,24 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
     if (bad) raise_status(p.status, bad);
 }
 
+// The kernel's shared memory, allowed once a device.
+template <typename T>
+cudaError_t prepare()
+{
+    static std::mutex mu;
+    static std::map<int, unsigned> done;   // device -> cache generation
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned gen = cache_generation();
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = done.find(dev);
+    if (it != done.end() && it->second == gen) return cudaSuccess;
+    e = cudaFuncSetAttribute(process_logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem<T>);
+    if (e == cudaSuccess) done[dev] = gen;
+    return e;
+}
+
 template <typename T>
 cudaError_t launch(const awq_logits_t &a, cudaStream_t stream)
 {
@@ -455,7 +475,7 @@ cudaError_t launch(const awq_logits_t &a, cudaStream_t stream)
     const int64_t want = std::max<int64_t>(1, 152 * kPerSm<T> / ranges);
     p.rows_per_cta = (int)std::max<int64_t>((a.rows + want - 1) / want, (a.rows + 65534) / 65535);
     constexpr size_t smem = kSmem<T>;
-    cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = prepare<T>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ranges, (unsigned)((a.rows + p.rows_per_cta - 1) / p.rows_per_cta));

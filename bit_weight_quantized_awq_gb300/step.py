@@ -17,13 +17,13 @@ from typing import NamedTuple
 
 import torch
 
-from ._binding import AWQError, Status, awq_kv_append, awq_paged_plan, awq_process_logits, awq_tree_attention
+from ._binding import AWQError, DType, Status, awq_kv_append, awq_paged_plan, awq_process_logits, awq_tree_attention
 from ._binding import pack_cache, pack_logits, pack_tree_attention
 from .layer import _check, _stream
 
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
-_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}     # awq_dtype_t
-_CACHE_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_DTYPES = {torch.float16: int(DType.F16), torch.bfloat16: int(DType.BF16), torch.float32: int(DType.F32)}
+_CACHE_DTYPES = {torch.float16: int(DType.F16), torch.bfloat16: int(DType.BF16)}
 
 
 class PagedPlan(NamedTuple):

@@ -526,12 +526,13 @@ awq_status_t awq_tree_attention(const awq_tree_attention_t *args, awq_stream_t s
 
 /*
  * awq_reserve_tree_attention -- awq_reserve for awq_tree_attention: sizes the
- * scratch of `stream` for calls of up to max_tokens new tokens in max_requests
- * requests, and leaves it as it was reserved or not. A reserved stream refuses
- * calls beyond its reservations with AWQ_ERR_TOO_LARGE.
+ * scratch of `stream` for calls of this head_dim (or a smaller one of at most 64,
+ * 128 or 256 if this one is), whatever their lengths, so that they neither allocate
+ * nor synchronise. It leaves the stream as it was, reserved by awq_reserve or not;
+ * a reserved stream whose scratch is too small refuses calls with AWQ_ERR_TOO_LARGE.
+ * Allocates and synchronises `stream` itself: call it at set-up.
  */
-awq_status_t awq_reserve_tree_attention(int64_t max_tokens, int64_t max_requests, int64_t q_heads,
-                                        int64_t kv_heads, int64_t head_dim, awq_stream_t stream);
+awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream);
 
 /*
  * awq_process_logits -- penalties for repeated tokens, biases and a grammar mask

@@ -8,9 +8,9 @@
  * In the fault-test build every device-side wait gives up after about 4e6 SM
  * clock cycles (about 2 ms) instead of 4e9, and:
  *
- * awq_test_inject_fault(on) -- while `on` is non-zero, every decode and
- *   prefill kernel launched afterwards (awq_linear_forward and the calls built
- *   on it) has the TMA producer of its CTA 0 issue no copy. That CTA's
+ * awq_test_inject_fault(on) -- while `on` is non-zero, every decode, prefill
+ *   and tree-attention kernel launched afterwards (awq_linear_forward and the
+ *   calls built on it, awq_tree_attention) has the TMA producer of its CTA 0 issue no copy. That CTA's
  *   consumer warps then wait on a stage barrier that never fills; the waits
  *   run out, record AWQ_ERR_TIMEOUT in the device status word, and the
  *   kernel returns. Other CTAs that wait for CTA 0's partial sums give up the

@@ -448,7 +448,7 @@ def test_attention_in_a_graph_follows_the_lengths():
     first = Step([100, 7], [3, 2], 8, 2, 64, 16, torch.float16, "tree", seed=1)
     later = Step([333, 90], [2, 3], 8, 2, 64, 16, torch.float16, "tree", seed=2)
     stream = torch.cuda.Stream()
-    assert awq.awq_reserve_tree_attention(5, 2, 8, 2, 64, stream.cuda_stream) == Status.OK
+    assert awq.awq_reserve_tree_attention(64, stream.cuda_stream) == Status.OK
     with torch.cuda.stream(stream):
         width = later.table.shape[1]
         blocks = later.k.shape[0]
