@@ -7,8 +7,8 @@
 // thousand tokens against a hundred thousand logits, but most of them are the
 // frequent tokens, which lie close together. A CTA owns a range of vocabulary
 // entries and a run of rows. Eight warps count the tokens of a request's history
-// that fall into the range in shared memory and list the entries met; then, row by
-// row, the listed entries are changed, an entry a thread, so that their number
+// that fall into the range in shared memory, and who meets an entry first lists it;
+// then, row by row, the listed entries are changed, an entry a thread, so that their number
 // alone counts and not how they crowd, and 16 bytes at a time are masked and
 // stored. A ninth warp brings the rows in, two ahead: logits by bulk copies, and
 // beside them whatever the others would have to wait for -- grammar words, path
@@ -38,7 +38,14 @@ constexpr int kThreads = 256;             // of the eight working warps
 // vocabulary entries of a CTA: 16 KB of a row
 template <typename T>
 constexpr int kRange = 16384 / sizeof(T);
-constexpr unsigned kPrompt = 1u << 31;    // counter: in the prompt; below it the generated count
+// A counter: in the prompt, in the list of the entries met, and the generated count.
+constexpr unsigned kPrompt = 1u << 31, kListed = 1u << 30, kCount = kListed - 1;
+// Up to this many tokens of a lane are counted one by one, more of them all at once: 64
+// rows of 131072 fp32 logits with histories of up to 4,000 tokens took 27 us so; 30 us
+// all one by one, where a third of the tokens fell into one range; with the tokens
+// spread evenly 20 us, and 23 all at once.
+constexpr int kTurns = 4;
+constexpr int kPairs = 2;                 // biases a thread keeps
 
 struct LogitsParams {
     awq_logits_t a;
@@ -98,11 +105,11 @@ struct RowInfo {
 };
 
 // shared memory: the rows' logits, each behind one spare piece and with one after
-// it; the counts; bitmaps of the entries met and of those with a bias; the list of
-// the entries met; what comes with the rows
+// it; the counts; a bitmap of the entries with a bias; the list of the entries met;
+// what comes with the rows
 template <typename T>
 constexpr size_t kSmem = kStages * (kRange<T> * sizeof(T) + 32) +
-                         (kRange<T> + 2 * (kRange<T> / 32)) * sizeof(unsigned) + kRange<T> * sizeof(uint16_t) +
+                         (kRange<T> + kRange<T> / 32) * sizeof(unsigned) + kRange<T> * sizeof(uint16_t) +
                          kStages * sizeof(RowInfo<T>);
 
 // CTAs an SM has room for: two rows of 16 KB are on their way to each
@@ -124,8 +131,7 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
     __shared__ int listed;
     T *stage = reinterpret_cast<T *>(smem);        // [kStages][kStage]
     unsigned *counts = reinterpret_cast<unsigned *>(stage + kStages * kStage);   // [kRange]
-    unsigned *touched = counts + kRange;           // [kBitmap]
-    unsigned *biased = touched + kBitmap;          // [kBitmap]
+    unsigned *biased = counts + kRange;            // [kBitmap]
     uint16_t *list = reinterpret_cast<uint16_t *>(biased + kBitmap);   // [kRange]
     RowInfo<T> *infos = reinterpret_cast<RowInfo<T> *>(list + kRange);  // [kStages]
     const awq_logits_t &a = p.a;
@@ -248,36 +254,35 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
     }
 
     // ---------------------------------------------------------------- counts, changes, output
-    // counts a token of the range; whether it is the first to meet its entry
-    auto count_token = [&](int token, unsigned add) {
-        const int at = token - (int)v0;
-        if (at < 0 || at >= range) {
-            if (token >= (int)a.vocab) bad |= kStatusBadIndex;
-            return false;
-        }
-        if (add == kPrompt) atomicOr(counts + at, kPrompt);
-        else atomicAdd(counts + at, add);
-        const unsigned bit = 1u << (at & 31);
-        return !(atomicOr(touched + (at >> 5), bit) & bit);
+    // Counts a token at an entry of the range. Who meets an entry first lists it; its
+    // mark stays when the count goes back to zero, so that none is listed twice.
+    auto enlist = [&](int at) {
+        atomicOr(counts + at, kListed);
+        list[atomicAdd(&listed, 1)] = (uint16_t)at;
+    };
+    auto count_at = [&](int at, unsigned add) {
+        const unsigned was = add == kPrompt ? atomicOr(counts + at, kPrompt) : atomicAdd(counts + at, add);
+        if (was == 0) enlist(at);
     };
     auto clamp_offset = [&](int at, int64_t size) {
         if (at < 0 || at > size) bad |= kStatusBadIndex;
         return (int)min(max((int64_t)at, (int64_t)0), size);
     };
     // The entry in the range that pair i of the request's list begins, given its token
-    // and the one before it, and the sum of all its pairs; -1 if it begins none.
-    auto bias_entry = [&](int i, int token, int before, int end, float &sum) {
+    // and those beside it (-1: none), and the sum of all its pairs; -1 if it begins none.
+    auto bias_entry = [&](int i, int token, int before, int after, int end, float &sum) {
         const int at = token - (int)v0;
         if (at < 0 || at >= range || before == token) return -1;
-        for (int k = i + 1; k < end && a.bias_tokens[k] == token; ++k) sum += a.bias_values[k];
+        if (after == token)
+            for (int k = i + 1; k < end && a.bias_tokens[k] == token; ++k) sum += a.bias_values[k];
         return at;
     };
 
     int have = -2;                                 // request whose counts are held
     float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
     bool penal = false;                            // else counts change nothing
-    int my_bias = -1, more_lo = 0, more_hi = 0;    // the entry of this thread's bias; pairs past the threads'
-    float my_sum = 0.f;
+    int my_bias[kPairs], more_lo = 0, more_hi = 0; // the entries of this thread's biases; pairs past the threads'
+    float my_sum[kPairs];
     int64_t first = 0;                             // the request's first drafted token
     int my_token = -1;                             // its token number tid
     int64_t held = -1;                             // the row whose path is counted, if any
@@ -302,66 +307,104 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
             const int bias_hi = clamp_offset(info.bias_hi, a.bias_size);
             // the first tokens, the thread's pair of the biases and its drafted token
             // are on their way while the counts are cleared
-            constexpr int kBatch = 16;
+            constexpr int kBatch = 16, kHalf = kBatch / 2;
             int token[kBatch];
-            auto load = [&](int i0) {
+            auto load = [&](int i0, int at0, int at1) {
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) token[u] = i0 + u * kThreads < h_hi ? a.history[i0 + u * kThreads] : -1;
+                for (int u = 0; u < kBatch; ++u)
+                    if (u >= at0 && u < at1) token[u] = i0 + u * kThreads < h_hi ? a.history[i0 + u * kThreads] : -1;
             };
-            load(h_lo + tid);
-            int bias_token = -1, bias_before = -1;
-            if (bias_lo + tid < bias_hi) {
-                bias_token = a.bias_tokens[bias_lo + tid];
-                my_sum = a.bias_values[bias_lo + tid];
-                if (tid > 0) bias_before = a.bias_tokens[bias_lo + tid - 1];
+            load(h_lo + tid, 0, kHalf);
+            if (h_hi - h_lo > kHalf * kThreads) load(h_lo + tid, kHalf, kBatch);
+            int bias_token[kPairs], bias_before[kPairs], bias_after[kPairs];
+#pragma unroll
+            for (int u = 0; u < kPairs; ++u) {
+                const int i = bias_lo + u * kThreads + tid;
+                bias_token[u] = bias_before[u] = bias_after[u] = -1;
+                if (i < bias_hi) {
+                    bias_token[u] = a.bias_tokens[i];
+                    my_sum[u] = a.bias_values[i];
+                    if (i > bias_lo) bias_before[u] = a.bias_tokens[i - 1];
+                    if (i + 1 < bias_hi) bias_after[u] = a.bias_tokens[i + 1];
+                }
             }
             my_token = -1;
             if (penal && a.draft_tokens && first + tid >= 0 && first + tid < a.rows) my_token = a.draft_tokens[first + tid];
             held = -1;
             held_word = 0;
-            for (int i = tid; i < (kRange + 2 * kBitmap) / 4; i += kThreads)
+            for (int i = tid; i < (kRange + kBitmap) / 4; i += kThreads)
                 reinterpret_cast<uint4 *>(counts)[i] = make_uint4(0, 0, 0, 0);
             if (tid == 0) listed = 0;
             ptx::named_barrier(1, kThreads);
+            int most = -1;
             for (int i0 = h_lo; i0 < h_hi; i0 += kThreads * kBatch) {
-                if (i0 > h_lo) load(i0 + tid);
+                const bool more = h_hi - i0 > kHalf * kThreads;
+                if (i0 > h_lo) {
+                    load(i0 + tid, 0, kHalf);
+                    if (more) load(i0 + tid, kHalf, kBatch);
+                }
+                // the thread's tokens in the range
+                unsigned mine = 0;
+                auto look = [&](int at0, int at1) {
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u)
-                    count_token(token[u], i0 + tid + u * kThreads - h_lo < info.prompt ? kPrompt : 1u);
+                    for (int u = 0; u < kBatch; ++u)
+                        if (u >= at0 && u < at1) {
+                            most = max(most, token[u]);
+                            mine |= ((unsigned)token[u] - (unsigned)v0 < (unsigned)range ? 1u : 0u) << u;
+                        }
+                };
+                look(0, kHalf);
+                if (more) look(kHalf, kBatch);
+                const int in_prompt = info.prompt - (i0 - h_lo) - tid;    // the thread's token u: u * kThreads < this
+                if (__reduce_max_sync(0xFFFFFFFFu, __popc(mine)) > kTurns) {
+                    unsigned met = 0;
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        if ((mine >> u) & 1u) {
+                            unsigned *count = counts + (token[u] - (int)v0);
+                            const unsigned was = u * kThreads < in_prompt ? atomicOr(count, kPrompt) : atomicAdd(count, 1u);
+                            met |= (was == 0 ? 1u : 0u) << u;
+                        }
+                    int place = met ? atomicAdd(&listed, __popc(met)) : 0;
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        if ((met >> u) & 1u) {
+                            const int at = token[u] - (int)v0;
+                            atomicOr(counts + at, kListed);
+                            list[place++] = (uint16_t)at;
+                        }
+                } else {
+                    // few: one of them a turn, so that a warp takes as many turns as its
+                    // busiest lane has tokens; the token is in the L1 cache
+                    while (mine) {
+                        const int u = __ffs(mine) - 1;
+                        mine &= mine - 1;
+                        const int at = a.history[i0 + tid + u * kThreads] - (int)v0;
+                        if ((unsigned)at < (unsigned)range) count_at(at, u * kThreads < in_prompt ? kPrompt : 1u);
+                    }
+                }
             }
+            if (most >= (int)a.vocab) bad |= kStatusBadIndex;
             // the request's biases: the thread's own pair, and those past the threads'
             auto check = [&](int t, int before) {
                 if (t < 0 || before > t || t >= a.vocab) bad |= kStatusBadIndex;
             };
-            my_bias = -1;
-            if (bias_lo + tid < bias_hi) {
-                check(bias_token, bias_before);
-                my_bias = bias_entry(bias_lo + tid, bias_token, bias_before, bias_hi, my_sum);
+#pragma unroll
+            for (int u = 0; u < kPairs; ++u) {
+                const int i = bias_lo + u * kThreads + tid;
+                my_bias[u] = -1;
+                if (i >= bias_hi) continue;
+                check(bias_token[u], bias_before[u]);
+                const int at = bias_entry(i, bias_token[u], bias_before[u], bias_after[u], bias_hi, my_sum[u]);
+                if (at >= 0) atomicOr(biased + (at >> 5), 1u << (at & 31));
+                my_bias[u] = at;
             }
-            more_lo = bias_lo + kThreads;
+            more_lo = bias_lo + kPairs * kThreads;
             more_hi = bias_hi;
-            if (my_bias >= 0) atomicOr(biased + (my_bias >> 5), 1u << (my_bias & 31));
             for (int i = more_lo + tid; i < more_hi; i += kThreads) {
                 const int t = a.bias_tokens[i], at = t - (int)v0;
                 check(t, a.bias_tokens[i - 1]);
                 if (at >= 0 && at < range) atomicOr(biased + (at >> 5), 1u << (at & 31));
-            }
-            ptx::named_barrier(1, kThreads);
-            // the entries met, listed: a warp takes its words of the bitmap one by one,
-            // a bit a lane
-            constexpr int kWarpWords = kBitmap / (kThreads / 32);
-            const unsigned *words = touched + (tid >> 5) * kWarpWords;
-            const unsigned mine = lane < kWarpWords ? words[lane] : 0u;
-            int place = 0;
-            const int met = __reduce_add_sync(0xFFFFFFFFu, __popc(mine));
-            if (lane == 0 && met > 0) place = atomicAdd(&listed, met);
-            place = __shfl_sync(0xFFFFFFFFu, place, 0);
-#pragma unroll 4
-            for (int i = 0; i < kWarpWords; ++i) {
-                const unsigned w = __shfl_sync(0xFFFFFFFFu, mine, i);
-                if ((w >> lane) & 1u)
-                    list[place + __popc(w & ((1u << lane) - 1))] = (uint16_t)(((tid >> 5) * kWarpWords + i) * 32 + lane);
-                place += __popc(w);
             }
             ptx::named_barrier(1, kThreads);
         }
@@ -387,8 +430,9 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
                     continue;
                 }
                 const int token = j == tid ? my_token : a.draft_tokens[first + j];
-                if (token >= 0 && count_token(token, now ? 1u : 0xFFFFFFFFu))
-                    list[atomicAdd(&listed, 1)] = (uint16_t)(token - (int)v0);
+                if (token >= (int)a.vocab) bad |= kStatusBadIndex;
+                const int at = token - (int)v0;
+                if (at >= 0 && at < range) count_at(at, now ? 1u : 0xFFFFFFFFu);
             }
             held = r;
             held_word = my_word;
@@ -403,8 +447,8 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
         // ---- the entries that change
         auto change = [&](int at, float sum) {
             float x = to_f<T>(at0[at]);
-            const unsigned c = counts[at], times = c & ~kPrompt;
-            if (c) x *= x > 0.f ? inv : rep;
+            const unsigned c = counts[at], times = c & kCount;
+            if (c & ~kListed) x *= x > 0.f ? inv : rep;
             if (times) x = fmaf(-freq, (float)times, x) - pres;
             at0[at] = from_f<T>(x + sum);
         };
@@ -413,10 +457,13 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
             const int at = list[i];
             if (!((biased[at >> 5] >> (at & 31)) & 1u)) change(at, 0.f);
         }
-        if (my_bias >= 0) change(my_bias, my_sum);
+#pragma unroll
+        for (int u = 0; u < kPairs; ++u)
+            if (my_bias[u] >= 0) change(my_bias[u], my_sum[u]);
         for (int i = more_lo + tid; i < more_hi; i += kThreads) {
             float sum = a.bias_values[i];
-            const int at = bias_entry(i, a.bias_tokens[i], a.bias_tokens[i - 1], more_hi, sum);
+            const int token = a.bias_tokens[i];
+            const int at = bias_entry(i, token, a.bias_tokens[i - 1], token, more_hi, sum);
             if (at >= 0) change(at, sum);
         }
         ptx::named_barrier(1, kThreads);

@@ -119,6 +119,12 @@ def test_logits_invalid(kw):
     assert logits(**kw) == INVALID
 
 
+def test_logits_history_limit():
+    # a counter keeps a token's occurrences in 30 bits
+    assert logits(history=A, history_offsets=A, history_size=2 ** 29) == INVALID
+    assert logits(history=A, history_offsets=A, history_size=2 ** 29 - 1, rows=0) == OK
+
+
 def test_logits_misaligned_and_empty():
     assert logits(logits=A + 1, out=A + 4) == MISALIGNED
     assert logits(logits=A + 2, out=A + 4, dtype=2) == MISALIGNED
