@@ -52,6 +52,17 @@ def _length(t: torch.Tensor | None, name: str, n: int):
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
 
 
+def _pointer(t: torch.Tensor | None, name: str, dtype: torch.dtype, dev: torch.device, index: int, n: int | None) -> int:
+    """The data of a contiguous tensor of n elements (any number if None), 0 for none."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.get_device() != index or not t.is_contiguous() or (n is not None and t.numel() != n):
+        _check(t, name, dtype, dev)
+        if n is not None:
+            _length(t, name, n)
+    return t.data_ptr()
+
+
 def _table(t: torch.Tensor, requests: int, index: int) -> int:
     """The table's row stride."""
     if t.dtype != _I32 or t.get_device() != index or t.dim() != 2:
@@ -224,47 +235,41 @@ def process_logits(logits: torch.Tensor, row_request: torch.Tensor | None = None
         raise ValueError("logits must be [rows, vocab] with adjacent elements in a row")
     rows, vocab = logits.shape
     # the requests: the rows, or as many as the per-request tensors have
-    B = rows if row_request is None else None
-    pointers = {}
-
-    def take(name, t, dtype, length=None, per_request=None):
-        nonlocal B
-        if t is None:
-            pointers[name] = 0
-            return
-        if t.dtype != dtype or t.get_device() != at or not t.is_contiguous():
-            _check(t, name, dtype, dev)
-        if per_request is not None:
-            if B is None:
-                B = t.numel() - per_request
-            length = B + per_request
-        if length is not None and t.numel() != length:
-            _length(t, name, length)
-        pointers[name] = t.data_ptr()
-
-    take("repetition", repetition, _F32, per_request=0)
-    take("frequency", frequency, _F32, per_request=0)
-    take("presence", presence, _F32, per_request=0)
-    take("prompt_lens", prompt_lens, _I32, per_request=0)
-    take("history_offsets", history_offsets, _I32, per_request=1)
-    take("bias_offsets", bias_offsets, _I32, per_request=1)
-    take("cu_new", cu_new, _I32, per_request=1)
-    take("row_request", row_request, _I32, rows)
-    take("history", history, _I32)
-    take("draft_tokens", draft_tokens, _I32, rows)
-    take("tree_mask", tree_mask, _I32)
-    take("bias_tokens", bias_tokens, _I32)
-    take("grammar_mask", grammar_mask, _I32)
-    take("grammar_rows", grammar_rows, _I32, rows)
-    if B is None:
-        B = 2 ** 31 - 1      # nothing is indexed by a request
+    if row_request is None:
+        B = rows
+    else:
+        B = 2 ** 31 - 1      # if nothing is indexed by a request
+        for t, more in ((repetition, 0), (frequency, 0), (presence, 0), (prompt_lens, 0), (history_offsets, 1),
+                        (bias_offsets, 1), (cu_new, 1)):
+            if t is not None:
+                B = t.numel() - more
+                break
     if bias_tokens is not None and (bias_values is None or bias_offsets is None):
         raise ValueError("bias_tokens, bias_values and bias_offsets go together")
-    take("bias_values", bias_values, _F32, None if bias_tokens is None else bias_tokens.numel())
     if history is not None and history_offsets is None:
         raise ValueError("history needs history_offsets")
     if draft_tokens is not None and cu_new is None:
         raise ValueError("draft_tokens needs cu_new")
+    biases = None if bias_tokens is None else bias_tokens.numel()
+    pointers = (
+        _pointer(row_request, "row_request", _I32, dev, at, rows),
+        _pointer(history, "history", _I32, dev, at, None),
+        _pointer(history_offsets, "history_offsets", _I32, dev, at, B + 1),
+        _pointer(prompt_lens, "prompt_lens", _I32, dev, at, B),
+        0 if history is None else history.numel(),
+        _pointer(repetition, "repetition", _F32, dev, at, B),
+        _pointer(frequency, "frequency", _F32, dev, at, B),
+        _pointer(presence, "presence", _F32, dev, at, B),
+        _pointer(draft_tokens, "draft_tokens", _I32, dev, at, rows),
+        _pointer(cu_new, "cu_new", _I32, dev, at, B + 1),
+        _pointer(tree_mask, "tree_mask", _I32, dev, at, None))
+    lists = (
+        _pointer(bias_tokens, "bias_tokens", _I32, dev, at, None),
+        _pointer(bias_offsets, "bias_offsets", _I32, dev, at, B + 1),
+        _pointer(bias_values, "bias_values", _F32, dev, at, biases),
+        biases or 0,
+        _pointer(grammar_mask, "grammar_mask", _I32, dev, at, None),
+        _pointer(grammar_rows, "grammar_rows", _I32, dev, at, rows))
     words = masks = 0
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.shape[0] != rows:
@@ -280,13 +285,8 @@ def process_logits(logits: torch.Tensor, row_request: torch.Tensor | None = None
         if out.dtype != dtype or out.device != dev or out.shape != logits.shape or \
                 (out.stride(1) != 1 and vocab > 1):
             raise ValueError("out must be like logits, with adjacent elements in a row")
-    p = pointers
     args = pack_logits(logits.data_ptr(), out.data_ptr(), logits.stride(0) if rows > 1 else vocab,
-                       out.stride(0) if rows > 1 else vocab, rows, vocab, B, p["row_request"], p["history"],
-                       p["history_offsets"], p["prompt_lens"], 0 if history is None else history.numel(),
-                       p["repetition"], p["frequency"], p["presence"], p["draft_tokens"], p["cu_new"],
-                       p["tree_mask"], words, p["bias_tokens"], p["bias_offsets"], p["bias_values"],
-                       0 if bias_tokens is None else bias_tokens.numel(), p["grammar_mask"], p["grammar_rows"], masks,
+                       out.stride(0) if rows > 1 else vocab, rows, vocab, B, *pointers, words, *lists, masks,
                        _DTYPES[dtype])
     st = awq_process_logits(args, _stream(dev))
     if st != Status.OK:
