@@ -211,7 +211,7 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
                 mask_row = a.grammar_rows ? a.grammar_rows[r + 1] : r + 1;
             }
             if (b < 0 || b >= a.B) {
-                if (a.B > 0 || a.row_request) bad |= kStatusBadIndex;
+                if ((a.B > 0 || a.row_request) && (b != -1 || !a.row_request)) bad |= kStatusBadIndex;
                 b = -1;
             }
             if (m < 0 || m >= a.grammar_count) {

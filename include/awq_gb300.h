@@ -546,6 +546,8 @@ awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream);
  *   x = x + sum of bias_values of token v in b's list
  *   out[r, v] = x, or -inf if bit v of grammar_mask[grammar_rows[r], :] is 0
  *
+ *   row_request    int32 [rows] or NULL; -1 (awq_paged_plan's for rows past its tokens)
+ *                  has no request: neither penalties nor biases
  *   history        int32 tokens of all requests, request b's at history_offsets[b]
  *                  .. history_offsets[b + 1] - 1 (int32 [B + 1]), the first
  *                  prompt_lens[b] of them its prompt (NULL: all generated).

@@ -565,6 +565,27 @@ def test_logits_many_rows_of_few_requests(rows):
     close(awq.process_logits(s.x.cuda(), **kw), s.want(), s.x)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32])
+@pytest.mark.parametrize("vocab", [600, 40001])
+def test_logits_long_histories_and_many_biases(dtype, vocab):
+    """Several batches of tokens, many or few of them in a range, and biases past those a thread keeps."""
+    s = Rows([2, 1, 3], vocab, dtype, history=9000, bias=1300, seed=vocab)
+    close(awq.process_logits(s.x.cuda(), **s.arguments()), s.want(), s.x)
+
+
+def test_logits_rows_without_a_request():
+    """The rows that a plan has past its tokens: as they are, and not reported."""
+    s = Rows([2, 3], 5000, torch.bfloat16, grammar=False, seed=12)
+    kw, x = s.arguments(), torch.cat([s.x, s.x[:2]]).cuda()
+    for name, fill in (("row_request", -1), ("draft_tokens", 7), ("tree_mask", 1)):
+        kw[name] = torch.cat([kw[name], torch.full_like(kw[name][:2], fill)])
+    got = awq.process_logits(x, **kw)
+    close(got[:5], s.want(), s.x)
+    assert torch.equal(got[5:], x[5:])
+    torch.cuda.synchronize()
+    assert awq.awq_last_device_status(None) == Status.OK
+
+
 @pytest.mark.parametrize("kinds", [(), ("rep",), ("freq",), ("pres",), ("bias",), ("grammar",), ("draft",)])
 def test_logits_each_control_alone(kinds):
     s = Rows([2, 3], 9000, torch.float16, seed=4)
