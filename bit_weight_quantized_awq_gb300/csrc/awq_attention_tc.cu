@@ -27,6 +27,12 @@
 // head, then the tensor cores and, close to them, the exponentials (128 x 128 of
 // them a stream and tile).
 //
+// Measured: 12 requests with trees of 64 over up to 16384 keys, 64 / 8 heads of 128,
+// fp16: 221 to 238 us, half of the bf16 matrix rate (tensor pipe 59% busy: S in halves
+// of 64 keys reads q twice a tile); 16 requests with trees of 13 over up to 6000 keys,
+// bf16: 66 us, 59% of the copy bandwidth; a tree of 26 over 131072 keys, 32 / 8 heads
+// of 64: 56 us, 72%.
+//
 //   warps 0, 3  producers of K and of V tiles, a TMA box a page, in one ring, in the
 //               order the MMAs take them
 //   warps 1, 2  the MMAs of streams 0 and 1: while one waits for its softmax the
