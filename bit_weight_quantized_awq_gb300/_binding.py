@@ -9,12 +9,14 @@ from __future__ import annotations
 
 import ctypes
 import enum
+import importlib.metadata
 import os
-import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libawq_gb300.so")
+# the module behind step.py, for the torch that is installed
+STEP_PATH = os.path.join(os.path.dirname(LIB_PATH), f"awq_step-{importlib.metadata.version('torch')}.so")
 
 # Every function the header declares; tests check the library exports them.
 EXPORTED = (
@@ -115,28 +117,9 @@ class Logits(ctypes.Structure):
                 ("dtype", _I32)]
 
 
-def _packer(structure):
-    """Packs a structure's fields, in order (a nested structure's one after another),
-    into bytes that are passed for a pointer to it: a third of the time that
-    filling the structure takes."""
-    codes = {_P: "P", _I64: "q", _I32: "i", ctypes.c_float: "f"}
-
-    def code(s):
-        return "".join(codes[t] if t in codes else code(t) for _, t in s._fields_)
-
-    layout = struct.Struct("@" + code(structure) + "0P")     # padded to a pointer's alignment, as C does
-    assert layout.size == ctypes.sizeof(structure)
-    return layout.pack
-
-
-pack_cache = _packer(Cache)
-pack_tree_attention = _packer(TreeAttention)
-pack_logits = _packer(Logits)
-
-
 def _arg(value):
-    """A structure or its packed bytes, as a pointer argument."""
-    return value if value is None or isinstance(value, bytes) else ctypes.byref(value)
+    """A structure as a pointer argument."""
+    return None if value is None else ctypes.byref(value)
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:

@@ -10,16 +10,23 @@ decode, prefill and attention kernels) compiled again with ``-DAWQ_FAULT_TEST`` 
 limit of about 2 ms and the switch declared in
 ``include/awq_gb300_fault_test.h``), linked with the other units' objects.
 
+And ``_build/awq_step-<torch version>.so``, the Python module behind ``step.py``
+(``csrc/awq_step_module.cpp``, compiled with the host compiler against the
+installed torch).
+
     python -m bit_weight_quantized_awq_gb300.build [--force] [--ptxas-verbose]
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -32,6 +39,8 @@ FAULT_BUILD = os.path.join(BUILD, "fault_test")
 # units whose kernels wait on barriers or flags (and the ABI that sets the switch)
 FAULT_UNITS = ("awq_api.cu", "awq_decode.cu", "awq_prefill.cu", "awq_attention.cu", "awq_attention_tc.cu")
 INCLUDE = os.path.join(ROOT, "include")
+STEP_SOURCE = os.path.join(CSRC, "awq_step_module.cpp")
+STEP_MODULE = os.path.join(BUILD, f"awq_step-{importlib.metadata.version('torch')}.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -65,6 +74,19 @@ def _fault_obj(src: str) -> str:
     return os.path.join(FAULT_BUILD, os.path.basename(src)[:-3] + ".o")
 
 
+def _step_command(out: str) -> list[str]:
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found: the AWQ step module needs a host compiler to build")
+    include = [sysconfig.get_paths()["include"], INCLUDE, os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    # torch has loaded its libraries by the time that the module is
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{d}" for d in include), STEP_SOURCE, "-o", out,
+            "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(FAULT_BUILD, exist_ok=True)
@@ -82,6 +104,10 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
             if force or _stale(fobj, [src] + headers + [os.path.abspath(__file__)]):
                 jobs.append((src + " (fault test)", [cc] + ARCH + NVCC_FLAGS + ["-DAWQ_FAULT_TEST", "-c", src,
                                                                                "-o", fobj]))
+    library_jobs = bool(jobs)
+    step_tmp = STEP_MODULE + f".tmp{os.getpid()}"
+    if force or _stale(STEP_MODULE, [STEP_SOURCE, os.path.join(INCLUDE, "awq_gb300.h"), os.path.abspath(__file__)]):
+        jobs.append((STEP_SOURCE, _step_command(step_tmp)))
     objs = [os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in _sources()]
     fault_objs = [_fault_obj(s) if os.path.basename(s) in FAULT_UNITS else
                   os.path.join(BUILD, os.path.basename(s)[:-3] + ".o") for s in _sources()]
@@ -101,9 +127,11 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = False)
                     sys.stderr.write(r.stderr)
     if failed:
         msg = "\n".join(f"--- {s}\n{e}" for s, e in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
+    if os.path.exists(step_tmp):
+        os.replace(step_tmp, STEP_MODULE)
     for lib, lib_objs in ((LIB, objs), (FAULT_LIB, fault_objs)):
-        if force or jobs or _stale(lib, lib_objs):
+        if force or library_jobs or _stale(lib, lib_objs):
             tmp = lib + f".tmp{os.getpid()}"
             cmd = [cc] + ARCH + ["-shared", "-o", tmp] + lib_objs
             r = subprocess.run(cmd, capture_output=True, text=True)
