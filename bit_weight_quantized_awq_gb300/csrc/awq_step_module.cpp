@@ -191,10 +191,21 @@ PyObject *paged_plan(PyObject *const *o)
     const int32_t *parents = checked<int32_t>(o[6], "parents", at::kInt, dev, T);
     int64_t width, stride;
     check_table(table, B, dev, width, stride);
-    const auto ints = at::TensorOptions(at::kCUDA, (c10::DeviceIndex)dev).dtype(at::kInt);
-    Tensor cu = at::empty({B + 1}, ints), slots = at::empty({T}, ints.dtype(at::kLong)), positions = at::empty({T}, ints);
-    Tensor request = at::empty({T}, ints), counts = at::empty({2}, ints), mask;
-    if (words > 0) mask = at::empty({T, words}, ints);
+    // one allocation for all (six took 6 us of 10); the 64-bit numbers come first
+    const Tensor area = at::empty({2 * T + (B + 1) + 2 * T + 2 + T * words},
+                                  at::TensorOptions(at::kCUDA, (c10::DeviceIndex)dev).dtype(at::kInt));
+    int64_t used = 0;
+    auto take = [&](at::ScalarType type, at::IntArrayRef sizes) {
+        Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(area.storage()),
+                                                            area.key_set(), c10::scalarTypeToTypeMeta(type));
+        t.unsafeGetTensorImpl()->set_storage_offset(used);     // in elements: the 64-bit ones have 0
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+        used += t.numel() * (type == at::kLong ? 2 : 1);
+        return t;
+    };
+    Tensor slots = take(at::kLong, {T}), cu = take(at::kInt, {B + 1}), positions = take(at::kInt, {T});
+    Tensor request = take(at::kInt, {T}), counts = take(at::kInt, {2}), mask;
+    if (words > 0) mask = take(at::kInt, {T, words});
     const awq_stream_t stream = stream_of(dev);
     const int status = call([&] {
         return plan_entry(data<int32_t>(&ctx), data<int32_t>(&fresh), B, data<int32_t>(&table), width, stride,

@@ -42,7 +42,7 @@ def _load():
 
 
 class PagedPlan(NamedTuple):
-    """What ``paged_plan`` lays out for a step (all on the device)."""
+    """What ``paged_plan`` lays out for a step (all on the device, in one allocation)."""
     cu_new: torch.Tensor          # int32 [B + 1]
     slot_map: torch.Tensor        # int64 [max_tokens]
     positions: torch.Tensor       # int32 [max_tokens]
