@@ -23,7 +23,7 @@
 // seven eighths padding and its operands and accumulators would take the detour over
 // shared and tensor memory.
 // Measured: 64 requests of up to 8192 tokens, 64 / 8 heads of 128, fp16: 197 us, 95%
-// of the copy bandwidth; one request of 500 tokens, 32 heads of 128: 11.4 us.
+// of the copy bandwidth; one request of 500 tokens, 32 heads of 128: 9.4 us.
 #include <algorithm>
 #include <cstring>
 #include <map>
@@ -45,6 +45,14 @@ constexpr int kBlockCost = 2;    // a row block's beginning and end, in tiles
 // Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
 // in the time that a second kernel would take to join the pieces.
 constexpr int kWholeTiles = 32;
+// Few row blocks are shared by the CTAs of a cluster (up to kMaxShare = 2^kShareLog, as
+// many as leave each kShareTiles tiles and find an SM): one token, 32 heads of 128 over
+// 500 keys took 9.4 us so and 11.5 without, over 1,000 keys 10.7 and 16.5; with two
+// tiles a CTA, 100 keys and 8 heads took 8.8 instead of 7.2. Beyond kSharedTiles a CTA the
+// split and join of the whole GPU is faster: 8 heads over 4,000 keys (16 tiles) 13.2 us
+// shared and 12.9 split, over 8,000 keys 19.7 and 14.7.
+constexpr int kShareLog = 3, kMaxShare = 1 << kShareLog;
+constexpr int kShareTiles = 4, kSharedTiles = 16;
 constexpr int kWarps = 3;        // consumer warps
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
@@ -99,8 +107,19 @@ struct Layout {
     }
 };
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
+// Tiles of a segment that CTA `rank` of a cluster of 2^share has.
+__device__ __forceinline__ void share_of(Segment &s, int share, int rank)
+{
+    const int n = s.tile1 - s.tile0;
+    s.tile1 = s.tile0 + ((n * (rank + 1)) >> share);
+    s.tile0 += (n * rank) >> share;
+}
+
+// kShared: a cluster has each row block, its CTAs a part of the keys each (few short
+// row blocks, which would leave most of the GPU idle). They leave m, l and O in shared
+// memory, where all of them read their part of the columns.
+template <typename T, int DP, bool kShared>
+__global__ void __launch_bounds__(kThreads, DP <= 128 && !kShared ? 2 : 1)
 attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ Params p)
 {
@@ -125,6 +144,16 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     Work<kRows, kKeys, kBlockCost> work;
     if (!work.template find<kThreads>(p)) return;   // its barriers also publish the mbarriers
     Segment s;
+    const int rank = kShared ? ptx::cluster_rank() : 0;
+    // Every thread of a cluster, a segment: all CTAs have left their part; whether each
+    // of them has.
+    auto parts_left = [&] {
+        ptx::cluster_sync();
+        int gave_up = 0;
+        for (int r = 0; r < 1 << p.share; ++r)
+            gave_up |= __float_as_int(ptx::cluster_load(ptx::cluster_addr(ptx::smem_addr(const_cast<int *>(abort_flag)), r)));
+        return gave_up == 0;
+    };
     const int box = min(1 << p.shift, kKeys);                // keys of one TMA box
     const Layout lay{(uint32_t)box * 128, box < kKeys ? (C::kHalves - 1) * 16u * 128u : 0u};
 
@@ -143,11 +172,12 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 #ifdef AWQ_FAULT_TEST
         if (p.fault && blockIdx.x == 0) ok = false;
 #endif
-        while (ok && work.next(p, s)) {
+        while ((ok || kShared) && work.next(p, s)) {
+            if (kShared) share_of(s, p.share, rank);
             const int keys = s.ctx + s.n;
             Pages ids;
             ids.open(p, s, (s.tile0 * kKeys) >> p.shift, lane);
-            for (int tile = s.tile0; tile < s.tile1; ++tile, ++it) {
+            for (int tile = s.tile0; tile < s.tile1 && ok; ++tile, ++it) {
                 const int key = tile * kKeys + (page < pages ? page * box : 0);
                 const int id = ids.block(p, key >> p.shift, lane);
                 const bool mine = page < pages && key < keys;
@@ -162,6 +192,14 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 if (mine)
                     ptx::tma_load_5d(ptx::smem_addr(smem + st * 2 * C::kTile) + to, map, fb, half * 64,
                                      (tile * kKeys) & ((1 << p.shift) - 1), 0, s.h, id);
+            }
+            if (kShared) {
+                const bool all = parts_left();
+                ptx::cluster_sync();
+                if (!all) {
+                    ok = false;
+                    break;
+                }
             }
         }
         if (!ok) {
@@ -179,6 +217,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     int base = 0;                    // tiles of the segments before
     bool ok = true;
     while (work.next(p, s)) {
+        if (kShared) share_of(s, p.share, rank);
         const int all_rows = s.n * p.group, row0 = s.rb * kRows;
         const int rows = min(kRows, all_rows - row0);
         // this lane's rows g and g + 8 (the last row again where they do not exist)
@@ -373,7 +412,13 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             warp_l[warp * kRows + g + 8] = lb;
         }
         // all leave together if one gave up
-        if (!ptx::named_barrier_and(1, kConsumers, ok)) return;
+        if (!ptx::named_barrier_and(1, kConsumers, ok)) {
+            if (kShared) {           // abort_flag is set: the others of the cluster leave too
+                parts_left();
+                ptx::cluster_sync();
+            }
+            return;
+        }
         float m2a = -INFINITY, m2b = -INFINITY, l2a = 0.f, l2b = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -412,7 +457,52 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 }
             ptx::named_barrier(1, kConsumers);
         }
-        if (s.whole()) {
+        if (kShared) {
+            // this CTA's part, then the columns that it joins
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) mine[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                if (t4 == 0) {
+                    warp_m[g] = m2a;
+                    warp_m[g + 8] = m2b;
+                    warp_l[g] = l2a;
+                    warp_l[g + 8] = l2b;
+                }
+            }
+            const bool all = parts_left();
+            const int parts = 1 << p.share, columns = DP >> p.share;
+            for (int e = threadIdx.x; all && e < rows * (columns / 2); e += kConsumers) {
+                const int r = e / (columns / 2), c = rank * columns + e % (columns / 2) * 2;
+                const uint32_t at_m = ptx::smem_addr(warp_m + r), at_l = ptx::smem_addr(warp_l + r);
+                // columns c and c + 1 of row r, where warp 0 has them
+                const uint32_t at_o = ptx::smem_addr(merge + ((c >> 3) * 32 + (r & 7) * 4 + ((c & 7) >> 1)) * 4 + (r >> 3) * 2);
+                float m[kMaxShare], l = 0.f, top = -INFINITY;
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < kMaxShare; ++i) {
+                    m[i] = i < parts ? ptx::cluster_load(ptx::cluster_addr(at_m, i)) : -INFINITY;
+                    top = fmaxf(top, m[i]);
+                }
+                const float mm = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                for (int i = 0; i < kMaxShare; ++i)
+                    if (i < parts) {
+                        const float f = exp2_fast(m[i] - mm);
+                        const float2 v = ptx::cluster_load2(ptx::cluster_addr(at_o, i));
+                        l += ptx::cluster_load(ptx::cluster_addr(at_l, i)) * f;
+                        sum.x += v.x * f;
+                        sum.y += v.y * f;
+                    }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t t = s.token0 + (row0 + r) / p.group, head = (int64_t)s.h * p.group + (row0 + r) % p.group;
+                if (c < p.head_dim)
+                    *reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (t * p.q_heads + head) * p.head_dim + c) =
+                        Elem<T>::pack(sum.x * inv, sum.y * inv);
+                if (c == 0) store_lse(p, s.token0, s.h, row0 + r, mm, l);
+            }
+            ptx::cluster_sync();
+            if (!all) return;
+        } else if (s.whole()) {
             if (warp == 0) {
                 const float ia = l2a == 0.f ? 0.f : 1.f / l2a, ib = l2b == 0.f ? 0.f : 1.f / l2b;
 #pragma unroll
@@ -453,12 +543,12 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 }
 
 struct LaunchInfo {
-    int ctas = 0;            // CTAs that fit the GPU at once
+    int sms = 0, ctas = 0;   // CTAs that fit the GPU at once
     cudaError_t err = cudaSuccess;
     unsigned gen = 0;
 };
 
-template <typename T, int DP>
+template <typename T, int DP, bool kShared>
 LaunchInfo launch_info()
 {
     static std::mutex mu;
@@ -473,12 +563,13 @@ LaunchInfo launch_info()
     if (it != cache.end() && it->second.gen == gen) return it->second;
     li.gen = gen;
     int sms = 0, per_sm = 0;
-    li.err = cudaFuncSetAttribute(attention_rows_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    li.err = cudaFuncSetAttribute(attention_rows_kernel<T, DP, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   Cfg<DP>::kSmem);
     if (li.err == cudaSuccess) li.err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (li.err == cudaSuccess)
-        li.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_rows_kernel<T, DP>, kThreads,
+        li.err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_rows_kernel<T, DP, kShared>, kThreads,
                                                                Cfg<DP>::kSmem);
+    li.sms = sms;
     li.ctas = sms * std::max(1, per_sm);
     if (li.err == cudaSuccess) cache[dev] = li;
     return li;
@@ -487,7 +578,7 @@ LaunchInfo launch_info()
 template <typename T, int DP>
 cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
 {
-    const LaunchInfo li = launch_info<T, DP>();
+    const LaunchInfo li = launch_info<T, DP, false>();
     if (li.err != cudaSuccess) return li.err;
     Params p = make_params(a);
     CUtensorMap tk, tv;
@@ -498,14 +589,24 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
     const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
-    p.whole = tiles <= kWholeTiles;
+    int share = 0;
+    while (blocks > 0 && share < kShareLog && (blocks << (share + 1)) <= li.sms && (tiles >> (share + 1)) >= kShareTiles) ++share;
+    p.whole = tiles <= (share > 0 ? (int64_t)kSharedTiles << share : kWholeTiles);
     p.min_units = p.whole ? 1 : kBlockCost + 8;
     const int64_t units = p.whole ? blocks : blocks * (kBlockCost + tiles);
-    const int ctas = lay_out(p, li.ctas, units);
 #ifdef AWQ_FAULT_TEST
     p.fault = fault_injection();
 #endif
-    return launch_pair<T, kRows, DP>(attention_rows_kernel<T, DP>, ctas, kThreads, Cfg<DP>::kSmem, stream, tk, tv, p);
+    if (p.whole) p.share = share;
+    if (p.share > 0) {
+        const LaunchInfo shared = launch_info<T, DP, true>();
+        if (shared.err != cudaSuccess) return shared.err;
+        p.lines = 1;
+        return launch_pair<T, kRows, DP>(attention_rows_kernel<T, DP, true>, (int)blocks << p.share, kThreads, Cfg<DP>::kSmem,
+                                         stream, tk, tv, p);
+    }
+    const int ctas = lay_out(p, li.ctas, units);
+    return launch_pair<T, kRows, DP>(attention_rows_kernel<T, DP, false>, ctas, kThreads, Cfg<DP>::kSmem, stream, tk, tv, p);
 }
 
 } // namespace

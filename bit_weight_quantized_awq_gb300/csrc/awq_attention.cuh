@@ -24,6 +24,9 @@
 // the pieces in the order of the CTAs, so the sum's order is the same in every
 // call, and no CTA ever waits for another. (Joined by whichever CTA came last the
 // pieces took 10 to 20 us at 256 rows: one CTA's loads, behind a fence.)
+//
+// Where the bounds allow only a few row blocks of few tiles, none is cut: a CTA has
+// each, or (few-row kernel) a cluster, whose CTAs join their parts through shared memory.
 #pragma once
 
 #include <algorithm>
@@ -64,6 +67,7 @@ struct Params {
     int shift;              // log2 of the block size
     int min_units;          // a CTA takes at least this many units: one tile at least
     int whole;              // row blocks are not split: one unit each, and nothing to join
+    int share;              // log2 of the CTAs (a cluster) that share each row block; 0 unless whole
     int lines;              // 1, or kv_heads: lines of work, one a key-value head (see Work)
     float scale_log2;       // scale * log2(e): scores are kept in powers of two
 #ifdef AWQ_FAULT_TEST
@@ -151,7 +155,7 @@ struct Work {
         if (tid == 0) p.joins[blockIdx.x].valid = 0;
         heads = p.lines == 1 ? p.kv_heads : 1;
         head0 = p.lines == 1 ? 0 : blockIdx.x % p.lines;
-        cta = blockIdx.x / p.lines;
+        cta = (blockIdx.x >> p.share) / p.lines;
         const int per = (p.B + THREADS - 1) / THREADS;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
         int64_t mine = 0, units0 = 0;          // of the thread's requests, and of the first of them
@@ -191,7 +195,7 @@ struct Work {
         }
         before += su - mine;
         if (units == 0) return false;
-        ctas = (int)min((int64_t)(gridDim.x / p.lines), max((int64_t)1, quotient(units, p.min_units)));
+        ctas = (int)min((int64_t)((gridDim.x >> p.share) / p.lines), max((int64_t)1, quotient(units, p.min_units)));
         if (cta >= ctas) return false;
         pos = begin_of(cta);
         end = begin_of(cta + 1);
@@ -578,11 +582,14 @@ cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t 
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1u << p.share;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = p.share > 0 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
     if (e != cudaSuccess) return e;
     if (ctas > 1 && !p.whole) {

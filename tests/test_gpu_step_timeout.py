@@ -26,10 +26,20 @@ def flib(gpu):
     lib.awq_test_inject_fault(0)
 
 
+@pytest.mark.parametrize("ctx,new,dim", [(500, 1, 128), (900, 1, 256), (300, 2, 64)])
+def test_wait_of_a_cluster_runs_out_then_next_calls_are_right(flib, ctx, new, dim):
+    """Short row blocks, which the CTAs of a cluster share: all of them leave."""
+    _runs_out(flib, ctx, new, dim)
+
+
 @pytest.mark.parametrize("new,dim", [(1, 128), (1, 256), (12, 64), (40, 128), (80, 128)])
 def test_wait_runs_out_then_next_calls_are_right(flib, new, dim):
+    _runs_out(flib, 2001, new, dim)
+
+
+def _runs_out(flib, ctx, new, dim):
     gen = torch.Generator().manual_seed(new + dim)
-    ctx, page = 2001, 32
+    page = 32
     blocks = -(-(ctx + new) // page)
     q = torch.randn((new, 8, dim), generator=gen).half()
     k, v = (torch.randn((blocks, page, 2, dim), generator=gen).half() for _ in range(2))
