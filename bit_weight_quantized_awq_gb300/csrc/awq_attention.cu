@@ -23,7 +23,7 @@
 // seven eighths padding and its operands and accumulators would take the detour over
 // shared and tensor memory.
 // Measured: 64 requests of up to 8192 tokens, 64 / 8 heads of 128, fp16: 197 us, 95%
-// of the copy bandwidth; one request of 500 tokens, 32 heads of 128: 9.4 us.
+// of the copy bandwidth; one request of 500 tokens, 32 heads of 128: 10.1 us.
 #include <algorithm>
 #include <cstring>
 #include <map>
@@ -45,14 +45,14 @@ constexpr int kBlockCost = 2;    // a row block's beginning and end, in tiles
 // Row blocks of up to this many tiles are not split: a CTA reads them (1,024 keys)
 // in the time that a second kernel would take to join the pieces.
 constexpr int kWholeTiles = 32;
-// Few row blocks are shared by the CTAs of a cluster (up to kMaxShare = 2^kShareLog, as
-// many as leave each kShareTiles tiles and find an SM): one token, 32 heads of 128 over
-// 500 keys took 9.4 us so and 11.5 without, over 1,000 keys 10.7 and 16.5; with two
-// tiles a CTA, 100 keys and 8 heads took 8.8 instead of 7.2. Beyond kSharedTiles a CTA the
-// split and join of the whole GPU is faster: 8 heads over 4,000 keys (16 tiles) 13.2 us
-// shared and 12.9 split, over 8,000 keys 19.7 and 14.7.
+// Few row blocks are shared by the CTAs of a cluster, as many (up to kMaxShare) as find
+// room on the GPU and have kShareTiles tiles each: one token, 32 heads of 128 over 1,000
+// keys took 10.5 us so and 16.5 without, 4 tokens of 64 / 8 heads over 400 keys 10.4 and
+// 12.9; with two tiles a CTA, 4 tokens over 100 keys 9.5 instead of 8.0. Beyond
+// kSharedTiles a CTA the split and join of the whole GPU is faster: 8 heads over 4,000
+// keys (16 tiles) 13.2 us shared and 12.9 split, over 8,000 keys 19.7 and 14.7.
 constexpr int kShareLog = 3, kMaxShare = 1 << kShareLog;
-constexpr int kShareTiles = 4, kSharedTiles = 16;
+constexpr int kShareTiles = 3, kSharedTiles = 16;
 constexpr int kWarps = 3;        // consumer warps
 constexpr int kConsumers = kWarps * 32;
 constexpr int kThreads = kConsumers + 32;
@@ -113,6 +113,74 @@ __device__ __forceinline__ void share_of(Segment &s, int share, int rank)
     const int n = s.tile1 - s.tile0;
     s.tile1 = s.tile0 + ((n * (rank + 1)) >> share);
     s.tile0 += (n * rank) >> share;
+}
+
+// Joins the parts that the CTAs of a cluster have left: at `pairs` m and l of the rows,
+// at `parts_o` O as the lanes of warp 0 had it. CTA `rank` does its part of the columns,
+// eight a warp and turn; a lane has rows g and g + 8. (A function of its own: inlined, its
+// registers were missing in the loop over the tiles at head_dim 256.)
+template <typename T, int DP>
+__device__ __noinline__ void join_shared(const Params &p, const Segment &s, uint32_t pairs, uint32_t parts_o, int rank,
+                                         int row0, int rows)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+    const int parts = 1 << p.share, turns = (DP / 8) >> p.share;
+    if (g >= rows) return;
+    float fa[kMaxShare], fb[kMaxShare], ka[kMaxShare], kb[kMaxShare];
+#pragma unroll
+    for (int i = 0; i < kMaxShare; ++i) {
+        float2 a = make_float2(-INFINITY, 0.f), b = a;
+        if (i < parts) {
+            a = ptx::cluster_load2(ptx::cluster_addr(pairs + g * 8, i));
+            b = ptx::cluster_load2(ptx::cluster_addr(pairs + (g + 8) * 8, i));
+        }
+        fa[i] = a.x;
+        ka[i] = a.y;
+        fb[i] = b.x;
+        kb[i] = b.y;
+    }
+    float top_a = -INFINITY, top_b = -INFINITY, sum_a = 0.f, sum_b = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxShare; ++i) {
+        top_a = fmaxf(top_a, fa[i]);
+        top_b = fmaxf(top_b, fb[i]);
+    }
+    const float za = top_a == -INFINITY ? 0.f : top_a, zb = top_b == -INFINITY ? 0.f : top_b;
+#pragma unroll
+    for (int i = 0; i < kMaxShare; ++i) {
+        fa[i] = exp2_fast(fa[i] - za);
+        fb[i] = exp2_fast(fb[i] - zb);
+        sum_a = fmaf(ka[i], fa[i], sum_a);
+        sum_b = fmaf(kb[i], fb[i], sum_b);
+    }
+    const float ia = sum_a == 0.f ? 0.f : 1.f / sum_a, ib = sum_b == 0.f ? 0.f : 1.f / sum_b;
+    auto out_of = [&](int r) {
+        const int64_t t = s.token0 + (row0 + r) / p.group, head = (int64_t)s.h * p.group + (row0 + r) % p.group;
+        return static_cast<T *>(p.out) + (t * p.q_heads + head) * p.head_dim + t4 * 2;
+    };
+    T *out_a = out_of(g), *out_b = out_of(g + 8);
+    for (int k = warp; k < turns; k += kWarps) {
+        const int i = rank * turns + k;
+        if (i * 8 >= p.head_dim) break;
+        float4 v[kMaxShare], x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kMaxShare; ++j)
+            if (j < parts) v[j] = ptx::cluster_load4(ptx::cluster_addr(parts_o + (i * 32 + lane) * 16, j));
+#pragma unroll
+        for (int j = 0; j < kMaxShare; ++j)
+            if (j < parts) {
+                x.x += v[j].x * fa[j];
+                x.y += v[j].y * fa[j];
+                x.z += v[j].z * fb[j];
+                x.w += v[j].w * fb[j];
+            }
+        *reinterpret_cast<uint32_t *>(out_a + i * 8) = Elem<T>::pack(x.x * ia, x.y * ia);
+        if (g + 8 < rows) *reinterpret_cast<uint32_t *>(out_b + i * 8) = Elem<T>::pack(x.z * ib, x.w * ib);
+    }
+    if (rank == 0 && warp == 0 && t4 == 0) {
+        store_lse(p, s.token0, s.h, row0 + g, za, sum_a);
+        if (g + 8 < rows) store_lse(p, s.token0, s.h, row0 + g + 8, zb, sum_b);
+    }
 }
 
 // kShared: a cluster has each row block, its CTAs a part of the keys each (few short
@@ -459,47 +527,17 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         }
         if (kShared) {
             // this CTA's part, then the columns that it joins
+            float2 *pairs = reinterpret_cast<float2 *>(warp_m);     // m and l of the rows
             if (warp == 0) {
 #pragma unroll
                 for (int i = 0; i < DP / 8; ++i) mine[i * 32] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 if (t4 == 0) {
-                    warp_m[g] = m2a;
-                    warp_m[g + 8] = m2b;
-                    warp_l[g] = l2a;
-                    warp_l[g + 8] = l2b;
+                    pairs[g] = make_float2(m2a, l2a);
+                    pairs[g + 8] = make_float2(m2b, l2b);
                 }
             }
             const bool all = parts_left();
-            const int parts = 1 << p.share, columns = DP >> p.share;
-            for (int e = threadIdx.x; all && e < rows * (columns / 2); e += kConsumers) {
-                const int r = e / (columns / 2), c = rank * columns + e % (columns / 2) * 2;
-                const uint32_t at_m = ptx::smem_addr(warp_m + r), at_l = ptx::smem_addr(warp_l + r);
-                // columns c and c + 1 of row r, where warp 0 has them
-                const uint32_t at_o = ptx::smem_addr(merge + ((c >> 3) * 32 + (r & 7) * 4 + ((c & 7) >> 1)) * 4 + (r >> 3) * 2);
-                float m[kMaxShare], l = 0.f, top = -INFINITY;
-                float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < kMaxShare; ++i) {
-                    m[i] = i < parts ? ptx::cluster_load(ptx::cluster_addr(at_m, i)) : -INFINITY;
-                    top = fmaxf(top, m[i]);
-                }
-                const float mm = top == -INFINITY ? 0.f : top;
-#pragma unroll
-                for (int i = 0; i < kMaxShare; ++i)
-                    if (i < parts) {
-                        const float f = exp2_fast(m[i] - mm);
-                        const float2 v = ptx::cluster_load2(ptx::cluster_addr(at_o, i));
-                        l += ptx::cluster_load(ptx::cluster_addr(at_l, i)) * f;
-                        sum.x += v.x * f;
-                        sum.y += v.y * f;
-                    }
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int64_t t = s.token0 + (row0 + r) / p.group, head = (int64_t)s.h * p.group + (row0 + r) % p.group;
-                if (c < p.head_dim)
-                    *reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + (t * p.q_heads + head) * p.head_dim + c) =
-                        Elem<T>::pack(sum.x * inv, sum.y * inv);
-                if (c == 0) store_lse(p, s.token0, s.h, row0 + r, mm, l);
-            }
+            if (all) join_shared<T, DP>(p, s, ptx::smem_addr(pairs), ptx::smem_addr(merge), rank, row0, rows);
             ptx::cluster_sync();
             if (!all) return;
         } else if (s.whole()) {
@@ -589,8 +627,10 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
     const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
     const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
     const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
+    const LaunchInfo shared = launch_info<T, DP, true>();
+    if (shared.err != cudaSuccess) return shared.err;
     int share = 0;
-    while (blocks > 0 && share < kShareLog && (blocks << (share + 1)) <= li.sms && (tiles >> (share + 1)) >= kShareTiles) ++share;
+    while (blocks > 0 && share < kShareLog && (blocks << (share + 1)) <= shared.ctas && (tiles >> (share + 1)) >= kShareTiles) ++share;
     p.whole = tiles <= (share > 0 ? (int64_t)kSharedTiles << share : kWholeTiles);
     p.min_units = p.whole ? 1 : kBlockCost + 8;
     const int64_t units = p.whole ? blocks : blocks * (kBlockCost + tiles);
@@ -599,8 +639,6 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
 #endif
     if (p.whole) p.share = share;
     if (p.share > 0) {
-        const LaunchInfo shared = launch_info<T, DP, true>();
-        if (shared.err != cudaSuccess) return shared.err;
         p.lines = 1;
         return launch_pair<T, kRows, DP>(attention_rows_kernel<T, DP, true>, (int)blocks << p.share, kThreads, Cfg<DP>::kSmem,
                                          stream, tk, tv, p);
@@ -707,7 +745,18 @@ cudaError_t launch_rows_any(const awq_tree_attention_t &a, cudaStream_t stream)
 cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream)
 {
     const int64_t rows = a.max_new * (a.q_heads / a.kv_heads);
-    if (rows > attn::kRows && a.head_dim <= 128) return attn::launch_tc_any(a, stream);
+    if (a.head_dim > 128 || rows <= attn::kRows) return attn::launch_rows_any(a, stream);
+    // With more rows the few-row kernel reads its keys once a block of 16. Small calls
+    // still take it: if all blocks have a CTA at once (or are two a head), and as long as
+    // that costs no more than the tensor-core kernel's longer way in and out, 8 us.
+    // 64 / 8 heads of 128, us with this kernel and with the other:
+    //    1 request,  32 tokens, 400 keys: 12 and 19    1 request,  32 tokens, 4000 keys: 31 and 32
+    //   16 requests,  4 tokens, 400 keys: 11 and 12   16 requests,  4 tokens, 4000 keys: 42 and 49
+    //   64 requests,  4 tokens, 400 keys: 27 and 37   64 requests,  4 tokens, 4000 keys: 153 and 122
+    //   16 requests,  8 tokens, 400 keys: 18 and 13   16 requests, 32 tokens, 400 keys: 42 and 20
+    const int64_t blocks = a.B * a.kv_heads * ((rows + attn::kRows - 1) / attn::kRows);
+    const int64_t tiles = (a.max_context + a.max_new + attn::kKeys - 1) / attn::kKeys;
+    if (blocks * tiles > (1 << 15) || (blocks > 304 && rows > 2 * attn::kRows)) return attn::launch_tc_any(a, stream);
     return attn::launch_rows_any(a, stream);
 }
 

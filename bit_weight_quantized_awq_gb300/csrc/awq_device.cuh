@@ -230,6 +230,14 @@ __device__ __forceinline__ float2 cluster_load2(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ float4 cluster_load4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // 4-D tiled TMA load global -> shared; coordinates innermost first.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, uint32_t bar,
                                             int32_t c0, int32_t c1, int32_t c2, int32_t c3) {

@@ -476,6 +476,89 @@ def test_attention_in_a_graph_follows_the_lengths():
     later.check(out, lse)
 
 
+# ---------------------------------------------------------------- attention, many rows
+# Bounds that allow a long cache, or many row blocks, for which the tensor-core kernel is taken.
+LONG = 2 ** 20
+
+
+@pytest.mark.parametrize("heads,kv_heads", HEADS)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("mask", ["causal", "tree"])
+def test_many_rows_heads_and_dims(heads, kv_heads, dim, dtype, mask):
+    s = Step([130, 0, 17], [35, 3, 1], heads, kv_heads, dim, 16, dtype, mask, seed=heads + dim)
+    s.check(*s.run(max_context=LONG))
+
+
+@pytest.mark.parametrize("dim", [8, 40, 72, 80, 96])
+def test_many_rows_odd_head_dims(dim):
+    for new in ([9, 2], [40, 9]):
+        s = Step([70, 5], new, 4, 2, dim, 32, torch.float16, "tree", seed=dim)
+        s.check(*s.run(max_context=LONG))
+
+
+@pytest.mark.parametrize("ctx,new", [
+    ([0], [64]), ([62], [5]), ([127], [9]), ([128], [33]), ([255, 256, 257], [5, 6, 7]), ([500], [33]), ([5], [129]),
+    ([1000, 3], [17, 200]), ([3, 1000], [1, 7]), ([0] * 20, [0] * 19 + [9])])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("mask", ["causal", "tree", "random"])
+def test_many_rows_lengths(ctx, new, page, mask):
+    s = Step(ctx, new, 8, 2, 64, page, torch.float16, mask, seed=sum(ctx) + page)
+    s.check(*s.run(max_context=LONG))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("mask", ["causal", "tree", "none"])
+def test_many_rows_of_many_requests_with_short_caches(dim, dtype, mask):
+    """Row blocks that are not cut, of 128 rows and of 256."""
+    rng = np.random.default_rng(dim)
+    for most in (24, 90):
+        ctx, new = rng.integers(0, 300, 40), rng.integers(0, most + 1, 40)
+        new[0], ctx[1] = most, 0
+        s = Step(ctx, new, 8, 2, dim, 32, dtype, mask, seed=most)
+        s.check(*s.run())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_rows_odd_values_in_unseen_keys_do_not_spread(bad, dtype):
+    for where in ("k", "v"):
+        s = Step([37], [60], 8, 2, 128, 16, dtype, "tree", seed=60)
+        node = 30
+        getattr(s, where)[s.table[0][(37 + node) // 16], (37 + node) % 16, 0, 5] = bad
+        out, lse = s.run(max_context=LONG)
+        sees = s.bits[:s.T, node]
+        assert sees.any() and not sees.all()
+        s.check(out, lse, rows=torch.from_numpy(~sees))
+        if where == "v":
+            seen = out[torch.from_numpy(sees).cuda()].float()
+            assert not seen[:, :4, 5].isfinite().any()
+            seen[:, :4, 5] = 0
+            assert seen.isfinite().all()
+
+
+@pytest.mark.parametrize("scale", [0.0, 4.0, -0.3])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_rows_scales_and_empty_rows(scale, dtype):
+    s = Step([200, 0], [50, 20], 4, 2, 64, 16, dtype, "none", seed=5)
+    out, lse = s.run(scale=scale, max_context=LONG)
+    s.check(out, lse)
+    assert (out[50:] == 0).all() and (lse[50:] == -torch.inf).all()
+
+
+@pytest.mark.parametrize("ctx,heads,kv_heads", [([100], 32, 32), ([450], 8, 1), ([1000], 32, 8), ([1000] * 5, 16, 2),
+                                                ([3900], 8, 8), ([7, 450, 0], 4, 2)])
+@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("dim", [64, 96, 128, 200, 256])
+def test_few_row_blocks_shared_by_clusters(ctx, heads, kv_heads, new, dim):
+    s = Step(ctx, [new] * len(ctx), heads, kv_heads, dim, 32, torch.bfloat16, "tree", seed=dim + new)
+    out, lse = s.run()
+    s.check(out, lse)
+    again, _ = s.run(max_new=max(1, new - 3))          # more row blocks than the bound allows for: several a cluster
+    s.check(again, lse)
+
+
 # ---------------------------------------------------------------- logits
 
 class Rows:

@@ -32,12 +32,18 @@ def test_wait_of_a_cluster_runs_out_then_next_calls_are_right(flib, ctx, new, di
     _runs_out(flib, ctx, new, dim)
 
 
+@pytest.mark.parametrize("new,dim", [(12, 64), (40, 128), (80, 128)])
+def test_wait_of_the_tensor_core_kernel_runs_out_then_next_calls_are_right(flib, new, dim):
+    """Bounds that allow a long cache, for which that kernel is taken."""
+    _runs_out(flib, 2001, new, dim, max_context=2 ** 20)
+
+
 @pytest.mark.parametrize("new,dim", [(1, 128), (1, 256), (12, 64), (40, 128), (80, 128)])
 def test_wait_runs_out_then_next_calls_are_right(flib, new, dim):
     _runs_out(flib, 2001, new, dim)
 
 
-def _runs_out(flib, ctx, new, dim):
+def _runs_out(flib, ctx, new, dim, max_context=None):
     gen = torch.Generator().manual_seed(new + dim)
     page = 32
     blocks = -(-(ctx + new) // page)
@@ -50,7 +56,7 @@ def _runs_out(flib, ctx, new, dim):
     cache = lambda t: Cache(t.data_ptr(), page * 2 * dim, 2 * dim, dim)  # noqa: E731
     args = TreeAttention(dev[0].data_ptr(), 8 * dim, dim, out.data_ptr(), None, cache(dev[1]), cache(dev[2]),
                          dev[3].data_ptr(), blocks, blocks, dev[4].data_ptr(), dev[5].data_ptr(), None, 0, 1, new, 8,
-                         2, dim, blocks, page, new, ctx, 0.1, 0)
+                         2, dim, blocks, page, new, max_context or ctx, 0.1, 0)
     stream = torch.cuda.current_stream().cuda_stream
     call = lambda: flib.awq_tree_attention(ctypes.byref(args), stream)  # noqa: E731
     assert flib.awq_last_device_status(stream) == Status.OK
