@@ -198,8 +198,9 @@ paged_plan_kernel(const PlanProblem p, unsigned int *status)
 // the keys and as many for the values; a CTA takes `per_cta` tokens, each
 // thread kAppendPieces loads before the first of its stores, so that enough
 // bytes are in flight to cover HBM's latency. Bound: HBM, each byte read and written
-// once. Measured: 9 prompts of up to 2048 tokens, 32 heads of 128: 75.5 us, 91% of
-// the copy bandwidth.
+// once. Measured: 9 prompts of up to 2048 tokens, 32 heads of 128: 75 us, 92% of
+// the copy bandwidth. (With the slots' test after all loads, so that rows need not wait
+// for slots: 108 us, at 114 registers.)
 constexpr int kAppendThreads = 256;
 constexpr int kAppendPieces = 8;
 
@@ -309,6 +310,8 @@ cudaError_t launch_kv_append(const AppendProblem &a, cudaStream_t stream)
     p.head_pieces = a.head_dim / 8;
     p.row_pieces = a.kv_heads * p.head_pieces;
     p.per_cta = std::max(1, kAppendThreads * kAppendPieces / (2 * p.row_pieces));
+    // but four CTAs an SM before one has several tokens (16 x 33 tokens, 8 heads of 128: 2.3 us, and 5.1 without)
+    p.per_cta = (int)std::min<int64_t>(p.per_cta, (a.tokens + 607) / 608);
     unsigned int *status = device_status_word();
     void *args[] = {&p, &status};
     return launch_dependent((const void *)kv_append_kernel, (a.tokens + p.per_cta - 1) / p.per_cta, kAppendThreads, 0,
