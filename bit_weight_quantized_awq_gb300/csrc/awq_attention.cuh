@@ -99,7 +99,7 @@ struct Work {
     static __device__ int tiles_of(const Params &p, int ctx, int n, int rb)
     {
         int seen = n;
-        if (p.mask == nullptr) seen = min(n, ((rb + 1) * RB - 1) / p.group + 1);
+        if (p.mask == nullptr && n > 1) seen = min(n, ((rb + 1) * RB - 1) / p.group + 1);
         return (ctx + seen + KT - 1) / KT;
     }
     static __device__ int row_blocks_of(const Params &p, int n) { return (n * p.group + RB - 1) / RB; }
@@ -117,7 +117,7 @@ struct Work {
     static __device__ int64_t head_units(const Params &p, int ctx, int n)
     {
         const int blocks = row_blocks_of(p, n);
-        if (blocks == 0) return 0;
+        if (blocks == 0 || p.whole) return blocks;
         if (p.mask != nullptr)
             return (blocks - 1) * block_units(p, ctx, n, 0) + block_units(p, ctx, n, blocks - 1);
         int64_t sum = 0;
@@ -155,7 +155,7 @@ struct Work {
         if (tid == 0) p.joins[blockIdx.x].valid = 0;
         heads = p.lines == 1 ? p.kv_heads : 1;
         head0 = p.lines == 1 ? 0 : blockIdx.x % p.lines;
-        cta = (blockIdx.x >> p.share) / p.lines;
+        cta = p.lines == 1 ? blockIdx.x >> p.share : blockIdx.x / p.lines;
         const int per = (p.B + THREADS - 1) / THREADS;
         const int b_lo = min(tid * per, p.B), b_hi = min(b_lo + per, p.B);
         int64_t mine = 0, units0 = 0;          // of the thread's requests, and of the first of them
@@ -195,10 +195,17 @@ struct Work {
         }
         before += su - mine;
         if (units == 0) return false;
-        ctas = (int)min((int64_t)((gridDim.x >> p.share) / p.lines), max((int64_t)1, quotient(units, p.min_units)));
+        const int there = p.lines == 1 ? gridDim.x >> p.share : gridDim.x / p.lines;
+        if (p.whole && units <= there) {     // a row block a CTA: no divisions, half a microsecond
+            ctas = (int)units;
+            pos = cta;
+            end = cta + 1;
+        } else {
+            ctas = (int)min((int64_t)there, max((int64_t)1, quotient(units, p.min_units)));
+            pos = begin_of(cta);
+            end = begin_of(cta + 1);
+        }
         if (cta >= ctas) return false;
-        pos = begin_of(cta);
-        end = begin_of(cta + 1);
         if (pos >= before && pos < before + mine) {
             // the request, and what has just been read of it
             int i = b_lo;
@@ -226,10 +233,13 @@ struct Work {
         row_blocks = row_blocks_of(p, n);
         int64_t rem = pos - found.before;
         const int64_t per_head = found.per_head;
-        h = (int)quotient(rem, per_head);
+        h = per_head == 1 ? (int)rem : (int)quotient(rem, per_head);
         rem -= h * per_head;
         rb = 0;
-        if (p.mask != nullptr) {
+        if (p.whole) {
+            rb = (int)rem;
+            rem = 0;
+        } else if (p.mask != nullptr) {
             const int64_t full = block_units(p, ctx, n, 0);
             rb = (int)min((int64_t)(row_blocks - 1), quotient(rem, full));
             rem -= rb * full;
