@@ -12,11 +12,13 @@
 // memory), the stream's four warps read S (a thread has one row: no shuffles),
 // write P = exp2(S - m) over it as 16-bit values, and O += P V takes P from tensor
 // memory. Tensor memory is full: S 2 streams x 2 halves x 64, O 2 x DP columns.
-// A stream's MMAs are issued by one thread and run in order, so S of the next
-// tile's half may be written over P as soon as it is issued behind O += P V; and
-// while that runs, the softmax has the other half. (S of 128 keys at once left the
-// softmax waiting for both products of every tile: 4,700 cycles a tile of two
-// streams, twice what either side needs.)
+// S of the next tile's half is written over P, so it is issued only once the O += P V
+// that reads this P has completed: products run in the order of their issue where they
+// share accumulator and shape, and these two do not. Meanwhile the softmax has the
+// other half and the tensor cores the other stream. (Without that wait 0.5 to 1% less for
+// 256 rows and for 128 of head_dim 128, 4% for a tree of 26 over 131072 keys, head_dim
+// 64. S of 128 keys at once left the softmax waiting for both products of every tile:
+// 4,700 cycles a tile of two streams, twice what either side needs.)
 //
 // The maximum is lazy: O is rescaled only when a row's maximum has grown by more
 // than 2^kSlack since the last time (P then is up to 2^kSlack instead of 1, which
@@ -28,10 +30,10 @@
 // them a stream and tile).
 //
 // Measured: 12 requests with trees of 64 over up to 16384 keys, 64 / 8 heads of 128,
-// fp16: 221 to 238 us, half of the bf16 matrix rate (tensor pipe 59% busy: S in halves
+// fp16: 224 to 238 us, half of the bf16 matrix rate (tensor pipe 59% busy: S in halves
 // of 64 keys reads q twice a tile); 16 requests with trees of 13 over up to 6000 keys,
 // bf16: 66 us, 59% of the copy bandwidth; a tree of 26 over 131072 keys, 32 / 8 heads
-// of 64: 56 us, 72%.
+// of 64: 59 us, 68%.
 //
 //   warps 0, 3  producers of K and of V tiles, a TMA box a page, in one ring, in the
 //               order the MMAs take them
@@ -249,6 +251,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
         const uint32_t done_bar = ptx::smem_addr(pv_done + stream), o_bar = ptx::smem_addr(o_full + stream);
         int slot = 0, seg = 0;
         uint32_t ring = 0, taken = 0;                // parities: of the slot's tile, of P
+        uint32_t products = 0;                       // O += P V issued
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t parity) {
             ok = __all_sync(0xFFFFFFFFu, wait_soon(bar, parity, abort_flag, p.status));
@@ -299,6 +302,9 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
             }
             __syncwarp();
         };
+        // The last O += P V is complete. After each one, so that the barrier is never
+        // more than one phase ahead of what is waited for.
+        auto pv_complete = [&] { return wait(done_bar, products++ & 1); };
         while (ok && work.next(p, s)) {
             const int nt = s.tile1 - s.tile0;
             const bool two = kRows > 128 && min(kRows, s.n * p.group - s.rb * kRows) > 128;
@@ -330,12 +336,12 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 advance(next, next_ring);
                 if (!wait_tile() || !wait(p_bar, taken & 1)) break;
                 pv(slot, 0, j < ahead, false);
-                if (more) {
-                    if (!wait(full0 + next * 8, next_ring)) break;
-                    qk(next, 0, two ? stream : 0);
-                }
+                if (more && !wait(full0 + next * 8, next_ring)) break;
+                if (!pv_complete()) break;
+                if (more) qk(next, 0, two ? stream : 0);
                 if (!wait(p_bar + 8, taken & 1)) break;
                 pv(slot, 1, false, !more);
+                if (!pv_complete()) break;
                 if (more) qk(next, 1, two ? stream : 0);
                 ++taken;
                 advance(slot, ring);
