@@ -46,6 +46,10 @@ struct ScratchEntry {
     void *xs = nullptr;            // activations in sorted row order (act-order forward)
     size_t xs_bytes = 0;
     bool reserved = false;         // sized by awq_reserve: never grows afterwards
+    // sized by awq_reserve_tree_attention: graphs captured since then hold the address of
+    // the partials, so an area that a later call outgrows stays until awq_shutdown
+    bool held = false;
+    std::vector<float *> outgrown;
 };
 
 // set when a call needed more scratch than its stream's reservation
@@ -79,10 +83,14 @@ bool get_scratch(cudaStream_t stream, size_t partial_floats, size_t n_counters, 
         return false;
     }
     if (e.partial_floats < partial_floats) {
-        // the old area may still be read by work queued on this stream
         if (e.partials) {
-            cudaStreamSynchronize(stream);
-            cudaFree(e.partials);
+            if (e.held) {
+                e.outgrown.push_back(e.partials);
+            } else {
+                // the old area may still be read by work queued on this stream
+                cudaStreamSynchronize(stream);
+                cudaFree(e.partials);
+            }
             e.partials = nullptr;
             e.partial_floats = 0;
         }
@@ -619,6 +627,7 @@ awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream)
         const bool ok = awq::get_scratch(s, floats, 0, &sc) && cudaStreamSynchronize(s) == cudaSuccess;
         std::lock_guard<std::mutex> lock(awq::g_mutex);
         awq::g_scratch[key].reserved = reserved;
+        awq::g_scratch[key].held = awq::g_scratch[key].held || ok;
         return ok ? AWQ_OK : AWQ_ERR_CUDA;
     } catch (...) {
         return AWQ_ERR_CUDA;
@@ -667,6 +676,7 @@ void awq_shutdown(void)
     for (auto &kv : awq::g_scratch) {
         cudaSetDevice(kv.first.first);
         if (kv.second.partials) cudaFree(kv.second.partials);
+        for (float *area : kv.second.outgrown) cudaFree(area);
         if (kv.second.counters) cudaFree(kv.second.counters);
         if (kv.second.w16) cudaFree(kv.second.w16);
         if (kv.second.xs) cudaFree(kv.second.xs);

@@ -1,0 +1,61 @@
+"""awq_reserve_tree_attention: what a stream holds afterwards, and which calls need nothing
+of it. Tolerances as in test_gpu_step.py."""
+import pytest
+import torch
+
+import bit_weight_quantized_awq_gb300 as awq
+from bit_weight_quantized_awq_gb300 import Status
+from test_gpu_step import LONG, Step, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _status(gpu):
+    """Every test starts and ends with a clean device status."""
+    awq.awq_last_device_status(None)
+    yield
+    torch.cuda.synchronize()
+    assert awq.awq_last_device_status(None) == Status.OK
+
+
+def on_the_gpu(s):
+    s.scale = 0.1
+    args = (s.q.cuda(), s.k.cuda(), s.v.cuda(), i32(s.table), i32(s.ctx), i32(s.cu), s.scale)
+    kw = dict(tree_mask=s.mask.cuda(), out=torch.empty(s.q.shape, dtype=s.q.dtype, device="cuda"),
+              lse=torch.empty(s.q.shape[:2], device="cuda"))
+    torch.cuda.synchronize()
+    return args, kw
+
+
+def free_bytes():
+    torch.cuda.synchronize()
+    return torch.cuda.mem_get_info()[0]
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_a_captured_call_outlives_a_larger_one(new):
+    """A later call on the stream needs more scratch than was reserved: the graph's stays."""
+    s = Step([20000], [new], 8, 2, 64, 32, torch.float16, "tree", seed=new)
+    args, kw = on_the_gpu(s)
+    big = Step([9000], [70], 8, 2, 128, 32, torch.float16, "tree", seed=7)
+    big_args, big_kw = on_the_gpu(big)
+    stream = torch.cuda.Stream()
+    assert awq.awq_reserve_tree_attention(64, stream.cuda_stream) == Status.OK
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream, capture_error_mode="global"):
+        awq.tree_attention(*args, new, LONG, **kw)
+    before = free_bytes()
+    with torch.cuda.stream(stream):
+        awq.tree_attention(*big_args, 70, LONG, **big_kw)
+    assert free_bytes() < before                       # it did need more
+    big.check(big_kw["out"], big_kw["lse"])
+    for _ in range(3):
+        kw["out"].fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            graph.replay()
+            awq.tree_attention(*big_args, 70, LONG, **big_kw)
+        stream.synchronize()
+        s.check(kw["out"], kw["lse"])
+        big.check(big_kw["out"], big_kw["lse"])
