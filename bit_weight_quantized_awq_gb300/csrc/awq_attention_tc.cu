@@ -570,6 +570,7 @@ attention_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_const
                 const int c_lo = two ? 0 : stream * (DP / 2), c_hi = two ? DP : c_lo + DP / 2;
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; c += 32) {
+                    __syncwarp();            // rows differ in what they store; tensor memory is read by whole warps
                     uint32_t raw[32];
                     float o[32];
                     tc::ld_32x32b_x32((two ? t_o : t_lane + kO) + c, raw);

@@ -202,9 +202,11 @@ __device__ __forceinline__ int cluster_rank()
 }
 
 // All threads of the cluster that have not ended, whole warps; what they wrote to
-// shared memory before is seen by all after.
+// shared memory before is seen by all after. The barrier's instructions are for a
+// converged warp, which lanes that come from different branches are not by themselves.
 __device__ __forceinline__ void cluster_sync()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

@@ -559,6 +559,17 @@ def test_few_row_blocks_shared_by_clusters(ctx, heads, kv_heads, new, dim):
     s.check(again, lse)
 
 
+@pytest.mark.parametrize("rows", range(1, 17))
+@pytest.mark.parametrize("heads,kv_heads", [(2, 2), (3, 1)])
+def test_row_blocks_of_any_height_shared_by_clusters(rows, heads, kv_heads):
+    """Lanes whose row a block does not have leave the join early and meet the others again."""
+    new = -(-rows * kv_heads // heads)
+    s = Step([500, 290], [new, 1], heads, kv_heads, 128, 16, torch.float16, "tree", seed=rows)
+    for _ in range(20):
+        out, lse = s.run()
+    s.check(out, lse)
+
+
 # ---------------------------------------------------------------- logits
 
 class Rows:
