@@ -15,6 +15,7 @@
 #include <string>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -76,10 +77,16 @@ int64_t integer(PyObject *o)
     return v;
 }
 
+// The device of the call: the library launches on the current one, with its scratch and
+// status word, so the tensors have to be there.
 int cuda_index(const Tensor &t)
 {
     if (!t.is_cuda()) refuse("the AWQ library runs on CUDA tensors only");
-    return t.get_device();
+    c10::DeviceIndex current = -1;
+    if (c10::cuda::GetDevice(&current) != cudaSuccess || t.get_device() != current)
+        refuse("the AWQ library works on the current CUDA device (%d), the tensors are on cuda:%d", (int)current,
+               (int)t.get_device());
+    return current;
 }
 
 bool on(const Tensor &t, int dev) { return t.is_cuda() && t.get_device() == dev; }

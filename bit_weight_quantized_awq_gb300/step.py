@@ -1,7 +1,8 @@
 """Torch-facing functions of the decoding step around the quantised layers
 (``include/awq_gb300.h`` has the operators' definitions). No arithmetic happens
 here, nothing waits for the GPU, and what is known on the device only (lengths,
-table entries, tokens) is checked there: ``awq_last_device_status`` reports it.
+table entries, tokens) is checked there: ``awq_last_device_status`` reports it. The
+tensors must be on the current CUDA device (``torch.cuda.set_device``), else ValueError.
 
 A step is ``paged_plan`` -> per layer ``kv_append``, ``tree_attention`` ->
 ``process_logits``: the plan's ``cu_new``, ``slot_map`` and ``tree_mask`` are the

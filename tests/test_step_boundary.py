@@ -144,3 +144,19 @@ def test_wrappers_refuse_cpu_tensors():
         awq.tree_attention(f, c, c, i[None], i[:1], i, 1.0, 2, 0)
     with pytest.raises(ValueError):
         awq.process_logits(torch.zeros((2, 10)))
+
+
+@pytest.mark.skipif(torch.cuda.is_available() and torch.cuda.device_count() < 2,
+                    reason="where torch sees a GPU, a fake tensor of cuda:1 needs a second one")
+def test_wrappers_refuse_tensors_of_another_than_the_current_device():
+    """Fake tensors, which have a device but no memory: refused before anything asks for it."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        make = lambda *shape, dtype=torch.int32: torch.empty(shape, dtype=dtype, device="cuda:1")  # noqa: E731
+        i, table, slots = make(2), make(2, 4), make(2, dtype=torch.int64)
+        q, cache = make(2, 4, 64, dtype=torch.float16), make(3, 16, 4, 64, dtype=torch.float16)
+        x = make(2, 10, dtype=torch.float32)
+    for call in (lambda: awq.paged_plan(i, i, table, i, 16, 2), lambda: awq.kv_append(q, q, cache, cache, slots),
+                 lambda: awq.tree_attention(q, cache, cache, table, i, i, 1.0, 2, 0), lambda: awq.process_logits(x)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
