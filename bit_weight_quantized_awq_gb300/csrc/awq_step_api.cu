@@ -124,7 +124,7 @@ awq_status_t awq_process_logits(const awq_logits_t *args, awq_stream_t stream)
     const uintptr_t size = a.dtype == AWQ_F32 ? 4 : 2;
     if (a.dtype != AWQ_F16 && a.dtype != AWQ_BF16 && a.dtype != AWQ_F32) return AWQ_ERR_INVALID_ARG;
     if (a.rows < 0 || a.rows >= kInt || a.vocab <= 0 || a.vocab > (int64_t(1) << 27) || a.B < 0 || a.B >= kInt ||
-        a.history_size < 0 || a.history_size >= (int64_t(1) << 29) || a.bias_size < 0 || a.bias_size >= kInt || a.mask_words < 0 ||
+        a.history_size < 0 || a.history_size >= (int64_t(1) << 29) || a.bias_size < 0 || a.bias_size > kInt / 2 || a.mask_words < 0 ||
         a.mask_words > (1 << 20) || a.grammar_count < 0)
         return AWQ_ERR_INVALID_ARG;
     if (a.rows > 1 && (a.logits_row_stride < a.vocab || a.out_row_stride < a.vocab)) return AWQ_ERR_INVALID_ARG;

@@ -125,6 +125,14 @@ def test_logits_history_limit():
     assert logits(history=A, history_offsets=A, history_size=2 ** 29 - 1, rows=0) == OK
 
 
+def test_logits_bias_limit():
+    # a thread's first pairs are numbered from the list's beginning in 32 bits: 2^31 less a few would wrap
+    lists = dict(bias_tokens=A, bias_values=A, bias_offsets=A)
+    for size in (2 ** 31 - 1, 2 ** 30 + 1):
+        assert logits(bias_size=size, **lists) == INVALID
+    assert logits(bias_size=2 ** 30, rows=0, **lists) == OK
+
+
 def test_logits_misaligned_and_empty():
     assert logits(logits=A + 1, out=A + 4) == MISALIGNED
     assert logits(logits=A + 2, out=A + 4, dtype=2) == MISALIGNED
