@@ -97,7 +97,7 @@ awq_status_t awq_tree_attention(const awq_tree_attention_t *args, awq_stream_t s
     const awq_tree_attention_t &a = *args;
     if (a.dtype != AWQ_F16 && a.dtype != AWQ_BF16) return AWQ_ERR_INVALID_ARG;
     if (a.B < 0 || a.B > kMaxRequests || a.tokens < 0 || a.tokens >= kInt || a.q_heads <= 0 || a.kv_heads <= 0 ||
-        a.q_heads >= kInt || a.q_heads % a.kv_heads != 0 || a.tokens * a.q_heads >= kInt || a.head_dim <= 0 ||
+        a.q_heads >= kInt || a.q_heads % a.kv_heads != 0 || a.tokens * a.q_heads >= kInt - 1024 || a.head_dim <= 0 ||
         a.head_dim % 8 != 0 || a.head_dim > 256 || a.num_blocks <= 0 || a.num_blocks >= kInt ||
         !page_size_ok(a.block_size) || a.max_new < 0 || a.max_context < 0 || a.max_new >= kInt || a.max_context >= kInt)
         return AWQ_ERR_INVALID_ARG;

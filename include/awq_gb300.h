@@ -503,9 +503,10 @@ awq_status_t awq_kv_append(const void *k, int64_t k_token_stride, int64_t k_head
  *
  * Requires head_dim % 8 == 0 and <= 256, q_heads % kv_heads == 0, block_size a
  * power of two from 16 to 1024, num_blocks < 2^31, table_width * block_size < 2^31 - 1024,
- * tokens * q_heads < 2^31, B <= 16384 (AWQ_ERR_INVALID_ARG otherwise). If cu_new decreases or leaves [0, tokens], or
- * a length is negative or exceeds the table's width, nothing is written and the
- * device status becomes AWQ_ERR_INVALID_ARG; so it does for a table entry outside
+ * tokens * q_heads < 2^31 - 1024 (a request's rows are rounded up to blocks in 32 bits), B <= 16384
+ * (AWQ_ERR_INVALID_ARG otherwise). If cu_new decreases or leaves [0, tokens], or a
+ * length is negative or exceeds the table's width, nothing is written and the device
+ * status becomes AWQ_ERR_INVALID_ARG; so it does for a table entry outside
  * [0, num_blocks) below a request's length, whose page then reads as zeros.
  */
 typedef struct {

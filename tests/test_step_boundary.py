@@ -88,6 +88,14 @@ def test_attention_invalid(kw):
     assert attention(**kw) == INVALID
 
 
+def test_attention_rows_limit():
+    # rows (tokens * group) are rounded up to whole blocks in 32 bits
+    wide = dict(q_heads=2, kv_heads=1, q_token_stride=128, B=0)
+    assert attention(tokens=2 ** 30 - 1, **wide) == INVALID
+    assert attention(tokens=2 ** 30 - 512, **wide) == INVALID
+    assert attention(tokens=2 ** 30 - 513, **wide) == OK
+
+
 def test_attention_misaligned_and_empty():
     assert attention(q=A + 8) == MISALIGNED
     assert attention(out=A + 2) == MISALIGNED
