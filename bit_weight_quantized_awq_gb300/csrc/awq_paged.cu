@@ -241,8 +241,9 @@ kv_append_kernel(const AppendParams p, unsigned int *status)
             }
             to[u] = p.dst[side] + (slot >> p.shift) * p.dst_block[side] +
                     (slot & ((1 << p.shift) - 1)) * p.dst_token[side] + head * p.dst_head[side] + at * 16;
-            v[u] = __ldg(reinterpret_cast<const uint4 *>(p.src[side] + t * p.src_token[side] +
-                                                         head * p.src_head[side] + at * 16));
+            // not a read-only load: this kernel may be resident while the one before writes k and v
+            v[u] = *reinterpret_cast<const uint4 *>(p.src[side] + t * p.src_token[side] + head * p.src_head[side] +
+                                                    at * 16);
         }
 #pragma unroll
         for (int u = 0; u < kAppendPieces; ++u)

@@ -178,6 +178,23 @@ def test_append_copies_into_slots(heads, dim, page, layout, dtype):
         assert torch.equal(got.reshape(blocks * page, heads, dim).view(torch.int16).cpu(), want)
 
 
+def test_append_takes_what_the_kernel_before_has_just_written():
+    """Back to back on one stream, an append reading the cache that the append before wrote:
+    dependent launches, whose blocks may be on the GPU before those writes."""
+    gen = torch.Generator().manual_seed(3)
+    T, heads, dim = 512, 8, 128
+    steps = [torch.randint(-2 ** 15, 2 ** 15, (T, heads, dim), dtype=torch.int16, generator=gen).cuda().view(torch.float16)
+             for _ in range(8)]
+    caches = torch.zeros((6, T // 16, 16, heads, dim), dtype=torch.float16, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    for k in steps * 8:
+        awq.kv_append(k, k, caches[0], caches[1], slots)
+        for i in (2, 4):
+            awq.kv_append(caches[i - 2].view(T, heads, dim), caches[i - 1].view(T, heads, dim), caches[i], caches[i + 1], slots)
+    for cache in caches:
+        assert torch.equal(cache.view(T, heads, dim).view(torch.int16), steps[-1].view(torch.int16))
+
+
 def test_append_skips_and_reports_slots_outside_the_cache():
     k = torch.ones((3, 1, 8), dtype=torch.float16, device="cuda")
     cache = torch.zeros((2, 2, 16, 1, 8), dtype=torch.float16, device="cuda")
