@@ -127,6 +127,8 @@ cudaError_t launch_gather_cols(const void *x, int64_t ldx, const int32_t *perm, 
 bool get_xs_scratch(cudaStream_t stream, size_t bytes, void **out);
 // ---- the decoding step around the layers (arguments already checked) ----
 
+constexpr int64_t kMaxRequests = 16384;   // of a step
+
 struct PlanProblem {
     const int32_t *context_lens, *new_lens;
     int32_t *block_table;

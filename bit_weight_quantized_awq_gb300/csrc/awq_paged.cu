@@ -11,6 +11,8 @@
 // step is one launch. Bound: latency (a few KB are read and written). Measured: 256
 // requests of one token 3.2 us, 64 trees of up to 60 nodes 5.0 us.
 #include <algorithm>
+#include <map>
+#include <mutex>
 
 #include <cuda_runtime.h>
 
@@ -267,16 +269,35 @@ cudaError_t launch_dependent(const void *kernel, int64_t grid, int block, size_t
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// The plan kernel's shared memory, two sums a request.
+constexpr size_t plan_smem_bytes(int64_t B) { return (size_t)2 * (B + 1) * sizeof(unsigned); }
+
+// Allowed once a device, for the most requests: a limit of a call's own size could be
+// lowered by another thread's call before this one's launch.
+cudaError_t prepare_plan()
+{
+    static std::mutex mu;
+    static std::map<int, unsigned> done;   // device -> cache generation
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned gen = cache_generation();
+    std::lock_guard<std::mutex> lock(mu);
+    const auto it = done.find(dev);
+    if (it != done.end() && it->second == gen) return cudaSuccess;
+    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)plan_smem_bytes(kMaxRequests));
+    if (e == cudaSuccess) done[dev] = gen;
+    return e;
+}
+
 } // namespace
 
 cudaError_t launch_paged_plan(const PlanProblem &p, cudaStream_t stream)
 {
-    const size_t smem = (size_t)2 * (p.B + 1) * sizeof(unsigned);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const size_t smem = plan_smem_bytes(p.B);
+    const cudaError_t e = prepare_plan();
+    if (e != cudaSuccess) return e;
     // every CTA scans all requests: few CTAs, each with several rounds of tokens once there are many
     const int64_t rounds = ((int64_t)p.max_tokens + kPlanTokens - 1) / kPlanTokens;
     const int64_t by_request = (p.B + kPlanThreads / 32 - 1) / (kPlanThreads / 32);

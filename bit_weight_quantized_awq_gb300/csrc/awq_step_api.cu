@@ -10,7 +10,7 @@
 
 namespace {
 
-constexpr int64_t kMaxRequests = 16384;
+using awq::kMaxRequests;
 constexpr int64_t kInt = int64_t(1) << 31;   // sizes below this fit an int
 
 bool aligned(const void *p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }

@@ -107,6 +107,27 @@ def test_plan_of_no_requests_and_of_deep_chains():
     assert torch.equal(a.tree_mask, b.tree_mask) and torch.equal(a.positions, b.positions)
 
 
+@pytest.mark.parametrize("requests", [6127, 6128, 6143, 6144, 16384])
+def test_plan_of_many_requests(requests):
+    """Two sums a request in shared memory, around the 48 KB that a kernel has without asking."""
+    rng = np.random.default_rng(requests)
+    ctx, new = rng.integers(0, 40, requests), rng.integers(0, 3, requests)
+    have = -(-ctx // 16)
+    need = int((-(-(ctx + new) // 16) - have).sum())
+    perm = rng.permutation(int(have.sum()) + need)
+    table = np.full((requests, 4), -1, dtype=np.int64)
+    at = 0
+    for b, n in enumerate(have):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    cu, want_table, slots, positions, request, _, counts = ref.plan(ctx.tolist(), new.tolist(), table, perm[at:], 16)
+    buf = i32(table)
+    p = awq.paged_plan(i32(ctx), i32(new), buf, i32(perm[at:]), 16, len(slots))
+    assert p.cu_new.tolist() == cu and p.counts.tolist() == counts
+    assert p.slot_map.tolist() == slots and p.positions.tolist() == positions and p.token_request.tolist() == request
+    assert np.array_equal(buf.cpu().numpy(), want_table)
+
+
 @pytest.mark.parametrize("what,status", [("free", Status.ERR_TOO_LARGE), ("width", Status.ERR_TOO_LARGE),
                                          ("tokens", Status.ERR_TOO_LARGE), ("mask", Status.ERR_TOO_LARGE),
                                          ("negative", Status.ERR_INVALID_ARG), ("parent", Status.ERR_INVALID_ARG),
