@@ -762,9 +762,14 @@ cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t st
 
 size_t tree_attention_partial_floats(int64_t head_dim, int sms)
 {
-    // at most four CTAs of the few-row kernel fit an SM's shared memory
-    const int dp = head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256;
-    return std::max(attn::scratch_floats(4 * sms, attn::kRows, dp), attn::tc_partial_floats(sms, head_dim));
+    // At most four CTAs of the few-row kernel fit an SM's shared memory. The smaller classes
+    // of head_dim too: the tensor-core kernel, which ends at 128, has the larger pieces.
+    size_t most = 0;
+    for (const int dp : {64, 128, 256}) {
+        if (dp > 64 && head_dim <= dp / 2) break;
+        most = std::max({most, attn::scratch_floats(4 * sms, attn::kRows, dp), attn::tc_partial_floats(sms, dp)});
+    }
+    return most;
 }
 
 } // namespace awq

@@ -152,7 +152,8 @@ struct AppendProblem {
 cudaError_t launch_kv_append(const AppendProblem &p, cudaStream_t stream);
 
 cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream);
-// floats of partial sums that the largest tree-attention launch asks for, whatever the lengths
+// floats of partial sums that the largest tree-attention launch of this head_dim or a smaller
+// one asks for, whatever the lengths
 size_t tree_attention_partial_floats(int64_t head_dim, int sms);
 
 cudaError_t launch_process_logits(const awq_logits_t &a, cudaStream_t stream);

@@ -527,9 +527,8 @@ awq_status_t awq_tree_attention(const awq_tree_attention_t *args, awq_stream_t s
 
 /*
  * awq_reserve_tree_attention -- awq_reserve for awq_tree_attention: sizes the
- * scratch of `stream` for calls of this head_dim (or a smaller one of at most 64,
- * 128 or 256 if this one is), whatever their lengths, so that they neither allocate
- * nor synchronise. It leaves the stream as it was, reserved by awq_reserve or not;
+ * scratch of `stream` for calls of this head_dim, rounded up to 64, 128 or 256, or of any
+ * smaller one, whatever their lengths, so that they neither allocate nor synchronise. It leaves the stream as it was, reserved by awq_reserve or not;
  * a reserved stream whose scratch is too small refuses calls with AWQ_ERR_TOO_LARGE.
  * Graphs captured on the stream afterwards stay valid whatever else runs there: an area
  * that a later call outgrows is kept until awq_shutdown().

@@ -59,3 +59,25 @@ def test_a_captured_call_outlives_a_larger_one(new):
         stream.synchronize()
         s.check(kw["out"], kw["lse"])
         big.check(big_kw["out"], big_kw["lse"])
+
+
+@pytest.mark.parametrize("reserved,dim", [(64, 8), (72, 128), (128, 64), (256, 64), (256, 128), (136, 256)])
+@pytest.mark.parametrize("new", [1, 70])
+def test_a_reservation_serves_smaller_head_dims(reserved, dim, new):
+    """Neither kernel allocates: cut row blocks, pieces of every CTA."""
+    s = Step([9000], [new], 8, 2, dim, 32, torch.float16, "tree", seed=dim)
+    args, kw = on_the_gpu(s)
+    stream = torch.cuda.Stream()
+    assert awq.awq_reserve_tree_attention(reserved, stream.cuda_stream) == Status.OK
+    before = free_bytes()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        awq.tree_attention(*args, new, LONG, **kw)
+    assert free_bytes() == before
+    s.check(kw["out"], kw["lse"])
+    kw["out"].fill_(float("nan"))
+    with torch.cuda.graph(graph, stream=stream, capture_error_mode="global"):
+        awq.tree_attention(*args, new, LONG, **kw)
+    graph.replay()
+    torch.cuda.synchronize()
+    s.check(kw["out"], kw["lse"])
