@@ -72,6 +72,34 @@ unsigned int *device_status_word()
     return static_cast<unsigned int *>(addr);
 }
 
+namespace {
+
+// Grows an entry's partial sums to at least this many floats; g_mutex is held.
+bool grow_partials(ScratchEntry &e, size_t partial_floats, cudaStream_t stream)
+{
+    if (e.partial_floats >= partial_floats) return true;
+    if (e.partials) {
+        if (e.held) {
+            e.outgrown.push_back(e.partials);
+        } else {
+            // the old area may still be read by work queued on this stream
+            cudaStreamSynchronize(stream);
+            cudaFree(e.partials);
+        }
+        e.partials = nullptr;
+        e.partial_floats = 0;
+    }
+    size_t want = partial_floats + partial_floats / 2;
+    if (cudaMalloc(&e.partials, want * sizeof(float)) != cudaSuccess) {
+        e.partials = nullptr;
+        return false;
+    }
+    e.partial_floats = want;
+    return true;
+}
+
+} // namespace
+
 bool get_scratch(cudaStream_t stream, size_t partial_floats, size_t n_counters, Scratch *out)
 {
     int dev = 0;
@@ -82,25 +110,7 @@ bool get_scratch(cudaStream_t stream, size_t partial_floats, size_t n_counters, 
         t_over_reservation = true;
         return false;
     }
-    if (e.partial_floats < partial_floats) {
-        if (e.partials) {
-            if (e.held) {
-                e.outgrown.push_back(e.partials);
-            } else {
-                // the old area may still be read by work queued on this stream
-                cudaStreamSynchronize(stream);
-                cudaFree(e.partials);
-            }
-            e.partials = nullptr;
-            e.partial_floats = 0;
-        }
-        size_t want = partial_floats + partial_floats / 2;
-        if (cudaMalloc(&e.partials, want * sizeof(float)) != cudaSuccess) {
-            e.partials = nullptr;
-            return false;
-        }
-        e.partial_floats = want;
-    }
+    if (!grow_partials(e, partial_floats, stream)) return false;
     if (e.n_counters < n_counters) {
         if (e.counters) {
             cudaStreamSynchronize(stream);
@@ -616,19 +626,11 @@ awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream)
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const size_t floats = awq::tree_attention_partial_floats(head_dim, sms);
     try {
-        const auto key = std::make_pair(dev, s);
-        bool reserved;
-        {
-            std::lock_guard<std::mutex> lock(awq::g_mutex);
-            reserved = awq::g_scratch[key].reserved;
-            awq::g_scratch[key].reserved = false;
-        }
-        awq::Scratch sc{};
-        const bool ok = awq::get_scratch(s, floats, 0, &sc) && cudaStreamSynchronize(s) == cudaSuccess;
         std::lock_guard<std::mutex> lock(awq::g_mutex);
-        awq::g_scratch[key].reserved = reserved;
-        awq::g_scratch[key].held = awq::g_scratch[key].held || ok;
-        return ok ? AWQ_OK : AWQ_ERR_CUDA;
+        awq::ScratchEntry &e = awq::g_scratch[std::make_pair(dev, s)];
+        if (!awq::grow_partials(e, floats, s) || cudaStreamSynchronize(s) != cudaSuccess) return AWQ_ERR_CUDA;
+        e.held = true;
+        return AWQ_OK;
     } catch (...) {
         return AWQ_ERR_CUDA;
     }
