@@ -60,7 +60,7 @@ struct Params {
     int64_t v_block_stride, v_token_stride, v_head_stride;
     const int32_t *ctx, *cu, *mask;
     float *partials;        // slots, two a CTA
-    struct Join *joins;     // one a CTA
+    struct Join *joins;     // one a CTA; null, as the slots, where no row block is cut
     unsigned int *status;
     int table_width, mask_words;
     int B, tokens, q_heads, kv_heads, group, head_dim, num_blocks;
@@ -152,7 +152,7 @@ struct Work {
             int b, ctx, token0, n;
         } found;
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        if (tid == 0) p.joins[blockIdx.x].valid = 0;
+        if (tid == 0 && p.joins != nullptr) p.joins[blockIdx.x].valid = 0;
         heads = p.lines == 1 ? p.kv_heads : 1;
         head0 = p.lines == 1 ? 0 : blockIdx.x % p.lines;
         cta = p.lines == 1 ? blockIdx.x >> p.share : blockIdx.x / p.lines;
@@ -578,15 +578,18 @@ inline int lay_out(Params &p, int most, int64_t units)
 }
 
 // Launches a main kernel of `ctas` CTAs and, unless there is one only or each has
-// whole row blocks, its join.
+// whole row blocks, its join; only then does the call need scratch.
 template <typename T, int RB, int DP, typename K>
 cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t stream, const CUtensorMap &tk,
                         const CUtensorMap &tv, Params &p)
 {
-    Scratch sc{};
-    if (!get_scratch(stream, scratch_floats(ctas, RB, DP), 0, &sc)) return cudaErrorMemoryAllocation;
-    p.partials = sc.partials;
-    p.joins = reinterpret_cast<Join *>(sc.partials + (size_t)ctas * 2 * slot_floats(RB, DP));
+    const bool cut = ctas > 1 && !p.whole;
+    if (cut) {
+        Scratch sc{};
+        if (!get_scratch(stream, scratch_floats(ctas, RB, DP), 0, &sc)) return cudaErrorMemoryAllocation;
+        p.partials = sc.partials;
+        p.joins = reinterpret_cast<Join *>(sc.partials + (size_t)ctas * 2 * slot_floats(RB, DP));
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3((unsigned)threads);
@@ -602,7 +605,7 @@ cudaError_t launch_pair(K kernel, int ctas, int threads, int smem, cudaStream_t 
     cfg.numAttrs = p.share > 0 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
     if (e != cudaSuccess) return e;
-    if (ctas > 1 && !p.whole) {
+    if (cut) {
         constexpr int kColumns = kJoinColumns * join_groups(RB);
         cfg.gridDim = dim3((unsigned)ctas, (unsigned)(p.head_dim + kColumns - 1) / kColumns);
         cfg.blockDim = dim3(kJoinThreads);

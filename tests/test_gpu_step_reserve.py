@@ -81,3 +81,24 @@ def test_a_reservation_serves_smaller_head_dims(reserved, dim, new):
     graph.replay()
     torch.cuda.synchronize()
     s.check(kw["out"], kw["lse"])
+
+
+@pytest.mark.parametrize("ctx,new,heads,kv_heads", [(100, 1, 4, 4), (900, 1, 32, 4), (900, 20, 64, 8), (0, 1, 1, 1),
+                                                    (0, 70, 8, 1)])
+def test_calls_that_cut_no_row_block_need_no_scratch(ctx, new, heads, kv_heads):
+    """Short caches, on a stream that holds nothing: nothing is allocated, so they can be captured."""
+    s = Step([ctx] * 2, [new] * 2, heads, kv_heads, 128, 32, torch.float16, "tree", seed=heads)
+    args, kw = on_the_gpu(s)
+    with torch.cuda.stream(torch.cuda.Stream()):       # the kernels' code is on the GPU after this
+        awq.tree_attention(*args, new, ctx, **kw)
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    before = free_bytes()
+    with torch.cuda.stream(stream):
+        awq.tree_attention(*args, new, ctx, **kw)
+    assert free_bytes() == before
+    with torch.cuda.graph(graph, stream=stream, capture_error_mode="global"):
+        awq.tree_attention(*args, new, ctx, **kw)
+    kw["out"].fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    s.check(kw["out"], kw["lse"])
