@@ -1,6 +1,6 @@
 // awq_logits.cu -- penalties for repeated tokens, biases and grammar masks on
 // logits, in one pass over them:
-//   x = x > 0 ? x / rep : x * rep   (token known; by 1 / rep),  x -= freq * count,
+//   x = x > 0 ? x / rep : x * rep   (token known),  x -= freq * count,
 //   x -= pres (count > 0),  x += bias,  -inf where the grammar's bit is 0.
 //
 // Bound: every logit is read and written once (HBM); a row's history has a few
@@ -451,7 +451,14 @@ process_logits_kernel(const __grid_constant__ LogitsParams p)
         auto change = [&](int at, float sum) {
             float x = to_f<T>(at0[at]);
             const unsigned c = counts[at], times = c & kCount;
-            if (c & ~kListed) x *= x > 0.f ? inv : rep;
+            // Where the result is rounded to 16 bits, times the reciprocal: its rounding is
+            // 2^-13 of that one or less. (580 rows of 100000: 60.5 us with divisions; 55 with
+            // the reciprocal's remainder taken into account; 64 rows of 131072 fp32: 28, and
+            // 27 by the reciprocal.)
+            if (c & ~kListed) {
+                if constexpr (sizeof(T) == 4) x = x > 0.f ? x / rep : x * rep;
+                else x *= x > 0.f ? inv : rep;
+            }
             if (times) x = fmaf(-freq, (float)times, x) - pres;
             at0[at] = from_f<T>(x + sum);
         };

@@ -543,7 +543,8 @@ awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream);
  * in the generated part of b's history and on the row's draft path, and known =
  * whether it occurs there or in the prompt part:
  *   x = logits[r, v]
- *   x = x > 0 ? x / repetition[b] : x * repetition[b]      if known
+ *   x = x > 0 ? x / repetition[b] : x * repetition[b]      if known (16-bit logits: times
+ *       the fp32 reciprocal of repetition[b], which is one fp32 rounding more)
  *   x = x - frequency[b] * count - (count > 0 ? presence[b] : 0)
  *   x = x + sum of bias_values of token v in b's list
  *   out[r, v] = x, or -inf if bit v of grammar_mask[grammar_rows[r], :] is 0

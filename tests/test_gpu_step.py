@@ -750,6 +750,20 @@ def test_logits_chain_without_a_mask_rows_without_a_mask_and_strides():
     assert (out[:, :8] == 3).all() and (out[:, 1009:] == 3).all()
 
 
+@pytest.mark.parametrize("rep", [1.1, 1.3, 3.0, 0.7, 1e-39, 1e38])
+def test_logits_repetition_is_one_division(rep):
+    """fp32 logits are divided, not multiplied by a rounded reciprocal: one rounding, and no overflow of the reciprocal."""
+    x = torch.randn((2, 5000), generator=torch.Generator().manual_seed(1)) * 1e-3
+    x[:, :40] = torch.tensor([2.0 ** e for e in range(-148, 128, 7)])
+    x[:, 40:44] = torch.tensor([0.0, -0.0, float("inf"), -float("inf")])
+    r = torch.tensor([rep, 1.7])
+    got = awq.process_logits(x.cuda(), history=i32(np.tile(np.arange(5000), 2)), history_offsets=i32([0, 5000, 10000]),
+                             repetition=r.cuda())
+    x64, r64 = x.double(), r.double()[:, None]
+    want = torch.where(x64 > 0, x64 / r64, x64 * r64).float()
+    assert torch.equal(got.cpu(), want)
+
+
 def test_logits_infinities_and_nan():
     x = torch.tensor([[float("inf"), -float("inf"), float("nan"), 1.0, float("nan"), 2.0]], device="cuda")
     got = awq.process_logits(x, history=i32([0, 1, 2, 3]), history_offsets=i32([0, 4]),
