@@ -194,7 +194,9 @@ PyObject *paged_plan(PyObject *const *o)
     check(ctx, "context_lens", at::kInt, dev);
     check(fresh, "new_lens", at::kInt, dev, B);
     check(free_blocks, "free_blocks", at::kInt, dev);
-    if (T < 0 || words < 0) refuse("max_tokens and mask_words must not be negative");
+    // the library's own limits, before memory of that size is asked for
+    if (T < 0 || T > int64_t(1) << 30) refuse("max_tokens must be 0 to 2^30, got %lld", (long long)T);
+    if (words < 0 || words > 1024) refuse("mask_words must be 0 to 1024, got %lld", (long long)words);
     const int32_t *parents = checked<int32_t>(o[6], "parents", at::kInt, dev, T);
     int64_t width, stride;
     check_table(table, B, dev, width, stride);

@@ -136,3 +136,13 @@ def test_statuses_of_the_library_become_its_error():
         awq.process_logits(kw["logits"], bias_values=kw["bias_values"])
     torch.cuda.synchronize()
     awq.awq_last_device_status(None)
+
+
+@pytest.mark.parametrize("name,bad", [("max_tokens", 2 ** 30 + 1), ("max_tokens", 2 ** 40), ("max_tokens", 2 ** 61),
+                                      ("max_tokens", 2 ** 62), ("mask_words", 1025), ("mask_words", 2 ** 50),
+                                      ("mask_words", 2 ** 62)])
+def test_sizes_that_no_plan_has_are_refused_before_memory_is_asked_for(name, bad):
+    kw = dict(plan_arguments(), parents=None)
+    kw[name] = bad
+    with pytest.raises(ValueError, match=name):
+        awq.paged_plan(**kw)
