@@ -624,9 +624,7 @@ cudaError_t launch_rows(const awq_tree_attention_t &a, cudaStream_t stream)
         !make_cache_map_5d(&tv, a, a.v_cache, kKeys, Cfg<DP>::kHalves))
         return cudaErrorInvalidValue;
     // a launch no larger than the work the bounds allow
-    const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
-    const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
-    const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
+    const int64_t tiles = tiles_bound(a, kKeys), blocks = blocks_bound(a, kRows);
     const LaunchInfo shared = launch_info<T, DP, true>();
     if (shared.err != cudaSuccess) return shared.err;
     int share = 0;
@@ -744,7 +742,7 @@ cudaError_t launch_rows_any(const awq_tree_attention_t &a, cudaStream_t stream)
 
 cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t stream)
 {
-    const int64_t rows = a.max_new * (a.q_heads / a.kv_heads);
+    const int64_t rows = attn::rows_bound(a);
     if (a.head_dim > 128 || rows <= attn::kRows) return attn::launch_rows_any(a, stream);
     // With more rows the few-row kernel reads its keys once a block of 16. Small calls
     // still take it: if all blocks have a CTA at once (or are two a head), and as long as
@@ -754,8 +752,7 @@ cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t st
     //   16 requests,  4 tokens, 400 keys: 11 and 12   16 requests,  4 tokens, 4000 keys: 42 and 49
     //   64 requests,  4 tokens, 400 keys: 27 and 37   64 requests,  4 tokens, 4000 keys: 153 and 122
     //   16 requests,  8 tokens, 400 keys: 18 and 13   16 requests, 32 tokens, 400 keys: 42 and 20
-    const int64_t blocks = a.B * a.kv_heads * ((rows + attn::kRows - 1) / attn::kRows);
-    const int64_t tiles = (a.max_context + a.max_new + attn::kKeys - 1) / attn::kKeys;
+    const int64_t blocks = attn::blocks_bound(a, attn::kRows), tiles = attn::tiles_bound(a, attn::kKeys);
     if (blocks * tiles > (1 << 15) || (blocks > 304 && rows > 2 * attn::kRows)) return attn::launch_tc_any(a, stream);
     return attn::launch_rows_any(a, stream);
 }

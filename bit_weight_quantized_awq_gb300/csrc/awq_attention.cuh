@@ -567,6 +567,20 @@ attention_join_kernel(const __grid_constant__ Params p)
     if (col == 0) store_lse(p, j.token0, j.h, row, m == -INFINITY ? 0.f : m, l);
 }
 
+// What a call's bounds allow, as sizes whose products stay far below 2^63 whatever the
+// bounds are: rows a key-value head (a request has no more new tokens than q has), row
+// blocks of all heads, key tiles of a request.
+inline int64_t rows_bound(const awq_tree_attention_t &a) { return std::min(a.max_new, a.tokens) * (a.q_heads / a.kv_heads); }
+inline int64_t blocks_bound(const awq_tree_attention_t &a, int rows)
+{
+    const int64_t a_head = std::max<int64_t>(1, (rows_bound(a) + rows - 1) / rows);
+    return std::min(a.B * a.kv_heads * a_head, int64_t(1) << 31);
+}
+inline int64_t tiles_bound(const awq_tree_attention_t &a, int keys)
+{
+    return std::max<int64_t>(1, (a.max_context + a.max_new + keys - 1) / keys);
+}
+
 // CTAs of a launch, at most `most` of them, and how its work is laid out: `units` as
 // the bounds allow, `min_units` a CTA.
 inline int lay_out(Params &p, int most, int64_t units)

@@ -676,9 +676,7 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
     CUtensorMap tk, tv;
     if (!make_cache_map(&tk, a, a.k_cache, kKeys) || !make_cache_map(&tv, a, a.v_cache, kKeys))
         return cudaErrorInvalidValue;
-    const int64_t rows = std::max<int64_t>(1, a.max_new) * p.group;
-    const int64_t tiles = std::max<int64_t>(1, (a.max_context + a.max_new + kKeys - 1) / kKeys);
-    const int64_t blocks = a.B * a.kv_heads * ((rows + kRows - 1) / kRows);
+    const int64_t tiles = tiles_bound(a, kKeys), blocks = blocks_bound(a, kRows);
     p.whole = tiles <= kWholeTiles;
     p.min_units = p.whole ? 1 : kBlockCost<kRows> + 4;
     const int64_t units = p.whole ? blocks : blocks * (kBlockCost<kRows> + (kRows > 128 ? 2 : 1) * tiles);
@@ -694,7 +692,7 @@ cudaError_t launch_tc(const awq_tree_attention_t &a, cudaStream_t stream)
 template <typename T, int DP>
 cudaError_t launch_tc_rows(const awq_tree_attention_t &a, cudaStream_t stream)
 {
-    return a.max_new * (a.q_heads / a.kv_heads) <= 128 ? launch_tc<T, DP, 128>(a, stream) : launch_tc<T, DP, 256>(a, stream);
+    return rows_bound(a) <= 128 ? launch_tc<T, DP, 128>(a, stream) : launch_tc<T, DP, 256>(a, stream);
 }
 
 cudaError_t launch_tc_any(const awq_tree_attention_t &a, cudaStream_t stream)

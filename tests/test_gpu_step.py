@@ -405,6 +405,26 @@ def test_attention_bounds_that_are_too_small_or_large(new):
         s.check(*s.run(max_new=bounds[0], max_context=bounds[1]))
 
 
+def test_attention_with_bounds_of_any_size_has_the_whole_gpu():
+    """The largest bounds that are taken: products of them that do not fit 64 bits left a CTA a head."""
+    s = Step([600] * 256, [1] * 256, 64, 8, 64, 16, torch.float16, "causal", seed=2)
+    args = (s.q.cuda(), s.k.cuda(), s.v.cuda(), i32(s.table), i32(s.ctx), i32(s.cu), 0.125)
+
+    def ms(most):
+        times = []
+        for _ in range(6):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            out = awq.tree_attention(*args, most, most)
+            end.record()
+            end.synchronize()
+            times.append(begin.elapsed_time(end))
+        return min(times), out
+    (tight, a), (loose, b) = ms(601), ms(2 ** 31 - 1)
+    assert (a.float() - b.float()).abs().max() <= 2.0 ** -9
+    assert loose <= 5 * tight
+
+
 def test_attention_rows_past_the_last_token_stay():
     s = Step([30], [3], 4, 2, 64, 16, torch.float16, "causal")
     s.scale = 0.1
