@@ -9,14 +9,16 @@ from __future__ import annotations
 
 import ctypes
 import enum
-import importlib.metadata
 import os
+import sys
 import threading
+
+import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libawq_gb300.so")
-# the module behind step.py, for the torch that is installed
-STEP_PATH = os.path.join(os.path.dirname(LIB_PATH), f"awq_step-{importlib.metadata.version('torch')}.so")
+# the module behind step.py, for the torch that is installed and the interpreter that runs
+STEP_PATH = os.path.join(os.path.dirname(LIB_PATH), f"awq_step-{torch.__version__}-{sys.implementation.cache_tag}.so")
 
 # Every function the header declares; tests check the library exports them.
 EXPORTED = (

@@ -10,7 +10,7 @@ decode, prefill and attention kernels) compiled again with ``-DAWQ_FAULT_TEST`` 
 limit of about 2 ms and the switch declared in
 ``include/awq_gb300_fault_test.h``), linked with the other units' objects.
 
-And ``_build/awq_step-<torch version>.so``, the Python module behind ``step.py``
+And ``_build/awq_step-<torch version>-<interpreter>.so``, the Python module behind ``step.py``
 (``csrc/awq_step_module.cpp``, compiled with the host compiler against the
 installed torch).
 
@@ -20,7 +20,6 @@ from __future__ import annotations
 
 import argparse
 import glob
-import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -28,6 +27,8 @@ import subprocess
 import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
+
+from ._binding import STEP_PATH as STEP_MODULE
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -40,7 +41,6 @@ FAULT_BUILD = os.path.join(BUILD, "fault_test")
 FAULT_UNITS = ("awq_api.cu", "awq_decode.cu", "awq_prefill.cu", "awq_attention.cu", "awq_attention_tc.cu")
 INCLUDE = os.path.join(ROOT, "include")
 STEP_SOURCE = os.path.join(CSRC, "awq_step_module.cpp")
-STEP_MODULE = os.path.join(BUILD, f"awq_step-{importlib.metadata.version('torch')}.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -1,5 +1,9 @@
 """Host-only checks of the decoding step's entry points: every refusal comes
 before any CUDA call, so these run without a GPU."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -176,3 +180,20 @@ def test_wrappers_refuse_tensors_of_another_than_the_current_device():
                  lambda: awq.tree_attention(q, cache, cache, table, i, i, 1.0, 2, 0), lambda: awq.process_logits(x)):
         with pytest.raises(ValueError, match="current CUDA device"):
             call()
+
+
+def test_package_imports_with_a_torch_that_has_no_package_metadata():
+    """A torch of one's own build on the path, say; and the module's name tells torch and Python apart."""
+    code = """
+import importlib.metadata, sys
+def missing(name, *_):
+    raise importlib.metadata.PackageNotFoundError(name)
+import torch
+importlib.metadata.version = missing
+from bit_weight_quantized_awq_gb300 import _binding, build
+assert build.STEP_MODULE == _binding.STEP_PATH
+assert torch.__version__ in _binding.STEP_PATH and sys.implementation.cache_tag in _binding.STEP_PATH
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
