@@ -746,14 +746,23 @@ cudaError_t launch_tree_attention(const awq_tree_attention_t &a, cudaStream_t st
     if (a.head_dim > 128 || rows <= attn::kRows) return attn::launch_rows_any(a, stream);
     // With more rows the few-row kernel reads its keys once a block of 16. Small calls
     // still take it: if all blocks have a CTA at once (or are two a head), and as long as
-    // that costs no more than the tensor-core kernel's longer way in and out, 8 us.
-    // 64 / 8 heads of 128, us with this kernel and with the other:
-    //    1 request,  32 tokens, 400 keys: 12 and 19    1 request,  32 tokens, 4000 keys: 31 and 32
-    //   16 requests,  4 tokens, 400 keys: 11 and 12   16 requests,  4 tokens, 4000 keys: 42 and 49
-    //   64 requests,  4 tokens, 400 keys: 27 and 37   64 requests,  4 tokens, 4000 keys: 153 and 122
-    //   16 requests,  8 tokens, 400 keys: 18 and 13   16 requests, 32 tokens, 400 keys: 42 and 20
+    // that costs no more than the tensor-core kernel's longer way in and out: up to about
+    // 20,000 tiles of 32 keys, read again by each block. Us with this kernel and with the other:
+    //   64 / 8 heads of 128     1 request,  64 tokens, 2000 keys (17k tiles): 33 and 36
+    //                           1 request,  64 tokens, 3000 keys (25k): 40 and 36
+    //                           1 request,  64 tokens, 4000 keys (33k): 48 and 35
+    //                          16 requests,  4 tokens,  400 keys  (3k): 12 and 17
+    //                          16 requests,  4 tokens, 2000 keys (16k): 40 and 48
+    //                          16 requests,  4 tokens, 3000 keys (24k): 55 and 58
+    //                          16 requests,  4 tokens, 4000 keys (32k): 76 and 67
+    //                           4 requests, 16 tokens, 4000 keys (32k): 53 and 34
+    //   32 / 8 heads of 64      1 request,  64 tokens, 4000 keys (16k): 25 and 28
+    //                          16 requests,  8 tokens, 2000 keys (16k): 27 and 34
+    //                           4 requests,  5 tokens, 16000 keys (32k): 41 and 38
+    // and where not all blocks have a CTA at once, 64 / 8 heads of 128, 400 keys:
+    //   16 requests, 8 tokens: 18 and 13; 32 tokens: 42 and 23
     const int64_t blocks = attn::blocks_bound(a, attn::kRows), tiles = attn::tiles_bound(a, attn::kKeys);
-    if (blocks * tiles > (1 << 15) || (blocks > 304 && rows > 2 * attn::kRows)) return attn::launch_tc_any(a, stream);
+    if (blocks * tiles > 20000 || (blocks > 304 && rows > 2 * attn::kRows)) return attn::launch_tc_any(a, stream);
     return attn::launch_rows_any(a, stream);
 }
 

@@ -251,3 +251,15 @@ def test_a_captured_call_follows_the_lengths():
     on_tensor_cores(graph.replay, joined=True)
     torch.cuda.synchronize()
     later.check(out, lse)
+
+
+@pytest.mark.parametrize("requests,new,ctx,few", [(1, 64, 4000, False), (4, 16, 4000, False), (1, 32, 4000, True),
+                                                  (1, 64, 2000, True), (16, 4, 2000, True), (16, 8, 400, False)])
+def test_each_call_takes_the_faster_kernel(requests, new, ctx, few):
+    """64 / 8 heads of 128: sizes at which the two kernels were timed against each other."""
+    s = Step([ctx] * requests, [new] * requests, 64, 8, 128, 64, torch.float16, "tree")
+    args = (s.q.cuda(), s.k.cuda(), s.v.cuda(), i32(s.table), i32(s.ctx), i32(s.cu), 0.1, new, ctx)
+    mask = s.mask.cuda()
+    names = kernels_of(lambda: awq.tree_attention(*args, tree_mask=mask))
+    if names:
+        assert any("attention_rows_kernel" in n for n in names) == few, names
