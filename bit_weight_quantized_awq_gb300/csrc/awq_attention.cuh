@@ -379,6 +379,11 @@ struct Pages {
 
 // ---- element types ----
 
+// The softmax weights are rounded to q's type for their product with v: a matrix
+// instruction takes both operands in one 16-bit type, and a second product with what the
+// rounding left would double that work. Their sum takes them unrounded, in fp32. Relative
+// error of the output against 64 bits, its own rounding included: fp16 2.6e-4 to 2.9e-4, bf16
+// 2.2e-3 to 2.4e-3; with weights in fp32 2.1e-4 and 1.7e-3.
 template <typename T>
 struct Elem;
 template <>

@@ -30,7 +30,7 @@
 // them a stream and tile).
 //
 // Measured: 12 requests with trees of 64 over up to 16384 keys, 64 / 8 heads of 128,
-// fp16: 224 to 238 us, half of the bf16 matrix rate (tensor pipe 59% busy: S in halves
+// fp16: 224 to 238 us, half of the bf16 matrix rate (tensor pipe 56% busy: S in halves
 // of 64 keys reads q twice a tile); 16 requests with trees of 13 over up to 6000 keys,
 // bf16: 66 us, 59% of the copy bandwidth; a tree of 26 over 131072 keys, 32 / 8 heads
 // of 64: 59 us, 68%.

@@ -19,7 +19,7 @@
 // 67 us.) Consecutive rows of one request -- the nodes of a drafted tree -- share
 // the counts: only the tokens in which the rows' paths differ are added or taken
 // back. Counts are whole numbers, so the atomics' order does not matter.
-// Measured: 64 rows of 131072 fp32 logits, histories of up to 4000 tokens: 27 us (13
+// Measured: 64 rows of 131072 fp32 logits, histories of up to 4000 tokens: 28 us (13
 // without a history; a plain copy takes 14); 580 rows of 100000 bf16 logits of 16
 // requests' trees: 53 us, 65% of the copy bandwidth; one row of 32000: 5.6 us.
 #include <algorithm>
@@ -44,8 +44,9 @@ constexpr int kRange = 16384 / sizeof(T);
 // A counter: in the prompt, in the list of the entries met, and the generated count.
 constexpr unsigned kPrompt = 1u << 31, kListed = 1u << 30, kCount = kListed - 1;
 // Up to this many tokens of a lane are counted one by one, more of them all at once: 64
-// rows of 131072 fp32 logits with histories of up to 4,000 tokens took 27 us so; 30 us
-// all one by one, where a third of the tokens fell into one range; with the tokens
+// rows of 131072 fp32 logits with histories of up to 4,000 tokens took 27 us so (28 since
+// they are divided by the penalty); 30 us all one by one, where a third of the tokens
+// fell into one range; with the tokens
 // spread evenly 20 us, and 23 all at once.
 constexpr int kTurns = 4;
 constexpr int kPairs = 2;                 // biases a thread keeps

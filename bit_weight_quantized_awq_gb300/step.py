@@ -84,7 +84,9 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     requests' caches, their own keys and values included: a token sees its whole
     context and, of the new tokens, those of its ``tree_mask`` row (itself and
     the ones before it if None). ``max_new`` and ``max_context`` bound the
-    lengths; ``lse`` (fp32 [tokens, q_heads]) receives the log-sum-exp."""
+    lengths; ``lse`` (fp32 [tokens, q_heads]) receives the log-sum-exp. Rows of q past
+    ``cu_new``'s end (a plan's padding) are left as they are in ``out``: undefined
+    where the call makes it."""
     made = (_step or _load()).tree_attention(q, k_cache, v_cache, block_table, context_lens, cu_new, scale, max_new,
                                              max_context, tree_mask, out, lse)
     if type(made) is int:

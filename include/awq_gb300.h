@@ -571,7 +571,8 @@ awq_status_t awq_reserve_tree_attention(int64_t head_dim, awq_stream_t stream);
  *   logits, out    fp16, bf16 or fp32 (dtype), the elements of a row contiguous,
  *                  rows `*_row_stride` elements apart; out == logits is allowed
  *                  (with the same stride)
- * A token, offset, request or mask index out of range is skipped and reported; a
+ * A token, offset, request or mask index out of range is skipped and reported (a
+ * history and a draft of a request whose three settings change nothing are not looked at); a
  * bias list that is not sorted is reported. Requires rows >= 0, 0 < vocab <= 2^27,
  * 0 <= B < 2^31, history_size < 2^29 (a token's count has 30 bits), bias_size <= 2^30,
  * logits and out aligned to their elements.
