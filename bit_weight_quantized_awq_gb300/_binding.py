@@ -49,6 +49,15 @@ EXPORTED = (
     "awq_tree_attention",
     "awq_reserve_tree_attention",
     "awq_process_logits",
+    "awq_rotary",
+    "awq_beam_select",
+    "awq_beam_select_workspace",
+    "awq_reorder_states",
+    "awq_fork_pages",
+    "awq_copy_pages",
+    "awq_free_pages",
+    "awq_pages_workspace",
+    "awq_compact_pages",
 )
 
 RESERVE_SORTED = 1
@@ -117,6 +126,30 @@ class Logits(ctypes.Structure):
                 ("mask_words", _I64), ("bias_tokens", _P), ("bias_offsets", _P), ("bias_values", _P),
                 ("bias_size", _I64), ("grammar_mask", _P), ("grammar_rows", _P), ("grammar_count", _I64),
                 ("dtype", _I32)]
+
+
+class Rotary(ctypes.Structure):
+    """awq_rotary_t"""
+    _fields_ = [("q", _P), ("k", _P), ("v", _P), ("q_token_stride", _I64), ("q_head_stride", _I64),
+                ("k_token_stride", _I64), ("k_head_stride", _I64), ("v_token_stride", _I64), ("v_head_stride", _I64),
+                ("q_out", _P), ("k_out", _P), ("q_out_token_stride", _I64), ("q_out_head_stride", _I64),
+                ("k_out_token_stride", _I64), ("k_out_head_stride", _I64), ("positions", _P), ("inv_freq", _P),
+                ("axes", _P), ("k_cache", Cache), ("v_cache", Cache), ("slot_map", _P), ("num_blocks", _I64),
+                ("block_size", _I64), ("tokens", _I64), ("q_heads", _I64), ("kv_heads", _I64), ("head_dim", _I64),
+                ("rotary_dim", _I64), ("num_axes", _I64), ("pairs", _I32), ("dtype", _I32)]
+
+
+class BeamSelect(ctypes.Structure):
+    """awq_beam_select_t"""
+    _fields_ = [("logits", _P), ("logits_row_stride", _I64), ("requests", _I64), ("beams", _I64), ("vocab", _I64),
+                ("scores", _P), ("num_beams", _I64), ("end_tokens", _P), ("num_ends", _I64), ("out_scores", _P),
+                ("out_parents", _P), ("out_tokens", _P), ("ended_scores", _P), ("ended_parents", _P),
+                ("ended_tokens", _P), ("workspace", _P), ("workspace_bytes", _I64), ("dtype", _I32)]
+
+
+class State(ctypes.Structure):
+    """awq_state_t"""
+    _fields_ = [("src", _P), ("dst", _P), ("src_row_stride", _I64), ("dst_row_stride", _I64), ("row_bytes", _I64)]
 
 
 def _arg(value):
@@ -192,6 +225,25 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.awq_reserve_tree_attention.restype = _INT
         lib.awq_process_logits.argtypes = [_P, _P]
         lib.awq_process_logits.restype = _INT
+        lib.awq_rotary.argtypes = [_P, _P]
+        lib.awq_rotary.restype = _INT
+        lib.awq_beam_select.argtypes = [_P, _P]
+        lib.awq_beam_select.restype = _INT
+        lib.awq_beam_select_workspace.argtypes = [_I64, _I64, _I64, _I64, _I64, _INT]
+        lib.awq_beam_select_workspace.restype = _I64
+        lib.awq_reorder_states.argtypes = [_P, _I64, _P, _I64, _I64, _P]
+        lib.awq_reorder_states.restype = _INT
+        lib.awq_fork_pages.argtypes = [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P,
+                                       _P, _P]
+        lib.awq_fork_pages.restype = _INT
+        lib.awq_copy_pages.argtypes = [_P, _I64, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _I64, _P, _P]
+        lib.awq_copy_pages.restype = _INT
+        lib.awq_free_pages.argtypes = [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _P, _P, _P]
+        lib.awq_free_pages.restype = _INT
+        lib.awq_pages_workspace.argtypes = [_I64]
+        lib.awq_pages_workspace.restype = _I64
+        lib.awq_compact_pages.argtypes = [_P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P]
+        lib.awq_compact_pages.restype = _INT
         lib.awq_shutdown.argtypes = []
         lib.awq_shutdown.restype = None
         _lib = lib
@@ -312,6 +364,54 @@ def awq_reserve_tree_attention(head_dim, stream) -> int:
 
 def awq_process_logits(args: Logits, stream) -> int:
     return load_library().awq_process_logits(_arg(args), stream)
+
+
+def awq_rotary(args: Rotary, stream) -> int:
+    return load_library().awq_rotary(_arg(args), stream)
+
+
+def awq_beam_select(args: BeamSelect, stream) -> int:
+    return load_library().awq_beam_select(_arg(args), stream)
+
+
+def awq_beam_select_workspace(requests, beams, vocab, num_beams, num_ends, dtype) -> int:
+    return load_library().awq_beam_select_workspace(requests, beams, vocab, num_beams, num_ends, int(dtype))
+
+
+def awq_reorder_states(states, count, parents, rows_out, rows_in, stream) -> int:
+    """``states``: a ctypes array of State, or None."""
+    return load_library().awq_reorder_states(states, count, parents, rows_out, rows_in, stream)
+
+
+def awq_fork_pages(block_table, rows_in, table_width, table_stride, lens, parents, rows_out, free_blocks, num_free,
+                   free_start, block_size, new_table, new_stride, new_lens, src, dst, tokens, count, stream) -> int:
+    return load_library().awq_fork_pages(block_table, rows_in, table_width, table_stride, lens, parents, rows_out,
+                                         free_blocks, num_free, free_start, block_size, new_table, new_stride, new_lens,
+                                         src, dst, tokens, count, stream)
+
+
+def awq_copy_pages(caches, num_caches, layout: Cache, num_blocks, block_size, kv_heads, head_dim, src, dst, tokens,
+                   pairs, count, stream) -> int:
+    """``caches``: a ctypes array of addresses, or None."""
+    return load_library().awq_copy_pages(caches, num_caches, _arg(layout), num_blocks, block_size, kv_heads, head_dim,
+                                         src, dst, tokens, pairs, count, stream)
+
+
+def awq_free_pages(block_table, rows, table_width, table_stride, lens, block_size, num_blocks, held, num_held,
+                   free_blocks, counts, workspace, stream) -> int:
+    return load_library().awq_free_pages(block_table, rows, table_width, table_stride, lens, block_size, num_blocks,
+                                         held, num_held, free_blocks, counts, workspace, stream)
+
+
+def awq_pages_workspace(num_blocks) -> int:
+    return load_library().awq_pages_workspace(num_blocks)
+
+
+def awq_compact_pages(block_table, rows, table_width, table_stride, lens, block_size, num_blocks, held, num_held,
+                      new_table, new_stride, block_map, src, dst, count, workspace, stream) -> int:
+    return load_library().awq_compact_pages(block_table, rows, table_width, table_stride, lens, block_size, num_blocks,
+                                            held, num_held, new_table, new_stride, block_map, src, dst, count,
+                                            workspace, stream)
 
 
 def awq_shutdown() -> None:

@@ -158,6 +158,66 @@ size_t tree_attention_partial_floats(int64_t head_dim, int sms);
 
 cudaError_t launch_process_logits(const awq_logits_t &a, cudaStream_t stream);
 
+cudaError_t launch_rotary(const awq_rotary_t &a, cudaStream_t stream);
+
+// stretches that a row of logits is read in
+int beam_stretches(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes);
+cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream);
+
+cudaError_t launch_reorder_states(const awq_state_t *states, int64_t count, const int32_t *parents, int64_t rows_out,
+                                  int64_t rows_in, cudaStream_t stream);
+
+struct ForkProblem {
+    const int32_t *table, *lens, *parents, *free_blocks, *free_start;
+    int32_t *new_table, *new_lens, *src, *dst, *tokens, *count;
+    int64_t stride, new_stride;
+    int rows_in, rows_out, width, num_free, block_size;
+};
+cudaError_t launch_fork_pages(const ForkProblem &p, cudaStream_t stream);
+
+struct CopyProblem {
+    void *const *caches;
+    awq_cache_t layout;
+    const int32_t *src, *dst, *tokens, *count;
+    int64_t num_caches, pairs;
+    int num_blocks, block_size, kv_heads, head_dim;
+};
+cudaError_t launch_copy_pages(const CopyProblem &p, cudaStream_t stream);
+
+// Of awq_free_pages (free_blocks is set) and of awq_compact_pages.
+struct PagesProblem {
+    const int32_t *table, *lens, *held;
+    int32_t *free_blocks, *counts;
+    int32_t *new_table, *block_map, *src, *dst, *moves;
+    uint32_t *workspace;
+    int64_t stride, new_stride, num_held;
+    int rows, width, block_size, num_blocks;
+};
+cudaError_t launch_pages(const PagesProblem &p, cudaStream_t stream);
+
+// Allows a kernel this much dynamic shared memory on the current device, once: a limit of a
+// call's own size could be lowered by another thread's call before this one's launch.
+cudaError_t allow_shared(const void *kernel, size_t bytes);
+
+// A launch whose grid may be scheduled before the kernel ahead of it in the stream has
+// ended; the kernel waits for it by itself (ptx::wait_prerequisites).
+inline cudaError_t launch_dependent(const void *kernel, int64_t grid, int block, size_t smem, cudaStream_t stream,
+                                    void **args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 // fp16 weight columns per window of the dequantise-then-GEMM path
 int64_t dequant_gemm_window(int64_t K, int64_t N);
 

@@ -253,22 +253,6 @@ kv_append_kernel(const AppendParams p, unsigned int *status)
     }
 }
 
-cudaError_t launch_dependent(const void *kernel, int64_t grid, int block, size_t smem, cudaStream_t stream, void **args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 // The plan kernel's shared memory, two sums a request.
 constexpr size_t plan_smem_bytes(int64_t B) { return (size_t)2 * (B + 1) * sizeof(unsigned); }
 

@@ -1,0 +1,467 @@
+// awq_pages.cu -- the pages of a paged cache between steps: fork_kernel (block tables of
+// the beams that go on), copy_pages_kernel (pages within caches), and the kernels that
+// list the free blocks and compact the used ones (mark_kernel, list_kernel, move_kernel).
+#include <algorithm>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include <cuda_runtime.h>
+
+#include "awq_device.cuh"
+#include "awq_internal.h"
+
+namespace awq {
+
+cudaError_t allow_shared(const void *kernel, size_t bytes)
+{
+    static std::mutex mu;
+    static std::map<std::pair<int, const void *>, unsigned> done;   // -> cache generation
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned gen = cache_generation();
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_pair(dev, kernel);
+    const auto it = done.find(key);
+    if (it != done.end() && it->second == gen) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done[key] = gen;
+    return e;
+}
+
+namespace {
+
+// A row's pages: lengths are read as max(length, 0), and none is longer than the table's width.
+__device__ __forceinline__ int pages_of(int length, int block_size, int shift, int width, unsigned &bad)
+{
+    if (length < 0) {
+        bad |= kStatusBadIndex;
+        return 0;
+    }
+    const unsigned pages = ((unsigned)length + block_size - 1) >> shift;
+    if (pages > (unsigned)width) {
+        bad |= kStatusTooLarge;
+        return width;
+    }
+    return (int)pages;
+}
+
+// ---------------------------------------------------------------------------
+// Fork. Which row is its parent's first and how many rows before it need a block follows
+// from the parents and lengths alone; every CTA computes both for all rows by itself, as the plan
+// does, so the step is one launch. Bound: latency; the tables are a few KB to a few MB.
+
+constexpr int kForkThreads = 512;
+constexpr int kForkEntries = 2048;          // of a row, a CTA and turn
+constexpr int kForkRows = 16384;
+
+__global__ void __launch_bounds__(kForkThreads)
+fork_kernel(const __grid_constant__ ForkProblem p, unsigned int *status)
+{
+    extern __shared__ int fork_smem[];
+    int *first = fork_smem;                 // [rows_in] the first row of each parent
+    int *rank = fork_smem + p.rows_in;      // [rows_out] 2 * blocks taken before the row + whether it takes one
+    __shared__ int sums[kForkThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int shift = __ffs(p.block_size) - 1, mask = p.block_size - 1;
+    unsigned bad = 0;
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+
+    for (int i = tid; i < p.rows_in; i += kForkThreads) first[i] = p.rows_out;
+    __syncthreads();
+    for (int r = tid; r < p.rows_out; r += kForkThreads) {
+        const int parent = p.parents[r];
+        if (parent < -1 || parent >= p.rows_in) bad |= kStatusBadIndex;
+        if (parent >= 0 && parent < p.rows_in) atomicMin(&first[parent], r);
+    }
+    __syncthreads();
+    int carry = 0;
+    for (int r0 = 0; r0 < p.rows_out; r0 += kForkThreads) {
+        const int r = r0 + tid;
+        bool need = false;
+        if (r < p.rows_out) {
+            const int parent = p.parents[r];
+            if (parent >= 0 && parent < p.rows_in && first[parent] != r) {
+                const int length = p.lens[parent];
+                // a length beyond the table's width has no page to copy
+                need = length > 0 && (length & mask) && (length >> shift) < p.width;
+            }
+        }
+        const unsigned votes = __ballot_sync(0xFFFFFFFFu, need);
+        if (lane == 0) sums[warp] = __popc(votes);
+        __syncthreads();
+        int before = carry;
+        for (int w = 0; w < kForkThreads / 32; ++w) {
+            if (w < warp) before += sums[w];
+            carry += sums[w];
+        }
+        if (r < p.rows_out) rank[r] = 2 * (before + __popc(votes & ((1u << lane) - 1))) + need;
+        __syncthreads();
+    }
+    int start = p.free_start ? *p.free_start : 0;
+    if (start < 0) {
+        bad |= kStatusBadIndex;
+        start = 0;
+    }
+    auto fresh = [&](int n) { return (int64_t)start + n < p.num_free ? max(p.free_blocks[start + n], -1) : -1; };
+
+    // ---- what there is one of a row
+    const int grid_threads = gridDim.x * kForkThreads;
+    if (blockIdx.x == 0 && tid == 0) {
+        *p.count = carry;
+        if ((int64_t)start + carry > p.num_free && carry > 0) bad |= kStatusTooLarge;
+    }
+    for (int r = blockIdx.x * kForkThreads + tid; r < p.rows_out; r += grid_threads) {
+        const int parent = p.parents[r];
+        const bool row = parent >= 0 && parent < p.rows_in;
+        const int length = row ? p.lens[parent] : 0;
+        pages_of(length, p.block_size, shift, p.width, bad);
+        p.new_lens[r] = max(length, 0);
+        const int n = rank[r] >> 1;
+        if (rank[r] & 1) {
+            const int to = fresh(n), from = p.table[parent * p.stride + (length >> shift)];
+            if (to < 0 && (int64_t)start + n < p.num_free) bad |= kStatusBadIndex;
+            if (from < 0) bad |= kStatusBadIndex;
+            p.src[n] = to < 0 ? -1 : from;
+            p.dst[n] = to;
+            p.tokens[n] = length & mask;
+        }
+        if (r >= carry) p.src[r] = p.dst[r] = p.tokens[r] = -1;
+    }
+
+    // ---- the tables
+    const int chunks = (p.width + kForkEntries - 1) / kForkEntries;
+    for (int64_t u = blockIdx.x; u < (int64_t)p.rows_out * chunks; u += gridDim.x) {
+        const int r = (int)(u / chunks), j0 = (int)(u - (int64_t)r * chunks) * kForkEntries + tid;
+        const int parent = p.parents[r];
+        unsigned ignored = 0;
+        const bool row = parent >= 0 && parent < p.rows_in;
+        const int have = row ? pages_of(p.lens[parent], p.block_size, shift, p.width, ignored) : 0;
+        int v[kForkEntries / kForkThreads];
+#pragma unroll
+        for (int i = 0; i < kForkEntries / kForkThreads; ++i) {
+            const int j = j0 + i * kForkThreads;
+            v[i] = -1;
+            if (j >= have) continue;
+            v[i] = j == have - 1 && (rank[r] & 1) ? fresh(rank[r] >> 1) : p.table[parent * p.stride + j];
+        }
+#pragma unroll
+        for (int i = 0; i < kForkEntries / kForkThreads; ++i) {
+            const int j = j0 + i * kForkThreads;
+            if (j < p.width) p.new_table[r * p.new_stride + j] = v[i];
+        }
+    }
+    if (bad) raise_status(status, bad);
+}
+
+// ---------------------------------------------------------------------------
+// Copies of pages, 16 bytes at a time, kCopyPieces of a thread under way. A unit is a
+// part of one page of one cache; the CTAs take units in turn, since how many there are is known
+// on the device only. Bound: HBM, each byte read and written once.
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyPieces = 8;
+constexpr int kCachesPerLaunch = 256;
+
+struct CopyParams {
+    char *cache[kCachesPerLaunch];
+    const int32_t *src, *dst, *tokens, *count;
+    unsigned int *status;
+    int64_t pairs;
+    int64_t block, token, head;       // strides in bytes
+    int caches, num_blocks, block_size, parts;
+    int row_pieces, head_pieces;      // of a token, of a head
+    bool heads_first;                 // a head's tokens lie together
+};
+
+__global__ void __launch_bounds__(kCopyThreads)
+copy_pages_kernel(const __grid_constant__ CopyParams p)
+{
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    int64_t pairs = p.pairs;
+    if (p.count) pairs = min(pairs, (int64_t)max(*p.count, 0));
+    const int64_t each = (int64_t)p.caches * p.parts;
+    for (int64_t u = blockIdx.x; u < pairs * each; u += gridDim.x) {
+        const int64_t n = u / each;
+        const int rest = (int)(u - n * each), cache = rest / p.parts, part = rest - cache * p.parts;
+        const int from = p.src[n], to = p.dst[n];
+        int tokens = p.tokens ? p.tokens[n] : p.block_size;
+        if (from == -1 || to == -1) continue;
+        if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks || tokens < 0 || tokens > p.block_size) {
+            if (threadIdx.x == 0) raise_status(p.status, kStatusBadIndex);
+            if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) continue;
+            tokens = min(max(tokens, 0), p.block_size);
+        }
+        if (from == to) continue;
+        const int pieces = tokens * p.row_pieces, e0 = part * kCopyThreads * kCopyPieces + threadIdx.x;
+        const char *src = p.cache[cache] + from * p.block;
+        char *dst = p.cache[cache] + to * p.block;
+        uint4 v[kCopyPieces];
+        int64_t at[kCopyPieces];
+#pragma unroll
+        for (int k = 0; k < kCopyPieces; ++k) {
+            const int e = e0 + k * kCopyThreads;
+            at[k] = -1;
+            if (e >= pieces) continue;
+            int token, head, piece;
+            if (p.heads_first) {
+                const int row = e / p.head_pieces;
+                piece = e - row * p.head_pieces;
+                head = row / tokens;
+                token = row - head * tokens;
+            } else {
+                token = e / p.row_pieces;
+                piece = e - token * p.row_pieces;
+                head = piece / p.head_pieces;
+                piece -= head * p.head_pieces;
+            }
+            at[k] = token * p.token + head * p.head + piece * 16;
+            v[k] = *reinterpret_cast<const uint4 *>(src + at[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kCopyPieces; ++k)
+            if (at[k] >= 0) *reinterpret_cast<uint4 *>(dst + at[k]) = v[k];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Used blocks as a bitmap, set from the tables (a bit that is set twice stays set: no
+// counts, and no order that results could depend on); then free blocks and moves are
+// numbered by the bits before them.
+
+constexpr int kPageThreads = 512;
+
+// Sum of v over the threads before this one, and over all.
+__device__ __forceinline__ int block_scan(int v, int *sums, int &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, s, d);
+        if (lane >= d) s += o;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+    for (int w = 0; w < kPageThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    return before + s - v;
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+clear_kernel(uint4 *words, int64_t n)
+{
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kPageThreads)
+        words[i] = make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void mark(const PagesProblem &p, int block, unsigned &bad)
+{
+    if (block < 0 || block >= p.num_blocks) bad |= kStatusBadIndex;
+    else atomicOr(&p.workspace[block >> 5], 1u << (block & 31));
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+mark_kernel(const __grid_constant__ PagesProblem p, unsigned int *status)
+{
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    const int shift = __ffs(p.block_size) - 1;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * kPageThreads / 32;
+    const int64_t warp = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) / 32;
+    unsigned bad = 0;
+    // a warp a piece of 256 entries of a row
+    const int parts = (p.width + 255) / 256;
+    for (int64_t u = warp; u < (int64_t)p.rows * parts; u += warps) {
+        const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
+        const int have = pages_of(p.lens[r], p.block_size, shift, p.width, bad);
+        int v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i * 32 + lane;
+            if (j < have) v[i] = p.table[r * p.stride + j];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j0 + i * 32 + lane < have) mark(p, v[i], bad);
+    }
+    for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < p.num_held;
+         i += (int64_t)gridDim.x * kPageThreads)
+        if (p.held[i] != -1) mark(p, p.held[i], bad);
+    if (bad) raise_status(status, bad);
+}
+
+// A CTA numbers the blocks of its words; it counts the bits before them, and all of them, by itself.
+__global__ void __launch_bounds__(kPageThreads)
+list_kernel(const __grid_constant__ PagesProblem p)
+{
+    __shared__ int sums[kPageThreads / 32];
+    const int tid = threadIdx.x;
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    const int words = (p.num_blocks + 31) / 32;
+    const int w = blockIdx.x * kPageThreads + tid, w0 = blockIdx.x * kPageThreads;
+    int before = 0, all = 0, ignored;
+    for (int i = tid; i < words; i += kPageThreads) {
+        const int n = __popc(p.workspace[i]);
+        all += n;
+        if (i < w0) before += n;
+    }
+    int used, used_before;
+    block_scan(all, sums, used);
+    block_scan(before, sums, used_before);
+    uint32_t word = w < words ? p.workspace[w] : 0;
+    used_before += block_scan(__popc(word), sums, ignored);
+    const int first = w * 32, blocks = w < words ? min(32, p.num_blocks - first) : 0;
+
+    if (p.free_blocks) {
+        if (w == 0) {
+            p.counts[0] = p.num_blocks - used;
+            p.counts[1] = used;
+        }
+        int at = first - used_before;
+        for (int i = 0; i < blocks; ++i) {
+            if (word >> i & 1) p.free_blocks[p.num_blocks - 1 - (used_before++)] = -1;
+            else p.free_blocks[at++] = first + i;
+        }
+        return;
+    }
+    // used blocks below `used` stay; of the others each takes the free block of its own rank there
+    int stay = 0;
+    for (int i = tid; i < words; i += kPageThreads) {
+        const int left = used - i * 32;
+        if (left > 0) stay += __popc(left >= 32 ? p.workspace[i] : p.workspace[i] & ((1u << left) - 1));
+    }
+    int stays;
+    block_scan(stay, sums, stays);
+    if (w == 0) *p.moves = used - stays;
+    if (w < words) p.workspace[words + w] = used_before;       // for the ranks that move_kernel looks up
+    const int half = p.num_blocks / 2;
+    for (int i = 0; i < blocks; ++i) {
+        const int b = first + i;
+        const bool in_use = word >> i & 1;
+        if (!in_use && b < used) p.dst[b - used_before] = b;
+        if (in_use && b >= used) p.src[used_before - stays] = b;
+        if (!in_use || b < used) p.block_map[b] = in_use ? b : -1;
+        if (b < half && b >= used - stays) p.src[b] = p.dst[b] = -1;
+        used_before += in_use;
+    }
+}
+
+// The map of the blocks that move, and the tables with the new numbers.
+__global__ void __launch_bounds__(kPageThreads)
+move_kernel(const __grid_constant__ PagesProblem p)
+{
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    const int shift = __ffs(p.block_size) - 1, words = (p.num_blocks + 31) / 32;
+    const int moves = *p.moves;
+    const int64_t thread = (int64_t)blockIdx.x * kPageThreads + threadIdx.x, threads = (int64_t)gridDim.x * kPageThreads;
+    for (int64_t i = thread; i < moves; i += threads) p.block_map[p.src[i]] = p.dst[i];
+    // the first block that moves tells where the moving ones begin
+    const int first = moves > 0 ? p.src[0] : p.num_blocks;
+    const int skipped = moves > 0 ? (int)p.workspace[words + (first >> 5)] +
+                                        __popc(p.workspace[first >> 5] & ((1u << (first & 31)) - 1)) : 0;
+    const int lane = threadIdx.x & 31;
+    const int parts = (p.width + 255) / 256;
+    for (int64_t u = thread / 32; u < (int64_t)p.rows * parts; u += threads / 32) {
+        const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
+        unsigned ignored = 0;
+        const int have = pages_of(p.lens[r], p.block_size, shift, p.width, ignored);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i * 32 + lane;
+            if (j >= p.width) continue;
+            int b = j < have ? p.table[r * p.stride + j] : -1;
+            if (b >= p.num_blocks || b < 0) b = -1;
+            if (b >= first) {
+                const int rank = (int)p.workspace[words + (b >> 5)] +
+                                 __popc(p.workspace[b >> 5] & ((1u << (b & 31)) - 1)) - skipped;
+                b = p.dst[rank];
+            }
+            p.new_table[r * p.new_stride + j] = b;
+        }
+    }
+}
+
+} // namespace
+
+cudaError_t launch_fork_pages(const ForkProblem &p, cudaStream_t stream)
+{
+    cudaError_t e = allow_shared((const void *)fork_kernel, 2 * kForkRows * sizeof(int));
+    if (e != cudaSuccess) return e;
+    const int64_t chunks = (p.width + kForkEntries - 1) / kForkEntries;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(304, p.rows_out * chunks));
+    ForkProblem prob = p;
+    unsigned int *status = device_status_word();
+    void *args[] = {&prob, &status};
+    return launch_dependent((const void *)fork_kernel, grid, kForkThreads,
+                            (size_t)(p.rows_in + p.rows_out) * sizeof(int), stream, args);
+}
+
+cudaError_t launch_copy_pages(const CopyProblem &c, cudaStream_t stream)
+{
+    for (int64_t n0 = 0; n0 < c.num_caches; n0 += kCachesPerLaunch) {
+        CopyParams p{};
+        p.caches = (int)std::min<int64_t>(c.num_caches - n0, kCachesPerLaunch);
+        for (int i = 0; i < p.caches; ++i) p.cache[i] = static_cast<char *>(c.caches[n0 + i]);
+        p.src = c.src;
+        p.dst = c.dst;
+        p.tokens = c.tokens;
+        p.count = c.count;
+        p.status = device_status_word();
+        p.pairs = c.pairs;
+        p.block = c.layout.block_stride * 2;
+        p.token = c.layout.token_stride * 2;
+        p.head = c.layout.head_stride * 2;
+        p.num_blocks = c.num_blocks;
+        p.block_size = c.block_size;
+        p.head_pieces = c.head_dim / 8;
+        p.row_pieces = c.kv_heads * p.head_pieces;
+        p.heads_first = c.layout.head_stride > c.layout.token_stride;
+        p.parts = (c.block_size * p.row_pieces + kCopyThreads * kCopyPieces - 1) / (kCopyThreads * kCopyPieces);
+        const int64_t grid = std::min<int64_t>(152 * 4, c.pairs * p.caches * p.parts);
+        void *args[] = {&p};
+        const cudaError_t e = launch_dependent((const void *)copy_pages_kernel, grid, kCopyThreads, 0, stream, args);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_pages(const PagesProblem &p, cudaStream_t stream)
+{
+    PagesProblem prob = p;
+    unsigned int *status = device_status_word();
+    const int64_t words = (p.num_blocks + 31) / 32;
+    uint4 *clear = reinterpret_cast<uint4 *>(p.workspace);
+    int64_t n = (words + 3) / 4;
+    void *clear_args[] = {&clear, &n};
+    cudaError_t e = launch_dependent((const void *)clear_kernel,
+                                     std::max<int64_t>(1, std::min<int64_t>(152, n / (4 * kPageThreads))), kPageThreads, 0,
+                                     stream, clear_args);
+    if (e != cudaSuccess) return e;
+    const int64_t pieces = (int64_t)p.rows * ((p.width + 255) / 256);
+    const int64_t grid = std::max<int64_t>(
+        1, std::min<int64_t>(608, std::max((pieces * 32 + kPageThreads - 1) / kPageThreads,
+                                           (p.num_held + kPageThreads - 1) / kPageThreads)));
+    void *mark_args[] = {&prob, &status};
+    e = launch_dependent((const void *)mark_kernel, grid, kPageThreads, 0, stream, mark_args);
+    if (e != cudaSuccess) return e;
+    void *args[] = {&prob};
+    e = launch_dependent((const void *)list_kernel, (words + kPageThreads - 1) / kPageThreads, kPageThreads, 0, stream, args);
+    if (e != cudaSuccess || p.free_blocks) return e;
+    return launch_dependent((const void *)move_kernel, grid, kPageThreads, 0, stream, args);
+}
+
+} // namespace awq

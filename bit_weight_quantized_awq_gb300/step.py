@@ -4,9 +4,11 @@ here, nothing waits for the GPU, and what is known on the device only (lengths,
 table entries, tokens) is checked there: ``awq_last_device_status`` reports it. The
 tensors must be on the current CUDA device (``torch.cuda.set_device``), else ValueError.
 
-A step is ``paged_plan`` -> per layer ``kv_append``, ``tree_attention`` ->
-``process_logits``: the plan's ``cu_new``, ``slot_map`` and ``tree_mask`` are the
-others' arguments.
+A step is ``paged_plan`` -> per layer ``rotary_append`` (or ``rotary`` and ``kv_append``),
+``tree_attention`` -> ``process_logits``: the plan's ``positions``, ``cu_new``, ``slot_map``
+and ``tree_mask`` are the others' arguments. With beams, ``beam_select`` -> ``reorder_states``,
+``fork_pages``, ``copy_pages`` -> ``free_pages`` come after it, whose list of free blocks the
+next plan takes from: nothing of this waits for the host.
 
 The arguments are tested, outputs allocated and the C ABI called in a native module
 (``csrc/awq_step_module.cpp``), since a step's kernels take a few microseconds each.
@@ -37,7 +39,10 @@ def _load():
     loader.exec_module(module)
     lib = load_library()
     module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
-                  (lib.awq_paged_plan, lib.awq_kv_append, lib.awq_tree_attention, lib.awq_process_logits)))
+                  (lib.awq_paged_plan, lib.awq_kv_append, lib.awq_tree_attention, lib.awq_process_logits,
+                   lib.awq_rotary, lib.awq_beam_select, lib.awq_beam_select_workspace, lib.awq_reorder_states,
+                   lib.awq_fork_pages, lib.awq_copy_pages, lib.awq_free_pages, lib.awq_compact_pages,
+                   lib.awq_pages_workspace)))
     _step = module
     return module
 
@@ -113,3 +118,145 @@ def process_logits(logits: torch.Tensor, row_request: torch.Tensor | None = None
     if type(made) is int:
         raise AWQError(made, "awq_process_logits")
     return made
+
+
+def rotary_axes(sections: list[int], interleaved: bool = False, device="cuda") -> torch.Tensor:
+    """The ``axes`` of ``rotary`` for frequencies shared out among axes (time, height, width, say):
+    ``sections[a]`` of them belong to axis a, in blocks one after the other, or
+    ``interleaved``: dealt out in turn for as long as an axis has some left."""
+    if not sections or any(n < 0 for n in sections):
+        raise ValueError("sections must be numbers of frequencies, one for each axis")
+    if interleaved:
+        order = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+    else:
+        order = [a for a, n in enumerate(sections) for _ in range(n)]
+    return torch.tensor(order, dtype=torch.int32, device=device)
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+           axes: torch.Tensor | None = None, pairs: bool = False, q_out: torch.Tensor | None = None,
+           k_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """q and k [tokens, heads, head_dim] turned by their tokens' ``positions`` (int32
+    [tokens], the plan's, or [axes, tokens] with ``axes`` saying which one each
+    frequency goes by). ``inv_freq`` (fp32) has half as many entries as elements of a head
+    are turned; element i is paired with the one half of them further, or with its neighbour
+    (``pairs``). Views of a fused projection's output serve as they are; ``q_out=q`` and
+    ``k_out=k`` work in place."""
+    made = (_step or _load()).rotary(q, k, positions, inv_freq, axes, pairs, q_out, k_out)
+    if type(made) is int:
+        raise AWQError(made, "awq_rotary")
+    return made
+
+
+def rotary_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                  k_cache: torch.Tensor, v_cache: torch.Tensor, slot_map: torch.Tensor,
+                  axes: torch.Tensor | None = None, pairs: bool = False,
+                  q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """``rotary`` and ``kv_append`` in one pass: returns the turned q; the turned keys and the
+    values go into their slots of the paged cache."""
+    made = (_step or _load()).rotary_append(q, k, v, positions, inv_freq, k_cache, v_cache, slot_map, axes, pairs, q_out)
+    if type(made) is int:
+        raise AWQError(made, "awq_rotary")
+    return made
+
+
+class BeamStep(NamedTuple):
+    """What ``beam_select`` keeps (all on the device): -inf, -1, -1 where there are fewer."""
+    scores: torch.Tensor          # fp32 [requests, num_beams], in descending order
+    parents: torch.Tensor         # int32 [requests, num_beams]: rows of the logits
+    tokens: torch.Tensor          # int32 [requests, num_beams]
+    ended_scores: torch.Tensor | None     # the same of the candidates that end; None without end_tokens
+    ended_parents: torch.Tensor | None
+    ended_tokens: torch.Tensor | None
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, num_beams: int,
+                end_tokens: torch.Tensor | None = None) -> BeamStep:
+    """The best continuations of every request's beams: ``scores`` (fp32 [requests, beams],
+    -inf for a beam that is none) plus the log-softmax of their logits [requests * beams, vocab]. The
+    first ``num_beams`` whose token is not one of ``end_tokens`` go on; those among the first
+    ``num_beams`` of all that end are given apart. Equal scores: the lower row, then the lower token."""
+    made = (_step or _load()).beam_select(logits, scores, num_beams, end_tokens)
+    if type(made) is int:
+        raise AWQError(made, "awq_beam_select")
+    return BeamStep._make(made)
+
+
+def reorder_states(states: list[torch.Tensor], parents: torch.Tensor,
+                   outs: list[torch.Tensor] | None = None) -> list[torch.Tensor]:
+    """Rows ``parents`` (int32 [rows]) of every tensor of ``states`` [rows, ...], whatever its type:
+    token histories, recurrent states. -1 gives zeros. ``outs`` must not overlap ``states``."""
+    made = (_step or _load()).reorder_states(states, parents, outs)
+    if type(made) is int:
+        raise AWQError(made, "awq_reorder_states")
+    return made
+
+
+class ForkedPages(NamedTuple):
+    """What ``fork_pages`` lays out (all on the device, in one allocation)."""
+    block_table: torch.Tensor     # int32 [rows, width]
+    lens: torch.Tensor            # int32 [rows]
+    src: torch.Tensor             # int32 [rows]: what copy_pages has to copy, -1 after the last
+    dst: torch.Tensor
+    tokens: torch.Tensor
+    count: torch.Tensor           # int32 [1]: how many that are, as many blocks were taken
+
+
+def fork_pages(block_table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor, free_blocks: torch.Tensor,
+               block_size: int, free_start: torch.Tensor | None = None) -> ForkedPages:
+    """Block tables of the rows that go on from rows ``parents`` (``beam_select``'s, flat) of
+    ``block_table``, which hold ``lens`` tokens. Full pages are shared; a partly filled last one
+    stays with its first child, the others take blocks from ``free_blocks`` (from
+    ``free_start`` on: a plan's ``counts[1:]``, say) and a copy, which
+    ``copy_pages(caches, f.src, f.dst, f.tokens, f.count)`` makes."""
+    made = (_step or _load()).fork_pages(block_table, lens, parents, free_blocks, block_size, free_start)
+    if type(made) is int:
+        raise AWQError(made, "awq_fork_pages")
+    return ForkedPages._make(made)
+
+
+def copy_pages(caches: list[torch.Tensor], src: torch.Tensor, dst: torch.Tensor, tokens: torch.Tensor | None = None,
+               count: torch.Tensor | None = None) -> None:
+    """Blocks ``src`` to blocks ``dst`` within every cache of a list (the keys and values of all
+    layers, of one shape), only their first ``tokens``, and only the first ``count`` (int32
+    [1]) of the pairs if given. All at once: no dst is another pair's src or dst."""
+    status = (_step or _load()).copy_pages(caches, src, dst, tokens, count)
+    if status is not None:
+        raise AWQError(status, "awq_copy_pages")
+
+
+class FreePages(NamedTuple):
+    """What ``free_pages`` finds (all on the device)."""
+    free_blocks: torch.Tensor     # int32 [num_blocks]: ascending, -1 after the last
+    counts: torch.Tensor          # int32 [2]: free blocks, used blocks
+
+
+def free_pages(block_table: torch.Tensor, lens: torch.Tensor, block_size: int, num_blocks: int,
+               held: torch.Tensor | None = None) -> FreePages:
+    """The blocks of a cache that none of the rows needs for its ``lens`` tokens and that are
+    not among ``held`` (int32; -1 is skipped): the free list of the next plan or fork. To
+    free a request, set its length to 0."""
+    made = (_step or _load()).free_pages(block_table, lens, block_size, num_blocks, held)
+    if type(made) is int:
+        raise AWQError(made, "awq_free_pages")
+    return FreePages._make(made)
+
+
+class CompactPages(NamedTuple):
+    """What ``compact_pages`` lays out (all on the device, in one allocation)."""
+    block_table: torch.Tensor     # int32 [rows, width], with the new numbers
+    block_map: torch.Tensor       # int32 [num_blocks]: a block's new number, -1 for a free one
+    src: torch.Tensor             # int32 [num_blocks // 2]: what copy_pages has to copy, -1 after the last
+    dst: torch.Tensor
+    count: torch.Tensor           # int32 [1]: how many that are
+
+
+def compact_pages(block_table: torch.Tensor, lens: torch.Tensor, block_size: int, num_blocks: int,
+                  held: torch.Tensor | None = None) -> CompactPages:
+    """Moves the used blocks (as in ``free_pages``) to the cache's beginning: those that lie past
+    it take the free blocks there. ``copy_pages(caches, c.src, c.dst, count=c.count)`` moves
+    their contents, ``block_map`` renames a caller's own ``held``."""
+    made = (_step or _load()).compact_pages(block_table, lens, block_size, num_blocks, held)
+    if type(made) is int:
+        raise AWQError(made, "awq_compact_pages")
+    return CompactPages._make(made)

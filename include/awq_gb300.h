@@ -384,10 +384,11 @@ awq_status_t awq_reserve(int64_t max_M, int64_t max_K, int64_t max_N, unsigned f
  * ---- The decoding step around the quantised layers -------------------------
  *
  * Between the qkv and the output projection of a serving process lies a paged
- * cache of keys and values; after the head lie the logits. The four calls below
- * plan, fill and read that cache for one step -- single tokens, drafted token
- * trees or causal chunks of new tokens, ragged over the requests -- and apply
- * the sampling controls to the logits. Requests are numbered 0 .. B - 1; the
+ * cache of keys and values; after the head lie the logits. The calls below plan,
+ * fill and read that cache for one step -- single tokens, drafted token trees or
+ * causal chunks of new tokens, ragged over the requests --, turn queries and keys by
+ * their positions, apply the sampling controls to the logits, keep the best beams,
+ * and fork, copy, free and compact the cache's pages. Requests are numbered 0 .. B - 1; the
  * new tokens of all requests lie one after another (request b's are rows
  * cu_new[b] .. cu_new[b + 1] - 1). A cache is [num_blocks, block_size,
  * kv_heads, head_dim] of fp16 or bf16; slot s is token s % block_size of block
@@ -595,6 +596,222 @@ typedef struct {
     int32_t dtype;
 } awq_logits_t;
 awq_status_t awq_process_logits(const awq_logits_t *args, awq_stream_t stream);
+
+/*
+ * awq_rotary -- rotary positions of q and k, with one position a token or one for
+ * each of several axes (time, height and width of images and video), from
+ * awq_paged_plan's positions or the caller's:
+ *   a[t, i] = positions[axes[i], t] * inv_freq[i]            0 <= i < rotary_dim / 2
+ *   (u, w)  = (x[i], x[i + rotary_dim / 2]), or with `pairs` (x[2 i], x[2 i + 1])
+ *   (u, w) <- (u cos a - w sin a, w cos a + u sin a)
+ * for every head x of q[t] and k[t]; elements from rotary_dim on are copied. The angle is
+ * the exact product of the whole position and the fp32 frequency, reduced to a turn
+ * in 64-bit fixed point, so far positions lose nothing; the rotation is in fp32 and
+ * rounded once.
+ *
+ * With slot_map the turned keys go straight into a paged cache, and so do the values:
+ * awq_rotary and awq_kv_append in one launch (k_out is then not used). A slot
+ * of -1 is skipped; any other slot outside [0, num_blocks * block_size) is skipped and
+ * reported; q is turned all the same. Two tokens with the same slot leave either one's.
+ *
+ *   q, k, v       [tokens, heads, head_dim] fp16 or bf16, 16-byte aligned, strides in
+ *                 elements, multiples of 8: parts of a fused projection's rows serve as
+ *                 they are. v with slot_map only.
+ *   q_out, k_out  likewise; each may be its input with the same strides (in place), and
+ *                 must not overlap the inputs otherwise
+ *   positions     int32 [num_axes, tokens], any sign
+ *   inv_freq      fp32 [rotary_dim / 2], finite
+ *   axes          int32 [rotary_dim / 2], or NULL for axis 0 throughout. An axis outside
+ *                 [0, num_axes) is reported and its pair is not turned.
+ * Requires tokens >= 0, q_heads > 0, kv_heads >= 0 (> 0 with slot_map; k may be NULL with 0),
+ * head_dim % 8 == 0, rotary_dim even, 0 < rotary_dim <= head_dim <= 1024, num_axes >= 1,
+ * tokens < 2^31, (q_heads + 2 kv_heads) * head_dim < 2^24 (AWQ_ERR_INVALID_ARG otherwise).
+ */
+typedef struct {
+    const void *q, *k, *v;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    void *q_out, *k_out;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+    const int32_t *positions;
+    const float *inv_freq;
+    const int32_t *axes;
+    awq_cache_t k_cache, v_cache;
+    const int64_t *slot_map;
+    int64_t num_blocks, block_size;
+    int64_t tokens, q_heads, kv_heads, head_dim, rotary_dim, num_axes;
+    int32_t pairs;
+    int32_t dtype;   /* AWQ_F16 or AWQ_BF16 */
+} awq_rotary_t;
+awq_status_t awq_rotary(const awq_rotary_t *args, awq_stream_t stream);
+
+/*
+ * awq_beam_select -- one step of beam search over the logits of every beam. Row
+ * r = b * beams + w of logits is beam w of request b; its candidates are the tokens
+ * v with
+ *   s(r, v) = scores[r] + logits[r, v] - ln sum_u exp(logits[r, u])
+ * A request's candidates are ordered by s, equal ones by row, then by logit, then by
+ * the lower token. It keeps the first num_beams whose token is not one of end_tokens:
+ *   out_scores, out_parents, out_tokens  fp32, int32, int32 [requests, num_beams]: s,
+ *                 r (for awq_fork_pages and awq_reorder_states) and v, in order
+ * and, with end_tokens, reports those among the first num_beams of all its candidates
+ * that end there:
+ *   ended_scores, ended_parents, ended_tokens  the same for these
+ * Places without a candidate hold -inf, -1 and -1. The sum is in fp32 and its parts are
+ * added up, and s compared, in 64 bits.
+ *
+ *   logits      [requests * beams, vocab] fp16, bf16 or fp32 (dtype), elements of a row
+ *               contiguous, rows logits_row_stride elements apart
+ *   scores      fp32 [requests * beams]; -inf: no beam, its row is not looked at
+ *   end_tokens  int32 [num_ends] or NULL; tokens outside [0, vocab) match nothing
+ *   workspace   awq_beam_select_workspace() bytes, 256-byte aligned, used until the
+ *               call's work is done
+ * A logit of -inf is no candidate. A row with a NaN or +inf among its logits, or with such a
+ * score, has no candidates and is reported. beams and num_beams may differ (a prompt's
+ * single row gives the first beams).
+ * Requires 0 <= requests <= 16384, 1 <= beams, num_beams <= 32, 0 <= num_ends <= 8,
+ * 0 < vocab <= 2^27, logits aligned to its elements (AWQ_ERR_INVALID_ARG otherwise, and for
+ * too small a workspace).
+ */
+typedef struct {
+    const void *logits;
+    int64_t logits_row_stride, requests, beams, vocab;
+    const float *scores;
+    int64_t num_beams;
+    const int32_t *end_tokens;
+    int64_t num_ends;
+    float *out_scores;
+    int32_t *out_parents, *out_tokens;
+    float *ended_scores;
+    int32_t *ended_parents, *ended_tokens;
+    void *workspace;
+    int64_t workspace_bytes;
+    int32_t dtype;
+} awq_beam_select_t;
+awq_status_t awq_beam_select(const awq_beam_select_t *args, awq_stream_t stream);
+
+/* Bytes of awq_beam_select's workspace for these sizes; -1 for sizes that it refuses.
+ * Host-only, no CUDA call. */
+int64_t awq_beam_select_workspace(int64_t requests, int64_t beams, int64_t vocab, int64_t num_beams,
+                                  int64_t num_ends, awq_dtype_t dtype);
+
+/*
+ * awq_reorder_states -- rows of several arrays by parent, as beams go on:
+ *   states[i].dst[r] = states[i].src[parents[r]]    0 <= r < rows_out
+ * for `count` arrays of rows of their own size. A parent of -1 gives zeros; any other
+ * outside [0, rows_in) too, and is reported. Strides and sizes are in bytes, of any
+ * alignment; dst must not overlap any src.
+ * Requires 0 <= count <= 4096, 0 <= rows_in, rows_out < 2^31, 0 <= row_bytes < 2^31, strides of at least
+ * row_bytes where there are several rows (AWQ_ERR_INVALID_ARG otherwise).
+ */
+typedef struct {
+    const void *src;
+    void *dst;
+    int64_t src_row_stride, dst_row_stride, row_bytes;
+} awq_state_t;
+awq_status_t awq_reorder_states(const awq_state_t *states, int64_t count, const int32_t *parents,
+                                int64_t rows_out, int64_t rows_in, awq_stream_t stream);
+
+/*
+ * awq_fork_pages -- block tables of the beams that go on. Row r of the new table
+ * continues row p = parents[r] of block_table, which has lens[p] tokens in
+ * have = ceil(lens[p] / block_size) pages:
+ *   new_table[r, j] = block_table[p, j] for j < have, else -1;  new_lens[r] = lens[p]
+ * Full pages are shared. A last page that is not full must become the row's own, since
+ * its next token goes there: the first row with parent p keeps it, every other one gets
+ *   new_table[r, have - 1] = free_blocks[*free_start + n]
+ * with n = 0, 1, .. in the order of those rows, and is listed for awq_copy_pages:
+ *   src[n] = block_table[p, have - 1], dst[n] = the new block, tokens[n] = lens[p] % block_size
+ *   count  = how many are listed; the entries of src, dst and tokens from there on get -1
+ * A parent of -1 leaves the row empty (length 0); pages that no row continues are those
+ * that awq_free_pages then finds. A last page that is not full is taken to be in one row only.
+ *
+ *   block_table  int32 [rows_in, table_width], rows table_stride apart; lens int32 [rows_in]
+ *   parents      int32 [rows_out]
+ *   free_blocks  int32 [num_free]; free_start int32 [1] or NULL for 0: how many of them
+ *                are taken already (awq_paged_plan's counts[1], say)
+ *   new_table    int32 [rows_out, table_width], rows new_stride apart, does not overlap
+ *                block_table; new_lens, src, dst, tokens int32 [rows_out]; count int32 [1]
+ * Where free blocks run out, the row's last page and its src and dst get -1 and the device
+ * status becomes AWQ_ERR_TOO_LARGE (so does it for a length beyond the table's width, which
+ * counts as that width, all its pages full). A negative length counts as 0, a parent outside [-1, rows_in) as -1, a
+ * negative *free_start as 0, each reported as AWQ_ERR_INVALID_ARG.
+ * Requires 0 <= rows_in, rows_out <= 16384, block_size a power of two from 16 to 1024,
+ * table_stride and new_stride >= table_width > 0, 0 <= num_free < 2^31.
+ */
+awq_status_t awq_fork_pages(const int32_t *block_table, int64_t rows_in, int64_t table_width,
+                            int64_t table_stride, const int32_t *lens, const int32_t *parents,
+                            int64_t rows_out, const int32_t *free_blocks, int64_t num_free,
+                            const int32_t *free_start, int64_t block_size, int32_t *new_table,
+                            int64_t new_stride, int32_t *new_lens, int32_t *src, int32_t *dst,
+                            int32_t *tokens, int32_t *count, awq_stream_t stream);
+
+/*
+ * awq_copy_pages -- copies pages within each of several caches of one shape (the keys
+ * and values of all layers):
+ *   cache[dst[i], t] = cache[src[i], t]   for t < tokens[i] (block_size if NULL), i < *count
+ *   caches       `num_caches` base pointers (a host array), 16-byte aligned
+ *   layout       the strides that all of them have (data is not used)
+ *   src, dst     int32 [pairs]; tokens int32 [pairs] or NULL; count int32 [1] or NULL for
+ *                `pairs` (values outside [0, pairs] are taken as the nearer end)
+ * All pairs are copied at once, in no order: a dst may not be a src or dst of another pair (the
+ * lists of awq_fork_pages and awq_compact_pages are so). A pair with src or dst -1, or of one block with itself, is
+ * skipped; a block outside [0, num_blocks) is skipped and reported; tokens are clamped to
+ * [0, block_size] and reported. 16-bit elements, head_dim % 8 == 0.
+ * Requires 0 <= num_caches <= 65536, 0 <= pairs < 2^31, 0 < num_blocks < 2^31, block_size a power of two
+ * from 16 to 1024, strides as in awq_cache_t, block_size * kv_heads * head_dim < 2^30.
+ */
+awq_status_t awq_copy_pages(void *const *caches, int64_t num_caches, const awq_cache_t *layout,
+                            int64_t num_blocks, int64_t block_size, int64_t kv_heads, int64_t head_dim,
+                            const int32_t *src, const int32_t *dst, const int32_t *tokens,
+                            int64_t pairs, const int32_t *count, awq_stream_t stream);
+
+/*
+ * awq_free_pages -- which blocks of a cache are in use, from the block tables alone: a
+ * block is used if it is one of the first ceil(lens[r] / block_size) entries of a row r,
+ * or one of `held`. However often it is shared, nothing is counted up or down, so a request
+ * is freed by its row's length becoming 0 (or by leaving the row out).
+ *   free_blocks  int32 [num_blocks]: the other blocks in ascending order, then -1 (the
+ *                list that awq_paged_plan and awq_fork_pages take blocks from)
+ *   counts       int32 [2]: free blocks, used blocks
+ *   block_table  int32 [rows, table_width], rows table_stride apart; lens int32 [rows]
+ *   held         int32 [num_held] or NULL: blocks that something else holds (a cache of
+ *                prompts); -1 is skipped
+ *   workspace    awq_pages_workspace(num_blocks) bytes, 256-byte aligned, used until the
+ *                call's work is done
+ * An entry outside [0, num_blocks) is skipped and reported; a negative length counts as 0
+ * and a length beyond the table's width as that width, each reported.
+ * Requires 0 <= rows <= 2^20, block_size a power of two from 16 to 1024, table_stride >=
+ * table_width > 0, 0 < num_blocks <= 2^28, 0 <= num_held < 2^31.
+ */
+awq_status_t awq_free_pages(const int32_t *block_table, int64_t rows, int64_t table_width,
+                            int64_t table_stride, const int32_t *lens, int64_t block_size,
+                            int64_t num_blocks, const int32_t *held, int64_t num_held,
+                            int32_t *free_blocks, int32_t *counts, void *workspace,
+                            awq_stream_t stream);
+
+/* Bytes of the workspace of awq_free_pages and awq_compact_pages; -1 if num_blocks is out
+ * of range. Host-only, no CUDA call. */
+int64_t awq_pages_workspace(int64_t num_blocks);
+
+/*
+ * awq_compact_pages -- gathers the used blocks (as awq_free_pages finds them) at the
+ * cache's beginning, so that it can end after them. With n used blocks, the used blocks
+ * from n on move, in ascending order, to the free blocks below n, in ascending order; the
+ * others stay:
+ *   block_map  int32 [num_blocks]: a used block's new number, -1 for a free block
+ *   new_table  int32 [rows, table_width], rows new_stride apart: the table with the new
+ *              numbers, -1 past a row's pages; does not overlap block_table
+ *   src, dst   int32 [num_blocks / 2], for awq_copy_pages: the blocks that move and where to, then -1
+ *   count      int32 [1]: how many move
+ * The blocks' contents are moved by awq_copy_pages; a caller's own `held` list follows by
+ * block_map. Other arguments, limits and reports as in awq_free_pages.
+ */
+awq_status_t awq_compact_pages(const int32_t *block_table, int64_t rows, int64_t table_width,
+                               int64_t table_stride, const int32_t *lens, int64_t block_size,
+                               int64_t num_blocks, const int32_t *held, int64_t num_held,
+                               int32_t *new_table, int64_t new_stride, int32_t *block_map,
+                               int32_t *src, int32_t *dst, int32_t *count, void *workspace,
+                               awq_stream_t stream);
 
 /* Static description of a status code. Never NULL. */
 const char *awq_status_string(awq_status_t status);
