@@ -1,16 +1,22 @@
 // awq_beam.cu -- one step of beam search over the logits, and rows of other state by parent.
 //
-// beam_rows_kernel reads every logit once. A CTA takes a stretch of one row; each thread
-// keeps the maximum m of what it has read, the 16 bytes it came from, and the sum of
-// exp(x - m). No list is kept while the logits stream by: the best K of a stretch can
-// only lie with the K threads whose maxima are the greatest (each of them has an element
+// beam_rows_kernel reads every logit once. The rows are a line of chunks of 1024 16-byte
+// pieces, cut into equal parts, one a CTA; a producer warp keeps a ring of bulk copies under way
+// across rows, so that HBM does not wait while a row's end is worked on. Each thread keeps the
+// maximum of what it has read. No list is kept while the logits stream by: the best K of a part
+// of a row can only lie with the K threads whose maxima are the greatest (each of them has an element
 // at least as great as the K-th greatest maximum, any other thread has none). Those
-// threads' pieces, K / kThreads of the stretch, are read a second time, and what
+// threads' pieces, K / 256 of the part, are read a second time, from the L2 cache, and what
 // reaches the K-th greatest maximum is sorted out. Logits that are equal are told apart by
-// their token, so all keys differ and the time does not depend on the data.
+// their place, so all keys differ and the time does not depend on the data.
 //
-// beam_merge_kernel, a CTA a request, adds up the sums of a row's stretches in 64 bits,
-// merges their lists, a warp a row, and takes the best over the rows.
+// The sum of exp(x - m) is taken for each chunk and warp by itself and added up in one order,
+// so that a row's log-sum-exp does not depend on where the line was cut: equal rows (at
+// the same place within 16 bytes) have equal ones, and their beams tie as they should.
+//
+// beam_merge_kernel, a CTA a request, adds up a row's sums in 64 bits, merges the lists of its
+// parts, a warp a row, and takes the best over the rows. The logarithms, in fp64, are one a lane of one warp:
+// by all warps they took longer than all the rest (fp64 runs at two operations a clock).
 //
 // Bound: HBM, one read of the logits; one exponential a logit.
 #include <algorithm>
@@ -34,10 +40,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct BeamParams {
     awq_beam_select_t a;
     unsigned int *status;
-    // workspace: of each stretch, maximum and sum [rows][stretches], and its best [rows][stretches][best]
+    // All rows as a line of chunks, `chunks` each, cut into `each` for a CTA. The part of a row that one CTA
+    // has is a stretch, number CTA + row: its best [best] are in the workspace, and the
+    // maximum and sum of each chunk and warp.
     float2 *sums;
     uint64_t *lists;
-    int stretches, best, element;     // element: bytes
+    int64_t rows, chunks, each;
+    int best, merge_lists, fault;     // merge_lists: the most stretches of a request
 };
 
 template <typename T>
@@ -120,159 +129,325 @@ __device__ void warp_best(uint64_t *keys, int n, int best, uint64_t *out)
     __syncwarp();
 }
 
-// A row as 16-byte pieces from an aligned address at or before it.
+// A row as 16-byte pieces from an aligned address at or before it. Pieces `whole` to
+// `end` - 1 lie in the row; what is outside them is one by one: `head` elements at its beginning,
+// `tail` at its end.
 template <typename T>
 struct Row {
     static constexpr int kEach = 16 / sizeof(T);
     const T *row;
     const uint4 *pieces;
-    int lead;           // elements of the first piece that are not the row's
-    int vocab, count;
+    int lead, whole, end, head, tail;   // lead: elements of the first piece that are not the row's
 
-    __device__ Row(const T *p, int n) : row(p), vocab(n)
+    __device__ Row(const T *p, int vocab) : row(p)
     {
         lead = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
         pieces = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
-        count = (lead + n + kEach - 1) / kEach;
+        whole = lead > 0;
+        head = lead > 0 ? min(kEach - lead, vocab) : 0;
+        end = max((lead + vocab) / kEach, whole);
+        tail = max(lead + vocab - end * kEach, 0);
     }
-    // not read-only loads: this kernel may be resident while the one before writes the logits
-    __device__ void load(int i, float (&x)[kEach]) const
-    {
-        const int first = i * kEach - lead;
-        if (first >= 0 && first + kEach <= vocab) {
-            widen<T>(pieces[i], x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < kEach; ++j)
-                x[j] = first + j >= 0 && first + j < vocab ? one(row + first + j) : -INFINITY;
-        }
-    }
+    __device__ unsigned token(int piece) const { return (unsigned)(piece * kEach - lead); }
 };
 
+// Two fp32 values in one register pair.
+__device__ __forceinline__ uint64_t both(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 apart(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
+// The greatest of a piece's elements as they are (a NaN gives way to a number), joined with `top`'s.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__device__ __forceinline__ uint32_t top_of(uint4 v, uint32_t top)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            top = __float_as_uint(fmaxf(__uint_as_float(top), __uint_as_float(w[i])));
+        } else if constexpr (std::is_same<T, __half>::value) {
+            const __half2 m = __hmax2(*reinterpret_cast<const __half2 *>(&top), *reinterpret_cast<const __half2 *>(&w[i]));
+            top = *reinterpret_cast<const uint32_t *>(&m);
+        } else {
+            const __nv_bfloat162 m =
+                __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&top), *reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+            top = *reinterpret_cast<const uint32_t *>(&m);
+        }
+    }
+    return top;
+}
+
+template <typename T>
+__device__ __forceinline__ float top_value(uint32_t top)
+{
+    if constexpr (sizeof(T) == 4) return __uint_as_float(top);
+    float x[16 / sizeof(T)];
+    widen<T>(make_uint4(top, top, top, top), x);
+    return fmaxf(x[0], x[1]);
+}
+
+// The 32 lanes' keys in descending order (a bitonic network).
+__device__ __forceinline__ uint64_t warp_sort(uint64_t key)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1) {
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, key, j);
+            const bool greater = ((lane & j) == 0) == ((lane & k) == 0);
+            key = (other > key) == greater ? other : key;
+        }
+    }
+    return key;
+}
+
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = kThreads * kLoads;     // pieces: 16 KB, a stage of the ring
+constexpr int kStages = 5;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads + 32, 2)
 beam_rows_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int kEach = 16 / sizeof(T);
-    constexpr int kRoom = kMostBest + kThreads * kEach;
-    __shared__ uint64_t keys[kRoom];
-    __shared__ uint64_t leaders[kMostBest];
-    __shared__ int who[kMostBest];
-    __shared__ float part[kThreads / 32];
-    __shared__ int listed, chosen;
+    constexpr int kRoom = kMostBest + kThreads * kEach + 32;
+    extern __shared__ __align__(128) uint4 ring[];       // [kStages][kChunk]
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ uint64_t keys[kRoom], sorted[kWarps][32], leaders[kMostBest];
+    __shared__ int who[kMostBest], listed[2];
+    __shared__ uint64_t least;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(ptx::smem_addr(full + i), 1);
+            ptx::mbar_init(ptx::smem_addr(empty + i), kWarps);
+        }
+        ptx::fence_mbar_init();
+        listed[0] = listed[1] = 0;
+    }
+    __syncthreads();
     ptx::launch_dependents();
     ptx::wait_prerequisites();
 
-    const int64_t r = blockIdx.x / p.stretches;
-    const int stretch = (int)(blockIdx.x - r * p.stretches);
-    // no beam: the merge does not look at it either
-    if (p.a.scores[r] == -INFINITY) return;
-    const Row<T> row(static_cast<const T *>(p.a.logits) + r * p.a.logits_row_stride, (int)p.a.vocab);
-    const int each = (row.count + p.stretches - 1) / p.stretches;
-    const int begin = min(stretch * each, row.count), end = min(begin + each, row.count);
+    const int64_t begin = blockIdx.x * p.each, end = min(begin + p.each, p.rows * p.chunks);
+    auto row_of = [&](int64_t r) {
+        return Row<T>(static_cast<const T *>(p.a.logits) + r * p.a.logits_row_stride, (int)p.a.vocab);
+    };
 
-    // ---- maximum and sum of what each thread reads
-    float m = -INFINITY, base = 0.f, s = 0.f;      // base: m once it is finite
-    int where = -1;
-    int i = begin + tid;
-    for (; i < end; i += kThreads * kLoads) {
-        float x[kLoads][kEach];
+    if (warp == kWarps) {
+        // ---------------------------------------------------------------- the rows' way in
+        if (lane > 0) return;
+        int64_t issued = 0;
+        bool ok = true;
+        for (int64_t at = begin, r = begin / p.chunks; at < end && ok; ++r) {
+            const int j0 = (int)(at - r * p.chunks), j1 = (int)min(p.chunks, j0 + end - at);
+            at += j1 - j0;
+            // no beam: nobody looks at it
+            if (p.a.scores[r] == -INFINITY) continue;
+            const Row<T> row = row_of(r);
+            for (int j = j0; j < j1 && ok; ++j) {
+                const int i = row.whole + j * kChunk;
+                if (i >= row.end) continue;
+                const int s = (int)(issued % kStages);
+                ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + s), ((issued / kStages) & 1) ^ 1, nullptr, p.status);
+                if (!ok) break;
+                const uint32_t bytes = (uint32_t)min(kChunk, row.end - i) * 16;
+                ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), bytes);
+                ++issued;
+#ifdef AWQ_FAULT_TEST
+                if (p.fault && blockIdx.x == 0) continue;
+#endif
+                ptx::bulk_load(ptx::smem_addr(ring + s * kChunk), row.pieces + i, bytes, ptx::smem_addr(full + s));
+            }
+        }
+        // after a wait that ran out: the copies on their way land before the shared memory goes
+        for (int64_t i = max((int64_t)0, issued - kStages); i < issued && !ok; ++i)
+            ptx::mbar_wait_bounded(ptx::smem_addr(full + i % kStages), (i / kStages) & 1, nullptr, nullptr);
+        return;
+    }
+
+    // ---------------------------------------------------------------- maxima, sums, lists
+    int64_t used = 0;
+    int turn = 0;
+    for (int64_t at = begin, r = begin / p.chunks; at < end; ++r) {
+        const int j0 = (int)(at - r * p.chunks), j1 = (int)min(p.chunks, j0 + end - at);
+        at += j1 - j0;
+        if (p.a.scores[r] == -INFINITY) continue;
+        const Row<T> row = row_of(r);
+        // what is not in whole pieces, one element a thread: the first chunk has the head, the last one the tail
+        const bool in_head = j0 == 0 && tid < row.head;
+        const bool in_tail = j1 == p.chunks && tid >= 32 && tid - 32 < row.tail;
+        const unsigned single_token = in_tail ? row.token(row.end) + tid - 32 : tid;
+        // not read-only loads: this kernel may be resident while the one before writes the logits
+        const float single = in_head || in_tail ? one(row.row + single_token) : -INFINITY;
+        const int single_chunk = in_tail ? j1 - 1 : j0;
+
+        // ---- each thread four neighbouring pieces of a chunk: its maximum, and the warp's sum
+        float m = -INFINITY;
+        int where = 0;
+        bool landed = true;
+        for (int j = j0; j < j1; ++j) {
+            constexpr uint32_t nothing = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+            const int i = row.whole + j * kChunk;
+            uint4 v[kLoads];
+            uint32_t all = nothing;
+            if (i < row.end) {
+                const int s = (int)(used % kStages);
+                landed = landed && ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (used / kStages) & 1, nullptr, p.status);
+                if (!__all_sync(0xFFFFFFFFu, landed)) {
+                    landed = false;
+                    break;
+                }
+                ++used;
+                const int left = row.end - i - tid * kLoads;
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            if (i + n * kThreads < end) {
-                row.load(i + n * kThreads, x[n]);
+                for (int u = 0; u < kLoads; ++u) {
+                    // in an order that keeps eight lanes off one another's banks
+                    const int piece = (u + (tid >> 1)) % kLoads;
+                    v[u] = ring[s * kChunk + tid * kLoads + piece];
+                    if (piece >= left) v[u] = make_uint4(nothing, nothing, nothing, nothing);
+                    all = top_of<T>(v[u], all);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(empty + s));
             } else {
 #pragma unroll
-                for (int j = 0; j < kEach; ++j) x[n][j] = -INFINITY;
+                for (int u = 0; u < kLoads; ++u) v[u] = make_uint4(nothing, nothing, nothing, nothing);
             }
-        }
-        float top = m;
-        int at = where;
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            float t = x[n][0];
-#pragma unroll
-            for (int j = 1; j < kEach; ++j) t = fmaxf(t, x[n][j]);
-            if (t > top) {
-                top = t;
-                at = i + n * kThreads;
+            const float top = top_value<T>(all);
+            if (top > m) {
+                m = top;
+                where = j;
             }
-        }
-        if (top > m) {
-            if (m > -INFINITY) s *= power((base - top) * kLog2e);
-            m = base = top;
-            where = at;
-        }
+            const float alone = j == single_chunk ? single : -INFINITY;
+            const uint32_t order = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key_of(fmaxf(top, alone), 0) >> 32));
+            const float most = logit_of((uint64_t)order << 32), base = most > -INFINITY ? most : 0.f;
+            const uint64_t minus = both(-base, -base), scale = both(kLog2e, kLog2e);
+            uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-        for (int n = 0; n < kLoads; ++n)
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) s += power((x[n][j] - base) * kLog2e);
-    }
-
-    // ---- the threads with the greatest maxima
-    uint64_t mine = 0;
-    if (where >= 0) {
-        float x[kEach];
-        row.load(where, x);
-#pragma unroll
-        for (int j = kEach - 1; j >= 0; --j)
-            if (x[j] == m) mine = key_of(m, where * kEach - row.lead + j);
-    }
-    keys[tid] = mine;
-    if (tid == 0) listed = chosen = 0;
-    __syncthreads();
-    if (warp == 0) warp_best(keys, kThreads, p.best, leaders);
-    __syncthreads();
-    const float top = logit_of(leaders[0]);       // of the stretch; leaders[0] is 0 without any logit
-    float sum = mine ? s * power((m - top) * kLog2e) : s;      // s that is no number stays so
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (lane == 0) part[warp] = sum;
-    const uint64_t least = max(leaders[p.best - 1], (uint64_t)1);
-    if (mine >= least) who[atomicAdd(&chosen, 1)] = tid;
-    __syncthreads();
-    const int64_t slot = r * p.stretches + stretch;
-    if (tid == 0) {
-        float all = 0.f;
-        for (int w = 0; w < kThreads / 32; ++w) all += part[w];
-        p.sums[slot] = make_float2(leaders[0] ? top : -INFINITY, all);
-    }
-
-    // ---- their pieces again: what reaches `least`, the order of `who` does not matter
-    uint64_t floor = least;
-    const int leads = chosen, turns = (end - begin + kThreads - 1) / kThreads;
-    for (int e0 = 0; e0 < leads * turns; e0 += kThreads) {
-        const int e = e0 + tid;
-        if (e < leads * turns) {
-            const int piece = begin + who[e % leads] + e / leads * kThreads;
-            if (piece < end) {
+            for (int u = 0; u < kLoads; ++u) {
                 float x[kEach];
-                row.load(piece, x);
+                widen<T>(v[u], x);
 #pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    if (!(x[j] > -INFINITY)) continue;
-                    const uint64_t key = key_of(x[j], piece * kEach - row.lead + j);
-                    if (key >= floor) keys[atomicAdd(&listed, 1)] = key;
+                for (int k = 0; k < kEach; k += 2) {
+                    const float2 t = apart(mul2(add2(both(x[k], x[k + 1]), minus), scale));
+                    const uint64_t e = both(power(t.x), power(t.y));
+                    if (k & 2) s1 = add2(s1, e);
+                    else s0 = add2(s0, e);
                 }
             }
+            const float2 sum2 = apart(add2(s0, s1));
+            // a NaN stays one
+            float sum = sum2.x + sum2.y + power((alone - base) * kLog2e);
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            if (lane == 0) p.sums[(r * p.chunks + j) * kWarps + warp] = make_float2(most, sum);
         }
-        __syncthreads();
-        const int n = listed;
-        __syncthreads();
-        if (n > kMostBest && e0 + kThreads < leads * turns) {     // room for the next round
-            if (warp == 0) {
-                warp_best(keys, n, p.best, leaders);
-                for (int k = lane; k < p.best; k += 32) keys[k] = leaders[k];
-                if (lane == 0) listed = p.best;
+
+        // ---- the threads with the greatest maxima: each warp sorts its own, then each key counts those
+        // before it in the other warps' lists. Equal maxima go by the place of their pieces, so keys differ
+        const uint64_t key = warp_sort(m > -INFINITY ? key_of(m, (unsigned)((where - j0) * kThreads + tid)) : 0);
+        sorted[warp][lane] = key;
+        if (tid == 0) least = 0;
+        if (!ptx::named_barrier_and(1, kThreads, landed)) break;
+        if (key && lane < p.best) {
+            int rank = lane;
+            int low[kWarps] = {};             // keys of warp w that are greater: found bit by bit
+#pragma unroll
+            for (int step = 32; step; step >>= 1)
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    if (low[w] + step <= 32 && sorted[w][low[w] + step - 1] > key) low[w] += step;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                if (w != warp) rank += low[w];
+            if (rank < p.best) who[rank] = (int)((0xFFFFFFFFu - (uint32_t)key) % kThreads);
+            if (rank == p.best - 1) least = key;
+        }
+        ptx::named_barrier(1, kThreads);
+
+        // ---- their pieces again: what reaches `least`
+        int leads = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) leads += __popc(__ballot_sync(0xFFFFFFFFu, sorted[w][lane] >= max(least, (uint64_t)1)));
+        const uint32_t floor_value = (uint32_t)(least >> 32);
+        uint64_t floor = 0;                   // of whole keys, once a list has been cut
+        const int items = leads * (j1 - j0) * kLoads;
+        int *count = &listed[turn & 1];
+        auto enlist = [&](float x, unsigned token) {
+            const uint64_t k = key_of(x, token);
+            if (x > -INFINITY && (uint32_t)(k >> 32) >= floor_value && k >= floor) keys[atomicAdd(count, 1)] = k;
+        };
+        enlist(single, single_token);
+        for (int e0 = 0; e0 < items; e0 += kThreads) {
+            const int e = e0 + tid;
+            if (e < items) {
+                const int l = e / kLoads % leads, j = e / kLoads / leads;
+                const int piece = row.whole + (j0 + j) * kChunk + who[l] * kLoads + e % kLoads;
+                if (piece < row.end) {
+                    float x[kEach];
+                    widen<T>(row.pieces[piece], x);
+                    // equal to the least maximum: only from its place on, so that no list overflows
+                    const uint64_t place = (uint64_t)floor_value << 32 | (0xFFFFFFFFu - (unsigned)(j * kThreads + who[l]));
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k)
+                        if ((uint32_t)(key_of(x[k], 0) >> 32) > floor_value || place >= least) enlist(x[k], row.token(piece) + k);
+                }
             }
-            __syncthreads();
-            floor = max(leaders[p.best - 1], floor);
+            ptx::named_barrier(1, kThreads);
+            const int have = *count;
+            ptx::named_barrier(1, kThreads);
+            if (have > kMostBest && e0 + kThreads < items) {      // room for the next round
+                if (warp == 0) {
+                    warp_best(keys, have, p.best, leaders);
+                    for (int k = lane; k < p.best; k += 32) keys[k] = leaders[k];
+                    if (lane == 0) *count = p.best;
+                }
+                ptx::named_barrier(1, kThreads);
+                floor = keys[p.best - 1];
+            }
         }
-    }
-    if (warp == 0) {
-        warp_best(keys, listed, p.best, leaders);
-        for (int k = lane; k < p.best; k += 32) p.lists[slot * p.best + k] = leaders[k];
+        if (items == 0) ptx::named_barrier(1, kThreads);
+        const int have = *count;
+        const int64_t slot = blockIdx.x + r;
+        if (tid == 0) listed[turn & 1 ^ 1] = 0;
+        // ---- the best of them in order
+        uint64_t *list = p.lists + slot * p.best;
+        if (have <= kThreads) {
+            if (tid < have) {
+                const uint64_t k = keys[tid];
+                int rank = 0;
+                for (int i = 0; i < have; ++i) rank += keys[i] > k;
+                if (rank < p.best) list[rank] = k;
+            }
+            for (int k = have + tid; k < p.best; k += kThreads) list[k] = 0;
+        } else if (warp == 0) {
+            warp_best(keys, have, p.best, leaders);
+            for (int k = lane; k < p.best; k += 32) list[k] = leaders[k];
+        }
+        ++turn;
     }
 }
 
@@ -292,51 +467,71 @@ __global__ void __launch_bounds__(32 * kMostBeams)
 beam_merge_kernel(const __grid_constant__ BeamParams p)
 {
     extern __shared__ uint64_t merge_smem[];
+    __shared__ double sums[kMostBeams], lses[kMostBeams];
+    __shared__ float tops[kMostBeams];
     const int beams = (int)p.a.beams, best = p.best, keep = (int)p.a.num_beams;
-    uint64_t *lists = merge_smem;                                                    // [beams][stretches][best]
-    uint64_t *scores = lists + beams * p.stretches * best;                           // [beams][best + 1]
-    unsigned *tokens = reinterpret_cast<unsigned *>(scores + beams * (best + 1));    // [beams][best]
+    uint64_t *scores = merge_smem;                                  // [beams][best + 1]: a row's best, 0 behind the last
+    uint64_t *lists = scores + beams * (best + 1);                  // [stretches of all rows][best]
+    unsigned *tokens = reinterpret_cast<unsigned *>(lists + p.merge_lists * best);   // [beams][best]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ptx::launch_dependents();
     ptx::wait_prerequisites();
 
+    // ---- a warp a row: its best from its stretches' lists, and its sum
     const int64_t request = blockIdx.x, r = request * beams + warp;
-    // ---- a warp a row: its log-sum-exp and its best, from the stretches' lists
     const float before = p.a.scores[r];
-    const int entries = p.stretches * best;
-    uint64_t *list = lists + warp * entries;
+    // one stretch in each CTA that has a part of the row
+    const int64_t first = r * p.chunks / p.each + r;
+    const int stretches = (int)(((r + 1) * p.chunks - 1) / p.each + r - first) + 1;
+    uint64_t *list = lists + (first - (request * beams * p.chunks / p.each + request * beams)) * best;
+    uint64_t *mine = scores + warp * (best + 1);
     int have = 0;
     if (before != -INFINITY) {
-        for (int i = lane; i < entries; i += 32) list[i] = p.lists[r * entries + i];
-        __syncwarp();
-        const float2 sum = lane < p.stretches ? p.sums[r * p.stretches + lane] : make_float2(-INFINITY, 0.f);
-        float top = sum.x;
+        const float2 *row_sums = p.sums + r * p.chunks * kWarps;
+        const int64_t parts = p.chunks * kWarps;
+        float top = -INFINITY;
+        double all = 0.;
+        for (int i = lane; i < stretches * best; i += 32) list[i] = p.lists[first * best + i];
+        for (int64_t i = lane; i < parts; i += 32) top = fmaxf(top, row_sums[i].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        double all = top == -INFINITY ? (double)sum.y : (double)sum.y * exp((double)sum.x - (double)top);
-        if (sum.x == -INFINITY && sum.y == 0.f) all = 0.;
+        for (int64_t i = lane; i < parts; i += 32) {
+            const float2 s = row_sums[i];
+            // a chunk without a logit has the sum 0, or NaN
+            all += s.x > -INFINITY ? s.y * power((s.x - top) * kLog2e) : s.y;
+        }
 #pragma unroll
         for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
         const bool sound = all >= 0. && top < INFINITY && before < INFINITY;         // not for NaN
-        if (!sound) {
-            if (lane == 0) raise_status(p.status, kStatusBadIndex);
-        } else if (all > 0.) {
-            const double lse = (double)top + log(all);
-            list += lane * best;      // of a stretch: none behind the last
+        if (!sound && lane == 0) raise_status(p.status, kStatusBadIndex);
+        if (lane == 0) {
+            tops[warp] = top;
+            sums[warp] = sound ? all : 0.;
+        }
+        __syncwarp();
+        if (sound && all > 0.) {
+            list += lane * best;      // of a stretch: 0 behind the last
             int at = 0;
-            uint64_t head = lane < p.stretches ? list[0] : 0;
+            uint64_t head = lane < stretches ? list[0] : 0;
             for (; have < best; ++have) {
                 const uint64_t key = warp_max(head);
                 if (key == 0) break;
                 if (head == key) head = ++at < best ? list[at] : 0;
-                if (lane == 0) {
-                    scores[warp * (best + 1) + have] = order_of((double)before + ((double)logit_of(key) - lse));
-                    tokens[warp * best + have] = token_of(key);
-                }
+                if (lane == 0) mine[have] = key;
             }
         }
     }
-    if (lane == 0) scores[warp * (best + 1) + have] = 0;
+    __syncthreads();
+    if (warp == 0 && lane < beams) lses[lane] = (double)tops[lane] + log(sums[lane]);
+    __syncthreads();
+    for (int i = lane; i <= best; i += 32) {
+        if (i < have) {
+            tokens[warp * best + i] = token_of(mine[i]);
+            mine[i] = order_of((double)before + ((double)logit_of(mine[i]) - lses[warp]));
+        } else {
+            mine[i] = 0;
+        }
+    }
     __syncthreads();
     if (warp > 0) return;
 
@@ -441,9 +636,9 @@ reorder_kernel(const __grid_constant__ StateParams p)
     }
 }
 
-constexpr size_t merge_bytes(int64_t beams, int64_t keys, int64_t best)
+constexpr size_t merge_bytes(int64_t beams, int64_t lists, int64_t best)
 {
-    return 8 * keys + beams * (8 * (best + 1) + 4 * best);
+    return 8 * lists * best + beams * (8 * (best + 1) + 4 * best);
 }
 
 template <typename T>
@@ -451,14 +646,21 @@ const void *rows_kernel() { return (const void *)beam_rows_kernel<T>; }
 
 } // namespace
 
-// As many stretches as give every SM eight CTAs, each of four pieces a thread at least,
-// and a request's lists the room that they have in the merge.
-int beam_stretches(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
+// The line of all rows' chunks, cut into equal parts for as many CTAs as the GPU holds; a row has at
+// most 32 stretches (a lane each in the merge), and a request's lists the room that they have there.
+BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
 {
-    const int64_t rows = std::max<int64_t>(requests * beams, 1);
-    const int64_t pieces = vocab * element_bytes / (16 * kThreads * kLoads);
-    return (int)std::max<int64_t>(
-        1, std::min({(8 * 152 + rows - 1) / rows, pieces, int64_t(kMergeKeys) / (beams * best), int64_t(32)}));
+    BeamCut c;
+    c.chunks = std::max<int64_t>(1, (vocab / (16 / element_bytes) + kChunk - 1) / kChunk);
+    const int64_t total = requests * beams * c.chunks;
+    const int64_t lists = kMergeKeys / best - beams - 1;
+    c.each = std::max({(total + 2 * 152 - 1) / (2 * 152), (c.chunks + 30) / 31, (beams * c.chunks + lists - 1) / lists,
+                       int64_t(1)});
+    c.ctas = (total + c.each - 1) / c.each;
+    c.merge_lists = beams * c.chunks / c.each + beams + 1;
+    // 8-byte words of the workspace: best keys a stretch, maximum and sum of each chunk and warp
+    c.words = (c.ctas + requests * beams) * best + total * kWarps;
+    return c;
 }
 
 cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
@@ -466,20 +668,28 @@ cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
     BeamParams p{};
     p.a = a;
     p.status = device_status_word();
-    p.element = a.dtype == AWQ_F32 ? 4 : 2;
-    const int64_t rows = a.requests * a.beams;
     p.best = (int)(a.num_beams + a.num_ends);
-    p.stretches = beam_stretches(a.requests, a.beams, a.vocab, p.best, p.element);
+    p.rows = a.requests * a.beams;
+    const BeamCut c = beam_cut(a.requests, a.beams, a.vocab, p.best, a.dtype == AWQ_F32 ? 4 : 2);
+    p.chunks = c.chunks;
+    p.each = c.each;
+    p.merge_lists = (int)c.merge_lists;
     p.lists = static_cast<uint64_t *>(a.workspace);
-    p.sums = reinterpret_cast<float2 *>(p.lists + rows * p.stretches * p.best);
+    p.sums = reinterpret_cast<float2 *>(p.lists + (c.ctas + p.rows) * p.best);
+#ifdef AWQ_FAULT_TEST
+    p.fault = fault_injection();
+#endif
     void *args[] = {&p};
     const void *kernel = a.dtype == AWQ_F16 ? rows_kernel<__half>()
                          : a.dtype == AWQ_BF16 ? rows_kernel<__nv_bfloat16>() : rows_kernel<float>();
-    cudaError_t e = allow_shared((const void *)beam_merge_kernel, merge_bytes(kMostBeams, kMergeKeys, kMostBest));
-    if (e == cudaSuccess) e = launch_dependent(kernel, rows * p.stretches, kThreads, 0, stream, args);
+    constexpr size_t ring = kStages * kChunk * sizeof(uint4);
+    cudaError_t e = allow_shared(kernel, ring);
+    if (e == cudaSuccess)
+        e = allow_shared((const void *)beam_merge_kernel, 8 * kMergeKeys + merge_bytes(kMostBeams, 0, kMostBest));
+    if (e == cudaSuccess) e = launch_dependent(kernel, c.ctas, kThreads + 32, ring, stream, args);
     if (e != cudaSuccess) return e;
-    const size_t smem = merge_bytes(a.beams, a.beams * p.stretches * p.best, p.best);
-    return launch_dependent((const void *)beam_merge_kernel, a.requests, 32 * (int)a.beams, smem, stream, args);
+    return launch_dependent((const void *)beam_merge_kernel, a.requests, 32 * (int)a.beams,
+                            merge_bytes(a.beams, c.merge_lists, p.best), stream, args);
 }
 
 cudaError_t launch_reorder_states(const awq_state_t *states, int64_t count, const int32_t *parents, int64_t rows_out,

@@ -160,8 +160,11 @@ cudaError_t launch_process_logits(const awq_logits_t &a, cudaStream_t stream);
 
 cudaError_t launch_rotary(const awq_rotary_t &a, cudaStream_t stream);
 
-// stretches that a row of logits is read in
-int beam_stretches(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes);
+// How beam_select's rows are shared out over CTAs, and its workspace in words of 8 bytes.
+struct BeamCut {
+    int64_t chunks, each, ctas, merge_lists, words;
+};
+BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes);
 cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream);
 
 cudaError_t launch_reorder_states(const awq_state_t *states, int64_t count, const int32_t *parents, int64_t rows_out,

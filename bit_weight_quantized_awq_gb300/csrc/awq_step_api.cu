@@ -194,8 +194,7 @@ int64_t awq_beam_select_workspace(int64_t requests, int64_t beams, int64_t vocab
         (dtype != AWQ_F16 && dtype != AWQ_BF16 && dtype != AWQ_F32))
         return -1;
     const int64_t best = num_beams + num_ends;
-    const int64_t stretches = awq::beam_stretches(requests, beams, vocab, best, dtype == AWQ_F32 ? 4 : 2);
-    return requests * beams * stretches * (8 * best + 8);
+    return 8 * awq::beam_cut(requests, beams, vocab, best, dtype == AWQ_F32 ? 4 : 2).words;
 }
 
 awq_status_t awq_beam_select(const awq_beam_select_t *args, awq_stream_t stream)
