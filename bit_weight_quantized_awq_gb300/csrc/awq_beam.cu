@@ -1,12 +1,12 @@
 // awq_beam.cu -- one step of beam search over the logits, and rows of other state by parent.
 //
-// beam_rows_kernel reads every logit once. The rows are a line of chunks of 1024 16-byte
+// beam_rows_kernel reads every logit once. The rows are a line of chunks of 512 16-byte
 // pieces, cut into equal parts, one a CTA; a producer warp keeps a ring of bulk copies under way
 // across rows, so that HBM does not wait while a row's end is worked on. Each thread keeps the
 // maximum of what it has read. No list is kept while the logits stream by: the best K of a part
 // of a row can only lie with the K threads whose maxima are the greatest (each of them has an element
 // at least as great as the K-th greatest maximum, any other thread has none). Those
-// threads' pieces, K / 256 of the part, are read a second time, from the L2 cache, and what
+// threads' pieces, where their chunks' maxima allow, are read a second time, from the L2 cache, and what
 // reaches the K-th greatest maximum is sorted out. Logits that are equal are told apart by
 // their place, so all keys differ and the time does not depend on the data.
 //
@@ -15,8 +15,8 @@
 // the same place within 16 bytes) have equal ones, and their beams tie as they should.
 //
 // beam_merge_kernel, a CTA a request, adds up a row's sums in 64 bits, merges the lists of its
-// parts, a warp a row, and takes the best over the rows. The logarithms, in fp64, are one a lane of one warp:
-// by all warps they took longer than all the rest (fp64 runs at two operations a clock).
+// parts and takes the best over the rows: pairs of fp32 numbers stand for 64 bits, since fp64 runs at two
+// operations a clock, and only for the few candidates that fp32 does not rule out.
 //
 // Bound: HBM, one read of the logits; one exponential a logit.
 #include <algorithm>
@@ -31,11 +31,14 @@
 namespace awq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;          // of the working warps
 constexpr int kLoads = 4;             // 16-byte pieces of a thread under way
 constexpr int kMostBeams = 32, kMostEnds = 8, kMostBest = kMostBeams + kMostEnds;
-constexpr int kMergeKeys = 8192;      // keys of a request's lists in the merge's shared memory
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMergeKeys = 6144;      // keys of a request's lists in the merge's shared memory
+constexpr int kMergeLists = 640;      // and its lists: as many as there are CTAs and beams, 608 + 32
+constexpr int kNoRow = 255;
+constexpr int kMostEnding = kMostBeams * kMostEnds;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct BeamParams {
     awq_beam_select_t a;
@@ -151,32 +154,6 @@ struct Row {
     __device__ unsigned token(int piece) const { return (unsigned)(piece * kEach - lead); }
 };
 
-// Two fp32 values in one register pair.
-__device__ __forceinline__ uint64_t both(float a, float b)
-{
-    uint64_t v;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
-    return v;
-}
-__device__ __forceinline__ float2 apart(uint64_t v)
-{
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t v;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t v;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-    return v;
-}
-
 // The greatest of a piece's elements as they are (a NaN gives way to a number), joined with `top`'s.
 template <typename T>
 __device__ __forceinline__ uint32_t top_of(uint4 v, uint32_t top)
@@ -224,19 +201,27 @@ __device__ __forceinline__ uint64_t warp_sort(uint64_t key)
 }
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = kThreads * kLoads;     // pieces: 16 KB, a stage of the ring
-constexpr int kStages = 5;
+constexpr int kChunk = kThreads * kLoads;     // pieces: 8 KB, a stage of the ring
+constexpr int kPerSm = 4;             // CTAs: while one sorts, the others read
+constexpr int kStages = 3;
+constexpr int kKnown = 64;            // chunks of a part whose threads' maxima are kept
+constexpr int kLeastChunks = 2;
+constexpr int kAtOnce = 8;            // units of a warp under way
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads + 32, 2)
+__global__ void __launch_bounds__(kThreads + 32, kPerSm)
 beam_rows_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int kEach = 16 / sizeof(T);
-    constexpr int kRoom = kMostBest + kThreads * kEach + 32;
+    constexpr int kUnit = kLoads * kEach;                // elements of a thread in a chunk
+    constexpr int kRound = 1024 / kUnit;                 // units read between two looks at the list's length
+    constexpr int kRoom = kMostBest + kRound * kUnit + 32;
     extern __shared__ __align__(128) uint4 ring[];       // [kStages][kChunk]
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t keys[kRoom], sorted[kWarps][32], leaders[kMostBest];
-    __shared__ int who[kMostBest], listed[2];
+    __shared__ uint16_t highs[kKnown][kThreads];         // upper halves of the threads' maxima, in their order
+    __shared__ uint16_t todo[kMostBest * kKnown];
+    __shared__ int who[kMostBest], listed[2], todos;
     __shared__ uint64_t least;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -321,15 +306,17 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
                     break;
                 }
                 ++used;
-                const int left = row.end - i - tid * kLoads;
+                // in an order that keeps eight lanes off one another's banks
 #pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    // in an order that keeps eight lanes off one another's banks
-                    const int piece = (u + (tid >> 1)) % kLoads;
-                    v[u] = ring[s * kChunk + tid * kLoads + piece];
-                    if (piece >= left) v[u] = make_uint4(nothing, nothing, nothing, nothing);
-                    all = top_of<T>(v[u], all);
+                for (int u = 0; u < kLoads; ++u) v[u] = ring[s * kChunk + tid * kLoads + (u + (tid >> 1)) % kLoads];
+                if (row.end - i < kChunk) {
+#pragma unroll
+                    for (int u = 0; u < kLoads; ++u)
+                        if (i + tid * kLoads + (u + (tid >> 1)) % kLoads >= row.end)
+                            v[u] = make_uint4(nothing, nothing, nothing, nothing);
                 }
+#pragma unroll
+                for (int u = 0; u < kLoads; ++u) all = top_of<T>(v[u], all);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_addr(empty + s));
             } else {
@@ -342,25 +329,34 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
                 where = j;
             }
             const float alone = j == single_chunk ? single : -INFINITY;
-            const uint32_t order = __reduce_max_sync(0xFFFFFFFFu, (uint32_t)(key_of(fmaxf(top, alone), 0) >> 32));
+            uint32_t order = (uint32_t)(key_of(top, 0) >> 32);
+            if (j - j0 < kKnown) highs[j - j0][tid] = (uint16_t)(order >> 16);
+            order = __reduce_max_sync(0xFFFFFFFFu, max(order, (uint32_t)(key_of(alone, 0) >> 32)));
             const float most = logit_of((uint64_t)order << 32), base = most > -INFINITY ? most : 0.f;
-            const uint64_t minus = both(-base, -base), scale = both(kLog2e, kLog2e);
-            uint64_t s0 = 0, s1 = 0;
+            // 2^(x log2 e - shift), one FMA; what shift's own rounding did is put right below
+            const float shift = base * kLog2e;
+            float sums[4] = {};
+            if (fabsf(base) < 0x1p120f) {
 #pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                float x[kEach];
-                widen<T>(v[u], x);
+                for (int u = 0; u < kLoads; ++u) {
+                    float x[kEach];
+                    widen<T>(v[u], x);
 #pragma unroll
-                for (int k = 0; k < kEach; k += 2) {
-                    const float2 t = apart(mul2(add2(both(x[k], x[k + 1]), minus), scale));
-                    const uint64_t e = both(power(t.x), power(t.y));
-                    if (k & 2) s1 = add2(s1, e);
-                    else s0 = add2(s0, e);
+                    for (int k = 0; k < kEach; ++k) sums[k % 4] += power(fmaf(x[k], kLog2e, -shift));
+                }
+            } else {      // where that product would leave fp32
+#pragma unroll 1
+                for (int u = 0; u < kLoads; ++u) {
+                    float x[kEach];
+                    widen<T>(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], x);
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) sums[k % 4] += power((x[k] - base) * kLog2e);
                 }
             }
-            const float2 sum2 = apart(add2(s0, s1));
+            float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+            if (fabsf(base) < 0x1p120f) sum = fmaf(sum, -kLn2 * fmaf(base, kLog2e, -shift), sum);
             // a NaN stays one
-            float sum = sum2.x + sum2.y + power((alone - base) * kLog2e);
+            sum += power((alone - base) * kLog2e);
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
             if (lane == 0) p.sums[(r * p.chunks + j) * kWarps + warp] = make_float2(most, sum);
@@ -370,7 +366,10 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         // before it in the other warps' lists. Equal maxima go by the place of their pieces, so keys differ
         const uint64_t key = warp_sort(m > -INFINITY ? key_of(m, (unsigned)((where - j0) * kThreads + tid)) : 0);
         sorted[warp][lane] = key;
-        if (tid == 0) least = 0;
+        if (tid == 0) {
+            least = 0;
+            todos = 0;
+        }
         if (!ptx::named_barrier_and(1, kThreads, landed)) break;
         if (key && lane < p.best) {
             int rank = lane;
@@ -394,42 +393,60 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         for (int w = 0; w < kWarps; ++w) leads += __popc(__ballot_sync(0xFFFFFFFFu, sorted[w][lane] >= max(least, (uint64_t)1)));
         const uint32_t floor_value = (uint32_t)(least >> 32);
         uint64_t floor = 0;                   // of whole keys, once a list has been cut
-        const int items = leads * (j1 - j0) * kLoads;
         int *count = &listed[turn & 1];
         auto enlist = [&](float x, unsigned token) {
             const uint64_t k = key_of(x, token);
             if (x > -INFINITY && (uint32_t)(k >> 32) >= floor_value && k >= floor) keys[atomicAdd(count, 1)] = k;
         };
         enlist(single, single_token);
-        for (int e0 = 0; e0 < items; e0 += kThreads) {
-            const int e = e0 + tid;
-            if (e < items) {
-                const int l = e / kLoads % leads, j = e / kLoads / leads;
-                const int piece = row.whole + (j0 + j) * kChunk + who[l] * kLoads + e % kLoads;
-                if (piece < row.end) {
-                    float x[kEach];
-                    widen<T>(row.pieces[piece], x);
-                    // equal to the least maximum: only from its place on, so that no list overflows
-                    const uint64_t place = (uint64_t)floor_value << 32 | (0xFFFFFFFFu - (unsigned)(j * kThreads + who[l]));
-#pragma unroll
-                    for (int k = 0; k < kEach; ++k)
-                        if ((uint32_t)(key_of(x[k], 0) >> 32) > floor_value || place >= least) enlist(x[k], row.token(piece) + k);
-                }
-            }
-            ptx::named_barrier(1, kThreads);
-            const int have = *count;
-            ptx::named_barrier(1, kThreads);
-            if (have > kMostBest && e0 + kThreads < items) {      // room for the next round
-                if (warp == 0) {
-                    warp_best(keys, have, p.best, leaders);
-                    for (int k = lane; k < p.best; k += 32) keys[k] = leaders[k];
-                    if (lane == 0) *count = p.best;
-                }
+        for (int g0 = j0; g0 < j1; g0 += kKnown) {
+            // the units -- chunk g0 + e / leads of thread who[e % leads] -- whose maximum is great enough
+            const int units = leads * min(kKnown, j1 - g0);
+            if (g0 > j0) {
+                if (tid == 0) todos = 0;
                 ptx::named_barrier(1, kThreads);
-                floor = keys[p.best - 1];
+            }
+            for (int e = tid; e < units; e += kThreads)
+                if (g0 > j0 || highs[e / leads][who[e % leads]] >= floor_value >> 16) todo[atomicAdd(&todos, 1)] = (uint16_t)e;
+            ptx::named_barrier(1, kThreads);
+            // their elements, a lane each
+            const int all = todos;
+            for (int i0 = 0; i0 < all; i0 += kRound) {
+                for (int i = i0 + warp * kAtOnce; i < min(i0 + kRound, all); i += kWarps * kAtOnce) {
+                    float x[kAtOnce];
+                    int element[kAtOnce];
+                    bool behind[kAtOnce];
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        const int e = todo[min(i + u, all - 1)], j = g0 + e / leads, l = who[e % leads];
+                        const int piece = row.whole + j * kChunk + l * kLoads;
+                        element[u] = (int)row.token(piece) + lane;
+                        // equal to the least maximum: only up to its place, so that lists stay short
+                        behind[u] = ((uint64_t)floor_value << 32 | (0xFFFFFFFFu - (unsigned)((j - j0) * kThreads + l))) < least;
+                        x[u] = -INFINITY;
+                        if (i + u < all && lane < kUnit && piece + lane / kEach < row.end) x[u] = one(row.row + element[u]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (x[u] > -INFINITY && (!behind[u] || (uint32_t)(key_of(x[u], 0) >> 32) > floor_value))
+                            enlist(x[u], element[u]);
+                }
+                if (i0 + kRound >= all && g0 + kKnown >= j1) break;
+                ptx::named_barrier(1, kThreads);
+                const int have = *count;
+                ptx::named_barrier(1, kThreads);
+                if (have > kMostBest) {               // room for the next round
+                    if (warp == 0) {
+                        warp_best(keys, have, p.best, leaders);
+                        for (int k = lane; k < p.best; k += 32) keys[k] = leaders[k];
+                        if (lane == 0) *count = p.best;
+                    }
+                    ptx::named_barrier(1, kThreads);
+                    floor = keys[p.best - 1];
+                }
             }
         }
-        if (items == 0) ptx::named_barrier(1, kThreads);
+        ptx::named_barrier(1, kThreads);
         const int have = *count;
         const int64_t slot = blockIdx.x + r;
         if (tid == 0) listed[turn & 1 ^ 1] = 0;
@@ -451,129 +468,261 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
     }
 }
 
-// Order of 64-bit scores as whole numbers; no candidate is 0.
-__device__ __forceinline__ uint64_t order_of(double s)
+// A sum of fp32 numbers with what its roundings lost (Knuth's two-sum): 2^-47 of it for the price of
+// fp32, where fp64 runs at two operations a clock.
+struct Sum {
+    float high = 0.f, low = 0.f;
+    __device__ __forceinline__ void add(float x)
+    {
+        const float s = high + x, t = s - high;
+        low += (high - (s - t)) + (x - t);
+        high = s;
+    }
+    // low below half of high's last place
+    __device__ __forceinline__ void settle()
+    {
+        const float s = high + low;
+        low -= s - high;
+        high = s;
+    }
+};
+
+// Adds ln(x.high + x.low), normal and positive, to `to`: x = 2^e m with m in [2/3, 4/3), ln m by the series of
+// 2 atanh(t) in t = (m - 1) / (m + 1), |t| <= 1/5. The quotient has its remainder; behind the first term
+// fp32 will do (2^-34 of ln m).
+__device__ __forceinline__ void add_log(Sum x, Sum &to)
 {
-    const uint64_t b = (uint64_t)__double_as_longlong(s + 0.);
-    return b ^ ((int64_t)b < 0 ? ~(uint64_t)0 : (uint64_t)1 << 63);
+    int bits = __float_as_int(x.high);
+    const int e = (bits - 0x3F2AAAAB) >> 23;
+    const float scale = __int_as_float((127 - e) << 23);       // two times below for e near the ends: sums are 1 to 2^28
+    const float m = x.high * scale, a = m - 1.f, b = m + 1.f;
+    const float r = 1.f / b, t = a * r;
+    // (a - t (m + 1)) / (m + 1), of b's own rounding too, and of x.low
+    const float rest = fmaf(-t, b, a) - t * (m - (b - 1.f));
+    const float t_low = (rest + x.low * scale * (1.f - t)) * r;
+    const float s = t * t;
+    const float more = t * s * (2.f / 3 + s * (2.f / 5 + s * (2.f / 7 + s * (2.f / 9 + s * (2.f / 11 + s * (2.f / 13))))));
+    to.add((float)e * 0.693145751953125f);                     // ln 2 in 14 bits, and the rest
+    to.add(2.f * t);
+    // of t's remainder the whole series' slope, 2 / (1 - t^2)
+    to.low += (float)e * 1.42860682e-6f + 2.f * t_low * (1.f + s * (1.f + s)) + more;
+    to.settle();
 }
 
-__device__ __forceinline__ double score_of(uint64_t o)
+// Order of such sums as whole numbers; no candidate is 0.
+__device__ __forceinline__ uint64_t order_of(Sum s)
 {
-    return __longlong_as_double((int64_t)(o >> 63 ? o ^ (uint64_t)1 << 63 : ~o));
+    return (key_of(s.high, 0) & 0xFFFFFFFF00000000ull) | key_of(s.low, 0) >> 32;
 }
 
 __global__ void __launch_bounds__(32 * kMostBeams)
 beam_merge_kernel(const __grid_constant__ BeamParams p)
 {
     extern __shared__ uint64_t merge_smem[];
-    __shared__ double sums[kMostBeams], lses[kMostBeams];
-    __shared__ float tops[kMostBeams];
-    const int beams = (int)p.a.beams, best = p.best, keep = (int)p.a.num_beams;
-    uint64_t *scores = merge_smem;                                  // [beams][best + 1]: a row's best, 0 behind the last
-    uint64_t *lists = scores + beams * (best + 1);                  // [stretches of all rows][best]
-    unsigned *tokens = reinterpret_cast<unsigned *>(lists + p.merge_lists * best);   // [beams][best]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ Sum lses[kMostBeams];                     // of the rows that have candidates
+    __shared__ float befores[kMostBeams];
+    __shared__ bool sound[kMostBeams];
+    __shared__ int first_list[kMostBeams], last_list[kMostBeams], end_tokens[kMostEnds];
+    __shared__ uint8_t row_of_list[kMergeLists];
+    __shared__ __align__(16) float heads[kMergeLists];
+    __shared__ float floor;
+    __shared__ uint64_t ending[kMostEnding];
+    __shared__ int ending_at[kMostEnding], picked, endings, told;
+    const int beams = (int)p.a.beams, best = p.best, keep = (int)p.a.num_beams, threads = blockDim.x;
+    const int ends = (int)p.a.num_ends;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t request = blockIdx.x, r0 = request * beams;
+    // a row has one list in each CTA that had a part of it
+    const int64_t first = r0 * p.chunks / p.each + r0;
+    if (tid < beams) {
+        const int64_t begin = (r0 + tid) * p.chunks;
+        first_list[tid] = (int)(begin / p.each + r0 + tid - first);
+        last_list[tid] = (int)((begin + p.chunks - 1) / p.each + r0 + tid - first);
+    }
+    if (tid == 0) {
+        picked = endings = told = 0;
+        floor = -INFINITY;
+    }
+    // a number that no part has, where a row and a CTA's share end together
+    for (int l = tid; l < p.merge_lists; l += threads) row_of_list[l] = kNoRow;
+    __syncthreads();
+    const int lists = last_list[beams - 1] + 1, candidates = lists * best;
+    uint64_t *keys = merge_smem, *picks = keys + p.merge_lists * best;      // picks: what reaches `floor`
+    int *pick_at = reinterpret_cast<int *>(picks + p.merge_lists * best);
+    float *highs = reinterpret_cast<float *>(pick_at + p.merge_lists * best);
+    if (warp < beams)
+        for (int l = first_list[warp] + lane; l <= last_list[warp]; l += 32) row_of_list[l] = warp;
     ptx::launch_dependents();
     ptx::wait_prerequisites();
 
-    // ---- a warp a row: its best from its stretches' lists, and its sum
-    const int64_t request = blockIdx.x, r = request * beams + warp;
-    const float before = p.a.scores[r];
-    // one stretch in each CTA that has a part of the row
-    const int64_t first = r * p.chunks / p.each + r;
-    const int stretches = (int)(((r + 1) * p.chunks - 1) / p.each + r - first) + 1;
-    uint64_t *list = lists + (first - (request * beams * p.chunks / p.each + request * beams)) * best;
-    uint64_t *mine = scores + warp * (best + 1);
-    int have = 0;
-    if (before != -INFINITY) {
+    // ---- the lists of the request's rows, and a warp a row: its sum
+    if (tid < ends) end_tokens[tid] = p.a.end_tokens[tid];
+    for (int c = tid; c < candidates; c += threads) keys[c] = p.lists[first * best + c];
+    if (warp < beams) {
+        const int64_t r = r0 + warp;
+        const float before = p.a.scores[r];
         const float2 *row_sums = p.sums + r * p.chunks * kWarps;
         const int64_t parts = p.chunks * kWarps;
+        constexpr int kHeld = 8;
+        float2 held[kHeld];
         float top = -INFINITY;
-        double all = 0.;
-        for (int i = lane; i < stretches * best; i += 32) list[i] = p.lists[first * best + i];
-        for (int64_t i = lane; i < parts; i += 32) top = fmaxf(top, row_sums[i].x);
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            held[i] = lane + 32 * i < parts ? row_sums[lane + 32 * i] : make_float2(-INFINITY, 0.f);
+            top = fmaxf(top, held[i].x);
+        }
+        for (int64_t i = lane + 32 * kHeld; i < parts; i += 32) top = fmaxf(top, row_sums[i].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        for (int64_t i = lane; i < parts; i += 32) {
-            const float2 s = row_sums[i];
-            // a chunk without a logit has the sum 0, or NaN
-            all += s.x > -INFINITY ? s.y * power((s.x - top) * kLog2e) : s.y;
-        }
+        // a chunk without a logit has the sum 0, or NaN
+        auto part = [&](float2 s) { return s.x > -INFINITY ? s.y * power((s.x - top) * kLog2e) : s.y; };
+        Sum all;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-        const bool sound = all >= 0. && top < INFINITY && before < INFINITY;         // not for NaN
-        if (!sound && lane == 0) raise_status(p.status, kStatusBadIndex);
+        for (int i = 0; i < kHeld; ++i)
+            if (32 * i < parts) all.add(part(held[i]));
+        for (int64_t i = lane + 32 * kHeld; i < parts; i += 32) all.add(part(row_sums[i]));
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            // the same on both lanes of a pair
+            const float high = __shfl_xor_sync(0xFFFFFFFFu, all.high, d), low = __shfl_xor_sync(0xFFFFFFFFu, all.low, d);
+            const float great = fmaxf(all.high, high), small = fminf(all.high, high);
+            const bool bad = !(all.high >= 0.f && high >= 0.f);
+            all.low += low;
+            all.high = great;
+            all.add(small);
+            if (bad) all.high = NAN;
+        }
         if (lane == 0) {
-            tops[warp] = top;
-            sums[warp] = sound ? all : 0.;
-        }
-        __syncwarp();
-        if (sound && all > 0.) {
-            list += lane * best;      // of a stretch: 0 behind the last
-            int at = 0;
-            uint64_t head = lane < stretches ? list[0] : 0;
-            for (; have < best; ++have) {
-                const uint64_t key = warp_max(head);
-                if (key == 0) break;
-                if (head == key) head = ++at < best ? list[at] : 0;
-                if (lane == 0) mine[have] = key;
-            }
+            // without a beam nothing was written; NaN fails all comparisons
+            const bool fine = all.high >= 0.f && top < INFINITY && before < INFINITY;
+            if (!fine && before != -INFINITY) raise_status(p.status, kStatusBadIndex);
+            sound[warp] = fine && all.high > 0.f && before != -INFINITY;
+            befores[warp] = before;
+            Sum lse;
+            lse.high = top;
+            if (sound[warp]) add_log(all, lse);
+            lses[warp] = lse;
         }
     }
     __syncthreads();
-    if (warp == 0 && lane < beams) lses[lane] = (double)tops[lane] + log(sums[lane]);
-    __syncthreads();
-    for (int i = lane; i <= best; i += 32) {
-        if (i < have) {
-            tokens[warp * best + i] = token_of(mine[i]);
-            mine[i] = order_of((double)before + ((double)logit_of(mine[i]) - lses[warp]));
-        } else {
-            mine[i] = 0;
-        }
-    }
-    __syncthreads();
-    if (warp > 0) return;
 
-    // ---- the best over the rows, a lane a row
-    const int ends = (int)p.a.num_ends;
-    const int end = lane < ends ? p.a.end_tokens[lane] : -1;
-    int at = 0, live = 0, ended = 0;
-    uint64_t head = lane < beams ? scores[lane * (best + 1)] : 0;
-    for (int rank = 0; live < keep; ++rank) {
-        const uint64_t top = warp_max(head);
-        if (top == 0) break;
-        // equal scores: the lowest row
-        const int w = __ffs(__ballot_sync(0xFFFFFFFFu, head == top)) - 1;
-        const int token = (int)tokens[w * best + __shfl_sync(0xFFFFFFFFu, at, w)];
-        if (lane == w) head = scores[lane * (best + 1) + ++at];
-        const bool ends_here = __any_sync(0xFFFFFFFFu, lane < ends && end == token);
-        if (ends_here && rank >= keep) continue;
-        if (lane == 0) {
-            const int64_t to = request * keep + (ends_here ? ended : live);
-            (ends_here ? p.a.ended_scores : p.a.out_scores)[to] = (float)score_of(top);
-            (ends_here ? p.a.ended_parents : p.a.out_parents)[to] = (int)(request * beams + w);
-            (ends_here ? p.a.ended_tokens : p.a.out_tokens)[to] = token;
+    // ---- every candidate's score in fp32, with a bound of what that is off by (16 times its roundings); NaN for
+    // none. Those that end are put aside
+    auto near = [&](uint64_t key, int w, float &off) {
+        const float x = logit_of(key);
+        off = fabsf(befores[w]) * 0x1p-20f + fabsf(x) * 0x1p-20f + fabsf(lses[w].high) * 0x1p-20f;
+        return befores[w] + (x - lses[w].high);
+    };
+    auto exact = [&](int c) {
+        const int w = row_of_list[c / best];
+        Sum s;
+        s.high = logit_of(keys[c]);
+        s.add(-lses[w].high);
+        s.add(befores[w]);
+        s.low -= lses[w].low;
+        s.settle();
+        if (!(fabsf(s.high) < INFINITY)) s.low = 0.f;
+        return order_of(s);
+    };
+    for (int c = tid; c < candidates; c += threads) {
+        const uint64_t key = keys[c];
+        const int w = row_of_list[c / best];
+        highs[c] = NAN;
+        if (w == kNoRow || key == 0 || !sound[w]) continue;
+        bool stops = false;
+        for (int i = 0; i < ends; ++i) stops |= end_tokens[i] == (int)token_of(key);
+        float off;
+        const float s = near(key, w, off);
+        if (!stops) {
+            highs[c] = s + off;
+        } else if (const int i = atomicAdd(&endings, 1); i < kMostEnding) {
+            ending[i] = exact(c);
+            ending_at[i] = c;
         }
-        if (ends_here) ++ended;
-        else ++live;
     }
-    for (int k = live + lane; k < keep; k += 32) {
-        p.a.out_scores[request * keep + k] = -INFINITY;
-        p.a.out_parents[request * keep + k] = -1;
-        p.a.out_tokens[request * keep + k] = -1;
+    __syncthreads();
+
+    // ---- The first `keep` reach `floor`: with a list's candidate number q (from 0, of those that go on) each
+    // list has q + 1 that are as good, so that where ceil(keep / (q + 1)) lists' reach it, `keep` do
+    const int q = (keep - 1) / lists, wanted = (keep + q) / (q + 1);
+    for (int l = tid; l < (lists + 3) / 4 * 4; l += threads) {
+        float head = -INFINITY;
+        for (int i = 0, live = 0; l < lists && i < best; ++i)
+            if (!isnan(highs[l * best + i]) && live++ == q) {
+                float off;
+                near(keys[l * best + i], row_of_list[l], off);
+                head = highs[l * best + i] - 3.f * off;
+                break;
+            }
+        heads[l] = head;
     }
-    for (int k = ended + lane; ends && k < keep; k += 32) {
-        p.a.ended_scores[request * keep + k] = -INFINITY;
-        p.a.ended_parents[request * keep + k] = -1;
-        p.a.ended_tokens[request * keep + k] = -1;
+    __syncthreads();
+    for (int l = tid; l < lists; l += threads) {
+        const float head = heads[l];
+        int rank = 0;
+#pragma unroll 1
+        for (int i = 0; i < lists; i += 4) {
+            const float4 h = *reinterpret_cast<const float4 *>(heads + i);
+            rank += (h.x > head || (h.x == head && i < l)) + (h.y > head || (h.y == head && i + 1 < l)) +
+                    (h.z > head || (h.z == head && i + 2 < l)) + (h.w > head || (h.w == head && i + 3 < l));
+        }
+        if (rank == wanted - 1) floor = head;
     }
+    __syncthreads();
+    for (int c = tid; c < candidates; c += threads)
+        if (highs[c] >= floor) {
+            const int i = atomicAdd(&picked, 1);
+            picks[i] = exact(c);
+            pick_at[i] = c;
+        }
+    __syncthreads();
+
+    // ---- in order: a candidate's place is the number of those before it, a warp a candidate. Equal scores go by
+    // row, then by logit and token
+    const int n = picked, e = min(endings, kMostEnding), warps = threads / 32;
+    auto place_in = [&](const uint64_t *others, const int *others_at, int count, uint64_t s, int c) {
+        int place = 0;
+        for (int j0 = 0; j0 < count; j0 += 32) {
+            const int j = j0 + lane;
+            bool before = j < count && others[j] > s;
+            if (j < count && others[j] == s && others_at[j] != c) {
+                const int d = others_at[j], rd = row_of_list[d / best], rc = row_of_list[c / best];
+                before = rd != rc ? rd < rc : keys[d] > keys[c];
+            }
+            place += __popc(__ballot_sync(0xFFFFFFFFu, before));
+        }
+        return place;
+    };
+    auto tell = [&](float *out_scores, int *out_parents, int *out_tokens, int place, uint64_t s, int c) {
+        const int64_t to = request * keep + place;
+        out_scores[to] = s ? logit_of(s) : -INFINITY;
+        out_parents[to] = s ? (int)(r0 + row_of_list[c / best]) : -1;
+        out_tokens[to] = s ? (int)token_of(keys[c]) : -1;
+    };
+    for (int i = warp; i < n + e; i += warps) {
+        const bool stops = i >= n;
+        const uint64_t s = stops ? ending[i - n] : picks[i];
+        const int c = stops ? ending_at[i - n] : pick_at[i];
+        const int live = place_in(picks, pick_at, n, s, c), gone = stops ? place_in(ending, ending_at, e, s, c) : 0;
+        if (live + gone >= keep || lane > 0) continue;
+        if (!stops) {
+            tell(p.a.out_scores, p.a.out_parents, p.a.out_tokens, live, s, c);
+        } else {
+            tell(p.a.ended_scores, p.a.ended_parents, p.a.ended_tokens, gone, s, c);
+            atomicAdd(&told, 1);
+        }
+    }
+    for (int k = n + tid; k < keep; k += threads) tell(p.a.out_scores, p.a.out_parents, p.a.out_tokens, k, 0, 0);
+    if (ends == 0) return;
+    __syncthreads();
+    for (int k = told + tid; k < keep; k += threads) tell(p.a.ended_scores, p.a.ended_parents, p.a.ended_tokens, k, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
 
 // Rows by parent, in pieces of the widest kind that the arrays' addresses, strides and
 // sizes allow; all of an array's pieces in a line, kPieces a thread under way.
+constexpr int kStateThreads = 256;
 constexpr int kStatePieces = 4;
 constexpr int kStatesPerLaunch = 64;
 
@@ -593,14 +742,14 @@ template <typename V>
 __device__ __forceinline__ void reorder_pieces(const StateParams &p, int n)
 {
     const auto &s = p.state[n];
-    const int64_t first = (int64_t)blockIdx.x * kThreads * kStatePieces;
+    const int64_t first = (int64_t)blockIdx.x * kStateThreads * kStatePieces;
     const int64_t row0 = first / s.row_pieces, total = p.rows_out * s.row_pieces;
     const int64_t off0 = first - row0 * s.row_pieces;
     V v[kStatePieces];
     V *to[kStatePieces];
 #pragma unroll
     for (int u = 0; u < kStatePieces; ++u) {
-        const int e = threadIdx.x + u * kThreads;
+        const int e = threadIdx.x + u * kStateThreads;
         to[u] = nullptr;
         if (first + e >= total) continue;
         int64_t row = row0, at = off0 + e;
@@ -620,7 +769,7 @@ __device__ __forceinline__ void reorder_pieces(const StateParams &p, int n)
         if (to[u]) *to[u] = v[u];
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kStateThreads)
 reorder_kernel(const __grid_constant__ StateParams p)
 {
     ptx::launch_dependents();
@@ -636,26 +785,24 @@ reorder_kernel(const __grid_constant__ StateParams p)
     }
 }
 
-constexpr size_t merge_bytes(int64_t beams, int64_t lists, int64_t best)
-{
-    return 8 * lists * best + beams * (8 * (best + 1) + 4 * best);
-}
+constexpr size_t merge_bytes(int64_t keys) { return (2 * sizeof(uint64_t) + sizeof(int) + sizeof(float)) * keys; }
 
 template <typename T>
 const void *rows_kernel() { return (const void *)beam_rows_kernel<T>; }
 
 } // namespace
 
-// The line of all rows' chunks, cut into equal parts for as many CTAs as the GPU holds; a row has at
+// The line of all rows' chunks, cut into equal parts for as many CTAs as the GPU holds, but of no more chunks
+// than have their maxima kept; a row has at
 // most 32 stretches (a lane each in the merge), and a request's lists the room that they have there.
 BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
 {
     BeamCut c;
     c.chunks = std::max<int64_t>(1, (vocab / (16 / element_bytes) + kChunk - 1) / kChunk);
     const int64_t total = requests * beams * c.chunks;
-    const int64_t lists = kMergeKeys / best - beams - 1;
-    c.each = std::max({(total + 2 * 152 - 1) / (2 * 152), (c.chunks + 30) / 31, (beams * c.chunks + lists - 1) / lists,
-                       int64_t(1)});
+    const int64_t lists = std::min<int64_t>(kMergeKeys / best, kMergeLists) - beams - 1;
+    c.each = std::max({std::min<int64_t>((total + kPerSm * 152 - 1) / (kPerSm * 152), kKnown), (c.chunks + 30) / 31,
+                       (beams * c.chunks + lists - 1) / lists, int64_t(kLeastChunks)});
     c.ctas = (total + c.each - 1) / c.each;
     c.merge_lists = beams * c.chunks / c.each + beams + 1;
     // 8-byte words of the workspace: best keys a stretch, maximum and sum of each chunk and warp
@@ -685,11 +832,11 @@ cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
     constexpr size_t ring = kStages * kChunk * sizeof(uint4);
     cudaError_t e = allow_shared(kernel, ring);
     if (e == cudaSuccess)
-        e = allow_shared((const void *)beam_merge_kernel, 8 * kMergeKeys + merge_bytes(kMostBeams, 0, kMostBest));
+        e = allow_shared((const void *)beam_merge_kernel, merge_bytes(kMergeKeys));
     if (e == cudaSuccess) e = launch_dependent(kernel, c.ctas, kThreads + 32, ring, stream, args);
     if (e != cudaSuccess) return e;
-    return launch_dependent((const void *)beam_merge_kernel, a.requests, 32 * (int)a.beams,
-                            merge_bytes(a.beams, c.merge_lists, p.best), stream, args);
+    return launch_dependent((const void *)beam_merge_kernel, a.requests, std::max(256, 32 * (int)a.beams),
+                            merge_bytes(c.merge_lists * p.best), stream, args);
 }
 
 cudaError_t launch_reorder_states(const awq_state_t *states, int64_t count, const int32_t *parents, int64_t rows_out,
@@ -719,14 +866,14 @@ cudaError_t launch_reorder_states(const awq_state_t *states, int64_t count, cons
             to.dst_stride = dst_stride;
             to.width = width;
             to.row_pieces = s.row_bytes >> width;
-            to.ctas = (rows_out * to.row_pieces + kThreads * kStatePieces - 1) / (kThreads * kStatePieces);
+            to.ctas = (rows_out * to.row_pieces + kStateThreads * kStatePieces - 1) / (kStateThreads * kStatePieces);
             grid = std::max(grid, to.ctas);
         }
         if (n == 0) continue;
         if (grid >= int64_t(1) << 31) return cudaErrorInvalidValue;
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)grid, (unsigned)n);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(kStateThreads);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -27,9 +27,10 @@ def scores(logits, before):
     x = np.asarray(logits, dtype=np.float64).reshape(B, W, -1)
     with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         top = x.max(-1, keepdims=True)
-        lse = top + np.log(np.exp(x - top).sum(-1, keepdims=True))
-        s = np.asarray(before, dtype=np.float64)[..., None] + (x - lse)
-    sound = np.isfinite(lse) & np.isfinite(before)[..., None]
+        total = np.log(np.exp(x - top).sum(-1, keepdims=True))
+        # not x - (top + total): next to a top of -3.4e38 the total would be lost, since 64 bits have steps of 2^75 there
+        s = np.asarray(before, dtype=np.float64)[..., None] + ((x - top) - total)
+    sound = np.isfinite(top) & np.isfinite(total) & np.isfinite(before)[..., None]
     return np.where(sound & (x > -np.inf), s, -np.inf)
 
 
