@@ -318,6 +318,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
         : "memory");
 }
 
+// Untiled bulk copy shared -> global (both 16-byte aligned, bytes % 16 == 0), tracked by the
+// issuing thread's bulk groups; and until all but the last n of those have been read.
+__device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                 ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(src), "r"(bytes) : "memory");
+}
+template <int n>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
+}
+
 // Orders this thread's earlier generic-proxy accesses (and what they
 // acquired) before its later async-proxy (TMA) accesses, in every state space.
 __device__ __forceinline__ void fence_proxy_async() {

@@ -192,7 +192,8 @@ struct PagesProblem {
     const int32_t *table, *lens, *held;
     int32_t *free_blocks, *counts;
     int32_t *new_table, *block_map, *src, *dst, *moves;
-    uint32_t *workspace;
+    uint32_t *workspace;          // bit b % 32 of word b / 32: block b is used
+    int *prefix, *groups;         // behind it: used blocks before each word, and of each group of words
     int64_t stride, new_stride, num_held;
     int rows, width, block_size, num_blocks;
 };

@@ -1,6 +1,6 @@
 // awq_pages.cu -- the pages of a paged cache between steps: fork_kernel (block tables of
 // the beams that go on), copy_pages_kernel (pages within caches), and the kernels that
-// list the free blocks and compact the used ones (mark_kernel, list_kernel, move_kernel).
+// list the free blocks and compact the used ones (mark_kernel, count_kernel, list_kernel, move_kernel).
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -174,9 +174,10 @@ struct CopyParams {
     int caches, num_blocks, block_size, parts;
     int row_pieces, head_pieces;      // of a token, of a head
     bool heads_first;                 // a head's tokens lie together
+    int runs, run_token;              // of a page: runs `head` apart, bytes of a token in one
 };
 
-__global__ void __launch_bounds__(kCopyThreads)
+__global__ void __launch_bounds__(kCopyThreads, 4)
 copy_pages_kernel(const __grid_constant__ CopyParams p)
 {
     ptx::launch_dependents();
@@ -227,12 +228,100 @@ copy_pages_kernel(const __grid_constant__ CopyParams p)
     }
 }
 
+// The same by bulk copies, for pages whose tokens lie in long runs: through a ring in shared memory, kAhead
+// loads and as many stores under way, all issued by one lane. The 32 lanes of the CTA look up 32 parts at
+// a time.
+constexpr int kRunBytes = 16384;            // of a run at once
+constexpr int kRing = 6, kAhead = 3;
+constexpr int kBulkPerSm = 2;
+constexpr int64_t kLeastRun = 4096, kLeastBulk = 16 << 20;      // bytes of a run, and of all pages, from which on they are used
+
+__global__ void __launch_bounds__(32)
+copy_runs_kernel(const __grid_constant__ CopyParams p)
+{
+    extern __shared__ __align__(128) char copy_ring[];     // [kRing][kRunBytes]
+    __shared__ uint64_t full[kRing];
+    __shared__ char *to[kRing];
+    __shared__ uint32_t size[kRing];
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < kRing; ++i) ptx::mbar_init(ptx::smem_addr(full + i), 1);
+        ptx::fence_mbar_init();
+    }
+    __syncwarp();
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    int64_t pairs = p.pairs;
+    if (p.count) pairs = min(pairs, (int64_t)max(*p.count, 0));
+    const int64_t each = (int64_t)p.caches * p.runs * p.parts, units = pairs * each;
+    int64_t loads = 0, stores = 0;
+    bool ok = true;
+    auto store = [&] {
+        const int s = (int)(stores % kRing);
+        ok = ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (stores / kRing) & 1, nullptr, p.status);
+        if (!ok) return;
+        ptx::bulk_store(to[s], ptx::smem_addr(copy_ring + s * kRunBytes), size[s]);
+        ptx::bulk_commit_group();
+        ++stores;
+    };
+    for (int64_t u0 = blockIdx.x; u0 < units; u0 += 32ll * gridDim.x) {
+        const int64_t u = u0 + (int64_t)lane * gridDim.x;
+        const char *src = nullptr;
+        char *dst = nullptr;
+        int bytes = 0;
+        if (u < units) {
+            const int64_t n = u / each;
+            const int rest = (int)(u - n * each), part = rest % p.parts, run = rest / p.parts % p.runs;
+            const int cache = rest / p.parts / p.runs;
+            const int from = p.src[n], dest = p.dst[n];
+            int tokens = p.tokens ? p.tokens[n] : p.block_size;
+            if (tokens < 0 || tokens > p.block_size) {
+                if (from != -1 && dest != -1) raise_status(p.status, kStatusBadIndex);
+                tokens = min(max(tokens, 0), p.block_size);
+            }
+            if (from == -1 || dest == -1 || from == dest) {
+            } else if (from < 0 || from >= p.num_blocks || dest < 0 || dest >= p.num_blocks) {
+                raise_status(p.status, kStatusBadIndex);
+            } else {
+                const int64_t at = run * p.head + (int64_t)part * kRunBytes;
+                bytes = max(0, min(kRunBytes, tokens * p.run_token - part * kRunBytes));
+                src = p.cache[cache] + from * p.block + at;
+                dst = p.cache[cache] + dest * p.block + at;
+            }
+        }
+        unsigned some = __ballot_sync(0xFFFFFFFFu, bytes > 0);
+        while (some) {
+            const int l = __ffs(some) - 1;
+            some &= some - 1;
+            const uint64_t from = __shfl_sync(0xFFFFFFFFu, (uint64_t)src, l), dest = __shfl_sync(0xFFFFFFFFu, (uint64_t)dst, l);
+            const uint32_t n = __shfl_sync(0xFFFFFFFFu, (uint32_t)bytes, l);
+            if (lane > 0 || !ok) continue;
+            const int s = (int)(loads % kRing);
+            // the store that read this place last: at most kRing - kAhead - 1 are committed after it
+            ptx::bulk_wait_read<kRing - kAhead - 1>();
+            to[s] = reinterpret_cast<char *>(dest);
+            size[s] = n;
+            ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), n);
+            ptx::bulk_load(ptx::smem_addr(copy_ring + s * kRunBytes), reinterpret_cast<const void *>(from), n, ptx::smem_addr(full + s));
+            if (++loads > kAhead) store();
+        }
+    }
+    if (lane > 0) return;
+    while (ok && stores < loads) store();
+    // after a wait that ran out: the copies on their way land before the shared memory goes
+    for (int64_t i = stores; i < loads; ++i)
+        ptx::mbar_wait_bounded(ptx::smem_addr(full + i % kRing), (i / kRing) & 1, nullptr, nullptr);
+    ptx::bulk_wait_all();
+}
+
 // ---------------------------------------------------------------------------
 // Used blocks as a bitmap, set from the tables (a bit that is set twice stays set: no
 // counts, and no order that results could depend on); then free blocks and moves are
 // numbered by the bits before them.
 
 constexpr int kPageThreads = 512;
+constexpr int kListWords = 64;            // of the bitmap, for a CTA
+constexpr int kManyWords = 8192;          // from here on counted in groups first
 
 // Sum of v over the threads before this one, and over all.
 __device__ __forceinline__ int block_scan(int v, int *sums, int &total)
@@ -302,60 +391,88 @@ mark_kernel(const __grid_constant__ PagesProblem p, unsigned int *status)
     if (bad) raise_status(status, bad);
 }
 
-// A CTA numbers the blocks of its words; it counts the bits before them, and all of them, by itself.
+// How many blocks of each kListWords words are used, for the lists of large caches.
+__global__ void __launch_bounds__(kPageThreads)
+count_kernel(const __grid_constant__ PagesProblem p)
+{
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    const int words = (p.num_blocks + 31) / 32, lane = threadIdx.x & 31;
+    const int groups = (words + kListWords - 1) / kListWords;
+    for (int g = (blockIdx.x * kPageThreads + threadIdx.x) / 32; g < groups; g += gridDim.x * kPageThreads / 32) {
+        int n = 0;
+        for (int i = lane; i < kListWords; i += 32)
+            if (g * kListWords + i < words) n += __popc(p.workspace[g * kListWords + i]);
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        if (lane == 0) p.groups[g] = n;
+    }
+}
+
+// A CTA numbers the blocks of kListWords words, a lane a block. It adds up the counts before them, and
+// all of them, by itself: of the words, or of count_kernel's groups where there are many.
 __global__ void __launch_bounds__(kPageThreads)
 list_kernel(const __grid_constant__ PagesProblem p)
 {
-    __shared__ int sums[kPageThreads / 32];
-    const int tid = threadIdx.x;
+    __shared__ int sums[kPageThreads / 32], before_word[kListWords];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ptx::launch_dependents();
     ptx::wait_prerequisites();
-    const int words = (p.num_blocks + 31) / 32;
-    const int w = blockIdx.x * kPageThreads + tid, w0 = blockIdx.x * kPageThreads;
+    const int words = (p.num_blocks + 31) / 32, w0 = blockIdx.x * kListWords;
+    // counts of `each` words
+    const int each = p.groups ? kListWords : 1, counts = (words + each - 1) / each;
+    auto count = [&](int i) { return p.groups ? p.groups[i] : __popc(p.workspace[i]); };
     int before = 0, all = 0, ignored;
-    for (int i = tid; i < words; i += kPageThreads) {
-        const int n = __popc(p.workspace[i]);
+#pragma unroll 4
+    for (int i = tid; i < counts; i += kPageThreads) {
+        const int n = count(i);
         all += n;
-        if (i < w0) before += n;
+        if (i * each < w0) before += n;
     }
     int used, used_before;
     block_scan(all, sums, used);
     block_scan(before, sums, used_before);
-    uint32_t word = w < words ? p.workspace[w] : 0;
-    used_before += block_scan(__popc(word), sums, ignored);
-    const int first = w * 32, blocks = w < words ? min(32, p.num_blocks - first) : 0;
-
-    if (p.free_blocks) {
-        if (w == 0) {
+    const int w = w0 + tid;
+    const int mine = tid < kListWords && w < words ? __popc(p.workspace[w]) : 0;
+    const int at = used_before + block_scan(mine, sums, ignored);
+    if (tid < kListWords) before_word[tid] = at;
+    int stays = 0;
+    if (!p.free_blocks) {
+        // used blocks below `used` stay; of the others each takes the free block of its own rank there
+        int stay = 0;
+        for (int i = tid; i < counts; i += kPageThreads)
+            if ((i + 1) * each * 32ll <= used) stay += count(i);
+        const int rest = used / 32 / each * each + tid;      // words of the count that `used` falls into
+        if (tid < each && rest * 32 < used) {
+            const int left = used - rest * 32;
+            stay += __popc(left >= 32 ? p.workspace[rest] : p.workspace[rest] & ((1u << left) - 1));
+        }
+        block_scan(stay, sums, stays);
+        if (tid < kListWords && w < words) p.prefix[w] = at;       // for the ranks that move_kernel looks up
+    }
+    __syncthreads();
+    if (blockIdx.x == 0 && tid == 0) {
+        if (p.free_blocks) {
             p.counts[0] = p.num_blocks - used;
             p.counts[1] = used;
+        } else {
+            *p.moves = used - stays;
         }
-        int at = first - used_before;
-        for (int i = 0; i < blocks; ++i) {
-            if (word >> i & 1) p.free_blocks[p.num_blocks - 1 - (used_before++)] = -1;
-            else p.free_blocks[at++] = first + i;
-        }
-        return;
     }
-    // used blocks below `used` stay; of the others each takes the free block of its own rank there
-    int stay = 0;
-    for (int i = tid; i < words; i += kPageThreads) {
-        const int left = used - i * 32;
-        if (left > 0) stay += __popc(left >= 32 ? p.workspace[i] : p.workspace[i] & ((1u << left) - 1));
-    }
-    int stays;
-    block_scan(stay, sums, stays);
-    if (w == 0) *p.moves = used - stays;
-    if (w < words) p.workspace[words + w] = used_before;       // for the ranks that move_kernel looks up
     const int half = p.num_blocks / 2;
-    for (int i = 0; i < blocks; ++i) {
-        const int b = first + i;
-        const bool in_use = word >> i & 1;
-        if (!in_use && b < used) p.dst[b - used_before] = b;
-        if (in_use && b >= used) p.src[used_before - stays] = b;
+    for (int i = warp; i < kListWords && w0 + i < words; i += kPageThreads / 32) {
+        const int b = (w0 + i) * 32 + lane;
+        if (b >= p.num_blocks) continue;
+        const uint32_t word = p.workspace[w0 + i];
+        const int rank = before_word[i] + __popc(word & ((1u << lane) - 1));      // used blocks before b
+        const bool in_use = word >> lane & 1;
+        if (p.free_blocks) {
+            p.free_blocks[in_use ? p.num_blocks - 1 - rank : b - rank] = in_use ? -1 : b;
+            continue;
+        }
+        if (!in_use && b < used) p.dst[b - rank] = b;
+        if (in_use && b >= used) p.src[rank - stays] = b;
         if (!in_use || b < used) p.block_map[b] = in_use ? b : -1;
         if (b < half && b >= used - stays) p.src[b] = p.dst[b] = -1;
-        used_before += in_use;
     }
 }
 
@@ -365,13 +482,13 @@ move_kernel(const __grid_constant__ PagesProblem p)
 {
     ptx::launch_dependents();
     ptx::wait_prerequisites();
-    const int shift = __ffs(p.block_size) - 1, words = (p.num_blocks + 31) / 32;
+    const int shift = __ffs(p.block_size) - 1;
     const int moves = *p.moves;
     const int64_t thread = (int64_t)blockIdx.x * kPageThreads + threadIdx.x, threads = (int64_t)gridDim.x * kPageThreads;
     for (int64_t i = thread; i < moves; i += threads) p.block_map[p.src[i]] = p.dst[i];
     // the first block that moves tells where the moving ones begin
     const int first = moves > 0 ? p.src[0] : p.num_blocks;
-    const int skipped = moves > 0 ? (int)p.workspace[words + (first >> 5)] +
+    const int skipped = moves > 0 ? p.prefix[first >> 5] +
                                         __popc(p.workspace[first >> 5] & ((1u << (first & 31)) - 1)) : 0;
     const int lane = threadIdx.x & 31;
     const int parts = (p.width + 255) / 256;
@@ -386,7 +503,7 @@ move_kernel(const __grid_constant__ PagesProblem p)
             int b = j < have ? p.table[r * p.stride + j] : -1;
             if (b >= p.num_blocks || b < 0) b = -1;
             if (b >= first) {
-                const int rank = (int)p.workspace[words + (b >> 5)] +
+                const int rank = p.prefix[b >> 5] +
                                  __popc(p.workspace[b >> 5] & ((1u << (b & 31)) - 1)) - skipped;
                 b = p.dst[rank];
             }
@@ -430,10 +547,26 @@ cudaError_t launch_copy_pages(const CopyProblem &c, cudaStream_t stream)
         p.head_pieces = c.head_dim / 8;
         p.row_pieces = c.kv_heads * p.head_pieces;
         p.heads_first = c.layout.head_stride > c.layout.token_stride;
-        p.parts = (c.block_size * p.row_pieces + kCopyThreads * kCopyPieces - 1) / (kCopyThreads * kCopyPieces);
-        const int64_t grid = std::min<int64_t>(152 * 4, c.pairs * p.caches * p.parts);
+        const int64_t row = c.head_dim * 2, page = row * c.kv_heads * c.block_size;
+        const bool whole = p.head == row && p.token == row * c.kv_heads;      // a page is one run
+        p.runs = whole ? 1 : c.kv_heads;
+        p.run_token = (int)(whole ? row * c.kv_heads : row);
+        const bool runs = (whole || p.token == row) && (int64_t)p.run_token * c.block_size >= kLeastRun &&
+                          page * c.pairs * p.caches >= kLeastBulk;
         void *args[] = {&p};
-        const cudaError_t e = launch_dependent((const void *)copy_pages_kernel, grid, kCopyThreads, 0, stream, args);
+        cudaError_t e;
+        if (runs) {
+            p.parts = (int)(((int64_t)p.run_token * c.block_size + kRunBytes - 1) / kRunBytes);
+            e = allow_shared((const void *)copy_runs_kernel, kRing * kRunBytes);
+            if (e == cudaSuccess)
+                e = launch_dependent((const void *)copy_runs_kernel,
+                                     std::min<int64_t>(152 * kBulkPerSm, c.pairs * p.caches * p.runs * p.parts), 32,
+                                     kRing * kRunBytes, stream, args);
+        } else {
+            p.parts = (c.block_size * p.row_pieces + kCopyThreads * kCopyPieces - 1) / (kCopyThreads * kCopyPieces);
+            e = launch_dependent((const void *)copy_pages_kernel, std::min<int64_t>(152 * 4, c.pairs * p.caches * p.parts),
+                                 kCopyThreads, 0, stream, args);
+        }
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -458,8 +591,16 @@ cudaError_t launch_pages(const PagesProblem &p, cudaStream_t stream)
     void *mark_args[] = {&prob, &status};
     e = launch_dependent((const void *)mark_kernel, grid, kPageThreads, 0, stream, mark_args);
     if (e != cudaSuccess) return e;
+    prob.prefix = reinterpret_cast<int *>(p.workspace + (words + 3) / 4 * 4);
+    const int64_t groups = (words + kListWords - 1) / kListWords;
+    prob.groups = words > kManyWords ? prob.prefix + words : nullptr;
     void *args[] = {&prob};
-    e = launch_dependent((const void *)list_kernel, (words + kPageThreads - 1) / kPageThreads, kPageThreads, 0, stream, args);
+    if (prob.groups) {
+        e = launch_dependent((const void *)count_kernel, std::min<int64_t>(304, (groups * 32 + kPageThreads - 1) / kPageThreads),
+                             kPageThreads, 0, stream, args);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_dependent((const void *)list_kernel, groups, kPageThreads, 0, stream, args);
     if (e != cudaSuccess || p.free_blocks) return e;
     return launch_dependent((const void *)move_kernel, grid, kPageThreads, 0, stream, args);
 }

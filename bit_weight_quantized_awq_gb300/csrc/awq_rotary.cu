@@ -4,13 +4,15 @@
 // Angles. cos and sin of position * frequency have to be right for positions in the
 // millions, where an fp32 product is off by whole degrees. The frequency is taken in
 // turns, F = frac(inv_freq / 2 pi) as a 64-bit fraction; position * F modulo 2^64 is
-// then the exact rest of a turn (the integer product wraps where whole turns fall away),
-// good to position * 2^-53 turns (the division by 2 pi, in fp64, once a CTA), and its upper 32
-// bits are the argument of sincospif.
+// then the rest of a turn (the integer product wraps where whole turns fall away), good to
+// position * 2^-63 turns, and its upper 32 bits are the argument of sincospif. 1 / 2 pi is
+// three fp32 numbers, whose products with inv_freq are exact as pairs: fp64 runs at two operations a
+// clock, which was a tenth of the time.
 //
-// Bound: HBM, every head read and written once. A CTA takes a few tokens; a token's
-// cosines and sines are computed once and shared by its heads through shared memory.
-// Each thread has the loads of kUnits pieces under way before it needs them.
+// Bound: HBM, every head read and written once. A CTA takes a few tokens and a part of their heads; the
+// cosines and sines are computed once for all of the CTA's heads, by all of its threads, and shared
+// through shared memory. Each thread asks for its first kItems pieces before that, so that their way in takes
+// no time of its own.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -24,7 +26,8 @@ namespace awq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnits = 4;          // units of a thread under way
+constexpr int kItems = 4;          // of a thread under way
+constexpr int kCtas = 3;           // of an SM
 
 struct Side {                      // of q, k and v; strides in bytes
     const char *src;
@@ -39,13 +42,15 @@ struct RotaryParams {
     const int64_t *slot_map;
     unsigned int *status;
     int64_t tokens, slots;
-    int num_axes, half, head_bytes;
-    int turned_heads, q_heads, v_heads;
-    int turn_units, head_units, copy_units;   // of a turned head: those that are turned, all; of a head of v
-    int token_units, per_cta, shift;
+    int num_axes, half, dim;
+    int q_heads, turned_heads, heads;   // heads: with v's
+    // A head is `lanes` items, of which `turns` turn something. A CTA takes per_cta tokens, `abreast` at once, and
+    // part_heads of their heads: one of `parts`.
+    int lanes, turns, abreast, per_cta, parts, part_heads;
+    int shift;
 };
 
-// kHalf: 8 elements and the 8 that lie rotary_dim / 2 further; kPairs: 4 neighbouring pairs; kSingle:
+// An item: kHalf: 8 elements and the 8 that lie rotary_dim / 2 further; kPairs: 4 neighbouring pairs; kSingle..:
 // one pair of either kind, for rotary_dim / 2 (or rotary_dim) that is no multiple of 8.
 enum Mode { kHalf, kPairs, kSingleHalf, kSinglePairs };
 
@@ -76,61 +81,19 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s)
     b = y * c + x * s;
 }
 
-// What unit `u` of a token is: a head of q, k or v and a place in it.
-struct Unit {
-    int side, head, at;      // at: bytes from the head's start
-    int turn;                // the first pair that it turns, -1 for a copy
-};
-
-template <int kMode>
-__device__ __forceinline__ Unit unit_of(const RotaryParams &p, int u)
+// frac(f / 2 pi) in units of 2^-64.
+__device__ __forceinline__ uint64_t in_turns(float f)
 {
-    Unit x;
-    const int turned = p.turned_heads * p.head_units;
-    if (u >= turned) {
-        u -= turned;
-        x.side = 2;
-        x.head = u / p.copy_units;
-        x.at = (u - x.head * p.copy_units) * 16;
-        x.turn = -1;
-        return x;
-    }
-    x.head = u / p.head_units;
-    const int j = u - x.head * p.head_units;
-    x.side = x.head >= p.q_heads;
-    if (x.side) x.head -= p.q_heads;
-    if (j < p.turn_units) {
-        x.turn = kMode == kHalf ? 8 * j : kMode == kPairs ? 4 * j : j;
-        x.at = kMode == kHalf ? 16 * j : kMode == kPairs ? 16 * j : kMode == kSingleHalf ? 2 * j : 4 * j;
-    } else {
-        constexpr int kBytes = kMode == kHalf || kMode == kPairs ? 16 : 2;
-        x.turn = -1;
-        x.at = 4 * p.half + (j - p.turn_units) * kBytes;
-    }
-    return x;
+    constexpr float k0 = 0.15915494f, k1 = 6.4206382e-09f, k2 = 7.342739e-17f;      // their sum is 1 / 2 pi to 2^-76
+    auto fixed = [](float x) { return (uint64_t)__float2ll_rn((x - rintf(x)) * 0x1p64f); };
+    const float a = f * k0, b = f * k1;
+    return fixed(a) + fixed(fmaf(f, k0, -a)) + fixed(b) + fixed(fmaf(f, k1, -b)) + fixed(f * k2);
 }
 
-template <typename T, int kMode>
-__global__ void __launch_bounds__(kThreads)
-rotary_kernel(const __grid_constant__ RotaryParams p)
+// Cosines and sines of a CTA's tokens and their slots, into shared memory.
+__device__ __forceinline__ void angles(const RotaryParams &p, int64_t t0, int tokens, float *cosine, float *sine, int64_t *slots)
 {
-    extern __shared__ __align__(16) char rotary_smem[];
-    const int tid = threadIdx.x;
-    // frequencies in turns, cosines and sines [per_cta][half], slots
-    uint64_t *turns = reinterpret_cast<uint64_t *>(rotary_smem);
-    int64_t *slots = reinterpret_cast<int64_t *>(turns + p.half);
-    float *cosine = reinterpret_cast<float *>(slots + p.per_cta + (p.per_cta + p.half) % 2);
-    float *sine = cosine + p.per_cta * p.half;
-    ptx::launch_dependents();
-    ptx::wait_prerequisites();
-
-    const int64_t t0 = (int64_t)blockIdx.x * p.per_cta;
-    const int tokens = (int)min((int64_t)p.per_cta, p.tokens - t0);
-    for (int i = tid; i < p.half; i += kThreads) {
-        const double f = (double)p.inv_freq[i] * 0.15915494309189533577;    // 1 / (2 pi)
-        turns[i] = (uint64_t)((f - floor(f)) * 18446744073709551616.);      // of 2^64
-    }
-    for (int i = tid; i < tokens; i += kThreads) {
+    for (int i = threadIdx.x; i < tokens; i += kThreads) {
         int64_t slot = p.slot_map ? p.slot_map[t0 + i] : 0;
         if (slot < 0 || slot >= p.slots) {
             if (slot != -1) raise_status(p.status, kStatusBadIndex);
@@ -138,92 +101,158 @@ rotary_kernel(const __grid_constant__ RotaryParams p)
         }
         slots[i] = slot;
     }
-    __syncthreads();
-    for (int e = tid; e < tokens * p.half; e += kThreads) {
-        const int t = e / p.half, i = e - t * p.half;
+    // a thread has one frequency and goes through the tokens
+    const int across = min(p.half, kThreads), rows = kThreads / across, row = threadIdx.x / across;
+    for (int i = threadIdx.x - row * across; i < p.half && row < rows; i += across) {
+        const uint64_t turns = in_turns(p.inv_freq[i]);
         const int axis = p.axes ? p.axes[i] : 0;
-        int position = 0;
-        if (axis >= 0 && axis < p.num_axes) position = p.positions[axis * p.tokens + t0 + t];
-        else raise_status(p.status, kStatusBadIndex);
-        const uint64_t rest = turns[i] * (uint64_t)(int64_t)position;
-        sincospif((float)(int32_t)(rest >> 32) * 0x1p-31f, &sine[e], &cosine[e]);
-    }
-    __syncthreads();
-
-    constexpr bool kVector = kMode == kHalf || kMode == kPairs;
-    const int units = tokens * p.token_units;
-    for (int e0 = tid; e0 < units; e0 += kThreads * kUnits) {
-        uint4 a[kUnits], b[kUnits];
-#pragma unroll
-        for (int n = 0; n < kUnits; ++n) {
-            const int e = e0 + n * kThreads;
-            if (e >= units) continue;
-            const int t = e / p.token_units;
-            const Unit x = unit_of<kMode>(p, e - t * p.token_units);
-            const Side &s = p.side[x.side];
-            const char *from = s.src + (t0 + t) * s.src_token + x.head * s.src_head + x.at;
-            if (kVector || x.side == 2) {
-                // not a read-only load: this kernel may be resident while the one before writes q, k and v
-                a[n] = *reinterpret_cast<const uint4 *>(from);
-                if (kMode == kHalf && x.turn >= 0) b[n] = *reinterpret_cast<const uint4 *>(from + 2 * p.half);
-            } else if (kMode == kSinglePairs && x.turn >= 0) {
-                a[n].x = *reinterpret_cast<const uint32_t *>(from);
-            } else {
-                a[n].x = *reinterpret_cast<const uint16_t *>(from);
-                if (x.turn >= 0) a[n].x |= (uint32_t)*reinterpret_cast<const uint16_t *>(from + 2 * p.half) << 16;
-            }
+        const bool known = axis >= 0 && axis < p.num_axes;
+        if (!known) raise_status(p.status, kStatusBadIndex);
+        const int32_t *positions = p.positions + (known ? axis : 0) * p.tokens + t0;
+        for (int t = row; t < tokens; t += rows) {
+            const uint64_t rest = known ? turns * (uint64_t)(int64_t)positions[t] : 0;
+            sincospif((float)(int32_t)(rest >> 32) * 0x1p-31f, &sine[t * p.half + i], &cosine[t * p.half + i]);
         }
+    }
+}
+
+// Vectors of 16 bytes. A thread has one place in one head, of which all is looked up once, and goes through
+// the CTA's tokens, kItems of them under way.
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kThreads, kCtas)
+rotary_kernel(const __grid_constant__ RotaryParams p)
+{
+    constexpr int kEach = kMode == kHalf ? 8 : 4;       // angles of an item
+    extern __shared__ __align__(16) char rotary_smem[];
+    float *cosine = reinterpret_cast<float *>(rotary_smem), *sine = cosine + p.per_cta * p.half;     // [per_cta][half]
+    int64_t *slots = reinterpret_cast<int64_t *>(sine + p.per_cta * p.half);
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+
+    const int64_t group = blockIdx.x / p.parts, t0 = group * p.per_cta;
+    const int tokens = (int)min((int64_t)p.per_cta, p.tokens - t0);
+    const int own = threadIdx.x / p.lanes, lane = threadIdx.x - own * p.lanes;
+    const int beside = own / p.part_heads;              // which of the tokens abreast
+    const int h = (int)(blockIdx.x - group * p.parts) * p.part_heads + own - beside * p.part_heads;
+    const bool works = beside < p.abreast && h < p.heads;
+    const bool v = h >= p.turned_heads, turns = !v && lane < p.turns;
+    const int side = v ? 2 : h >= p.q_heads, number = h - (v ? p.turned_heads : h >= p.q_heads ? p.q_heads : 0);
+    // the item's first 16 bytes in the head, and how far the second are; 0: none
+    int at = 16 * lane, more = 0;
+    if (kMode == kHalf) {
+        if (turns) {
+            more = 2 * p.half;
+        } else if (v) {
+            more = at + 16 * p.lanes < 2 * p.dim ? 16 * p.lanes : 0;
+        } else {
+            at = 4 * p.half + 32 * (lane - p.turns);
+            more = at + 16 < 2 * p.dim ? 16 : 0;
+        }
+    }
+    const int64_t src_token = p.side[side].src_token, dst_token = p.side[side].dst_token, dst_block = p.side[side].dst_block;
+    const char *src = p.side[side].src + t0 * src_token + number * p.side[side].src_head + at;
+    char *dst = p.side[side].dst + (dst_block ? 0 : t0 * dst_token) + number * p.side[side].dst_head + at;
+
+    uint4 a[kItems], b[kItems];
+    const int step = p.abreast * kItems, end = works ? tokens : 0;
+    auto load = [&](int t1) {
 #pragma unroll
-        for (int n = 0; n < kUnits; ++n) {
-            const int e = e0 + n * kThreads;
-            if (e >= units) continue;
-            const int t = e / p.token_units;
-            const Unit x = unit_of<kMode>(p, e - t * p.token_units);
-            const Side &s = p.side[x.side];
-            char *to = s.dst;
-            if (s.dst_block) {
+        for (int u = 0; u < kItems; ++u) {
+            const int t = t1 + u * p.abreast;
+            if (t >= end) continue;
+            // not a read-only load: this kernel may be resident while the one before writes q, k and v
+            const char *from = src + t * src_token;
+            a[u] = *reinterpret_cast<const uint4 *>(from);
+            if (kMode == kHalf && more) b[u] = *reinterpret_cast<const uint4 *>(from + more);
+        }
+    };
+    load(beside);
+    angles(p, t0, tokens, cosine, sine, slots);
+    __syncthreads();
+    for (int t1 = beside; t1 < end; t1 += step) {
+        if (t1 != beside) load(t1);
+#pragma unroll
+        for (int u = 0; u < kItems; ++u) {
+            const int t = t1 + u * p.abreast;
+            if (t >= end) continue;
+            char *to = dst;
+            if (dst_block) {
                 const int64_t slot = slots[t];
                 if (slot < 0) continue;
-                to += (slot >> p.shift) * s.dst_block + (slot & ((1 << p.shift) - 1)) * s.dst_token;
+                to += (slot >> p.shift) * dst_block + (slot & ((1 << p.shift) - 1)) * dst_token;
             } else {
-                to += (t0 + t) * s.dst_token;
+                to += t * dst_token;
             }
-            to += x.head * s.dst_head + x.at;
-            const float *c = cosine + t * p.half + x.turn, *d = sine + t * p.half + x.turn;
-            if (kMode == kHalf && x.turn >= 0) {
-                uint32_t *va = &a[n].x, *vb = &b[n].x;
+            if (turns) {
+                uint32_t *va = &a[u].x, *vb = &b[u].x;
+                const float4 *c = reinterpret_cast<const float4 *>(cosine + t * p.half + kEach * lane);
+                const float4 *d = reinterpret_cast<const float4 *>(sine + t * p.half + kEach * lane);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 cc = reinterpret_cast<const float2 *>(c)[i], dd = reinterpret_cast<const float2 *>(d)[i];
-                    float2 u = unpack<T>(va[i]), w = unpack<T>(vb[i]);
-                    turn(u.x, w.x, cc.x, dd.x);
-                    turn(u.y, w.y, cc.y, dd.y);
-                    va[i] = pack<T>(u.x, u.y);
-                    vb[i] = pack<T>(w.x, w.y);
+                for (int q = 0; q < 4; ++q) {
+                    float2 x = unpack<T>(va[q]);
+                    if (kMode == kHalf) {
+                        const float4 cc = c[q / 2], dd = d[q / 2];
+                        float2 y = unpack<T>(vb[q]);
+                        turn(x.x, y.x, q % 2 ? cc.z : cc.x, q % 2 ? dd.z : dd.x);
+                        turn(x.y, y.y, q % 2 ? cc.w : cc.y, q % 2 ? dd.w : dd.y);
+                        vb[q] = pack<T>(y.x, y.y);
+                    } else {
+                        const float4 cc = *c, dd = *d;
+                        turn(x.x, x.y, q == 0 ? cc.x : q == 1 ? cc.y : q == 2 ? cc.z : cc.w,
+                             q == 0 ? dd.x : q == 1 ? dd.y : q == 2 ? dd.z : dd.w);
+                    }
+                    va[q] = pack<T>(x.x, x.y);
                 }
-                *reinterpret_cast<uint4 *>(to + 2 * p.half) = b[n];
-            } else if (kMode == kPairs && x.turn >= 0) {
-                uint32_t *va = &a[n].x;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float2 u = unpack<T>(va[i]);
-                    turn(u.x, u.y, c[i], d[i]);
-                    va[i] = pack<T>(u.x, u.y);
-                }
-            } else if (!kVector && x.turn >= 0) {
-                float2 u = unpack<T>(a[n].x);
-                turn(u.x, u.y, c[0], d[0]);
-                a[n].x = pack<T>(u.x, u.y);
             }
-            if (kVector || x.side == 2) {
-                *reinterpret_cast<uint4 *>(to) = a[n];
-            } else if (kMode == kSinglePairs && x.turn >= 0) {
-                *reinterpret_cast<uint32_t *>(to) = a[n].x;
-            } else {
-                *reinterpret_cast<uint16_t *>(to) = (uint16_t)a[n].x;
-                if (x.turn >= 0) *reinterpret_cast<uint16_t *>(to + 2 * p.half) = (uint16_t)(a[n].x >> 16);
-            }
+            *reinterpret_cast<uint4 *>(to) = a[u];
+            if (kMode == kHalf && more) *reinterpret_cast<uint4 *>(to + more) = b[u];
         }
+    }
+}
+
+// Single pairs and elements.
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kThreads)
+rotary_single_kernel(const __grid_constant__ RotaryParams p)
+{
+    extern __shared__ __align__(16) char rotary_smem[];
+    float *cosine = reinterpret_cast<float *>(rotary_smem), *sine = cosine + p.per_cta * p.half;     // [per_cta][half]
+    int64_t *slots = reinterpret_cast<int64_t *>(sine + p.per_cta * p.half);
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+
+    const int64_t group = blockIdx.x / p.parts, t0 = group * p.per_cta;
+    const int first = (int)(blockIdx.x - group * p.parts) * p.part_heads, heads = min(p.part_heads, p.heads - first);
+    const int tokens = (int)min((int64_t)p.per_cta, p.tokens - t0);
+    angles(p, t0, tokens, cosine, sine, slots);
+    __syncthreads();
+    for (int e = threadIdx.x; e < tokens * heads * p.lanes; e += kThreads) {
+        const int i = e / p.lanes, lane = e - i * p.lanes;
+        const int t = i / heads, h = first + i - t * heads;
+        const bool v = h >= p.turned_heads;
+        const Side &s = p.side[v ? 2 : h >= p.q_heads];
+        const int head = h - (v ? p.turned_heads : h >= p.q_heads ? p.q_heads : 0);
+        const uint16_t *from = reinterpret_cast<const uint16_t *>(s.src + (t0 + t) * s.src_token + head * s.src_head);
+        char *to = s.dst + head * s.dst_head;
+        if (s.dst_block) {
+            const int64_t slot = slots[t];
+            if (slot < 0) continue;
+            to += (slot >> p.shift) * s.dst_block + (slot & ((1 << p.shift) - 1)) * s.dst_token;
+        } else {
+            to += (t0 + t) * s.dst_token;
+        }
+        uint16_t *out = reinterpret_cast<uint16_t *>(to);
+        if (v || lane >= p.turns) {
+            // of v, which has more elements than another head has items, two each
+            for (int k = v ? lane : p.half + lane; k < p.dim; k += v ? p.lanes : p.dim) out[k] = from[k];
+            continue;
+        }
+        const int at = kMode == kSingleHalf ? lane : 2 * lane, other = kMode == kSingleHalf ? at + p.half : at + 1;
+        float2 x = unpack<T>(from[at] | (uint32_t)from[other] << 16);
+        turn(x.x, x.y, cosine[t * p.half + lane], sine[t * p.half + lane]);
+        const uint32_t y = pack<T>(x.x, x.y);
+        out[at] = (uint16_t)y;
+        out[other] = (uint16_t)(y >> 16);
     }
 }
 
@@ -233,8 +262,8 @@ const void *kernel_of(int mode)
     switch (mode) {
     case kHalf: return (const void *)rotary_kernel<T, kHalf>;
     case kPairs: return (const void *)rotary_kernel<T, kPairs>;
-    case kSingleHalf: return (const void *)rotary_kernel<T, kSingleHalf>;
-    default: return (const void *)rotary_kernel<T, kSinglePairs>;
+    case kSingleHalf: return (const void *)rotary_single_kernel<T, kSingleHalf>;
+    default: return (const void *)rotary_single_kernel<T, kSinglePairs>;
     }
 }
 
@@ -266,32 +295,36 @@ cudaError_t launch_rotary(const awq_rotary_t &a, cudaStream_t stream)
     while (append && (1 << p.shift) < a.block_size) ++p.shift;
     p.num_axes = (int)a.num_axes;
     p.half = (int)a.rotary_dim / 2;
-    p.head_bytes = (int)a.head_dim * 2;
+    p.dim = (int)a.head_dim;
     p.q_heads = (int)a.q_heads;
     p.turned_heads = (int)(a.q_heads + a.kv_heads);
-    p.v_heads = append ? (int)a.kv_heads : 0;
+    p.heads = p.turned_heads + (append ? (int)a.kv_heads : 0);
     const int R = (int)a.rotary_dim, D = (int)a.head_dim;
     int mode;
     if (a.pairs ? R % 8 == 0 : R % 16 == 0) {
         mode = a.pairs ? kPairs : kHalf;
-        p.turn_units = a.pairs ? R / 8 : R / 16;
-        p.head_units = p.turn_units + (D - R) / 8;
+        p.turns = a.pairs ? R / 8 : R / 16;
+        p.lanes = a.pairs ? D / 8 : p.turns + ((D - R) / 8 + 1) / 2;
     } else {
         mode = a.pairs ? kSinglePairs : kSingleHalf;
-        p.turn_units = R / 2;
-        p.head_units = p.turn_units + (D - R);
+        p.turns = R / 2;
+        p.lanes = p.turns + (D - R);
     }
-    p.copy_units = D / 8;
-    p.token_units = p.turned_heads * p.head_units + p.v_heads * p.copy_units;
-    // as many tokens as the CTA's threads have units for at once, but four CTAs an SM before one has several
-    p.per_cta = std::max(1, kThreads * kUnits / p.token_units);
-    p.per_cta = (int)std::min<int64_t>(p.per_cta, (a.tokens + 607) / 608);
-    // and no more than the cosines' share of shared memory
-    p.per_cta = std::max(1, std::min(p.per_cta, 4096 / p.half));
-    const size_t smem = 8 * ((size_t)p.half + p.per_cta + 1) + 8 * (size_t)p.per_cta * p.half;
+    // the heads are shared out over CTAs, an item a thread, and few heads let several tokens go abreast
+    const int at_once = std::max(1, kThreads / p.lanes);
+    p.parts = (p.heads + at_once - 1) / at_once;
+    p.part_heads = (p.heads + p.parts - 1) / p.parts;
+    p.abreast = at_once / p.part_heads;
+    // as many tokens for a CTA as keep all its threads at their angles and all its loads under way, but
+    // not before there are kCtas CTAs an SM
+    const int busy = std::max((kThreads + p.half - 1) / p.half, p.abreast * kItems);
+    p.per_cta = (int)std::max<int64_t>(
+        1, std::min<int64_t>({busy, (a.tokens * p.parts + kCtas * 152 - 1) / (kCtas * 152), 4096 / p.half}));
+    const int64_t grid = (a.tokens + p.per_cta - 1) / p.per_cta * p.parts;
+    const size_t smem = 8 * (size_t)p.per_cta * (p.half + 1);
     void *args[] = {&p};
     const void *kernel = a.dtype == AWQ_F16 ? kernel_of<__half>(mode) : kernel_of<__nv_bfloat16>(mode);
-    return launch_dependent(kernel, (a.tokens + p.per_cta - 1) / p.per_cta, kThreads, smem, stream, args);
+    return launch_dependent(kernel, grid, kThreads, smem, stream, args);
 }
 
 } // namespace awq

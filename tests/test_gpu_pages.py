@@ -155,6 +155,44 @@ def test_blocks_behind_the_first_four_gigabytes():
     assert (cache[39997, :63] == 3).all() and (cache[39997, 63] == 0).all() and (cache[39998] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["plain", "heads_first", "together"])
+@pytest.mark.parametrize("page,heads,dim", [(64, 8, 128), (32, 3, 136), (1024, 1, 64), (16, 40, 80)])
+def test_many_bytes_go_in_bulk(kind, page, heads, dim):
+    """Long runs, many pages: parts of pages, none of them, and counts that say less than the lists."""
+    blocks = 2 * (1 + 4_000_000 // (page * heads * dim)) + 5
+    rng = np.random.default_rng(page)
+    caches = caches_of(kind, 5, blocks, page, heads, dim, BF16)
+    perm = rng.permutation(blocks)
+    n = (blocks - 5) // 2
+    src, dst, tokens = perm[:n].copy(), perm[n:2 * n].copy(), rng.integers(0, page + 1, n)
+    tokens[:3] = 0, page, 1
+    src[n // 2], dst[n // 3] = -1, -1
+    dst[n // 4] = src[n // 4]
+    for given, count in ((None, None), (tokens, n - 2), (tokens, 0)):
+        want = [c.clone() for c in caches]
+        awq.copy_pages(caches, i32(src), i32(dst), tokens=None if given is None else i32(given),
+                       count=None if count is None else i32([count]))
+        good = (src >= 0) & (dst >= 0) & (np.arange(n) < (n if count is None else count))
+        t = np.full(n, page) if given is None else given
+        kept = torch.from_numpy(np.arange(page) < t[good][:, None]).cuda()[:, :, None, None]
+        s, d = torch.from_numpy(src[good]).cuda(), torch.from_numpy(dst[good]).cuda()
+        for w in want:
+            w[d] = torch.where(kept, w[s], w[d])
+        for c, w in zip(caches, want):
+            assert torch.equal(c, w)
+    bad = src.copy()
+    bad[0], bad[1] = blocks, -7
+    want = [c.clone() for c in caches]
+    long = tokens.copy()
+    long[2] = page + 1
+    awq.copy_pages(caches, i32(bad[:3]).repeat(n), i32(dst[:3]).repeat(n), tokens=i32(long[:3]).repeat(n), count=i32([3]))
+    assert awq.awq_last_device_status(None) == Status.ERR_INVALID_ARG
+    for c, w in zip(caches, want):
+        if dst[2] >= 0 and bad[2] >= 0:
+            w[int(dst[2])] = w[int(bad[2])]
+        assert torch.equal(c, w)
+
+
 def test_bad_pairs_are_skipped_and_reported():
     cache = torch.randn((4, 16, 1, 8), device="cuda").half()
     before = cache.clone()
