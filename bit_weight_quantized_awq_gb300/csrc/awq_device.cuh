@@ -225,6 +225,13 @@ __device__ __forceinline__ float cluster_load(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ uint32_t cluster_load_u32(uint32_t addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ float2 cluster_load2(uint32_t addr)
 {
     float2 v;

@@ -204,20 +204,22 @@ cudaError_t launch_pages(const PagesProblem &p, cudaStream_t stream);
 cudaError_t allow_shared(const void *kernel, size_t bytes);
 
 // A launch whose grid may be scheduled before the kernel ahead of it in the stream has
-// ended; the kernel waits for it by itself (ptx::wait_prerequisites).
+// ended; the kernel waits for it by itself (ptx::wait_prerequisites). cluster: CTAs of a cluster.
 inline cudaError_t launch_dependent(const void *kernel, int64_t grid, int block, size_t smem, cudaStream_t stream,
-                                    void **args)
+                                    void **args, int cluster = 1)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelExC(&cfg, kernel, args);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -1,6 +1,7 @@
 // awq_pages.cu -- the pages of a paged cache between steps: fork_kernel (block tables of
 // the beams that go on), copy_pages_kernel (pages within caches), and the kernels that
-// list the free blocks and compact the used ones (mark_kernel, count_kernel, list_kernel, move_kernel).
+// list the free blocks and compact the used ones (pages_cluster_kernel, or mark_kernel,
+// count_kernel, list_kernel and move_kernel for large caches).
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -320,10 +321,10 @@ copy_runs_kernel(const __grid_constant__ CopyParams p)
 // numbered by the bits before them.
 
 constexpr int kPageThreads = 512;
-constexpr int kListWords = 64;            // of the bitmap, for a CTA
-constexpr int kManyWords = 8192;          // from here on counted in groups first
+constexpr int kListWords = 256;           // of the bitmap, for a CTA
 
 // Sum of v over the threads before this one, and over all.
+template <int kThreads = kPageThreads>
 __device__ __forceinline__ int block_scan(int v, int *sums, int &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -338,7 +339,7 @@ __device__ __forceinline__ int block_scan(int v, int *sums, int &total)
     __syncthreads();
     int before = 0;
     total = 0;
-    for (int w = 0; w < kPageThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += sums[w];
         total += sums[w];
     }
@@ -354,25 +355,19 @@ clear_kernel(uint4 *words, int64_t n)
         words[i] = make_uint4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ void mark(const PagesProblem &p, int block, unsigned &bad)
+// Calls f for every entry of the tables' pages and of `held` that is a block, shared out over `threads`
+// threads of which this is number `thread`, whole warps; reports those that are none.
+template <typename F>
+__device__ __forceinline__ void each_used(const PagesProblem &p, int64_t thread, int64_t threads, unsigned &bad, F f)
 {
-    if (block < 0 || block >= p.num_blocks) bad |= kStatusBadIndex;
-    else atomicOr(&p.workspace[block >> 5], 1u << (block & 31));
-}
-
-__global__ void __launch_bounds__(kPageThreads)
-mark_kernel(const __grid_constant__ PagesProblem p, unsigned int *status)
-{
-    ptx::launch_dependents();
-    ptx::wait_prerequisites();
-    const int shift = __ffs(p.block_size) - 1;
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * kPageThreads / 32;
-    const int64_t warp = ((int64_t)blockIdx.x * kPageThreads + threadIdx.x) / 32;
-    unsigned bad = 0;
+    const int shift = __ffs(p.block_size) - 1, lane = threadIdx.x & 31;
+    auto check = [&](int block) {
+        if (block < 0 || block >= p.num_blocks) bad |= kStatusBadIndex;
+        else f(block);
+    };
     // a warp a piece of 256 entries of a row
     const int parts = (p.width + 255) / 256;
-    for (int64_t u = warp; u < (int64_t)p.rows * parts; u += warps) {
+    for (int64_t u = thread / 32; u < (int64_t)p.rows * parts; u += threads / 32) {
         const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
         const int have = pages_of(p.lens[r], p.block_size, shift, p.width, bad);
         int v[8];
@@ -383,15 +378,59 @@ mark_kernel(const __grid_constant__ PagesProblem p, unsigned int *status)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (j0 + i * 32 + lane < have) mark(p, v[i], bad);
+            if (j0 + i * 32 + lane < have) check(v[i]);
     }
-    for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < p.num_held;
-         i += (int64_t)gridDim.x * kPageThreads)
-        if (p.held[i] != -1) mark(p, p.held[i], bad);
+    for (int64_t i = thread; i < p.num_held; i += threads)
+        if (p.held[i] != -1) check(p.held[i]);
+}
+
+// The tables with the new numbers that `moved` gives for blocks from `first` on.
+template <typename F>
+__device__ __forceinline__ void renumber(const PagesProblem &p, int64_t thread, int64_t threads, int first, F moved)
+{
+    const int shift = __ffs(p.block_size) - 1, lane = threadIdx.x & 31;
+    const int parts = (p.width + 255) / 256;
+    for (int64_t u = thread / 32; u < (int64_t)p.rows * parts; u += threads / 32) {
+        const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
+        unsigned ignored = 0;
+        const int have = pages_of(p.lens[r], p.block_size, shift, p.width, ignored);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = j0 + i * 32 + lane;
+            if (j >= p.width) continue;
+            int b = j < have ? p.table[r * p.stride + j] : -1;
+            if (b >= p.num_blocks || b < 0) b = -1;
+            p.new_table[r * p.new_stride + j] = b >= first ? moved(b) : b;
+        }
+    }
+}
+
+// What block b's entry in the lists is: `rank` used blocks lie before it, `used` there are, of which the first
+// `stays` below `used` stay; of the others each takes the free block of its own rank there.
+__device__ __forceinline__ void list_block(const PagesProblem &p, int b, bool in_use, int rank, int used, int stays)
+{
+    if (p.free_blocks) {
+        p.free_blocks[in_use ? p.num_blocks - 1 - rank : b - rank] = in_use ? -1 : b;
+        return;
+    }
+    if (!in_use && b < used) p.dst[b - rank] = b;
+    if (in_use && b >= used) p.src[rank - stays] = b;
+    if (!in_use || b < used) p.block_map[b] = in_use ? b : -1;
+    if (b < p.num_blocks / 2 && b >= used - stays) p.src[b] = p.dst[b] = -1;
+}
+
+__global__ void __launch_bounds__(kPageThreads)
+mark_kernel(const __grid_constant__ PagesProblem p, unsigned int *status)
+{
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    unsigned bad = 0;
+    each_used(p, (int64_t)blockIdx.x * kPageThreads + threadIdx.x, (int64_t)gridDim.x * kPageThreads, bad,
+              [&](int b) { atomicOr(&p.workspace[b >> 5], 1u << (b & 31)); });
     if (bad) raise_status(status, bad);
 }
 
-// How many blocks of each kListWords words are used, for the lists of large caches.
+// How many blocks of each kListWords words are used.
 __global__ void __launch_bounds__(kPageThreads)
 count_kernel(const __grid_constant__ PagesProblem p)
 {
@@ -401,6 +440,7 @@ count_kernel(const __grid_constant__ PagesProblem p)
     const int groups = (words + kListWords - 1) / kListWords;
     for (int g = (blockIdx.x * kPageThreads + threadIdx.x) / 32; g < groups; g += gridDim.x * kPageThreads / 32) {
         int n = 0;
+#pragma unroll
         for (int i = lane; i < kListWords; i += 32)
             if (g * kListWords + i < words) n += __popc(p.workspace[g * kListWords + i]);
         n = __reduce_add_sync(0xFFFFFFFFu, n);
@@ -409,7 +449,7 @@ count_kernel(const __grid_constant__ PagesProblem p)
 }
 
 // A CTA numbers the blocks of kListWords words, a lane a block. It adds up the counts before them, and
-// all of them, by itself: of the words, or of count_kernel's groups where there are many.
+// all of them, by itself.
 __global__ void __launch_bounds__(kPageThreads)
 list_kernel(const __grid_constant__ PagesProblem p)
 {
@@ -417,32 +457,27 @@ list_kernel(const __grid_constant__ PagesProblem p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ptx::launch_dependents();
     ptx::wait_prerequisites();
-    const int words = (p.num_blocks + 31) / 32, w0 = blockIdx.x * kListWords;
-    // counts of `each` words
-    const int each = p.groups ? kListWords : 1, counts = (words + each - 1) / each;
-    auto count = [&](int i) { return p.groups ? p.groups[i] : __popc(p.workspace[i]); };
+    const int words = (p.num_blocks + 31) / 32, w0 = blockIdx.x * kListWords, w = w0 + tid;
+    const int counts = (words + kListWords - 1) / kListWords;
     int before = 0, all = 0, ignored;
-#pragma unroll 4
     for (int i = tid; i < counts; i += kPageThreads) {
-        const int n = count(i);
+        const int n = p.groups[i];
         all += n;
-        if (i * each < w0) before += n;
+        if (i < blockIdx.x) before += n;
     }
+    const uint32_t word = tid < kListWords && w < words ? p.workspace[w] : 0;
     int used, used_before;
     block_scan(all, sums, used);
     block_scan(before, sums, used_before);
-    const int w = w0 + tid;
-    const int mine = tid < kListWords && w < words ? __popc(p.workspace[w]) : 0;
-    const int at = used_before + block_scan(mine, sums, ignored);
+    const int at = used_before + block_scan(__popc(word), sums, ignored);
     if (tid < kListWords) before_word[tid] = at;
     int stays = 0;
     if (!p.free_blocks) {
-        // used blocks below `used` stay; of the others each takes the free block of its own rank there
         int stay = 0;
         for (int i = tid; i < counts; i += kPageThreads)
-            if ((i + 1) * each * 32ll <= used) stay += count(i);
-        const int rest = used / 32 / each * each + tid;      // words of the count that `used` falls into
-        if (tid < each && rest * 32 < used) {
+            if ((i + 1) * (32ll * kListWords) <= used) stay += p.groups[i];
+        const int rest = used / (32 * kListWords) * kListWords + tid;      // words of the count that `used` falls into
+        if (tid < kListWords && rest * 32 < used) {
             const int left = used - rest * 32;
             stay += __popc(left >= 32 ? p.workspace[rest] : p.workspace[rest] & ((1u << left) - 1));
         }
@@ -458,21 +493,12 @@ list_kernel(const __grid_constant__ PagesProblem p)
             *p.moves = used - stays;
         }
     }
-    const int half = p.num_blocks / 2;
-    for (int i = warp; i < kListWords && w0 + i < words; i += kPageThreads / 32) {
+#pragma unroll 4
+    for (int i = warp; i < kListWords; i += kPageThreads / 32) {
         const int b = (w0 + i) * 32 + lane;
-        if (b >= p.num_blocks) continue;
-        const uint32_t word = p.workspace[w0 + i];
-        const int rank = before_word[i] + __popc(word & ((1u << lane) - 1));      // used blocks before b
-        const bool in_use = word >> lane & 1;
-        if (p.free_blocks) {
-            p.free_blocks[in_use ? p.num_blocks - 1 - rank : b - rank] = in_use ? -1 : b;
-            continue;
-        }
-        if (!in_use && b < used) p.dst[b - rank] = b;
-        if (in_use && b >= used) p.src[rank - stays] = b;
-        if (!in_use || b < used) p.block_map[b] = in_use ? b : -1;
-        if (b < half && b >= used - stays) p.src[b] = p.dst[b] = -1;
+        if (w0 + i >= words || b >= p.num_blocks) continue;
+        const uint32_t bits = p.workspace[w0 + i];
+        list_block(p, b, bits >> lane & 1, before_word[i] + __popc(bits & ((1u << lane) - 1)), used, stays);
     }
 }
 
@@ -482,34 +508,90 @@ move_kernel(const __grid_constant__ PagesProblem p)
 {
     ptx::launch_dependents();
     ptx::wait_prerequisites();
-    const int shift = __ffs(p.block_size) - 1;
     const int moves = *p.moves;
     const int64_t thread = (int64_t)blockIdx.x * kPageThreads + threadIdx.x, threads = (int64_t)gridDim.x * kPageThreads;
     for (int64_t i = thread; i < moves; i += threads) p.block_map[p.src[i]] = p.dst[i];
-    // the first block that moves tells where the moving ones begin
-    const int first = moves > 0 ? p.src[0] : p.num_blocks;
-    const int skipped = moves > 0 ? p.prefix[first >> 5] +
-                                        __popc(p.workspace[first >> 5] & ((1u << (first & 31)) - 1)) : 0;
-    const int lane = threadIdx.x & 31;
-    const int parts = (p.width + 255) / 256;
-    for (int64_t u = thread / 32; u < (int64_t)p.rows * parts; u += threads / 32) {
-        const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
-        unsigned ignored = 0;
-        const int have = pages_of(p.lens[r], p.block_size, shift, p.width, ignored);
+    auto before = [&](int b) { return p.prefix[b >> 5] + __popc(p.workspace[b >> 5] & ((1u << (b & 31)) - 1)); };
+    // the first block that moves tells how many stay
+    const int first = moves > 0 ? p.src[0] : p.num_blocks, stays = moves > 0 ? before(first) : 0;
+    renumber(p, thread, threads, first, [&](int b) { return p.dst[before(b) - stays]; });
+}
+
+// All of it in one launch of one cluster, for caches of up to kClusterWords words and small tables. Each CTA marks
+// its share of the entries in a bitmap of its own, then owns an eighth of the words: joins them from all
+// CTAs' bitmaps, counts and lists them. (256 rows of up to 256 pages: 5 us, and 9 in three launches.)
+constexpr int kCluster = 8, kClusterThreads = 1024;
+constexpr int kClusterWords = kCluster * kClusterThreads;       // a word a thread
+constexpr int64_t kClusterEntries = 1 << 18;
+
+__global__ void __launch_bounds__(kClusterThreads)
+pages_cluster_kernel(const __grid_constant__ PagesProblem p, unsigned int *status)
+{
+    extern __shared__ uint32_t bitmap[];            // [words]
+    __shared__ uint32_t own[kClusterThreads];       // the CTA's words, and the used blocks before them
+    __shared__ int prefix[kClusterThreads], sums[kClusterThreads / 32], total;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = ptx::cluster_rank();
+    const int words = (p.num_blocks + 31) / 32, each = (words + kCluster - 1) / kCluster;
+    const int thread = rank * kClusterThreads + tid, threads = kCluster * kClusterThreads;
+    for (int i = tid; i < words; i += kClusterThreads) bitmap[i] = 0;
+    __syncthreads();
+    ptx::launch_dependents();
+    ptx::wait_prerequisites();
+    unsigned bad = 0;
+    each_used(p, thread, threads, bad, [&](int b) { atomicOr(&bitmap[b >> 5], 1u << (b & 31)); });
+    if (bad) raise_status(status, bad);
+    ptx::cluster_sync();
+    const int w = rank * each + tid;
+    uint32_t word = 0;
+    if (tid < each && w < words) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = j0 + i * 32 + lane;
-            if (j >= p.width) continue;
-            int b = j < have ? p.table[r * p.stride + j] : -1;
-            if (b >= p.num_blocks || b < 0) b = -1;
-            if (b >= first) {
-                const int rank = p.prefix[b >> 5] +
-                                 __popc(p.workspace[b >> 5] & ((1u << (b & 31)) - 1)) - skipped;
-                b = p.dst[rank];
-            }
-            p.new_table[r * p.new_stride + j] = b;
+        for (int c = 0; c < kCluster; ++c) word |= ptx::cluster_load_u32(ptx::cluster_addr(ptx::smem_addr(bitmap + w), c));
+    }
+    own[tid] = word;
+    int mine;
+    int before = block_scan<kClusterThreads>(__popc(word), sums, mine);
+    if (tid == 0) total = mine;
+    ptx::cluster_sync();
+    int used = 0;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+        const int n = (int)ptx::cluster_load_u32(ptx::cluster_addr(ptx::smem_addr(&total), c));
+        used += n;
+        if (c < rank) before += n;
+    }
+    prefix[tid] = before;
+    int stays = used;
+    // used blocks before block b, from the CTA that owns its word
+    auto used_before = [&](int b) {
+        const int at = b >> 5, c = at / each, i = at - c * each;
+        return (int)ptx::cluster_load_u32(ptx::cluster_addr(ptx::smem_addr(prefix + i), c)) +
+               __popc(ptx::cluster_load_u32(ptx::cluster_addr(ptx::smem_addr(own + i), c)) & ((1u << (b & 31)) - 1));
+    };
+    if (p.free_blocks) {
+        __syncthreads();
+    } else {
+        ptx::cluster_sync();
+        if (used < words * 32) stays = used_before(used);
+    }
+    if (thread == 0) {
+        if (p.free_blocks) {
+            p.counts[0] = p.num_blocks - used;
+            p.counts[1] = used;
+        } else {
+            *p.moves = used - stays;
         }
     }
+    for (int i = warp; i < each; i += kClusterThreads / 32) {
+        const int b = (rank * each + i) * 32 + lane;
+        if (b >= p.num_blocks) continue;
+        list_block(p, b, own[i] >> lane & 1, prefix[i] + __popc(own[i] & ((1u << lane) - 1)), used, stays);
+    }
+    if (!p.free_blocks) {
+        ptx::cluster_sync();           // the lists are there for all
+        for (int i = thread; i < used - stays; i += threads) p.block_map[p.src[i]] = p.dst[i];
+        renumber(p, thread, threads, used, [&](int b) { return p.dst[used_before(b) - stays]; });
+    }
+    ptx::cluster_sync();               // none ends while others read its words
 }
 
 } // namespace
@@ -577,6 +659,13 @@ cudaError_t launch_pages(const PagesProblem &p, cudaStream_t stream)
     PagesProblem prob = p;
     unsigned int *status = device_status_word();
     const int64_t words = (p.num_blocks + 31) / 32;
+    void *mark_args[] = {&prob, &status};
+    if (words <= kClusterWords && (int64_t)p.rows * p.width + p.num_held <= kClusterEntries) {
+        const cudaError_t e = allow_shared((const void *)pages_cluster_kernel, kClusterWords * sizeof(uint32_t));
+        if (e != cudaSuccess) return e;
+        return launch_dependent((const void *)pages_cluster_kernel, kCluster, kClusterThreads, words * sizeof(uint32_t), stream,
+                                mark_args, kCluster);
+    }
     uint4 *clear = reinterpret_cast<uint4 *>(p.workspace);
     int64_t n = (words + 3) / 4;
     void *clear_args[] = {&clear, &n};
@@ -588,19 +677,15 @@ cudaError_t launch_pages(const PagesProblem &p, cudaStream_t stream)
     const int64_t grid = std::max<int64_t>(
         1, std::min<int64_t>(608, std::max((pieces * 32 + kPageThreads - 1) / kPageThreads,
                                            (p.num_held + kPageThreads - 1) / kPageThreads)));
-    void *mark_args[] = {&prob, &status};
     e = launch_dependent((const void *)mark_kernel, grid, kPageThreads, 0, stream, mark_args);
     if (e != cudaSuccess) return e;
     prob.prefix = reinterpret_cast<int *>(p.workspace + (words + 3) / 4 * 4);
+    prob.groups = prob.prefix + words;
     const int64_t groups = (words + kListWords - 1) / kListWords;
-    prob.groups = words > kManyWords ? prob.prefix + words : nullptr;
     void *args[] = {&prob};
-    if (prob.groups) {
-        e = launch_dependent((const void *)count_kernel, std::min<int64_t>(304, (groups * 32 + kPageThreads - 1) / kPageThreads),
-                             kPageThreads, 0, stream, args);
-        if (e != cudaSuccess) return e;
-    }
-    e = launch_dependent((const void *)list_kernel, groups, kPageThreads, 0, stream, args);
+    e = launch_dependent((const void *)count_kernel, std::min<int64_t>(304, (groups * 32 + kPageThreads - 1) / kPageThreads),
+                         kPageThreads, 0, stream, args);
+    if (e == cudaSuccess) e = launch_dependent((const void *)list_kernel, groups, kPageThreads, 0, stream, args);
     if (e != cudaSuccess || p.free_blocks) return e;
     return launch_dependent((const void *)move_kernel, grid, kPageThreads, 0, stream, args);
 }

@@ -290,8 +290,8 @@ awq_status_t awq_copy_pages(void *const *caches, int64_t num_caches, const awq_c
 int64_t awq_pages_workspace(int64_t num_blocks)
 {
     if (num_blocks <= 0 || num_blocks > (int64_t(1) << 28)) return -1;
-    const int64_t words = (num_blocks + 31) / 32;      // the bitmap, sums before its words, sums of 64 words
-    return 8 * words + (words + 63) / 64 * 4 + 16;
+    const int64_t words = (num_blocks + 31) / 32;      // the bitmap, sums before its words, sums of 256 words
+    return 8 * words + (words + 255) / 256 * 4 + 16;
 }
 
 awq_status_t awq_free_pages(const int32_t *block_table, int64_t rows, int64_t table_width, int64_t table_stride,
