@@ -204,12 +204,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = kThreads * kLoads;     // pieces: 8 KB, a stage of the ring
 constexpr int kPerSm = 4;             // CTAs: while one sorts, the others read
 constexpr int kStages = 3;
-constexpr int kKnown = 64;            // chunks of a part whose threads' maxima are kept
+constexpr int kKnown = 48;            // chunks of a part whose threads' maxima are kept
 constexpr int kLeastChunks = 2;
 constexpr int kAtOnce = 8;            // units of a warp under way
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads + 32, kPerSm)
+__global__ void __launch_bounds__(kThreads + 32, kPerSm + 1)     // registers that leave room for the merge's CTAs
 beam_rows_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int kEach = 16 / sizeof(T);
@@ -526,7 +526,6 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
     __shared__ uint8_t row_of_list[kMergeLists];
     __shared__ __align__(16) float heads[kMergeLists];
     __shared__ float floor;
-    __shared__ uint64_t ending[kMostEnding];
     __shared__ int ending_at[kMostEnding], picked, endings, told;
     const int beams = (int)p.a.beams, best = p.best, keep = (int)p.a.num_beams, threads = blockDim.x;
     const int ends = (int)p.a.num_ends;
@@ -547,7 +546,8 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
     for (int l = tid; l < p.merge_lists; l += threads) row_of_list[l] = kNoRow;
     __syncthreads();
     const int lists = last_list[beams - 1] + 1, candidates = lists * best;
-    uint64_t *keys = merge_smem, *picks = keys + p.merge_lists * best;      // picks: what reaches `floor`
+    // picks: those that end, and behind them what reaches `floor`
+    uint64_t *keys = merge_smem, *picks = keys + p.merge_lists * best;
     int *pick_at = reinterpret_cast<int *>(picks + p.merge_lists * best);
     float *highs = reinterpret_cast<float *>(pick_at + p.merge_lists * best);
     if (warp < beams)
@@ -636,7 +636,6 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
         if (!stops) {
             highs[c] = s + off;
         } else if (const int i = atomicAdd(&endings, 1); i < kMostEnding) {
-            ending[i] = exact(c);
             ending_at[i] = c;
         }
     }
@@ -669,53 +668,53 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
         if (rank == wanted - 1) floor = head;
     }
     __syncthreads();
-    for (int c = tid; c < candidates; c += threads)
-        if (highs[c] >= floor) {
-            const int i = atomicAdd(&picked, 1);
-            picks[i] = exact(c);
-            pick_at[i] = c;
-        }
+    const int e = min(endings, kMostEnding);
+    for (int c = tid; c < candidates + e; c += threads) {
+        const bool stops = c >= candidates;
+        if (!stops && !(highs[c] >= floor)) continue;
+        const int i = stops ? c - candidates : e + atomicAdd(&picked, 1), at = stops ? ending_at[i] : c;
+        picks[i] = exact(at);
+        pick_at[i] = at;
+    }
     __syncthreads();
 
     // ---- in order: a candidate's place is the number of those before it, a warp a candidate. Equal scores go by
     // row, then by logit and token
-    const int n = picked, e = min(endings, kMostEnding), warps = threads / 32;
-    auto place_in = [&](const uint64_t *others, const int *others_at, int count, uint64_t s, int c) {
-        int place = 0;
-        for (int j0 = 0; j0 < count; j0 += 32) {
+    const int n = e + picked;
+    for (int i = warp; i < n; i += threads / 32) {
+        const bool stops = i < e;
+        const uint64_t s = picks[i];
+        const int c = pick_at[i];
+        int live = 0, gone = 0;
+#pragma unroll 1
+        for (int j0 = 0; j0 < n; j0 += 32) {
             const int j = j0 + lane;
-            bool before = j < count && others[j] > s;
-            if (j < count && others[j] == s && others_at[j] != c) {
-                const int d = others_at[j], rd = row_of_list[d / best], rc = row_of_list[c / best];
+            const uint64_t other = j < n ? picks[j] : 0;
+            bool before = other > s;
+            if (other == s && j != i) {
+                const int d = pick_at[j], rd = row_of_list[d / best], rc = row_of_list[c / best];
                 before = rd != rc ? rd < rc : keys[d] > keys[c];
             }
-            place += __popc(__ballot_sync(0xFFFFFFFFu, before));
+            gone += __popc(__ballot_sync(0xFFFFFFFFu, before && j < e));
+            live += __popc(__ballot_sync(0xFFFFFFFFu, before && j >= e));
         }
-        return place;
-    };
-    auto tell = [&](float *out_scores, int *out_parents, int *out_tokens, int place, uint64_t s, int c) {
-        const int64_t to = request * keep + place;
-        out_scores[to] = s ? logit_of(s) : -INFINITY;
-        out_parents[to] = s ? (int)(r0 + row_of_list[c / best]) : -1;
-        out_tokens[to] = s ? (int)token_of(keys[c]) : -1;
-    };
-    for (int i = warp; i < n + e; i += warps) {
-        const bool stops = i >= n;
-        const uint64_t s = stops ? ending[i - n] : picks[i];
-        const int c = stops ? ending_at[i - n] : pick_at[i];
-        const int live = place_in(picks, pick_at, n, s, c), gone = stops ? place_in(ending, ending_at, e, s, c) : 0;
-        if (live + gone >= keep || lane > 0) continue;
-        if (!stops) {
-            tell(p.a.out_scores, p.a.out_parents, p.a.out_tokens, live, s, c);
-        } else {
-            tell(p.a.ended_scores, p.a.ended_parents, p.a.ended_tokens, gone, s, c);
-            atomicAdd(&told, 1);
-        }
+        if (live + (stops ? gone : 0) >= keep || lane > 0) continue;
+        const int64_t to = request * keep + (stops ? gone : live);
+        (stops ? p.a.ended_scores : p.a.out_scores)[to] = logit_of(s);
+        (stops ? p.a.ended_parents : p.a.out_parents)[to] = (int)r0 + row_of_list[c / best];
+        (stops ? p.a.ended_tokens : p.a.out_tokens)[to] = (int)token_of(keys[c]);
+        if (stops) atomicAdd(&told, 1);
     }
-    for (int k = n + tid; k < keep; k += threads) tell(p.a.out_scores, p.a.out_parents, p.a.out_tokens, k, 0, 0);
-    if (ends == 0) return;
-    __syncthreads();
-    for (int k = told + tid; k < keep; k += threads) tell(p.a.ended_scores, p.a.ended_parents, p.a.ended_tokens, k, 0, 0);
+    // places without a candidate
+    if (ends > 0) __syncthreads();
+    for (int k = tid; k < 2 * keep; k += threads) {
+        const bool stops = k >= keep;
+        const int place = stops ? k - keep : k;
+        if (place < (stops ? told : n - e) || (stops && ends == 0)) continue;
+        (stops ? p.a.ended_scores : p.a.out_scores)[request * keep + place] = -INFINITY;
+        (stops ? p.a.ended_parents : p.a.out_parents)[request * keep + place] = -1;
+        (stops ? p.a.ended_tokens : p.a.out_tokens)[request * keep + place] = -1;
+    }
 }
 
 // ---------------------------------------------------------------------------
