@@ -6,7 +6,7 @@ only what is older than its sources (any header change rebuilds all units).
 
 It also builds ``_build/libawq_gb300_fault_test.so``, the fault-test build
 used only by the tests: the units with bounded device waits (the C ABI, the
-decode, prefill, attention and beam kernels) compiled again with ``-DAWQ_FAULT_TEST`` (a wait
+decode, prefill, attention, beam and page kernels) compiled again with ``-DAWQ_FAULT_TEST`` (a wait
 limit of about 2 ms and the switch declared in
 ``include/awq_gb300_fault_test.h``), linked with the other units' objects.
 
@@ -39,7 +39,7 @@ FAULT_LIB = os.path.join(BUILD, "libawq_gb300_fault_test.so")
 FAULT_BUILD = os.path.join(BUILD, "fault_test")
 # units whose kernels wait on barriers or flags (and the ABI that sets the switch)
 FAULT_UNITS = ("awq_api.cu", "awq_decode.cu", "awq_prefill.cu", "awq_attention.cu", "awq_attention_tc.cu",
-               "awq_beam.cu")
+               "awq_beam.cu", "awq_pages.cu")
 INCLUDE = os.path.join(ROOT, "include")
 STEP_SOURCE = os.path.join(CSRC, "awq_step_module.cpp")
 

@@ -176,6 +176,7 @@ struct CopyParams {
     int row_pieces, head_pieces;      // of a token, of a head
     bool heads_first;                 // a head's tokens lie together
     int runs, run_token;              // of a page: runs `head` apart, bytes of a token in one
+    int fault;
 };
 
 __global__ void __launch_bounds__(kCopyThreads, 4)
@@ -303,7 +304,11 @@ copy_runs_kernel(const __grid_constant__ CopyParams p)
             to[s] = reinterpret_cast<char *>(dest);
             size[s] = n;
             ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), n);
-            ptx::bulk_load(ptx::smem_addr(copy_ring + s * kRunBytes), reinterpret_cast<const void *>(from), n, ptx::smem_addr(full + s));
+#ifdef AWQ_FAULT_TEST
+            if (!p.fault || blockIdx.x > 0)
+#endif
+                ptx::bulk_load(ptx::smem_addr(copy_ring + s * kRunBytes), reinterpret_cast<const void *>(from), n,
+                               ptx::smem_addr(full + s));
             if (++loads > kAhead) store();
         }
     }
@@ -635,6 +640,9 @@ cudaError_t launch_copy_pages(const CopyProblem &c, cudaStream_t stream)
         p.run_token = (int)(whole ? row * c.kv_heads : row);
         const bool runs = (whole || p.token == row) && (int64_t)p.run_token * c.block_size >= kLeastRun &&
                           page * c.pairs * p.caches >= kLeastBulk;
+#ifdef AWQ_FAULT_TEST
+        p.fault = fault_injection();
+#endif
         void *args[] = {&p};
         cudaError_t e;
         if (runs) {

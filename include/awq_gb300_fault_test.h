@@ -9,8 +9,9 @@
  * clock cycles (about 2 ms) instead of 4e9, and:
  *
  * awq_test_inject_fault(on) -- while `on` is non-zero, every decode, prefill
- *   and tree-attention kernel launched afterwards (awq_linear_forward and the
- *   calls built on it, awq_tree_attention) has the TMA producer of its CTA 0 issue no copy. That CTA's
+ *   and tree-attention kernel, every kernel that reads beams' logits and every bulk copy of pages
+ *   launched afterwards (awq_linear_forward and the calls built on it, awq_tree_attention,
+ *   awq_beam_select, awq_copy_pages) has the TMA producer of its CTA 0 issue no copy. That CTA's
  *   consumer warps then wait on a stage barrier that never fills; the waits
  *   run out, record AWQ_ERR_TIMEOUT in the device status word, and the
  *   kernel returns. Other CTAs that wait for CTA 0's partial sums give up the
