@@ -1,6 +1,6 @@
 // awq_beam.cu -- one step of beam search over the logits, and rows of other state by parent.
 //
-// beam_rows_kernel reads every logit once. The rows are a line of chunks of 512 16-byte
+// beam_rows_kernel reads every logit once. The rows are a line of chunks of 1024 16-byte
 // pieces, cut into equal parts, one a CTA; a producer warp keeps a ring of bulk copies under way
 // across rows, so that HBM does not wait while a row's end is worked on. Each thread keeps the
 // maximum of what it has read. No list is kept while the logits stream by: the best K of a part
@@ -32,7 +32,7 @@ namespace awq {
 namespace {
 
 constexpr int kThreads = 128;          // of the working warps
-constexpr int kLoads = 4;             // 16-byte pieces of a thread under way
+constexpr int kLoads = 8;             // 16-byte pieces of a thread in a chunk
 constexpr int kMostBeams = 32, kMostEnds = 8, kMostBest = kMostBeams + kMostEnds;
 constexpr int kMergeKeys = 6144;      // keys of a request's lists in the merge's shared memory
 constexpr int kMergeLists = 640;      // and its lists: as many as there are CTAs and beams, 608 + 32
@@ -154,6 +154,32 @@ struct Row {
     __device__ unsigned token(int piece) const { return (unsigned)(piece * kEach - lead); }
 };
 
+// Two fp32 values in one register pair.
+__device__ __forceinline__ uint64_t both(float a, float b)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ float2 apart(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t v;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t v;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+    return v;
+}
+
 // The greatest of a piece's elements as they are (a NaN gives way to a number), joined with `top`'s.
 template <typename T>
 __device__ __forceinline__ uint32_t top_of(uint4 v, uint32_t top)
@@ -201,22 +227,23 @@ __device__ __forceinline__ uint64_t warp_sort(uint64_t key)
 }
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = kThreads * kLoads;     // pieces: 8 KB, a stage of the ring
+constexpr int kChunk = kThreads * kLoads;     // pieces: 16 KB
+constexpr int kStage = kChunk / 2;            // pieces of a stage of the ring, for half of the warps
 constexpr int kPerSm = 4;             // CTAs: while one sorts, the others read
-constexpr int kStages = 3;
-constexpr int kKnown = 48;            // chunks of a part whose threads' maxima are kept
-constexpr int kLeastChunks = 2;
-constexpr int kAtOnce = 8;            // units of a warp under way
+constexpr int kStages = 4;
+constexpr int kKnown = 24;            // chunks of a part whose threads' maxima are kept
+constexpr int kLeastChunks = 1;
+constexpr int kAtOnce = 4;            // units of a warp under way
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads + 32, kPerSm + 1)     // registers that leave room for the merge's CTAs
+__global__ void __launch_bounds__(kThreads + 32, kPerSm)
 beam_rows_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int kEach = 16 / sizeof(T);
     constexpr int kUnit = kLoads * kEach;                // elements of a thread in a chunk
     constexpr int kRound = 1024 / kUnit;                 // units read between two looks at the list's length
     constexpr int kRoom = kMostBest + kRound * kUnit + 32;
-    extern __shared__ __align__(128) uint4 ring[];       // [kStages][kChunk]
+    extern __shared__ __align__(128) uint4 ring[];       // [kStages][kStage]
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t keys[kRoom], sorted[kWarps][32], leaders[kMostBest];
     __shared__ uint16_t highs[kKnown][kThreads];         // upper halves of the threads' maxima, in their order
@@ -227,7 +254,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(ptx::smem_addr(full + i), 1);
-            ptx::mbar_init(ptx::smem_addr(empty + i), kWarps);
+            ptx::mbar_init(ptx::smem_addr(empty + i), kWarps / 2);
         }
         ptx::fence_mbar_init();
         listed[0] = listed[1] = 0;
@@ -253,18 +280,20 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             if (p.a.scores[r] == -INFINITY) continue;
             const Row<T> row = row_of(r);
             for (int j = j0; j < j1 && ok; ++j) {
-                const int i = row.whole + j * kChunk;
-                if (i >= row.end) continue;
-                const int s = (int)(issued % kStages);
-                ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + s), ((issued / kStages) & 1) ^ 1, nullptr, p.status);
-                if (!ok) break;
-                const uint32_t bytes = (uint32_t)min(kChunk, row.end - i) * 16;
-                ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), bytes);
-                ++issued;
+                if (row.whole + j * kChunk >= row.end) continue;
+                for (int half = 0; half < 2; ++half) {
+                    const int i = row.whole + j * kChunk + half * kStage, s = (int)(issued % kStages);
+                    ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + s), ((issued / kStages) & 1) ^ 1, nullptr, p.status);
+                    if (!ok) break;
+                    const uint32_t bytes = (uint32_t)max(min(kStage, row.end - i), 0) * 16;
+                    ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), bytes);
+                    ++issued;
+                    if (bytes == 0) continue;
 #ifdef AWQ_FAULT_TEST
-                if (p.fault && blockIdx.x == 0) continue;
+                    if (p.fault && blockIdx.x == 0) continue;
 #endif
-                ptx::bulk_load(ptx::smem_addr(ring + s * kChunk), row.pieces + i, bytes, ptx::smem_addr(full + s));
+                    ptx::bulk_load(ptx::smem_addr(ring + s * kStage), row.pieces + i, bytes, ptx::smem_addr(full + s));
+                }
             }
         }
         // after a wait that ran out: the copies on their way land before the shared memory goes
@@ -299,20 +328,22 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             uint4 v[kLoads];
             uint32_t all = nothing;
             if (i < row.end) {
-                const int s = (int)(used % kStages);
-                landed = landed && ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (used / kStages) & 1, nullptr, p.status);
+                const int64_t stage = 2 * used + tid / (kThreads / 2);
+                const int s = (int)(stage % kStages);
+                landed = landed && ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (stage / kStages) & 1, nullptr, p.status);
                 if (!__all_sync(0xFFFFFFFFu, landed)) {
                     landed = false;
                     break;
                 }
                 ++used;
                 // in an order that keeps eight lanes off one another's banks
+                const uint4 *from = ring + s * kStage + tid % (kThreads / 2) * kLoads;
 #pragma unroll
-                for (int u = 0; u < kLoads; ++u) v[u] = ring[s * kChunk + tid * kLoads + (u + (tid >> 1)) % kLoads];
+                for (int u = 0; u < kLoads; ++u) v[u] = from[(u + tid) % kLoads];
                 if (row.end - i < kChunk) {
 #pragma unroll
                     for (int u = 0; u < kLoads; ++u)
-                        if (i + tid * kLoads + (u + (tid >> 1)) % kLoads >= row.end)
+                        if (i + tid * kLoads + (u + tid) % kLoads >= row.end)
                             v[u] = make_uint4(nothing, nothing, nothing, nothing);
                 }
 #pragma unroll
@@ -335,26 +366,36 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             const float most = logit_of((uint64_t)order << 32), base = most > -INFINITY ? most : 0.f;
             // 2^(x log2 e - shift), one FMA; what shift's own rounding did is put right below
             const float shift = base * kLog2e;
-            float sums[4] = {};
-            if (fabsf(base) < 0x1p120f) {
+            const bool usual = fabsf(base) < 0x1p120f;       // else that product would leave fp32
+            uint64_t s0 = 0, s1 = 0;
+            float sum;
+            if (usual) {
+                const uint64_t scale = both(kLog2e, kLog2e), minus = both(-shift, -shift);
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
                     float x[kEach];
                     widen<T>(v[u], x);
 #pragma unroll
-                    for (int k = 0; k < kEach; ++k) sums[k % 4] += power(fmaf(x[k], kLog2e, -shift));
+                    for (int k = 0; k < kEach; k += 2) {
+                        const float2 t = apart(fma2(both(x[k], x[k + 1]), scale, minus));
+                        const uint64_t e = both(power(t.x), power(t.y));
+                        if (k & 2) s1 = add2(s1, e);
+                        else s0 = add2(s0, e);
+                    }
                 }
-            } else {      // where that product would leave fp32
-#pragma unroll 1
+                const float2 sums = apart(add2(s0, s1));
+                sum = sums.x + sums.y;
+                sum = fmaf(sum, -kLn2 * fmaf(base, kLog2e, -shift), sum);
+            } else {
+                sum = 0.f;
+#pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
                     float x[kEach];
-                    widen<T>(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3], x);
+                    widen<T>(v[u], x);
 #pragma unroll
-                    for (int k = 0; k < kEach; ++k) sums[k % 4] += power((x[k] - base) * kLog2e);
+                    for (int k = 0; k < kEach; ++k) sum += power((x[k] - base) * kLog2e);
                 }
             }
-            float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-            if (fabsf(base) < 0x1p120f) sum = fmaf(sum, -kLn2 * fmaf(base, kLog2e, -shift), sum);
             // a NaN stays one
             sum += power((alone - base) * kLog2e);
 #pragma unroll
@@ -413,7 +454,8 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             const int all = todos;
             for (int i0 = 0; i0 < all; i0 += kRound) {
                 for (int i = i0 + warp * kAtOnce; i < min(i0 + kRound, all); i += kWarps * kAtOnce) {
-                    float x[kAtOnce];
+                    constexpr int kLane = kUnit / 32;              // elements of a lane
+                    float x[kAtOnce][kLane];
                     int element[kAtOnce];
                     bool behind[kAtOnce];
 #pragma unroll
@@ -423,13 +465,18 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
                         element[u] = (int)row.token(piece) + lane;
                         // equal to the least maximum: only up to its place, so that lists stay short
                         behind[u] = ((uint64_t)floor_value << 32 | (0xFFFFFFFFu - (unsigned)((j - j0) * kThreads + l))) < least;
-                        x[u] = -INFINITY;
-                        if (i + u < all && lane < kUnit && piece + lane / kEach < row.end) x[u] = one(row.row + element[u]);
+#pragma unroll
+                        for (int k = 0; k < kLane; ++k) {
+                            x[u][k] = -INFINITY;
+                            if (i + u < all && piece + (lane + 32 * k) / kEach < row.end) x[u][k] = one(row.row + element[u] + 32 * k);
+                        }
                     }
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u)
-                        if (x[u] > -INFINITY && (!behind[u] || (uint32_t)(key_of(x[u], 0) >> 32) > floor_value))
-                            enlist(x[u], element[u]);
+#pragma unroll
+                        for (int k = 0; k < kLane; ++k)
+                            if (x[u][k] > -INFINITY && (!behind[u] || (uint32_t)(key_of(x[u][k], 0) >> 32) > floor_value))
+                                enlist(x[u][k], element[u] + 32 * k);
                 }
                 if (i0 + kRound >= all && g0 + kKnown >= j1) break;
                 ptx::named_barrier(1, kThreads);
@@ -828,7 +875,7 @@ cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
     void *args[] = {&p};
     const void *kernel = a.dtype == AWQ_F16 ? rows_kernel<__half>()
                          : a.dtype == AWQ_BF16 ? rows_kernel<__nv_bfloat16>() : rows_kernel<float>();
-    constexpr size_t ring = kStages * kChunk * sizeof(uint4);
+    constexpr size_t ring = kStages * kStage * sizeof(uint4);
     cudaError_t e = allow_shared(kernel, ring);
     if (e == cudaSuccess)
         e = allow_shared((const void *)beam_merge_kernel, merge_bytes(kMergeKeys));
