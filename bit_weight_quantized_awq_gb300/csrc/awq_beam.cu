@@ -753,11 +753,12 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
         if (stops) atomicAdd(&told, 1);
     }
     // places without a candidate
-    if (ends > 0) __syncthreads();
+    const bool tells = p.a.ended_scores != nullptr;
+    if (tells) __syncthreads();
     for (int k = tid; k < 2 * keep; k += threads) {
         const bool stops = k >= keep;
         const int place = stops ? k - keep : k;
-        if (place < (stops ? told : n - e) || (stops && ends == 0)) continue;
+        if (place < (stops ? told : n - e) || (stops && !tells)) continue;
         (stops ? p.a.ended_scores : p.a.out_scores)[request * keep + place] = -INFINITY;
         (stops ? p.a.ended_parents : p.a.out_parents)[request * keep + place] = -1;
         (stops ? p.a.ended_tokens : p.a.out_tokens)[request * keep + place] = -1;

@@ -29,7 +29,7 @@ bool cache_strides_ok(const awq_cache_t &c)
 // What awq_free_pages and awq_compact_pages ask of their sizes.
 bool pages_ok(int64_t rows, int64_t width, int64_t stride, int64_t block_size, int64_t num_blocks, int64_t num_held)
 {
-    return rows >= 0 && rows <= (1 << 20) && width > 0 && width < kInt && stride >= width && page_size_ok(block_size) &&
+    return rows >= 0 && rows <= (1 << 20) && width > 0 && width <= kInt / 2 && stride >= width && page_size_ok(block_size) &&
            num_blocks > 0 && num_blocks <= (1 << 28) && num_held >= 0 && num_held < kInt;
 }
 
@@ -208,7 +208,7 @@ awq_status_t awq_beam_select(const awq_beam_select_t *args, awq_stream_t stream)
         return AWQ_ERR_INVALID_ARG;
     if (a.requests == 0) return AWQ_OK;
     if (!a.logits || !a.scores || !a.out_scores || !a.out_parents || !a.out_tokens || !a.workspace ||
-        a.workspace_bytes < bytes || (a.num_ends > 0 && (!a.ended_scores || !a.ended_parents || !a.ended_tokens)))
+        a.workspace_bytes < bytes || ((a.num_ends > 0 || a.ended_scores) && (!a.ended_scores || !a.ended_parents || !a.ended_tokens)))
         return AWQ_ERR_INVALID_ARG;
     if (!aligned(a.logits, a.dtype == AWQ_F32 ? 4 : 2) || !aligned(a.scores, 4) || !aligned(a.end_tokens, 4) ||
         !aligned(a.out_scores, 4) || !aligned(a.out_parents, 4) || !aligned(a.out_tokens, 4) ||
@@ -248,7 +248,7 @@ awq_status_t awq_fork_pages(const int32_t *block_table, int64_t rows_in, int64_t
                             int32_t *count, awq_stream_t stream)
 {
     if (rows_in < 0 || rows_in > kMaxRequests || rows_out < 0 || rows_out > kMaxRequests || !page_size_ok(block_size) ||
-        table_width <= 0 || table_width >= kInt || table_stride < table_width || new_stride < table_width ||
+        table_width <= 0 || table_width > kInt / 2 || table_stride < table_width || new_stride < table_width ||
         num_free < 0 || num_free >= kInt)
         return AWQ_ERR_INVALID_ARG;
     if (!count || (rows_in > 0 && (!block_table || !lens)) || (num_free > 0 && !free_blocks) ||

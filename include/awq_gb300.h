@@ -656,13 +656,16 @@ awq_status_t awq_rotary(const awq_rotary_t *args, awq_stream_t stream);
  * and, with end_tokens, reports those among the first num_beams of all its candidates
  * that end there:
  *   ended_scores, ended_parents, ended_tokens  the same for these
- * Places without a candidate hold -inf, -1 and -1. The sum is in fp32 and its parts are
- * added up, and s compared, in 64 bits.
+ * Places without a candidate hold -inf, -1 and -1. The sum is in fp32 over chunks of 16 KB;
+ * the chunks are added up, and s compared, with pairs of fp32 numbers (about 48 bits). What a
+ * row gives does not depend on the other rows: rows with equal logits, at the same place within 16
+ * bytes, and equal scores tie.
  *
  *   logits      [requests * beams, vocab] fp16, bf16 or fp32 (dtype), elements of a row
  *               contiguous, rows logits_row_stride elements apart
  *   scores      fp32 [requests * beams]; -inf: no beam, its row is not looked at
- *   end_tokens  int32 [num_ends] or NULL; tokens outside [0, vocab) match nothing
+ *   end_tokens  int32 [num_ends] or NULL; tokens outside [0, vocab) match nothing. ended_*
+ *               may be NULL without any
  *   workspace   awq_beam_select_workspace() bytes, 256-byte aligned, used until the
  *               call's work is done
  * A logit of -inf is no candidate. A row with a NaN or +inf among its logits, or with such a
@@ -736,7 +739,7 @@ awq_status_t awq_reorder_states(const awq_state_t *states, int64_t count, const 
  * counts as that width, all its pages full). A negative length counts as 0, a parent outside [-1, rows_in) as -1, a
  * negative *free_start as 0, each reported as AWQ_ERR_INVALID_ARG.
  * Requires 0 <= rows_in, rows_out <= 16384, block_size a power of two from 16 to 1024,
- * table_stride and new_stride >= table_width > 0, 0 <= num_free < 2^31.
+ * table_stride and new_stride >= table_width, 0 < table_width <= 2^30, 0 <= num_free < 2^31.
  */
 awq_status_t awq_fork_pages(const int32_t *block_table, int64_t rows_in, int64_t table_width,
                             int64_t table_stride, const int32_t *lens, const int32_t *parents,
@@ -781,7 +784,7 @@ awq_status_t awq_copy_pages(void *const *caches, int64_t num_caches, const awq_c
  * An entry outside [0, num_blocks) is skipped and reported; a negative length counts as 0
  * and a length beyond the table's width as that width, each reported.
  * Requires 0 <= rows <= 2^20, block_size a power of two from 16 to 1024, table_stride >=
- * table_width > 0, 0 < num_blocks <= 2^28, 0 <= num_held < 2^31.
+ * table_width, 0 < table_width <= 2^30, 0 < num_blocks <= 2^28, 0 <= num_held < 2^31.
  */
 awq_status_t awq_free_pages(const int32_t *block_table, int64_t rows, int64_t table_width,
                             int64_t table_stride, const int32_t *lens, int64_t block_size,

@@ -83,6 +83,11 @@ def test_beam_select_misaligned(kw):
     assert beam(**kw) == MISALIGNED
 
 
+def test_beam_select_without_end_tokens():
+    none = dict(end_tokens=None, num_ends=0)
+    assert beam(**none, ended_parents=None) == INVALID and beam(**none, ended_scores=None, workspace=None) == INVALID
+
+
 def test_beam_select_empty_and_workspace():
     assert beam(requests=0, logits=None, scores=None, workspace=None) == OK
     assert awq.awq_beam_select(None, None) == INVALID
@@ -121,7 +126,7 @@ def fork(**k):
 
 @pytest.mark.parametrize("kw", [
     dict(rows_in=-1), dict(rows_in=16385), dict(rows_out=-1), dict(rows_out=16385), dict(page=8), dict(page=48), dict(width=0),
-    dict(width=2 ** 31, stride=2 ** 31, new_stride=2 ** 31), dict(stride=7), dict(new_stride=7), dict(num_free=-1),
+    dict(width=2 ** 30 + 1, stride=2 ** 31, new_stride=2 ** 31), dict(stride=7), dict(new_stride=7), dict(num_free=-1),
     dict(num_free=2 ** 31), dict(table=None), dict(lens=None), dict(parents=None), dict(free=None), dict(new=None),
     dict(new_lens=None), dict(src=None), dict(dst=None), dict(tokens=None), dict(count=None), dict(new=A)])
 def test_fork_invalid(kw):
@@ -170,9 +175,12 @@ def compact(**k):
 
 @pytest.mark.parametrize("call", [free, compact])
 @pytest.mark.parametrize("kw", [
-    dict(rows=-1), dict(rows=2 ** 20 + 1), dict(width=0), dict(stride=7), dict(page=8), dict(page=100), dict(blocks=0),
+    dict(rows=-1), dict(rows=2 ** 20 + 1), dict(width=0), dict(width=2 ** 30 + 1, stride=2 ** 31, new_stride=2 ** 31), dict(stride=7),
+    dict(page=8), dict(page=100), dict(blocks=0),
     dict(blocks=2 ** 28 + 1), dict(num_held=-1), dict(num_held=1), dict(table=None), dict(lens=None), dict(workspace=None)])
 def test_pages_invalid(call, kw):
+    if call is free:
+        kw = {k: v for k, v in kw.items() if k != "new_stride"}
     assert call(**kw) == INVALID
 
 

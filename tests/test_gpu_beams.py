@@ -88,7 +88,7 @@ def test_beams_match_the_reference(dtype, B, W, V, keep, ends):
 
 
 @pytest.mark.parametrize("dtype", [FP16, FP32])
-@pytest.mark.parametrize("kind", ["equal", "few", "descending", "ascending", "periodic", "zeros"])
+@pytest.mark.parametrize("kind", ["equal", "few", "descending", "ascending", "periodic", "one_place", "zeros"])
 def test_ties_and_orders(dtype, kind):
     """Equal logits go by the lowest token; data whose best lie together are found as well."""
     B, W, V, keep = 2, 3, 20011, 9
@@ -98,6 +98,8 @@ def test_ties_and_orders(dtype, kind):
               "few": torch.randint(3, (V,), device="cuda", generator=gen).float(),
               # the best all at one residue of the pieces that a thread reads
               "periodic": (at % 2048 < 8).float() * (10 + at / V),
+              # and all of them with one thread
+              "one_place": (at % 8192 < 64).float() * (10 + at / V),
               "zeros": torch.where(at % 2 == 0, -0.0, 0.0)}[kind]
     logits = logits.expand(B * W, V).to(dtype).contiguous()
     # rows far apart, so that rows do not tie
@@ -173,21 +175,34 @@ def test_end_tokens():
     assert (step.parents == -1).all() and step.ended_tokens[0].tolist() == [0, 1]
 
 
+def test_an_empty_list_of_end_tokens():
+    step = awq.beam_select(torch.randn((3, 50), device="cuda"), torch.zeros((1, 3), device="cuda"), 4, end_tokens=i32([]))
+    assert (step.ended_scores == -torch.inf).all() and (step.ended_parents == -1).all() and (step.ended_tokens == -1).all()
+
+
+def test_a_row_gives_the_same_alone_and_among_others():
+    """Bit for bit, wherever it lies in the batch and however the batch is shared out."""
+    for V in (32000, 151936):
+        logits = torch.randn((60, V), device="cuda").bfloat16()
+        before = -torch.rand((60, 1), device="cuda")
+        every = awq.beam_select(logits, before, 5)
+        for r in (0, 7, 59):
+            one = awq.beam_select(logits[r:r + 1], before[r:r + 1], 5)
+            assert torch.equal(one.scores[0], every.scores[r]) and torch.equal(one.tokens[0], every.tokens[r])
+
+
 def test_no_requests():
     step = awq.beam_select(torch.zeros((0, 10), device="cuda"), torch.zeros((0, 4), device="cuda"), 4, end_tokens=i32([1]))
     assert step.scores.shape == (0, 4) and step.ended_tokens.shape == (0, 4)
 
 
-def test_a_large_vocabulary_is_read_in_several_rounds():
-    V = 2 ** 22 + 5
-    logits = torch.randn((33, V), device="cuda").half()
+@pytest.mark.parametrize("V", [2 ** 22 + 5, 2 ** 24 + 3])
+def test_a_large_vocabulary_is_read_in_several_rounds(V):
     at = torch.arange(V, device="cuda")
-    logits[0] = (at % 2048 < 8).half() * (at / V).half()       # the best with few threads: lists that fill up
-    before = -torch.arange(33, device="cuda").float()[None]
-    before[:, 32] = 0
-    for row in (0, 32):
-        step = check(logits[row:row + 1], before[:, row:row + 1].contiguous(), 32, (7,))
-    assert step is not None
+    # among others the best with few threads, or one, so that lists fill up
+    for row in ((at % 2048 < 8).half() * (at / V).half(), (at % 8192 < 64).half() * (at / V).half(),
+                torch.randn(V, device="cuda").half()):
+        check(row[None], torch.zeros((1, 1), device="cuda"), 32, (7,))
 
 
 # ---------------------------------------------------------------- states
