@@ -271,6 +271,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
     if (warp == kWarps) {
         // ---------------------------------------------------------------- the rows' way in
         if (lane > 0) return;
+        const uint64_t policy = ptx::evict_first_policy();
         int64_t issued = 0;
         bool ok = true;
         for (int64_t at = begin, r = begin / p.chunks; at < end && ok; ++r) {
@@ -292,7 +293,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
 #ifdef AWQ_FAULT_TEST
                     if (p.fault && blockIdx.x == 0) continue;
 #endif
-                    ptx::bulk_load(ptx::smem_addr(ring + s * kStage), row.pieces + i, bytes, ptx::smem_addr(full + s));
+                    ptx::bulk_load(ptx::smem_addr(ring + s * kStage), row.pieces + i, bytes, ptx::smem_addr(full + s), policy);
                 }
             }
         }
