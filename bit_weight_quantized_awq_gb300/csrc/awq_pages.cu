@@ -51,7 +51,8 @@ __device__ __forceinline__ int pages_of(int length, int block_size, int shift, i
 // ---------------------------------------------------------------------------
 // Fork. Which row is its parent's first and how many rows before it need a block follows
 // from the parents and lengths alone; every CTA computes both for all rows by itself, as the plan
-// does, so the step is one launch. Bound: latency; the tables are a few KB to a few MB.
+// does, so the step is one launch. Bound: latency; the tables are a few KB to a few MB. Measured: 8 rows 3.7 us,
+// 384 rows 5.1 us.
 
 constexpr int kForkThreads = 512;
 constexpr int kForkEntries = 2048;          // of a row, a CTA and turn
@@ -160,7 +161,8 @@ fork_kernel(const __grid_constant__ ForkProblem p, unsigned int *status)
 // ---------------------------------------------------------------------------
 // Copies of pages, 16 bytes at a time, kCopyPieces of a thread under way. A unit is a
 // part of one page of one cache; the CTAs take units in turn, since how many there are is known
-// on the device only. Bound: HBM, each byte read and written once.
+// on the device only. Bound: HBM, each byte read and written once. For small copies (2 layers, pages of 16 KB: 2.4
+// us) and layouts without long runs; 24 layers of 48 x 8 beams took 189 us so, and 139 in bulk.
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPieces = 8;
@@ -230,7 +232,8 @@ copy_pages_kernel(const __grid_constant__ CopyParams p)
     }
 }
 
-// The same by bulk copies, for pages whose tokens lie in long runs: through a ring in shared memory, kAhead
+// The same by bulk copies (90 % of the copy bandwidth; 1.5 GB of moved pages 253 us, 284 by the
+// kernel above), for pages whose tokens lie in long runs: through a ring in shared memory, kAhead
 // loads and as many stores under way, all issued by one lane. The 32 lanes of the CTA look up 32 parts at
 // a time.
 constexpr int kRunBytes = 16384;            // of a run at once
@@ -323,7 +326,9 @@ copy_runs_kernel(const __grid_constant__ CopyParams p)
 // ---------------------------------------------------------------------------
 // Used blocks as a bitmap, set from the tables (a bit that is set twice stays set: no
 // counts, and no order that results could depend on); then free blocks and moves are
-// numbered by the bits before them.
+// numbered by the bits before them. Bound for large caches: the work of L2, in which every entry sets a random
+// bit (2.2 million of 2.5 million blocks: 17 us of 27; bytes instead of bits are not faster, and ranges of blocks in
+// shared memory, joined word by word, 8 % at best).
 
 constexpr int kPageThreads = 512;
 constexpr int kListWords = 256;           // of the bitmap, for a CTA

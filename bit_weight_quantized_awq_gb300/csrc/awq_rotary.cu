@@ -13,6 +13,11 @@
 // cosines and sines are computed once for all of the CTA's heads, by all of its threads, and shared
 // through shared memory. Each thread asks for its first kItems pieces before that, so that their way in takes
 // no time of its own.
+// Measured: 16,383 tokens of 64 / 8 heads of 128 bf16 into a cache 110 us, 90 % of the copy bandwidth
+// (torch's copy of as many dense bytes takes 106); 30,001 tokens of 16 / 4 heads of 96 with three axes
+// 48 us (a dense copy: 41); one token of 32 heads 4.3 us a call. With places of heads worked out item by
+// item the first took 152 us; with more tokens a CTA 121 (twice) and 125 (four times); with two items a thread and
+// five CTAs an SM 111. A shorter way to the angles (fp32 pairs, own series) changed nothing.
 #include <algorithm>
 
 #include <cuda_bf16.h>

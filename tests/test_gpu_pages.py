@@ -252,6 +252,17 @@ def test_free_and_compact_of_millions_of_blocks():
     check_pages(table, lens, 16, blocks)
 
 
+@pytest.mark.parametrize("rows,longest,spare", [(3000, 16 * 600, 1000), (700, 16 * 2000, 0), (2, 40, 300000), (5000, 16 * 3000, 100)])
+def test_many_rows_that_share_many_blocks(rows, longest, spare):
+    """More entries than blocks, from a few thousand blocks to millions."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(0, longest + 1, rows)
+    have = -(-lens // 16)
+    blocks = max(int(have.sum()) // 9, 1) + spare
+    table = rng.integers(0, blocks, (rows, int(have.max()) + 1))
+    check_pages(table, lens, 16, blocks)
+
+
 def test_tables_that_are_views():
     wide = torch.full((3, 10), -9, dtype=torch.int32, device="cuda")
     wide[:, 4:7] = i32([[5, 6, -1], [1, -1, -1], [7, 2, 0]])
