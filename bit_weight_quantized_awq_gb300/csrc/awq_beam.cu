@@ -238,7 +238,6 @@ constexpr int kStage = kChunk / 2;            // pieces of a stage of the ring, 
 constexpr int kPerSm = 4;             // CTAs: while one sorts, the others read
 constexpr int kStages = 4;
 constexpr int kKnown = 24;            // chunks of a part whose threads' maxima are kept
-constexpr int kLeastChunks = 1;
 constexpr int kAtOnce = 4;            // units of a warp under way
 
 template <typename T>
@@ -325,7 +324,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         const float single = in_head || in_tail ? one(row.row + single_token) : -INFINITY;
         const int single_chunk = in_tail ? j1 - 1 : j0;
 
-        // ---- each thread four neighbouring pieces of a chunk: its maximum, and the warp's sum
+        // ---- each thread kLoads neighbouring pieces of a chunk: its maximum, and the warp's sum
         float m = -INFINITY;
         int where = 0;
         bool landed = true;
@@ -548,7 +547,7 @@ __device__ __forceinline__ void add_log(Sum x, Sum &to)
 {
     int bits = __float_as_int(x.high);
     const int e = (bits - 0x3F2AAAAB) >> 23;
-    const float scale = __int_as_float((127 - e) << 23);       // two times below for e near the ends: sums are 1 to 2^28
+    const float scale = __int_as_float((127 - e) << 23);       // a normal number: sums are 1 to 2^28
     const float m = x.high * scale, a = m - 1.f, b = m + 1.f;
     const float r = 1.f / b, t = a * r;
     // (a - t (m + 1)) / (m + 1), of b's own rounding too, and of x.low
@@ -671,11 +670,12 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
         const int w = row_of_list[c / best];
         Sum s;
         s.high = logit_of(keys[c]);
+        // below the least fp32 number, where two-sums have no remainder, all are one: -inf
+        if (befores[w] + (s.high - lses[w].high) == -INFINITY) return order_of({-INFINITY, 0.f});
         s.add(-lses[w].high);
         s.add(befores[w]);
         s.low -= lses[w].low;
         s.settle();
-        if (!(fabsf(s.high) < INFINITY)) s.low = 0.f;
         return order_of(s);
     };
     for (int c = tid; c < candidates; c += threads) {
@@ -856,7 +856,7 @@ BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, i
     const int64_t total = requests * beams * c.chunks;
     const int64_t lists = std::min<int64_t>(kMergeKeys / best, kMergeLists) - beams - 1;
     c.each = std::max({std::min<int64_t>((total + kPerSm * 152 - 1) / (kPerSm * 152), kKnown), (c.chunks + 30) / 31,
-                       (beams * c.chunks + lists - 1) / lists, int64_t(kLeastChunks)});
+                       (beams * c.chunks + lists - 1) / lists, int64_t(1)});
     c.ctas = (total + c.each - 1) / c.each;
     c.merge_lists = beams * c.chunks / c.each + beams + 1;
     // 8-byte words of the workspace: best keys a stretch, maximum and sum of each chunk and warp

@@ -139,6 +139,30 @@ def test_masked_rows_and_dead_beams(dtype):
     assert (step.parents[2] == -1).all() and (step.ended_parents[2] == -1).all()
 
 
+@pytest.mark.parametrize("V", [500, 300000])
+def test_scores_below_the_least_fp32_number(V):
+    """They are rounded to -inf, and their tokens are candidates all the same."""
+    logits = torch.full((2, V), torch.finfo(FP32).min, device="cuda")
+    logits[:, 7] = 3e38
+    logits[1, 9:] = -torch.inf
+    step = awq.beam_select(logits, torch.tensor([[-1.0], [-2.0]], device="cuda"), 4)
+    assert step.tokens[0].tolist() == [7, 0, 1, 2] and step.tokens[1].tolist() == [7, 0, 1, 2]
+    assert step.parents.tolist() == [[0] * 4, [1] * 4] and step.scores.tolist() == [[-1.0] + [-torch.inf] * 3, [-2.0] + [-torch.inf] * 3]
+
+
+@pytest.mark.parametrize("requests", [1, 3, 38, 39])
+@pytest.mark.parametrize("V", [9, 8191, 8192, 20000])
+def test_few_and_many_requests_give_the_same(requests, V):
+    """However the rows are shared out over CTAs."""
+    logits = torch.randn((39 * 3, V), device="cuda").half()
+    before = -torch.rand((39, 3), device="cuda")
+    before[2, 1] = -torch.inf
+    every = awq.beam_select(logits, before, 7, end_tokens=i32([3, 5]))
+    some = awq.beam_select(logits[:3 * requests], before[:requests], 7, end_tokens=i32([3, 5]))
+    for a, b in zip(some, every):
+        assert torch.equal(a, b[:requests])
+
+
 @pytest.mark.parametrize("bad", [torch.nan, torch.inf])
 @pytest.mark.parametrize("where", [0, 4999, 10002])
 def test_rows_with_nan_or_infinity_have_no_candidates_and_are_reported(bad, where):
