@@ -38,7 +38,7 @@ namespace awq {
 namespace {
 
 constexpr int kThreads = 128;          // of the working warps
-constexpr int kLoads = 8;             // 16-byte pieces of a thread in a chunk
+constexpr int kLoads = 8;             // 16-byte pieces of a thread in a chunk at most
 constexpr int kMostBeams = 32, kMostEnds = 8, kMostBest = kMostBeams + kMostEnds;
 constexpr int kMergeKeys = 6144;      // keys of a request's lists in the merge's shared memory
 constexpr int kMergeLists = 640;      // and its lists; beam_cut keeps to both
@@ -55,6 +55,7 @@ struct BeamParams {
     float2 *sums;
     uint64_t *lists;
     int64_t rows, chunks, each;
+    int chunk, own;                   // pieces of a chunk, and of a thread in it
     int best, merge_lists, fault;     // merge_lists: the most stretches of a request
 };
 
@@ -233,27 +234,25 @@ __device__ __forceinline__ uint64_t warp_sort(uint64_t key)
 }
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = kThreads * kLoads;     // pieces: 16 KB
+constexpr int kChunk = kThreads * kLoads;     // pieces at most: 16 KB
 constexpr int kStage = kChunk / 2;            // pieces of a stage of the ring, for half of the warps
+constexpr int kRoom = 512;            // keys of a part that the list of the best is taken from
 constexpr int kPerSm = 4;             // CTAs: while one sorts, the others read
 constexpr int kStages = 4;
 constexpr int kKnown = 24;            // chunks of a part whose threads' maxima are kept
-constexpr int kAtOnce = 4;            // units of a warp under way
+constexpr int kAtOnce = 4;            // pieces of a thread under way
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads + 32, kPerSm)
 beam_rows_kernel(const __grid_constant__ BeamParams p)
 {
     constexpr int kEach = 16 / sizeof(T);
-    constexpr int kUnit = kLoads * kEach;                // elements of a thread in a chunk
-    constexpr int kRound = 1024 / kUnit;                 // units read between two looks at the list's length
-    constexpr int kRoom = kMostBest + kRound * kUnit + 32;
     extern __shared__ __align__(128) uint4 ring[];       // [kStages][kStage]
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ uint64_t keys[kRoom], sorted[kWarps][32], leaders[kMostBest];
     __shared__ uint16_t highs[kKnown][kThreads];         // upper halves of the threads' maxima, in their order
-    __shared__ uint16_t todo[kMostBest * kKnown];
-    __shared__ int who[kMostBest], listed[2], todos;
+    __shared__ uint16_t todo[kMostBest * kKnown];        // kThreads * chunk + thread
+    __shared__ int who[kMostBest], listed, todos;
     __shared__ uint64_t least;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -262,7 +261,6 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             ptx::mbar_init(ptx::smem_addr(empty + i), kWarps / 2);
         }
         ptx::fence_mbar_init();
-        listed[0] = listed[1] = 0;
     }
     __syncthreads();
     ptx::launch_dependents();
@@ -273,6 +271,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         return Row<T>(static_cast<const T *>(p.a.logits) + r * p.a.logits_row_stride, (int)p.a.vocab);
     };
 
+    const int first_half = kThreads / 2 * p.own;
     if (warp == kWarps) {
         // ---------------------------------------------------------------- the rows' way in
         if (lane > 0) return;
@@ -286,12 +285,15 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             if (p.a.scores[r] == -INFINITY) continue;
             const Row<T> row = row_of(r);
             for (int j = j0; j < j1 && ok; ++j) {
-                if (row.whole + j * kChunk >= row.end) continue;
+                const int i0 = row.whole + j * p.chunk, i2 = min(i0 + p.chunk, row.end);
+                if (i0 >= i2) continue;
                 for (int half = 0; half < 2; ++half) {
-                    const int i = row.whole + j * kChunk + half * kStage, s = (int)(issued % kStages);
+                    // the first half of the threads have the first stage
+                    const int i = half ? min(i0 + first_half, i2) : i0, i1 = half ? i2 : min(i0 + first_half, i2);
+                    const int s = (int)(issued % kStages);
                     ok = ptx::mbar_wait_bounded(ptx::smem_addr(empty + s), ((issued / kStages) & 1) ^ 1, nullptr, p.status);
                     if (!ok) break;
-                    const uint32_t bytes = (uint32_t)max(min(kStage, row.end - i), 0) * 16;
+                    const uint32_t bytes = (uint32_t)(i1 - i) * 16;
                     ptx::mbar_arrive_expect_tx(ptx::smem_addr(full + s), bytes);
                     ++issued;
                     if (bytes == 0) continue;
@@ -309,8 +311,8 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
     }
 
     // ---------------------------------------------------------------- maxima, sums, lists
+    constexpr uint32_t nothing = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
     int64_t used = 0;
-    int turn = 0;
     for (int64_t at = begin, r = begin / p.chunks; at < end; ++r) {
         const int j0 = (int)(at - r * p.chunks), j1 = (int)min(p.chunks, j0 + end - at);
         at += j1 - j0;
@@ -329,11 +331,10 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         int where = 0;
         bool landed = true;
         for (int j = j0; j < j1; ++j) {
-            constexpr uint32_t nothing = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
-            const int i = row.whole + j * kChunk;
+            const int i = row.whole + j * p.chunk, count = min(p.chunk, row.end - i);
             uint4 v[kLoads];
             uint32_t all = nothing;
-            if (i < row.end) {
+            if (count > 0) {
                 const int64_t stage = 2 * used + tid / (kThreads / 2);
                 const int s = (int)(stage % kStages);
                 landed = landed && ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (stage / kStages) & 1, nullptr, p.status);
@@ -343,14 +344,17 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
                 }
                 ++used;
                 // in an order that keeps eight lanes off one another's banks
-                const uint4 *from = ring + s * kStage + tid % (kThreads / 2) * kLoads;
+                const uint4 *from = ring + s * kStage + tid % (kThreads / 2) * p.own;
+                if (p.own == kLoads && (warp + 1) * 32 * kLoads <= count) {
 #pragma unroll
-                for (int u = 0; u < kLoads; ++u) v[u] = from[(u + tid) % kLoads];
-                if (row.end - i < kChunk) {
+                    for (int u = 0; u < kLoads; ++u) v[u] = from[(u + tid) % kLoads];
+                } else {
+                    const int mine = min(p.own, count - tid * p.own);
 #pragma unroll
-                    for (int u = 0; u < kLoads; ++u)
-                        if (i + tid * kLoads + (u + tid) % kLoads >= row.end)
-                            v[u] = make_uint4(nothing, nothing, nothing, nothing);
+                    for (int u = 0; u < kLoads; ++u) {
+                        v[u] = make_uint4(nothing, nothing, nothing, nothing);
+                        if ((u + tid) % kLoads < mine) v[u] = from[(u + tid) % kLoads];
+                    }
                 }
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) all = top_of<T>(v[u], all);
@@ -415,7 +419,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         sorted[warp][lane] = key;
         if (tid == 0) {
             least = 0;
-            todos = 0;
+            todos = listed = 0;
         }
         if (!ptx::named_barrier_and(1, kThreads, landed)) break;
         if (key && lane < p.best) {
@@ -438,86 +442,101 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         int leads = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) leads += __popc(__ballot_sync(0xFFFFFFFFu, sorted[w][lane] >= max(least, (uint64_t)1)));
-        const uint32_t floor_value = (uint32_t)(least >> 32);
-        uint64_t floor = 0;                   // of whole keys, once a list has been cut
-        int *count = &listed[turn & 1];
-        auto enlist = [&](float x, unsigned token) {
+        const uint64_t lowest = least;
+        const uint32_t lowest_value = (uint32_t)(lowest >> 32);
+        const float lowest_logit = lowest ? logit_of(lowest) : -INFINITY;
+        uint64_t floor = 0;                   // of keys, once there were too many
+        // behind: of a unit whose place is behind that of the least maximum, where only what is greater than it counts
+        auto enlist = [&](float x, unsigned token, bool behind) {
+            if (!(x > -INFINITY)) return;
             const uint64_t k = key_of(x, token);
-            if (x > -INFINITY && (uint32_t)(k >> 32) >= floor_value && k >= floor) keys[atomicAdd(count, 1)] = k;
+            const uint32_t value = (uint32_t)(k >> 32);
+            if (value < lowest_value || (behind && value == lowest_value) || k < floor) return;
+            // past the room each takes the place of another with the chance that all have: a sample of them
+            const unsigned at = atomicAdd(&listed, 1);
+            const unsigned slot = at < kRoom ? at : __umulhi(at * 2654435761u, at);
+            if (slot < kRoom) keys[slot] = k;
         };
-        enlist(single, single_token);
-        for (int g0 = j0; g0 < j1; g0 += kKnown) {
-            // the units -- chunk g0 + e / leads of thread who[e % leads] -- whose maximum is great enough
-            const int units = leads * min(kKnown, j1 - g0);
-            if (g0 > j0) {
-                if (tid == 0) todos = 0;
+        while (true) {
+            enlist(single, single_token, false);
+            for (int g0 = j0; g0 < j1; g0 += kKnown) {
+                // the units -- chunk j of a leading thread -- whose maximum is great enough
+                const int units = leads * min(kKnown, j1 - g0);
+                if (g0 > j0 || floor) {
+                    ptx::named_barrier(1, kThreads);
+                    if (tid == 0) todos = 0;
+                    ptx::named_barrier(1, kThreads);
+                }
+                for (int e = tid; e < units; e += kThreads) {
+                    const int j = e / leads, l = who[e - j * leads];
+                    if (g0 > j0 || highs[j][l] >= lowest_value >> 16) todo[atomicAdd(&todos, 1)] = (uint16_t)(j * kThreads + l);
+                }
                 ptx::named_barrier(1, kThreads);
-            }
-            for (int e = tid; e < units; e += kThreads)
-                if (g0 > j0 || highs[e / leads][who[e % leads]] >= floor_value >> 16) todo[atomicAdd(&todos, 1)] = (uint16_t)e;
-            ptx::named_barrier(1, kThreads);
-            // their elements, a lane each
-            const int all = todos;
-            for (int i0 = 0; i0 < all; i0 += kRound) {
-                for (int i = i0 + warp * kAtOnce; i < min(i0 + kRound, all); i += kWarps * kAtOnce) {
-                    constexpr int kLane = kUnit / 32;              // elements of a lane
-                    float x[kAtOnce][kLane];
-                    int element[kAtOnce];
-                    bool behind[kAtOnce];
+                // Their pieces, kAtOnce of a thread under way. Few have an element that will do: those are taken
+                // once more, from L1, so that what follows is there once
+                const int pieces = todos * p.own;
+                auto piece_of = [&](int e, bool &behind) {
+                    if (e >= pieces) return -1;
+                    const int unit = todo[e / p.own], j = g0 + unit / kThreads, l = unit % kThreads;
+                    const int at = l * p.own + e % p.own, i = row.whole + j * p.chunk + at;
+                    behind = ((uint64_t)lowest_value << 32 | (0xFFFFFFFFu - (unsigned)((j - j0) * kThreads + l))) < lowest;
+                    return at < p.chunk && i < row.end ? i : -1;
+                };
+                for (int e0 = tid; e0 < pieces; e0 += kThreads * kAtOnce) {
+                    uint4 v[kAtOnce];
+                    bool behind;
 #pragma unroll
                     for (int u = 0; u < kAtOnce; ++u) {
-                        const int e = todo[min(i + u, all - 1)], j = g0 + e / leads, l = who[e % leads];
-                        const int piece = row.whole + j * kChunk + l * kLoads;
-                        element[u] = (int)row.token(piece) + lane;
-                        // equal to the least maximum: only up to its place, so that lists stay short
-                        behind[u] = ((uint64_t)floor_value << 32 | (0xFFFFFFFFu - (unsigned)((j - j0) * kThreads + l))) < least;
-#pragma unroll
-                        for (int k = 0; k < kLane; ++k) {
-                            x[u][k] = -INFINITY;
-                            if (i + u < all && piece + (lane + 32 * k) / kEach < row.end) x[u][k] = one(row.row + element[u] + 32 * k);
-                        }
+                        const int i = piece_of(e0 + u * kThreads, behind);
+                        v[u] = i >= 0 ? row.pieces[i] : make_uint4(nothing, nothing, nothing, nothing);
                     }
+                    unsigned good = 0;
 #pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        float x[kEach];
+                        widen<T>(v[u], x);
 #pragma unroll
-                        for (int k = 0; k < kLane; ++k)
-                            if (x[u][k] > -INFINITY && (!behind[u] || (uint32_t)(key_of(x[u][k], 0) >> 32) > floor_value))
-                                enlist(x[u][k], element[u] + 32 * k);
-                }
-                if (i0 + kRound >= all && g0 + kKnown >= j1) break;
-                ptx::named_barrier(1, kThreads);
-                const int have = *count;
-                ptx::named_barrier(1, kThreads);
-                if (have > kMostBest) {               // room for the next round
-                    if (warp == 0) {
-                        warp_best(keys, have, p.best, leaders);
-                        for (int k = lane; k < p.best; k += 32) keys[k] = leaders[k];
-                        if (lane == 0) *count = p.best;
+                        for (int k = 0; k < kEach; ++k) good |= (x[k] >= lowest_logit ? 1u : 0u) << (u * kEach + k);
                     }
-                    ptx::named_barrier(1, kThreads);
-                    floor = keys[p.best - 1];
+#pragma unroll 1
+                    for (; good; good &= good - 1) {
+                        const int bit = __ffs(good) - 1, i = piece_of(e0 + bit / kEach * kThreads, behind);
+                        const unsigned token = row.token(i) + bit % kEach;
+                        if (i >= 0) enlist(one(row.row + token), token, behind);
+                    }
                 }
             }
+            ptx::named_barrier(1, kThreads);
+            const int have = listed;
+            if (have <= kRoom) break;
+            // too many: `best` at least reach the sample's number `best`, and few more; once more with those
+            ptx::named_barrier(1, kThreads);
+            if (warp == 0) {
+                warp_best(keys, kRoom, p.best, leaders);
+                if (lane == 0) listed = 0;
+            }
+            ptx::named_barrier(1, kThreads);
+            floor = leaders[p.best - 1];
         }
-        ptx::named_barrier(1, kThreads);
-        const int have = *count;
-        const int64_t slot = blockIdx.x + r;
-        if (tid == 0) listed[turn & 1 ^ 1] = 0;
         // ---- the best of them in order
-        uint64_t *list = p.lists + slot * p.best;
-        if (have <= kThreads) {
-            if (tid < have) {
-                const uint64_t k = keys[tid];
-                int rank = 0;
-                for (int i = 0; i < have; ++i) rank += keys[i] > k;
-                if (rank < p.best) list[rank] = k;
-            }
-            for (int k = have + tid; k < p.best; k += kThreads) list[k] = 0;
-        } else if (warp == 0) {
-            warp_best(keys, have, p.best, leaders);
-            for (int k = lane; k < p.best; k += 32) list[k] = leaders[k];
+        const int have = listed;
+        uint64_t *list = p.lists + (blockIdx.x + r) * p.best;
+        uint64_t mine[kRoom / kThreads];
+        int place[kRoom / kThreads] = {};
+#pragma unroll
+        for (int u = 0; u < kRoom / kThreads; ++u) mine[u] = tid + u * kThreads < have ? keys[tid + u * kThreads] : ~(uint64_t)0;
+#pragma unroll 4
+        for (int i = 0; i < have; ++i) {
+            const uint64_t other = keys[i];
+#pragma unroll
+            for (int u = 0; u < kRoom / kThreads; ++u)
+                if (u == 0 || have > u * kThreads) place[u] += other > mine[u];
         }
-        ++turn;
+#pragma unroll
+        for (int u = 0; u < kRoom / kThreads; ++u)
+            if (tid + u * kThreads < have && place[u] < p.best) list[place[u]] = mine[u];
+        for (int k = have + tid; k < p.best; k += kThreads) list[k] = 0;
+        ptx::named_barrier(1, kThreads);
     }
 }
 
@@ -571,14 +590,14 @@ __device__ __forceinline__ uint64_t order_of(Sum s)
 __global__ void __launch_bounds__(32 * kMostBeams)
 beam_merge_kernel(const __grid_constant__ BeamParams p)
 {
-    extern __shared__ uint64_t merge_smem[];
+    extern __shared__ __align__(16) uint64_t merge_smem[];
     __shared__ Sum lses[kMostBeams];                     // of the rows that have candidates
     __shared__ float befores[kMostBeams];
     __shared__ bool sound[kMostBeams];
     __shared__ int first_list[kMostBeams], last_list[kMostBeams], end_tokens[kMostEnds];
     __shared__ uint8_t row_of_list[kMergeLists];
-    __shared__ __align__(16) float heads[kMergeLists];
-    __shared__ float floor;
+    __shared__ int stopping[kMergeLists];                // of a list's candidates: how many end
+    __shared__ uint32_t floor_order;
     __shared__ int ending_at[kMostEnding], picked, endings, told;
     const int beams = (int)p.a.beams, best = p.best, keep = (int)p.a.num_beams, threads = blockDim.x;
     const int ends = (int)p.a.num_ends;
@@ -593,14 +612,18 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
     }
     if (tid == 0) {
         picked = endings = told = 0;
-        floor = -INFINITY;
+        floor_order = 0;
     }
     // a number that no part has, where a row and a CTA's share end together
-    for (int l = tid; l < p.merge_lists; l += threads) row_of_list[l] = kNoRow;
+    for (int l = tid; l < p.merge_lists; l += threads) {
+        row_of_list[l] = kNoRow;
+        stopping[l] = 0;
+    }
     __syncthreads();
     const int lists = last_list[beams - 1] + 1, candidates = lists * best;
-    // picks: those that end, and behind them what reaches `floor`
-    uint64_t *keys = merge_smem, *picks = keys + p.merge_lists * best;
+    // picks: those that end, and behind them what reaches `floor`: score, and what goes before at equal scores
+    uint64_t *keys = merge_smem;
+    ulonglong2 *picks = reinterpret_cast<ulonglong2 *>(keys + (p.merge_lists * best + 1) / 2 * 2);
     int *pick_at = reinterpret_cast<int *>(picks + p.merge_lists * best);
     float *highs = reinterpret_cast<float *>(pick_at + p.merge_lists * best);
     if (warp < beams)
@@ -689,75 +712,90 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
         const float s = near(key, w, off);
         if (!stops) {
             highs[c] = s + off;
-        } else if (const int i = atomicAdd(&endings, 1); i < kMostEnding) {
-            ending_at[i] = c;
+        } else {
+            atomicAdd(&stopping[c / best], 1);
+            if (const int i = atomicAdd(&endings, 1); i < kMostEnding) ending_at[i] = c;
         }
     }
     __syncthreads();
 
     // ---- The first `keep` reach `floor`: with a list's candidate number q (from 0, of those that go on) each
-    // list has q + 1 that are as good, so that where ceil(keep / (q + 1)) lists' reach it, `keep` do
-    const int q = (keep - 1) / lists, wanted = (keep + q) / (q + 1);
-    for (int l = tid; l < (lists + 3) / 4 * 4; l += threads) {
+    // list has q + 1 that are as good, so that where ceil(keep / (q + 1)) lists' reach it, `keep` do. Which q gives
+    // the highest floor hangs on how unlike the lists are: several are tried
+    float *heads = reinterpret_cast<float *>(picks);               // [tries][wide]
+    const int least_q = (keep - 1) / lists, wide = (lists + 3) / 4 * 4;
+    auto q_of = [&](int k) { return k == 0 ? least_q : (2 << k) - 1; };             // least_q, 3, 7, 15
+    int tries = 1;
+    while (tries < 4 && q_of(tries) < keep && 4 * (tries + 1) * wide <= 16 * candidates) ++tries;
+    for (int i = tid; i < tries * wide; i += threads) {
+        const int k = i / wide, l = i - k * wide;
         float head = -INFINITY;
-        for (int i = 0, live = 0; l < lists && i < best; ++i)
-            if (!isnan(highs[l * best + i]) && live++ == q) {
+        if (l < lists) {
+            const int at = q_of(k) + stopping[l], w = row_of_list[l];
+            const uint64_t key = at < best && w != kNoRow && sound[w] ? keys[l * best + at] : 0;
+            if (key) {
                 float off;
-                near(keys[l * best + i], row_of_list[l], off);
-                head = highs[l * best + i] - 3.f * off;
-                break;
+                const float s = near(key, w, off);
+                head = s - 2.f * off;
             }
-        heads[l] = head;
-    }
-    __syncthreads();
-    for (int l = tid; l < lists; l += threads) {
-        const float head = heads[l];
-        int rank = 0;
-#pragma unroll 1
-        for (int i = 0; i < lists; i += 4) {
-            const float4 h = *reinterpret_cast<const float4 *>(heads + i);
-            rank += (h.x > head || (h.x == head && i < l)) + (h.y > head || (h.y == head && i + 1 < l)) +
-                    (h.z > head || (h.z == head && i + 2 < l)) + (h.w > head || (h.w == head && i + 3 < l));
         }
-        if (rank == wanted - 1) floor = head;
+        heads[i] = head;
     }
     __syncthreads();
+    for (int i = tid; i < tries * wide; i += threads) {
+        const int k = i / wide, l = i - k * wide;
+        const float head = heads[i];
+        int rank = 0;
+#pragma unroll 2
+        for (int j = 0; j < lists; j += 4) {
+            const float4 h = *reinterpret_cast<const float4 *>(heads + k * wide + j);
+            rank += (h.x > head || (h.x == head && j < l)) + (h.y > head || (h.y == head && j + 1 < l)) +
+                    (h.z > head || (h.z == head && j + 2 < l)) + (h.w > head || (h.w == head && j + 3 < l));
+        }
+        if (l < lists && rank == (keep + q_of(k)) / (q_of(k) + 1) - 1) atomicMax(&floor_order, (uint32_t)(key_of(head, 0) >> 32));
+    }
+    __syncthreads();
+    const float floor = floor_order ? logit_of((uint64_t)floor_order << 32) : -INFINITY;
     const int e = min(endings, kMostEnding);
     for (int c = tid; c < candidates + e; c += threads) {
         const bool stops = c >= candidates;
         if (!stops && !(highs[c] >= floor)) continue;
         const int i = stops ? c - candidates : e + atomicAdd(&picked, 1), at = stops ? ending_at[i] : c;
-        picks[i] = exact(at);
+        // equal scores: the lower row (of 32), the greater logit, the lower token (of 2^27)
+        picks[i] = make_ulonglong2(exact(at), (uint64_t)(31 - row_of_list[at / best]) << 59 | (keys[at] >> 32) << 27 |
+                                                  (keys[at] & 0x7FFFFFF));
         pick_at[i] = at;
     }
     __syncthreads();
 
-    // ---- in order: a candidate's place is the number of those before it, a warp a candidate. Equal scores go by
-    // row, then by logit and token
+    // ---- in order: a candidate's place is the number of those before it
     const int n = e + picked;
-    for (int i = warp; i < n; i += threads / 32) {
+    for (int i = tid; i < n; i += threads) {
         const bool stops = i < e;
-        const uint64_t s = picks[i];
-        const int c = pick_at[i];
-        int live = 0, gone = 0;
-#pragma unroll 1
-        for (int j0 = 0; j0 < n; j0 += 32) {
-            const int j = j0 + lane;
-            const uint64_t other = j < n ? picks[j] : 0;
-            bool before = other > s;
-            if (other == s && j != i) {
-                const int d = pick_at[j], rd = row_of_list[d / best], rc = row_of_list[c / best];
-                before = rd != rc ? rd < rc : keys[d] > keys[c];
+        const ulonglong2 mine = picks[i];
+        const uint64_t s = mine.x;
+        auto before = [&](int from, int to) {
+            int place = 0;
+#pragma unroll 4
+            for (int j = from; j < to; ++j) {
+                const ulonglong2 other = picks[j];
+                place += (int)(other.x > mine.x) | ((int)(other.x == mine.x) & (int)(other.y > mine.y));
             }
-            gone += __popc(__ballot_sync(0xFFFFFFFFu, before && j < e));
-            live += __popc(__ballot_sync(0xFFFFFFFFu, before && j >= e));
+            return place;
+        };
+        int place = before(e, n);
+        if (place >= keep) continue;
+        if (stops) {
+            const int gone = before(0, e);
+            if (place + gone >= keep) continue;
+            place = gone;
+            atomicAdd(&told, 1);
         }
-        if (live + (stops ? gone : 0) >= keep || lane > 0) continue;
-        const int64_t to = request * keep + (stops ? gone : live);
+        const int c = pick_at[i];
+        const int64_t to = request * keep + place;
         (stops ? p.a.ended_scores : p.a.out_scores)[to] = logit_of(s);
         (stops ? p.a.ended_parents : p.a.out_parents)[to] = (int)r0 + row_of_list[c / best];
         (stops ? p.a.ended_tokens : p.a.out_tokens)[to] = (int)token_of(keys[c]);
-        if (stops) atomicAdd(&told, 1);
     }
     // places without a candidate
     const bool tells = p.a.ended_scores != nullptr;
@@ -839,20 +877,24 @@ reorder_kernel(const __grid_constant__ StateParams p)
     }
 }
 
-constexpr size_t merge_bytes(int64_t keys) { return (2 * sizeof(uint64_t) + sizeof(int) + sizeof(float)) * keys; }
+constexpr size_t merge_bytes(int64_t keys) { return (3 * sizeof(uint64_t) + sizeof(int) + sizeof(float)) * keys + 8; }
 
 template <typename T>
 const void *rows_kernel() { return (const void *)beam_rows_kernel<T>; }
 
 } // namespace
 
-// The line of all rows' chunks, cut into equal parts for as many CTAs as the GPU holds, but of no more chunks
+// A row is cut into equal chunks. The line of all rows' chunks is cut into equal parts for as many CTAs as the GPU holds, but of no more chunks
 // than have their maxima kept; a row has at
 // most 32 stretches (a lane each in the merge), and a request's lists the room that they have there.
 BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
 {
     BeamCut c;
-    c.chunks = std::max<int64_t>(1, (vocab / (16 / element_bytes) + kChunk - 1) / kChunk);
+    const int64_t pieces = std::max<int64_t>(1, vocab / (16 / element_bytes));      // whole ones at most
+    c.chunks = (pieces + kChunk - 1) / kChunk;
+    c.chunk = (pieces + c.chunks - 1) / c.chunks;
+    // eight pieces a thread, while that gives more threads a part than there are best to be found
+    c.own = c.chunk >= kLoads * 64 ? kLoads : (c.chunk + kThreads - 1) / kThreads;
     const int64_t total = requests * beams * c.chunks;
     const int64_t lists = std::min<int64_t>(kMergeKeys / best, kMergeLists) - beams - 1;
     c.each = std::max({std::min<int64_t>((total + kPerSm * 152 - 1) / (kPerSm * 152), kKnown), (c.chunks + 30) / 31,
@@ -873,6 +915,8 @@ cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
     p.rows = a.requests * a.beams;
     const BeamCut c = beam_cut(a.requests, a.beams, a.vocab, p.best, a.dtype == AWQ_F32 ? 4 : 2);
     p.chunks = c.chunks;
+    p.chunk = (int)c.chunk;
+    p.own = (int)c.own;
     p.each = c.each;
     p.merge_lists = (int)c.merge_lists;
     p.lists = static_cast<uint64_t *>(a.workspace);
