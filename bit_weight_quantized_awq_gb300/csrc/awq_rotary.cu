@@ -13,11 +13,13 @@
 // cosines and sines are computed once for all of the CTA's heads, by all of its threads, and shared
 // through shared memory. Each thread asks for its first kItems pieces before that, so that their way in takes
 // no time of its own.
-// Measured: 16,383 tokens of 64 / 8 heads of 128 bf16 into a cache 110 us, 90 % of the copy bandwidth
+// Measured: 16,383 tokens of 64 / 8 heads of 128 bf16 into a cache 108 us, 92 % of the copy bandwidth
 // (torch's copy of as many dense bytes takes 106); 30,001 tokens of 16 / 4 heads of 96 with three axes
 // 48 us (a dense copy: 41); one token of 32 heads 4.3 us a call. With places of heads worked out item by
 // item the first took 152 us; with more tokens a CTA 121 (twice) and 125 (four times); with two items a thread and
-// five CTAs an SM 111. A shorter way to the angles (fp32 pairs, own series) changed nothing.
+// five CTAs an SM 111; with CTAs of only as many warps as have items 117, since the angles then take two turns. A
+// shorter way to the angles (fp32 pairs, own series) changed nothing; a thread with another frequency at each
+// angle cost 10 %.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -31,7 +33,6 @@ namespace awq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kItems = 4;          // of a thread under way
 constexpr int kCtas = 3;           // of an SM
 
 struct Side {                      // of q, k and v; strides in bytes
@@ -49,15 +50,19 @@ struct RotaryParams {
     int64_t tokens, slots;
     int num_axes, half, dim;
     int q_heads, turned_heads, heads;   // heads: with v's
-    // A head is `lanes` items, of which `turns` turn something. A CTA takes per_cta tokens, `abreast` at once, and
-    // part_heads of their heads: one of `parts`.
-    int lanes, turns, abreast, per_cta, parts, part_heads;
+    // A head is `items` items, of which `turns` turn something; `lanes` of them beside each other, `blocks` times.
+    // A CTA takes per_cta tokens, `abreast` at once, and part_heads blocks of their heads: one of `parts`.
+    int items, turns, lanes, blocks, abreast, per_cta, parts, part_heads;
     int shift;
 };
 
-// An item: kHalf: 8 elements and the 8 that lie rotary_dim / 2 further; kPairs: 4 neighbouring pairs; kSingle..:
-// one pair of either kind, for rotary_dim / 2 (or rotary_dim) that is no multiple of 8.
-enum Mode { kHalf, kPairs, kSingleHalf, kSinglePairs };
+// An item: kHalf: kWidth elements (8, 4, 2 or 1) and those that lie rotary_dim / 2 further; kPairs: kWidth
+// elements (8, 4 or 2), neighbouring pairs. As many as rotary_dim / 2, or rotary_dim, is a multiple of: with one pair
+// a thread and no loads ahead, 17 heads of 72 of which 36 turn took 80 us for 12,911 tokens, and take 18 in twos.
+enum Mode { kHalf, kPairs };
+
+template <int kMode, int kWidth>
+constexpr int kItems = kMode == kHalf ? std::min(16, 32 / kWidth) : std::min(16, 64 / kWidth);     // of a thread under way
 
 template <typename T>
 __device__ __forceinline__ float2 unpack(uint32_t v)
@@ -121,13 +126,39 @@ __device__ __forceinline__ void angles(const RotaryParams &p, int64_t t0, int to
     }
 }
 
-// Vectors of 16 bytes. A thread has one place in one head, of which all is looked up once, and goes through
-// the CTA's tokens, kItems of them under way.
-template <typename T, int kMode>
+template <int kWidth>
+struct Vector;
+template <> struct Vector<8> { using type = uint4; };
+template <> struct Vector<4> { using type = uint2; };
+template <> struct Vector<2> { using type = uint32_t; };
+template <> struct Vector<1> { using type = uint16_t; };
+
+// n angles, at a multiple of n (or of 4) from an aligned start.
+template <int n>
+__device__ __forceinline__ void take(const float *from, float (&x)[n])
+{
+#pragma unroll
+    for (int i = 0; i < n; i += n % 4 == 0 ? 4 : n % 2 == 0 ? 2 : 1) {
+        if constexpr (n % 4 == 0) {
+            const float4 v = *reinterpret_cast<const float4 *>(from + i);
+            x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+        } else if constexpr (n % 2 == 0) {
+            const float2 v = *reinterpret_cast<const float2 *>(from + i);
+            x[i] = v.x, x[i + 1] = v.y;
+        } else {
+            x[i] = from[i];
+        }
+    }
+}
+
+// A thread has one place in one head, of which all is looked up once, and goes through the CTA's tokens,
+// kItems of them under way.
+template <typename T, int kMode, int kWidth>
 __global__ void __launch_bounds__(kThreads, kCtas)
 rotary_kernel(const __grid_constant__ RotaryParams p)
 {
-    constexpr int kEach = kMode == kHalf ? 8 : 4;       // angles of an item
+    using V = typename Vector<kWidth>::type;
+    constexpr int kItems = awq::kItems<kMode, kWidth>, kBytes = 2 * kWidth, kEach = kMode == kHalf ? kWidth : kWidth / 2;
     extern __shared__ __align__(16) char rotary_smem[];
     float *cosine = reinterpret_cast<float *>(rotary_smem), *sine = cosine + p.per_cta * p.half;     // [per_cta][half]
     int64_t *slots = reinterpret_cast<int64_t *>(sine + p.per_cta * p.half);
@@ -136,29 +167,30 @@ rotary_kernel(const __grid_constant__ RotaryParams p)
 
     const int64_t group = blockIdx.x / p.parts, t0 = group * p.per_cta;
     const int tokens = (int)min((int64_t)p.per_cta, p.tokens - t0);
-    const int own = threadIdx.x / p.lanes, lane = threadIdx.x - own * p.lanes;
+    const int own = threadIdx.x / p.lanes;
     const int beside = own / p.part_heads;              // which of the tokens abreast
-    const int h = (int)(blockIdx.x - group * p.parts) * p.part_heads + own - beside * p.part_heads;
-    const bool works = beside < p.abreast && h < p.heads;
+    const int block = (int)(blockIdx.x - group * p.parts) * p.part_heads + own - beside * p.part_heads;
+    const int h = block / p.blocks, lane = (block - h * p.blocks) * p.lanes + threadIdx.x - own * p.lanes;
+    const bool works = beside < p.abreast && h < p.heads && lane < p.items;
     const bool v = h >= p.turned_heads, turns = !v && lane < p.turns;
     const int side = v ? 2 : h >= p.q_heads, number = h - (v ? p.turned_heads : h >= p.q_heads ? p.q_heads : 0);
-    // the item's first 16 bytes in the head, and how far the second are; 0: none
-    int at = 16 * lane, more = 0;
+    // the item's first elements in the head, in bytes, and how far the second are; 0: none
+    int at = kBytes * lane, more = 0;
     if (kMode == kHalf) {
         if (turns) {
             more = 2 * p.half;
         } else if (v) {
-            more = at + 16 * p.lanes < 2 * p.dim ? 16 * p.lanes : 0;
+            more = at + kBytes * p.items < 2 * p.dim ? kBytes * p.items : 0;
         } else {
-            at = 4 * p.half + 32 * (lane - p.turns);
-            more = at + 16 < 2 * p.dim ? 16 : 0;
+            at = 4 * p.half + 2 * kBytes * (lane - p.turns);
+            more = at + kBytes < 2 * p.dim ? kBytes : 0;
         }
     }
     const int64_t src_token = p.side[side].src_token, dst_token = p.side[side].dst_token, dst_block = p.side[side].dst_block;
     const char *src = p.side[side].src + t0 * src_token + number * p.side[side].src_head + at;
     char *dst = p.side[side].dst + (dst_block ? 0 : t0 * dst_token) + number * p.side[side].dst_head + at;
 
-    uint4 a[kItems], b[kItems];
+    V a[kItems], b[kItems];
     const int step = p.abreast * kItems, end = works ? tokens : 0;
     auto load = [&](int t1) {
 #pragma unroll
@@ -167,8 +199,8 @@ rotary_kernel(const __grid_constant__ RotaryParams p)
             if (t >= end) continue;
             // not a read-only load: this kernel may be resident while the one before writes q, k and v
             const char *from = src + t * src_token;
-            a[u] = *reinterpret_cast<const uint4 *>(from);
-            if (kMode == kHalf && more) b[u] = *reinterpret_cast<const uint4 *>(from + more);
+            a[u] = *reinterpret_cast<const V *>(from);
+            if (kMode == kHalf && more) b[u] = *reinterpret_cast<const V *>(from + more);
         }
     };
     load(beside);
@@ -189,87 +221,47 @@ rotary_kernel(const __grid_constant__ RotaryParams p)
                 to += t * dst_token;
             }
             if (turns) {
-                uint32_t *va = &a[u].x, *vb = &b[u].x;
-                const float4 *c = reinterpret_cast<const float4 *>(cosine + t * p.half + kEach * lane);
-                const float4 *d = reinterpret_cast<const float4 *>(sine + t * p.half + kEach * lane);
+                float c[kEach], d[kEach];
+                take(cosine + t * p.half + kEach * lane, c);
+                take(sine + t * p.half + kEach * lane, d);
+                if constexpr (kWidth == 1) {
+                    float2 x = unpack<T>(a[u] | (uint32_t)b[u] << 16);
+                    turn(x.x, x.y, c[0], d[0]);
+                    const uint32_t y = pack<T>(x.x, x.y);
+                    a[u] = (uint16_t)y;
+                    b[u] = (uint16_t)(y >> 16);
+                } else {
+                    uint32_t *va = reinterpret_cast<uint32_t *>(&a[u]), *vb = reinterpret_cast<uint32_t *>(&b[u]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float2 x = unpack<T>(va[q]);
-                    if (kMode == kHalf) {
-                        const float4 cc = c[q / 2], dd = d[q / 2];
-                        float2 y = unpack<T>(vb[q]);
-                        turn(x.x, y.x, q % 2 ? cc.z : cc.x, q % 2 ? dd.z : dd.x);
-                        turn(x.y, y.y, q % 2 ? cc.w : cc.y, q % 2 ? dd.w : dd.y);
-                        vb[q] = pack<T>(y.x, y.y);
-                    } else {
-                        const float4 cc = *c, dd = *d;
-                        turn(x.x, x.y, q == 0 ? cc.x : q == 1 ? cc.y : q == 2 ? cc.z : cc.w,
-                             q == 0 ? dd.x : q == 1 ? dd.y : q == 2 ? dd.z : dd.w);
+                    for (int q = 0; q < kWidth / 2; ++q) {
+                        float2 x = unpack<T>(va[q]);
+                        if constexpr (kMode == kHalf) {
+                            float2 y = unpack<T>(vb[q]);
+                            turn(x.x, y.x, c[2 * q], d[2 * q]);
+                            turn(x.y, y.y, c[2 * q + 1], d[2 * q + 1]);
+                            vb[q] = pack<T>(y.x, y.y);
+                        } else {
+                            turn(x.x, x.y, c[q], d[q]);
+                        }
+                        va[q] = pack<T>(x.x, x.y);
                     }
-                    va[q] = pack<T>(x.x, x.y);
                 }
             }
-            *reinterpret_cast<uint4 *>(to) = a[u];
-            if (kMode == kHalf && more) *reinterpret_cast<uint4 *>(to + more) = b[u];
+            *reinterpret_cast<V *>(to) = a[u];
+            if (kMode == kHalf && more) *reinterpret_cast<V *>(to + more) = b[u];
         }
-    }
-}
-
-// Single pairs and elements.
-template <typename T, int kMode>
-__global__ void __launch_bounds__(kThreads)
-rotary_single_kernel(const __grid_constant__ RotaryParams p)
-{
-    extern __shared__ __align__(16) char rotary_smem[];
-    float *cosine = reinterpret_cast<float *>(rotary_smem), *sine = cosine + p.per_cta * p.half;     // [per_cta][half]
-    int64_t *slots = reinterpret_cast<int64_t *>(sine + p.per_cta * p.half);
-    ptx::launch_dependents();
-    ptx::wait_prerequisites();
-
-    const int64_t group = blockIdx.x / p.parts, t0 = group * p.per_cta;
-    const int first = (int)(blockIdx.x - group * p.parts) * p.part_heads, heads = min(p.part_heads, p.heads - first);
-    const int tokens = (int)min((int64_t)p.per_cta, p.tokens - t0);
-    angles(p, t0, tokens, cosine, sine, slots);
-    __syncthreads();
-    for (int e = threadIdx.x; e < tokens * heads * p.lanes; e += kThreads) {
-        const int i = e / p.lanes, lane = e - i * p.lanes;
-        const int t = i / heads, h = first + i - t * heads;
-        const bool v = h >= p.turned_heads;
-        const Side &s = p.side[v ? 2 : h >= p.q_heads];
-        const int head = h - (v ? p.turned_heads : h >= p.q_heads ? p.q_heads : 0);
-        const uint16_t *from = reinterpret_cast<const uint16_t *>(s.src + (t0 + t) * s.src_token + head * s.src_head);
-        char *to = s.dst + head * s.dst_head;
-        if (s.dst_block) {
-            const int64_t slot = slots[t];
-            if (slot < 0) continue;
-            to += (slot >> p.shift) * s.dst_block + (slot & ((1 << p.shift) - 1)) * s.dst_token;
-        } else {
-            to += (t0 + t) * s.dst_token;
-        }
-        uint16_t *out = reinterpret_cast<uint16_t *>(to);
-        if (v || lane >= p.turns) {
-            // of v, which has more elements than another head has items, two each
-            for (int k = v ? lane : p.half + lane; k < p.dim; k += v ? p.lanes : p.dim) out[k] = from[k];
-            continue;
-        }
-        const int at = kMode == kSingleHalf ? lane : 2 * lane, other = kMode == kSingleHalf ? at + p.half : at + 1;
-        float2 x = unpack<T>(from[at] | (uint32_t)from[other] << 16);
-        turn(x.x, x.y, cosine[t * p.half + lane], sine[t * p.half + lane]);
-        const uint32_t y = pack<T>(x.x, x.y);
-        out[at] = (uint16_t)y;
-        out[other] = (uint16_t)(y >> 16);
     }
 }
 
 template <typename T>
-const void *kernel_of(int mode)
+const void *kernel_of(Mode mode, int width)
 {
-    switch (mode) {
-    case kHalf: return (const void *)rotary_kernel<T, kHalf>;
-    case kPairs: return (const void *)rotary_kernel<T, kPairs>;
-    case kSingleHalf: return (const void *)rotary_single_kernel<T, kSingleHalf>;
-    default: return (const void *)rotary_single_kernel<T, kSinglePairs>;
-    }
+    if (mode == kPairs)
+        return width == 8 ? (const void *)rotary_kernel<T, kPairs, 8>
+               : width == 4 ? (const void *)rotary_kernel<T, kPairs, 4> : (const void *)rotary_kernel<T, kPairs, 2>;
+    return width == 8 ? (const void *)rotary_kernel<T, kHalf, 8>
+           : width == 4 ? (const void *)rotary_kernel<T, kHalf, 4>
+           : width == 2 ? (const void *)rotary_kernel<T, kHalf, 2> : (const void *)rotary_kernel<T, kHalf, 1>;
 }
 
 } // namespace
@@ -305,30 +297,34 @@ cudaError_t launch_rotary(const awq_rotary_t &a, cudaStream_t stream)
     p.turned_heads = (int)(a.q_heads + a.kv_heads);
     p.heads = p.turned_heads + (append ? (int)a.kv_heads : 0);
     const int R = (int)a.rotary_dim, D = (int)a.head_dim;
-    int mode;
-    if (a.pairs ? R % 8 == 0 : R % 16 == 0) {
-        mode = a.pairs ? kPairs : kHalf;
-        p.turns = a.pairs ? R / 8 : R / 16;
-        p.lanes = a.pairs ? D / 8 : p.turns + ((D - R) / 8 + 1) / 2;
-    } else {
-        mode = a.pairs ? kSinglePairs : kSingleHalf;
-        p.turns = R / 2;
-        p.lanes = p.turns + (D - R);
+    const Mode mode = a.pairs ? kPairs : kHalf;
+    int width = 8;
+    while ((a.pairs ? R : R / 2) % width) width /= 2;
+    p.turns = a.pairs ? R / width : R / 2 / width;
+    p.items = a.pairs ? D / width : p.turns + ((D - R) / width + 1) / 2;
+    p.blocks = (p.items + kThreads - 1) / kThreads;
+    p.lanes = (p.items + p.blocks - 1) / p.blocks;
+    // The heads are shared out over CTAs, an item a thread, and few heads let several tokens go abreast. More
+    // parts than are needed can leave fewer threads idle, but each works out its tokens' angles, and two angles
+    // cost about what an item does: 16,383 x 80 heads of 128 take 107.6 us in 5 parts of 16 heads and 111 in 3 of 27;
+    // 10,361 x 40 of 64 22.0 in 2 and 24.0 in one.
+    const int at_once = kThreads / p.lanes, all = p.heads * p.blocks, items = std::min(16, (mode == kHalf ? 32 : 64) / width);
+    const int least = (all + at_once - 1) / at_once;
+    double best = 0;
+    for (int n = least; n <= std::min(all, 4 * least); ++n) {
+        const int heads = (all + n - 1) / n, abreast = at_once / heads;
+        const double score = (double)heads * abreast * all / (n * heads) / (1 + (double)n * p.half / (all * p.lanes));
+        if (score > best) best = score, p.parts = n, p.part_heads = heads, p.abreast = abreast;
     }
-    // the heads are shared out over CTAs, an item a thread, and few heads let several tokens go abreast
-    const int at_once = std::max(1, kThreads / p.lanes);
-    p.parts = (p.heads + at_once - 1) / at_once;
-    p.part_heads = (p.heads + p.parts - 1) / p.parts;
-    p.abreast = at_once / p.part_heads;
     // as many tokens for a CTA as keep all its threads at their angles and all its loads under way, but
     // not before there are kCtas CTAs an SM
-    const int busy = std::max((kThreads + p.half - 1) / p.half, p.abreast * kItems);
+    const int busy = std::max((kThreads + p.half - 1) / p.half, p.abreast * items);
     p.per_cta = (int)std::max<int64_t>(
         1, std::min<int64_t>({busy, (a.tokens * p.parts + kCtas * 152 - 1) / (kCtas * 152), 4096 / p.half}));
     const int64_t grid = (a.tokens + p.per_cta - 1) / p.per_cta * p.parts;
     const size_t smem = 8 * (size_t)p.per_cta * (p.half + 1);
     void *args[] = {&p};
-    const void *kernel = a.dtype == AWQ_F16 ? kernel_of<__half>(mode) : kernel_of<__nv_bfloat16>(mode);
+    const void *kernel = a.dtype == AWQ_F16 ? kernel_of<__half>(mode, width) : kernel_of<__nv_bfloat16>(mode, width);
     return launch_dependent(kernel, grid, kThreads, smem, stream, args);
 }
 

@@ -207,3 +207,20 @@ def test_statuses_of_the_library_become_its_error():
         kw = append_arguments()
         kw.update(k_cache=torch.zeros((2, 24, 2, 64), device="cuda", dtype=FP16), v_cache=torch.zeros((2, 24, 2, 64), device="cuda", dtype=FP16))
         awq.rotary_append(**kw)
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("R", [2, 6, 12, 14, 44, 60, 66, 128, 510, 1022])
+def test_turned_parts_of_any_size(pairs, R):
+    """Every width of a thread's item, heads of more items than a CTA has threads, into a cache."""
+    D, T, H, K = (-(-R // 8) * 8 if R < 500 else 1024), 37, 3, 2
+    qkv = torch.randn((T, H + 2 * K, D), device="cuda").half()
+    q, k, v = qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]
+    positions, f = torch.randint(0, 9000, (T,), device="cuda", dtype=torch.int32), frequencies(R // 2)
+    caches = [torch.zeros((5, 16, K, D), device="cuda", dtype=FP16) for _ in range(2)]
+    slots = torch.randperm(80, device="cuda")[:T]
+    got_q, got_k = awq.rotary(q, k, positions, f, pairs=pairs)
+    check(got_q, q, positions, f, pairs=pairs)
+    check(got_k, k, positions, f, pairs=pairs)
+    assert torch.equal(awq.rotary_append(q, k, v, positions, f, *caches, slots, pairs=pairs), got_q)
+    assert torch.equal(caches[0].flatten(0, 1)[slots], got_k) and torch.equal(caches[1].flatten(0, 1)[slots], v)
