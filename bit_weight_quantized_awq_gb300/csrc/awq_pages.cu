@@ -162,7 +162,7 @@ fork_kernel(const __grid_constant__ ForkProblem p, unsigned int *status)
 // Copies of pages, 16 bytes at a time, kCopyPieces of a thread under way. A unit is a
 // part of one page of one cache; the CTAs take units in turn, since how many there are is known
 // on the device only. Bound: HBM, each byte read and written once. For small copies (2 layers, pages of 16 KB: 2.4
-// us) and layouts without long runs; 24 layers of 48 x 8 beams took 189 us so, and 139 in bulk.
+// us) and layouts without long runs; 24 layers of 48 x 8 beams took 189 us so, and 130 in bulk.
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPieces = 8;
@@ -232,14 +232,18 @@ copy_pages_kernel(const __grid_constant__ CopyParams p)
     }
 }
 
-// The same by bulk copies (90 % of the copy bandwidth; 1.5 GB of moved pages 253 us, 284 by the
+// The same by bulk copies (92 % of the copy bandwidth; 1.5 GB of moved pages 258 us, 284 by the
 // kernel above), for pages whose tokens lie in long runs: through a ring in shared memory, kAhead
 // loads and as many stores under way, all issued by one lane. The 32 lanes of the CTA look up 32 parts at
-// a time.
-constexpr int kRunBytes = 16384;            // of a run at once
-constexpr int kRing = 6, kAhead = 3;
-constexpr int kBulkPerSm = 2;
-constexpr int64_t kLeastRun = 4096, kLeastBulk = 16 << 20;      // bytes of a run, and of all pages, from which on they are used
+// a time. (24 layers of 48 x 8 beams: 135 us; with 2 CTAs of twice the parts and ring 142. 8 tokens of 320 bytes
+// of pages of 32, 32 layers of 20 x 16 beams: 14.5 and 25; in parts of 4 KB 14, but long pages of few tokens 28 for 23.5.)
+constexpr int kRunBytes = 8192;             // of a run at once
+constexpr int kRing = 4, kAhead = 2;
+constexpr int kBulkPerSm = 6;
+// Bytes of a page that is one run, of a run of a head, and of all pages, from which on they are used. 16,000 pages of
+// 2 KB: 18 us, and 41 by threads; 128,000 runs of up to 2 KB, 8 to a page: 117 and 69 (1 GB in runs of 8 KB: 334 and
+// 370); 8.9 of 16 MB: 6.4 and 8.3.
+constexpr int64_t kLeastPage = 1024, kLeastRun = 4096, kLeastBulk = 2 << 20;
 
 __global__ void __launch_bounds__(32)
 copy_runs_kernel(const __grid_constant__ CopyParams p)
@@ -258,7 +262,9 @@ copy_runs_kernel(const __grid_constant__ CopyParams p)
     ptx::wait_prerequisites();
     int64_t pairs = p.pairs;
     if (p.count) pairs = min(pairs, (int64_t)max(*p.count, 0));
-    const int64_t each = (int64_t)p.caches * p.runs * p.parts, units = pairs * each;
+    // the parts of one number of all pages, then those of the next: where few tokens of each are copied, the
+    // later ones are empty
+    const int64_t each = (int64_t)p.caches * p.runs, units = pairs * each * p.parts;
     int64_t loads = 0, stores = 0;
     bool ok = true;
     auto store = [&] {
@@ -275,9 +281,9 @@ copy_runs_kernel(const __grid_constant__ CopyParams p)
         char *dst = nullptr;
         int bytes = 0;
         if (u < units) {
-            const int64_t n = u / each;
-            const int rest = (int)(u - n * each), part = rest % p.parts, run = rest / p.parts % p.runs;
-            const int cache = rest / p.parts / p.runs;
+            const int part = (int)(u / (pairs * each));
+            const int64_t within = u - part * (pairs * each), n = within / each;
+            const int rest = (int)(within - n * each), cache = rest / p.runs, run = rest - cache * p.runs;
             const int from = p.src[n], dest = p.dst[n];
             int tokens = p.tokens ? p.tokens[n] : p.block_size;
             if (tokens < 0 || tokens > p.block_size) {
@@ -643,7 +649,7 @@ cudaError_t launch_copy_pages(const CopyProblem &c, cudaStream_t stream)
         const bool whole = p.head == row && p.token == row * c.kv_heads;      // a page is one run
         p.runs = whole ? 1 : c.kv_heads;
         p.run_token = (int)(whole ? row * c.kv_heads : row);
-        const bool runs = (whole || p.token == row) && (int64_t)p.run_token * c.block_size >= kLeastRun &&
+        const bool runs = (whole ? page >= kLeastPage : p.token == row && row * c.block_size >= kLeastRun) &&
                           page * c.pairs * p.caches >= kLeastBulk;
 #ifdef AWQ_FAULT_TEST
         p.fault = fault_injection();

@@ -193,6 +193,24 @@ def test_many_bytes_go_in_bulk(kind, page, heads, dim):
         assert torch.equal(c, w)
 
 
+@pytest.mark.parametrize("kind", ["plain", "heads_first", "together"])
+@pytest.mark.parametrize("page,dim", [(16, 32), (16, 40), (16, 24), (64, 16)])
+def test_small_pages_in_bulk(kind, page, dim):
+    """Pages of one run from a KB on (and one below), of which few tokens are copied."""
+    blocks, n = 8000, 3500
+    rng = np.random.default_rng(dim)
+    caches = caches_of(kind, 3, blocks, page, 1, dim, FP16)
+    perm, tokens = rng.permutation(blocks), rng.integers(0, page + 1, n)
+    src, dst = perm[:n], perm[n:2 * n]
+    before = [c.clone() for c in caches]
+    awq.copy_pages(caches, i32(src), i32(dst), tokens=i32(tokens), count=i32([n - 100]))
+    s, d, t = (torch.from_numpy(x[:n - 100]).cuda().long() for x in (src, dst, tokens))
+    keep = (torch.arange(page, device="cuda")[None] >= t[:, None])[..., None, None]
+    for c, b in zip(caches, before):
+        b[d] = torch.where(keep, b[d], b[s])
+        assert torch.equal(c, b)
+
+
 def test_bad_pairs_are_skipped_and_reported():
     cache = torch.randn((4, 16, 1, 8), device="cuda").half()
     before = cache.clone()
