@@ -1,31 +1,35 @@
 // awq_beam.cu -- one step of beam search over the logits, and rows of other state by parent.
 //
-// beam_rows_kernel reads every logit once. The rows are a line of chunks of 1024 16-byte
-// pieces, cut into equal parts, one a CTA; a producer warp keeps a ring of bulk copies under way
-// across rows, so that HBM does not wait while a row's end is worked on. Each thread keeps the
+// beam_rows_kernel reads every logit once. The rows are cut into equal chunks of up to 1024
+// 16-byte pieces, and those shared out over the CTAs (beam_cut); a producer warp keeps a ring of bulk copies
+// under way across rows, so that HBM does not wait while a row's end is worked on. Each thread keeps the
 // maximum of what it has read. No list is kept while the logits stream by: the best K of a part
 // of a row can only lie with the K threads whose maxima are the greatest (each of them has an element
 // at least as great as the K-th greatest maximum, any other thread has none). Those
 // threads' pieces, where their chunks' maxima allow, are read a second time, from the L2 cache, and what
-// reaches the K-th greatest maximum is sorted out. Logits that are equal are told apart by
+// reaches the K-th greatest maximum is sorted out, by counting. Where that is more than there is room for, a sample of
+// it gives a better bound, and it is done again. Logits that are equal are told apart by
 // their place, so all keys differ, and how the data lie hardly matters to the time.
 //
 // The sum of exp(x - m) is taken for each chunk and warp by itself and added up in one order,
-// so that a row's log-sum-exp does not depend on where the line was cut: equal rows (at
+// so that a row's log-sum-exp does not depend on how the rows are shared out: equal rows (at
 // the same place within 16 bytes) have equal ones, and their beams tie as they should.
 //
 // beam_merge_kernel, a CTA a request, adds up a row's sums and takes the best of the lists of all its
-// rows' parts. Pairs of fp32 numbers stand for 64 bits, since fp64 runs at two operations a clock, and
-// are formed only for the few candidates that fp32 does not rule out.
+// rows' parts. A bound from the lists' candidates of several numbers leaves few that can be among the first;
+// their scores, as pairs of fp32 numbers, since fp64 runs at two operations a clock, decide.
 //
 // Bound: HBM, one read of the logits; one exponential a logit, and about seven instructions
 // around it, issued in 56 % of the cycles. Measured, with the reordering of token histories: 64 requests of 8
-// beams over 131,072 bf16 logits 40 us (rows 28.6, merge 7.7, histories 3.7; the read alone 20), 15 of 32
-// over 100,003 fp32 logits 54 us (37, 14, 3.3; 28), 4 beams over 32,000 17 us. On the way there: plain loads,
+// beams over 131,072 bf16 logits 38 us (rows 27.7, merge 6.4, histories 3.5; the read alone 20), 15 of 32
+// over 100,003 fp32 logits 50 us (36, 11, 3.2; 28), 4 beams over 32,000 16.5 us. On the way there: plain loads,
 // keys sorted by one warp, sums and merges in fp64 94 and 153 us; the ring and sorted maxima 62 and 103; four small CTAs an
 // SM instead of two, fp32 pairs in the merge 50 and 62; eight pieces a thread and packed fp32
-// instructions 46 and 57; logits that leave L2 before anything else, so that code and lists stay, 43 and 56 (replayed).
+// instructions 46 and 57; logits that leave L2 before anything else, so that code and lists stay, 43 and 56 (replayed);
+// equal chunks, several bounds in the merge 42 and 53; parts that end with rows 39.5 and 52.
 #include <algorithm>
+#include <cmath>
+#include <numeric>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,12 +53,12 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct BeamParams {
     awq_beam_select_t a;
     unsigned int *status;
-    // All rows as a line of chunks, `chunks` each, cut into `each` for a CTA. The part of a row that one CTA
-    // has is a stretch, number CTA + row: its best [best] are in the workspace, and the
+    // All rows as a line of chunks, in which a row takes `span` and has `chunks`, cut into `each` for a CTA. The part of
+    // a row that one CTA has is a stretch, number CTA + row: its best [best] are in the workspace, and the
     // maximum and sum of each chunk and warp.
     float2 *sums;
     uint64_t *lists;
-    int64_t rows, chunks, each;
+    int64_t rows, chunks, span, each;
     int chunk, own;                   // pieces of a chunk, and of a thread in it
     int best, merge_lists, fault;     // merge_lists: the most stretches of a request
 };
@@ -239,7 +243,7 @@ constexpr int kStage = kChunk / 2;            // pieces of a stage of the ring, 
 constexpr int kRoom = 512;            // keys of a part that the list of the best is taken from
 constexpr int kPerSm = 4;             // CTAs: while one sorts, the others read
 constexpr int kStages = 4;
-constexpr int kKnown = 24;            // chunks of a part whose threads' maxima are kept
+constexpr int kKnown = 48;            // chunks of a part whose threads' maxima are kept
 constexpr int kAtOnce = 4;            // pieces of a thread under way
 
 template <typename T>
@@ -266,7 +270,7 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
     ptx::launch_dependents();
     ptx::wait_prerequisites();
 
-    const int64_t begin = blockIdx.x * p.each, end = min(begin + p.each, p.rows * p.chunks);
+    const int64_t begin = blockIdx.x * p.each, end = min(begin + p.each, p.rows * p.span);
     auto row_of = [&](int64_t r) {
         return Row<T>(static_cast<const T *>(p.a.logits) + r * p.a.logits_row_stride, (int)p.a.vocab);
     };
@@ -278,9 +282,9 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
         const uint64_t policy = ptx::evict_first_policy();
         int64_t issued = 0;
         bool ok = true;
-        for (int64_t at = begin, r = begin / p.chunks; at < end && ok; ++r) {
-            const int j0 = (int)(at - r * p.chunks), j1 = (int)min(p.chunks, j0 + end - at);
-            at += j1 - j0;
+        for (int64_t at = begin, r = begin / p.span; at < end && ok; ++r) {
+            const int j0 = (int)(at - r * p.span), j1 = (int)min(p.chunks, j0 + end - at);
+            at = (r + 1) * p.span;
             // no beam: nobody looks at it
             if (p.a.scores[r] == -INFINITY) continue;
             const Row<T> row = row_of(r);
@@ -313,9 +317,9 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
     // ---------------------------------------------------------------- maxima, sums, lists
     constexpr uint32_t nothing = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
     int64_t used = 0;
-    for (int64_t at = begin, r = begin / p.chunks; at < end; ++r) {
-        const int j0 = (int)(at - r * p.chunks), j1 = (int)min(p.chunks, j0 + end - at);
-        at += j1 - j0;
+    for (int64_t at = begin, r = begin / p.span; at < end; ++r) {
+        const int j0 = (int)(at - r * p.span), j1 = (int)min(p.chunks, j0 + end - at);
+        at = (r + 1) * p.span;
         if (p.a.scores[r] == -INFINITY) continue;
         const Row<T> row = row_of(r);
         // what is not in whole pieces, one element a thread: the first chunk has the head, the last one the tail
@@ -604,9 +608,9 @@ beam_merge_kernel(const __grid_constant__ BeamParams p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t request = blockIdx.x, r0 = request * beams;
     // a row has one list in each CTA that had a part of it
-    const int64_t first = r0 * p.chunks / p.each + r0;
+    const int64_t first = r0 * p.span / p.each + r0;
     if (tid < beams) {
-        const int64_t begin = (r0 + tid) * p.chunks;
+        const int64_t begin = (r0 + tid) * p.span;
         first_list[tid] = (int)(begin / p.each + r0 + tid - first);
         last_list[tid] = (int)((begin + p.chunks - 1) / p.each + r0 + tid - first);
     }
@@ -884,9 +888,14 @@ const void *rows_kernel() { return (const void *)beam_rows_kernel<T>; }
 
 } // namespace
 
-// A row is cut into equal chunks. The line of all rows' chunks is cut into equal parts for as many CTAs as the GPU holds, but of no more chunks
-// than have their maxima kept; a row has at
-// most 32 stretches (a lane each in the merge), and a request's lists the room that they have there.
+// A row is cut into equal chunks of 16 KB at most, and all rows, as a line of chunks, into equal parts, one a CTA. What a
+// CTA takes is its start, its chunks, and the end of each part of a row, which sorts out its best. So where few CTAs
+// are left idle, parts end with their rows: several parts of each row, or several rows of each part, or a row a part
+// for more CTAs than run at once, which go on as others end. In chunks of 16 KB (1.3 us, when all CTAs read) an end costs
+// about 3 and the more the more are kept, a start 2. 38 x 7 rows of 151,927 bf16: 20.3 us in two parts each, 22.4 in
+// equal ones; 300 x 4 of 100,000: 44 in pairs, 61; 44 x 32 of 33,377, 40 kept: 36.7 one by one, 42.7.
+// A part has no more chunks of a row than have their maxima kept (it can, but is slow: what is read again is
+// not picked); a row has at most 32 parts (a lane each in the merge), and a request's lists the room that they have there.
 BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
 {
     BeamCut c;
@@ -895,12 +904,26 @@ BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, i
     c.chunk = (pieces + c.chunks - 1) / c.chunks;
     // eight pieces a thread, while that gives more threads a part than there are best to be found
     c.own = c.chunk >= kLoads * 64 ? kLoads : (c.chunk + kThreads - 1) / kThreads;
-    const int64_t total = requests * beams * c.chunks;
+    const int64_t rows = requests * beams, total = rows * c.chunks, most = kPerSm * 152;
     const int64_t lists = std::min<int64_t>(kMergeKeys / best, kMergeLists) - beams - 1;
-    c.each = std::max({std::min<int64_t>((total + kPerSm * 152 - 1) / (kPerSm * 152), kKnown), (c.chunks + 30) / 31,
-                       (beams * c.chunks + lists - 1) / lists, int64_t(1)});
-    c.ctas = (total + c.each - 1) / c.each;
-    c.merge_lists = beams * c.chunks / c.each + beams + 1;
+    double cost = INFINITY;
+    // `each` chunks a CTA, of a line in which a row takes `span`
+    auto consider = [&](int64_t each, int64_t span) {
+        const int64_t ctas = (rows * span + each - 1) / each;
+        const int64_t ends = (each + span - std::gcd(each, span) + span - 1) / span;
+        const double waves = ctas <= most ? 1 : std::max(2., (double)ctas / most + 0.3);
+        const double takes = waves * (std::min(each, total) + ends * (3 + best / 16.) + 2);
+        if (takes < cost) cost = takes, c.each = each, c.span = span, c.ctas = ctas;
+    };
+    const int64_t least = std::max({(c.chunks + 30) / 31, (beams * c.chunks + lists - 1) / lists, int64_t(1)});
+    for (int64_t n = std::min({c.chunks, lists / beams, int64_t(31)}); n > 0; --n) {
+        const int64_t each = (c.chunks + n - 1) / n;
+        if (each <= kKnown && (c.chunks + each - 1) / each == n) consider(each, n * each);
+    }
+    const int64_t equal = (total + most - 1) / most, whole = (rows + most - 1) / most;
+    consider(std::max(least, c.chunks <= kKnown ? equal : std::min<int64_t>(equal, kKnown)), c.chunks);
+    if (c.chunks <= kKnown) consider(whole * c.chunks, c.chunks);
+    c.merge_lists = beams * c.span / c.each + beams + 1;
     // 8-byte words of the workspace: best keys a stretch, maximum and sum of each chunk and warp
     c.words = (c.ctas + requests * beams) * best + total * kWarps;
     return c;
@@ -918,6 +941,7 @@ cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
     p.chunk = (int)c.chunk;
     p.own = (int)c.own;
     p.each = c.each;
+    p.span = c.span;
     p.merge_lists = (int)c.merge_lists;
     p.lists = static_cast<uint64_t *>(a.workspace);
     p.sums = reinterpret_cast<float2 *>(p.lists + (c.ctas + p.rows) * p.best);
@@ -933,7 +957,10 @@ cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream)
         e = allow_shared((const void *)beam_merge_kernel, merge_bytes(kMergeKeys));
     if (e == cudaSuccess) e = launch_dependent(kernel, c.ctas, kThreads + 32, ring, stream, args);
     if (e != cudaSuccess) return e;
-    return launch_dependent((const void *)beam_merge_kernel, a.requests, std::max(256, 32 * (int)a.beams),
+    // a thread a candidate, as far as that goes: 3 requests of 18 lists of 16 10 us, 13 by 256 threads
+    const int64_t candidates = c.merge_lists * p.best;
+    const int threads = (int)std::max({int64_t(256), 32 * a.beams, std::min<int64_t>(1024, (candidates + 31) / 32 * 32)});
+    return launch_dependent((const void *)beam_merge_kernel, a.requests, threads,
                             merge_bytes(c.merge_lists * p.best), stream, args);
 }
 

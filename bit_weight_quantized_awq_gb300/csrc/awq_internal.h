@@ -162,7 +162,7 @@ cudaError_t launch_rotary(const awq_rotary_t &a, cudaStream_t stream);
 
 // How beam_select's rows are shared out over CTAs, and its workspace in words of 8 bytes.
 struct BeamCut {
-    int64_t chunks, chunk, own, each, ctas, merge_lists, words;
+    int64_t chunks, chunk, own, span, each, ctas, merge_lists, words;
 };
 BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes);
 cudaError_t launch_beam_select(const awq_beam_select_t &a, cudaStream_t stream);

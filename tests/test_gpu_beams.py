@@ -111,9 +111,11 @@ def test_equal_scores_go_by_the_lower_row():
     logits = torch.randn((4, 5000), device="cuda").half()
     logits[1:] = logits[:1]
     step = awq.beam_select(logits, torch.full((1, 4), -3.0, device="cuda"), 10)
-    best = logits[0].float().topk(3).indices.tolist()
-    assert step.tokens[0].tolist() == [best[0]] * 4 + [best[1]] * 4 + [best[2]] * 2
-    assert step.parents[0].tolist() == [0, 1, 2, 3, 0, 1, 2, 3, 0, 1]
+    # tokens of one fp16 logit tie too: score, row, token
+    top = logits[0].float().sort(descending=True)
+    want = sorted((-x, r, t) for x, t in zip(top.values[:20].tolist(), top.indices[:20].tolist()) for r in range(4))[:10]
+    assert step.tokens[0].tolist() == [t for _, _, t in want]
+    assert step.parents[0].tolist() == [r for _, r, _ in want]
 
 
 @pytest.mark.parametrize("dtype", [FP16, BF16, FP32])
@@ -310,3 +312,29 @@ def test_reorder_states_refuses():
             with pytest.raises(TypeError):
                 awq.reorder_states(states, parents)
     assert issubclass(AWQError, RuntimeError)
+
+
+@pytest.mark.parametrize("R,W,V,keep,ends,dtype", [
+    (160, 2, 70000, 8, 0, BF16),      # two parts of each row, some with a chunk fewer
+    (5, 3, 290000, 16, 3, FP32),      # a chunk a part
+    (163, 4, 50001, 4, 1, BF16),      # two rows a part, the last part of one
+    (70, 10, 17003, 32, 8, FP16),     # a row a part, more parts than CTAs at once
+    (77, 8, 70003, 8, 0, BF16),       # parts that end within rows
+    (1, 2, 1_100_000, 32, 8, FP32),   # parts of many chunks
+])
+def test_ways_to_share_out_the_rows(R, W, V, keep, ends, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(R + V)
+    logits = torch.randn((R * W, V), generator=gen, device="cuda").to(dtype)
+    scores = -torch.rand((R, W), generator=gen, device="cuda")
+    end_tokens = torch.randperm(V, generator=gen, device="cuda")[:ends].int() if ends else None
+    step = awq.beam_select(logits, scores, keep, end_tokens)
+    x = logits.double()
+    s = (scores.double().reshape(-1, 1) + torch.log_softmax(x, 1)).reshape(R, W * V)
+    if ends:
+        s[:, (torch.arange(W, device="cuda")[:, None] * V + end_tokens[None]).flatten()] = -torch.inf
+    want = s.topk(keep).values
+    bound = (V / 256 + 64) * 2.0 ** -24 + 2.0 ** -24 * want.abs()        # of sums and scores, as in check
+    assert ((step.scores.double() - want).abs() <= bound).all()
+    at = step.parents.long() % W * V + step.tokens.long()
+    assert (torch.div(step.parents, W, rounding_mode="floor") == torch.arange(R, device="cuda")[:, None]).all()
+    assert ((s.gather(1, at) - want).abs() <= 2 * bound).all() and all(len(set(a)) == keep for a in at.tolist())
