@@ -907,22 +907,25 @@ BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, i
     const int64_t rows = requests * beams, total = rows * c.chunks, most = kPerSm * 152;
     const int64_t lists = std::min<int64_t>(kMergeKeys / best, kMergeLists) - beams - 1;
     double cost = INFINITY;
-    // `each` chunks a CTA, of a line in which a row takes `span`
-    auto consider = [&](int64_t each, int64_t span) {
+    // `each` chunks a CTA, of a line in which a row takes `span`; in how many parts of rows they end at most
+    auto consider = [&](int64_t each, int64_t span, int64_t ends) {
         const int64_t ctas = (rows * span + each - 1) / each;
-        const int64_t ends = (each + span - std::gcd(each, span) + span - 1) / span;
         const double waves = ctas <= most ? 1 : std::max(2., (double)ctas / most + 0.3);
         const double takes = waves * (std::min(each, total) + ends * (3 + best / 16.) + 2);
         if (takes < cost) cost = takes, c.each = each, c.span = span, c.ctas = ctas;
     };
     const int64_t least = std::max({(c.chunks + 30) / 31, (beams * c.chunks + lists - 1) / lists, int64_t(1)});
-    for (int64_t n = std::min({c.chunks, lists / beams, int64_t(31)}); n > 0; --n) {
+    // several parts of a row, as many as leave each a CTA
+    if (const int64_t n = std::min({c.chunks, lists / beams, int64_t(31), most / rows}); n > 1) {
         const int64_t each = (c.chunks + n - 1) / n;
-        if (each <= kKnown && (c.chunks + each - 1) / each == n) consider(each, n * each);
+        if (each <= kKnown) consider(each, (c.chunks + each - 1) / each * each, 1);
     }
-    const int64_t equal = (total + most - 1) / most, whole = (rows + most - 1) / most;
-    consider(std::max(least, c.chunks <= kKnown ? equal : std::min<int64_t>(equal, kKnown)), c.chunks);
-    if (c.chunks <= kKnown) consider(whole * c.chunks, c.chunks);
+    // one row, or several
+    const int64_t several = (rows + most - 1) / most;
+    for (int64_t n = 1; c.chunks <= kKnown && n <= several; n += std::max<int64_t>(1, several - 1)) consider(n * c.chunks, c.chunks, n);
+    // equal parts
+    const int64_t equal = (total + most - 1) / most, each = std::max(least, c.chunks <= kKnown ? equal : std::min<int64_t>(equal, kKnown));
+    consider(each, c.chunks, (each + 2 * c.chunks - std::gcd(each, c.chunks) - 1) / c.chunks);
     c.merge_lists = beams * c.span / c.each + beams + 1;
     // 8-byte words of the workspace: best keys a stretch, maximum and sum of each chunk and warp
     c.words = (c.ctas + requests * beams) * best + total * kWarps;

@@ -315,10 +315,10 @@ def test_reorder_states_refuses():
 
 
 @pytest.mark.parametrize("R,W,V,keep,ends,dtype", [
-    (160, 2, 70000, 8, 0, BF16),      # two parts of each row, some with a chunk fewer
+    (125, 2, 70000, 8, 0, BF16),      # two parts of each row, some with a chunk fewer
     (5, 3, 290000, 16, 3, FP32),      # a chunk a part
-    (163, 4, 50001, 4, 1, BF16),      # two rows a part, the last part of one
-    (70, 10, 17003, 32, 8, FP16),     # a row a part, more parts than CTAs at once
+    (143, 7, 50001, 4, 1, BF16),      # two rows a part, the last part of one
+    (44, 32, 33377, 32, 8, FP16),     # a row a part, more parts than CTAs at once
     (77, 8, 70003, 8, 0, BF16),       # parts that end within rows
     (1, 2, 1_100_000, 32, 8, FP32),   # parts of many chunks
 ])
