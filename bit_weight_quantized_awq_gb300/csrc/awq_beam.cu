@@ -922,9 +922,11 @@ BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, i
     }
     // one row, or several
     const int64_t several = (rows + most - 1) / most;
-    for (int64_t n = 1; c.chunks <= kKnown && n <= several; n += std::max<int64_t>(1, several - 1)) consider(n * c.chunks, c.chunks, n);
+    for (int64_t n = 1; c.chunks <= kKnown && n <= several; n += std::max<int64_t>(1, several - 1))
+        consider(n * c.chunks, c.chunks, n);
     // equal parts
-    const int64_t equal = (total + most - 1) / most, each = std::max(least, c.chunks <= kKnown ? equal : std::min<int64_t>(equal, kKnown));
+    const int64_t equal = (total + most - 1) / most;
+    const int64_t each = std::max(least, c.chunks <= kKnown ? equal : std::min<int64_t>(equal, kKnown));
     consider(each, c.chunks, (each + 2 * c.chunks - std::gcd(each, c.chunks) - 1) / c.chunks);
     c.merge_lists = beams * c.span / c.each + beams + 1;
     // 8-byte words of the workspace: best keys a stretch, maximum and sum of each chunk and warp

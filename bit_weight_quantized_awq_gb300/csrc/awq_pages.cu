@@ -371,31 +371,43 @@ clear_kernel(uint4 *words, int64_t n)
         words[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Calls f for every entry of the tables' pages and of `held` that is a block, shared out over `threads`
-// threads of which this is number `thread`, whole warps; reports those that are none.
+// Calls f(row, its pages, entry) for the tables' entries in eights: entry is the first, the next ones lie `apart`
+// further. Shared out over `threads` threads of which this is number `thread`, whole warps: neighbouring
+// lanes have neighbouring entries, 256 entries of a row a warp; but where there are more short rows than warps,
+// a row has no more lanes than it needs. (3,941 rows of a page, free blocks, replayed: 8 us, and 18 with a row a warp, as each
+// waits for 16 rows in turn; 80,000 rows: 18 and 228.)
+template <typename F>
+__device__ __forceinline__ void each_eight(const PagesProblem &p, int64_t thread, int64_t threads, unsigned &bad, F f)
+{
+    const int shift = __ffs(p.block_size) - 1, lane = threadIdx.x & 31;
+    const int parts = (p.width + 255) / 256;
+    int apart = 32, beside = 1;
+    while (apart > 1 && 4 * apart >= p.width && (int64_t)p.rows > threads / 32 * beside) apart /= 2, beside *= 2;
+    for (int64_t u0 = thread / 32 * beside; u0 < (int64_t)p.rows * parts; u0 += threads / 32 * beside) {
+        const int64_t u = u0 + lane / apart;
+        if (u >= (int64_t)p.rows * parts) continue;
+        const int r = (int)(u / parts), part = (int)(u - (int64_t)r * parts);
+        f(r, pages_of(p.lens[r], p.block_size, shift, p.width, bad), 256 * part + lane % apart, apart);
+    }
+}
+
+// Calls f for every entry of the tables' pages and of `held` that is a block; reports those that are none.
 template <typename F>
 __device__ __forceinline__ void each_used(const PagesProblem &p, int64_t thread, int64_t threads, unsigned &bad, F f)
 {
-    const int shift = __ffs(p.block_size) - 1, lane = threadIdx.x & 31;
     auto check = [&](int block) {
         if (block < 0 || block >= p.num_blocks) bad |= kStatusBadIndex;
         else f(block);
     };
-    // a warp a piece of 256 entries of a row
-    const int parts = (p.width + 255) / 256;
-    for (int64_t u = thread / 32; u < (int64_t)p.rows * parts; u += threads / 32) {
-        const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
-        const int have = pages_of(p.lens[r], p.block_size, shift, p.width, bad);
+    each_eight(p, thread, threads, bad, [&](int r, int have, int j0, int apart) {
         int v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int j = j0 + i * 32 + lane;
-            if (j < have) v[i] = p.table[r * p.stride + j];
-        }
+        for (int i = 0; i < 8; ++i)
+            if (j0 + i * apart < have) v[i] = p.table[r * p.stride + j0 + i * apart];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (j0 + i * 32 + lane < have) check(v[i]);
-    }
+            if (j0 + i * apart < have) check(v[i]);
+    });
     for (int64_t i = thread; i < p.num_held; i += threads)
         if (p.held[i] != -1) check(p.held[i]);
 }
@@ -404,21 +416,22 @@ __device__ __forceinline__ void each_used(const PagesProblem &p, int64_t thread,
 template <typename F>
 __device__ __forceinline__ void renumber(const PagesProblem &p, int64_t thread, int64_t threads, int first, F moved)
 {
-    const int shift = __ffs(p.block_size) - 1, lane = threadIdx.x & 31;
-    const int parts = (p.width + 255) / 256;
-    for (int64_t u = thread / 32; u < (int64_t)p.rows * parts; u += threads / 32) {
-        const int r = (int)(u / parts), j0 = (int)(u - (int64_t)r * parts) * 256;
-        unsigned ignored = 0;
-        const int have = pages_of(p.lens[r], p.block_size, shift, p.width, ignored);
+    unsigned ignored = 0;
+    each_eight(p, thread, threads, ignored, [&](int r, int have, int j0, int apart) {
+        int v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int j = j0 + i * 32 + lane;
-            if (j >= p.width) continue;
-            int b = j < have ? p.table[r * p.stride + j] : -1;
-            if (b >= p.num_blocks || b < 0) b = -1;
-            p.new_table[r * p.new_stride + j] = b >= first ? moved(b) : b;
+            const int j = j0 + i * apart;
+            v[i] = j < have ? p.table[r * p.stride + j] : -1;
+            if (v[i] >= p.num_blocks || v[i] < 0) v[i] = -1;
         }
-    }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (v[i] >= first) v[i] = moved(v[i]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (j0 + i * apart < p.width) p.new_table[r * p.new_stride + j0 + i * apart] = v[i];
+    });
 }
 
 // What block b's entry in the lists is: `rank` used blocks lie before it, `used` there are, of which the first

@@ -321,6 +321,7 @@ def test_reorder_states_refuses():
     (44, 32, 33377, 32, 8, FP16),     # a row a part, more parts than CTAs at once
     (77, 8, 70003, 8, 0, BF16),       # parts that end within rows
     (1, 2, 1_100_000, 32, 8, FP32),   # parts of many chunks
+    (1, 32, 1_600_000, 32, 8, BF16),  # of more than have their maxima kept
 ])
 def test_ways_to_share_out_the_rows(R, W, V, keep, ends, dtype):
     gen = torch.Generator(device="cuda").manual_seed(R + V)

@@ -255,6 +255,18 @@ def test_free_and_compact_match_the_reference(page, rows, longest, spare):
         check_pages(table, lens, page, blocks, held=np.append(free[:5], [-1, table[0, 0]]))
 
 
+@pytest.mark.parametrize("rows,width", [(255, 3), (257, 128), (300, 65), (700, 64), (5000, 33), (9000, 9), (20000, 8), (30001, 1)])
+def test_many_short_rows(rows, width):
+    """More rows than warps: several beside each other in one, of all widths that share it."""
+    rng = np.random.default_rng(rows)
+    have = rng.integers(0, width + 1, rows)
+    blocks = int(have.sum()) + 50
+    table = np.full((rows, width), -7)
+    table[np.arange(width)[None] < have[:, None]] = rng.permutation(blocks)[:have.sum()]
+    table[rows // 2], have[rows // 2] = table[0], have[0]               # shared
+    check_pages(table, np.maximum(0, have * 16 - 5), 16, blocks)
+
+
 def test_free_and_compact_at_the_ends():
     check_pages(np.zeros((0, 3), dtype=np.int64), [], 16, 100)                                  # no rows
     check_pages(np.full((2, 3), -1), [0, 0], 16, 1)                                             # nothing used
