@@ -898,6 +898,7 @@ const void *rows_kernel() { return (const void *)beam_rows_kernel<T>; }
 // not picked); a row has at most 32 parts (a lane each in the merge), and a request's lists the room that they have there.
 BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
 {
+    if (requests == 0) return {};
     BeamCut c;
     const int64_t pieces = std::max<int64_t>(1, vocab / (16 / element_bytes));      // whole ones at most
     c.chunks = (pieces + kChunk - 1) / kChunk;

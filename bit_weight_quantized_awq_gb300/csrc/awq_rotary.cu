@@ -311,7 +311,7 @@ cudaError_t launch_rotary(const awq_rotary_t &a, cudaStream_t stream)
     const int at_once = kThreads / p.lanes, all = p.heads * p.blocks, items = std::min(16, (mode == kHalf ? 32 : 64) / width);
     const int least = (all + at_once - 1) / at_once;
     double best = 0;
-    for (int n = least; n <= std::min(all, 4 * least); ++n) {
+    for (int n = least; n <= std::min({all, 4 * least, least + 8}); ++n) {
         const int heads = (all + n - 1) / n, abreast = at_once / heads;
         const double score = (double)heads * abreast * all / (n * heads) / (1 + (double)n * p.half / (all * p.lanes));
         if (score > best) best = score, p.parts = n, p.part_heads = heads, p.abreast = abreast;

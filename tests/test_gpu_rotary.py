@@ -224,3 +224,11 @@ def test_turned_parts_of_any_size(pairs, R):
     check(got_k, k, positions, f, pairs=pairs)
     assert torch.equal(awq.rotary_append(q, k, v, positions, f, *caches, slots, pairs=pairs), got_q)
     assert torch.equal(caches[0].flatten(0, 1)[slots], got_k) and torch.equal(caches[1].flatten(0, 1)[slots], v)
+
+
+@pytest.mark.parametrize("pairs,R", [(False, 4), (True, 4), (False, 8), (True, 2)])
+def test_a_million_tokens_of_one_small_head(pairs, R):
+    """A CTA has as many tokens as its shared memory holds angles of."""
+    q = torch.randn((1_000_003, 1, 8), device="cuda").half()
+    positions, f = torch.arange(1_000_003, device="cuda", dtype=torch.int32), frequencies(R // 2)
+    check(awq.rotary(q, None, positions, f, pairs=pairs)[0], q, positions, f, pairs=pairs)
