@@ -381,13 +381,12 @@ __device__ __forceinline__ void each_eight(const PagesProblem &p, int64_t thread
 {
     const int shift = __ffs(p.block_size) - 1, lane = threadIdx.x & 31;
     const int parts = (p.width + 255) / 256;
-    int apart = 32, beside = 1;
-    while (apart > 1 && 4 * apart >= p.width && (int64_t)p.rows > threads / 32 * beside) apart /= 2, beside *= 2;
-    for (int64_t u0 = thread / 32 * beside; u0 < (int64_t)p.rows * parts; u0 += threads / 32 * beside) {
-        const int64_t u = u0 + lane / apart;
-        if (u >= (int64_t)p.rows * parts) continue;
-        const int r = (int)(u / parts), part = (int)(u - (int64_t)r * parts);
-        f(r, pages_of(p.lens[r], p.block_size, shift, p.width, bad), 256 * part + lane % apart, apart);
+    int share = 5;                       // 2^share lanes a row
+    while (share > 0 && 4 << share >= p.width && (int64_t)p.rows > threads >> share) --share;
+    const int64_t units = (int64_t)p.rows * parts, beside = 32 >> share;
+    for (int64_t u = (thread / 32 * beside) + (lane >> share); u < units; u += threads / 32 * beside) {
+        const int r = (int)(parts == 1 ? u : u / parts), part = (int)(u - (int64_t)r * parts);
+        f(r, pages_of(p.lens[r], p.block_size, shift, p.width, bad), 256 * part + (lane & ((1 << share) - 1)), 1 << share);
     }
 }
 
