@@ -378,37 +378,36 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             if (j - j0 < kKnown) highs[j - j0][tid] = (uint16_t)(order >> 16);
             order = __reduce_max_sync(0xFFFFFFFFu, max(order, (uint32_t)(key_of(alone, 0) >> 32)));
             const float most = logit_of((uint64_t)order << 32), base = most > -INFINITY ? most : 0.f;
-            // 2^(x log2 e - shift), one FMA; what shift's own rounding did is put right below
-            const float shift = base * kLog2e;
-            const bool usual = fabsf(base) < 0x1p120f;       // else that product would leave fp32
-            uint64_t s0 = 0, s1 = 0;
-            float sum;
-            if (usual) {
-                const uint64_t scale = both(kLog2e, kLog2e), minus = both(-shift, -shift);
+            const uint64_t scale = both(kLog2e, kLog2e);
+            auto sum_of = [&](auto exponents) {
+                uint64_t s0 = 0, s1 = 0;
 #pragma unroll
                 for (int u = 0; u < kLoads; ++u) {
                     float x[kEach];
                     widen<T>(v[u], x);
 #pragma unroll
                     for (int k = 0; k < kEach; k += 2) {
-                        const float2 t = apart(fma2(both(x[k], x[k + 1]), scale, minus));
+                        const float2 t = apart(exponents(both(x[k], x[k + 1])));
                         const uint64_t e = both(power(t.x), power(t.y));
                         if (k & 2) s1 = add2(s1, e);
                         else s0 = add2(s0, e);
                     }
                 }
                 const float2 sums = apart(add2(s0, s1));
-                sum = sums.x + sums.y;
+                return sums.x + sums.y;
+            };
+            float sum;
+            if (fabsf(base) < 0x1p12f) {
+                // 2^(x log2 e - shift), one FMA. Shift's own rounding, d <= 2^-12, is put right to first order, which
+                // leaves (d ln 2)^2 / 2 < 2^-26
+                const float shift = base * kLog2e;
+                const uint64_t minus = both(-shift, -shift);
+                sum = sum_of([&](uint64_t x) { return fma2(x, scale, minus); });
                 sum = fmaf(sum, -kLn2 * fmaf(base, kLog2e, -shift), sum);
             } else {
-                sum = 0.f;
-#pragma unroll
-                for (int u = 0; u < kLoads; ++u) {
-                    float x[kEach];
-                    widen<T>(v[u], x);
-#pragma unroll
-                    for (int k = 0; k < kEach; ++k) sum += power((x[k] - base) * kLog2e);
-                }
+                // parts of which a mask leaves nothing, rows far from zero: there d would be anything up to infinity
+                const uint64_t minus = both(-base, -base);
+                sum = sum_of([&](uint64_t x) { return fma2(add2(x, minus), scale, 0); });
             }
             // a NaN stays one
             sum += power((alone - base) * kLog2e);
