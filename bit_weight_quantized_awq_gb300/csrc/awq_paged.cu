@@ -149,7 +149,8 @@ paged_plan_kernel(const PlanProblem p, unsigned int *status)
             if (block < 0) bad |= kStatusBadIndex;
         } else if (base[b] + page - have < (unsigned)p.num_free) {
             block = p.free_blocks[base[b] + page - have];
-            if (block < 0) bad |= kStatusBadIndex;
+            // -1 (free_pages' lists have it behind the last free block): none left
+            if (block < 0) bad |= block == -1 ? kStatusTooLarge : kStatusBadIndex;
         }
         p.slot_map[t] = block < 0 ? -1 : ((int64_t)block << shift) + ((ctx + i) & (p.block_size - 1));
         p.token_request[t] = b;

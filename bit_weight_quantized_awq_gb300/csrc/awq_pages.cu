@@ -107,14 +107,13 @@ fork_kernel(const __grid_constant__ ForkProblem p, unsigned int *status)
         bad |= kStatusBadIndex;
         start = 0;
     }
-    auto fresh = [&](int n) { return (int64_t)start + n < p.num_free ? max(p.free_blocks[start + n], -1) : -1; };
+    // -1 (free_pages' lists have it behind the last free block): none left
+    auto entry = [&](int n) { return (int64_t)start + n < p.num_free ? p.free_blocks[start + n] : -1; };
+    auto fresh = [&](int n) { return max(entry(n), -1); };
 
     // ---- what there is one of a row
     const int grid_threads = gridDim.x * kForkThreads;
-    if (blockIdx.x == 0 && tid == 0) {
-        *p.count = carry;
-        if ((int64_t)start + carry > p.num_free && carry > 0) bad |= kStatusTooLarge;
-    }
+    if (blockIdx.x == 0 && tid == 0) *p.count = carry;
     for (int r = blockIdx.x * kForkThreads + tid; r < p.rows_out; r += grid_threads) {
         const int parent = p.parents[r];
         const bool row = parent >= 0 && parent < p.rows_in;
@@ -123,8 +122,8 @@ fork_kernel(const __grid_constant__ ForkProblem p, unsigned int *status)
         p.new_lens[r] = max(length, 0);
         const int n = rank[r] >> 1;
         if (rank[r] & 1) {
-            const int to = fresh(n), from = p.table[parent * p.stride + (length >> shift)];
-            if (to < 0 && (int64_t)start + n < p.num_free) bad |= kStatusBadIndex;
+            const int free = entry(n), to = max(free, -1), from = p.table[parent * p.stride + (length >> shift)];
+            if (free < 0) bad |= free == -1 ? kStatusTooLarge : kStatusBadIndex;
             if (from < 0) bad |= kStatusBadIndex;
             p.src[n] = to < 0 ? -1 : from;
             p.dst[n] = to;

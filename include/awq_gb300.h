@@ -423,7 +423,8 @@ typedef enum { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 } awq_dtype_t;
  *   new_lens     int32 [B]  tokens this step adds                       (read)
  *   block_table  int32 [B, table_width], rows table_stride apart (read, written)
  *   free_blocks  int32 [num_free], taken from the start on (read; the caller
- *                drops counts[1] of them)
+ *                drops counts[1] of them); an entry of -1 is none (awq_free_pages has
+ *                them behind the last free block)
  *   parents      int32 [max_tokens] or NULL: the index within its request of each
  *                new token's parent, smaller than its own, or -1 for a child of
  *                the context's last token. NULL: each token follows the one before
@@ -435,7 +436,10 @@ typedef enum { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 } awq_dtype_t;
  * it when cu_new[B] > max_tokens: the tokens past it are dropped, or when a
  * request has more new tokens than its mask has bits).
  * A negative length counts as 0, a bad parent as -1, a negative table entry of
- * the context gives slot -1; each is reported as AWQ_ERR_INVALID_ARG.
+ * the context and a free block below -1 give slot -1; each is reported as AWQ_ERR_INVALID_ARG.
+ * Later calls of the step report the pages that are then missing in the table as
+ * AWQ_ERR_INVALID_ARG too, and the status word gives that one first: whether blocks ran out
+ * is told by counts[1] against awq_free_pages' counts[0].
  *
  * Requires 0 <= B <= 16384, block_size a power of two from 16 to 1024,
  * 0 <= max_tokens <= 2^30, table_stride >= table_width > 0, num_free >= 0,
@@ -734,10 +738,10 @@ awq_status_t awq_reorder_states(const awq_state_t *states, int64_t count, const 
  *                are taken already (awq_paged_plan's counts[1], say)
  *   new_table    int32 [rows_out, table_width], rows new_stride apart, does not overlap
  *                block_table; new_lens, src, dst, tokens int32 [rows_out]; count int32 [1]
- * Where free blocks run out, the row's last page and its src and dst get -1 and the device
- * status becomes AWQ_ERR_TOO_LARGE (so does it for a length beyond the table's width, which
- * counts as that width, all its pages full). A negative length counts as 0, a parent outside [-1, rows_in) as -1, a
- * negative *free_start as 0, each reported as AWQ_ERR_INVALID_ARG.
+ * Where free blocks run out -- at num_free, or at an entry of -1 --, the row's last page and its src
+ * and dst get -1 and the device status becomes AWQ_ERR_TOO_LARGE (so does it for a length beyond the table's width,
+ * which counts as that width, all its pages full). A negative length counts as 0, a parent outside [-1, rows_in)
+ * as -1, a negative *free_start as 0, a free block below -1 as -1, each reported as AWQ_ERR_INVALID_ARG.
  * Requires 0 <= rows_in, rows_out <= 16384, block_size a power of two from 16 to 1024,
  * table_stride and new_stride >= table_width, 0 < table_width <= 2^30, 0 <= num_free < 2^31.
  */
