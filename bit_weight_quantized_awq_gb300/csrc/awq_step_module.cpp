@@ -17,6 +17,7 @@
 #include <vector>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -187,8 +188,7 @@ int call(F entry)
     return status;
 }
 
-// One allocation of a call for all of its results and its workspace (six took 6 us of
-// 10), in words of 4 bytes.
+// One allocation of a call for all of its results (six took 6 us of 10), in words of 4 bytes.
 class Area {
 public:
     Area(int dev, int64_t words)
@@ -206,12 +206,15 @@ public:
         used_ += t.numel() * each;
         return t;
     }
-    char *data() { return static_cast<char *>(area_.data_ptr()); }
 
 private:
     Tensor area_;
     int64_t used_ = 0;
 };
+
+// A call's workspace, apart from its results: a caller that keeps those does not keep it. It is the current
+// stream's, as the call is, so that its memory serves the next one there; begins on 512 bytes.
+c10::DataPtr workspace_of(int64_t bytes) { return c10::cuda::CUDACachingAllocator::get()->allocate((size_t)bytes); }
 
 PyObject *keep(PyObject *o)
 {
@@ -569,10 +572,9 @@ PyObject *beam_select(PyObject *const *o)
     if (a.workspace_bytes < 0)
         refuse("beam_select takes up to 16384 requests, 1 to 32 beams and num_beams, up to 8 end_tokens and a vocabulary of 1 to 2^27");
     const int64_t n = a.requests * a.num_beams;
-    // the workspace first, which begins on 256 bytes as the allocation does
-    Area area(dev, a.workspace_bytes / 4 + (ends ? 6 : 3) * n);
-    a.workspace = area.data();
-    area.take(at::kInt, {a.workspace_bytes / 4});
+    const c10::DataPtr workspace = workspace_of(a.workspace_bytes);
+    a.workspace = workspace.get();
+    Area area(dev, (ends ? 6 : 3) * n);
     Tensor made[6];
     for (int i = 0; i < (ends ? 6 : 3); ++i) made[i] = area.take(i % 3 == 0 ? at::kFloat : at::kInt, {a.requests, a.num_beams});
     a.out_scores = data<float>(&made[0]);
@@ -778,14 +780,13 @@ Pages pages(PyObject *const *o)
 PyObject *free_pages(PyObject *const *o)
 {
     const Pages p = pages(o);
-    // the workspace first, which begins on 256 bytes as the allocation does
-    Area area(p.dev, p.workspace / 4 + p.num_blocks + 2);
-    area.take(at::kInt, {p.workspace / 4});
+    const c10::DataPtr workspace = workspace_of(p.workspace);
+    Area area(p.dev, p.num_blocks + 2);
     Tensor list = area.take(at::kInt, {p.num_blocks}), counts = area.take(at::kInt, {2});
     const awq_stream_t stream = stream_of(p.dev);
     const int status = call([&] {
         return free_entry(p.table, p.rows, p.width, p.stride, p.lens, p.block_size, p.num_blocks, p.held, p.num_held,
-                          data<int32_t>(&list), data<int32_t>(&counts), area.data(), stream);
+                          data<int32_t>(&list), data<int32_t>(&counts), workspace.get(), stream);
     });
     if (status != AWQ_OK) return PyLong_FromLong(status);
     return tuple_of(list, counts);
@@ -795,15 +796,15 @@ PyObject *compact_pages(PyObject *const *o)
 {
     const Pages p = pages(o);
     const int64_t half = p.num_blocks / 2;
-    Area area(p.dev, p.workspace / 4 + p.rows * p.width + p.num_blocks + 2 * half + 1);
-    area.take(at::kInt, {p.workspace / 4});
+    const c10::DataPtr workspace = workspace_of(p.workspace);
+    Area area(p.dev, p.rows * p.width + p.num_blocks + 2 * half + 1);
     Tensor table = area.take(at::kInt, {p.rows, p.width}), map = area.take(at::kInt, {p.num_blocks});
     Tensor src = area.take(at::kInt, {half}), dst = area.take(at::kInt, {half}), count = area.take(at::kInt, {1});
     const awq_stream_t stream = stream_of(p.dev);
     const int status = call([&] {
         return compact_entry(p.table, p.rows, p.width, p.stride, p.lens, p.block_size, p.num_blocks, p.held, p.num_held,
                              data<int32_t>(&table), p.width, data<int32_t>(&map), data<int32_t>(&src),
-                             data<int32_t>(&dst), data<int32_t>(&count), area.data(), stream);
+                             data<int32_t>(&dst), data<int32_t>(&count), workspace.get(), stream);
     });
     if (status != AWQ_OK) return PyLong_FromLong(status);
     return tuple_of(table, map, src, dst, count);
