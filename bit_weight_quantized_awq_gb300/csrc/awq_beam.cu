@@ -424,7 +424,17 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             least = 0;
             todos = listed = 0;
         }
-        if (!ptx::named_barrier_and(1, kThreads, landed)) break;
+        if (!ptx::named_barrier_and(1, kThreads, landed)) {
+            // A wait ran out. What the workspace holds for this row and the share's later ones is from earlier calls:
+            // empty lists, and sums that leave their rows without candidates
+            for (; r * p.span < end; ++r) {
+                for (int k = tid; k < p.best; k += kThreads) p.lists[(blockIdx.x + r) * p.best + k] = 0;
+                const int64_t first = max(begin - r * p.span, (int64_t)0), last = min(p.chunks, end - r * p.span);
+                for (int64_t i = (r * p.chunks + first) * kWarps + tid; i < (r * p.chunks + last) * kWarps; i += kThreads)
+                    p.sums[i] = make_float2(-INFINITY, NAN);
+            }
+            break;
+        }
         if (key && lane < p.best) {
             int rank = lane;
             int low[kWarps] = {};             // keys of warp w that are greater: found bit by bit

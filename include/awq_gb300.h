@@ -673,7 +673,8 @@ awq_status_t awq_rotary(const awq_rotary_t *args, awq_stream_t stream);
  *   workspace   awq_beam_select_workspace() bytes, 256-byte aligned, used until the
  *               call's work is done
  * A logit of -inf is no candidate. A row with a NaN or +inf among its logits, or with such a
- * score, has no candidates and is reported. beams and num_beams may differ (a prompt's
+ * score, has no candidates and is reported. Nor has a row whose logits a bounded wait
+ * gave up on (AWQ_ERR_TIMEOUT): parents and tokens are in range all the same. beams and num_beams may differ (a prompt's
  * single row gives the first beams).
  * Requires 0 <= requests <= 16384, 1 <= beams, num_beams <= 32, 0 <= num_ends <= 8,
  * 0 < vocab <= 2^27, logits aligned to its elements (AWQ_ERR_INVALID_ARG otherwise, and for

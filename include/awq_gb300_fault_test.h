@@ -16,7 +16,8 @@
  *   run out, record AWQ_ERR_TIMEOUT in the device status word, and the
  *   kernel returns. Other CTAs that wait for CTA 0's partial sums give up the
  *   same way. Nothing traps, faults or spins without a limit. The result of
- *   such a call is not defined; awq_last_device_status() then returns
+ *   such a call is not defined (but for awq_beam_select: the rows of which CTA 0 has a
+ *   part have no candidates); awq_last_device_status() then returns
  *   AWQ_ERR_TIMEOUT and resets the split-K counters. Host-side switch; takes
  *   effect at the next launch. No CUDA call.
  */
