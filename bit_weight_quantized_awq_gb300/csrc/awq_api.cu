@@ -666,7 +666,7 @@ awq_status_t awq_last_device_status(awq_stream_t stream)
 #ifdef AWQ_FAULT_TEST
 void awq_test_inject_fault(int on)
 {
-    awq::g_fault_injection.store(on ? 1 : 0, std::memory_order_release);
+    awq::g_fault_injection.store(on, std::memory_order_release);
 }
 #endif
 

@@ -302,15 +302,17 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
                     ++issued;
                     if (bytes == 0) continue;
 #ifdef AWQ_FAULT_TEST
-                    if (p.fault && blockIdx.x == 0) continue;
+                    if (p.fault == 1 && blockIdx.x == 0) continue;
 #endif
                     ptx::bulk_load(ptx::smem_addr(ring + s * kStage), row.pieces + i, bytes, ptx::smem_addr(full + s), policy);
                 }
             }
         }
-        // after a wait that ran out: the copies on their way land before the shared memory goes
-        for (int64_t i = max((int64_t)0, issued - kStages); i < issued && !ok; ++i)
-            ptx::mbar_wait_bounded(ptx::smem_addr(full + i % kStages), (i / kStages) & 1, nullptr, nullptr);
+        // The copies on their way land before the shared memory goes: the working warps may have given up on them (if
+        // not, they wait for the same stages). Those behind one that never lands have had as long
+        bool landed = true;
+        for (int64_t i = max((int64_t)0, issued - kStages); i < issued && landed; ++i)
+            landed = ptx::mbar_wait_bounded(ptx::smem_addr(full + i % kStages), (i / kStages) & 1, nullptr, nullptr);
         return;
     }
 
@@ -341,6 +343,12 @@ beam_rows_kernel(const __grid_constant__ BeamParams p)
             if (count > 0) {
                 const int64_t stage = 2 * used + tid / (kThreads / 2);
                 const int s = (int)(stage % kStages);
+#ifdef AWQ_FAULT_TEST
+                if (p.fault == 2 && blockIdx.x == 0) {
+                    raise_status(p.status, kStatusTimeout);
+                    landed = false;
+                }
+#endif
                 landed = landed && ptx::mbar_wait_bounded(ptx::smem_addr(full + s), (stage / kStages) & 1, nullptr, p.status);
                 if (!__all_sync(0xFFFFFFFFu, landed)) {
                     landed = false;

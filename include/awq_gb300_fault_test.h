@@ -20,6 +20,9 @@
  *   part have no candidates); awq_last_device_status() then returns
  *   AWQ_ERR_TIMEOUT and resets the split-K counters. Host-side switch; takes
  *   effect at the next launch. No CUDA call.
+ *
+ * awq_test_inject_fault(2) -- the same, but in awq_beam_select the copies of CTA 0 are issued
+ *   and its consumer warps give up on them at once: the copies land while the kernel ends.
  */
 #ifndef AWQ_GB300_FAULT_TEST_H
 #define AWQ_GB300_FAULT_TEST_H

@@ -87,3 +87,24 @@ def test_rows_whose_logits_do_not_come_have_no_candidates(flib, B, W, V, keep, d
     # requests that CTA 0 has no part of are as they should be
     for a, b in zip(failed, call.out):
         assert torch.equal(a[B // 2 + 1:], b[B // 2 + 1:])
+
+
+@pytest.mark.parametrize("B,W,V,keep,dtype", SIZES)
+def test_copies_land_before_a_row_that_was_given_up_ends(flib, B, W, V, keep, dtype):
+    """The working warps leave while copies are under way; the producer waits for those. Shares that fit the ring
+    and longer ones."""
+    call = Call(flib, B, W, V, keep, dtype)
+    call()
+    right = [t.clone() for t in call.out]
+    for _ in range(5):
+        call.space.fill_(STALE)
+        flib.awq_test_inject_fault(2)
+        try:
+            call()
+        finally:
+            flib.awq_test_inject_fault(0)
+        assert call.status() == Status.ERR_TIMEOUT
+        call.in_range()
+        assert not (call.out[1] == 0).any()
+        call()
+        assert call.status() == Status.OK and all(torch.equal(a, b) for a, b in zip(call.out, right))
