@@ -608,10 +608,31 @@ private:
     const char *name_;
 };
 
-// The bytes that a tensor of dense rows lies in.
+// The bytes that rows lie in: `rows` of `size`, `stride` apart.
 struct Bytes {
-    uintptr_t first, last;
+    uintptr_t first;
+    int64_t rows, stride, size;
+    uintptr_t last() const { return first + (rows - 1) * stride + size; }
 };
+
+// Whether rows of one share a byte with rows of the other, which may lie between them. Both have rows and bytes.
+bool overlap(const Bytes &a, const Bytes &b)
+{
+    if (a.last() <= b.first || b.last() <= a.first) return false;
+    if (a.stride < a.size || b.stride < b.size) return true;       // not rows one after the other
+    if (a.stride == b.stride) {
+        const int64_t off = (int64_t)(b.first - a.first) % a.stride, behind = off < 0 ? off + a.stride : off;
+        if (behind >= a.size && behind + b.size <= a.stride) return false;      // all of one in the other's gaps
+    }
+    // the rows of both in turn, past those that end before the other's begins
+    uintptr_t x = a.first, y = b.first;
+    while (x < a.last() && y < b.last()) {
+        if (x + a.size <= y) x += (y - x - a.size) / a.stride * a.stride + a.stride;
+        else if (y + b.size <= x) y += (x - y - b.size) / b.stride * b.stride + b.stride;
+        else return true;
+    }
+    return false;
+}
 
 // Rows [n, ...] whose elements lie together, as an address, a stride and a size in bytes.
 int64_t dense_row(const Tensor &t, const char *name)
@@ -668,14 +689,15 @@ PyObject *reorder_states(PyObject *const *o)
         a.dst = made[i].data_ptr();
         a.src_row_stride = rows_in > 1 ? s.stride(0) * size : a.row_bytes;
         a.dst_row_stride = rows > 1 ? made[i].stride(0) * size : a.row_bytes;
-        const uintptr_t src = reinterpret_cast<uintptr_t>(a.src), dst = reinterpret_cast<uintptr_t>(a.dst);
-        if (rows_in > 0 && a.row_bytes > 0) from.push_back({src, src + (rows_in - 1) * a.src_row_stride + a.row_bytes});
-        if (rows > 0 && a.row_bytes > 0) to.push_back({dst, dst + (rows - 1) * a.dst_row_stride + a.row_bytes});
+        if (rows_in > 0 && a.row_bytes > 0)
+            from.push_back({reinterpret_cast<uintptr_t>(a.src), rows_in, a.src_row_stride, a.row_bytes});
+        if (rows > 0 && a.row_bytes > 0)
+            to.push_back({reinterpret_cast<uintptr_t>(a.dst), rows, a.dst_row_stride, a.row_bytes});
     }
     if (given)
         for (const Bytes &x : to)
             for (const Bytes &y : from)
-                if (x.first < y.last && y.first < x.last) refuse("outs must not overlap states");
+                if (overlap(x, y)) refuse("outs must not overlap states");
     const awq_stream_t stream = stream_of(dev);
     const int status =
         call([&] { return reorder_entry(all.data(), n, data<int32_t>(&parents), rows, rows_in, stream); });

@@ -25,7 +25,7 @@ def i32(values):
 
 @pytest.mark.parametrize("from_,to", [
     (np.s_[:, 0], np.s_[:, 1]), (np.s_[:, 1], np.s_[:, 0]),          # beside each other in one allocation
-    (np.s_[:, 0, 3:], np.s_[:, 0, :3]),                              # parts of one row
+    (np.s_[:, 0, 4:], np.s_[:, 0, :3]),                              # parts of one row
     (np.s_[::2, 0], np.s_[1::2, 1]),                                 # rows that alternate
     (np.s_[:9:4, 0], np.s_[1:8:2, 0]), (np.s_[8::3, 1], np.s_[::2, 0]),  # of different strides
     (np.s_[:3], np.s_[3:])])
