@@ -77,7 +77,10 @@ const Tensor &tensor(PyObject *o, const char *name)
         PyErr_Format(PyExc_TypeError, "%s must be a tensor, got %s", name, Py_TYPE(o)->tp_name);
         throw Raised{};
     }
-    return THPVariable_Unpack(o);
+    const Tensor &t = THPVariable_Unpack(o);
+    // their memory holds something else than their elements
+    if (t.is_conj() || t.is_neg()) refuse("%s is conjugated or negated only when it is read: resolve_conj(), resolve_neg()", name);
+    return t;
 }
 
 const Tensor *tensor_or_none(PyObject *o, const char *name) { return o == Py_None ? nullptr : &tensor(o, name); }

@@ -52,3 +52,19 @@ def test_outputs_that_overlap_the_states_are_refused(from_, to):
         awq.reorder_states([torch.zeros((buf[from_].shape[0], 3), device="cuda"), buf[from_]],
                            torch.zeros(buf[to].shape[0], device="cuda", dtype=torch.int32),
                            outs=[torch.zeros((buf[to].shape[0], 3), device="cuda"), buf[to]])
+
+
+def test_views_that_are_conjugated_or_negated_are_refused():
+    z = torch.randn((4, 6), device="cuda", dtype=torch.complex64)
+    parents = i32([3, 0])
+    conjugate, negated = z.conj(), z.conj().imag
+    assert conjugate.is_conj() and negated.is_neg()
+    for view, plain in ((conjugate, conjugate.resolve_conj()), (negated, negated.resolve_neg())):
+        with pytest.raises(ValueError):
+            awq.reorder_states([view], parents)
+        with pytest.raises(ValueError):
+            awq.reorder_states([plain], parents, outs=[torch.empty_like(plain)[:2].conj() if plain.is_complex() else view[:2]])
+        got, = awq.reorder_states([plain], parents)
+        assert torch.equal(got, plain[[3, 0]])
+    with pytest.raises(ValueError):
+        awq.beam_select(negated, torch.zeros((1, 4), device="cuda"), 2)
