@@ -642,6 +642,8 @@ int64_t dense_row(const Tensor &t, const char *name)
 {
     if (t.dim() < 1) refuse("%s must have a first dimension of rows", name);
     int64_t n = 1;
+    for (const int64_t size : t.sizes().slice(1))
+        if (size == 0) return 0;
     for (int64_t d = t.dim() - 1; d > 0; --d) {
         if (t.size(d) != 1 && t.stride(d) != n) refuse("a row of %s must be contiguous", name);
         n *= t.size(d);

@@ -68,3 +68,13 @@ def test_views_that_are_conjugated_or_negated_are_refused():
         assert torch.equal(got, plain[[3, 0]])
     with pytest.raises(ValueError):
         awq.beam_select(negated, torch.zeros((1, 4), device="cuda"), 2)
+
+
+@pytest.mark.parametrize("shape", [(0,), (3, 0), (0, 3), (2, 0, 5), (2, 5, 0)])
+def test_rows_without_elements(shape):
+    empty, full = torch.zeros((4, *shape), device="cuda"), torch.randn((4, 3), device="cuda")
+    got, other = awq.reorder_states([empty, full], i32([3, 0, -1]))
+    assert got.shape == (3, *shape) and torch.equal(other[:2], full[[3, 0]])
+    outs = [torch.zeros((3, *shape), device="cuda"), torch.empty((3, 3), device="cuda")]
+    awq.reorder_states([empty, full], i32([3, 0, -1]), outs=outs)
+    assert torch.equal(outs[1], other)
