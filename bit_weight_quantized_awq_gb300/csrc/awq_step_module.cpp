@@ -759,10 +759,12 @@ PyObject *copy_pages(PyObject *const *o)
     const awq_cache_t layout = cache(like, "a cache", type, dev, like);
     std::vector<void *> data_of(n);
     for (int64_t i = 0; i < n; ++i) {
-        const Tensor &c = caches[i];
-        if (c.scalar_type() != type || !on(c, dev) || c.sizes() != like.sizes() || c.strides() != like.strides())
-            refuse("the caches must have the same type, device, shape and strides");
-        data_of[i] = c.data_ptr();
+        // an axis with one entry has no stride to differ in
+        const awq_cache_t c = cache(caches[i], "a cache", type, dev, like);
+        if (c.block_stride != layout.block_stride || c.token_stride != layout.token_stride ||
+            c.head_stride != layout.head_stride)
+            refuse("the caches must have the same strides");
+        data_of[i] = c.data;
     }
     const awq_stream_t stream = stream_of(dev);
     const int status = call([&] {
