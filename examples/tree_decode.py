@@ -3,10 +3,10 @@ is filled in, then every step drafts a tree of tokens, checks all of its nodes i
 one pass and keeps the longest path that the model itself would have taken.
 
 The step's operators run as a serving process uses them: ``paged_plan`` lays the
-step out from the request lengths, each layer appends its keys and values
-(``kv_append``) and attends over the paged cache (``tree_attention``) between its
-quantised projections, and ``process_logits`` applies penalties, biases and a
-token mask to every node's logits.
+step out from the request lengths, each layer turns its queries and keys by their
+positions, appends the keys and values (``rotary_append``) and attends over the paged cache
+(``tree_attention``) between its quantised projections, and ``process_logits`` applies
+penalties, biases and a token mask to every node's logits.
 
     python examples/tree_decode.py [--steps 8] [--requests 3]
 """
@@ -31,15 +31,6 @@ def quantised_layer(K: int, N: int, seed: int) -> awq.AWQLinear:
     return awq.AWQLinear(4, 64, p.qweight, p.qzeros, p.scales, None)
 
 
-def rotate(x: torch.Tensor, positions: torch.Tensor) -> torch.Tensor:
-    """Rotary position embedding of [tokens, heads, DIM]."""
-    half = DIM // 2
-    angle = positions[:, None].float() * 10000.0 ** (-torch.arange(half, device=x.device) / half)
-    cos, sin = angle.cos()[:, None].to(x.dtype), angle.sin()[:, None].to(x.dtype)
-    a, b = x[..., :half], x[..., half:]
-    return torch.cat([a * cos - b * sin, a * sin + b * cos], -1).contiguous()
-
-
 def norm(x: torch.Tensor) -> torch.Tensor:
     return (x.float() * torch.rsqrt(x.float().square().mean(-1, keepdim=True) + 1e-6)).half()
 
@@ -53,6 +44,7 @@ class Decoder:
         self.layers = [(quantised_layer(HIDDEN, (HEADS + 2 * KV_HEADS) * DIM, seed + 4 * i),
                         quantised_layer(HIDDEN, HIDDEN, seed + 4 * i + 1)) for i in range(LAYERS)]
         self.head = quantised_layer(HIDDEN, VOCAB, seed + 99)
+        self.inv_freq = (10000.0 ** (-torch.arange(DIM // 2) / (DIM // 2))).float().cuda()
         pages = -(-max_tokens // PAGE)
         self.caches = [[torch.zeros((requests * pages, PAGE, KV_HEADS, DIM), dtype=torch.float16, device="cuda")
                         for _ in range(2)] for _ in range(LAYERS)]
@@ -70,9 +62,8 @@ class Decoder:
         x = self.embedding[tokens.long()]
         for (qkv, out), (k_cache, v_cache) in zip(self.layers, self.caches):
             y = qkv(norm(x)).view(-1, HEADS + 2 * KV_HEADS, DIM)
-            q = rotate(y[:, :HEADS], plan.positions)
-            k = rotate(y[:, HEADS:HEADS + KV_HEADS], plan.positions)
-            awq.kv_append(k, y[:, HEADS + KV_HEADS:], k_cache, v_cache, plan.slot_map)
+            q = awq.rotary_append(y[:, :HEADS], y[:, HEADS:HEADS + KV_HEADS], y[:, HEADS + KV_HEADS:], plan.positions,
+                                  self.inv_freq, k_cache, v_cache, plan.slot_map)
             a = awq.tree_attention(q, k_cache, v_cache, self.table, self.lengths, plan.cu_new, DIM ** -0.5,
                                    max(new), self.longest, tree_mask=plan.tree_mask)
             x = x + out(a.view(-1, HIDDEN))
