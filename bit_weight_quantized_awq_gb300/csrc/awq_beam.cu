@@ -22,7 +22,9 @@
 // Bound: HBM, one read of the logits; one exponential a logit, and about seven instructions
 // around it, issued in 56 % of the cycles. Measured, with the reordering of token histories: 64 requests of 8
 // beams over 131,072 bf16 logits 38 us (rows 27.7, merge 6.4, histories 3.5; the read alone 20), 15 of 32
-// over 100,003 fp32 logits 50 us (36, 11, 3.2; 28), 4 beams over 32,000 16.5 us. On the way there: plain loads,
+// over 100,003 fp32 logits 50 us (36, 11, 3.2; 28), 4 beams over 32,000 11.5 us
+// replayed (17 to 20 a call, the host's). Masked parts cost little more (64 x 8 over 65,536 fp16, of which a mask leaves a
+// tenth: 20.7 us, 20.1 without). On the way there: plain loads,
 // keys sorted by one warp, sums and merges in fp64 94 and 153 us; the ring and sorted maxima 62 and 103; four small CTAs an
 // SM instead of two, fp32 pairs in the merge 50 and 62; eight pieces a thread and packed fp32
 // instructions 46 and 57; logits that leave L2 before anything else, so that code and lists stay, 43 and 56 (replayed);
@@ -581,8 +583,8 @@ struct Sum {
 };
 
 // Adds ln(x.high + x.low), normal and positive, to `to`: x = 2^e m with m in [2/3, 4/3), ln m by the series of
-// 2 atanh(t) in t = (m - 1) / (m + 1), |t| <= 1/5. The quotient has its remainder; behind the first term
-// fp32 will do (2^-34 of ln m).
+// 2 atanh(t) in t = (m - 1) / (m + 1), |t| <= 1/5. The quotient has its remainder; what
+// is behind the first term, 0.0055 at most, is formed and added in fp32: seven roundings, below 2^-28 in all.
 __device__ __forceinline__ void add_log(Sum x, Sum &to)
 {
     int bits = __float_as_int(x.high);
@@ -912,7 +914,7 @@ const void *rows_kernel() { return (const void *)beam_rows_kernel<T>; }
 // about 3 and the more the more are kept, a start 2. 38 x 7 rows of 151,927 bf16: 20.3 us in two parts each, 22.4 in
 // equal ones; 300 x 4 of 100,000: 44 in pairs, 61; 44 x 32 of 33,377, 40 kept: 36.7 one by one, 42.7.
 // A part has no more chunks of a row than have their maxima kept (it can, but is slow: what is read again is
-// not picked); a row has at most 32 parts (a lane each in the merge), and a request's lists the room that they have there.
+// not picked); a row has at most 32 parts, since the merge looks at each list, and a request's lists the room that they have there.
 BeamCut beam_cut(int64_t requests, int64_t beams, int64_t vocab, int64_t best, int element_bytes)
 {
     if (requests == 0) return {};

@@ -51,8 +51,8 @@ __device__ __forceinline__ int pages_of(int length, int block_size, int shift, i
 // ---------------------------------------------------------------------------
 // Fork. Which row is its parent's first and how many rows before it need a block follows
 // from the parents and lengths alone; every CTA computes both for all rows by itself, as the plan
-// does, so the step is one launch. Bound: latency; the tables are a few KB to a few MB. Measured: 8 rows 3.7 us,
-// 384 rows 5.1 us.
+// does, so the step is one launch. Bound: latency; the tables are a few KB to a few MB. Measured
+// (replayed): 8 rows 3.1 us, 384 rows 4.0 us.
 
 constexpr int kForkThreads = 512;
 constexpr int kForkEntries = 2048;          // of a row, a CTA and turn
@@ -161,7 +161,7 @@ fork_kernel(const __grid_constant__ ForkProblem p, unsigned int *status)
 // Copies of pages, 16 bytes at a time, kCopyPieces of a thread under way. A unit is a
 // part of one page of one cache; the CTAs take units in turn, since how many there are is known
 // on the device only. Bound: HBM, each byte read and written once. For small copies (2 layers, pages of 16 KB: 2.4
-// us) and layouts without long runs; 24 layers of 48 x 8 beams took 189 us so, and 130 in bulk.
+// us) and layouts without long runs; 24 layers of 48 x 8 beams took 189 us so, and 129 in bulk.
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyPieces = 8;
@@ -234,7 +234,7 @@ copy_pages_kernel(const __grid_constant__ CopyParams p)
 // The same by bulk copies (92 % of the copy bandwidth; 1.5 GB of moved pages 258 us, 284 by the
 // kernel above), for pages whose tokens lie in long runs: through a ring in shared memory, kAhead
 // loads and as many stores under way, all issued by one lane. The 32 lanes of the CTA look up 32 parts at
-// a time. (24 layers of 48 x 8 beams: 135 us; with 2 CTAs of twice the parts and ring 142. 8 tokens of 320 bytes
+// a time. (24 layers of 48 x 8 beams, with the tables: 135 us; with 2 CTAs of twice the parts and ring 142. 8 tokens of 320 bytes
 // of pages of 32, 32 layers of 20 x 16 beams: 14.5 and 25; in parts of 4 KB 14, but long pages of few tokens 28 for 23.5.)
 constexpr int kRunBytes = 8192;             // of a run at once
 constexpr int kRing = 4, kAhead = 2;
@@ -546,7 +546,8 @@ move_kernel(const __grid_constant__ PagesProblem p)
 
 // All of it in one launch of one cluster, for caches of up to kClusterWords words and small tables. Each CTA marks
 // its share of the entries in a bitmap of its own, then owns an eighth of the words: joins them from all
-// CTAs' bitmaps, counts and lists them. (256 rows of up to 256 pages: 5 us, and 9 in three launches.)
+// CTAs' bitmaps, counts and lists them. (Free blocks of 256 rows of up to 256 pages: 7.4 us replayed, 14.8 in
+// launches of their own for marking and listing; compacted 18.)
 constexpr int kCluster = 8, kClusterThreads = 1024;
 constexpr int kClusterWords = kCluster * kClusterThreads;       // a word a thread
 constexpr int64_t kClusterEntries = 1 << 18;

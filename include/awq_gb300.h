@@ -660,8 +660,9 @@ awq_status_t awq_rotary(const awq_rotary_t *args, awq_stream_t stream);
  * and, with end_tokens, reports those among the first num_beams of all its candidates
  * that end there:
  *   ended_scores, ended_parents, ended_tokens  the same for these
- * Places without a candidate hold -inf, -1 and -1. The sum is in fp32 over chunks of 16 KB;
- * the chunks are added up, and s compared, with pairs of fp32 numbers (about 48 bits). What a
+ * Places without a candidate hold -inf, -1 and -1. The exponentials and their sums over parts of 4 KB
+ * are in fp32, which leaves the logarithm of the sum good to 2^-17, whatever the vocabulary; the parts are added up, and s
+ * formed and compared, with pairs of fp32 numbers (about 48 bits; the logarithm by itself is good to 2^-28). What a
  * row gives does not depend on the other rows: rows with equal logits, at the same place within 16
  * bytes, and equal scores tie.
  *
