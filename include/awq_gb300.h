@@ -400,7 +400,8 @@ awq_status_t awq_reserve(int64_t max_M, int64_t max_K, int64_t max_N, unsigned f
  * runs (a length, an index, a table entry out of range) never makes it read or
  * write out of bounds: it is recorded for awq_last_device_status, as
  * AWQ_ERR_INVALID_ARG, or AWQ_ERR_TOO_LARGE where a capacity was exceeded.
- * Integer arrays need their natural alignment only.
+ * Integer arrays need their natural alignment only. A call's outputs overlap neither its inputs
+ * nor one another unless it says that they may: other CTAs may still read what one has written over.
  */
 typedef enum { AWQ_F16 = 0, AWQ_BF16 = 1, AWQ_F32 = 2 } awq_dtype_t;
 
