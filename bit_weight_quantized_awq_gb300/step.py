@@ -63,7 +63,9 @@ def paged_plan(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: 
     """One step's layout from request lengths: extends ``block_table`` in place
     with blocks from the start of ``free_blocks`` and gives every new token its
     cache slot, position and request, and with ``mask_words`` > 0 its ancestors in
-    the drafted tree that ``parents`` describes (a chain if None)."""
+    the drafted tree that ``parents`` describes (a chain if None). ``free_blocks`` may
+    be ``free_pages``' whole list: an entry of -1 means that none is left (slots of -1,
+    ERR_TOO_LARGE in the device status)."""
     made = (_step or _load()).paged_plan(context_lens, new_lens, block_table, free_blocks, block_size, max_tokens,
                                          parents, mask_words)
     if type(made) is int:
@@ -208,7 +210,8 @@ def fork_pages(block_table: torch.Tensor, lens: torch.Tensor, parents: torch.Ten
     ``block_table``, which hold ``lens`` tokens. Full pages are shared; a partly filled last one
     stays with its first child, the others take blocks from ``free_blocks`` (from
     ``free_start`` on: a plan's ``counts[1:]``, say) and a copy, which
-    ``copy_pages(caches, f.src, f.dst, f.tokens, f.count)`` makes."""
+    ``copy_pages(caches, f.src, f.dst, f.tokens, f.count)`` makes. Where no block is left (the
+    list's end, or an entry of -1), the row's last page is -1 and the device status ERR_TOO_LARGE."""
     made = (_step or _load()).fork_pages(block_table, lens, parents, free_blocks, block_size, free_start)
     if type(made) is int:
         raise AWQError(made, "awq_fork_pages")
